@@ -10,7 +10,9 @@ Names follow the C ABI (``conv_fwd``, ``pack_ncdhw_bf16_to_ndhwc``,
 ``pack_ncdhw_bf16_to_ndhwc_fp8``, ...).  ``conv3d``, ``conv2d`` and
 ``conv1d`` are the convenience wrappers: 2-D and 1-D convolutions run as the
 degenerate 3-D forms D=T=1 (and H=R=1 for 1-D), as the FlyDSL PR #860
-conv2d/conv1d wrapper commit does.
+conv2d/conv1d wrapper commit does.  ``rms_norm_quant``, ``act_quant`` and
+``linear_w8a8`` (module ``token_ops``) are the 8-bit operators on the tokens
+that a patch embedding makes.
 """
 from __future__ import annotations
 
@@ -751,6 +753,8 @@ def conv1d(x, w, stride=1, padding=0, dilation=1, scale_x=None, scale_w=None, **
     return y[:, 0, 0]
 
 
+from .token_ops import act_quant, linear_w8a8, rms_norm_quant   # noqa: E402
+
 __all__ = [
     "conv_fwd", "conv_fwd_noalloc", "conv_fwd_plan", "conv_out_dims", "conv_get_device_status",
     "conv_set_wait_limit_ns", "pack_ncdhw_bf16_to_ndhwc", "pack_ncdhw_bf16_to_ndhwc_fp8",
@@ -760,4 +764,5 @@ __all__ = [
     "conv_fwd_ncdhw_plan", "conv_bwd_point_workspace_bytes", "conv_bwd_data_point",
     "conv_bwd_weight_point", "conv_fwd_workspace_size", "conv_get_device_status_stream",
     "set_overrides", "overrides", "conv_fwd_ncdhw_fp8", "conv_fwd_ncdhw_fp8_workspace_size",
+    "rms_norm_quant", "act_quant", "linear_w8a8",
 ]

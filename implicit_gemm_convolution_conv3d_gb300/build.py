@@ -21,8 +21,11 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libconv3d.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["conv_igemm.cu", "aux_kernels.cu", "conv3d_api.cu", "conv_noalloc.cu", "conv_fused_q.cu"]
+SOURCES = ["conv_igemm.cu", "aux_kernels.cu", "conv3d_api.cu", "conv_noalloc.cu", "conv_fused_q.cu",
+           "token_quant.cu", "linear_w8a8.cu", "token_api.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "tile_table.h", "kernel_common.cuh"]
+TOKEN_HEADERS = ["token_common.cuh", "token_ops_internal.h"]   # the token operators' own
+PUBLIC_HEADERS = ["conv3d.h", "token_ops.h"]
 
 
 def nvcc_path() -> str:
@@ -44,7 +47,8 @@ def _stale(obj: str, src: str) -> bool:
     if not os.path.exists(obj):
         return True
     t = os.path.getmtime(obj)
-    deps = [src] + [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, "conv3d.h")]
+    deps = [src] + [os.path.join(CSRC, h) for h in HEADERS + TOKEN_HEADERS]
+    deps += [os.path.join(INCLUDE, h) for h in PUBLIC_HEADERS]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -1,0 +1,176 @@
+// token_api.cu -- the C ABI of the token operators (declared in
+// include/token_ops.h): argument checks and launches.  No allocation.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <cstdio>
+
+#include "internal.h"
+#include "token_common.cuh"
+#include "token_ops.h"
+#include "token_ops_internal.h"
+
+namespace c3d {
+
+namespace {
+
+constexpr int64_t kMaxDim = (1ll << 31) - 1;
+
+int invalid(const char* what) {
+    set_last_error(what);
+    return CONV_ERR_INVALID;
+}
+
+int launched(cudaError_t e, const char* where) {
+    if (e == cudaSuccess) return CONV_OK;
+    char msg[160];
+    std::snprintf(msg, sizeof msg, "%s: %s", where, cudaGetErrorString(e));
+    set_last_error(msg);
+    return CONV_ERR_CUDA;
+}
+
+bool is_float_type(int t) { return t == CONV_DTYPE_BF16 || t == CONV_DTYPE_F16 || t == CONV_DTYPE_F32; }
+bool is_code_type(int t) { return t == CONV_DTYPE_INT8 || t == CONV_DTYPE_FP8_E4M3; }
+int size_of(int t) {
+    return t == CONV_DTYPE_F32 ? 4 : t == CONV_DTYPE_BF16 || t == CONV_DTYPE_F16 ? 2 : 1;
+}
+bool aligned_to(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) % bytes) == 0; }
+
+// the checks that every matrix of rows shares
+const char* bad_rows(const void* p, int64_t stride, int64_t row, int64_t rows, int elt) {
+    if (!p) return "null pointer";
+    if (stride < row && rows > 1) return "a row stride is below the row's length";
+    if (!aligned_to(p, elt)) return "a pointer is not aligned to its element type";
+    return nullptr;
+}
+
+}  // namespace
+
+}  // namespace c3d
+
+using namespace c3d;
+
+extern "C" {
+
+int rms_norm_quant_fwd(const void* x, int x_dtype, int64_t x_stride, const void* residual,
+                       int res_dtype, int64_t res_stride, const void* weight, int weight_dtype,
+                       float eps, int64_t tokens, int64_t width, int q_dtype, void* q,
+                       int64_t q_stride, float* scale, void* residual_out,
+                       int64_t res_out_stride, cudaStream_t stream) {
+    if (tokens < 0 || tokens > kMaxDim || width < 1 || width > kMaxDim)
+        return invalid("tokens must be 0 or more and width 1 or more, below 2^31");
+    if (!is_float_type(x_dtype)) return invalid("x_dtype must be BF16, F16 or F32");
+    if (!is_code_type(q_dtype)) return invalid("q_dtype must be INT8 or FP8_E4M3");
+    if (residual && res_dtype != x_dtype && res_dtype != CONV_DTYPE_F32)
+        return invalid("res_dtype must be x_dtype or F32");
+    if (weight && weight_dtype != x_dtype && weight_dtype != CONV_DTYPE_F32)
+        return invalid("weight_dtype must be x_dtype or F32");
+    if (residual_out && !residual) return invalid("residual_out needs a residual");
+    if (!(eps >= 0.0f)) return invalid("eps must be 0 or more");
+    if (tokens == 0) return CONV_OK;
+    if (const char* e = bad_rows(x, x_stride, width, tokens, size_of(x_dtype))) return invalid(e);
+    if (const char* e = bad_rows(q, q_stride, width, tokens, 1)) return invalid(e);
+    if (const char* e = bad_rows(scale, 1, 1, tokens, 4)) return invalid(e);
+    if (residual)
+        if (const char* e = bad_rows(residual, res_stride, width, tokens, size_of(res_dtype)))
+            return invalid(e);
+    if (residual_out)
+        if (const char* e = bad_rows(residual_out, res_out_stride, width, tokens, size_of(res_dtype)))
+            return invalid(e);
+    if (weight && !aligned_to(weight, size_of(weight_dtype)))
+        return invalid("a pointer is not aligned to its element type");
+    NormParams p{};
+    p.x = x;
+    p.res = residual;
+    p.weight = weight;
+    p.res_out = residual_out;
+    p.q = static_cast<uint8_t*>(q);
+    p.scale = scale;
+    p.x_stride = x_stride;
+    p.res_stride = res_stride;
+    p.res_out_stride = res_out_stride;
+    p.q_stride = q_stride;
+    p.tokens = tokens;
+    p.width = width;
+    p.eps = eps;
+    p.shrink = 1.0f;
+    while (static_cast<double>(p.shrink) * p.shrink * static_cast<double>(width) > 1.0) p.shrink *= 0.5f;
+    p.mean_of = static_cast<float>(
+        1.0 / (static_cast<double>(p.shrink) * p.shrink * static_cast<double>(width)));
+    p.x_dtype = x_dtype;
+    p.res_dtype = residual ? res_dtype : x_dtype;
+    p.weight_dtype = weight ? weight_dtype : x_dtype;
+    p.q_dtype = q_dtype;
+    return launched(launch_norm_quant(p, stream), "rms_norm_quant_fwd launch");
+}
+
+int act_quant_fwd(const void* x, int x_dtype, int64_t x_stride, int act, int gated,
+                  int64_t tokens, int64_t width, int q_dtype, void* q, int64_t q_stride,
+                  float* scale, cudaStream_t stream) {
+    if (tokens < 0 || tokens > kMaxDim || width < 1 || width > kMaxDim / 2)
+        return invalid("tokens must be 0 or more and width 1 or more, below 2^31 (2^30)");
+    if (!is_float_type(x_dtype)) return invalid("x_dtype must be BF16, F16 or F32");
+    if (!is_code_type(q_dtype)) return invalid("q_dtype must be INT8 or FP8_E4M3");
+    if (act < CONV_ACT_NONE || act > CONV_ACT_GELU) return invalid("unknown activation");
+    if (tokens == 0) return CONV_OK;
+    if (const char* e = bad_rows(x, x_stride, gated ? 2 * width : width, tokens, size_of(x_dtype)))
+        return invalid(e);
+    if (const char* e = bad_rows(q, q_stride, width, tokens, 1)) return invalid(e);
+    if (const char* e = bad_rows(scale, 1, 1, tokens, 4)) return invalid(e);
+    ActParams p{};
+    p.x = x;
+    p.q = static_cast<uint8_t*>(q);
+    p.scale = scale;
+    p.x_stride = x_stride;
+    p.q_stride = q_stride;
+    p.tokens = tokens;
+    p.width = width;
+    p.x_dtype = x_dtype;
+    p.q_dtype = q_dtype;
+    p.act = act;
+    p.gated = gated != 0;
+    return launched(launch_act_quant(p, stream), "act_quant_fwd launch");
+}
+
+size_t linear_w8a8_workspace_size(const void*, int64_t, const void*, int64_t, int64_t, int64_t,
+                                  int64_t) {
+    return 0;
+}
+
+int linear_w8a8_fwd(const void* x, int64_t x_stride, const void* w, int64_t w_stride, int dtype,
+                    int64_t tokens, int64_t outputs, int64_t width, const float* scale_x,
+                    const float* scale_w, const float* bias, int act, void* out, int out_dtype,
+                    int64_t out_stride, void*, size_t, cudaStream_t stream) {
+    if (tokens < 0 || tokens > kMaxDim || outputs < 0 || outputs > kMaxDim || width < 1 ||
+        width > kMaxDim)
+        return invalid("tokens and outputs must be 0 or more and width 1 or more, below 2^31");
+    if (!is_code_type(dtype)) return invalid("dtype must be INT8 or FP8_E4M3");
+    if (!is_float_type(out_dtype)) return invalid("out_dtype must be BF16, F16 or F32");
+    if (act < CONV_ACT_NONE || act > CONV_ACT_GELU) return invalid("unknown activation");
+    if (tokens == 0 || outputs == 0) return CONV_OK;
+    if (const char* e = bad_rows(x, x_stride, width, tokens, 1)) return invalid(e);
+    if (const char* e = bad_rows(w, w_stride, width, outputs, 1)) return invalid(e);
+    if (const char* e = bad_rows(out, out_stride, outputs, tokens, size_of(out_dtype)))
+        return invalid(e);
+    if (!aligned_to(scale_x, 4) || !aligned_to(scale_w, 4) || !aligned_to(bias, 4))
+        return invalid("a pointer is not aligned to its element type");
+    LinearParams p{};
+    p.x = static_cast<const uint8_t*>(x);
+    p.w = static_cast<const uint8_t*>(w);
+    p.scale_x = scale_x;
+    p.scale_w = scale_w;
+    p.bias = bias;
+    p.out = out;
+    p.x_stride = x_stride;
+    p.w_stride = w_stride;
+    p.out_stride = out_stride;
+    p.tokens = tokens;
+    p.outputs = outputs;
+    p.width = width;
+    p.e4m3 = dtype == CONV_DTYPE_FP8_E4M3;
+    p.act = act;
+    p.out_dtype = out_dtype;
+    return launched(launch_linear_w8a8(p, stream), "linear_w8a8_fwd launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,52 @@
+// token_ops_internal.h -- parameter blocks and launch entry points shared by
+// token_api.cu and the token kernels.  Not part of the public ABI.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace c3d {
+
+struct NormParams {
+    const void* x;
+    const void* res;      // NULL: no residual
+    const void* weight;   // NULL: ones
+    void* res_out;        // NULL: not stored
+    uint8_t* q;
+    float* scale;
+    long long x_stride, res_stride, res_out_stride, q_stride;
+    long long tokens, width;
+    float eps;
+    // the sum of squares is taken of h * shrink (a power of two near
+    // 1/sqrt(width), so that it overflows only where the mean does) and the
+    // mean is that sum * mean_of
+    float shrink, mean_of;
+    int x_dtype, res_dtype, weight_dtype, q_dtype;
+};
+
+struct ActParams {
+    const void* x;
+    uint8_t* q;
+    float* scale;
+    long long x_stride, q_stride;
+    long long tokens, width;
+    int x_dtype, q_dtype, act, gated;
+};
+
+struct LinearParams {
+    const uint8_t* x;
+    const uint8_t* w;
+    const float* scale_x;   // NULL: ones
+    const float* scale_w;   // NULL: ones
+    const float* bias;      // NULL: none
+    void* out;
+    long long x_stride, w_stride, out_stride;
+    long long tokens, outputs, width;
+    int e4m3, act, out_dtype;
+};
+
+cudaError_t launch_norm_quant(const NormParams& p, cudaStream_t stream);
+cudaError_t launch_act_quant(const ActParams& p, cudaStream_t stream);
+cudaError_t launch_linear_w8a8(const LinearParams& p, cudaStream_t stream);
+
+}  // namespace c3d
