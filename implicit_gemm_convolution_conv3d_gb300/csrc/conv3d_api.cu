@@ -1215,6 +1215,26 @@ size_t splitk_workspace_bytes(const int64_t x_dims[5], const int64_t w_dims[5],
 
 void set_last_error(const char* msg) { std::snprintf(t_last_error, sizeof t_last_error, "%s", msg); }
 
+int launch_limits(LaunchLimits* l) {
+    DeviceInfo* d = nullptr;
+    int rc = device_info(&d);
+    if (rc) return rc;
+    *l = LaunchLimits{d->num_sms, d->smem_optin, d->status, g_wait_ns};
+    return CONV_OK;
+}
+
+int encode_rows_u8(CUtensorMap* m, const void* ptr, long long cols, long long rows, long long pitch,
+                   int box_rows) {
+    if (!load_entry_points()) {
+        set_error("the driver's tensor-map encoders are not available");
+        return CONV_ERR_CUDA;
+    }
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+    const cuuint32_t box[2] = {128u, static_cast<cuuint32_t>(box_rows)};
+    return encode_tiled(m, 1, 2, ptr, dims, strides, box, 128);
+}
+
 Overrides overrides() {
     std::lock_guard<std::mutex> lk(g_ovr_mutex);
     return g_ovr;

@@ -278,6 +278,21 @@ cudaError_t launch_pack_tma(const CUtensorMap* in_map, long long N, long long C,
                             int num_sms, int smem_optin, int* status, unsigned long long wait_ns,
                             cudaStream_t stream);
 
+// What a launch needs to know of the current device, and the bound on the
+// kernels' waits.
+struct LaunchLimits {
+    int num_sms, smem_optin;
+    int* status;
+    unsigned long long wait_ns;
+};
+int launch_limits(LaunchLimits* l);
+
+// Tensor map of a byte matrix [rows, cols] with `pitch` bytes between rows
+// (base and pitch multiples of 16): boxes of 128 columns x box_rows rows in the
+// 128-byte swizzle, zeros outside the matrix.
+int encode_rows_u8(CUtensorMap* m, const void* ptr, long long cols, long long rows, long long pitch,
+                   int box_rows);
+
 int* device_status_ptr();   // device address of the status word (current device)
 
 // The process's plan / path overrides (conv_set_overrides), copied under a

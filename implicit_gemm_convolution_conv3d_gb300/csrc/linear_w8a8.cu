@@ -1,6 +1,15 @@
 // linear_w8a8.cu -- the product of 8-bit tokens and weights with a scale per
-// token and per output channel.
+// token and per output channel:
+//
+//   out[m,n] = act(scale_x[m] * scale_w[n] * sum_k x[m,k] w[n,k] + bias[n])
+//
+// sm_103a has no tensor-core product of 8-bit integers (tcgen05 kind::i8 is not
+// among its features), so int8 codes go through kind::f16: every code is exact in
+// f16, every product in fp32, and the fp32 sums are exact up to 2^24.  e4m3
+// codes go through kind::f8f6f4 as they are.
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "token_common.cuh"
 #include "token_ops_internal.h"
@@ -9,71 +18,480 @@ namespace c3d {
 
 namespace {
 
-constexpr int kT = 64;   // outputs and tokens of a tile
-constexpr int kKB = 32;  // reduction elements of a step
+constexpr int kRows = 128;        // weight rows of a tile (tcgen05 M)
+constexpr int kStep = 128;        // reduction elements (bytes) of a k-step
+constexpr int kMaxTok = 128;      // tokens of a tile at most
+constexpr int kCvtThreads = 256;  // converter / epilogue threads
+constexpr int kThreads = 128 + kCvtThreads;
+constexpr int kMaxStages = 8, kMaxCvt = 4;
+constexpr uint32_t kBarBytes = 16u * (kMaxStages + kMaxCvt) + 16u;
 
-__device__ __forceinline__ void store_out(void* out, int dtype, long long at, float v) {
+// The byte of the 16-byte chunk `c` of row `r` in a 128-byte-swizzled tile.
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+    return static_cast<uint32_t>(r) * 128u + (static_cast<uint32_t>(c ^ (r & 7)) << 4);
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
+// Four int8 codes as four f16 values: with the sign bit flipped a byte is the
+// code + 128, and below the byte 0x64 it is the f16 number 1024 + 128 + code;
+// 1152 subtracts exactly.  Five instructions for four codes.
+__device__ __forceinline__ void i8x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// One 16-byte chunk (16 codes) as 8 registers of f16 pairs.
+__device__ __forceinline__ void cvt_chunk(const uint4& v, uint32_t* o) {
+    i8x4_to_f16x4(v.x, o[0], o[1]);
+    i8x4_to_f16x4(v.y, o[2], o[3]);
+    i8x4_to_f16x4(v.z, o[4], o[5]);
+    i8x4_to_f16x4(v.w, o[6], o[7]);
+}
+
+// Epilogue activation: the convolutions' forms for 16-bit outputs, the
+// fp32-accurate ones for fp32 outputs; both keep a NaN.
+__device__ __forceinline__ float epi_act(float v, int act, int out_dtype) {
+    if (act == kActNone) return v;
+    if (act == kActRelu || out_dtype == kTokF32) return activate_f32(v, act);
+    return activate(v, act);
+}
+
+__device__ __forceinline__ void store_one(void* out, int dtype, long long at, float v) {
     if (dtype == kTokBf16) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
     else if (dtype == kTokF16) static_cast<__half*>(out)[at] = __float2half_rn(v);
     else static_cast<float*>(out)[at] = v;
 }
 
-template <bool E4M3>
-__device__ __forceinline__ float code_value(uint8_t c) {
-    if (E4M3) return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
-    return static_cast<float>(static_cast<int8_t>(c));
+__device__ __forceinline__ uint32_t pack2(float a, float b, int dtype) {
+    if (dtype == kTokBf16) return pack_bf16x2(a, b);
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// A 64 x 64 tile per block of 256 threads, 4 x 4 outputs a thread.
+// ---------------------------------------------------------------- split tiles
+// One tile (128 outputs x up to 128 tokens) per cluster, its reduction split
+// over the cluster's CTAs: the form for few tokens, where the weights are all
+// there is to read and 128-row tiles alone would leave most SMs idle.  The
+// weights are the MMA's 128-row operand, so that a tile holds as few tokens as
+// there are; partial tiles meet in distributed shared memory and are summed in
+// rank order.
+//   warp 0     TMA producer: raw 128-byte rows of weights and tokens
+//   warp 1     TMEM, MMA issuer
+//   warps 4-7  int8: weights to f16 into TMEM (lane = row); epilogue
+//   warps 8-11 int8: tokens to f16 into shared memory;       epilogue
+struct SplitParams {
+    LinearParams p;
+    int tok_tile, out_tiles;
+    int splits, k_steps, stages, cvt;
+    uint32_t stage_bytes, cvt_bytes;
+};
+
 template <bool E4M3>
-__global__ void __launch_bounds__(256) linear_tile_kernel(const LinearParams p) {
-    __shared__ float xs[kKB][kT + 1], ws[kKB][kT + 1];
-    const long long n0 = static_cast<long long>(blockIdx.x) * kT;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const long long m_tiles = (p.tokens + kT - 1) / kT;
-    for (long long mt = blockIdx.y; mt < m_tiles; mt += gridDim.y) {
-        const long long m0 = mt * kT;
-        float acc[4][4] = {};
-        for (long long k0 = 0; k0 < p.width; k0 += kKB) {
-            for (int i = threadIdx.x; i < kT * kKB; i += 256) {
-                const int r = i / kKB, c = i % kKB;
-                const bool kin = k0 + c < p.width;
-                xs[c][r] = kin && m0 + r < p.tokens
-                               ? code_value<E4M3>(p.x[(m0 + r) * p.x_stride + k0 + c]) : 0.0f;
-                ws[c][r] = kin && n0 + r < p.outputs
-                               ? code_value<E4M3>(p.w[(n0 + r) * p.w_stride + k0 + c]) : 0.0f;
-            }
-            __syncthreads();
-            for (int k = 0; k < kKB; ++k)
-                for (int i = 0; i < 4; ++i)
-                    for (int j = 0; j < 4; ++j)
-                        acc[i][j] = fmaf(xs[k][ty + 16 * i], ws[k][tx + 16 * j], acc[i][j]);
-            __syncthreads();
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_split_kernel(const __grid_constant__ CUtensorMap w_map,
+                        const __grid_constant__ CUtensorMap x_map, const SplitParams s) {
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    const LinearParams& p = s.p;
+    const int nt = s.tok_tile;
+    const uint32_t ring = base;
+    const uint32_t cvt0 = ring + static_cast<uint32_t>(s.stages) * s.stage_bytes;
+    const uint32_t bars = cvt0 + static_cast<uint32_t>(s.cvt) * s.cvt_bytes;
+    const uint32_t full0 = bars, empty0 = full0 + 8u * kMaxStages;
+    const uint32_t cfull0 = empty0 + 8u * kMaxStages, cempty0 = cfull0 + 8u * kMaxCvt;
+    const uint32_t acc_bar = cempty0 + 8u * kMaxCvt, drain_bar = acc_bar + 8u;
+    uint32_t* misc = reinterpret_cast<uint32_t*>(smem_raw + (drain_bar + 8u - raw));
+    // misc[0] TMEM base, [1] abort flag, [2] k-steps issued, [3] k-steps consumed
+    volatile uint32_t* abort_flag = misc + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(blockIdx.x % static_cast<unsigned>(s.splits));
+    const int tile = static_cast<int>(blockIdx.x / static_cast<unsigned>(s.splits));
+    const int n0 = (tile % s.out_tiles) * kRows;
+    const long long m0 = static_cast<long long>(tile / s.out_tiles) * nt;
+    const int ks0 = static_cast<int>(static_cast<long long>(s.k_steps) * rank / s.splits);
+    const int ks1 = static_cast<int>(static_cast<long long>(s.k_steps) * (rank + 1) / s.splits);
+    const int steps = ks1 - ks0;   // at least one: splits <= k_steps
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < s.stages; ++i) {
+            mbar_init(full0 + 8 * i, 1);
+            mbar_init(empty0 + 8 * i, E4M3 ? 1 : kCvtThreads / 32);
         }
-        for (int i = 0; i < 4; ++i) {
-            const long long m = m0 + ty + 16 * i;
-            if (m >= p.tokens) continue;
-            const float sx = p.scale_x ? p.scale_x[m] : 1.0f;
-            for (int j = 0; j < 4; ++j) {
-                const long long n = n0 + tx + 16 * j;
-                if (n >= p.outputs) continue;
-                float v = acc[i][j] * sx * (p.scale_w ? p.scale_w[n] : 1.0f);
-                if (p.bias) v += p.bias[n];
-                store_out(p.out, p.out_dtype, m * p.out_stride + n, activate_f32(v, p.act));
+        for (int i = 0; i < s.cvt; ++i) {
+            mbar_init(cfull0 + 8 * i, kCvtThreads / 32);
+            mbar_init(cempty0 + 8 * i, 1);
+        }
+        mbar_init(acc_bar, 1);
+        mbar_init(drain_bar, 1);
+        misc[1] = 0u;
+        misc[2] = 0u;
+        misc[3] = 0u;
+        fence_mbar_init();
+        prefetch_tmap(&w_map);
+        prefetch_tmap(&x_map);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(misc), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+    const uint32_t tmem_a = tmem + kMaxTok;   // converted weights behind the accumulator
+    griddep_launch_dependents();
+    griddep_wait();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int st = 0;
+            uint32_t ph = 0;
+            for (int i = 0; i < steps; ++i) {
+                if (!wait_bar(empty0 + 8 * st, ph ^ 1u, abort_flag, p.status, p.wait_ns)) break;
+                const uint32_t fb = full0 + 8 * st, dst = ring + st * s.stage_bytes;
+                mbar_arrive_expect_tx(fb, s.stage_bytes);
+                tma_load_2d(dst, &w_map, fb, (ks0 + i) * kStep, n0);
+                tma_load_2d(dst + kRows * kStep, &x_map, fb, (ks0 + i) * kStep, static_cast<int>(m0));
+                misc[2] = i + 1;
+                if (++st == s.stages) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // D: fp32, operands f16 (or e4m3: both codes are 0), N tokens, M 128
+            const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(nt >> 3) << 17) | ((kRows >> 4) << 24);
+            const uint64_t adesc = make_smem_desc(ring, 1024u, 2u);
+            const uint64_t bdesc = make_smem_desc(E4M3 ? ring + kRows * kStep : cvt0, 1024u, 2u);
+            const uint32_t step = (E4M3 ? s.stage_bytes : s.cvt_bytes) >> 4;
+            const int depth = E4M3 ? s.stages : s.cvt;
+            int st = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int i = 0; i < steps; ++i) {
+                const uint32_t fb = (E4M3 ? full0 : cfull0) + 8 * st;
+                if (!wait_bar(fb, ph, abort_flag, p.status, p.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                if (E4M3) misc[3] = i + 1;
+                tc_fence_after();
+                const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(st) * step);
+                if (E4M3) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma_f8(tmem, adesc + off + 2 * k, bdesc + off + 2 * k, idesc, (i | k) != 0);
+                } else {
+                    const uint32_t box = static_cast<uint32_t>(nt) * 128u >> 4;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        tc_mma_f16_ta(tmem, tmem_a + st * 64 + k * 8,
+                                      bdesc + off + (k >> 2) * box + 2 * (k & 3), idesc, (i | k) != 0);
+                }
+                tc_commit((E4M3 ? empty0 : cempty0) + 8 * st);
+                if (++st == depth) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (ok) tc_commit(acc_bar);
+        }
+    } else if (warp >= 4) {
+        bool ok = true;
+        if (!E4M3) {
+            int st = 0, c = 0;
+            uint32_t ph = 0, cph = 0;
+            for (int i = 0; i < steps; ++i) {
+                ok = wait_bar(full0 + 8 * st, ph, abort_flag, p.status, p.wait_ns) &&
+                     wait_bar(cempty0 + 8 * c, cph ^ 1u, abort_flag, p.status, p.wait_ns);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                if (threadIdx.x == 128) misc[3] = i + 1;
+                const uint32_t src = ring + st * s.stage_bytes;
+                if (warp < 8) {
+                    tc_fence_after();
+                    const int r = (warp & 3) * 32 + lane;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) cvt_chunk(lds128(src + swz(r, 4 * h + j)), v + 8 * j);
+                        tmem_st_32x32b_x32(tmem_a + (static_cast<uint32_t>((warp & 3) * 32) << 16) +
+                                               c * 64 + h * 32, v);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                } else {
+                    const uint32_t dst = cvt0 + c * s.cvt_bytes;
+                    for (int u = threadIdx.x - 256; u < nt * 8; u += 128) {
+                        const int r = u >> 3, ch = u & 7;
+                        uint32_t v[8];
+                        cvt_chunk(lds128(src + kRows * kStep + swz(r, ch)), v);
+                        const uint32_t box = dst + static_cast<uint32_t>((ch >> 2) * nt) * 128u;
+                        // the two halves in opposite order in the second box:
+                        // its rows start at the first box's banks
+                        const int d = 2 * (ch & 3);
+                        if (ch < 4) {
+                            sts128(box + swz(r, d), v[0], v[1], v[2], v[3]);
+                            sts128(box + swz(r, d + 1), v[4], v[5], v[6], v[7]);
+                        } else {
+                            sts128(box + swz(r, d + 1), v[4], v[5], v[6], v[7]);
+                            sts128(box + swz(r, d), v[0], v[1], v[2], v[3]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(empty0 + 8 * st);
+                    mbar_arrive(cfull0 + 8 * c);
+                }
+                if (++st == s.stages) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+                if (++c == s.cvt) {
+                    c = 0;
+                    cph ^= 1u;
+                }
+            }
+        }
+        // the accumulator as [token][output] fp32 over the ring, which every
+        // load and MMA has left by now
+        if (ok && wait_bar(acc_bar, 0, abort_flag, p.status, p.wait_ns)) {
+            tc_fence_after();
+            const int q = warp & 3, half = warp >= 8;
+            const int valid = static_cast<int>(min(static_cast<long long>(nt), p.tokens - m0));
+            for (int t0 = half * (nt / 2); t0 < (half + 1) * (nt / 2); t0 += 8) {
+                if (t0 >= valid) break;
+                uint32_t v[8];
+                tmem_ld_32x32b_x8(tmem + (static_cast<uint32_t>(q * 32) << 16) + t0, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(
+                                     ring + static_cast<uint32_t>((t0 + j) * kRows + q * 32 + lane) * 4u),
+                                 "r"(v[j]) : "memory");
+            }
+            tc_fence_before();
+        }
+    }
+    __syncwarp();
+    if (s.splits > 1) cluster_sync();
+    else __syncthreads();
+    if (warp >= 4 && !*abort_flag) {
+        // this rank's share of the tile's tokens, a row of 128 outputs per warp
+        const int t_lo = nt * rank / s.splits, t_hi = nt * (rank + 1) / s.splits;
+        const int n = n0 + 4 * lane;
+        float sw[4], b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool in = n + j < p.outputs;
+            sw[j] = in && p.scale_w ? __ldg(p.scale_w + n + j) : 1.0f;
+            b[j] = in && p.bias ? __ldg(p.bias + n + j) : 0.0f;
+        }
+        const int elt = p.out_dtype == kTokF32 ? 4 : 2;
+        const bool wide = n + 3 < p.outputs &&
+                          ((reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(p.out_stride * elt)) &
+                           (4 * elt - 1)) == 0;
+        for (int t = t_lo + warp - 4; t < t_hi; t += kCvtThreads / 32) {
+            const long long m = m0 + t;
+            if (m >= p.tokens) break;
+            const uint32_t a = ring + static_cast<uint32_t>(t * kRows + 4 * lane) * 4u;
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int r = 0; r < s.splits; ++r) {
+                const float4 f = ld_cluster_f4(mapa_shared(a, s.splits > 1 ? r : cluster_ctarank()));
+                v[0] += f.x;
+                v[1] += f.y;
+                v[2] += f.z;
+                v[3] += f.w;
+            }
+            const float sx = p.scale_x ? __ldg(p.scale_x + m) : 1.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = epi_act(v[j] * sx * sw[j] + b[j], p.act, p.out_dtype);
+            const long long at = m * p.out_stride + n;
+            if (wide) {
+                if (elt == 4)
+                    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) =
+                        make_float4(v[0], v[1], v[2], v[3]);
+                else
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+                        make_uint2(pack2(v[0], v[1], p.out_dtype), pack2(v[2], v[3], p.out_dtype));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n + j < p.outputs) store_one(p.out, p.out_dtype, at + j, v[j]);
             }
         }
     }
+    __syncwarp();
+    if (s.splits > 1) cluster_sync();   // the peers have read this CTA's partial tile
+    else __syncthreads();
+    if (*abort_flag) {
+        // drain: boxes armed but never waited for, then the MMAs in flight
+        if (threadIdx.x == 0) {
+            const uint32_t issued = misc[2], consumed = misc[3];
+            for (uint32_t i = consumed; i < issued; ++i)
+                drain_wait(full0 + 8 * (i % static_cast<uint32_t>(s.stages)),
+                           (i / static_cast<uint32_t>(s.stages)) & 1u);
+        }
+        if (warp == 1 && lane == 0) {
+            tc_commit(drain_bar);
+            drain_wait(drain_bar, 0);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Rows of any alignment copied to a 16-byte pitch, zeros behind each row: one
+// thread per 16-byte word, put together from the aligned 4-byte words that its
+// bytes lie in.
+__global__ void __launch_bounds__(256) pad_rows_kernel(const uint8_t* src, long long stride,
+                                                       long long rows, long long cols, uint8_t* dst,
+                                                       long long pitch) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const long long words = pitch >> 4, total = rows * words;
+    for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total;
+         i += static_cast<long long>(gridDim.x) * 256) {
+        const long long r = i / words, c = (i - r * words) << 4;
+        const int n = static_cast<int>(min(16ll, cols - c));   // bytes of the row in this word
+        uint32_t o[4] = {0u, 0u, 0u, 0u};
+        if (n > 0) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(src + r * stride + c);
+            const int sh = static_cast<int>(a & 3u);
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(a - sh);
+            const int need = (sh + n + 3) >> 2;   // aligned words that hold a byte of the row
+            uint32_t v[5];
+#pragma unroll
+            for (int j = 0; j < 5; ++j) v[j] = j < need ? q[j] : 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                o[j] = __funnelshift_r(v[j], v[j + 1], 8 * sh);
+                const int left = n - 4 * j;   // bytes of this word inside the row
+                if (left < 4) o[j] = left <= 0 ? 0u : o[j] & ((1u << (8 * left)) - 1u);
+            }
+        }
+        *reinterpret_cast<uint4*>(dst + r * pitch + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+template <typename Kernel, typename... Args>
+cudaError_t launch_ex(Kernel kern, unsigned grid, unsigned threads, size_t smem, int cluster,
+                      cudaStream_t stream, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = overrides().pdl != 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <bool E4M3>
+cudaError_t launch_split(const CUtensorMap& w_map, const CUtensorMap& x_map, const SplitParams& s,
+                         const LinearPlan& plan, cudaStream_t stream) {
+    static std::atomic<int> smem_set[kMaxDevices];
+    cudaError_t e = ensure_dynamic_smem(linear_split_kernel<E4M3>, plan.smem, smem_set);
+    if (e != cudaSuccess) return e;
+    const long long grid = static_cast<long long>(plan.out_tiles) * plan.tok_tiles * plan.splits;
+    return launch_ex(linear_split_kernel<E4M3>, static_cast<unsigned>(grid), kThreads, plan.smem,
+                     plan.splits, stream, w_map, x_map, s);
 }
 
 }  // namespace
 
-cudaError_t launch_linear_w8a8(const LinearParams& p, cudaStream_t stream) {
-    const long long mt = (p.tokens + kT - 1) / kT;
-    const dim3 grid(static_cast<unsigned>((p.outputs + kT - 1) / kT),
-                    static_cast<unsigned>(mt < 65535 ? mt : 65535));
-    if (p.e4m3) linear_tile_kernel<true><<<grid, 256, 0, stream>>>(p);
-    else linear_tile_kernel<false><<<grid, 256, 0, stream>>>(p);
-    return cudaGetLastError();
+LinearPlan plan_linear(const LinearParams& p, int num_sms) {
+    LinearPlan r{};
+    r.tok_tiles = static_cast<int>((p.tokens + kMaxTok - 1) / kMaxTok);
+    const long long per = (p.tokens + r.tok_tiles - 1) / r.tok_tiles;
+    r.tok_tile = static_cast<int>((per + 15) / 16 * 16);
+    r.tok_tiles = static_cast<int>((p.tokens + r.tok_tile - 1) / r.tok_tile);
+    r.out_tiles = static_cast<int>((p.outputs + kRows - 1) / kRows);
+    const long long tiles = static_cast<long long>(r.tok_tiles) * r.out_tiles;
+    const long long k_steps = (p.width + kStep - 1) / kStep;
+    r.splits = 1;
+    while (r.splits < 8 && tiles * r.splits * 2 <= num_sms && r.splits * 2 <= k_steps) r.splits *= 2;
+    // rings within 200 KB: raw stages of both operands, converted tokens (f16)
+    const int stage = (kRows + r.tok_tile) * kStep, cvt = r.tok_tile * 256;
+    r.cvt_stages = p.e4m3 ? 0 : (r.tok_tile <= 64 ? kMaxCvt : 2);
+    r.stages = std::min(kMaxStages, (200 * 1024 - r.cvt_stages * cvt) / stage);
+    const long long per_rank = (k_steps + r.splits - 1) / r.splits;
+    r.stages = static_cast<int>(std::max<long long>(1, std::min<long long>(r.stages, per_rank)));
+    // the ring also holds the fp32 partial tile
+    const int ring = std::max(r.stages * stage, r.tok_tile * kRows * 4);
+    r.stages = std::max(r.stages, (ring + stage - 1) / stage);
+    r.smem = static_cast<size_t>(r.stages) * stage + static_cast<size_t>(r.cvt_stages) * cvt + kBarBytes +
+             32 + 1024;
+    return r;
+}
+
+cudaError_t launch_linear(const CUtensorMap* w_map, const CUtensorMap* x_map, const LinearParams& p,
+                          const LinearPlan& plan, cudaStream_t stream) {
+    SplitParams s{};
+    s.p = p;
+    s.tok_tile = plan.tok_tile;
+    s.out_tiles = plan.out_tiles;
+    s.splits = plan.splits;
+    s.k_steps = static_cast<int>((p.width + kStep - 1) / kStep);
+    s.stages = plan.stages;
+    s.cvt = plan.cvt_stages;
+    s.stage_bytes = static_cast<uint32_t>((kRows + plan.tok_tile) * kStep);
+    s.cvt_bytes = static_cast<uint32_t>(plan.tok_tile * 256);
+    return p.e4m3 ? launch_split<true>(*w_map, *x_map, s, plan, stream)
+                  : launch_split<false>(*w_map, *x_map, s, plan, stream);
+}
+
+cudaError_t launch_pad_rows(const uint8_t* src, long long stride, long long rows, long long cols,
+                            uint8_t* dst, long long pitch, cudaStream_t stream) {
+    const long long blocks = (rows * (pitch >> 4) + 255) / 256;
+    return launch_ex(pad_rows_kernel, static_cast<unsigned>(std::min(blocks, 152ll * 64)), 256, 0, 1,
+                     stream, src, stride, rows, cols, dst, pitch);
 }
 
 }  // namespace c3d

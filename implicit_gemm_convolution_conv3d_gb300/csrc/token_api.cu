@@ -44,6 +44,13 @@ const char* bad_rows(const void* p, int64_t stride, int64_t row, int64_t rows, i
     return nullptr;
 }
 
+long long round16(int64_t b) { return (b + 15) / 16 * 16; }
+
+// whether TMA can address these rows (one row has no stride to align)
+bool tma_rows(const void* p, int64_t stride, int64_t rows) {
+    return aligned_to(p, 16) && (rows == 1 || stride % 16 == 0);
+}
+
 }  // namespace
 
 }  // namespace c3d
@@ -132,15 +139,20 @@ int act_quant_fwd(const void* x, int x_dtype, int64_t x_stride, int act, int gat
     return launched(launch_act_quant(p, stream), "act_quant_fwd launch");
 }
 
-size_t linear_w8a8_workspace_size(const void*, int64_t, const void*, int64_t, int64_t, int64_t,
-                                  int64_t) {
-    return 0;
+size_t linear_w8a8_workspace_size(const void* x, int64_t x_stride, const void* w,
+                                  int64_t w_stride, int64_t tokens, int64_t outputs,
+                                  int64_t width) {
+    if (tokens < 1 || outputs < 1 || width < 1) return 0;
+    const size_t pitch = static_cast<size_t>(round16(width));
+    return (tma_rows(x, x_stride, tokens) ? 0 : pitch * static_cast<size_t>(tokens)) +
+           (tma_rows(w, w_stride, outputs) ? 0 : pitch * static_cast<size_t>(outputs));
 }
 
 int linear_w8a8_fwd(const void* x, int64_t x_stride, const void* w, int64_t w_stride, int dtype,
                     int64_t tokens, int64_t outputs, int64_t width, const float* scale_x,
                     const float* scale_w, const float* bias, int act, void* out, int out_dtype,
-                    int64_t out_stride, void*, size_t, cudaStream_t stream) {
+                    int64_t out_stride, void* workspace, size_t workspace_bytes,
+                    cudaStream_t stream) {
     if (tokens < 0 || tokens > kMaxDim || outputs < 0 || outputs > kMaxDim || width < 1 ||
         width > kMaxDim)
         return invalid("tokens and outputs must be 0 or more and width 1 or more, below 2^31");
@@ -170,7 +182,41 @@ int linear_w8a8_fwd(const void* x, int64_t x_stride, const void* w, int64_t w_st
     p.e4m3 = dtype == CONV_DTYPE_FP8_E4M3;
     p.act = act;
     p.out_dtype = out_dtype;
-    return launched(launch_linear_w8a8(p, stream), "linear_w8a8_fwd launch");
+    const size_t need = linear_w8a8_workspace_size(x, x_stride, w, w_stride, tokens, outputs, width);
+    if (need && (!workspace || workspace_bytes < need || !aligned_to(workspace, 16)))
+        return invalid("rows that are not 16-byte aligned need a 16-byte aligned workspace of "
+                       "linear_w8a8_workspace_size bytes");
+    LaunchLimits lim;
+    int rc = launch_limits(&lim);
+    if (rc) return rc;
+    p.status = lim.status;
+    p.wait_ns = lim.wait_ns;
+    // operands that TMA cannot address are copied to an aligned pitch first
+    const bool copy_x = !tma_rows(x, x_stride, tokens), copy_w = !tma_rows(w, w_stride, outputs);
+    const long long pitch = round16(width);
+    uint8_t* at = static_cast<uint8_t*>(workspace);
+    const uint8_t *src_x = p.x, *src_w = p.w;
+    if (copy_x) {
+        p.x = at;
+        at += pitch * tokens;
+    }
+    if (copy_w) p.w = at;
+    p.x_stride = copy_x || tokens == 1 ? pitch : x_stride;
+    p.w_stride = copy_w || outputs == 1 ? pitch : w_stride;
+    const LinearPlan plan = plan_linear(p, lim.num_sms);
+    if (static_cast<long long>(plan.out_tiles) * plan.tok_tiles > kMaxDim) {
+        set_last_error("the output has more than 2^31 tiles");
+        return CONV_ERR_UNSUPPORTED;
+    }
+    CUtensorMap xm, wm;
+    if ((rc = encode_rows_u8(&xm, p.x, width, tokens, p.x_stride, plan.tok_tile))) return rc;
+    if ((rc = encode_rows_u8(&wm, p.w, width, outputs, p.w_stride, 128))) return rc;
+    cudaError_t e = cudaSuccess;
+    if (copy_x) e = launch_pad_rows(src_x, x_stride, tokens, width, const_cast<uint8_t*>(p.x), pitch, stream);
+    if (e == cudaSuccess && copy_w)
+        e = launch_pad_rows(src_w, w_stride, outputs, width, const_cast<uint8_t*>(p.w), pitch, stream);
+    if (e == cudaSuccess) e = launch_linear(&wm, &xm, p, plan, stream);
+    return launched(e, "linear_w8a8_fwd launch");
 }
 
 }  // extern "C"

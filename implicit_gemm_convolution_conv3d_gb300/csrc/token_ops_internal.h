@@ -3,6 +3,7 @@
 #pragma once
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace c3d {
@@ -34,6 +35,7 @@ struct ActParams {
 };
 
 struct LinearParams {
+    // operands as the kernels read them: rows at 16-byte aligned pitches
     const uint8_t* x;
     const uint8_t* w;
     const float* scale_x;   // NULL: ones
@@ -43,10 +45,28 @@ struct LinearParams {
     long long x_stride, w_stride, out_stride;
     long long tokens, outputs, width;
     int e4m3, act, out_dtype;
+    int* status;            // device status word and the bound on every wait
+    unsigned long long wait_ns;
 };
+
+// How linear_w8a8_fwd runs a problem (plan_linear)
+struct LinearPlan {
+    int tok_tile;           // tokens of a tile
+    int out_tiles, tok_tiles;
+    int splits;             // CTAs of a cluster that share a tile's reduction
+    int stages, cvt_stages; // rings of TMA boxes and of converted (int8) operands
+    size_t smem;
+};
+LinearPlan plan_linear(const LinearParams& p, int num_sms);
 
 cudaError_t launch_norm_quant(const NormParams& p, cudaStream_t stream);
 cudaError_t launch_act_quant(const ActParams& p, cudaStream_t stream);
-cudaError_t launch_linear_w8a8(const LinearParams& p, cudaStream_t stream);
+cudaError_t launch_linear(const CUtensorMap* w_map, const CUtensorMap* x_map, const LinearParams& p,
+                          const LinearPlan& plan, cudaStream_t stream);
+
+// dst rows of `pitch` bytes (a multiple of 16, 16-byte aligned) from rows of
+// `cols` bytes `stride` apart, zeros behind each row
+cudaError_t launch_pad_rows(const uint8_t* src, long long stride, long long rows, long long cols,
+                            uint8_t* dst, long long pitch, cudaStream_t stream);
 
 }  // namespace c3d
