@@ -293,6 +293,12 @@ int launch_limits(LaunchLimits* l);
 int encode_rows_u8(CUtensorMap* m, const void* ptr, long long cols, long long rows, long long pitch,
                    int box_rows);
 
+// Tensor map of an output [rows, cols] of 2- or 4-byte elements, `pitch` bytes
+// between rows (base and pitch multiples of 16): boxes of 32 rows x 128 bytes in
+// the 128-byte swizzle.
+int encode_rows_out(CUtensorMap* m, const void* ptr, int elt, long long cols, long long rows,
+                    long long pitch);
+
 int* device_status_ptr();   // device address of the status word (current device)
 
 // The process's plan / path overrides (conv_set_overrides), copied under a

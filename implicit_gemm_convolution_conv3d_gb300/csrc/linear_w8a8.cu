@@ -377,6 +377,436 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// ---------------------------------------------------------------- paired tiles
+// Persistent CTA pairs, 256 tokens x up to 256 outputs a tile: the form for many
+// tokens.  Here the tokens are the MMA's row operand (128 per CTA) and each CTA
+// holds half of the tile's weight rows.
+//   warp 0       TMA producer
+//   warp 1       TMEM, MMA issuer (leader CTA)
+//   warps 4-11   epilogue: lane = token, 128 outputs a warp
+//   warps 12-15  int8: tokens to f16 into TMEM
+//   warps 16-19  int8: weights to f16 into shared memory
+// int8: the raw operands cross shared memory once as bytes; of their f16 form only
+// the weights do, as the tokens' goes to TMEM.  Per 64-element step of a CTA (512
+// cycles of MMA) shared memory moves 16 KB for the MMA's B, 16 KB raw in, 16 KB
+// raw out, 16 KB f16 in: 125 of its 128 bytes a cycle.  With both operands in
+// shared memory it would be 192.
+struct PairParams {
+    LinearParams p;
+    int bn;                   // outputs of a tile: a multiple of 32, at most 256
+    int m_tiles, n_tiles, group_m;
+    int k_steps, stages, cvt;
+    int nacc;                 // accumulators in TMEM
+    int staged;               // 4 KB staging buffers of an epilogue warp
+    int tma_out;              // output rows that TMA can address
+    FastDiv f_group, f_gm;
+};
+
+constexpr int kPairEpi = 256;                         // epilogue threads
+constexpr uint32_t kPairStage = 2u * kRows * kStep;   // raw bytes of a k-step and CTA
+constexpr uint32_t kPairCvt = kRows * kStep * 2u;     // f16 bytes of a k-step's weights
+constexpr int kPairThreads8 = 128 + kPairEpi, kPairThreadsI = kPairThreads8 + 256;
+constexpr uint32_t kTmemA = 256;                      // TMEM columns of the converted tokens
+
+// The activation of a chunk (out of line: one loop per activation).
+__device__ __noinline__ void act_chunk(uint32_t (&v)[32], int act, bool f32) {
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(f(__uint_as_float(v[j])));
+    };
+    if (act == kActRelu) each([](float y) { return y < 0.0f ? 0.0f : y; });
+    else if (f32) each([act](float y) { return activate_f32(y, act); });
+    else if (act == kActSilu) each([](float y) { return activate_c<kActSilu>(y); });
+    else each([](float y) { return activate_c<kActGelu>(y); });
+}
+
+struct PairTile {
+    int mt, nt;
+};
+
+// Groups of group_m token tiles, token tile fastest: the tiles in flight form a
+// near-square block, whose token and weight rows are read from L2.
+__device__ __forceinline__ PairTile pair_tile(int t, const PairParams& s) {
+    const int g = static_cast<int>(fdiv(static_cast<uint32_t>(t), s.f_group));
+    const int first = g * s.group_m, local = t - g * s.group_m * s.n_tiles;
+    const int gm = min(s.group_m, s.m_tiles - first);
+    const int nt = gm == s.group_m ? static_cast<int>(fdiv(static_cast<uint32_t>(local), s.f_gm)) : local / gm;
+    return PairTile{first + local - nt * gm, nt};
+}
+
+// Outputs that tile nt's MMAs compute: bn, or the rest rounded up to 32.
+__device__ __forceinline__ int pair_cols(int nt, const PairParams& s) {
+    const long long rest = s.p.outputs - static_cast<long long>(nt) * s.bn;
+    return rest >= s.bn ? s.bn : static_cast<int>((rest + 31) & ~31ll);
+}
+
+template <bool E4M3>
+__global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap x_map,
+                       const __grid_constant__ CUtensorMap w_map,
+                       const __grid_constant__ CUtensorMap o_map, const PairParams s) {
+    extern __shared__ __align__(1024) unsigned char smem_pair[];
+    const LinearParams& p = s.p;
+    const uint32_t ring = smem_u32(smem_pair);
+    const uint32_t cvt0 = ring + static_cast<uint32_t>(s.stages) * kPairStage;
+    const uint32_t epi0 = cvt0 + static_cast<uint32_t>(s.cvt) * kPairCvt;
+    const uint32_t cols0 = epi0 + static_cast<uint32_t>(s.staged) * 8u * 4096u;   // scale_w, bias
+    const uint32_t full0 = cols0 + 2048u, empty0 = full0 + 8u * kMaxStages;
+    const uint32_t cfull0 = empty0 + 8u * kMaxStages, cempty0 = cfull0 + 8u * kMaxCvt;
+    const uint32_t tfull0 = cempty0 + 8u * kMaxCvt, tempty0 = tfull0 + 16u;
+    const uint32_t drain_bar = tempty0 + 16u;
+    uint32_t* misc = reinterpret_cast<uint32_t*>(smem_pair + (drain_bar + 8u - ring));
+    volatile uint32_t* abort_flag = misc + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int tiles = s.m_tiles * s.n_tiles;
+    const int first = static_cast<int>(blockIdx.x) >> 1, stride = static_cast<int>(gridDim.x) >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < s.stages; ++i) {
+            mbar_init(full0 + 8 * i, 1);
+            mbar_init(empty0 + 8 * i, E4M3 ? 1 : 8);
+        }
+        for (int i = 0; i < s.cvt; ++i) {
+            mbar_init(cfull0 + 8 * i, 16);
+            mbar_init(cempty0 + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(tfull0 + 8 * i, 1);
+            mbar_init(tempty0 + 8 * i, 16);
+        }
+        mbar_init(drain_bar, 1);
+        misc[1] = 0u;
+        misc[2] = 0u;
+        misc[3] = 0u;
+        fence_mbar_init();
+        prefetch_tmap(&x_map);
+        prefetch_tmap(&w_map);
+        if (s.tma_out) prefetch_tmap(&o_map);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(misc), 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // both CTAs' barriers exist before any cross-CTA signal
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+    griddep_launch_dependents();
+    griddep_wait();
+
+    if (warp == 0) {
+        // ------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int st = 0;
+            uint32_t ph = 0, issued = 0;
+            bool ok = true;
+            for (int t = first; t < tiles && ok; t += stride) {
+                const PairTile tl = pair_tile(t, s);
+                const int m0 = tl.mt * 256 + rank * kRows;
+                const int n0 = tl.nt * s.bn + rank * (pair_cols(tl.nt, s) >> 1);
+                for (int i = 0; i < s.k_steps; ++i) {
+                    if (!wait_bar(empty0 + 8 * st, ph ^ 1u, abort_flag, p.status, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = ring + st * kPairStage;
+                    if (E4M3) {
+                        // the leader's barrier counts both CTAs' bytes
+                        if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * st, 2u * kPairStage);
+                        const uint32_t fb = mapa_shared(full0 + 8 * st, 0);
+                        tma_load_2d_pair(dst, &x_map, fb, i * kStep, m0);
+                        tma_load_2d_pair(dst + kRows * kStep, &w_map, fb, i * kStep, n0);
+                    } else {
+                        const uint32_t fb = full0 + 8 * st;
+                        mbar_arrive_expect_tx(fb, kPairStage);
+                        tma_load_2d(dst, &x_map, fb, i * kStep, m0);
+                        tma_load_2d(dst + kRows * kStep, &w_map, fb, i * kStep, n0);
+                    }
+                    misc[2] = ++issued;
+                    if (++st == s.stages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------ MMA issuer
+        if (lane == 0 && rank == 0) {
+            const uint64_t adesc = make_smem_desc(ring, 1024u, 2u);
+            const uint64_t bdesc = make_smem_desc(E4M3 ? ring + kRows * kStep : cvt0, 1024u, 2u);
+            const uint32_t step = (E4M3 ? kPairStage : kPairCvt) >> 4;
+            const uint32_t ready0 = E4M3 ? full0 : cfull0, free0 = E4M3 ? empty0 : cempty0;
+            const int depth = E4M3 ? s.stages : s.cvt;
+            int st = 0, it = 0;
+            uint32_t ph = 0, consumed = 0;
+            bool ok = true;
+            for (int t = first; t < tiles && ok; t += stride, ++it) {
+                const PairTile tl = pair_tile(t, s);
+                // D fp32, operands f16 (or e4m3: both codes are 0), N, M 256
+                const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(pair_cols(tl.nt, s) >> 3) << 17) |
+                                       ((256u >> 4) << 24);
+                const int acc = it % s.nacc;
+                const uint32_t aph = static_cast<uint32_t>(it / s.nacc) & 1u;
+                if (!wait_bar(tempty0 + 8 * acc, aph ^ 1u, abort_flag, p.status, p.wait_ns)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + static_cast<uint32_t>(acc * s.bn);
+                for (int i = 0; i < s.k_steps; ++i) {
+                    const uint32_t fb = ready0 + 8 * st;
+                    if (!mbar_try_wait_cluster(fb, ph)) {
+                        if (!wait_bar(fb, ph, abort_flag, p.status, p.wait_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_try_wait_cluster(fb, ph);   // complete: acquires at cluster scope
+                    }
+                    if (E4M3) misc[3] = ++consumed;
+                    tc_fence_after();
+                    const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(st) * step);
+                    if (E4M3) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc_mma_f8_pair(d, adesc + off + 2 * k, bdesc + off + 2 * k, idesc, (i | k) != 0);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            tc_mma_f16_ta_pair(d, tmem + kTmemA + st * 64 + k * 8,
+                                               bdesc + off + (k >> 2) * ((kRows * 128u) >> 4) + 2 * (k & 3),
+                                               idesc, (i | k) != 0);
+                    }
+                    tc_commit_pair(free0 + 8 * st, 3);
+                    if (++st == depth) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (ok) tc_commit_pair(tfull0 + 8 * acc, 3);
+            }
+        }
+    } else if (warp >= 4 && warp < 12) {
+        // ------------------------------------------------------ epilogue
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t tempty_dst = mapa_shared(tempty0, 0);
+        const uint32_t buf0 = epi0 + static_cast<uint32_t>((warp - 4) * s.staged) * 4096u;
+        // 32 scales and 32 biases of the chunk at hand, read as broadcasts
+        float* wcols = reinterpret_cast<float*>(smem_pair + (cols0 - ring)) + (warp - 4) * 64;
+        const bool f32 = p.out_dtype == kTokF32;
+        const int bcols = f32 ? 32 : 64;   // outputs of a 128-byte staged row
+        int it = 0, nbuf = 0;
+        for (int t = first; t < tiles; t += stride, ++it) {
+            const PairTile tl = pair_tile(t, s);
+            const int ncols = pair_cols(tl.nt, s);
+            const long long nbase = static_cast<long long>(tl.nt) * s.bn;
+            const long long m0 = static_cast<long long>(tl.mt) * 256 + rank * kRows + q * 32;
+            // this lane's scale and bias of each 32-column chunk
+            float csw[4], cbi[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = half * 128 + 32 * j + lane;
+                const bool in = c < ncols && nbase + c < p.outputs;
+                csw[j] = in && p.scale_w ? __ldg(p.scale_w + nbase + c) : 1.0f;
+                cbi[j] = in && p.bias ? __ldg(p.bias + nbase + c) : 0.0f;
+            }
+            const float sx = p.scale_x && m0 + lane < p.tokens ? __ldg(p.scale_x + m0 + lane) : 1.0f;
+            const int acc = it % s.nacc;
+            const uint32_t aph = static_cast<uint32_t>(it / s.nacc) & 1u;
+            if (!__all_sync(0xffffffffu,
+                            wait_bar(tfull0 + 8 * acc, aph, abort_flag, p.status, p.wait_ns)))
+                break;
+            tc_fence_after();
+            const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) +
+                                static_cast<uint32_t>(acc * s.bn);
+            const int c_end = min(ncols, (half + 1) * 128);
+            const bool rows_in = m0 < p.tokens;
+#pragma unroll
+            for (int cj = 0; cj < 4; ++cj) {
+                const int c = half * 128 + 32 * cj;
+                if (c >= c_end) break;
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(tb + c, v);
+                __syncwarp();
+                wcols[lane] = csw[cj];
+                wcols[32 + lane] = cbi[cj];
+                __syncwarp();
+                tmem_ld_wait();
+                if (c + 32 >= c_end) {   // the accumulator has been read
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(tempty_dst + 8 * acc);
+                }
+                if (!rows_in) continue;
+                const float4* sw4 = reinterpret_cast<const float4*>(wcols);
+                const float4* bi4 = reinterpret_cast<const float4*>(wcols + 32);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 sw = sw4[j], bi = bi4[j];
+                    const float f[4] = {sw.x, sw.y, sw.z, sw.w}, b[4] = {bi.x, bi.y, bi.z, bi.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[4 * j + i] = __float_as_uint(__uint_as_float(v[4 * j + i]) * sx * f[i] + b[i]);
+                }
+                if (p.act != kActNone) act_chunk(v, p.act, f32);
+                // staged rows of 128 bytes: 64 16-bit outputs (two chunks) or 32 of fp32
+                const int part = f32 ? 0 : (c >> 5) & 1;
+                const uint32_t buf = buf0 + static_cast<uint32_t>(nbuf % s.staged) * 4096u;
+                if (part == 0) {
+                    if (s.tma_out && lane == 0) {
+                        if (s.staged == 2) bulk_wait_read<1>();
+                        else bulk_wait_read<0>();
+                    }
+                    __syncwarp();
+                }
+                if (f32) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        sts128(buf + swz(lane, j), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            w[i] = pack2(__uint_as_float(v[8 * j + 2 * i]),
+                                         __uint_as_float(v[8 * j + 2 * i + 1]), p.out_dtype);
+                        sts128(buf + swz(lane, 4 * part + j), w[0], w[1], w[2], w[3]);
+                    }
+                    if (part == 0 && c + 32 < c_end) continue;
+                }
+                const int c0 = f32 ? c : c - 32 * part;   // the buffer's first column
+                if (s.tma_out) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        // columns and rows outside the output are not written
+                        tma_store_2d(&o_map, buf, static_cast<int>(nbase) + c0, static_cast<int>(m0));
+                        bulk_commit();
+                    }
+                } else {
+                    // rows that TMA cannot address: element stores, 32 columns at once
+                    __syncwarp();
+                    const int left = static_cast<int>(min(static_cast<long long>(min(bcols, c_end - c0)),
+                                                          p.outputs - nbase - c0));
+                    for (int r = 0; r < 32 && m0 + r < p.tokens; ++r) {
+                        const long long at = (m0 + r) * p.out_stride + nbase + c0;
+                        for (int j = lane; j < left; j += 32) {
+                            if (f32) {
+                                uint32_t x;
+                                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x)
+                                             : "r"(buf + swz(r, j >> 2) + 4u * (j & 3)) : "memory");
+                                static_cast<uint32_t*>(p.out)[at + j] = x;
+                            } else {
+                                uint16_t x;
+                                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x)
+                                             : "r"(buf + swz(r, j >> 3) + 2u * (j & 7)) : "memory");
+                                static_cast<uint16_t*>(p.out)[at + j] = x;
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+                ++nbuf;
+            }
+            if (half * 128 >= c_end) {   // a narrow tile has no columns for this half
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(tempty_dst + 8 * acc);
+            }
+        }
+        // the staging buffers are read out before the CTA leaves
+        if (s.tma_out && lane == 0) bulk_wait_read<0>();
+    } else if (!E4M3 && warp >= 12) {
+        // ------------------------------------------------------ converters (int8)
+        const uint32_t cfull_dst = mapa_shared(cfull0, 0);
+        int st = 0, c = 0;
+        uint32_t ph = 0, cph = 0, seen = 0;
+        const int total = first < tiles ? ((tiles - first + stride - 1) / stride) * s.k_steps : 0;
+        for (int i = 0; i < total; ++i) {
+            const bool ok = wait_bar(full0 + 8 * st, ph, abort_flag, p.status, p.wait_ns) &&
+                            wait_bar(cempty0 + 8 * c, cph ^ 1u, abort_flag, p.status, p.wait_ns);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (threadIdx.x == 12 * 32) misc[3] = ++seen;
+            const uint32_t src = ring + st * kPairStage;
+            if (warp < 16) {
+                tc_fence_after();
+                const int r = (warp & 3) * 32 + lane;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) cvt_chunk(lds128(src + swz(r, 4 * h + j)), v + 8 * j);
+                    tmem_st_32x32b_x32(tmem + kTmemA + (static_cast<uint32_t>((warp & 3) * 32) << 16) +
+                                           c * 64 + h * 32, v);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+            } else {
+                const uint32_t dst = cvt0 + c * kPairCvt;
+#pragma unroll 4
+                for (int u = threadIdx.x - 512; u < kRows * 8; u += 128) {
+                    const int r = u >> 3, ch = u & 7;
+                    uint32_t v[8];
+                    cvt_chunk(lds128(src + kRows * kStep + swz(r, ch)), v);
+                    const uint32_t box = dst + static_cast<uint32_t>((ch >> 2) * kRows) * 128u;
+                    // the second box's rows start at the first box's banks: its
+                    // halves go in the opposite order
+                    const int d = 2 * (ch & 3);
+                    if (ch < 4) {
+                        sts128(box + swz(r, d), v[0], v[1], v[2], v[3]);
+                        sts128(box + swz(r, d + 1), v[4], v[5], v[6], v[7]);
+                    } else {
+                        sts128(box + swz(r, d + 1), v[4], v[5], v[6], v[7]);
+                        sts128(box + swz(r, d), v[0], v[1], v[2], v[3]);
+                    }
+                }
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(empty0 + 8 * st);
+                mbar_arrive_cluster(cfull_dst + 8 * c);
+            }
+            if (++st == s.stages) {
+                st = 0;
+                ph ^= 1u;
+            }
+            if (++c == s.cvt) {
+                c = 0;
+                cph ^= 1u;
+            }
+        }
+    }
+
+    __syncthreads();
+    // both CTAs finish their roles before either drains, frees TMEM or leaves
+    cluster_sync();
+    if (*abort_flag) {
+        // a CTA's e4m3 loads signal the leader's barriers, so it cannot watch
+        // them land: after an abort ~100 us pass first
+        const long long t0 = clock64();
+        while (clock64() - t0 < 200000) {
+        }
+        if (threadIdx.x == 0 && (!E4M3 || rank == 0)) {
+            const uint32_t issued = misc[2], consumed = misc[3];
+            for (uint32_t i = consumed; i < issued; ++i)
+                drain_wait(full0 + 8 * (i % static_cast<uint32_t>(s.stages)),
+                           (i / static_cast<uint32_t>(s.stages)) & 1u);
+        }
+        if (warp == 1 && lane == 0 && rank == 0) {
+            tc_commit_pair(drain_bar, 1);
+            drain_wait(drain_bar, 0);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
 // Rows of any alignment copied to a 16-byte pitch, zeros behind each row: one
 // thread per 16-byte word, put together from the aligned 4-byte words that its
 // bytes lie in.
@@ -444,47 +874,101 @@ cudaError_t launch_split(const CUtensorMap& w_map, const CUtensorMap& x_map, con
                      plan.splits, stream, w_map, x_map, s);
 }
 
+template <bool E4M3>
+cudaError_t launch_pair(const LinearMaps& maps, const PairParams& s, const LinearPlan& plan,
+                        cudaStream_t stream) {
+    static std::atomic<int> smem_set[kMaxDevices];
+    cudaError_t e = ensure_dynamic_smem(linear_pair_kernel<E4M3>, plan.smem, smem_set);
+    if (e != cudaSuccess) return e;
+    return launch_ex(linear_pair_kernel<E4M3>, static_cast<unsigned>(plan.grid),
+                     E4M3 ? kPairThreads8 : kPairThreadsI, plan.smem, 2, stream, maps.x, maps.w,
+                     maps.out, s);
+}
+
+void plan_pair(const LinearParams& p, int num_sms, LinearPlan* r) {
+    r->pair = 1;
+    r->tok_tile = 256;
+    r->out_tile = 256;
+    r->tok_box = r->out_box = kRows;
+    r->tok_tiles = static_cast<int>((p.tokens + 255) / 256);
+    r->out_tiles = static_cast<int>((p.outputs + r->out_tile - 1) / r->out_tile);
+    r->splits = 1;
+    r->stages = p.e4m3 ? 6 : 3;
+    r->cvt_stages = p.e4m3 ? 0 : 2;
+    r->staged = p.e4m3 ? 1 : 2;
+    r->smem = static_cast<size_t>(r->stages) * kPairStage + static_cast<size_t>(r->cvt_stages) * kPairCvt +
+              static_cast<size_t>(r->staged) * 8 * 4096 + 2048 + kBarBytes + 32 + 32;
+    const long long tiles = static_cast<long long>(r->tok_tiles) * r->out_tiles;
+    r->grid = static_cast<int>(2 * std::min<long long>(tiles, num_sms / 2));
+}
+
+void plan_split(const LinearParams& p, int num_sms, LinearPlan* r) {
+    r->pair = 0;
+    r->tok_tiles = static_cast<int>((p.tokens + kMaxTok - 1) / kMaxTok);
+    const long long per = (p.tokens + r->tok_tiles - 1) / r->tok_tiles;
+    r->tok_tile = static_cast<int>((per + 15) / 16 * 16);
+    r->out_tile = r->out_box = kRows;
+    r->tok_box = r->tok_tile;
+    r->tok_tiles = static_cast<int>((p.tokens + r->tok_tile - 1) / r->tok_tile);
+    r->out_tiles = static_cast<int>((p.outputs + kRows - 1) / kRows);
+    const long long tiles = static_cast<long long>(r->tok_tiles) * r->out_tiles;
+    const long long k_steps = (p.width + kStep - 1) / kStep;
+    r->splits = 1;
+    while (r->splits < 8 && tiles * r->splits * 2 <= num_sms && r->splits * 2 <= k_steps) r->splits *= 2;
+    // rings within 200 KB: raw stages of both operands, converted tokens (f16)
+    const int stage = (kRows + r->tok_tile) * kStep, cvt = r->tok_tile * 256;
+    r->cvt_stages = p.e4m3 ? 0 : (r->tok_tile <= 64 ? kMaxCvt : 2);
+    r->stages = std::min(kMaxStages, (200 * 1024 - r->cvt_stages * cvt) / stage);
+    const long long per_rank = (k_steps + r->splits - 1) / r->splits;
+    r->stages = static_cast<int>(std::max<long long>(1, std::min<long long>(r->stages, per_rank)));
+    // the ring also holds the fp32 partial tile
+    const int ring = std::max(r->stages * stage, r->tok_tile * kRows * 4);
+    r->stages = std::max(r->stages, (ring + stage - 1) / stage);
+    r->smem = static_cast<size_t>(r->stages) * stage + static_cast<size_t>(r->cvt_stages) * cvt + kBarBytes +
+              32 + 1024;
+}
+
 }  // namespace
 
 LinearPlan plan_linear(const LinearParams& p, int num_sms) {
     LinearPlan r{};
-    r.tok_tiles = static_cast<int>((p.tokens + kMaxTok - 1) / kMaxTok);
-    const long long per = (p.tokens + r.tok_tiles - 1) / r.tok_tiles;
-    r.tok_tile = static_cast<int>((per + 15) / 16 * 16);
-    r.tok_tiles = static_cast<int>((p.tokens + r.tok_tile - 1) / r.tok_tile);
-    r.out_tiles = static_cast<int>((p.outputs + kRows - 1) / kRows);
-    const long long tiles = static_cast<long long>(r.tok_tiles) * r.out_tiles;
-    const long long k_steps = (p.width + kStep - 1) / kStep;
-    r.splits = 1;
-    while (r.splits < 8 && tiles * r.splits * 2 <= num_sms && r.splits * 2 <= k_steps) r.splits *= 2;
-    // rings within 200 KB: raw stages of both operands, converted tokens (f16)
-    const int stage = (kRows + r.tok_tile) * kStep, cvt = r.tok_tile * 256;
-    r.cvt_stages = p.e4m3 ? 0 : (r.tok_tile <= 64 ? kMaxCvt : 2);
-    r.stages = std::min(kMaxStages, (200 * 1024 - r.cvt_stages * cvt) / stage);
-    const long long per_rank = (k_steps + r.splits - 1) / r.splits;
-    r.stages = static_cast<int>(std::max<long long>(1, std::min<long long>(r.stages, per_rank)));
-    // the ring also holds the fp32 partial tile
-    const int ring = std::max(r.stages * stage, r.tok_tile * kRows * 4);
-    r.stages = std::max(r.stages, (ring + stage - 1) / stage);
-    r.smem = static_cast<size_t>(r.stages) * stage + static_cast<size_t>(r.cvt_stages) * cvt + kBarBytes +
-             32 + 1024;
+    if (p.tokens > 512) plan_pair(p, num_sms, &r);
+    else plan_split(p, num_sms, &r);
     return r;
 }
 
-cudaError_t launch_linear(const CUtensorMap* w_map, const CUtensorMap* x_map, const LinearParams& p,
-                          const LinearPlan& plan, cudaStream_t stream) {
+cudaError_t launch_linear(const LinearMaps& maps, const LinearParams& p, const LinearPlan& plan,
+                          cudaStream_t stream) {
+    const int k_steps = static_cast<int>((p.width + kStep - 1) / kStep);
+    if (plan.pair) {
+        PairParams s{};
+        s.p = p;
+        s.bn = plan.out_tile;
+        s.m_tiles = plan.tok_tiles;
+        s.n_tiles = plan.out_tiles;
+        s.group_m = 8;
+        s.k_steps = k_steps;
+        s.stages = plan.stages;
+        s.cvt = plan.cvt_stages;
+        s.nacc = p.e4m3 ? 512 / s.bn >= 2 ? 2 : 1 : static_cast<int>(kTmemA) / s.bn >= 2 ? 2 : 1;
+        s.staged = plan.staged;
+        s.tma_out = plan.tma_out;
+        s.f_group = make_fastdiv(static_cast<uint32_t>(s.group_m * s.n_tiles));
+        s.f_gm = make_fastdiv(static_cast<uint32_t>(s.group_m));
+        return p.e4m3 ? launch_pair<true>(maps, s, plan, stream) : launch_pair<false>(maps, s, plan, stream);
+    }
     SplitParams s{};
     s.p = p;
     s.tok_tile = plan.tok_tile;
     s.out_tiles = plan.out_tiles;
     s.splits = plan.splits;
-    s.k_steps = static_cast<int>((p.width + kStep - 1) / kStep);
+    s.k_steps = k_steps;
     s.stages = plan.stages;
     s.cvt = plan.cvt_stages;
     s.stage_bytes = static_cast<uint32_t>((kRows + plan.tok_tile) * kStep);
     s.cvt_bytes = static_cast<uint32_t>(plan.tok_tile * 256);
-    return p.e4m3 ? launch_split<true>(*w_map, *x_map, s, plan, stream)
-                  : launch_split<false>(*w_map, *x_map, s, plan, stream);
+    return p.e4m3 ? launch_split<true>(maps.w, maps.x, s, plan, stream)
+                  : launch_split<false>(maps.w, maps.x, s, plan, stream);
 }
 
 cudaError_t launch_pad_rows(const uint8_t* src, long long stride, long long rows, long long cols,

@@ -203,19 +203,24 @@ int linear_w8a8_fwd(const void* x, int64_t x_stride, const void* w, int64_t w_st
     if (copy_w) p.w = at;
     p.x_stride = copy_x || tokens == 1 ? pitch : x_stride;
     p.w_stride = copy_w || outputs == 1 ? pitch : w_stride;
-    const LinearPlan plan = plan_linear(p, lim.num_sms);
-    if (static_cast<long long>(plan.out_tiles) * plan.tok_tiles > kMaxDim) {
+    LinearPlan plan = plan_linear(p, lim.num_sms);
+    if (static_cast<long long>(plan.out_tiles) * plan.tok_tiles * plan.splits > kMaxDim) {
         set_last_error("the output has more than 2^31 tiles");
         return CONV_ERR_UNSUPPORTED;
     }
-    CUtensorMap xm, wm;
-    if ((rc = encode_rows_u8(&xm, p.x, width, tokens, p.x_stride, plan.tok_tile))) return rc;
-    if ((rc = encode_rows_u8(&wm, p.w, width, outputs, p.w_stride, 128))) return rc;
+    const long long elt = size_of(out_dtype);
+    plan.tma_out = aligned_to(out, 16) && (tokens == 1 || out_stride * elt % 16 == 0);
+    LinearMaps maps{};
+    if ((rc = encode_rows_u8(&maps.x, p.x, width, tokens, p.x_stride, plan.tok_box))) return rc;
+    if ((rc = encode_rows_u8(&maps.w, p.w, width, outputs, p.w_stride, plan.out_box))) return rc;
+    if (plan.pair && plan.tma_out &&
+        (rc = encode_rows_out(&maps.out, out, static_cast<int>(elt), outputs, tokens, out_stride * elt)))
+        return rc;
     cudaError_t e = cudaSuccess;
     if (copy_x) e = launch_pad_rows(src_x, x_stride, tokens, width, const_cast<uint8_t*>(p.x), pitch, stream);
     if (e == cudaSuccess && copy_w)
         e = launch_pad_rows(src_w, w_stride, outputs, width, const_cast<uint8_t*>(p.w), pitch, stream);
-    if (e == cudaSuccess) e = launch_linear(&wm, &xm, p, plan, stream);
+    if (e == cudaSuccess) e = launch_linear(maps, p, plan, stream);
     return launched(e, "linear_w8a8_fwd launch");
 }
 

@@ -51,18 +51,27 @@ struct LinearParams {
 
 // How linear_w8a8_fwd runs a problem (plan_linear)
 struct LinearPlan {
-    int tok_tile;           // tokens of a tile
+    int pair;               // CTA-pair kernel for many tokens, else the split kernel
+    int tok_tile, out_tile; // tokens and outputs of a tile
+    int tok_box, out_box;   // rows of a TMA box of either operand
     int out_tiles, tok_tiles;
-    int splits;             // CTAs of a cluster that share a tile's reduction
+    int splits;             // split: CTAs of a cluster that share a tile's reduction
     int stages, cvt_stages; // rings of TMA boxes and of converted (int8) operands
+    int staged;             // pair: 4 KB output staging buffers of a warp
+    int tma_out;            // pair: the output's rows can be stored by TMA
+    int grid;               // pair: CTAs
     size_t smem;
 };
 LinearPlan plan_linear(const LinearParams& p, int num_sms);
 
+struct LinearMaps {
+    CUtensorMap x, w, out;  // out: pair kernel with tma_out only
+};
+
 cudaError_t launch_norm_quant(const NormParams& p, cudaStream_t stream);
 cudaError_t launch_act_quant(const ActParams& p, cudaStream_t stream);
-cudaError_t launch_linear(const CUtensorMap* w_map, const CUtensorMap* x_map, const LinearParams& p,
-                          const LinearPlan& plan, cudaStream_t stream);
+cudaError_t launch_linear(const LinearMaps& maps, const LinearParams& p, const LinearPlan& plan,
+                          cudaStream_t stream);
 
 // dst rows of `pitch` bytes (a multiple of 16, 16-byte aligned) from rows of
 // `cols` bytes `stride` apart, zeros behind each row
