@@ -383,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // holds half of the tile's weight rows.
 //   warp 0       TMA producer
 //   warp 1       TMEM, MMA issuer (leader CTA)
+//   warp 2       int8: tells the leader that this CTA's converters are done
 //   warps 4-11   epilogue: lane = token, 128 outputs a warp
 //   warps 12-15  int8: tokens to f16 into TMEM
 //   warps 16-19  int8: weights to f16 into shared memory
@@ -408,16 +409,31 @@ constexpr uint32_t kPairCvt = kRows * kStep * 2u;     // f16 bytes of a k-step's
 constexpr int kPairThreads8 = 128 + kPairEpi, kPairThreadsI = kPairThreads8 + 256;
 constexpr uint32_t kTmemA = 256;                      // TMEM columns of the converted tokens
 
-// The activation of a chunk (out of line: one loop per activation).
-__device__ __noinline__ void act_chunk(uint32_t (&v)[32], int act, bool f32) {
+// The activation of a chunk.  The fp32 forms are long: out of line, on a copy,
+// so that only their callers' values go through memory.
+__device__ __noinline__ void act_chunk_f32(float (&y)[32], int act) {
+    for (int j = 0; j < 32; ++j) y[j] = activate_f32(y[j], act);
+}
+
+__device__ __forceinline__ void act_chunk(uint32_t (&v)[32], int act, bool f32) {
     auto each = [&](auto f) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(f(__uint_as_float(v[j])));
     };
-    if (act == kActRelu) each([](float y) { return y < 0.0f ? 0.0f : y; });
-    else if (f32) each([act](float y) { return activate_f32(y, act); });
-    else if (act == kActSilu) each([](float y) { return activate_c<kActSilu>(y); });
-    else each([](float y) { return activate_c<kActGelu>(y); });
+    if (act == kActRelu) {
+        each([](float y) { return y < 0.0f ? 0.0f : y; });
+    } else if (f32) {
+        float y[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(v[j]);
+        act_chunk_f32(y, act);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(y[j]);
+    } else if (act == kActSilu) {
+        each([](float y) { return activate_c<kActSilu>(y); });
+    } else {
+        each([](float y) { return activate_c<kActGelu>(y); });
+    }
 }
 
 struct PairTile {
@@ -453,7 +469,8 @@ __global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
     const uint32_t cols0 = epi0 + static_cast<uint32_t>(s.staged) * 8u * 4096u;   // scale_w, bias
     const uint32_t full0 = cols0 + 2048u, empty0 = full0 + 8u * kMaxStages;
     const uint32_t cfull0 = empty0 + 8u * kMaxStages, cempty0 = cfull0 + 8u * kMaxCvt;
-    const uint32_t tfull0 = cempty0 + 8u * kMaxCvt, tempty0 = tfull0 + 16u;
+    const uint32_t clocal0 = cempty0 + 8u * kMaxCvt;
+    const uint32_t tfull0 = clocal0 + 8u * kMaxCvt, tempty0 = tfull0 + 16u;
     const uint32_t drain_bar = tempty0 + 16u;
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem_pair + (drain_bar + 8u - ring));
     volatile uint32_t* abort_flag = misc + 1;
@@ -469,8 +486,9 @@ __global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
             mbar_init(empty0 + 8 * i, E4M3 ? 1 : 8);
         }
         for (int i = 0; i < s.cvt; ++i) {
-            mbar_init(cfull0 + 8 * i, 16);
+            mbar_init(cfull0 + 8 * i, 2);
             mbar_init(cempty0 + 8 * i, 1);
+            mbar_init(clocal0 + 8 * i, 8);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull0 + 8 * i, 1);
@@ -584,6 +602,27 @@ __global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
                     }
                 }
                 if (ok) tc_commit_pair(tfull0 + 8 * acc, 3);
+            }
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------ relay (int8)
+        // A CTA's converted stage is signalled to the leader by one arrival: a
+        // release at cluster scope waits for all of its thread's stores, which
+        // every converter warp would pay per step
+        if (!E4M3 && lane == 0) {
+            const uint32_t dst = mapa_shared(cfull0, 0);
+            const int total = first < tiles ? ((tiles - first + stride - 1) / stride) * s.k_steps : 0;
+            int c = 0;
+            uint32_t cph = 0;
+            for (int i = 0; i < total; ++i) {
+                if (!wait_bar(clocal0 + 8 * c, cph, abort_flag, p.status, p.wait_ns)) break;
+                tc_fence_after();
+                tc_fence_before();
+                mbar_arrive_cluster(dst + 8 * c);
+                if (++c == s.cvt) {
+                    c = 0;
+                    cph ^= 1u;
+                }
             }
         }
     } else if (warp >= 4 && warp < 12) {
@@ -718,7 +757,6 @@ __global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
         if (s.tma_out && lane == 0) bulk_wait_read<0>();
     } else if (!E4M3 && warp >= 12) {
         // ------------------------------------------------------ converters (int8)
-        const uint32_t cfull_dst = mapa_shared(cfull0, 0);
         int st = 0, c = 0;
         uint32_t ph = 0, cph = 0, seen = 0;
         const int total = first < tiles ? ((tiles - first + stride - 1) / stride) * s.k_steps : 0;
@@ -765,7 +803,7 @@ __global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(empty0 + 8 * st);
-                mbar_arrive_cluster(cfull_dst + 8 * c);
+                mbar_arrive(clocal0 + 8 * c);
             }
             if (++st == s.stages) {
                 st = 0;
@@ -894,10 +932,10 @@ void plan_pair(const LinearParams& p, int num_sms, LinearPlan* r) {
     r->out_tiles = static_cast<int>((p.outputs + r->out_tile - 1) / r->out_tile);
     r->splits = 1;
     r->stages = p.e4m3 ? 6 : 3;
-    r->cvt_stages = p.e4m3 ? 0 : 2;
-    r->staged = p.e4m3 ? 1 : 2;
+    r->cvt_stages = p.e4m3 ? 0 : 3;
+    r->staged = 1;
     r->smem = static_cast<size_t>(r->stages) * kPairStage + static_cast<size_t>(r->cvt_stages) * kPairCvt +
-              static_cast<size_t>(r->staged) * 8 * 4096 + 2048 + kBarBytes + 32 + 32;
+              static_cast<size_t>(r->staged) * 8 * 4096 + 2048 + kBarBytes + 8 * kMaxCvt + 32 + 32;
     const long long tiles = static_cast<long long>(r->tok_tiles) * r->out_tiles;
     r->grid = static_cast<int>(2 * std::min<long long>(tiles, num_sms / 2));
 }
