@@ -1223,31 +1223,22 @@ int launch_limits(LaunchLimits* l) {
     return CONV_OK;
 }
 
-int encode_rows_u8(CUtensorMap* m, const void* ptr, long long cols, long long rows, long long pitch,
-                   int box_rows) {
+int encode_rows(CUtensorMap* m, const void* ptr, int elt, long long cols, long long rows,
+                long long pitch, int box_rows) {
     if (!load_entry_points()) {
         set_error("the driver's tensor-map encoders are not available");
         return CONV_ERR_CUDA;
     }
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
-    const cuuint32_t box[2] = {128u, static_cast<cuuint32_t>(box_rows)};
-    return encode_tiled(m, 1, 2, ptr, dims, strides, box, 128);
-}
-
-int encode_rows_out(CUtensorMap* m, const void* ptr, int elt, long long cols, long long rows,
-                    long long pitch) {
-    if (!load_entry_points()) {
-        set_error("the driver's tensor-map encoders are not available");
-        return CONV_ERR_CUDA;
-    }
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elt), 32u}, es[2] = {1u, 1u};
-    CUresult r = g_encode_tiled(m, elt == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
-                                2, const_cast<void*>(ptr), dims, strides, box, es,
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elt), static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t es[2] = {1u, 1u};
+    const CUtensorMapDataType type = elt == 4   ? CU_TENSOR_MAP_DATA_TYPE_UINT32
+                                     : elt == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16
+                                                : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    CUresult r = g_encode_tiled(m, type, 2, const_cast<void*>(ptr), dims, strides, box, es,
                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         set_error("cuTensorMapEncodeTiled failed (code %s%lld)", "", static_cast<long long>(r));
         return CONV_ERR_CUDA;

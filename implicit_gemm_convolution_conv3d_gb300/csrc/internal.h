@@ -287,17 +287,11 @@ struct LaunchLimits {
 };
 int launch_limits(LaunchLimits* l);
 
-// Tensor map of a byte matrix [rows, cols] with `pitch` bytes between rows
-// (base and pitch multiples of 16): boxes of 128 columns x box_rows rows in the
-// 128-byte swizzle, zeros outside the matrix.
-int encode_rows_u8(CUtensorMap* m, const void* ptr, long long cols, long long rows, long long pitch,
-                   int box_rows);
-
-// Tensor map of an output [rows, cols] of 2- or 4-byte elements, `pitch` bytes
-// between rows (base and pitch multiples of 16): boxes of 32 rows x 128 bytes in
-// the 128-byte swizzle.
-int encode_rows_out(CUtensorMap* m, const void* ptr, int elt, long long cols, long long rows,
-                    long long pitch);
+// Tensor map of a matrix [rows, cols] of 1-, 2- or 4-byte elements, `pitch` bytes
+// between rows (base and pitch multiples of 16): boxes of box_rows rows x 128
+// bytes in the 128-byte swizzle, zeros outside the matrix.
+int encode_rows(CUtensorMap* m, const void* ptr, int elt, long long cols, long long rows,
+                long long pitch, int box_rows);
 
 int* device_status_ptr();   // device address of the status word (current device)
 

@@ -26,6 +26,30 @@ constexpr int kThreads = 128 + kCvtThreads;
 constexpr int kMaxStages = 8, kMaxCvt = 4;
 constexpr uint32_t kBarBytes = 16u * (kMaxStages + kMaxCvt) + 16u;
 
+// Bounded wait (see wait_bar) of a role that may wait for thousands of cycles:
+// it sleeps in hardware between looks, so that its polling leaves the issue slots
+// to the converters and the epilogue.
+__device__ __noinline__ bool wait_long_slow(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                            int* status, unsigned long long limit_ns) {
+    const long long t0 = clock64();
+    const long long limit = static_cast<long long>(limit_ns > (1ull << 61) ? (1ull << 61) : limit_ns) * 2;
+    while (!mbar_try_wait_for(bar, parity, 100000u)) {
+        if (*abort_flag) return false;
+        if (clock64() - t0 > limit) {
+            *abort_flag = 1u;
+            atomicExch(status, kStatusTimeout);
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                          int* status, unsigned long long limit_ns) {
+    return mbar_try_wait_for(bar, parity, 100000u) ||
+           wait_long_slow(bar, parity, abort_flag, status, limit_ns);
+}
+
 // The byte of the 16-byte chunk `c` of row `r` in a 128-byte-swizzled tile.
 __device__ __forceinline__ uint32_t swz(int r, int c) {
     return static_cast<uint32_t>(r) * 128u + (static_cast<uint32_t>(c ^ (r & 7)) << 4);
@@ -69,6 +93,25 @@ __device__ __forceinline__ void cvt_chunk(const uint4& v, uint32_t* o) {
     i8x4_to_f16x4(v.y, o[2], o[3]);
     i8x4_to_f16x4(v.z, o[4], o[5]);
     i8x4_to_f16x4(v.w, o[6], o[7]);
+}
+
+// A k-step of `rows` int8 rows (a multiple of 16; 128 bytes each, swizzled) as two
+// boxes of f16 rows (64 elements each, swizzled), by `threads` threads.  Eight
+// threads that share a shared-memory cycle take four neighbouring chunks of row
+// r and of row r^5: bit 2 keeps their reads, bit 0 their writes off each other's
+// banks.
+__device__ __forceinline__ void cvt_rows(uint32_t src, uint32_t dst, int rows, int t,
+                                         int threads) {
+    const int c4 = t & 3, flip = (t & 4) ? 5 : 0;
+#pragma unroll 4
+    for (int u = t >> 3; u < rows; u += threads >> 3) {
+        const int h = 2 * u >= rows, r = (2 * u - (h ? rows : 0)) ^ flip;
+        uint32_t v[8];
+        cvt_chunk(lds128(src + swz(r, 4 * h + c4)), v);
+        const uint32_t box = dst + static_cast<uint32_t>(h * rows) * 128u;
+        sts128(box + swz(r, 2 * c4), v[0], v[1], v[2], v[3]);
+        sts128(box + swz(r, 2 * c4 + 1), v[4], v[5], v[6], v[7]);
+    }
 }
 
 // Epilogue activation: the convolutions' forms for 16-bit outputs, the
@@ -251,23 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_st_wait();
                     tc_fence_before();
                 } else {
-                    const uint32_t dst = cvt0 + c * s.cvt_bytes;
-                    for (int u = threadIdx.x - 256; u < nt * 8; u += 128) {
-                        const int r = u >> 3, ch = u & 7;
-                        uint32_t v[8];
-                        cvt_chunk(lds128(src + kRows * kStep + swz(r, ch)), v);
-                        const uint32_t box = dst + static_cast<uint32_t>((ch >> 2) * nt) * 128u;
-                        // the two halves in opposite order in the second box:
-                        // its rows start at the first box's banks
-                        const int d = 2 * (ch & 3);
-                        if (ch < 4) {
-                            sts128(box + swz(r, d), v[0], v[1], v[2], v[3]);
-                            sts128(box + swz(r, d + 1), v[4], v[5], v[6], v[7]);
-                        } else {
-                            sts128(box + swz(r, d + 1), v[4], v[5], v[6], v[7]);
-                            sts128(box + swz(r, d), v[0], v[1], v[2], v[3]);
-                        }
-                    }
+                    cvt_rows(src + kRows * kStep, cvt0 + c * s.cvt_bytes, nt, threadIdx.x - 256, 128);
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
@@ -385,29 +412,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   warp 1       TMEM, MMA issuer (leader CTA)
 //   warp 2       int8: tells the leader that this CTA's converters are done
 //   warps 4-11   epilogue: lane = token, 128 outputs a warp
-//   warps 12-15  int8: tokens to f16 into TMEM
-//   warps 16-19  int8: weights to f16 into shared memory
-// int8: the raw operands cross shared memory once as bytes; of their f16 form only
-// the weights do, as the tokens' goes to TMEM.  Per 64-element step of a CTA (512
-// cycles of MMA) shared memory moves 16 KB for the MMA's B, 16 KB raw in, 16 KB
-// raw out, 16 KB f16 in: 125 of its 128 bytes a cycle.  With both operands in
-// shared memory it would be 192.
+//   warps 12-19  int8: tokens to f16 into TMEM, two groups on alternate k-steps
+// int8: the tokens cross shared memory once as bytes (their f16 form goes to
+// TMEM); the weights come as f16 from the workspace, where one short launch has
+// put them.  What decides this is shared memory, 128 bytes a cycle: per k-step (1024 cycles of
+// MMA) it moves 16 KB of raw tokens in and out, 32 KB of weights in and 32 KB
+// of the MMA's reads, 96 bytes a cycle.  Converting the weights here too
+// takes 128 (raw in and out, f16 in and out), and measured 1475 TFLOP/s at
+// 16384 x 8192 x 8192 against WIDE_TFLOPS; the launch reads and writes 3 bytes per weight.
 struct PairParams {
     LinearParams p;
-    int bn;                   // outputs of a tile: a multiple of 32, at most 256
+    int bn;                   // outputs of a tile: a multiple of 64, at most 256
     int m_tiles, n_tiles, group_m;
-    int k_steps, stages, cvt;
+    int k_steps, stages;
     int nacc;                 // accumulators in TMEM
-    int staged;               // 4 KB staging buffers of an epilogue warp
     int tma_out;              // output rows that TMA can address
     FastDiv f_group, f_gm;
 };
 
-constexpr int kPairEpi = 256;                         // epilogue threads
-constexpr uint32_t kPairStage = 2u * kRows * kStep;   // raw bytes of a k-step and CTA
-constexpr uint32_t kPairCvt = kRows * kStep * 2u;     // f16 bytes of a k-step's weights
-constexpr int kPairThreads8 = 128 + kPairEpi, kPairThreadsI = kPairThreads8 + 256;
-constexpr uint32_t kTmemA = 256;                      // TMEM columns of the converted tokens
+constexpr int kPairEpi = 256;                             // epilogue threads
+constexpr uint32_t kTokBytes = kRows * kStep;             // tokens of a k-step and CTA
+constexpr uint32_t kTmemA = 256;                          // TMEM columns of the converted tokens
+template <bool E4M3>
+struct PairShape {
+    static constexpr uint32_t kWBytes = kRows * kStep * (E4M3 ? 1u : 2u);   // weights of a k-step
+    static constexpr uint32_t kStage = kTokBytes + kWBytes;
+    static constexpr int kStages = E4M3 ? 6 : 4;
+    static constexpr int kThreads = 128 + kPairEpi + (E4M3 ? 0 : 256);
+};
 
 // The activation of a chunk.  The fp32 forms are long: out of line, on a copy,
 // so that only their callers' values go through memory.
@@ -457,22 +489,27 @@ __device__ __forceinline__ int pair_cols(int nt, const PairParams& s) {
 }
 
 template <bool E4M3>
-__global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
+__global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap x_map,
                        const __grid_constant__ CUtensorMap w_map,
                        const __grid_constant__ CUtensorMap o_map, const PairParams s) {
+    using Shape = PairShape<E4M3>;
     extern __shared__ __align__(1024) unsigned char smem_pair[];
     const LinearParams& p = s.p;
     const uint32_t ring = smem_u32(smem_pair);
-    const uint32_t cvt0 = ring + static_cast<uint32_t>(s.stages) * kPairStage;
-    const uint32_t epi0 = cvt0 + static_cast<uint32_t>(s.cvt) * kPairCvt;
-    const uint32_t cols0 = epi0 + static_cast<uint32_t>(s.staged) * 8u * 4096u;   // scale_w, bias
-    const uint32_t full0 = cols0 + 2048u, empty0 = full0 + 8u * kMaxStages;
-    const uint32_t cfull0 = empty0 + 8u * kMaxStages, cempty0 = cfull0 + 8u * kMaxCvt;
-    const uint32_t clocal0 = cempty0 + 8u * kMaxCvt;
-    const uint32_t tfull0 = clocal0 + 8u * kMaxCvt, tempty0 = tfull0 + 16u;
+    const uint32_t epi0 = ring + static_cast<uint32_t>(s.stages) * Shape::kStage;
+    const uint32_t cols0 = epi0 + 8u * 4096u;             // scale_w, bias
+    // wfull: both CTAs' weights (and e4m3 tokens), on the leader; xfull: this
+    // CTA's int8 tokens; xcvt: its 4 converter warps; ready: both CTAs' relays,
+    // on the leader; empty: the stage's MMAs
+    const uint32_t wfull0 = cols0 + 2048u, xfull0 = wfull0 + 8u * kMaxStages;
+    const uint32_t xcvt0 = xfull0 + 8u * kMaxStages, ready0 = xcvt0 + 8u * kMaxStages;
+    const uint32_t empty0 = ready0 + 8u * kMaxStages;
+    const uint32_t tfull0 = empty0 + 8u * kMaxStages, tempty0 = tfull0 + 16u;
     const uint32_t drain_bar = tempty0 + 16u;
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem_pair + (drain_bar + 8u - ring));
+    // misc[0] TMEM base, [1] abort flag, [2] k-steps issued, [3] k-steps whose
+    // weights, [4] whose tokens were waited for
     volatile uint32_t* abort_flag = misc + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -482,22 +519,18 @@ __global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < s.stages; ++i) {
-            mbar_init(full0 + 8 * i, 1);
-            mbar_init(empty0 + 8 * i, E4M3 ? 1 : 8);
-        }
-        for (int i = 0; i < s.cvt; ++i) {
-            mbar_init(cfull0 + 8 * i, 2);
-            mbar_init(cempty0 + 8 * i, 1);
-            mbar_init(clocal0 + 8 * i, 8);
+            mbar_init(wfull0 + 8 * i, 1);
+            mbar_init(xfull0 + 8 * i, 1);
+            mbar_init(xcvt0 + 8 * i, 4);
+            mbar_init(ready0 + 8 * i, 2);
+            mbar_init(empty0 + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull0 + 8 * i, 1);
             mbar_init(tempty0 + 8 * i, 16);
         }
         mbar_init(drain_bar, 1);
-        misc[1] = 0u;
-        misc[2] = 0u;
-        misc[3] = 0u;
+        for (int i = 1; i < 5; ++i) misc[i] = 0u;
         fence_mbar_init();
         prefetch_tmap(&x_map);
         prefetch_tmap(&w_map);
@@ -514,6 +547,8 @@ __global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
     const uint32_t tmem = misc[0];
     griddep_launch_dependents();
     griddep_wait();
+    // k-steps of this pair's tiles
+    const int total = first < tiles ? ((tiles - first + stride - 1) / stride) * s.k_steps : 0;
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
@@ -526,22 +561,24 @@ __global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
                 const int m0 = tl.mt * 256 + rank * kRows;
                 const int n0 = tl.nt * s.bn + rank * (pair_cols(tl.nt, s) >> 1);
                 for (int i = 0; i < s.k_steps; ++i) {
-                    if (!wait_bar(empty0 + 8 * st, ph ^ 1u, abort_flag, p.status, p.wait_ns)) {
+                    if (!wait_long(empty0 + 8 * st, ph ^ 1u, abort_flag, p.status, p.wait_ns)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = ring + st * kPairStage;
+                    const uint32_t dst = ring + st * Shape::kStage;
+                    // the leader's barrier counts both CTAs' bytes
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(wfull0 + 8 * st, 2u * (E4M3 ? Shape::kStage : Shape::kWBytes));
+                    const uint32_t fb = mapa_shared(wfull0 + 8 * st, 0);
                     if (E4M3) {
-                        // the leader's barrier counts both CTAs' bytes
-                        if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * st, 2u * kPairStage);
-                        const uint32_t fb = mapa_shared(full0 + 8 * st, 0);
                         tma_load_2d_pair(dst, &x_map, fb, i * kStep, m0);
-                        tma_load_2d_pair(dst + kRows * kStep, &w_map, fb, i * kStep, n0);
+                        tma_load_2d_pair(dst + kTokBytes, &w_map, fb, i * kStep, n0);
                     } else {
-                        const uint32_t fb = full0 + 8 * st;
-                        mbar_arrive_expect_tx(fb, kPairStage);
-                        tma_load_2d(dst, &x_map, fb, i * kStep, m0);
-                        tma_load_2d(dst + kRows * kStep, &w_map, fb, i * kStep, n0);
+                        mbar_arrive_expect_tx(xfull0 + 8 * st, kTokBytes);
+                        tma_load_2d(dst, &x_map, xfull0 + 8 * st, i * kStep, m0);
+                        // f16: two boxes of 64 elements
+                        tma_load_2d_pair(dst + kTokBytes, &w_map, fb, i * kStep, n0);
+                        tma_load_2d_pair(dst + 2 * kTokBytes, &w_map, fb, i * kStep + 64, n0);
                     }
                     misc[2] = ++issued;
                     if (++st == s.stages) {
@@ -555,10 +592,7 @@ __global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
         // ------------------------------------------------------ MMA issuer
         if (lane == 0 && rank == 0) {
             const uint64_t adesc = make_smem_desc(ring, 1024u, 2u);
-            const uint64_t bdesc = make_smem_desc(E4M3 ? ring + kRows * kStep : cvt0, 1024u, 2u);
-            const uint32_t step = (E4M3 ? kPairStage : kPairCvt) >> 4;
-            const uint32_t ready0 = E4M3 ? full0 : cfull0, free0 = E4M3 ? empty0 : cempty0;
-            const int depth = E4M3 ? s.stages : s.cvt;
+            const uint64_t bdesc = make_smem_desc(ring + kTokBytes, 1024u, 2u);
             int st = 0, it = 0;
             uint32_t ph = 0, consumed = 0;
             bool ok = true;
@@ -569,21 +603,24 @@ __global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
                                        ((256u >> 4) << 24);
                 const int acc = it % s.nacc;
                 const uint32_t aph = static_cast<uint32_t>(it / s.nacc) & 1u;
-                if (!wait_bar(tempty0 + 8 * acc, aph ^ 1u, abort_flag, p.status, p.wait_ns)) break;
+                if (!wait_long(tempty0 + 8 * acc, aph ^ 1u, abort_flag, p.status, p.wait_ns)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + static_cast<uint32_t>(acc * s.bn);
                 for (int i = 0; i < s.k_steps; ++i) {
-                    const uint32_t fb = ready0 + 8 * st;
-                    if (!mbar_try_wait_cluster(fb, ph)) {
-                        if (!wait_bar(fb, ph, abort_flag, p.status, p.wait_ns)) {
+                    if (!wait_long(wfull0 + 8 * st, ph, abort_flag, p.status, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    misc[3] = ++consumed;
+                    if (!E4M3 && !mbar_try_wait_cluster(ready0 + 8 * st, ph)) {
+                        if (!wait_long(ready0 + 8 * st, ph, abort_flag, p.status, p.wait_ns)) {
                             ok = false;
                             break;
                         }
-                        mbar_try_wait_cluster(fb, ph);   // complete: acquires at cluster scope
+                        mbar_try_wait_cluster(ready0 + 8 * st, ph);   // complete: acquires at cluster scope
                     }
-                    if (E4M3) misc[3] = ++consumed;
                     tc_fence_after();
-                    const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(st) * step);
+                    const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(st) * (Shape::kStage >> 4));
                     if (E4M3) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -592,11 +629,11 @@ __global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             tc_mma_f16_ta_pair(d, tmem + kTmemA + st * 64 + k * 8,
-                                               bdesc + off + (k >> 2) * ((kRows * 128u) >> 4) + 2 * (k & 3),
+                                               bdesc + off + (k >> 2) * (kTokBytes >> 4) + 2 * (k & 3),
                                                idesc, (i | k) != 0);
                     }
-                    tc_commit_pair(free0 + 8 * st, 3);
-                    if (++st == depth) {
+                    tc_commit_pair(empty0 + 8 * st, 3);
+                    if (++st == s.stages) {
                         st = 0;
                         ph ^= 1u;
                     }
@@ -610,18 +647,17 @@ __global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
         // release at cluster scope waits for all of its thread's stores, which
         // every converter warp would pay per step
         if (!E4M3 && lane == 0) {
-            const uint32_t dst = mapa_shared(cfull0, 0);
-            const int total = first < tiles ? ((tiles - first + stride - 1) / stride) * s.k_steps : 0;
-            int c = 0;
-            uint32_t cph = 0;
+            const uint32_t dst = mapa_shared(ready0, 0);
+            int st = 0;
+            uint32_t ph = 0;
             for (int i = 0; i < total; ++i) {
-                if (!wait_bar(clocal0 + 8 * c, cph, abort_flag, p.status, p.wait_ns)) break;
+                if (!wait_long(xcvt0 + 8 * st, ph, abort_flag, p.status, p.wait_ns)) break;
                 tc_fence_after();
                 tc_fence_before();
-                mbar_arrive_cluster(dst + 8 * c);
-                if (++c == s.cvt) {
-                    c = 0;
-                    cph ^= 1u;
+                mbar_arrive_cluster(dst + 8 * st);
+                if (++st == s.stages) {
+                    st = 0;
+                    ph ^= 1u;
                 }
             }
         }
@@ -629,12 +665,12 @@ __global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
         // ------------------------------------------------------ epilogue
         const int q = warp & 3, half = (warp - 4) >> 2;
         const uint32_t tempty_dst = mapa_shared(tempty0, 0);
-        const uint32_t buf0 = epi0 + static_cast<uint32_t>((warp - 4) * s.staged) * 4096u;
+        const uint32_t buf = epi0 + static_cast<uint32_t>(warp - 4) * 4096u;   // this warp's staging
         // 32 scales and 32 biases of the chunk at hand, read as broadcasts
         float* wcols = reinterpret_cast<float*>(smem_pair + (cols0 - ring)) + (warp - 4) * 64;
         const bool f32 = p.out_dtype == kTokF32;
         const int bcols = f32 ? 32 : 64;   // outputs of a 128-byte staged row
-        int it = 0, nbuf = 0;
+        int it = 0;
         for (int t = first; t < tiles; t += stride, ++it) {
             const PairTile tl = pair_tile(t, s);
             const int ncols = pair_cols(tl.nt, s);
@@ -653,7 +689,7 @@ __global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
             const int acc = it % s.nacc;
             const uint32_t aph = static_cast<uint32_t>(it / s.nacc) & 1u;
             if (!__all_sync(0xffffffffu,
-                            wait_bar(tfull0 + 8 * acc, aph, abort_flag, p.status, p.wait_ns)))
+                            wait_long(tfull0 + 8 * acc, aph, abort_flag, p.status, p.wait_ns)))
                 break;
             tc_fence_after();
             const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) +
@@ -690,12 +726,8 @@ __global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
                 if (p.act != kActNone) act_chunk(v, p.act, f32);
                 // staged rows of 128 bytes: 64 16-bit outputs (two chunks) or 32 of fp32
                 const int part = f32 ? 0 : (c >> 5) & 1;
-                const uint32_t buf = buf0 + static_cast<uint32_t>(nbuf % s.staged) * 4096u;
                 if (part == 0) {
-                    if (s.tma_out && lane == 0) {
-                        if (s.staged == 2) bulk_wait_read<1>();
-                        else bulk_wait_read<0>();
-                    }
+                    if (s.tma_out && lane == 0) bulk_wait_read<0>();
                     __syncwarp();
                 }
                 if (f32) {
@@ -746,7 +778,6 @@ __global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
                     }
                     __syncwarp();
                 }
-                ++nbuf;
             }
             if (half * 128 >= c_end) {   // a narrow tile has no columns for this half
                 __syncwarp();
@@ -757,61 +788,34 @@ __global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
         if (s.tma_out && lane == 0) bulk_wait_read<0>();
     } else if (!E4M3 && warp >= 12) {
         // ------------------------------------------------------ converters (int8)
-        int st = 0, c = 0;
-        uint32_t ph = 0, cph = 0, seen = 0;
-        const int total = first < tiles ? ((tiles - first + stride - 1) / stride) * s.k_steps : 0;
-        for (int i = 0; i < total; ++i) {
-            const bool ok = wait_bar(full0 + 8 * st, ph, abort_flag, p.status, p.wait_ns) &&
-                            wait_bar(cempty0 + 8 * c, cph ^ 1u, abort_flag, p.status, p.wait_ns);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            if (threadIdx.x == 12 * 32) misc[3] = ++seen;
-            const uint32_t src = ring + st * kPairStage;
-            if (warp < 16) {
-                tc_fence_after();
-                const int r = (warp & 3) * 32 + lane;
+        // A stage's TMEM columns are free when its shared memory is (the same
+        // MMAs read both), so its tokens' arrival is all there is to wait for.
+        const int group = (warp - 12) >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t ta = tmem + kTmemA + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        int st = group;
+        uint32_t ph = 0;
+        for (int i = group; i < total; i += 2) {
+            if (!__all_sync(0xffffffffu,
+                            wait_long(xfull0 + 8 * st, ph, abort_flag, p.status, p.wait_ns)))
+                break;
+            if ((warp & 3) == 0 && lane == 0) misc[4] = static_cast<uint32_t>(i + 1);
+            tc_fence_after();
+            const uint32_t src = ring + st * Shape::kStage;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t v[32];
+            for (int h = 0; h < 2; ++h) {
+                uint32_t v[32];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) cvt_chunk(lds128(src + swz(r, 4 * h + j)), v + 8 * j);
-                    tmem_st_32x32b_x32(tmem + kTmemA + (static_cast<uint32_t>((warp & 3) * 32) << 16) +
-                                           c * 64 + h * 32, v);
-                }
-                tmem_st_wait();
-                tc_fence_before();
-            } else {
-                const uint32_t dst = cvt0 + c * kPairCvt;
-#pragma unroll 4
-                for (int u = threadIdx.x - 512; u < kRows * 8; u += 128) {
-                    const int r = u >> 3, ch = u & 7;
-                    uint32_t v[8];
-                    cvt_chunk(lds128(src + kRows * kStep + swz(r, ch)), v);
-                    const uint32_t box = dst + static_cast<uint32_t>((ch >> 2) * kRows) * 128u;
-                    // the second box's rows start at the first box's banks: its
-                    // halves go in the opposite order
-                    const int d = 2 * (ch & 3);
-                    if (ch < 4) {
-                        sts128(box + swz(r, d), v[0], v[1], v[2], v[3]);
-                        sts128(box + swz(r, d + 1), v[4], v[5], v[6], v[7]);
-                    } else {
-                        sts128(box + swz(r, d + 1), v[4], v[5], v[6], v[7]);
-                        sts128(box + swz(r, d), v[0], v[1], v[2], v[3]);
-                    }
-                }
-                fence_proxy_async_smem();
+                for (int j = 0; j < 4; ++j) cvt_chunk(lds128(src + swz(r, 4 * h + j)), v + 8 * j);
+                tmem_st_32x32b_x32(ta + st * 64 + h * 32, v);
             }
+            tmem_st_wait();
+            tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(empty0 + 8 * st);
-                mbar_arrive(clocal0 + 8 * c);
-            }
-            if (++st == s.stages) {
-                st = 0;
+            if (lane == 0) mbar_arrive(xcvt0 + 8 * st);
+            st += 2;
+            if (st >= s.stages) {   // an even number of stages
+                st -= s.stages;
                 ph ^= 1u;
-            }
-            if (++c == s.cvt) {
-                c = 0;
-                cph ^= 1u;
             }
         }
     }
@@ -820,16 +824,17 @@ __global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
     // both CTAs finish their roles before either drains, frees TMEM or leaves
     cluster_sync();
     if (*abort_flag) {
-        // a CTA's e4m3 loads signal the leader's barriers, so it cannot watch
-        // them land: after an abort ~100 us pass first
+        // the peer's loads signal the leader's barriers, so it cannot watch them
+        // land: after an abort ~100 us pass first
         const long long t0 = clock64();
         while (clock64() - t0 < 200000) {
         }
-        if (threadIdx.x == 0 && (!E4M3 || rank == 0)) {
-            const uint32_t issued = misc[2], consumed = misc[3];
-            for (uint32_t i = consumed; i < issued; ++i)
-                drain_wait(full0 + 8 * (i % static_cast<uint32_t>(s.stages)),
-                           (i / static_cast<uint32_t>(s.stages)) & 1u);
+        if (threadIdx.x == 0) {
+            const uint32_t issued = misc[2], depth = static_cast<uint32_t>(s.stages);
+            for (uint32_t i = misc[3]; rank == 0 && i < issued; ++i)
+                drain_wait(wfull0 + 8 * (i % depth), (i / depth) & 1u);
+            for (uint32_t i = misc[4]; !E4M3 && i < issued; ++i)
+                drain_wait(xfull0 + 8 * (i % depth), (i / depth) & 1u);
         }
         if (warp == 1 && lane == 0 && rank == 0) {
             tc_commit_pair(drain_bar, 1);
@@ -845,9 +850,31 @@ __global__ void __launch_bounds__(E4M3 ? kPairThreads8 : kPairThreadsI, 1)
     }
 }
 
+// Up to 16 bytes (left < 16: the rest zeros) from any address, put together from
+// the aligned 4-byte words that hold at least one of them.
+__device__ __forceinline__ uint4 load_bytes(const uint8_t* src, long long left) {
+    const int n = static_cast<int>(min(16ll, left));
+    uint32_t o[4] = {0u, 0u, 0u, 0u};
+    if (n > 0) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(src);
+        const int sh = static_cast<int>(a & 3u);
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(a - sh);
+        const int need = (sh + n + 3) >> 2;
+        uint32_t v[5];
+#pragma unroll
+        for (int j = 0; j < 5; ++j) v[j] = j < need ? q[j] : 0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            o[j] = __funnelshift_r(v[j], v[j + 1], 8 * sh);
+            const int in = n - 4 * j;   // bytes of this word that were asked for
+            if (in < 4) o[j] = in <= 0 ? 0u : o[j] & ((1u << (8 * in)) - 1u);
+        }
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // Rows of any alignment copied to a 16-byte pitch, zeros behind each row: one
-// thread per 16-byte word, put together from the aligned 4-byte words that its
-// bytes lie in.
+// thread per 16-byte word.
 __global__ void __launch_bounds__(256) pad_rows_kernel(const uint8_t* src, long long stride,
                                                        long long rows, long long cols, uint8_t* dst,
                                                        long long pitch) {
@@ -857,24 +884,28 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const uint8_t* src, long 
     for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total;
          i += static_cast<long long>(gridDim.x) * 256) {
         const long long r = i / words, c = (i - r * words) << 4;
-        const int n = static_cast<int>(min(16ll, cols - c));   // bytes of the row in this word
-        uint32_t o[4] = {0u, 0u, 0u, 0u};
-        if (n > 0) {
-            const uintptr_t a = reinterpret_cast<uintptr_t>(src + r * stride + c);
-            const int sh = static_cast<int>(a & 3u);
-            const uint32_t* q = reinterpret_cast<const uint32_t*>(a - sh);
-            const int need = (sh + n + 3) >> 2;   // aligned words that hold a byte of the row
-            uint32_t v[5];
-#pragma unroll
-            for (int j = 0; j < 5; ++j) v[j] = j < need ? q[j] : 0u;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                o[j] = __funnelshift_r(v[j], v[j + 1], 8 * sh);
-                const int left = n - 4 * j;   // bytes of this word inside the row
-                if (left < 4) o[j] = left <= 0 ? 0u : o[j] & ((1u << (8 * left)) - 1u);
-            }
-        }
-        *reinterpret_cast<uint4*>(dst + r * pitch + c) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + r * pitch + c) = load_bytes(src + r * stride + c, cols - c);
+    }
+}
+
+// int8 rows as f16 rows of `pitch` elements (a multiple of 16), zeros behind each
+// row: one thread per 16 codes, read as one word where rows are 16-byte aligned.
+__global__ void __launch_bounds__(256) widen_rows_kernel(const uint8_t* src, long long stride,
+                                                         long long rows, long long cols,
+                                                         uint8_t* dst, long long pitch, int aligned) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const long long words = pitch >> 4, total = rows * words;
+    for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total;
+         i += static_cast<long long>(gridDim.x) * 256) {
+        const long long r = i / words, c = (i - r * words) << 4;
+        const uint4 v = aligned && c + 16 <= cols ? *reinterpret_cast<const uint4*>(src + r * stride + c)
+                                                  : load_bytes(src + r * stride + c, cols - c);
+        uint32_t o[8];
+        cvt_chunk(v, o);
+        uint4* d = reinterpret_cast<uint4*>(dst + 2 * (r * pitch + c));
+        d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        d[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
 }
 
@@ -919,7 +950,7 @@ cudaError_t launch_pair(const LinearMaps& maps, const PairParams& s, const Linea
     cudaError_t e = ensure_dynamic_smem(linear_pair_kernel<E4M3>, plan.smem, smem_set);
     if (e != cudaSuccess) return e;
     return launch_ex(linear_pair_kernel<E4M3>, static_cast<unsigned>(plan.grid),
-                     E4M3 ? kPairThreads8 : kPairThreadsI, plan.smem, 2, stream, maps.x, maps.w,
+                     PairShape<E4M3>::kThreads, plan.smem, 2, stream, maps.x, maps.w,
                      maps.out, s);
 }
 
@@ -931,11 +962,9 @@ void plan_pair(const LinearParams& p, int num_sms, LinearPlan* r) {
     r->tok_tiles = static_cast<int>((p.tokens + 255) / 256);
     r->out_tiles = static_cast<int>((p.outputs + r->out_tile - 1) / r->out_tile);
     r->splits = 1;
-    r->stages = p.e4m3 ? 6 : 3;
-    r->cvt_stages = p.e4m3 ? 0 : 3;
-    r->staged = 1;
-    r->smem = static_cast<size_t>(r->stages) * kPairStage + static_cast<size_t>(r->cvt_stages) * kPairCvt +
-              static_cast<size_t>(r->staged) * 8 * 4096 + 2048 + kBarBytes + 8 * kMaxCvt + 32 + 32;
+    r->stages = p.e4m3 ? PairShape<true>::kStages : PairShape<false>::kStages;
+    r->smem = static_cast<size_t>(r->stages) * (p.e4m3 ? PairShape<true>::kStage : PairShape<false>::kStage) +
+              8 * 4096 + 2048 + 5 * 8 * kMaxStages + 40 + 24;
     const long long tiles = static_cast<long long>(r->tok_tiles) * r->out_tiles;
     r->grid = static_cast<int>(2 * std::min<long long>(tiles, num_sms / 2));
 }
@@ -968,9 +997,11 @@ void plan_split(const LinearParams& p, int num_sms, LinearPlan* r) {
 
 }  // namespace
 
+bool linear_pair_form(long long tokens) { return tokens > 512; }
+
 LinearPlan plan_linear(const LinearParams& p, int num_sms) {
     LinearPlan r{};
-    if (p.tokens > 512) plan_pair(p, num_sms, &r);
+    if (linear_pair_form(p.tokens)) plan_pair(p, num_sms, &r);
     else plan_split(p, num_sms, &r);
     return r;
 }
@@ -987,9 +1018,7 @@ cudaError_t launch_linear(const LinearMaps& maps, const LinearParams& p, const L
         s.group_m = 8;
         s.k_steps = k_steps;
         s.stages = plan.stages;
-        s.cvt = plan.cvt_stages;
         s.nacc = p.e4m3 ? 512 / s.bn >= 2 ? 2 : 1 : static_cast<int>(kTmemA) / s.bn >= 2 ? 2 : 1;
-        s.staged = plan.staged;
         s.tma_out = plan.tma_out;
         s.f_group = make_fastdiv(static_cast<uint32_t>(s.group_m * s.n_tiles));
         s.f_gm = make_fastdiv(static_cast<uint32_t>(s.group_m));
@@ -1014,6 +1043,14 @@ cudaError_t launch_pad_rows(const uint8_t* src, long long stride, long long rows
     const long long blocks = (rows * (pitch >> 4) + 255) / 256;
     return launch_ex(pad_rows_kernel, static_cast<unsigned>(std::min(blocks, 152ll * 64)), 256, 0, 1,
                      stream, src, stride, rows, cols, dst, pitch);
+}
+
+cudaError_t launch_widen_rows(const uint8_t* src, long long stride, long long rows, long long cols,
+                              uint8_t* dst, long long pitch, cudaStream_t stream) {
+    const long long blocks = (rows * (pitch >> 4) + 255) / 256;
+    const int aligned = (reinterpret_cast<uintptr_t>(src) & 15u) == 0 && stride % 16 == 0;
+    return launch_ex(widen_rows_kernel, static_cast<unsigned>(std::min(blocks, 152ll * 64)), 256, 0, 1,
+                     stream, src, stride, rows, cols, dst, pitch, aligned);
 }
 
 }  // namespace c3d

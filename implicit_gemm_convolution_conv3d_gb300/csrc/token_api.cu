@@ -140,12 +140,13 @@ int act_quant_fwd(const void* x, int x_dtype, int64_t x_stride, int act, int gat
 }
 
 size_t linear_w8a8_workspace_size(const void* x, int64_t x_stride, const void* w,
-                                  int64_t w_stride, int64_t tokens, int64_t outputs,
+                                  int64_t w_stride, int dtype, int64_t tokens, int64_t outputs,
                                   int64_t width) {
     if (tokens < 1 || outputs < 1 || width < 1) return 0;
     const size_t pitch = static_cast<size_t>(round16(width));
+    const bool widen = dtype == CONV_DTYPE_INT8 && linear_pair_form(tokens);
     return (tma_rows(x, x_stride, tokens) ? 0 : pitch * static_cast<size_t>(tokens)) +
-           (tma_rows(w, w_stride, outputs) ? 0 : pitch * static_cast<size_t>(outputs));
+           (widen ? 2 : tma_rows(w, w_stride, outputs) ? 0 : 1) * pitch * static_cast<size_t>(outputs);
 }
 
 int linear_w8a8_fwd(const void* x, int64_t x_stride, const void* w, int64_t w_stride, int dtype,
@@ -182,17 +183,21 @@ int linear_w8a8_fwd(const void* x, int64_t x_stride, const void* w, int64_t w_st
     p.e4m3 = dtype == CONV_DTYPE_FP8_E4M3;
     p.act = act;
     p.out_dtype = out_dtype;
-    const size_t need = linear_w8a8_workspace_size(x, x_stride, w, w_stride, tokens, outputs, width);
+    const size_t need =
+        linear_w8a8_workspace_size(x, x_stride, w, w_stride, dtype, tokens, outputs, width);
     if (need && (!workspace || workspace_bytes < need || !aligned_to(workspace, 16)))
-        return invalid("rows that are not 16-byte aligned need a 16-byte aligned workspace of "
+        return invalid("this product needs a 16-byte aligned workspace of "
                        "linear_w8a8_workspace_size bytes");
     LaunchLimits lim;
     int rc = launch_limits(&lim);
     if (rc) return rc;
     p.status = lim.status;
     p.wait_ns = lim.wait_ns;
-    // operands that TMA cannot address are copied to an aligned pitch first
-    const bool copy_x = !tma_rows(x, x_stride, tokens), copy_w = !tma_rows(w, w_stride, outputs);
+    // operands that TMA cannot address are copied to an aligned pitch first, and
+    // the pair form's int8 weights are widened to f16
+    const bool widen = !p.e4m3 && linear_pair_form(tokens);
+    const bool copy_x = !tma_rows(x, x_stride, tokens);
+    const bool copy_w = !widen && !tma_rows(w, w_stride, outputs);
     const long long pitch = round16(width);
     uint8_t* at = static_cast<uint8_t*>(workspace);
     const uint8_t *src_x = p.x, *src_w = p.w;
@@ -200,9 +205,9 @@ int linear_w8a8_fwd(const void* x, int64_t x_stride, const void* w, int64_t w_st
         p.x = at;
         at += pitch * tokens;
     }
-    if (copy_w) p.w = at;
+    if (copy_w || widen) p.w = at;
     p.x_stride = copy_x || tokens == 1 ? pitch : x_stride;
-    p.w_stride = copy_w || outputs == 1 ? pitch : w_stride;
+    p.w_stride = copy_w || widen || outputs == 1 ? pitch : w_stride;
     LinearPlan plan = plan_linear(p, lim.num_sms);
     if (static_cast<long long>(plan.out_tiles) * plan.tok_tiles * plan.splits > kMaxDim) {
         set_last_error("the output has more than 2^31 tiles");
@@ -211,13 +216,18 @@ int linear_w8a8_fwd(const void* x, int64_t x_stride, const void* w, int64_t w_st
     const long long elt = size_of(out_dtype);
     plan.tma_out = aligned_to(out, 16) && (tokens == 1 || out_stride * elt % 16 == 0);
     LinearMaps maps{};
-    if ((rc = encode_rows_u8(&maps.x, p.x, width, tokens, p.x_stride, plan.tok_box))) return rc;
-    if ((rc = encode_rows_u8(&maps.w, p.w, width, outputs, p.w_stride, plan.out_box))) return rc;
+    if ((rc = encode_rows(&maps.x, p.x, 1, width, tokens, p.x_stride, plan.tok_box))) return rc;
+    if ((rc = encode_rows(&maps.w, p.w, widen ? 2 : 1, width, outputs, p.w_stride * (widen ? 2 : 1),
+                          plan.out_box)))
+        return rc;
     if (plan.pair && plan.tma_out &&
-        (rc = encode_rows_out(&maps.out, out, static_cast<int>(elt), outputs, tokens, out_stride * elt)))
+        (rc = encode_rows(&maps.out, out, static_cast<int>(elt), outputs, tokens,
+                          (tokens == 1 ? outputs * elt + 15 & ~15ll : out_stride * elt), 32)))
         return rc;
     cudaError_t e = cudaSuccess;
     if (copy_x) e = launch_pad_rows(src_x, x_stride, tokens, width, const_cast<uint8_t*>(p.x), pitch, stream);
+    if (e == cudaSuccess && widen)
+        e = launch_widen_rows(src_w, w_stride, outputs, width, const_cast<uint8_t*>(p.w), pitch, stream);
     if (e == cudaSuccess && copy_w)
         e = launch_pad_rows(src_w, w_stride, outputs, width, const_cast<uint8_t*>(p.w), pitch, stream);
     if (e == cudaSuccess) e = launch_linear(maps, p, plan, stream);

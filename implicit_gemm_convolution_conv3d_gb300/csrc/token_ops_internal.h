@@ -56,12 +56,15 @@ struct LinearPlan {
     int tok_box, out_box;   // rows of a TMA box of either operand
     int out_tiles, tok_tiles;
     int splits;             // split: CTAs of a cluster that share a tile's reduction
-    int stages, cvt_stages; // rings of TMA boxes and of converted (int8) operands
-    int staged;             // pair: 4 KB output staging buffers of a warp
+    int stages;             // ring of TMA boxes
+    int cvt_stages;         // split, int8: ring of converted operands
     int tma_out;            // pair: the output's rows can be stored by TMA
     int grid;               // pair: CTAs
     size_t smem;
 };
+// whether the pair form runs a product of this many tokens; its int8 weights are
+// then f16 rows in the workspace (launch_widen_rows)
+bool linear_pair_form(long long tokens);
 LinearPlan plan_linear(const LinearParams& p, int num_sms);
 
 struct LinearMaps {
@@ -77,5 +80,9 @@ cudaError_t launch_linear(const LinearMaps& maps, const LinearParams& p, const L
 // `cols` bytes `stride` apart, zeros behind each row
 cudaError_t launch_pad_rows(const uint8_t* src, long long stride, long long rows, long long cols,
                             uint8_t* dst, long long pitch, cudaStream_t stream);
+
+// f16 rows of `pitch` elements (a multiple of 16, 16-byte aligned) from int8 rows
+cudaError_t launch_widen_rows(const uint8_t* src, long long stride, long long rows, long long cols,
+                              uint8_t* dst, long long pitch, cudaStream_t stream);
 
 }  // namespace c3d

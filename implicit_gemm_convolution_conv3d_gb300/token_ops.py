@@ -36,7 +36,7 @@ def _bind():
     lib.act_quant_fwd.argtypes = [vp, i32, i64, i32, i32, i64, i64, i32, vp, i64, vp, vp]
     lib.linear_w8a8_fwd.argtypes = [vp, i64, vp, i64, i32, i64, i64, i64, vp, vp, vp, i32, vp,
                                     i32, i64, vp, ctypes.c_size_t, vp]
-    lib.linear_w8a8_workspace_size.argtypes = [vp, i64, vp, i64, i64, i64, i64]
+    lib.linear_w8a8_workspace_size.argtypes = [vp, i64, vp, i64, i32, i64, i64, i64]
     lib.linear_w8a8_workspace_size.restype = ctypes.c_size_t
     _fns = lib
     return lib
@@ -173,8 +173,8 @@ def linear_w8a8(x: torch.Tensor, w: torch.Tensor, scale_x: Optional[torch.Tensor
     and w [outputs, width] of one type, with fp32 row scales (None: ones),
     fp32 bias and fp32 sums -> [..., outputs] in bf16, fp16 or fp32
     (``out``'s type, where given).  A workspace is taken from torch's
-    allocator when the operands' rows need one (they are not 16-byte aligned)
-    and none is given."""
+    allocator when the product needs one (int8 with many tokens, rows that are
+    not 16-byte aligned) and none is given."""
     code = ACT_CODES.get(act)
     if code is None:
         raise ValueError(f"act must be one of {sorted(ACT_CODES)}")
@@ -195,7 +195,7 @@ def linear_w8a8(x: torch.Tensor, w: torch.Tensor, scale_x: Optional[torch.Tensor
         raise ValueError(f"out must have shape {tuple(x.shape[:-1]) + (outputs,)}")
     _, _, os_, oc = _rows(out, _FLOAT, "out")
     xp, wp = x.data_ptr(), w.data_ptr()
-    need = lib.linear_w8a8_workspace_size(xp, xs, wp, ws, rows, outputs, width)
+    need = lib.linear_w8a8_workspace_size(xp, xs, wp, ws, qc, rows, outputs, width)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
         if not workspace.is_cuda or not workspace.is_contiguous():

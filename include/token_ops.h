@@ -78,11 +78,11 @@ int linear_w8a8_fwd(const void* x, int64_t x_stride, const void* w, int64_t w_st
                     int64_t out_stride, void* workspace, size_t workspace_bytes,
                     cudaStream_t stream);
 
-/* Bytes of workspace linear_w8a8_fwd needs for these operands: 0 when the
- * rows of x and w are 16-byte aligned (base and stride), else room for
- * copies of the unaligned ones at an aligned pitch.  Host-only. */
+/* Bytes of workspace linear_w8a8_fwd needs for these operands: an f16 copy of
+ * int8 weights when there are many tokens, and copies at a 16-byte pitch of
+ * rows that are not 16-byte aligned (base and stride).  Host-only. */
 size_t linear_w8a8_workspace_size(const void* x, int64_t x_stride, const void* w,
-                                  int64_t w_stride, int64_t tokens, int64_t outputs,
+                                  int64_t w_stride, int dtype, int64_t tokens, int64_t outputs,
                                   int64_t width);
 
 #ifdef __cplusplus
