@@ -1224,20 +1224,20 @@ int launch_limits(LaunchLimits* l) {
 }
 
 int encode_rows(CUtensorMap* m, const void* ptr, int elt, long long cols, long long rows,
-                long long pitch, int box_rows) {
+                long long pitch, int box_rows, int box_bytes) {
     if (!load_entry_points()) {
         set_error("the driver's tensor-map encoders are not available");
         return CONV_ERR_CUDA;
     }
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elt), static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_bytes / elt), static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t es[2] = {1u, 1u};
     const CUtensorMapDataType type = elt == 4   ? CU_TENSOR_MAP_DATA_TYPE_UINT32
                                      : elt == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16
                                                 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     CUresult r = g_encode_tiled(m, type, 2, const_cast<void*>(ptr), dims, strides, box, es,
-                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle_for(box_bytes),
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         set_error("cuTensorMapEncodeTiled failed (code %s%lld)", "", static_cast<long long>(r));

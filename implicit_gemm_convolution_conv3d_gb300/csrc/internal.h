@@ -288,10 +288,10 @@ struct LaunchLimits {
 int launch_limits(LaunchLimits* l);
 
 // Tensor map of a matrix [rows, cols] of 1-, 2- or 4-byte elements, `pitch` bytes
-// between rows (base and pitch multiples of 16): boxes of box_rows rows x 128
-// bytes in the 128-byte swizzle, zeros outside the matrix.
+// between rows (base and pitch multiples of 16): boxes of box_rows rows x
+// box_bytes (64 or 128, the swizzle too), zeros outside the matrix.
 int encode_rows(CUtensorMap* m, const void* ptr, int elt, long long cols, long long rows,
-                long long pitch, int box_rows);
+                long long pitch, int box_rows, int box_bytes);
 
 int* device_status_ptr();   // device address of the status word (current device)
 

@@ -29,7 +29,7 @@ constexpr uint32_t kBarBytes = 16u * (kMaxStages + kMaxCvt) + 16u;
 // Bounded wait (see wait_bar) of a role that may wait for thousands of cycles:
 // it sleeps in hardware between looks, so that its polling leaves the issue slots
 // to the converters and the epilogue.
-__device__ __noinline__ bool wait_long_slow(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
+__device__ __forceinline__ bool wait_long_slow(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
                                             int* status, unsigned long long limit_ns) {
     const long long t0 = clock64();
     const long long limit = static_cast<long long>(limit_ns > (1ull << 61) ? (1ull << 61) : limit_ns) * 2;
@@ -53,6 +53,11 @@ __device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatil
 // The byte of the 16-byte chunk `c` of row `r` in a 128-byte-swizzled tile.
 __device__ __forceinline__ uint32_t swz(int r, int c) {
     return static_cast<uint32_t>(r) * 128u + (static_cast<uint32_t>(c ^ (r & 7)) << 4);
+}
+
+// The same for 64-byte rows in the 64-byte swizzle.
+__device__ __forceinline__ uint32_t swz64(int r, int c) {
+    return static_cast<uint32_t>(r) * 64u + (static_cast<uint32_t>(c ^ ((r >> 1) & 3)) << 4);
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -408,9 +413,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Persistent CTA pairs, 256 tokens x up to 256 outputs a tile: the form for many
 // tokens.  Here the tokens are the MMA's row operand (128 per CTA) and each CTA
 // holds half of the tile's weight rows.
-//   warp 0       TMA producer
+//   warp 0       TMA producer (int8: of the weights)
 //   warp 1       TMEM, MMA issuer (leader CTA)
-//   warp 2       int8: tells the leader that this CTA's converters are done
+//   warp 2       int8: TMA producer of the tokens
 //   warps 4-11   epilogue: lane = token, 128 outputs a warp
 //   warps 12-19  int8: tokens to f16 into TMEM, two groups on alternate k-steps
 // int8: the tokens cross shared memory once as bytes (their f16 form goes to
@@ -420,11 +425,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 // of the MMA's reads, 96 bytes a cycle.  Converting the weights here too
 // takes 128 (raw in and out, f16 in and out), and measured 1475 TFLOP/s at
 // 16384 x 8192 x 8192 against WIDE_TFLOPS; the launch reads and writes 3 bytes per weight.
+//
+// Rings: the tokens' raw slots are free once converted, so that their loads run
+// ahead of the MMAs by both rings (3 raw slots, 4 in TMEM); one ring for both
+// operands refilled a stage in 4100 cycles, over the 3072 that it had.
+// Accumulators: e4m3 has two, int8 one (its tokens take the other half of
+// TMEM), which the epilogue therefore first loads into registers as a whole
+// (128 a thread; setmaxnreg gives its warps what the others do not need) and
+// hands back before it scales, packs and stores: the MMAs wait for the loads
+// only, not for the 6000 cycles that a tile's epilogue took chunk by chunk.
 struct PairParams {
     LinearParams p;
     int bn;                   // outputs of a tile: a multiple of 64, at most 256
     int m_tiles, n_tiles, group_m;
-    int k_steps, stages;
+    int k_steps;
     int nacc;                 // accumulators in TMEM
     int tma_out;              // output rows that TMA can address
     FastDiv f_group, f_gm;
@@ -436,36 +450,27 @@ constexpr uint32_t kTmemA = 256;                          // TMEM columns of the
 template <bool E4M3>
 struct PairShape {
     static constexpr uint32_t kWBytes = kRows * kStep * (E4M3 ? 1u : 2u);   // weights of a k-step
-    static constexpr uint32_t kStage = kTokBytes + kWBytes;
+    // a ring stage: e4m3 tokens and weights, int8 weights (f16) alone
+    static constexpr uint32_t kStage = kWBytes + (E4M3 ? kTokBytes : 0u);
     static constexpr int kStages = E4M3 ? 6 : 4;
+    static constexpr int kTokSlots = E4M3 ? 0 : 3;   // int8: raw tokens
     static constexpr int kThreads = 128 + kPairEpi + (E4M3 ? 0 : 256);
+    static constexpr uint32_t kEpi0 = kStages * kStage + kTokSlots * kTokBytes;
+    static constexpr uint32_t kCols0 = kEpi0 + 8u * 4096u;
+    static constexpr uint32_t kBars0 = kCols0 + 8u * 256u;
+    static constexpr uint32_t kBytes = kBars0 + 5u * 8u * kMaxStages + 40u + 32u;
 };
+static_assert(PairShape<true>::kBytes <= 227u * 1024u && PairShape<false>::kBytes <= 227u * 1024u, "");
 
-// The activation of a chunk.  The fp32 forms are long: out of line, on a copy,
-// so that only their callers' values go through memory.
-__device__ __noinline__ void act_chunk_f32(float (&y)[32], int act) {
-    for (int j = 0; j < 32; ++j) y[j] = activate_f32(y[j], act);
-}
-
-__device__ __forceinline__ void act_chunk(uint32_t (&v)[32], int act, bool f32) {
+// The activation of a chunk in registers, in the forms for 16-bit outputs.
+__device__ __forceinline__ void act_chunk(uint32_t (&v)[32], int act) {
     auto each = [&](auto f) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(f(__uint_as_float(v[j])));
     };
-    if (act == kActRelu) {
-        each([](float y) { return y < 0.0f ? 0.0f : y; });
-    } else if (f32) {
-        float y[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(v[j]);
-        act_chunk_f32(y, act);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(y[j]);
-    } else if (act == kActSilu) {
-        each([](float y) { return activate_c<kActSilu>(y); });
-    } else {
-        each([](float y) { return activate_c<kActGelu>(y); });
-    }
+    if (act == kActRelu) each([](float y) { return y < 0.0f ? 0.0f : y; });
+    else if (act == kActSilu) each([](float y) { return activate_c<kActSilu>(y); });
+    else each([](float y) { return activate_c<kActGelu>(y); });
 }
 
 struct PairTile {
@@ -497,19 +502,18 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem_pair[];
     const LinearParams& p = s.p;
     const uint32_t ring = smem_u32(smem_pair);
-    const uint32_t epi0 = ring + static_cast<uint32_t>(s.stages) * Shape::kStage;
-    const uint32_t cols0 = epi0 + 8u * 4096u;             // scale_w, bias
-    // wfull: both CTAs' weights (and e4m3 tokens), on the leader; xfull: this
-    // CTA's int8 tokens; xcvt: its 4 converter warps; ready: both CTAs' relays,
-    // on the leader; empty: the stage's MMAs
-    const uint32_t wfull0 = cols0 + 2048u, xfull0 = wfull0 + 8u * kMaxStages;
-    const uint32_t xcvt0 = xfull0 + 8u * kMaxStages, ready0 = xcvt0 + 8u * kMaxStages;
+    const uint32_t toks = ring + Shape::kStages * Shape::kStage;
+    // wfull: both CTAs' weights (and e4m3 tokens), on the leader; xfull, xempty:
+    // this CTA's int8 tokens; ready: both CTAs' 4 converter warps of the step, on
+    // the leader; empty: the stage's MMAs
+    const uint32_t wfull0 = ring + Shape::kBars0, xfull0 = wfull0 + 8u * kMaxStages;
+    const uint32_t xempty0 = xfull0 + 8u * kMaxStages, ready0 = xempty0 + 8u * kMaxStages;
     const uint32_t empty0 = ready0 + 8u * kMaxStages;
     const uint32_t tfull0 = empty0 + 8u * kMaxStages, tempty0 = tfull0 + 16u;
     const uint32_t drain_bar = tempty0 + 16u;
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem_pair + (drain_bar + 8u - ring));
-    // misc[0] TMEM base, [1] abort flag, [2] k-steps issued, [3] k-steps whose
-    // weights, [4] whose tokens were waited for
+    // misc[0] TMEM base, [1] abort flag, [2] weights' k-steps issued, [3] waited
+    // for, [4] tokens' k-steps issued, [5] waited for
     volatile uint32_t* abort_flag = misc + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -518,11 +522,11 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
     const int first = static_cast<int>(blockIdx.x) >> 1, stride = static_cast<int>(gridDim.x) >> 1;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < s.stages; ++i) {
+        for (int i = 0; i < Shape::kStages; ++i) {
             mbar_init(wfull0 + 8 * i, 1);
             mbar_init(xfull0 + 8 * i, 1);
-            mbar_init(xcvt0 + 8 * i, 4);
-            mbar_init(ready0 + 8 * i, 2);
+            mbar_init(xempty0 + 8 * i, 4);
+            mbar_init(ready0 + 8 * i, 8);
             mbar_init(empty0 + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -530,7 +534,7 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
             mbar_init(tempty0 + 8 * i, 16);
         }
         mbar_init(drain_bar, 1);
-        for (int i = 1; i < 5; ++i) misc[i] = 0u;
+        for (int i = 1; i < 6; ++i) misc[i] = 0u;
         fence_mbar_init();
         prefetch_tmap(&x_map);
         prefetch_tmap(&w_map);
@@ -550,127 +554,135 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
     // k-steps of this pair's tiles
     const int total = first < tiles ? ((tiles - first + stride - 1) / stride) * s.k_steps : 0;
 
-    if (warp == 0) {
-        // ------------------------------------------------------ TMA producer
-        if (lane == 0) {
-            int st = 0;
-            uint32_t ph = 0, issued = 0;
-            bool ok = true;
-            for (int t = first; t < tiles && ok; t += stride) {
-                const PairTile tl = pair_tile(t, s);
-                const int m0 = tl.mt * 256 + rank * kRows;
-                const int n0 = tl.nt * s.bn + rank * (pair_cols(tl.nt, s) >> 1);
-                for (int i = 0; i < s.k_steps; ++i) {
-                    if (!wait_long(empty0 + 8 * st, ph ^ 1u, abort_flag, p.status, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t dst = ring + st * Shape::kStage;
-                    // the leader's barrier counts both CTAs' bytes
-                    if (rank == 0)
-                        mbar_arrive_expect_tx(wfull0 + 8 * st, 2u * (E4M3 ? Shape::kStage : Shape::kWBytes));
-                    const uint32_t fb = mapa_shared(wfull0 + 8 * st, 0);
-                    if (E4M3) {
-                        tma_load_2d_pair(dst, &x_map, fb, i * kStep, m0);
-                        tma_load_2d_pair(dst + kTokBytes, &w_map, fb, i * kStep, n0);
-                    } else {
-                        mbar_arrive_expect_tx(xfull0 + 8 * st, kTokBytes);
-                        tma_load_2d(dst, &x_map, xfull0 + 8 * st, i * kStep, m0);
-                        // f16: two boxes of 64 elements
-                        tma_load_2d_pair(dst + kTokBytes, &w_map, fb, i * kStep, n0);
-                        tma_load_2d_pair(dst + 2 * kTokBytes, &w_map, fb, i * kStep + 64, n0);
-                    }
-                    misc[2] = ++issued;
-                    if (++st == s.stages) {
-                        st = 0;
-                        ph ^= 1u;
-                    }
-                }
-            }
-        }
-    } else if (warp == 1) {
-        // ------------------------------------------------------ MMA issuer
-        if (lane == 0 && rank == 0) {
-            const uint64_t adesc = make_smem_desc(ring, 1024u, 2u);
-            const uint64_t bdesc = make_smem_desc(ring + kTokBytes, 1024u, 2u);
-            int st = 0, it = 0;
-            uint32_t ph = 0, consumed = 0;
-            bool ok = true;
-            for (int t = first; t < tiles && ok; t += stride, ++it) {
-                const PairTile tl = pair_tile(t, s);
-                // D fp32, operands f16 (or e4m3: both codes are 0), N, M 256
-                const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(pair_cols(tl.nt, s) >> 3) << 17) |
-                                       ((256u >> 4) << 24);
-                const int acc = it % s.nacc;
-                const uint32_t aph = static_cast<uint32_t>(it / s.nacc) & 1u;
-                if (!wait_long(tempty0 + 8 * acc, aph ^ 1u, abort_flag, p.status, p.wait_ns)) break;
-                tc_fence_after();
-                const uint32_t d = tmem + static_cast<uint32_t>(acc * s.bn);
-                for (int i = 0; i < s.k_steps; ++i) {
-                    if (!wait_long(wfull0 + 8 * st, ph, abort_flag, p.status, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    misc[3] = ++consumed;
-                    if (!E4M3 && !mbar_try_wait_cluster(ready0 + 8 * st, ph)) {
-                        if (!wait_long(ready0 + 8 * st, ph, abort_flag, p.status, p.wait_ns)) {
+    // Each warpgroup takes its share of the launch's registers: int8, 20 warps of
+    // 96: 4 x 40 + 8 x 168 + 8 x 48 <= 1920; e4m3, 12 warps of 168: 4 x 56 + 8 x 216
+    // <= 2016.
+    if (warp < 4) {
+        set_max_regs_dec<E4M3 ? 56 : 40>();
+        if (warp == 0) {
+            // ------------------------------------------------------ TMA producer
+            if (lane == 0) {
+                int st = 0;
+                uint32_t ph = 0, issued = 0;
+                bool ok = true;
+                for (int t = first; t < tiles && ok; t += stride) {
+                    const PairTile tl = pair_tile(t, s);
+                    const int m0 = tl.mt * 256 + rank * kRows;
+                    const int n0 = tl.nt * s.bn + rank * (pair_cols(tl.nt, s) >> 1);
+                    for (int i = 0; i < s.k_steps; ++i) {
+                        if (!wait_long(empty0 + 8 * st, ph ^ 1u, abort_flag, p.status, p.wait_ns)) {
                             ok = false;
                             break;
                         }
-                        mbar_try_wait_cluster(ready0 + 8 * st, ph);   // complete: acquires at cluster scope
-                    }
-                    tc_fence_after();
-                    const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(st) * (Shape::kStage >> 4));
-                    if (E4M3) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tc_mma_f8_pair(d, adesc + off + 2 * k, bdesc + off + 2 * k, idesc, (i | k) != 0);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            tc_mma_f16_ta_pair(d, tmem + kTmemA + st * 64 + k * 8,
-                                               bdesc + off + (k >> 2) * (kTokBytes >> 4) + 2 * (k & 3),
-                                               idesc, (i | k) != 0);
-                    }
-                    tc_commit_pair(empty0 + 8 * st, 3);
-                    if (++st == s.stages) {
-                        st = 0;
-                        ph ^= 1u;
+                        const uint32_t dst = ring + st * Shape::kStage;
+                        // the leader's barrier counts both CTAs' bytes
+                        if (rank == 0) mbar_arrive_expect_tx(wfull0 + 8 * st, 2u * Shape::kStage);
+                        const uint32_t fb = mapa_shared(wfull0 + 8 * st, 0);
+                        if (E4M3) {
+                            tma_load_2d_pair(dst, &x_map, fb, i * kStep, m0);
+                            tma_load_2d_pair(dst + kTokBytes, &w_map, fb, i * kStep, n0);
+                        } else {
+                            // f16: two boxes of 64 elements
+                            tma_load_2d_pair(dst, &w_map, fb, i * kStep, n0);
+                            tma_load_2d_pair(dst + kTokBytes, &w_map, fb, i * kStep + 64, n0);
+                        }
+                        misc[2] = ++issued;
+                        if (++st == Shape::kStages) {
+                            st = 0;
+                            ph ^= 1u;
+                        }
                     }
                 }
-                if (ok) tc_commit_pair(tfull0 + 8 * acc, 3);
             }
-        }
-    } else if (warp == 2) {
-        // ------------------------------------------------------ relay (int8)
-        // A CTA's converted stage is signalled to the leader by one arrival: a
-        // release at cluster scope waits for all of its thread's stores, which
-        // every converter warp would pay per step
-        if (!E4M3 && lane == 0) {
-            const uint32_t dst = mapa_shared(ready0, 0);
-            int st = 0;
-            uint32_t ph = 0;
-            for (int i = 0; i < total; ++i) {
-                if (!wait_long(xcvt0 + 8 * st, ph, abort_flag, p.status, p.wait_ns)) break;
-                tc_fence_after();
-                tc_fence_before();
-                mbar_arrive_cluster(dst + 8 * st);
-                if (++st == s.stages) {
-                    st = 0;
-                    ph ^= 1u;
+        } else if (warp == 1) {
+            // ------------------------------------------------------ MMA issuer
+            if (lane == 0 && rank == 0) {
+                const uint64_t adesc = make_smem_desc(ring, 1024u, 2u);
+                const uint64_t bdesc = make_smem_desc(ring + (E4M3 ? kTokBytes : 0u), 1024u, 2u);
+                int st = 0, it = 0;
+                uint32_t ph = 0, consumed = 0;
+                bool ok = true, landed = false;   // landed: this stage's operands were seen
+                auto here = [&](int stage, uint32_t phase) {
+                    return mbar_test_wait(wfull0 + 8 * stage, phase) &&
+                           (E4M3 || mbar_test_wait(ready0 + 8 * stage, phase));
+                };
+                for (int t = first; t < tiles && ok; t += stride, ++it) {
+                    const PairTile tl = pair_tile(t, s);
+                    // D fp32, operands f16 (or e4m3: both codes are 0), N, M 256
+                    const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(pair_cols(tl.nt, s) >> 3) << 17) |
+                                           ((256u >> 4) << 24);
+                    const int acc = it % s.nacc;
+                    const uint32_t aph = static_cast<uint32_t>(it / s.nacc) & 1u;
+                    if (!wait_bar(tempty0 + 8 * acc, aph ^ 1u, abort_flag, p.status, p.wait_ns)) break;
+                    const uint32_t d = tmem + static_cast<uint32_t>(acc * s.bn);
+                    for (int i = 0; i < s.k_steps; ++i) {
+                        if (!landed &&
+                            (!wait_bar(wfull0 + 8 * st, ph, abort_flag, p.status, p.wait_ns) ||
+                             (!E4M3 && !wait_bar(ready0 + 8 * st, ph, abort_flag, p.status, p.wait_ns)))) {
+                            ok = false;
+                            break;
+                        }
+                        misc[3] = ++consumed;
+                        tc_fence_after();
+                        const uint64_t off =
+                            static_cast<uint64_t>(static_cast<uint32_t>(st) * (Shape::kStage >> 4));
+                        const int nst = st + 1 == Shape::kStages ? 0 : st + 1;
+                        const uint32_t nph = nst ? ph : ph ^ 1u;
+                        // The pipe queues a couple of MMAs: the next stage is looked at
+                        // before the last one of this stage, while they run.
+                        constexpr int kMma = E4M3 ? 4 : 8;
+#pragma unroll
+                        for (int k = 0; k < kMma; ++k) {
+                            if (k == kMma - 1) landed = here(nst, nph);
+                            if (E4M3)
+                                tc_mma_f8_pair(d, adesc + off + 2 * k, bdesc + off + 2 * k, idesc,
+                                               (i | k) != 0);
+                            else
+                                tc_mma_f16_ta_pair(d, tmem + kTmemA + st * 64 + k * 8,
+                                                   bdesc + off + (k >> 2) * (kTokBytes >> 4) + 2 * (k & 3),
+                                                   idesc, (i | k) != 0);
+                        }
+                        tc_commit_pair(empty0 + 8 * st, 3);
+                        st = nst;
+                        ph = nph;
+                    }
+                    if (ok) tc_commit_pair(tfull0 + 8 * acc, 3);
+                }
+            }
+        } else if (warp == 2) {
+            // ------------------------------------------------------ tokens' producer (int8)
+            if (!E4M3 && lane == 0) {
+                int xs = 0;
+                uint32_t ph = 0, issued = 0;
+                bool ok = true;
+                for (int t = first; t < tiles && ok; t += stride) {
+                    const int m0 = pair_tile(t, s).mt * 256 + rank * kRows;
+                    for (int i = 0; i < s.k_steps; ++i) {
+                        if (!wait_long(xempty0 + 8 * xs, ph ^ 1u, abort_flag, p.status, p.wait_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(xfull0 + 8 * xs, kTokBytes);
+                        tma_load_2d(toks + xs * kTokBytes, &x_map, xfull0 + 8 * xs, i * kStep, m0);
+                        misc[4] = ++issued;
+                        if (++xs == Shape::kTokSlots) {
+                            xs = 0;
+                            ph ^= 1u;
+                        }
+                    }
                 }
             }
         }
-    } else if (warp >= 4 && warp < 12) {
+    } else if (warp < 12) {
         // ------------------------------------------------------ epilogue
+        set_max_regs_inc<E4M3 ? 216 : 168>();
         const int q = warp & 3, half = (warp - 4) >> 2;
         const uint32_t tempty_dst = mapa_shared(tempty0, 0);
-        const uint32_t buf = epi0 + static_cast<uint32_t>(warp - 4) * 4096u;   // this warp's staging
+        const uint32_t buf0 = ring + Shape::kEpi0 + static_cast<uint32_t>(warp - 4) * 4096u;
         // 32 scales and 32 biases of the chunk at hand, read as broadcasts
-        float* wcols = reinterpret_cast<float*>(smem_pair + (cols0 - ring)) + (warp - 4) * 64;
+        float* cols = reinterpret_cast<float*>(smem_pair + Shape::kCols0) + (warp - 4) * 64;
         const bool f32 = p.out_dtype == kTokF32;
-        const int bcols = f32 ? 32 : 64;   // outputs of a 128-byte staged row
-        int it = 0;
+        int it = 0, nbuf = 0;
         for (int t = first; t < tiles; t += stride, ++it) {
             const PairTile tl = pair_tile(t, s);
             const int ncols = pair_cols(tl.nt, s);
@@ -693,60 +705,62 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
                 break;
             tc_fence_after();
             const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) +
-                                static_cast<uint32_t>(acc * s.bn);
-            const int c_end = min(ncols, (half + 1) * 128);
-            const bool rows_in = m0 < p.tokens;
-#pragma unroll
-            for (int cj = 0; cj < 4; ++cj) {
-                const int c = half * 128 + 32 * cj;
-                if (c >= c_end) break;
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(tb + c, v);
+                                static_cast<uint32_t>(acc * s.bn + half * 128);
+            // 32-column chunks of this half that have outputs; all four are loaded (the
+            // columns exist), so that the accumulator goes back at once
+            const int chunks = max(0, min(4, (ncols - half * 128 + 31) >> 5));
+            auto chunk = [&](uint32_t (&v)[32], int j) {
                 __syncwarp();
-                wcols[lane] = csw[cj];
-                wcols[32 + lane] = cbi[cj];
+                cols[lane] = csw[j];
+                cols[32 + lane] = cbi[j];
                 __syncwarp();
-                tmem_ld_wait();
-                if (c + 32 >= c_end) {   // the accumulator has been read
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(tempty_dst + 8 * acc);
-                }
-                if (!rows_in) continue;
-                const float4* sw4 = reinterpret_cast<const float4*>(wcols);
-                const float4* bi4 = reinterpret_cast<const float4*>(wcols + 32);
+                const float4* sw4 = reinterpret_cast<const float4*>(cols);
+                const float4* bi4 = reinterpret_cast<const float4*>(cols + 32);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float4 sw = sw4[j], bi = bi4[j];
+                for (int i = 0; i < 8; ++i) {
+                    const float4 sw = sw4[i], bi = bi4[i];
                     const float f[4] = {sw.x, sw.y, sw.z, sw.w}, b[4] = {bi.x, bi.y, bi.z, bi.w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[4 * j + i] = __float_as_uint(__uint_as_float(v[4 * j + i]) * sx * f[i] + b[i]);
+                    for (int k = 0; k < 4; ++k)
+                        v[4 * i + k] = __float_as_uint(
+                            __uint_as_float(v[4 * i + k]) * sx * f[k] + b[k]);
                 }
-                if (p.act != kActNone) act_chunk(v, p.act, f32);
-                // staged rows of 128 bytes: 64 16-bit outputs (two chunks) or 32 of fp32
-                const int part = f32 ? 0 : (c >> 5) & 1;
-                if (part == 0) {
-                    if (s.tma_out && lane == 0) bulk_wait_read<0>();
-                    __syncwarp();
+                if (p.act != kActNone && !f32) act_chunk(v, p.act);
+                // staged as 32 rows of 64 bytes (16-bit outputs, two buffers) or 128 (fp32)
+                const uint32_t buf = f32 ? buf0 : buf0 + static_cast<uint32_t>(nbuf & 1) * 2048u;
+                ++nbuf;
+                if (s.tma_out && lane == 0) {
+                    if (f32) bulk_wait_read<0>();
+                    else bulk_wait_read<1>();
                 }
+                __syncwarp();
                 if (f32) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        sts128(buf + swz(lane, j), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            w[i] = pack2(__uint_as_float(v[8 * j + 2 * i]),
-                                         __uint_as_float(v[8 * j + 2 * i + 1]), p.out_dtype);
-                        sts128(buf + swz(lane, 4 * part + j), w[0], w[1], w[2], w[3]);
+                    for (int i = 0; i < 8; ++i)
+                        sts128(buf + swz(lane, i), v[4 * i], v[4 * i + 1], v[4 * i + 2],
+                               v[4 * i + 3]);
+                    // the fp32 activations are long: a loop over the staged row
+                    for (int i = 0; p.act != kActNone && i < 32; ++i) {
+                        float* y = reinterpret_cast<float*>(
+                            smem_pair + (buf - ring) + swz(lane, i >> 2) + 4 * (i & 3));
+                        *y = activate_f32(*y, p.act);
                     }
-                    if (part == 0 && c + 32 < c_end) continue;
+                } else {
+                    // one branch a chunk: the compiler would test the type at every pair
+                    if (p.out_dtype == kTokBf16) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            v[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            v[i] = pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), kTokF16);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sts128(buf + swz64(lane, i), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                 }
-                const int c0 = f32 ? c : c - 32 * part;   // the buffer's first column
+                const int c0 = half * 128 + 32 * j;
                 if (s.tma_out) {
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -758,64 +772,78 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
                 } else {
                     // rows that TMA cannot address: element stores, 32 columns at once
                     __syncwarp();
-                    const int left = static_cast<int>(min(static_cast<long long>(min(bcols, c_end - c0)),
-                                                          p.outputs - nbase - c0));
+                    const bool in = nbase + c0 + lane < p.outputs;
                     for (int r = 0; r < 32 && m0 + r < p.tokens; ++r) {
-                        const long long at = (m0 + r) * p.out_stride + nbase + c0;
-                        for (int j = lane; j < left; j += 32) {
-                            if (f32) {
-                                uint32_t x;
-                                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x)
-                                             : "r"(buf + swz(r, j >> 2) + 4u * (j & 3)) : "memory");
-                                static_cast<uint32_t*>(p.out)[at + j] = x;
-                            } else {
-                                uint16_t x;
-                                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x)
-                                             : "r"(buf + swz(r, j >> 3) + 2u * (j & 7)) : "memory");
-                                static_cast<uint16_t*>(p.out)[at + j] = x;
-                            }
+                        const long long at = (m0 + r) * p.out_stride + nbase + c0 + lane;
+                        if (f32) {
+                            uint32_t x;
+                            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x)
+                                         : "r"(buf + swz(r, lane >> 2) + 4u * (lane & 3)) : "memory");
+                            if (in) static_cast<uint32_t*>(p.out)[at] = x;
+                        } else {
+                            uint16_t x;
+                            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x)
+                                         : "r"(buf + swz64(r, lane >> 3) + 2u * (lane & 7)) : "memory");
+                            if (in) static_cast<uint16_t*>(p.out)[at] = x;
                         }
                     }
                     __syncwarp();
                 }
-            }
-            if (half * 128 >= c_end) {   // a narrow tile has no columns for this half
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(tempty_dst + 8 * acc);
-            }
+            };
+            uint32_t v0[32], v1[32], v2[32], v3[32];
+            tmem_ld_32x32b_x32(tb, v0);
+            tmem_ld_32x32b_x32(tb + 32, v1);
+            tmem_ld_32x32b_x32(tb + 64, v2);
+            tmem_ld_32x32b_x32(tb + 96, v3);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(tempty_dst + 8 * acc);
+            if (m0 >= p.tokens) continue;
+            if (chunks > 0) chunk(v0, 0);
+            if (chunks > 1) chunk(v1, 1);
+            if (chunks > 2) chunk(v2, 2);
+            if (chunks > 3) chunk(v3, 3);
         }
         // the staging buffers are read out before the CTA leaves
         if (s.tma_out && lane == 0) bulk_wait_read<0>();
-    } else if (!E4M3 && warp >= 12) {
+    } else if (!E4M3) {
         // ------------------------------------------------------ converters (int8)
-        // A stage's TMEM columns are free when its shared memory is (the same
-        // MMAs read both), so its tokens' arrival is all there is to wait for.
+        set_max_regs_dec<48>();
         const int group = (warp - 12) >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t ta = tmem + kTmemA + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        int st = group;
-        uint32_t ph = 0;
+        const uint32_t ready_dst = mapa_shared(ready0, 0);
+        int xs = group, ts = group;   // raw slot, TMEM slot (the weights' stage)
+        uint32_t xph = 0, tph = 0;
         for (int i = group; i < total; i += 2) {
-            if (!__all_sync(0xffffffffu,
-                            wait_long(xfull0 + 8 * st, ph, abort_flag, p.status, p.wait_ns)))
-                break;
-            if ((warp & 3) == 0 && lane == 0) misc[4] = static_cast<uint32_t>(i + 1);
+            const bool ok = wait_long(xfull0 + 8 * xs, xph, abort_flag, p.status, p.wait_ns) &&
+                            wait_long(empty0 + 8 * ts, tph ^ 1u, abort_flag, p.status, p.wait_ns);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if ((warp & 3) == 0 && lane == 0) misc[5] = static_cast<uint32_t>(i + 1);
             tc_fence_after();
-            const uint32_t src = ring + st * Shape::kStage;
+            const uint32_t src = toks + xs * kTokBytes;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t v[32];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) cvt_chunk(lds128(src + swz(r, 4 * h + j)), v + 8 * j);
-                tmem_st_32x32b_x32(ta + st * 64 + h * 32, v);
+                tmem_st_32x32b_x32(ta + ts * 64 + h * 32, v);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(xempty0 + 8 * xs);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(xcvt0 + 8 * st);
-            st += 2;
-            if (st >= s.stages) {   // an even number of stages
-                st -= s.stages;
-                ph ^= 1u;
+            if (lane == 0) mbar_arrive_cluster_relaxed(ready_dst + 8 * ts);
+            xs += 2;
+            if (xs >= Shape::kTokSlots) {
+                xs -= Shape::kTokSlots;
+                xph ^= 1u;
+            }
+            ts += 2;
+            if (ts >= Shape::kStages) {
+                ts -= Shape::kStages;
+                tph ^= 1u;
             }
         }
     }
@@ -830,11 +858,11 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
         while (clock64() - t0 < 200000) {
         }
         if (threadIdx.x == 0) {
-            const uint32_t issued = misc[2], depth = static_cast<uint32_t>(s.stages);
-            for (uint32_t i = misc[3]; rank == 0 && i < issued; ++i)
-                drain_wait(wfull0 + 8 * (i % depth), (i / depth) & 1u);
-            for (uint32_t i = misc[4]; !E4M3 && i < issued; ++i)
-                drain_wait(xfull0 + 8 * (i % depth), (i / depth) & 1u);
+            for (uint32_t i = misc[3]; rank == 0 && i < misc[2]; ++i)
+                drain_wait(wfull0 + 8 * (i % Shape::kStages), (i / Shape::kStages) & 1u);
+            for (uint32_t i = misc[5]; !E4M3 && i < misc[4]; ++i)
+                drain_wait(xfull0 + 8 * (i % PairShape<false>::kTokSlots),
+                           (i / PairShape<false>::kTokSlots) & 1u);
         }
         if (warp == 1 && lane == 0 && rank == 0) {
             tc_commit_pair(drain_bar, 1);
@@ -962,9 +990,7 @@ void plan_pair(const LinearParams& p, int num_sms, LinearPlan* r) {
     r->tok_tiles = static_cast<int>((p.tokens + 255) / 256);
     r->out_tiles = static_cast<int>((p.outputs + r->out_tile - 1) / r->out_tile);
     r->splits = 1;
-    r->stages = p.e4m3 ? PairShape<true>::kStages : PairShape<false>::kStages;
-    r->smem = static_cast<size_t>(r->stages) * (p.e4m3 ? PairShape<true>::kStage : PairShape<false>::kStage) +
-              8 * 4096 + 2048 + 5 * 8 * kMaxStages + 40 + 24;
+    r->smem = p.e4m3 ? PairShape<true>::kBytes : PairShape<false>::kBytes;
     const long long tiles = static_cast<long long>(r->tok_tiles) * r->out_tiles;
     r->grid = static_cast<int>(2 * std::min<long long>(tiles, num_sms / 2));
 }
@@ -1017,7 +1043,6 @@ cudaError_t launch_linear(const LinearMaps& maps, const LinearParams& p, const L
         s.n_tiles = plan.out_tiles;
         s.group_m = 8;
         s.k_steps = k_steps;
-        s.stages = plan.stages;
         s.nacc = p.e4m3 ? 512 / s.bn >= 2 ? 2 : 1 : static_cast<int>(kTmemA) / s.bn >= 2 ? 2 : 1;
         s.tma_out = plan.tma_out;
         s.f_group = make_fastdiv(static_cast<uint32_t>(s.group_m * s.n_tiles));

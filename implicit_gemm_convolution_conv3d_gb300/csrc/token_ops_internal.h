@@ -56,8 +56,7 @@ struct LinearPlan {
     int tok_box, out_box;   // rows of a TMA box of either operand
     int out_tiles, tok_tiles;
     int splits;             // split: CTAs of a cluster that share a tile's reduction
-    int stages;             // ring of TMA boxes
-    int cvt_stages;         // split, int8: ring of converted operands
+    int stages, cvt_stages; // split: rings of TMA boxes and of converted (int8) operands
     int tma_out;            // pair: the output's rows can be stored by TMA
     int grid;               // pair: CTAs
     size_t smem;
