@@ -72,6 +72,10 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
                  : "memory");
 }
 
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -416,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   warp 0       TMA producer (int8: of the weights)
 //   warp 1       TMEM, MMA issuer (leader CTA)
 //   warp 2       int8: TMA producer of the tokens
-//   warps 4-11   epilogue: lane = token, 128 outputs a warp
+//   warps 4-     epilogue (e4m3 16 warps, int8 8): lane = token, 64 or 128 outputs a warp
 //   warps 12-19  int8: tokens to f16 into TMEM, two groups on alternate k-steps
 // int8: the tokens cross shared memory once as bytes (their f16 form goes to
 // TMEM); the weights come as f16 from the workspace, where one short launch has
@@ -444,7 +448,6 @@ struct PairParams {
     FastDiv f_group, f_gm;
 };
 
-constexpr int kPairEpi = 256;                             // epilogue threads
 constexpr uint32_t kTokBytes = kRows * kStep;             // tokens of a k-step and CTA
 constexpr uint32_t kTmemA = 256;                          // TMEM columns of the converted tokens
 template <bool E4M3>
@@ -454,13 +457,27 @@ struct PairShape {
     static constexpr uint32_t kStage = kWBytes + (E4M3 ? kTokBytes : 0u);
     static constexpr int kStages = E4M3 ? 6 : 4;
     static constexpr int kTokSlots = E4M3 ? 0 : 3;   // int8: raw tokens
-    static constexpr int kThreads = 128 + kPairEpi + (E4M3 ? 0 : 256);
+    // epilogue warps, and the 32-column chunks that each takes of a tile
+    static constexpr int kEpiWarps = E4M3 ? 16 : 8, kChunks = 32 / kEpiWarps;
+    static constexpr uint32_t kStaging = E4M3 ? 2048u : 4096u;   // of a warp: one or two 2 KB buffers
+    static constexpr int kThreads = 128 + 32 * kEpiWarps + (E4M3 ? 0 : 256);
     static constexpr uint32_t kEpi0 = kStages * kStage + kTokSlots * kTokBytes;
-    static constexpr uint32_t kCols0 = kEpi0 + 8u * 4096u;
-    static constexpr uint32_t kBars0 = kCols0 + 8u * 256u;
+    static constexpr uint32_t kBars0 = kEpi0 + kEpiWarps * kStaging;
     static constexpr uint32_t kBytes = kBars0 + 5u * 8u * kMaxStages + 40u + 32u;
 };
 static_assert(PairShape<true>::kBytes <= 227u * 1024u && PairShape<false>::kBytes <= 227u * 1024u, "");
+
+// Two accumulators: v * sx * f + b, with the two-wide fp32 instructions.
+__device__ __forceinline__ void scale2(uint32_t& v0, uint32_t& v1, float sx, uint32_t f0, uint32_t f1,
+                                       uint32_t b0, uint32_t b1) {
+    asm("{\n\t.reg .b64 v, s, f, b;\n\t"
+        "mov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\t"
+        "mov.b64 f, {%3, %4};\n\tmov.b64 b, {%5, %6};\n\t"
+        "mul.rn.f32x2 v, v, s;\n\tfma.rn.f32x2 v, v, f, b;\n\t"
+        "mov.b64 {%0, %1}, v;\n\t}"
+        : "+r"(v0), "+r"(v1)
+        : "r"(__float_as_uint(sx)), "r"(f0), "r"(f1), "r"(b0), "r"(b1));
+}
 
 // The activation of a chunk in registers, in the forms for 16-bit outputs.
 __device__ __forceinline__ void act_chunk(uint32_t (&v)[32], int act) {
@@ -531,7 +548,7 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull0 + 8 * i, 1);
-            mbar_init(tempty0 + 8 * i, 16);
+            mbar_init(tempty0 + 8 * i, 2 * Shape::kEpiWarps);
         }
         mbar_init(drain_bar, 1);
         for (int i = 1; i < 6; ++i) misc[i] = 0u;
@@ -554,9 +571,8 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
     // k-steps of this pair's tiles
     const int total = first < tiles ? ((tiles - first + stride - 1) / stride) * s.k_steps : 0;
 
-    // Each warpgroup takes its share of the launch's registers: int8, 20 warps of
-    // 96: 4 x 40 + 8 x 168 + 8 x 48 <= 1920; e4m3, 12 warps of 168: 4 x 56 + 8 x 216
-    // <= 2016.
+    // Each warpgroup takes its share of the launch's registers, 20 warps of 96:
+    // e4m3 4 x 56 + 16 x 104, int8 4 x 40 + 8 x 168 + 8 x 48, both <= 1920.
     if (warp < 4) {
         set_max_regs_dec<E4M3 ? 56 : 40>();
         if (warp == 0) {
@@ -673,14 +689,12 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
                 }
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < 4 + Shape::kEpiWarps) {
         // ------------------------------------------------------ epilogue
-        set_max_regs_inc<E4M3 ? 216 : 168>();
-        const int q = warp & 3, half = (warp - 4) >> 2;
+        set_max_regs_inc<E4M3 ? 104 : 168>();
+        const int q = warp & 3, col0 = ((warp - 4) >> 2) * 32 * Shape::kChunks;
         const uint32_t tempty_dst = mapa_shared(tempty0, 0);
-        const uint32_t buf0 = ring + Shape::kEpi0 + static_cast<uint32_t>(warp - 4) * 4096u;
-        // 32 scales and 32 biases of the chunk at hand, read as broadcasts
-        float* cols = reinterpret_cast<float*>(smem_pair + Shape::kCols0) + (warp - 4) * 64;
+        const uint32_t buf0 = ring + Shape::kEpi0 + static_cast<uint32_t>(warp - 4) * Shape::kStaging;
         const bool f32 = p.out_dtype == kTokF32;
         int it = 0, nbuf = 0;
         for (int t = first; t < tiles; t += stride, ++it) {
@@ -689,10 +703,10 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
             const long long nbase = static_cast<long long>(tl.nt) * s.bn;
             const long long m0 = static_cast<long long>(tl.mt) * 256 + rank * kRows + q * 32;
             // this lane's scale and bias of each 32-column chunk
-            float csw[4], cbi[4];
+            float csw[Shape::kChunks], cbi[Shape::kChunks];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = half * 128 + 32 * j + lane;
+            for (int j = 0; j < Shape::kChunks; ++j) {
+                const int c = col0 + 32 * j + lane;
                 const bool in = c < ncols && nbase + c < p.outputs;
                 csw[j] = in && p.scale_w ? __ldg(p.scale_w + nbase + c) : 1.0f;
                 cbi[j] = in && p.bias ? __ldg(p.bias + nbase + c) : 0.0f;
@@ -705,62 +719,28 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
                 break;
             tc_fence_after();
             const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) +
-                                static_cast<uint32_t>(acc * s.bn + half * 128);
-            // 32-column chunks of this half that have outputs; all four are loaded (the
-            // columns exist), so that the accumulator goes back at once
-            const int chunks = max(0, min(4, (ncols - half * 128 + 31) >> 5));
-            auto chunk = [&](uint32_t (&v)[32], int j) {
+                                static_cast<uint32_t>(acc * s.bn + col0);
+            // chunks that have outputs; all are loaded (the columns exist), so that the
+            // accumulator goes back at once
+            const int chunks = max(0, min(Shape::kChunks, (ncols - col0 + 31) >> 5));
+            uint32_t v[Shape::kChunks][32];
+#pragma unroll
+            for (int j = 0; j < Shape::kChunks; ++j) tmem_ld_32x32b_x32(tb + 32 * j, v[j]);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(tempty_dst + 8 * acc);
+            if (m0 >= p.tokens) continue;
+            // Outputs leave through 2 KB buffers of 32 rows x 64 bytes.  free_buffer:
+            // the next one, when its last store has read it; store_buffer: its
+            // columns [c0, c0 + width) to the output.
+            auto free_buffer = [&]() {
+                const uint32_t buf = buf0 + (E4M3 ? 0u : static_cast<uint32_t>(nbuf++ & 1) * 2048u);
+                if (s.tma_out && lane == 0) bulk_wait_read<E4M3 ? 0 : 1>();
                 __syncwarp();
-                cols[lane] = csw[j];
-                cols[32 + lane] = cbi[j];
-                __syncwarp();
-                const float4* sw4 = reinterpret_cast<const float4*>(cols);
-                const float4* bi4 = reinterpret_cast<const float4*>(cols + 32);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 sw = sw4[i], bi = bi4[i];
-                    const float f[4] = {sw.x, sw.y, sw.z, sw.w}, b[4] = {bi.x, bi.y, bi.z, bi.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        v[4 * i + k] = __float_as_uint(
-                            __uint_as_float(v[4 * i + k]) * sx * f[k] + b[k]);
-                }
-                if (p.act != kActNone && !f32) act_chunk(v, p.act);
-                // staged as 32 rows of 64 bytes (16-bit outputs, two buffers) or 128 (fp32)
-                const uint32_t buf = f32 ? buf0 : buf0 + static_cast<uint32_t>(nbuf & 1) * 2048u;
-                ++nbuf;
-                if (s.tma_out && lane == 0) {
-                    if (f32) bulk_wait_read<0>();
-                    else bulk_wait_read<1>();
-                }
-                __syncwarp();
-                if (f32) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        sts128(buf + swz(lane, i), v[4 * i], v[4 * i + 1], v[4 * i + 2],
-                               v[4 * i + 3]);
-                    // the fp32 activations are long: a loop over the staged row
-                    for (int i = 0; p.act != kActNone && i < 32; ++i) {
-                        float* y = reinterpret_cast<float*>(
-                            smem_pair + (buf - ring) + swz(lane, i >> 2) + 4 * (i & 3));
-                        *y = activate_f32(*y, p.act);
-                    }
-                } else {
-                    // one branch a chunk: the compiler would test the type at every pair
-                    if (p.out_dtype == kTokBf16) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            v[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            v[i] = pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), kTokF16);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        sts128(buf + swz64(lane, i), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                }
-                const int c0 = half * 128 + 32 * j;
+                return buf;
+            };
+            auto store_buffer = [&](uint32_t buf, int c0) {
                 if (s.tma_out) {
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -769,41 +749,81 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
                         tma_store_2d(&o_map, buf, static_cast<int>(nbase) + c0, static_cast<int>(m0));
                         bulk_commit();
                     }
-                } else {
-                    // rows that TMA cannot address: element stores, 32 columns at once
-                    __syncwarp();
-                    const bool in = nbase + c0 + lane < p.outputs;
-                    for (int r = 0; r < 32 && m0 + r < p.tokens; ++r) {
-                        const long long at = (m0 + r) * p.out_stride + nbase + c0 + lane;
-                        if (f32) {
-                            uint32_t x;
-                            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x)
-                                         : "r"(buf + swz(r, lane >> 2) + 4u * (lane & 3)) : "memory");
-                            if (in) static_cast<uint32_t*>(p.out)[at] = x;
-                        } else {
-                            uint16_t x;
-                            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x)
-                                         : "r"(buf + swz64(r, lane >> 3) + 2u * (lane & 7)) : "memory");
-                            if (in) static_cast<uint16_t*>(p.out)[at] = x;
-                        }
-                    }
-                    __syncwarp();
+                    return;
                 }
+                // rows that TMA cannot address: element stores, 64 bytes of a row at once
+                __syncwarp();
+                if (f32) {
+                    const int c = lane & 15;
+                    for (int r = lane >> 4; r < 32 && m0 + r < p.tokens; r += 2) {
+                        uint32_t x;
+                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x)
+                                     : "r"(buf + swz64(r, c >> 2) + 4u * (c & 3)) : "memory");
+                        if (nbase + c0 + c < p.outputs)
+                            static_cast<uint32_t*>(p.out)[(m0 + r) * p.out_stride + nbase + c0 + c] = x;
+                    }
+                } else {
+                    for (int r = 0; r < 32 && m0 + r < p.tokens; ++r) {
+                        uint16_t x;
+                        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x)
+                                     : "r"(buf + swz64(r, lane >> 3) + 2u * (lane & 7)) : "memory");
+                        if (nbase + c0 + lane < p.outputs)
+                            static_cast<uint16_t*>(p.out)[(m0 + r) * p.out_stride + nbase + c0 + lane] = x;
+                    }
+                }
+                __syncwarp();
             };
-            uint32_t v0[32], v1[32], v2[32], v3[32];
-            tmem_ld_32x32b_x32(tb, v0);
-            tmem_ld_32x32b_x32(tb + 32, v1);
-            tmem_ld_32x32b_x32(tb + 64, v2);
-            tmem_ld_32x32b_x32(tb + 96, v3);
-            tmem_ld_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(tempty_dst + 8 * acc);
-            if (m0 >= p.tokens) continue;
-            if (chunks > 0) chunk(v0, 0);
-            if (chunks > 1) chunk(v1, 1);
-            if (chunks > 2) chunk(v2, 2);
-            if (chunks > 3) chunk(v3, 3);
+#pragma unroll
+            for (int j = 0; j < Shape::kChunks; ++j) {
+                if (j >= chunks) break;
+                uint32_t(&y)[32] = v[j];
+                uint32_t buf = free_buffer();
+                // the chunk's 32 scales and 32 biases, through the buffer as broadcasts
+                sts32(buf + 4u * lane, __float_as_uint(csw[j]));
+                sts32(buf + 128u + 4u * lane, __float_as_uint(cbi[j]));
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 f = lds128(buf + 16u * i), b = lds128(buf + 128u + 16u * i);
+                    scale2(y[4 * i], y[4 * i + 1], sx, f.x, f.y, b.x, b.y);
+                    scale2(y[4 * i + 2], y[4 * i + 3], sx, f.z, f.w, b.z, b.w);
+                }
+                __syncwarp();
+                const int c0 = col0 + 32 * j;
+                if (f32) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {   // 16 columns a buffer
+                        if (h == 1) buf = free_buffer();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            sts128(buf + swz64(lane, i), y[16 * h + 4 * i], y[16 * h + 4 * i + 1],
+                                   y[16 * h + 4 * i + 2], y[16 * h + 4 * i + 3]);
+                        // the fp32 activations are long: a loop over the staged row
+                        for (int i = 0; p.act != kActNone && i < 16; ++i) {
+                            float* e = reinterpret_cast<float*>(
+                                smem_pair + (buf - ring) + swz64(lane, i >> 2) + 4 * (i & 3));
+                            *e = activate_f32(*e, p.act);
+                        }
+                        store_buffer(buf, c0 + 16 * h);
+                    }
+                    continue;
+                }
+                if (p.act != kActNone) act_chunk(y, p.act);
+                // one branch a chunk: the compiler would test the type at every pair
+                if (p.out_dtype == kTokBf16) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        y[i] = pack_bf16x2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        y[i] = pack2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]), kTokF16);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sts128(buf + swz64(lane, i), y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                store_buffer(buf, c0);
+            }
         }
         // the staging buffers are read out before the CTA leaves
         if (s.tma_out && lane == 0) bulk_wait_read<0>();

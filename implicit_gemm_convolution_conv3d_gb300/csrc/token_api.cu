@@ -222,7 +222,7 @@ int linear_w8a8_fwd(const void* x, int64_t x_stride, const void* w, int64_t w_st
         return rc;
     if (plan.pair && plan.tma_out &&
         (rc = encode_rows(&maps.out, out, static_cast<int>(elt), outputs, tokens,
-                          (tokens == 1 ? outputs * elt + 15 & ~15ll : out_stride * elt), 32, elt == 4 ? 128 : 64)))
+                          (tokens == 1 ? outputs * elt + 15 & ~15ll : out_stride * elt), 32, 64)))
         return rc;
     cudaError_t e = cudaSuccess;
     if (copy_x) e = launch_pad_rows(src_x, x_stride, tokens, width, const_cast<uint8_t*>(p.x), pitch, stream);
