@@ -957,29 +957,6 @@ __global__ void __launch_bounds__(256) widen_rows_kernel(const uint8_t* src, lon
     }
 }
 
-template <typename Kernel, typename... Args>
-cudaError_t launch_ex(Kernel kern, unsigned grid, unsigned threads, size_t smem, int cluster,
-                      cudaStream_t stream, const Args&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(threads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    int n = 0;
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n++].val.programmaticStreamSerializationAllowed = overrides().pdl != 0;
-    if (cluster > 1) {
-        attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
-        attr[n].val.clusterDim.y = 1;
-        attr[n++].val.clusterDim.z = 1;
-    }
-    cfg.attrs = attr;
-    cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <bool E4M3>
 cudaError_t launch_split(const CUtensorMap& w_map, const CUtensorMap& x_map, const SplitParams& s,
                          const LinearPlan& plan, cudaStream_t stream) {

@@ -1,0 +1,104 @@
+// token_act.cu -- the (gated) activation with an 8-bit output:
+//
+//   v = act(x), or act(gate) * value for a row [gate | value]
+//   scale = max|v| / qmax;  q = nearest code of v / scale
+//
+// Read once, held in registers for the row's maximum, written as codes: 3 bytes an
+// element for 16-bit inputs, 5 gated.
+#include <cuda_runtime.h>
+
+#include "token_ops_internal.h"
+#include "token_rows.cuh"
+
+namespace c3d {
+
+namespace {
+
+template <typename TX, int ACT, bool E4M3, int VEC>
+__global__ void __launch_bounds__(kMaxRowThreads)
+    act_row_kernel(const ActParams p) {
+    __shared__ uint32_t shu[32];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int n = static_cast<int>(p.width), t = threadIdx.x, threads = blockDim.x;
+    const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (row >= p.tokens) return;   // whole warps: a row's threads leave together
+    const TX* x = static_cast<const TX*>(p.x) + row * p.x_stride;
+    float v[kHeld];
+    load_row<VEC>(x, n, t, threads, v);
+    if (p.gated) {
+        float b[kHeld];
+        load_row<VEC>(x + n, n, t, threads, b);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) v[i] = activate_f32(v[i], ACT) * b[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) v[i] = activate_f32(v[i], ACT);
+    }
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) m = max_abs_nan(m, v[i]);
+    const uint32_t top = row_max(__float_as_uint(m), threads >> 5, shu);
+    const float scale = row_scale(top, E4M3 ? 448.0f : 127.0f);
+    store_codes<VEC, E4M3>(p.q + row * p.q_stride, n, t, threads, v, scale, row_blank(top), p.wide_q);
+    if (t == 0) p.scale[row] = scale;
+}
+
+// Rows that do not fit: read twice.
+template <typename TX, bool E4M3>
+__global__ void __launch_bounds__(kWideThreads)
+    act_wide_kernel(const ActParams p) {
+    __shared__ uint32_t shu[32];
+    griddep_launch_dependents();
+    griddep_wait();
+    const long long n = p.width, row = blockIdx.x;
+    const TX* x = static_cast<const TX*>(p.x) + row * p.x_stride;
+    uint8_t* q = p.q + row * p.q_stride;
+    auto v_at = [&](long long i) {
+        const float a = activate_f32(to_f32(x[i]), p.act);
+        return p.gated ? a * to_f32(x[n + i]) : a;
+    };
+    uint32_t m = 0;
+    for (long long i = threadIdx.x; i < n; i += blockDim.x) m = max(m, abs_bits(v_at(i)));
+    const uint32_t top = row_max(m, blockDim.x >> 5, shu);
+    const float scale = row_scale(top, E4M3 ? 448.0f : 127.0f);
+    for (long long i = threadIdx.x; i < n; i += blockDim.x)
+        q[i] = row_blank(top) ? 0 : static_cast<uint8_t>(code_of<E4M3>(v_at(i), scale));
+    if (threadIdx.x == 0) p.scale[row] = scale;
+}
+
+template <typename TX, int ACT, bool E4M3>
+cudaError_t act_launch(const ActParams& p, cudaStream_t stream) {
+    const int xb = elt_bytes(p.x_dtype);
+    const bool wide = p.width % 8 == 0 && aligned_rows(p.x, p.x_stride, p.tokens, xb, 16);
+    const dim3 block = row_block(p.width);
+    const unsigned grid = row_blocks(p.tokens, block);
+    return wide ? launch_ex(act_row_kernel<TX, ACT, E4M3, 8>, grid, block, 0, 1, stream, p)
+                : launch_ex(act_row_kernel<TX, ACT, E4M3, 1>, grid, block, 0, 1, stream, p);
+}
+
+template <typename TX, bool E4M3>
+cudaError_t act_kind(const ActParams& p, cudaStream_t stream) {
+    if (p.width > kMaxRowWidth)
+        return launch_ex(act_wide_kernel<TX, E4M3>, static_cast<unsigned>(p.tokens),
+                         dim3(kWideThreads), 0, 1, stream, p);
+    if (p.act == kActRelu) return act_launch<TX, kActRelu, E4M3>(p, stream);
+    if (p.act == kActSilu) return act_launch<TX, kActSilu, E4M3>(p, stream);
+    if (p.act == kActGelu) return act_launch<TX, kActGelu, E4M3>(p, stream);
+    return act_launch<TX, kActNone, E4M3>(p, stream);
+}
+
+template <typename TX>
+cudaError_t act_types(const ActParams& p, cudaStream_t stream) {
+    return p.q_dtype == kTokE4m3 ? act_kind<TX, true>(p, stream) : act_kind<TX, false>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_act_quant(const ActParams& p, cudaStream_t stream) {
+    if (p.x_dtype == kTokBf16) return act_types<__nv_bfloat16>(p, stream);
+    if (p.x_dtype == kTokF16) return act_types<__half>(p, stream);
+    return act_types<float>(p, stream);
+}
+
+}  // namespace c3d

@@ -72,4 +72,30 @@ __device__ __forceinline__ uint32_t code_of(float v, float scale) {
     return static_cast<uint32_t>(__float2int_rn(c)) & 0xFFu;
 }
 
+// Launch with programmatic stream serialization (unless overridden): the kernel
+// may start while the previous one in the stream runs, and waits for it
+// (griddep_wait) before it touches global memory.  cluster: CTAs of a cluster.
+template <typename Kernel, typename... Args>
+inline cudaError_t launch_ex(Kernel kern, unsigned grid, dim3 block, size_t smem, int cluster,
+                             cudaStream_t stream, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = overrides().pdl != 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 }  // namespace c3d

@@ -1,0 +1,139 @@
+// token_norm.cu -- the root-mean-square norm with the residual's addition and an
+// 8-bit output:
+//
+//   h = x + residual;  r = 1 / sqrt(mean(h^2) + eps);  v = h r w
+//   scale = max|v| / qmax;  q = nearest code of v / scale
+//
+// Bound by memory: x and the residual are read once and h, q and the scale
+// written once (7 bytes an element for a bf16 stream); the row waits in registers
+// for its two reductions.
+#include <cuda_runtime.h>
+
+#include "token_ops_internal.h"
+#include "token_rows.cuh"
+
+namespace c3d {
+
+namespace {
+
+template <typename TX, typename TR, bool E4M3, int VEC>
+__global__ void __launch_bounds__(kMaxRowThreads)
+    norm_row_kernel(const NormParams p) {
+    __shared__ float shf[32];
+    __shared__ uint32_t shu[32];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int n = static_cast<int>(p.width), t = threadIdx.x, threads = blockDim.x;
+    const int warps = threads >> 5;
+    const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (row >= p.tokens) return;   // whole warps: a row's threads leave together
+    float h[kHeld];
+    load_row<VEC>(static_cast<const TX*>(p.x) + row * p.x_stride, n, t, threads, h);
+    if (p.res) {
+        float r[kHeld];
+        load_row<VEC>(static_cast<const TR*>(p.res) + row * p.res_stride, n, t, threads, r);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) h[i] += r[i];
+        if (p.res_out)
+            store_row<VEC>(static_cast<TR*>(p.res_out) + row * p.res_out_stride, n, t, threads, h);
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const float s = h[i] * p.shrink;
+        ss = fmaf(s, s, ss);
+    }
+    const float rms = 1.0f / sqrtf(row_sum(ss, warps, shf) * p.mean_of + p.eps);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) h[i] *= rms;
+    if (p.weight) {
+        float w[kHeld];
+        if (p.weight_dtype == kTokF32)
+            load_row<VEC>(static_cast<const float*>(p.weight), n, t, threads, w);
+        else
+            load_row<VEC>(static_cast<const TX*>(p.weight), n, t, threads, w);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) h[i] *= w[i];
+    }
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) m = max_abs_nan(m, h[i]);
+    const uint32_t top = row_max(__float_as_uint(m), warps, shu);
+    const float scale = row_scale(top, E4M3 ? 448.0f : 127.0f);
+    store_codes<VEC, E4M3>(p.q + row * p.q_stride, n, t, threads, h, scale, row_blank(top), p.wide_q);
+    if (t == 0) p.scale[row] = scale;
+}
+
+// Rows that do not fit: read again for each pass (mean square, maximum, codes).
+template <typename TX, typename TR, bool E4M3>
+__global__ void __launch_bounds__(kWideThreads)
+    norm_wide_kernel(const NormParams p) {
+    __shared__ float shf[32];
+    __shared__ uint32_t shu[32];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int n = static_cast<int>(p.width), warps = blockDim.x >> 5;
+    const long long row = blockIdx.x;
+    const TX* x = static_cast<const TX*>(p.x) + row * p.x_stride;
+    const TR* r = p.res ? static_cast<const TR*>(p.res) + row * p.res_stride : nullptr;
+    TR* ro = p.res_out ? static_cast<TR*>(p.res_out) + row * p.res_out_stride : nullptr;
+    uint8_t* q = p.q + row * p.q_stride;
+    auto h_at = [&](int i) { return to_f32(x[i]) + (r ? to_f32(r[i]) : 0.0f); };
+    float ss = 0.0f;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const float h = h_at(i) * p.shrink;
+        ss = fmaf(h, h, ss);
+    }
+    const float rms = 1.0f / sqrtf(row_sum(ss, warps, shf) * p.mean_of + p.eps);
+    auto v_of = [&](float h, int i) {
+        const float w = !p.weight ? 1.0f
+                        : p.weight_dtype == kTokF32 ? static_cast<const float*>(p.weight)[i]
+                                                    : to_f32(static_cast<const TX*>(p.weight)[i]);
+        return h * rms * w;
+    };
+    uint32_t m = 0;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) m = max(m, abs_bits(v_of(h_at(i), i)));
+    const uint32_t top = row_max(m, warps, shu);
+    const float scale = row_scale(top, E4M3 ? 448.0f : 127.0f);
+    // each element is read before this thread writes it: residual_out may be an input
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const float h = h_at(i);
+        q[i] = row_blank(top) ? 0 : static_cast<uint8_t>(code_of<E4M3>(v_of(h, i), scale));
+        if (ro) ro[i] = from_f32<TR>(h);
+    }
+    if (threadIdx.x == 0) p.scale[row] = scale;
+}
+
+template <typename TX, typename TR, bool E4M3>
+cudaError_t norm_launch(const NormParams& p, cudaStream_t stream) {
+    if (p.width > kMaxRowWidth)
+        return launch_ex(norm_wide_kernel<TX, TR, E4M3>, static_cast<unsigned>(p.tokens),
+                         dim3(kWideThreads), 0, 1, stream, p);
+    const int xb = elt_bytes(p.x_dtype), rb = elt_bytes(p.res_dtype);
+    const bool wide = p.width % 8 == 0 && aligned_rows(p.x, p.x_stride, p.tokens, xb, 16) &&
+                      aligned_rows(p.res, p.res_stride, p.tokens, rb, 16) &&
+                      aligned_rows(p.res_out, p.res_out_stride, p.tokens, rb, 16) &&
+                      aligned_rows(p.weight, 0, 1, 1, 16);
+    const dim3 block = row_block(p.width);
+    const unsigned grid = row_blocks(p.tokens, block);
+    return wide ? launch_ex(norm_row_kernel<TX, TR, E4M3, 8>, grid, block, 0, 1, stream, p)
+                : launch_ex(norm_row_kernel<TX, TR, E4M3, 1>, grid, block, 0, 1, stream, p);
+}
+
+template <typename TX>
+cudaError_t norm_types(const NormParams& p, cudaStream_t stream) {
+    const bool e4m3 = p.q_dtype == kTokE4m3;
+    if (p.res && p.res_dtype == kTokF32)
+        return e4m3 ? norm_launch<TX, float, true>(p, stream) : norm_launch<TX, float, false>(p, stream);
+    return e4m3 ? norm_launch<TX, TX, true>(p, stream) : norm_launch<TX, TX, false>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_quant(const NormParams& p, cudaStream_t stream) {
+    if (p.x_dtype == kTokBf16) return norm_types<__nv_bfloat16>(p, stream);
+    if (p.x_dtype == kTokF16) return norm_types<__half>(p, stream);
+    return norm_types<float>(p, stream);
+}
+
+}  // namespace c3d
