@@ -143,6 +143,137 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, int dtype) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Up to 16 bytes (left < 16: the rest zeros) from any address, put together from
+// the aligned 4-byte words that hold at least one of them.
+__device__ __forceinline__ uint4 load_bytes(const uint8_t* src, long long left) {
+    const int n = static_cast<int>(min(16ll, left));
+    uint32_t o[4] = {0u, 0u, 0u, 0u};
+    if (n > 0) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(src);
+        const int sh = static_cast<int>(a & 3u);
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(a - sh);
+        const int need = (sh + n + 3) >> 2;
+        uint32_t v[5];
+#pragma unroll
+        for (int j = 0; j < 5; ++j) v[j] = j < need ? q[j] : 0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            o[j] = __funnelshift_r(v[j], v[j + 1], 8 * sh);
+            const int in = n - 4 * j;   // bytes of this word that were asked for
+            if (in < 4) o[j] = in <= 0 ? 0u : o[j] & ((1u << (8 * in)) - 1u);
+        }
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// ---------------------------------------------------------------- few tokens
+// Up to 16 tokens: the weights are all there is to read, once, and latency is what
+// is left.  A CTA takes 16 weight rows, its warps interleave over the reduction
+// in steps of 64 bytes, and everything goes from global memory to registers to
+// mma.sync (m16n8k16, f16): a dot product does not care in which order its terms
+// come, so a lane's 16 contiguous bytes of a weight row and of a token serve as
+// the k pairs that the instruction's fragments want (lane t of a quad: bytes
+// 16 t .. 16 t + 15 of the step, four k16 products).  tcgen05's detour (TMA ring,
+// tensor memory, a cluster's reduction) took 8.1 us for one token through
+// 8192 x 2048 int8 against THIN_US here; its 128-row operand would be 1/16 full.
+// Rows of any alignment: the unaligned ones are put together from aligned words.
+constexpr int kThinRows = 16, kThinTok = 16, kThinMaxWarps = 16;
+
+template <bool E4M3>
+__device__ __forceinline__ void thin_cvt(const uint4& v, uint32_t (&o)[8]) {
+    if (!E4M3) {
+        cvt_chunk(v, o);
+        return;
+    }
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(o[2 * i]), "=r"(o[2 * i + 1]) : "r"(w[i]));
+}
+
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The 16 bytes at column c of a row (zeros outside it, or where the row is NULL).
+template <bool ALIGNED>
+__device__ __forceinline__ uint4 thin_load(const uint8_t* row, long long c, long long width) {
+    if (!row || c >= width) return make_uint4(0u, 0u, 0u, 0u);
+    if (ALIGNED && c + 16 <= width) return __ldg(reinterpret_cast<const uint4*>(row + c));
+    return load_bytes(row + c, width - c);
+}
+
+// NB blocks of 8 tokens
+template <bool E4M3, int NB, bool ALIGNED>
+__global__ void __launch_bounds__(32 * kThinMaxWarps)
+    linear_thin_kernel(const LinearParams p) {
+    __shared__ float part[kThinMaxWarps][8 * NB][kThinRows];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const long long n0 = static_cast<long long>(blockIdx.x) * kThinRows;
+    const uint8_t* w0 = n0 + g < p.outputs ? p.w + (n0 + g) * p.w_stride : nullptr;
+    const uint8_t* w1 = n0 + g + 8 < p.outputs ? p.w + (n0 + g + 8) * p.w_stride : nullptr;
+    const uint8_t* xr[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) xr[b] = 8 * b + g < p.tokens ? p.x + (8 * b + g) * p.x_stride : nullptr;
+    float acc[NB][4] = {};
+    const long long step = 64ll * warps;
+    constexpr int kAhead = 4;   // steps whose loads are in flight together
+    for (long long c = 64ll * warp + 16 * t; c - 16 * t < p.width; c += kAhead * step) {
+        uint4 a[kAhead][2], x[kAhead][NB];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            a[i][0] = thin_load<ALIGNED>(w0, c + i * step, p.width);
+            a[i][1] = thin_load<ALIGNED>(w1, c + i * step, p.width);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) x[i][b] = thin_load<ALIGNED>(xr[b], c + i * step, p.width);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            uint32_t u[8], v[8];
+            thin_cvt<E4M3>(a[i][0], u);
+            thin_cvt<E4M3>(a[i][1], v);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                uint32_t y[8];
+                thin_cvt<E4M3>(x[i][b], y);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    mma_f16_16816(acc[b], u[2 * j], v[2 * j], u[2 * j + 1], v[2 * j + 1], y[2 * j],
+                                  y[2 * j + 1]);
+            }
+        }
+    }
+    // the warps' partial sums, added in warp order
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        part[warp][8 * b + 2 * t][g] = acc[b][0];
+        part[warp][8 * b + 2 * t + 1][g] = acc[b][1];
+        part[warp][8 * b + 2 * t][g + 8] = acc[b][2];
+        part[warp][8 * b + 2 * t + 1][g + 8] = acc[b][3];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 8 * NB * kThinRows; i += blockDim.x) {
+        const int m = i / kThinRows, r = i % kThinRows;
+        const long long n = n0 + r;
+        if (m >= p.tokens || n >= p.outputs) continue;
+        float v = 0.0f;
+        for (int k = 0; k < warps; ++k) v += part[k][m][r];
+        v = v * (p.scale_x ? p.scale_x[m] : 1.0f) * (p.scale_w ? p.scale_w[n] : 1.0f) +
+            (p.bias ? p.bias[n] : 0.0f);
+        store_one(p.out, p.out_dtype, m * p.out_stride + n, epi_act(v, p.act, p.out_dtype));
+    }
+}
+
 // ---------------------------------------------------------------- split tiles
 // One tile (128 outputs x up to 128 tokens) per cluster, its reduction split
 // over the cluster's CTAs: the form for few tokens, where the weights are all
@@ -898,29 +1029,6 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
     }
 }
 
-// Up to 16 bytes (left < 16: the rest zeros) from any address, put together from
-// the aligned 4-byte words that hold at least one of them.
-__device__ __forceinline__ uint4 load_bytes(const uint8_t* src, long long left) {
-    const int n = static_cast<int>(min(16ll, left));
-    uint32_t o[4] = {0u, 0u, 0u, 0u};
-    if (n > 0) {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(src);
-        const int sh = static_cast<int>(a & 3u);
-        const uint32_t* q = reinterpret_cast<const uint32_t*>(a - sh);
-        const int need = (sh + n + 3) >> 2;
-        uint32_t v[5];
-#pragma unroll
-        for (int j = 0; j < 5; ++j) v[j] = j < need ? q[j] : 0u;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            o[j] = __funnelshift_r(v[j], v[j + 1], 8 * sh);
-            const int in = n - 4 * j;   // bytes of this word that were asked for
-            if (in < 4) o[j] = in <= 0 ? 0u : o[j] & ((1u << (8 * in)) - 1u);
-        }
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
 // Rows of any alignment copied to a 16-byte pitch, zeros behind each row: one
 // thread per 16-byte word.
 __global__ void __launch_bounds__(256) pad_rows_kernel(const uint8_t* src, long long stride,
@@ -1021,6 +1129,28 @@ void plan_split(const LinearParams& p, int num_sms, LinearPlan* r) {
 }  // namespace
 
 bool linear_pair_form(long long tokens) { return tokens > 512; }
+bool linear_thin_form(long long tokens) { return tokens <= kThinTok; }
+
+cudaError_t launch_linear_thin(const LinearParams& p, int num_sms, cudaStream_t stream) {
+    const unsigned grid = static_cast<unsigned>((p.outputs + kThinRows - 1) / kThinRows);
+    // as many warps on a row block's reduction as fill the GPU to about 24 warps an
+    // SM, each with at least one step
+    int warps = kThinMaxWarps;
+    while (warps > 2 && (static_cast<long long>(grid) * warps > 24ll * num_sms || 64ll * warps / 2 >= p.width))
+        warps /= 2;
+    const bool aligned = (reinterpret_cast<uintptr_t>(p.x) & 15u) == 0 &&
+                         (reinterpret_cast<uintptr_t>(p.w) & 15u) == 0 &&
+                         (p.tokens == 1 || p.x_stride % 16 == 0) && (p.outputs == 1 || p.w_stride % 16 == 0);
+    const dim3 block(static_cast<unsigned>(32 * warps));
+#define C3D_THIN(F8, NB, AL) launch_ex(linear_thin_kernel<F8, NB, AL>, grid, block, 0, 1, stream, p)
+    if (p.tokens <= 8) {
+        if (p.e4m3) return aligned ? C3D_THIN(true, 1, true) : C3D_THIN(true, 1, false);
+        return aligned ? C3D_THIN(false, 1, true) : C3D_THIN(false, 1, false);
+    }
+    if (p.e4m3) return aligned ? C3D_THIN(true, 2, true) : C3D_THIN(true, 2, false);
+    return aligned ? C3D_THIN(false, 2, true) : C3D_THIN(false, 2, false);
+#undef C3D_THIN
+}
 
 LinearPlan plan_linear(const LinearParams& p, int num_sms) {
     LinearPlan r{};

@@ -144,7 +144,7 @@ int act_quant_fwd(const void* x, int x_dtype, int64_t x_stride, int act, int gat
 size_t linear_w8a8_workspace_size(const void* x, int64_t x_stride, const void* w,
                                   int64_t w_stride, int dtype, int64_t tokens, int64_t outputs,
                                   int64_t width) {
-    if (tokens < 1 || outputs < 1 || width < 1) return 0;
+    if (tokens < 1 || outputs < 1 || width < 1 || linear_thin_form(tokens)) return 0;
     const size_t pitch = static_cast<size_t>(round16(width));
     const bool widen = dtype == CONV_DTYPE_INT8 && linear_pair_form(tokens);
     return (tma_rows(x, x_stride, tokens) ? 0 : pitch * static_cast<size_t>(tokens)) +
@@ -195,6 +195,8 @@ int linear_w8a8_fwd(const void* x, int64_t x_stride, const void* w, int64_t w_st
     if (rc) return rc;
     p.status = lim.status;
     p.wait_ns = lim.wait_ns;
+    if (linear_thin_form(tokens))
+        return launched(launch_linear_thin(p, lim.num_sms, stream), "linear_w8a8_fwd launch");
     // operands that TMA cannot address are copied to an aligned pitch first, and
     // the pair form's int8 weights are widened to f16
     const bool widen = !p.e4m3 && linear_pair_form(tokens);
