@@ -175,7 +175,7 @@ __device__ __forceinline__ uint4 load_bytes(const uint8_t* src, long long left) 
 // the k pairs that the instruction's fragments want (lane t of a quad: bytes
 // 16 t .. 16 t + 15 of the step, four k16 products).  tcgen05's detour (TMA ring,
 // tensor memory, a cluster's reduction) took 8.1 us for one token through
-// 8192 x 2048 int8 against THIN_US here; its 128-row operand would be 1/16 full.
+// 8192 x 2048 int8 against 5.0 here; its 128-row operand would be 1/16 full.
 // Rows of any alignment: the unaligned ones are put together from aligned words.
 constexpr int kThinRows = 16, kThinTok = 16, kThinMaxWarps = 16;
 
@@ -210,8 +210,8 @@ __device__ __forceinline__ uint4 thin_load(const uint8_t* row, long long c, long
     return load_bytes(row + c, width - c);
 }
 
-// NB blocks of 8 tokens
-template <bool E4M3, int NB, bool ALIGNED>
+// NB blocks of 8 tokens; AHEAD steps whose loads are in flight together
+template <bool E4M3, int NB, bool ALIGNED, int AHEAD>
 __global__ void __launch_bounds__(32 * kThinMaxWarps)
     linear_thin_kernel(const LinearParams p) {
     __shared__ float part[kThinMaxWarps][8 * NB][kThinRows];
@@ -227,18 +227,17 @@ __global__ void __launch_bounds__(32 * kThinMaxWarps)
     for (int b = 0; b < NB; ++b) xr[b] = 8 * b + g < p.tokens ? p.x + (8 * b + g) * p.x_stride : nullptr;
     float acc[NB][4] = {};
     const long long step = 64ll * warps;
-    constexpr int kAhead = 4;   // steps whose loads are in flight together
-    for (long long c = 64ll * warp + 16 * t; c - 16 * t < p.width; c += kAhead * step) {
-        uint4 a[kAhead][2], x[kAhead][NB];
+    for (long long c = 64ll * warp + 16 * t; c - 16 * t < p.width; c += AHEAD * step) {
+        uint4 a[AHEAD][2], x[AHEAD][NB];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
+        for (int i = 0; i < AHEAD; ++i) {
             a[i][0] = thin_load<ALIGNED>(w0, c + i * step, p.width);
             a[i][1] = thin_load<ALIGNED>(w1, c + i * step, p.width);
 #pragma unroll
             for (int b = 0; b < NB; ++b) x[i][b] = thin_load<ALIGNED>(xr[b], c + i * step, p.width);
         }
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
+        for (int i = 0; i < AHEAD; ++i) {
             uint32_t u[8], v[8];
             thin_cvt<E4M3>(a[i][0], u);
             thin_cvt<E4M3>(a[i][1], v);
@@ -1133,16 +1132,22 @@ bool linear_thin_form(long long tokens) { return tokens <= kThinTok; }
 
 cudaError_t launch_linear_thin(const LinearParams& p, int num_sms, cudaStream_t stream) {
     const unsigned grid = static_cast<unsigned>((p.outputs + kThinRows - 1) / kThinRows);
-    // as many warps on a row block's reduction as fill the GPU to about 24 warps an
-    // SM, each with at least one step
+    // Few row blocks: 16 warps each, four steps ahead (95 registers).  Many: as many
+    // warps as fill the GPU to 48 an SM, two steps ahead, so that more of them are
+    // resident.  Measured each way: 2048 x 8192 int8 5.6 us against 7.5, 8192 x 2048
+    // 6.2 against 5.0, 8192 x 8192 e4m3 16.9 against 12.7.
+    const bool many = grid >= 2u * static_cast<unsigned>(num_sms);
     int warps = kThinMaxWarps;
-    while (warps > 2 && (static_cast<long long>(grid) * warps > 24ll * num_sms || 64ll * warps / 2 >= p.width))
+    while (warps > 2 && ((many && static_cast<long long>(grid) * warps > 48ll * num_sms) ||
+                         64ll * warps / 2 >= p.width))
         warps /= 2;
     const bool aligned = (reinterpret_cast<uintptr_t>(p.x) & 15u) == 0 &&
                          (reinterpret_cast<uintptr_t>(p.w) & 15u) == 0 &&
                          (p.tokens == 1 || p.x_stride % 16 == 0) && (p.outputs == 1 || p.w_stride % 16 == 0);
     const dim3 block(static_cast<unsigned>(32 * warps));
-#define C3D_THIN(F8, NB, AL) launch_ex(linear_thin_kernel<F8, NB, AL>, grid, block, 0, 1, stream, p)
+#define C3D_THIN(F8, NB, AL)                                                                     \
+    (many ? launch_ex(linear_thin_kernel<F8, NB, AL, 2>, grid, block, 0, 1, stream, p)          \
+          : launch_ex(linear_thin_kernel<F8, NB, AL, 4>, grid, block, 0, 1, stream, p))
     if (p.tokens <= 8) {
         if (p.e4m3) return aligned ? C3D_THIN(true, 1, true) : C3D_THIN(true, 1, false);
         return aligned ? C3D_THIN(false, 1, true) : C3D_THIN(false, 1, false);

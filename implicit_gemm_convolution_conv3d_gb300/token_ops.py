@@ -18,6 +18,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import ACT_CODES, _check, _stream_handle, load_library
+from . import _raw_current_stream as _raw_stream
 
 CONV_DTYPE_INT8, CONV_DTYPE_F16, CONV_DTYPE_F32 = 2, 3, 4
 _FLOAT = {torch.bfloat16: 0, torch.float16: CONV_DTYPE_F16, torch.float32: CONV_DTYPE_F32}
@@ -74,26 +75,42 @@ def _vector(t: Optional[torch.Tensor], n: int, what: str, other=torch.float32) -
     """Data pointer of a contiguous CUDA vector of n elements, fp32 (or `other`)."""
     if t is None:
         return None
-    if t.dtype != torch.float32 and t.dtype != other:
-        raise TypeError(f"{what} must be float32" + ("" if other == torch.float32 else f" or {other}"))
+    if t.dtype is not torch.float32 and t.dtype is not other:
+        raise TypeError(f"{what} must be float32" + ("" if other is torch.float32 else f" or {other}"))
     if t.numel() != n or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous CUDA tensor of {n} elements")
     return t.data_ptr()
 
 
-def _codes_out(x, width, qdtype, out, scale_out):
-    """The (given or new) code and scale tensors for rows of x, with their layout."""
+def _given_rows(t: torch.Tensor, shape, width: int, rows: int, types: dict,
+                what: str) -> Tuple[int, int]:
+    """(row stride, type code) of a given output for tokens of `shape`, `width` wide."""
+    out_rows, out_width, stride, code = _rows(t, types, what)
+    if out_width != width or out_rows != rows or len(t.shape) != len(shape) or (
+            len(shape) > 2 and t.shape[:-1] != shape[:-1]):
+        raise ValueError(f"{what} must have shape {tuple(shape[:-1]) + (width,)}")
+    return stride, code
+
+
+def _stream(stream: Optional[torch.cuda.Stream], x: torch.Tensor):
+    return _stream_handle(stream, x.device.index) if stream is not None or _raw_stream is None \
+        else _raw_stream(x.device.index)
+
+
+def _codes_out(x, rows, width, qdtype, out, scale_out):
+    """The (given or new) code and scale tensors for rows of x: with the codes'
+    row stride and type and the scales' pointer."""
     if out is None:
-        if qdtype not in _CODE:
+        code = _CODE.get(qdtype)
+        if code is None:
             raise TypeError("qdtype must be torch.int8 or torch.float8_e4m3fn")
-        out = torch.empty(x.shape[:-1] + (width,), dtype=qdtype, device=x.device)
-    elif out.shape[:-1] != x.shape[:-1] or out.shape[-1] != width:
-        raise ValueError(f"out must have shape {tuple(x.shape[:-1]) + (width,)}")
+        out, stride = torch.empty(x.shape[:-1] + (width,), dtype=qdtype, device=x.device), width
+    else:
+        stride, code = _given_rows(out, x.shape, width, rows, _CODE, "out")
     if scale_out is None:
         scale_out = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    elif scale_out.dtype != torch.float32:
-        raise TypeError("scale_out must be float32")
-    return out, scale_out
+        return out, scale_out, stride, code, scale_out.data_ptr()
+    return out, scale_out, stride, code, _vector(scale_out, rows, "scale_out")
 
 
 def rms_norm_quant(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
@@ -111,10 +128,9 @@ def rms_norm_quant(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: 
     stands in for ``qdtype``."""
     lib = _fns or _bind()
     rows, width, xs, xc = _rows(x, _FLOAT, "x")
-    out, scale_out = _codes_out(x, width, qdtype, out, scale_out)
-    _, _, qs, qc = _rows(out, _CODE, "out")
+    out, scale_out, qs, qc, sp = _codes_out(x, rows, width, qdtype, out, scale_out)
     wp = _vector(weight, width, "weight", x.dtype)
-    wc = xc if weight is None or weight.dtype == x.dtype else CONV_DTYPE_F32
+    wc = xc if weight is None or weight.dtype is x.dtype else CONV_DTYPE_F32
     rp = op = None
     rc = rs = os_ = 0
     if residual is not None:
@@ -122,16 +138,18 @@ def rms_norm_quant(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: 
             raise ValueError("residual must have x's shape")
         _, _, rs, rc = _rows(residual, _FLOAT, "residual")
         if residual_out is None:
-            residual_out = torch.empty(residual.shape, dtype=residual.dtype, device=x.device)
-        elif residual_out.shape != x.shape or residual_out.dtype != residual.dtype:
-            raise ValueError("residual_out must have the residual's shape and type")
+            residual_out, os_ = torch.empty(x.shape, dtype=residual.dtype, device=x.device), width
+        elif residual_out is residual:
+            os_ = rs
+        else:
+            os_, oc = _given_rows(residual_out, x.shape, width, rows, _FLOAT, "residual_out")
+            if oc != rc:
+                raise ValueError("residual_out must have the residual's type")
         rp, op = residual.data_ptr(), residual_out.data_ptr()
-        _, _, os_, _ = _rows(residual_out, _FLOAT, "residual_out")
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     st = lib.rms_norm_quant_fwd(x.data_ptr(), xc, xs, rp, rc, rs, wp, wc, eps, rows, width, qc,
-                                out.data_ptr(), qs, _vector(scale_out, rows, "scale_out"), op,
-                                os_, _stream_handle(stream, x.device.index))
+                                out.data_ptr(), qs, sp, op, os_, _stream(stream, x))
     if st:
         _check(st, "rms_norm_quant_fwd")
     return out, scale_out, residual_out
@@ -154,14 +172,27 @@ def act_quant(x: torch.Tensor, act: str = "none", gated: bool = False,
         if width % 2:
             raise ValueError("a gated x must have an even number of columns")
         width //= 2
-    out, scale_out = _codes_out(x, width, qdtype, out, scale_out)
-    _, _, qs, qc = _rows(out, _CODE, "out")
+    out, scale_out, qs, qc, sp = _codes_out(x, rows, width, qdtype, out, scale_out)
     st = lib.act_quant_fwd(x.data_ptr(), xc, xs, code, 1 if gated else 0, rows, width, qc,
-                           out.data_ptr(), qs, _vector(scale_out, rows, "scale_out"),
-                           _stream_handle(stream, x.device.index))
+                           out.data_ptr(), qs, sp, _stream(stream, x))
     if st:
         _check(st, "act_quant_fwd")
     return out, scale_out
+
+
+# workspace bytes by the operands' sizes, strides and alignment
+_need_cache: dict = {}
+
+
+def _linear_need(lib, xp, xs, wp, ws, qc, rows, outputs, width) -> int:
+    key = (xs, ws, qc, rows, outputs, width, xp & 15, wp & 15)
+    need = _need_cache.get(key)
+    if need is None:
+        need = lib.linear_w8a8_workspace_size(xp, xs, wp, ws, qc, rows, outputs, width)
+        if len(_need_cache) >= 1024:
+            _need_cache.clear()
+        _need_cache[key] = need
+    return need
 
 
 def linear_w8a8(x: torch.Tensor, w: torch.Tensor, scale_x: Optional[torch.Tensor] = None,
@@ -188,27 +219,28 @@ def linear_w8a8(x: torch.Tensor, w: torch.Tensor, scale_x: Optional[torch.Tensor
     if w_width != width:
         raise ValueError(f"x has rows of {width} elements, w of {w_width}")
     if out is None:
-        if out_dtype not in _FLOAT:
+        oc = _FLOAT.get(out_dtype)
+        if oc is None:
             raise TypeError("out_dtype must be bfloat16, float16 or float32")
-        out = torch.empty(x.shape[:-1] + (outputs,), dtype=out_dtype, device=x.device)
-    elif out.shape[:-1] != x.shape[:-1] or out.shape[-1] != outputs:
-        raise ValueError(f"out must have shape {tuple(x.shape[:-1]) + (outputs,)}")
-    _, _, os_, oc = _rows(out, _FLOAT, "out")
+        out, os_ = torch.empty(x.shape[:-1] + (outputs,), dtype=out_dtype, device=x.device), outputs
+    else:
+        os_, oc = _given_rows(out, x.shape, outputs, rows, _FLOAT, "out")
     xp, wp = x.data_ptr(), w.data_ptr()
-    need = lib.linear_w8a8_workspace_size(xp, xs, wp, ws, qc, rows, outputs, width)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
         if not workspace.is_cuda or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor")
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    elif need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-        ws_ptr, ws_bytes = workspace.data_ptr(), need
+    else:
+        need = _linear_need(lib, xp, xs, wp, ws, qc, rows, outputs, width)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            ws_ptr, ws_bytes = workspace.data_ptr(), need
     st = lib.linear_w8a8_fwd(xp, xs, wp, ws, qc, rows, outputs, width,
                              _vector(scale_x, rows, "scale_x"),
                              _vector(scale_w, outputs, "scale_w"),
                              _vector(bias, outputs, "bias"), code, out.data_ptr(), oc, os_,
-                             ws_ptr, ws_bytes, _stream_handle(stream, x.device.index))
+                             ws_ptr, ws_bytes, _stream(stream, x))
     if st:
         _check(st, "linear_w8a8_fwd")
     return out
