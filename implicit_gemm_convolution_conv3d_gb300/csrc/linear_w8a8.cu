@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // 16384 x 8192 x 8192 against WIDE_TFLOPS; the launch reads and writes 3 bytes per weight.
 //
 // Rings: the tokens' raw slots are free once converted, so that their loads run
-// ahead of the MMAs by both rings (3 raw slots, 4 in TMEM); one ring for both
+// ahead of the MMAs by both rings (4 raw slots, 4 in TMEM); one ring for both
 // operands refilled a stage in 4100 cycles, over the 3072 that it had.
 // Accumulators: e4m3 has two, int8 one (its tokens take the other half of
 // TMEM), which the epilogue therefore first loads into registers as a whole
@@ -586,7 +586,11 @@ struct PairShape {
     // a ring stage: e4m3 tokens and weights, int8 weights (f16) alone
     static constexpr uint32_t kStage = kWBytes + (E4M3 ? kTokBytes : 0u);
     static constexpr int kStages = E4M3 ? 6 : 4;
-    static constexpr int kTokSlots = E4M3 ? 0 : 3;   // int8: raw tokens
+    static constexpr int kTokSlots = E4M3 ? 0 : 4;   // int8: raw tokens
+    // The two converter groups take alternate k-steps.  A parity wait tells a phase
+    // from its neighbours only, so a group has to see every phase of the slots it
+    // waits for: rings of even length, each slot one group's.
+    static_assert(kTokSlots % 2 == 0 && kStages % 2 == 0, "");
     // epilogue warps, and the 32-column chunks that each takes of a tile
     static constexpr int kEpiWarps = E4M3 ? 16 : 8, kChunks = 32 / kEpiWarps;
     static constexpr uint32_t kStaging = E4M3 ? 2048u : 4096u;   // of a warp: one or two 2 KB buffers

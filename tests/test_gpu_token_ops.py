@@ -359,6 +359,34 @@ def test_linear_same_bits_every_time(pkg, q):
 
 
 @pytest.mark.parametrize("q", [I8, E4])
+@pytest.mark.parametrize("m", [520, 700, 1024])
+def test_linear_waiting_for_its_weights(pkg, m, q):
+    """Few token tiles and weights larger than the L2 cache: the products wait for
+    the weights while the tokens run ahead; back to back, and the same bits
+    each time."""
+    g = _gen(m)
+    n = k = 8192
+    x, w = _codes(g, m, k, q), _codes(g, n, k, q)
+    outs = [pkg.linear_w8a8(x, w, out_dtype=FF) for _ in range(12)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(outs[0], o) for o in outs[1:])
+    ref.check_linear(outs[0][:, :512], x, w[:512])
+    ref.check_linear(outs[0][:, -300:], x, w[-300:])
+
+
+@pytest.mark.parametrize("q", [I8, E4])
+@pytest.mark.parametrize("wx,ww", [(1, 0), (0, 1), (1, 1)])
+def test_linear_workspace_follows_each_operand(pkg, q, wx, ww):
+    """The workspace's size depends on either operand's alignment."""
+    g = _gen(5)
+    x, w = _codes(g, 40, 656, q), _codes(g, 100, 656, q)
+    for ox, ow in ((wx, 0), (0, ww), (wx, ww), (0, 0)):
+        a = _unaligned(x.view(torch.uint8), 0, ox).view(q)
+        b = _unaligned(w.view(torch.uint8), 0, ow).view(q)
+        _linear_case(pkg, 40, 100, 656, q, x=a, w=b)
+
+
+@pytest.mark.parametrize("q", [I8, E4])
 def test_linear_past_32_bits(pkg, q):
     """An output of more than 2^32 bytes and 2^31 elements, and token rows that
     lie more than 2^32 bytes apart: sampled rows."""
