@@ -21,10 +21,11 @@ namespace {
 constexpr int kRows = 128;        // weight rows of a tile (tcgen05 M)
 constexpr int kStep = 128;        // reduction elements (bytes) of a k-step
 constexpr int kMaxTok = 128;      // tokens of a tile at most
-constexpr int kCvtThreads = 256;  // converter / epilogue threads
-constexpr int kThreads = 128 + kCvtThreads;
-constexpr int kMaxStages = 8, kMaxCvt = 4;
+template <bool E4M3>
+constexpr int kSplitThreads = 128 + 32 * (E4M3 ? 8 : 16);   // converters / epilogue behind four warps
+constexpr int kMaxStages = 8, kMaxCvt = 4, kMaxSplits = 8;
 constexpr uint32_t kBarBytes = 16u * (kMaxStages + kMaxCvt) + 16u;
+constexpr int kSplitSmem = 206 * 1024;   // rings (200 KB at most), barriers, alignment
 
 // Bounded wait (see wait_bar) of a role that may wait for thousands of cycles:
 // it sleeps in hardware between looks, so that its polling leaves the issue slots
@@ -282,8 +283,11 @@ __global__ void __launch_bounds__(32 * kThinMaxWarps)
 // rank order.
 //   warp 0     TMA producer: raw 128-byte rows of weights and tokens
 //   warp 1     TMEM, MMA issuer
-//   warps 4-7  int8: weights to f16 into TMEM (lane = row); epilogue
-//   warps 8-11 int8: tokens to f16 into shared memory;       epilogue
+//   warps 4-11  int8: weights to f16 into TMEM (lane = row); epilogue
+//   warps 12-19 int8 only: tokens to f16 into shared memory;  epilogue
+// The converters of either operand are two groups of four warps on alternate
+// k-steps: a group's step is 600 to 1600 cycles of latency (wait, read, convert,
+// write, fence) that the other's hides.
 struct SplitParams {
     LinearParams p;
     int tok_tile, out_tiles;
@@ -292,12 +296,13 @@ struct SplitParams {
 };
 
 template <bool E4M3>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kSplitThreads<E4M3>, 1)
     linear_split_kernel(const __grid_constant__ CUtensorMap w_map,
                         const __grid_constant__ CUtensorMap x_map, const SplitParams s) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
+    constexpr int kCvtWarps = kSplitThreads<E4M3> / 32 - 4;
     const LinearParams& p = s.p;
     const int nt = s.tok_tile;
     const uint32_t ring = base;
@@ -322,10 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < s.stages; ++i) {
             mbar_init(full0 + 8 * i, 1);
-            mbar_init(empty0 + 8 * i, E4M3 ? 1 : kCvtThreads / 32);
+            mbar_init(empty0 + 8 * i, E4M3 ? 1 : 8);
         }
         for (int i = 0; i < s.cvt; ++i) {
-            mbar_init(cfull0 + 8 * i, kCvtThreads / 32);
+            mbar_init(cfull0 + 8 * i, 8);
             mbar_init(cempty0 + 8 * i, 1);
         }
         mbar_init(acc_bar, 1);
@@ -408,18 +413,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= 4) {
         bool ok = true;
         if (!E4M3) {
-            int st = 0, c = 0;
+            // even rings: a group sees every phase of the slots it waits for
+            const int group = ((warp - 4) >> 2) & 1;
+            int st = group, c = group;
             uint32_t ph = 0, cph = 0;
-            for (int i = 0; i < steps; ++i) {
+            for (int i = group; i < steps; i += 2) {
                 ok = wait_bar(full0 + 8 * st, ph, abort_flag, p.status, p.wait_ns) &&
                      wait_bar(cempty0 + 8 * c, cph ^ 1u, abort_flag, p.status, p.wait_ns);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
                 }
-                if (threadIdx.x == 128) misc[3] = i + 1;
+                if ((warp == 4 || warp == 8) && lane == 0) misc[3] = i + 1;
                 const uint32_t src = ring + st * s.stage_bytes;
-                if (warp < 8) {
+                if (warp < 12) {
                     tc_fence_after();
                     const int r = (warp & 3) * 32 + lane;
 #pragma unroll
@@ -433,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_st_wait();
                     tc_fence_before();
                 } else {
-                    cvt_rows(src + kRows * kStep, cvt0 + c * s.cvt_bytes, nt, threadIdx.x - 256, 128);
+                    cvt_rows(src + kRows * kStep, cvt0 + c * s.cvt_bytes, nt, threadIdx.x & 127, 128);
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
@@ -441,19 +448,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(empty0 + 8 * st);
                     mbar_arrive(cfull0 + 8 * c);
                 }
-                if (++st == s.stages) {
-                    st = 0;
+                st += 2;
+                if (st >= s.stages) {
+                    st -= s.stages;
                     ph ^= 1u;
                 }
-                if (++c == s.cvt) {
-                    c = 0;
+                c += 2;
+                if (c >= s.cvt) {
+                    c -= s.cvt;
                     cph ^= 1u;
                 }
             }
         }
         // the accumulator as [token][output] fp32 over the ring, which every
         // load and MMA has left by now
-        if (ok && wait_bar(acc_bar, 0, abort_flag, p.status, p.wait_ns)) {
+        if (warp < 12 && ok && wait_bar(acc_bar, 0, abort_flag, p.status, p.wait_ns)) {
             tc_fence_after();
             const int q = warp & 3, half = warp >= 8;
             const int valid = static_cast<int>(min(static_cast<long long>(nt), p.tokens - m0));
@@ -475,8 +484,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (s.splits > 1) cluster_sync();
     else __syncthreads();
     if (warp >= 4 && !*abort_flag) {
-        // this rank's share of the tile's tokens, a row of 128 outputs per warp
-        const int t_lo = nt * rank / s.splits, t_hi = nt * (rank + 1) / s.splits;
+        // this rank's share of the tile's tokens, a row of 128 outputs per warp and turn
+        const int t_lo = nt * rank / s.splits;
+        const int t_hi = static_cast<int>(min(static_cast<long long>(nt * (rank + 1) / s.splits), p.tokens - m0));
         const int n = n0 + 4 * lane;
         float sw[4], b[4];
 #pragma unroll
@@ -489,22 +499,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool wide = n + 3 < p.outputs &&
                           ((reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(p.out_stride * elt)) &
                            (4 * elt - 1)) == 0;
-        for (int t = t_lo + warp - 4; t < t_hi; t += kCvtThreads / 32) {
-            const long long m = m0 + t;
-            if (m >= p.tokens) break;
-            const uint32_t a = ring + static_cast<uint32_t>(t * kRows + 4 * lane) * 4u;
-            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            for (int r = 0; r < s.splits; ++r) {
-                const float4 f = ld_cluster_f4(mapa_shared(a, s.splits > 1 ? r : cluster_ctarank()));
-                v[0] += f.x;
-                v[1] += f.y;
-                v[2] += f.z;
-                v[3] += f.w;
-            }
-            const float sx = p.scale_x ? __ldg(p.scale_x + m) : 1.0f;
+        auto finish = [&](float (&v)[4], int t, float sx) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] = epi_act(v[j] * sx * sw[j] + b[j], p.act, p.out_dtype);
-            const long long at = m * p.out_stride + n;
+            const long long at = (m0 + t) * p.out_stride + n;
             if (wide) {
                 if (elt == 4)
                     *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) =
@@ -516,6 +514,45 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (n + j < p.outputs) store_one(p.out, p.out_dtype, at + j, v[j]);
+            }
+        };
+        if (s.splits > 1) {
+            // one token a turn: the ranks' partials at once (a peer's shared memory is
+            // far away), then added in rank order
+            for (int t = t_lo + warp - 4; t < t_hi; t += kCvtWarps) {
+                const uint32_t a = ring + static_cast<uint32_t>(t * kRows + 4 * lane) * 4u;
+                const float sx = p.scale_x ? __ldg(p.scale_x + m0 + t) : 1.0f;
+                float4 f[kMaxSplits];
+#pragma unroll
+                for (int r = 0; r < kMaxSplits; ++r)
+                    f[r] = r < s.splits ? ld_cluster_f4(mapa_shared(a, r)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int r = 0; r < kMaxSplits; ++r) {
+                    v[0] += f[r].x;
+                    v[1] += f[r].y;
+                    v[2] += f[r].z;
+                    v[3] += f[r].w;
+                }
+                finish(v, t, sx);
+            }
+        } else {
+            constexpr int kTurns = 4;   // tokens whose loads are in flight together
+            for (int t0 = t_lo + warp - 4; t0 < t_hi; t0 += kTurns * kCvtWarps) {
+                float v[kTurns][4], sx[kTurns];
+#pragma unroll
+                for (int u = 0; u < kTurns; ++u) {
+                    const int t = min(t0 + u * kCvtWarps, t_hi - 1);
+                    const uint4 w = lds128(ring + static_cast<uint32_t>(t * kRows + 4 * lane) * 4u);
+                    v[u][0] = __uint_as_float(w.x);
+                    v[u][1] = __uint_as_float(w.y);
+                    v[u][2] = __uint_as_float(w.z);
+                    v[u][3] = __uint_as_float(w.w);
+                    sx[u] = p.scale_x ? __ldg(p.scale_x + m0 + t) : 1.0f;
+                }
+#pragma unroll
+                for (int u = 0; u < kTurns; ++u)
+                    if (t0 + u * kCvtWarps < t_hi) finish(v[u], t0 + u * kCvtWarps, sx[u]);
             }
         }
     }
@@ -1068,14 +1105,57 @@ __global__ void __launch_bounds__(256) widen_rows_kernel(const uint8_t* src, lon
     }
 }
 
+// Clusters of 2, 4 and 8 split-kernel CTAs (one per SM) that the current device
+// runs at once; asked once per device (the GPCs' sizes decide it, not the SM count).
+struct ClusterRoom {
+    int of[4];   // by log2 of the cluster's size
+};
+
+template <bool E4M3>
+cudaError_t cluster_room(int num_sms, ClusterRoom* room) {
+    static std::atomic<int> known[kMaxDevices][4];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    room->of[0] = num_sms;
+    for (int i = 1; i < 4; ++i) {
+        int n = dev < kMaxDevices ? known[dev][i].load(std::memory_order_acquire) : 0;
+        if (n == 0) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(num_sms / (1 << i) * (1 << i)), 1, 1);
+            cfg.blockDim = dim3(kSplitThreads<E4M3>, 1, 1);
+            cfg.dynamicSmemBytes = kSplitSmem;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 1u << i;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if ((e = cudaOccupancyMaxActiveClusters(&n, linear_split_kernel<E4M3>, &cfg)) != cudaSuccess)
+                return e;
+            n = std::max(n, 1);
+            if (dev < kMaxDevices) known[dev][i].store(n, std::memory_order_release);
+        }
+        room->of[i] = n;
+    }
+    return cudaSuccess;
+}
+
+// the split kernel may use kSplitSmem bytes
+template <bool E4M3>
+cudaError_t allow_split_smem() {
+    static std::atomic<int> smem_set[kMaxDevices];
+    return ensure_dynamic_smem(linear_split_kernel<E4M3>, kSplitSmem, smem_set);
+}
+
 template <bool E4M3>
 cudaError_t launch_split(const CUtensorMap& w_map, const CUtensorMap& x_map, const SplitParams& s,
                          const LinearPlan& plan, cudaStream_t stream) {
-    static std::atomic<int> smem_set[kMaxDevices];
-    cudaError_t e = ensure_dynamic_smem(linear_split_kernel<E4M3>, plan.smem, smem_set);
+    cudaError_t e = allow_split_smem<E4M3>();
     if (e != cudaSuccess) return e;
     const long long grid = static_cast<long long>(plan.out_tiles) * plan.tok_tiles * plan.splits;
-    return launch_ex(linear_split_kernel<E4M3>, static_cast<unsigned>(grid), kThreads, plan.smem,
+    return launch_ex(linear_split_kernel<E4M3>, static_cast<unsigned>(grid), kSplitThreads<E4M3>, plan.smem,
                      plan.splits, stream, w_map, x_map, s);
 }
 
@@ -1103,7 +1183,7 @@ void plan_pair(const LinearParams& p, int num_sms, LinearPlan* r) {
     r->grid = static_cast<int>(2 * std::min<long long>(tiles, num_sms / 2));
 }
 
-void plan_split(const LinearParams& p, int num_sms, LinearPlan* r) {
+void plan_split(const LinearParams& p, const ClusterRoom& room, LinearPlan* r) {
     r->pair = 0;
     r->tok_tiles = static_cast<int>((p.tokens + kMaxTok - 1) / kMaxTok);
     const long long per = (p.tokens + r->tok_tiles - 1) / r->tok_tiles;
@@ -1114,17 +1194,21 @@ void plan_split(const LinearParams& p, int num_sms, LinearPlan* r) {
     r->out_tiles = static_cast<int>((p.outputs + kRows - 1) / kRows);
     const long long tiles = static_cast<long long>(r->tok_tiles) * r->out_tiles;
     const long long k_steps = (p.width + kStep - 1) / kStep;
+    // the reduction over as many CTAs as can run at once (a second wave costs more
+    // than it gives) and have a step each
     r->splits = 1;
-    while (r->splits < 8 && tiles * r->splits * 2 <= num_sms && r->splits * 2 <= k_steps) r->splits *= 2;
+    for (int i = 1; i < 4; ++i)
+        if (tiles <= room.of[i] && (1 << i) <= k_steps) r->splits = 1 << i;
     // rings within 200 KB: raw stages of both operands, converted tokens (f16)
     const int stage = (kRows + r->tok_tile) * kStep, cvt = r->tok_tile * 256;
     r->cvt_stages = p.e4m3 ? 0 : (r->tok_tile <= 64 ? kMaxCvt : 2);
     r->stages = std::min(kMaxStages, (200 * 1024 - r->cvt_stages * cvt) / stage);
     const long long per_rank = (k_steps + r->splits - 1) / r->splits;
-    r->stages = static_cast<int>(std::max<long long>(1, std::min<long long>(r->stages, per_rank)));
+    r->stages = static_cast<int>(std::min<long long>(r->stages, per_rank));
+    r->stages = std::max(2, r->stages / 2 * 2);   // even (see the converters)
     // the ring also holds the fp32 partial tile
     const int ring = std::max(r->stages * stage, r->tok_tile * kRows * 4);
-    r->stages = std::max(r->stages, (ring + stage - 1) / stage);
+    r->stages = std::max(r->stages, (ring + 2 * stage - 1) / (2 * stage) * 2);
     r->smem = static_cast<size_t>(r->stages) * stage + static_cast<size_t>(r->cvt_stages) * cvt + kBarBytes +
               32 + 1024;
 }
@@ -1161,11 +1245,17 @@ cudaError_t launch_linear_thin(const LinearParams& p, int num_sms, cudaStream_t 
 #undef C3D_THIN
 }
 
-LinearPlan plan_linear(const LinearParams& p, int num_sms) {
-    LinearPlan r{};
-    if (linear_pair_form(p.tokens)) plan_pair(p, num_sms, &r);
-    else plan_split(p, num_sms, &r);
-    return r;
+cudaError_t plan_linear(const LinearParams& p, int num_sms, LinearPlan* r) {
+    *r = LinearPlan{};
+    if (linear_pair_form(p.tokens)) {
+        plan_pair(p, num_sms, r);
+        return cudaSuccess;
+    }
+    ClusterRoom room;
+    cudaError_t e = p.e4m3 ? allow_split_smem<true>() : allow_split_smem<false>();
+    if (e == cudaSuccess) e = p.e4m3 ? cluster_room<true>(num_sms, &room) : cluster_room<false>(num_sms, &room);
+    if (e == cudaSuccess) plan_split(p, room, r);
+    return e;
 }
 
 cudaError_t launch_linear(const LinearMaps& maps, const LinearParams& p, const LinearPlan& plan,

@@ -212,7 +212,8 @@ int linear_w8a8_fwd(const void* x, int64_t x_stride, const void* w, int64_t w_st
     if (copy_w || widen) p.w = at;
     p.x_stride = copy_x || tokens == 1 ? pitch : x_stride;
     p.w_stride = copy_w || widen || outputs == 1 ? pitch : w_stride;
-    LinearPlan plan = plan_linear(p, lim.num_sms);
+    LinearPlan plan;
+    if ((rc = launched(plan_linear(p, lim.num_sms, &plan), "linear_w8a8_fwd plan"))) return rc;
     if (static_cast<long long>(plan.out_tiles) * plan.tok_tiles * plan.splits > kMaxDim) {
         set_last_error("the output has more than 2^31 tiles");
         return CONV_ERR_UNSUPPORTED;

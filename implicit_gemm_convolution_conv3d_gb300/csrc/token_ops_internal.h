@@ -69,7 +69,7 @@ bool linear_pair_form(long long tokens);
 // whether the form for few tokens runs it: any alignment, no tensor maps
 bool linear_thin_form(long long tokens);
 cudaError_t launch_linear_thin(const LinearParams& p, int num_sms, cudaStream_t stream);
-LinearPlan plan_linear(const LinearParams& p, int num_sms);
+cudaError_t plan_linear(const LinearParams& p, int num_sms, LinearPlan* plan);
 
 struct LinearMaps {
     CUtensorMap x, w, out;  // out: pair kernel with tma_out only
