@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kSplitThreads<E4M3>, 1)
 // MMA) it moves 16 KB of raw tokens in and out, 32 KB of weights in and 32 KB
 // of the MMA's reads, 96 bytes a cycle.  Converting the weights here too
 // takes 128 (raw in and out, f16 in and out), and measured 1475 TFLOP/s at
-// 16384 x 8192 x 8192 against WIDE_TFLOPS; the launch reads and writes 3 bytes per weight.
+// 16384 x 8192 x 8192 against 1907; the launch moves 3 bytes per weight.
 //
 // Rings: the tokens' raw slots are free once converted, so that their loads run
 // ahead of the MMAs by both rings (4 raw slots, 4 in TMEM); one ring for both
@@ -1215,7 +1215,19 @@ void plan_split(const LinearParams& p, const ClusterRoom& room, LinearPlan* r) {
 
 }  // namespace
 
-bool linear_pair_form(long long tokens) { return tokens > 512; }
+// The pair form's tile is 256 tokens high and its k-step costs the same at any
+// width, so it pays where the split form's 128 x 128 tiles would need a second
+// wave (152 SMs): 512 x 8192 x 2048 int8 24.5 us against 33.4, e4m3 11.0 against
+// 21.6; within one wave the split form wins (1024 x 2048 x 2048 int8 16.9 us
+// against 19.3, 512 x 2048 x 8192 e4m3 15.3 against 24.0) except for e4m3 with more
+// than 512 tokens (1024 x 2048 x 2048: 9.9 pair, 11.0 split).  Up to 256 tokens
+// the pair's second CTA would have nothing to do, and int8 weights are not worth
+// widening (256 x 8192 x 2048: 23.5 pair, 16.9 split).
+bool linear_pair_form(long long tokens, long long outputs, int e4m3) {
+    if (tokens <= 256) return false;
+    const long long tiles = (tokens + kMaxTok - 1) / kMaxTok * ((outputs + kRows - 1) / kRows);
+    return tiles > 152 || (e4m3 && tokens > 512);
+}
 bool linear_thin_form(long long tokens) { return tokens <= kThinTok; }
 
 cudaError_t launch_linear_thin(const LinearParams& p, int num_sms, cudaStream_t stream) {
@@ -1247,7 +1259,7 @@ cudaError_t launch_linear_thin(const LinearParams& p, int num_sms, cudaStream_t 
 
 cudaError_t plan_linear(const LinearParams& p, int num_sms, LinearPlan* r) {
     *r = LinearPlan{};
-    if (linear_pair_form(p.tokens)) {
+    if (linear_pair_form(p.tokens, p.outputs, p.e4m3)) {
         plan_pair(p, num_sms, r);
         return cudaSuccess;
     }

@@ -63,9 +63,9 @@ struct LinearPlan {
     int grid;               // pair: CTAs
     size_t smem;
 };
-// whether the pair form runs a product of this many tokens; its int8 weights are
-// then f16 rows in the workspace (launch_widen_rows)
-bool linear_pair_form(long long tokens);
+// whether the pair form runs this product; its int8 weights are then f16 rows in
+// the workspace (launch_widen_rows)
+bool linear_pair_form(long long tokens, long long outputs, int e4m3);
 // whether the form for few tokens runs it: any alignment, no tensor maps
 bool linear_thin_form(long long tokens);
 cudaError_t launch_linear_thin(const LinearParams& p, int num_sms, cudaStream_t stream);
