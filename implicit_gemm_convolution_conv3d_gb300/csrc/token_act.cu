@@ -14,7 +14,7 @@ namespace c3d {
 
 namespace {
 
-template <typename TX, int ACT, bool E4M3, int VEC>
+template <typename TX, int ACT, bool GATED, bool E4M3, int VEC>
 __global__ void __launch_bounds__(kMaxRowThreads)
     act_row_kernel(const ActParams p) {
     __shared__ uint32_t shu[32];
@@ -26,14 +26,17 @@ __global__ void __launch_bounds__(kMaxRowThreads)
     const TX* x = static_cast<const TX*>(p.x) + row * p.x_stride;
     float v[kHeld];
     load_row<VEC>(x, n, t, threads, v);
-    if (p.gated) {
-        float b[kHeld];
-        load_row<VEC>(x + n, n, t, threads, b);
+    float b[GATED ? kHeld : 1];
+    if constexpr (GATED) load_row<VEC>(x + n, n, t, threads, b);
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) v[i] = activate_f32(v[i], ACT) * b[i];
-    } else {
+    for (int i = 0; i < kHeld; i += 2) {
+        const float2 y = act2<ACT>(make_float2(v[i], v[i + 1]));
+        v[i] = y.x;
+        v[i + 1] = y.y;
+    }
+    if (GATED) {
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) v[i] = activate_f32(v[i], ACT);
+        for (int i = 0; i < kHeld; ++i) v[i] *= b[i];
     }
     float m = 0.0f;
 #pragma unroll
@@ -73,8 +76,10 @@ cudaError_t act_launch(const ActParams& p, cudaStream_t stream) {
     const bool wide = p.width % 8 == 0 && aligned_rows(p.x, p.x_stride, p.tokens, xb, 16);
     const dim3 block = row_block(p.width);
     const unsigned grid = row_blocks(p.tokens, block);
-    return wide ? launch_ex(act_row_kernel<TX, ACT, E4M3, 8>, grid, block, 0, 1, stream, p)
-                : launch_ex(act_row_kernel<TX, ACT, E4M3, 1>, grid, block, 0, 1, stream, p);
+#define C3D_ACT(G, V) launch_ex(act_row_kernel<TX, ACT, G, E4M3, V>, grid, block, 0, 1, stream, p)
+    if (p.gated) return wide ? C3D_ACT(true, 8) : C3D_ACT(true, 1);
+    return wide ? C3D_ACT(false, 8) : C3D_ACT(false, 1);
+#undef C3D_ACT
 }
 
 template <typename TX, bool E4M3>

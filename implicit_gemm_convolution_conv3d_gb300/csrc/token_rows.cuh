@@ -116,6 +116,68 @@ __device__ __forceinline__ float max_abs_nan(float a, float b) {
     return r;
 }
 
+// ---------------------------------------------------------------- activations
+// Two at a time with the two-wide fp32 instructions: the row kernels have about 16
+// (ungated) to 27 (gated) instruction slots an element before arithmetic costs
+// more than memory does, where erfcf alone takes more.  Two of them are
+// special-function operations (2^x and 1/x, a quarter of the rate).
+
+__device__ __forceinline__ float ex2_approx(float x) {   // 2 ulp; subnormal results kept
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// e^-y for y >= 0: 2^-t with t = y log2(e) rounded, times e^(t ln 2 - y), what the
+// rounding left over, as 1 + (t ln 2 - y); ln 2 in two parts (Cody and Waite,
+// "Software Manual for the Elementary Functions", 1980).  Without it t's rounding
+// costs y * 2^-24 of relative error.
+__device__ __forceinline__ float2 exp_neg2(float2 y) {
+    const float2 t = __fmul2_rn(y, make_float2(1.44269504f, 1.44269504f));
+    float2 r = __ffma2_rn(t, make_float2(0.693147182f, 0.693147182f), make_float2(-y.x, -y.y));
+    r = __ffma2_rn(t, make_float2(-1.90465421e-9f, -1.90465421e-9f), r);
+    const float2 e = make_float2(ex2_approx(-t.x), ex2_approx(-t.y));
+    return __ffma2_rn(e, r, e);
+}
+
+// v * sigmoid(v) with e = e^-|v|: v / (1 + e), or v e / (1 + e) below zero (no
+// overflow on either side; beyond 128 e is 0 in any case).
+__device__ __forceinline__ float2 silu2(float2 v) {
+    const float2 e = exp_neg2(make_float2(fminf(fabsf(v.x), 128.0f), fminf(fabsf(v.y), 128.0f)));
+    const float2 d = __fadd2_rn(e, make_float2(1.0f, 1.0f));
+    const float2 r = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+    const float2 n = make_float2(v.x < 0.0f ? e.x : 1.0f, v.y < 0.0f ? e.y : 1.0f);
+    return __fmul2_rn(__fmul2_rn(v, n), r);
+}
+
+// v * Phi(v) through the tail P = Phi(-|v|) = e^(-v^2/2) g(|v|), which keeps its
+// relative accuracy: Phi = P below zero and 1 - P above.  g(a) = t Q(t) with
+// t = 1 / (1 + 0.35 a); Q, of degree 8, is a minimax fit of e^(a^2/2) Phi(-a) / t over
+// 0 <= a <= 14 (reweighted least squares in 64 bits; relative error 3.2e-8,
+// 3.4e-7 at most as evaluated in fp32).  Beyond 64 the tail is 0 in any case.
+__device__ __forceinline__ float2 gelu2(float2 v) {
+    const float2 a = make_float2(fminf(fabsf(v.x), 64.0f), fminf(fabsf(v.y), 64.0f));
+    const float2 d = __ffma2_rn(a, make_float2(0.35f, 0.35f), make_float2(1.0f, 1.0f));
+    const float2 t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+    constexpr float kQ[9] = {0.13962141f, 0.13986187f, 0.11983292f, 0.10550778f, -0.023109227f,
+                             0.15917318f, -0.25571328f, 0.14397119f, -0.029145816f};
+    float2 q = make_float2(kQ[8], kQ[8]);
+#pragma unroll
+    for (int i = 7; i >= 0; --i) q = __ffma2_rn(q, t, make_float2(kQ[i], kQ[i]));
+    const float2 e = exp_neg2(__fmul2_rn(__fmul2_rn(a, a), make_float2(0.5f, 0.5f)));
+    const float2 tail = __fmul2_rn(__fmul2_rn(q, t), e);
+    const float2 rest = __ffma2_rn(tail, make_float2(-1.0f, -1.0f), make_float2(1.0f, 1.0f));
+    return __fmul2_rn(v, make_float2(v.x < 0.0f ? tail.x : rest.x, v.y < 0.0f ? tail.y : rest.y));
+}
+
+template <int ACT>
+__device__ __forceinline__ float2 act2(float2 v) {
+    if (ACT == kActRelu) return make_float2(v.x < 0.0f ? 0.0f : v.x, v.y < 0.0f ? 0.0f : v.y);
+    if (ACT == kActSilu) return silu2(v);
+    if (ACT == kActGelu) return gelu2(v);
+    return v;
+}
+
 // Four int8 codes of quotients within +-127: adding 1.5 * 2^23 rounds each to the
 // nearest integer (ties to even) and leaves its two's complement in the low byte.
 __device__ __forceinline__ uint32_t int8x4(float a, float b, float c, float d) {
@@ -126,21 +188,22 @@ __device__ __forceinline__ uint32_t int8x4(float a, float b, float c, float d) {
 }
 
 // The thread's codes: the nearest to v / scale, the quotient by the corrected
-// reciprocal (quot_corrected's steps; int8 needs no sign of zero) or, for scales
-// it is not valid for, by division.
+// reciprocal (quot_corrected's steps, two at a time; the sign of a zero quotient,
+// which they may lose, is no matter here) or, for scales that is not valid for, by
+// division.
 template <int VEC, bool E4M3>
 __device__ __forceinline__ void store_codes(uint8_t* q, int n, int t, int threads, float (&v)[kHeld],
                                             float scale, bool blank, bool wide_q) {
     if (quot_corrected_ok(scale)) {
-        const float y = 1.0f / scale;
+        const float y1 = 1.0f / scale;
+        const float2 y = make_float2(y1, y1), ns = make_float2(-scale, -scale);
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            if (E4M3) {
-                v[i] = quot_corrected(v[i], scale, y);
-            } else {
-                const float q0 = __fmul_rn(v[i], y);
-                v[i] = __fmaf_rn(__fmaf_rn(-scale, q0, v[i]), y, q0);
-            }
+        for (int i = 0; i < kHeld; i += 2) {
+            const float2 x = make_float2(v[i], v[i + 1]);
+            const float2 q0 = __fmul2_rn(x, y);
+            const float2 q1 = __ffma2_rn(__ffma2_rn(ns, q0, x), y, q0);
+            v[i] = q1.x;
+            v[i + 1] = q1.y;
         }
     } else {
 #pragma unroll
