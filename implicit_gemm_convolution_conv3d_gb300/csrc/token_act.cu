@@ -14,7 +14,7 @@ namespace c3d {
 
 namespace {
 
-template <typename TX, int ACT, bool GATED, bool E4M3, int VEC>
+template <typename TX, int ACT, bool GATED, bool E4M3, bool PHASED>
 __global__ void __launch_bounds__(kMaxRowThreads)
     act_row_kernel(const ActParams p) {
     __shared__ uint32_t shu[32];
@@ -24,10 +24,11 @@ __global__ void __launch_bounds__(kMaxRowThreads)
     const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (row >= p.tokens) return;   // whole warps: a row's threads leave together
     const TX* x = static_cast<const TX*>(p.x) + row * p.x_stride;
+    const int lead = PHASED ? row_lead(x) : 0;
     float v[kHeld];
-    load_row<VEC>(x, n, t, threads, v);
+    load_row<PHASED>(x, n, lead, t, threads, v);
     float b[GATED ? kHeld : 1];
-    if constexpr (GATED) load_row<VEC>(x + n, n, t, threads, b);
+    if constexpr (GATED) load_row<PHASED>(x + n, n, lead, t, threads, b);
 #pragma unroll
     for (int i = 0; i < kHeld; i += 2) {
         const float2 y = act2<ACT>(make_float2(v[i], v[i + 1]));
@@ -38,18 +39,15 @@ __global__ void __launch_bounds__(kMaxRowThreads)
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) v[i] *= b[i];
     }
-    float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) m = max_abs_nan(m, v[i]);
-    const uint32_t top = row_max(__float_as_uint(m), threads >> 5, shu);
+    const uint32_t top = row_max(held_max(v), threads >> 5, shu);
     const float scale = row_scale(top, E4M3 ? 448.0f : 127.0f);
-    store_codes<VEC, E4M3>(p.q + row * p.q_stride, n, t, threads, v, scale, row_blank(top), p.wide_q);
+    store_codes<PHASED, E4M3>(p.q + row * p.q_stride, n, lead, t, threads, v, scale, row_blank(top));
     if (t == 0) p.scale[row] = scale;
 }
 
 // Rows that do not fit: read twice.
 template <typename TX, bool E4M3>
-__global__ void __launch_bounds__(kWideThreads)
+__global__ void __launch_bounds__(kMaxRowThreads)
     act_wide_kernel(const ActParams p) {
     __shared__ uint32_t shu[32];
     griddep_launch_dependents();
@@ -74,11 +72,11 @@ template <typename TX, int ACT, bool E4M3>
 cudaError_t act_launch(const ActParams& p, cudaStream_t stream) {
     const int xb = elt_bytes(p.x_dtype);
     const bool wide = p.width % 8 == 0 && aligned_rows(p.x, p.x_stride, p.tokens, xb, 16);
-    const dim3 block = row_block(p.width);
+    const dim3 block = row_block(p.width, !wide);
     const unsigned grid = row_blocks(p.tokens, block);
 #define C3D_ACT(G, V) launch_ex(act_row_kernel<TX, ACT, G, E4M3, V>, grid, block, 0, 1, stream, p)
-    if (p.gated) return wide ? C3D_ACT(true, 8) : C3D_ACT(true, 1);
-    return wide ? C3D_ACT(false, 8) : C3D_ACT(false, 1);
+    if (p.gated) return wide ? C3D_ACT(true, false) : C3D_ACT(true, true);
+    return wide ? C3D_ACT(false, false) : C3D_ACT(false, true);
 #undef C3D_ACT
 }
 
@@ -86,7 +84,7 @@ template <typename TX, bool E4M3>
 cudaError_t act_kind(const ActParams& p, cudaStream_t stream) {
     if (p.width > kMaxRowWidth)
         return launch_ex(act_wide_kernel<TX, E4M3>, static_cast<unsigned>(p.tokens),
-                         dim3(kWideThreads), 0, 1, stream, p);
+                         dim3(kMaxRowThreads), 0, 1, stream, p);
     if (p.act == kActRelu) return act_launch<TX, kActRelu, E4M3>(p, stream);
     if (p.act == kActSilu) return act_launch<TX, kActSilu, E4M3>(p, stream);
     if (p.act == kActGelu) return act_launch<TX, kActGelu, E4M3>(p, stream);

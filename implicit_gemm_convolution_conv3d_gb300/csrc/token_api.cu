@@ -108,7 +108,6 @@ int rms_norm_quant_fwd(const void* x, int x_dtype, int64_t x_stride, const void*
     p.res_dtype = residual ? res_dtype : x_dtype;
     p.weight_dtype = weight ? weight_dtype : x_dtype;
     p.q_dtype = q_dtype;
-    p.wide_q = aligned_to(q, 8) && (tokens == 1 || q_stride % 8 == 0);
     return launched(launch_norm_quant(p, stream), "rms_norm_quant_fwd launch");
 }
 
@@ -135,7 +134,6 @@ int act_quant_fwd(const void* x, int x_dtype, int64_t x_stride, int act, int gat
     p.width = width;
     p.x_dtype = x_dtype;
     p.q_dtype = q_dtype;
-    p.wide_q = aligned_to(q, 8) && (tokens == 1 || q_stride % 8 == 0);
     p.act = act;
     p.gated = gated != 0;
     return launched(launch_act_quant(p, stream), "act_quant_fwd launch");

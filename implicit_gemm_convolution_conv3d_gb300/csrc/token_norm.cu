@@ -16,7 +16,7 @@ namespace c3d {
 
 namespace {
 
-template <typename TX, typename TR, bool E4M3, int VEC>
+template <typename TX, typename TR, bool E4M3, bool PHASED>
 __global__ void __launch_bounds__(kMaxRowThreads)
     norm_row_kernel(const NormParams p) {
     __shared__ float shf[32];
@@ -27,15 +27,17 @@ __global__ void __launch_bounds__(kMaxRowThreads)
     const int warps = threads >> 5;
     const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (row >= p.tokens) return;   // whole warps: a row's threads leave together
+    const TX* x = static_cast<const TX*>(p.x) + row * p.x_stride;
+    const int lead = PHASED ? row_lead(x) : 0;
     float h[kHeld];
-    load_row<VEC>(static_cast<const TX*>(p.x) + row * p.x_stride, n, t, threads, h);
+    load_row<PHASED>(x, n, lead, t, threads, h);
     if (p.res) {
         float r[kHeld];
-        load_row<VEC>(static_cast<const TR*>(p.res) + row * p.res_stride, n, t, threads, r);
+        load_row<PHASED>(static_cast<const TR*>(p.res) + row * p.res_stride, n, lead, t, threads, r);
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) h[i] += r[i];
         if (p.res_out)
-            store_row<VEC>(static_cast<TR*>(p.res_out) + row * p.res_out_stride, n, t, threads, h);
+            store_row<PHASED>(static_cast<TR*>(p.res_out) + row * p.res_out_stride, n, lead, t, threads, h);
     }
     float ss = 0.0f;
 #pragma unroll
@@ -49,24 +51,21 @@ __global__ void __launch_bounds__(kMaxRowThreads)
     if (p.weight) {
         float w[kHeld];
         if (p.weight_dtype == kTokF32)
-            load_row<VEC>(static_cast<const float*>(p.weight), n, t, threads, w);
+            load_row<PHASED>(static_cast<const float*>(p.weight), n, lead, t, threads, w);
         else
-            load_row<VEC>(static_cast<const TX*>(p.weight), n, t, threads, w);
+            load_row<PHASED>(static_cast<const TX*>(p.weight), n, lead, t, threads, w);
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) h[i] *= w[i];
     }
-    float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) m = max_abs_nan(m, h[i]);
-    const uint32_t top = row_max(__float_as_uint(m), warps, shu);
+    const uint32_t top = row_max(held_max(h), warps, shu);
     const float scale = row_scale(top, E4M3 ? 448.0f : 127.0f);
-    store_codes<VEC, E4M3>(p.q + row * p.q_stride, n, t, threads, h, scale, row_blank(top), p.wide_q);
+    store_codes<PHASED, E4M3>(p.q + row * p.q_stride, n, lead, t, threads, h, scale, row_blank(top));
     if (t == 0) p.scale[row] = scale;
 }
 
 // Rows that do not fit: read again for each pass (mean square, maximum, codes).
 template <typename TX, typename TR, bool E4M3>
-__global__ void __launch_bounds__(kWideThreads)
+__global__ void __launch_bounds__(kMaxRowThreads)
     norm_wide_kernel(const NormParams p) {
     __shared__ float shf[32];
     __shared__ uint32_t shu[32];
@@ -108,16 +107,15 @@ template <typename TX, typename TR, bool E4M3>
 cudaError_t norm_launch(const NormParams& p, cudaStream_t stream) {
     if (p.width > kMaxRowWidth)
         return launch_ex(norm_wide_kernel<TX, TR, E4M3>, static_cast<unsigned>(p.tokens),
-                         dim3(kWideThreads), 0, 1, stream, p);
+                         dim3(kMaxRowThreads), 0, 1, stream, p);
     const int xb = elt_bytes(p.x_dtype), rb = elt_bytes(p.res_dtype);
     const bool wide = p.width % 8 == 0 && aligned_rows(p.x, p.x_stride, p.tokens, xb, 16) &&
                       aligned_rows(p.res, p.res_stride, p.tokens, rb, 16) &&
-                      aligned_rows(p.res_out, p.res_out_stride, p.tokens, rb, 16) &&
                       aligned_rows(p.weight, 0, 1, 1, 16);
-    const dim3 block = row_block(p.width);
+    const dim3 block = row_block(p.width, !wide);
     const unsigned grid = row_blocks(p.tokens, block);
-    return wide ? launch_ex(norm_row_kernel<TX, TR, E4M3, 8>, grid, block, 0, 1, stream, p)
-                : launch_ex(norm_row_kernel<TX, TR, E4M3, 1>, grid, block, 0, 1, stream, p);
+    return wide ? launch_ex(norm_row_kernel<TX, TR, E4M3, false>, grid, block, 0, 1, stream, p)
+                : launch_ex(norm_row_kernel<TX, TR, E4M3, true>, grid, block, 0, 1, stream, p);
 }
 
 template <typename TX>

@@ -23,7 +23,6 @@ struct NormParams {
     // mean is that sum * mean_of
     float shrink, mean_of;
     int x_dtype, res_dtype, weight_dtype, q_dtype;
-    bool wide_q;   // rows of q are 8-byte aligned
 };
 
 struct ActParams {
@@ -33,7 +32,6 @@ struct ActParams {
     long long x_stride, q_stride;
     long long tokens, width;
     int x_dtype, q_dtype, act, gated;
-    bool wide_q;   // rows of q are 8-byte aligned
 };
 
 struct LinearParams {

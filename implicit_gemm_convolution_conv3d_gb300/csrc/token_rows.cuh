@@ -1,14 +1,16 @@
 // token_rows.cuh -- what the row kernels (token_norm.cu, token_act.cu) share: a
 // row held in registers, its reductions, and its codes.
 //
-// A row of `n` elements is held by `threads` threads, kVec x 8 elements each
-// (as fp32): read once, and everything that needs the whole row (its mean
-// square, its largest value) is a reduction between registers.  Two layouts:
-//   VEC 8: thread t holds the 8-element pieces t, t + threads, ... (16-byte
-//          loads of 16-bit types; width, strides and bases in whole pieces)
-//   VEC 1: thread t holds the elements t, t + threads, ... (any alignment)
-// Rows of up to kMaxRowWidth elements go this way; a wider row is read again
-// for each pass.
+// A row of `n` elements is held by `threads` threads, kVec pieces of 8 elements each
+// (as fp32): read once, and everything that needs the whole row (its mean square,
+// its largest value) is a reduction between registers.  Thread t holds the pieces
+// t, t + threads, ...; a piece is one 16-byte access of a 16-bit matrix.  With
+// PHASED rows (any width, stride and base) the pieces start `lead` elements before
+// the row, where x's 16-byte blocks do: in a dense matrix of odd width every row of
+// every operand then has aligned blocks inside, and only the pieces at the row's
+// ends (and operands of another phase) go element by element.
+// 64 registers a thread, so that 1024 threads an SM keep their loads in flight: with
+// 80 (768 threads) the 216000 x 2048 norm took 549 us against 499.
 #pragma once
 #include "token_common.cuh"
 
@@ -16,9 +18,8 @@ namespace c3d {
 
 constexpr int kVec = 4;                      // pieces of 8 elements per thread
 constexpr int kHeld = 8 * kVec;
-constexpr int kMaxRowThreads = 512;         // 128 registers a thread
-constexpr int kWideThreads = 1024;
-constexpr long long kMaxRowWidth = static_cast<long long>(kHeld) * kMaxRowThreads;
+constexpr int kMaxRowThreads = 1024;
+constexpr long long kMaxRowWidth = static_cast<long long>(kHeld) * kMaxRowThreads - 8;
 constexpr int kWarpRows = 4;                 // rows of a block when one warp holds a row
 
 // 8 consecutive elements (16- or 32-byte aligned) as fp32
@@ -62,57 +63,72 @@ __device__ __forceinline__ void store8(__half* p, const float* v) {
     *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
 }
 
-// Index of the first element of piece j of thread t, and whether the piece (VEC 8)
-// or element e of it (VEC 1) lies in the row.
-template <int VEC>
-__device__ __forceinline__ int piece_at(int j, int t, int threads) {
-    return VEC == 8 ? (j * threads + t) * 8 : j * 8 * threads + t;
+// Elements of the row that a 16-byte block of x begins before it.
+template <typename TX>
+__device__ __forceinline__ int row_lead(const TX* x) {
+    return static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(TX));
+}
+
+// Whether pieces that start `lead` elements before p lie on boundaries of `bytes`.
+template <typename T>
+__device__ __forceinline__ bool in_phase(const T* p, int lead, unsigned bytes) {
+    return ((reinterpret_cast<uintptr_t>(p) - static_cast<uintptr_t>(lead) * sizeof(T)) & (bytes - 1u)) == 0;
 }
 
 // The thread's elements of a row; those outside it are zeros.
-template <int VEC, typename T>
-__device__ __forceinline__ void load_row(const T* p, int n, int t, int threads, float (&v)[kHeld]) {
+template <bool PHASED, typename T>
+__device__ __forceinline__ void load_row(const T* p, int n, int lead, int t, int threads,
+                                         float (&v)[kHeld]) {
+    const bool wide = !PHASED || in_phase(p, lead, 16u);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
-        const int i0 = piece_at<VEC>(j, t, threads);
-        if (VEC == 8) {
-            if (i0 < n) {
-                load8(p + i0, v + 8 * j);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[8 * j + e] = 0.0f;
-            }
+        const int i0 = (j * threads + t) * 8 - (PHASED ? lead : 0);
+        if (PHASED ? wide && i0 >= 0 && i0 + 8 <= n : i0 < n) {
+            load8(p + i0, v + 8 * j);
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int i = i0 + e * threads;
-                v[8 * j + e] = i < n ? to_f32(p[i]) : 0.0f;
-            }
+            for (int e = 0; e < 8; ++e)
+                v[8 * j + e] = PHASED && i0 + e >= 0 && i0 + e < n ? to_f32(p[i0 + e]) : 0.0f;
         }
     }
 }
 
-template <int VEC, typename T>
-__device__ __forceinline__ void store_row(T* p, int n, int t, int threads, const float (&v)[kHeld]) {
+template <bool PHASED, typename T>
+__device__ __forceinline__ void store_row(T* p, int n, int lead, int t, int threads,
+                                          const float (&v)[kHeld]) {
+    const bool wide = in_phase(p, PHASED ? lead : 0, 16u);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
-        const int i0 = piece_at<VEC>(j, t, threads);
-        if (VEC == 8) {
-            if (i0 < n) store8(p + i0, v + 8 * j);
+        const int i0 = (j * threads + t) * 8 - (PHASED ? lead : 0);
+        if (wide && (PHASED ? i0 >= 0 && i0 + 8 <= n : i0 < n)) {
+            store8(p + i0, v + 8 * j);
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int i = i0 + e * threads;
-                if (i < n) p[i] = from_f32<T>(v[8 * j + e]);
-            }
+            for (int e = 0; e < 8; ++e)
+                if (i0 + e >= 0 && i0 + e < n) p[i0 + e] = from_f32<T>(v[8 * j + e]);
         }
     }
 }
 
-// max(a, |b|), a NaN if either is one
-__device__ __forceinline__ float max_abs_nan(float a, float b) {
+// max(a, |b|, |c|), a NaN if any is one
+__device__ __forceinline__ float max_abs_nan(float a, float b, float c) {
     float r;
-    asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %2;\n\tmax.NaN.f32 %0, %1, t;\n\t}" : "=f"(r) : "f"(a), "f"(b));
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// The largest magnitude of the thread's elements, as bits that order like it.
+__device__ __forceinline__ uint32_t held_max(const float (&v)[kHeld]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kHeld; i += 2) m = max_abs_nan(m, v[i], v[i + 1]);
+    return __float_as_uint(m);
+}
+
+// max(v, 0) that keeps a NaN
+__device__ __forceinline__ float relu_nan(float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(v));
     return r;
 }
 
@@ -128,51 +144,51 @@ __device__ __forceinline__ float ex2_approx(float x) {   // 2 ulp; subnormal res
     return r;
 }
 
-// e^-y for y >= 0: 2^-t with t = y log2(e) rounded, times e^(t ln 2 - y), what the
-// rounding left over, as 1 + (t ln 2 - y); ln 2 in two parts (Cody and Waite,
+// e^m for m <= 0: 2^-t with t = -m log2(e) rounded, times e^(m + t ln 2), what the
+// rounding left over, as 1 + (m + t ln 2); ln 2 in two parts (Cody and Waite,
 // "Software Manual for the Elementary Functions", 1980).  Without it t's rounding
-// costs y * 2^-24 of relative error.
-__device__ __forceinline__ float2 exp_neg2(float2 y) {
-    const float2 t = __fmul2_rn(y, make_float2(1.44269504f, 1.44269504f));
-    float2 r = __ffma2_rn(t, make_float2(0.693147182f, 0.693147182f), make_float2(-y.x, -y.y));
+// costs |m| * 2^-24 of relative error.
+__device__ __forceinline__ float2 exp_neg2(float2 m) {
+    const float2 t = __fmul2_rn(m, make_float2(-1.44269504f, -1.44269504f));
+    float2 r = __ffma2_rn(t, make_float2(0.693147182f, 0.693147182f), m);
     r = __ffma2_rn(t, make_float2(-1.90465421e-9f, -1.90465421e-9f), r);
     const float2 e = make_float2(ex2_approx(-t.x), ex2_approx(-t.y));
     return __ffma2_rn(e, r, e);
 }
 
-// v * sigmoid(v) with e = e^-|v|: v / (1 + e), or v e / (1 + e) below zero (no
-// overflow on either side; beyond 128 e is 0 in any case).
+// Both activations are max(v, 0) - |v| T(|v|) with a tail T that falls to 0:
+//   v sigmoid(v):  T = e / (1 + e), e = e^-|v|
+//   v Phi(v):      T = Phi(-|v|) = e^(-v^2/2) g(|v|)
+// Below zero that is the tail alone, with its relative accuracy, and nothing
+// overflows on either side.  n = -|v|, cut where the tail is 0 in any case (128; 64).
 __device__ __forceinline__ float2 silu2(float2 v) {
-    const float2 e = exp_neg2(make_float2(fminf(fabsf(v.x), 128.0f), fminf(fabsf(v.y), 128.0f)));
+    const float2 n = make_float2(fmaxf(-fabsf(v.x), -128.0f), fmaxf(-fabsf(v.y), -128.0f));
+    const float2 e = exp_neg2(n);
     const float2 d = __fadd2_rn(e, make_float2(1.0f, 1.0f));
-    const float2 r = make_float2(rcp_approx(d.x), rcp_approx(d.y));
-    const float2 n = make_float2(v.x < 0.0f ? e.x : 1.0f, v.y < 0.0f ? e.y : 1.0f);
-    return __fmul2_rn(__fmul2_rn(v, n), r);
+    const float2 tail = __fmul2_rn(e, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+    return __ffma2_rn(n, tail, make_float2(relu_nan(v.x), relu_nan(v.y)));
 }
 
-// v * Phi(v) through the tail P = Phi(-|v|) = e^(-v^2/2) g(|v|), which keeps its
-// relative accuracy: Phi = P below zero and 1 - P above.  g(a) = t Q(t) with
-// t = 1 / (1 + 0.35 a); Q, of degree 8, is a minimax fit of e^(a^2/2) Phi(-a) / t over
-// 0 <= a <= 14 (reweighted least squares in 64 bits; relative error 3.2e-8,
-// 3.4e-7 at most as evaluated in fp32).  Beyond 64 the tail is 0 in any case.
+// g(a) = t Q(t), t = 1 / (1 + 0.35 a); Q, of degree 8, is a minimax fit of
+// e^(a^2/2) Phi(-a) / t over 0 <= a <= 14 (reweighted least squares in 64 bits;
+// relative error 3.2e-8, 3.4e-7 at most as evaluated in fp32).
 __device__ __forceinline__ float2 gelu2(float2 v) {
-    const float2 a = make_float2(fminf(fabsf(v.x), 64.0f), fminf(fabsf(v.y), 64.0f));
-    const float2 d = __ffma2_rn(a, make_float2(0.35f, 0.35f), make_float2(1.0f, 1.0f));
+    const float2 n = make_float2(fmaxf(-fabsf(v.x), -64.0f), fmaxf(-fabsf(v.y), -64.0f));
+    const float2 d = __ffma2_rn(n, make_float2(-0.35f, -0.35f), make_float2(1.0f, 1.0f));
     const float2 t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
     constexpr float kQ[9] = {0.13962141f, 0.13986187f, 0.11983292f, 0.10550778f, -0.023109227f,
                              0.15917318f, -0.25571328f, 0.14397119f, -0.029145816f};
     float2 q = make_float2(kQ[8], kQ[8]);
 #pragma unroll
     for (int i = 7; i >= 0; --i) q = __ffma2_rn(q, t, make_float2(kQ[i], kQ[i]));
-    const float2 e = exp_neg2(__fmul2_rn(__fmul2_rn(a, a), make_float2(0.5f, 0.5f)));
+    const float2 e = exp_neg2(__fmul2_rn(__fmul2_rn(n, n), make_float2(-0.5f, -0.5f)));
     const float2 tail = __fmul2_rn(__fmul2_rn(q, t), e);
-    const float2 rest = __ffma2_rn(tail, make_float2(-1.0f, -1.0f), make_float2(1.0f, 1.0f));
-    return __fmul2_rn(v, make_float2(v.x < 0.0f ? tail.x : rest.x, v.y < 0.0f ? tail.y : rest.y));
+    return __ffma2_rn(n, tail, make_float2(relu_nan(v.x), relu_nan(v.y)));
 }
 
 template <int ACT>
 __device__ __forceinline__ float2 act2(float2 v) {
-    if (ACT == kActRelu) return make_float2(v.x < 0.0f ? 0.0f : v.x, v.y < 0.0f ? 0.0f : v.y);
+    if (ACT == kActRelu) return make_float2(relu_nan(v.x), relu_nan(v.y));
     if (ACT == kActSilu) return silu2(v);
     if (ACT == kActGelu) return gelu2(v);
     return v;
@@ -191,9 +207,9 @@ __device__ __forceinline__ uint32_t int8x4(float a, float b, float c, float d) {
 // reciprocal (quot_corrected's steps, two at a time; the sign of a zero quotient,
 // which they may lose, is no matter here) or, for scales that is not valid for, by
 // division.
-template <int VEC, bool E4M3>
-__device__ __forceinline__ void store_codes(uint8_t* q, int n, int t, int threads, float (&v)[kHeld],
-                                            float scale, bool blank, bool wide_q) {
+template <bool PHASED, bool E4M3>
+__device__ __forceinline__ void store_codes(uint8_t* q, int n, int lead, int t, int threads,
+                                            float (&v)[kHeld], float scale, bool blank) {
     if (quot_corrected_ok(scale)) {
         const float y1 = 1.0f / scale;
         const float2 y = make_float2(y1, y1), ns = make_float2(-scale, -scale);
@@ -209,6 +225,7 @@ __device__ __forceinline__ void store_codes(uint8_t* q, int n, int t, int thread
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) v[i] = v[i] / scale;
     }
+    const bool wide = in_phase(q, PHASED ? lead : 0, 8u);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
         uint32_t w[2];
@@ -225,23 +242,13 @@ __device__ __forceinline__ void store_codes(uint8_t* q, int n, int t, int thread
                 w[h] = int8x4(c[0], c[1], c[2], c[3]);
             if (blank) w[h] = 0u;
         }
-        const int i0 = piece_at<VEC>(j, t, threads);
-        if (VEC == 8) {
-            if (i0 < n) {
-                if (wide_q) {
-                    *reinterpret_cast<uint2*>(q + i0) = make_uint2(w[0], w[1]);
-                } else {   // the inputs decide the layout, so that results do not depend on q
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        q[i0 + e] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
-                }
-            }
+        const int i0 = (j * threads + t) * 8 - (PHASED ? lead : 0);
+        if (wide && (PHASED ? i0 >= 0 && i0 + 8 <= n : i0 < n)) {
+            *reinterpret_cast<uint2*>(q + i0) = make_uint2(w[0], w[1]);
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int i = i0 + e * threads;
-                if (i < n) q[i] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
-            }
+            for (int e = 0; e < 8; ++e)
+                if (i0 + e >= 0 && i0 + e < n) q[i0 + e] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
         }
     }
 }
@@ -270,9 +277,10 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, int warps, uint32_t* sh)
     return __reduce_max_sync(0xffffffffu, lane < warps ? sh[lane] : 0u);
 }
 
-// The block of a row of n elements, and the grid for `tokens` rows.
-inline dim3 row_block(long long n) {
-    const int warps = static_cast<int>((n + 32 * kHeld - 1) / (32 * kHeld));
+// The block of a row of n elements (and a lead of up to 7 before it), and the grid
+// for `tokens` rows.
+inline dim3 row_block(long long n, bool phased) {
+    const int warps = static_cast<int>((n + (phased ? 7 : 0) + 32 * kHeld - 1) / (32 * kHeld));
     return warps <= 1 ? dim3(32, kWarpRows) : dim3(static_cast<unsigned>(32 * warps), 1);
 }
 inline unsigned row_blocks(long long tokens, const dim3& block) {
