@@ -71,8 +71,9 @@ __global__ void __launch_bounds__(kMaxRowThreads)
 template <typename TX, int ACT, bool E4M3>
 cudaError_t act_launch(const ActParams& p, cudaStream_t stream) {
     const int xb = elt_bytes(p.x_dtype);
-    const bool wide = p.width % 8 == 0 && aligned_rows(p.x, p.x_stride, p.tokens, xb, 16);
-    const dim3 block = row_block(p.width, !wide);
+    const bool inputs = p.width % 8 == 0 && aligned_rows(p.x, p.x_stride, p.tokens, xb, 16);
+    const bool wide = inputs && aligned_rows(p.q, p.q_stride, p.tokens, 1, 8);
+    const dim3 block = row_block(p.width, inputs);
     const unsigned grid = row_blocks(p.tokens, block);
 #define C3D_ACT(G, V) launch_ex(act_row_kernel<TX, ACT, G, E4M3, V>, grid, block, 0, 1, stream, p)
     if (p.gated) return wide ? C3D_ACT(true, false) : C3D_ACT(true, true);

@@ -109,10 +109,12 @@ cudaError_t norm_launch(const NormParams& p, cudaStream_t stream) {
         return launch_ex(norm_wide_kernel<TX, TR, E4M3>, static_cast<unsigned>(p.tokens),
                          dim3(kMaxRowThreads), 0, 1, stream, p);
     const int xb = elt_bytes(p.x_dtype), rb = elt_bytes(p.res_dtype);
-    const bool wide = p.width % 8 == 0 && aligned_rows(p.x, p.x_stride, p.tokens, xb, 16) &&
+    const bool inputs = p.width % 8 == 0 && aligned_rows(p.x, p.x_stride, p.tokens, xb, 16) &&
                       aligned_rows(p.res, p.res_stride, p.tokens, rb, 16) &&
                       aligned_rows(p.weight, 0, 1, 1, 16);
-    const dim3 block = row_block(p.width, !wide);
+    const bool wide = inputs && aligned_rows(p.res_out, p.res_out_stride, p.tokens, rb, 16) &&
+                      aligned_rows(p.q, p.q_stride, p.tokens, 1, 8);
+    const dim3 block = row_block(p.width, inputs);
     const unsigned grid = row_blocks(p.tokens, block);
     return wide ? launch_ex(norm_row_kernel<TX, TR, E4M3, false>, grid, block, 0, 1, stream, p)
                 : launch_ex(norm_row_kernel<TX, TR, E4M3, true>, grid, block, 0, 1, stream, p);

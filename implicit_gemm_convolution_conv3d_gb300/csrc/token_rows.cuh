@@ -96,13 +96,13 @@ __device__ __forceinline__ void load_row(const T* p, int n, int lead, int t, int
 template <bool PHASED, typename T>
 __device__ __forceinline__ void store_row(T* p, int n, int lead, int t, int threads,
                                           const float (&v)[kHeld]) {
-    const bool wide = in_phase(p, PHASED ? lead : 0, 16u);
+    const bool wide = !PHASED || in_phase(p, lead, 16u);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
         const int i0 = (j * threads + t) * 8 - (PHASED ? lead : 0);
-        if (wide && (PHASED ? i0 >= 0 && i0 + 8 <= n : i0 < n)) {
+        if (PHASED ? wide && i0 >= 0 && i0 + 8 <= n : i0 < n) {
             store8(p + i0, v + 8 * j);
-        } else {
+        } else if (PHASED) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (i0 + e >= 0 && i0 + e < n) p[i0 + e] = from_f32<T>(v[8 * j + e]);
@@ -225,7 +225,7 @@ __device__ __forceinline__ void store_codes(uint8_t* q, int n, int lead, int t, 
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) v[i] = v[i] / scale;
     }
-    const bool wide = in_phase(q, PHASED ? lead : 0, 8u);
+    const bool wide = !PHASED || in_phase(q, lead, 8u);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
         uint32_t w[2];
@@ -243,9 +243,9 @@ __device__ __forceinline__ void store_codes(uint8_t* q, int n, int lead, int t, 
             if (blank) w[h] = 0u;
         }
         const int i0 = (j * threads + t) * 8 - (PHASED ? lead : 0);
-        if (wide && (PHASED ? i0 >= 0 && i0 + 8 <= n : i0 < n)) {
+        if (PHASED ? wide && i0 >= 0 && i0 + 8 <= n : i0 < n) {
             *reinterpret_cast<uint2*>(q + i0) = make_uint2(w[0], w[1]);
-        } else {
+        } else if (PHASED) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (i0 + e >= 0 && i0 + e < n) q[i0 + e] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
@@ -277,10 +277,11 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, int warps, uint32_t* sh)
     return __reduce_max_sync(0xffffffffu, lane < warps ? sh[lane] : 0u);
 }
 
-// The block of a row of n elements (and a lead of up to 7 before it), and the grid
-// for `tokens` rows.
-inline dim3 row_block(long long n, bool phased) {
-    const int warps = static_cast<int>((n + (phased ? 7 : 0) + 32 * kHeld - 1) / (32 * kHeld));
+// The block of a row of n elements (with a lead of up to 7 before it unless the
+// inputs are aligned: the inputs alone decide which thread adds what, so that
+// results do not depend on the outputs' alignment), and the grid for `tokens` rows.
+inline dim3 row_block(long long n, bool inputs_aligned) {
+    const int warps = static_cast<int>((n + (inputs_aligned ? 0 : 7) + 32 * kHeld - 1) / (32 * kHeld));
     return warps <= 1 ? dim3(32, kWarpRows) : dim3(static_cast<unsigned>(32 * warps), 1);
 }
 inline unsigned row_blocks(long long tokens, const dim3& block) {
