@@ -25,10 +25,11 @@ __global__ void __launch_bounds__(kMaxRowThreads)
     if (row >= p.tokens) return;   // whole warps: a row's threads leave together
     const TX* x = static_cast<const TX*>(p.x) + row * p.x_stride;
     const int lead = PHASED ? row_lead(x) : 0;
+    const bool inner = row > 0 && row + 1 < p.tokens && n >= 8;   // neighbours of a block or more
     float v[kHeld];
-    load_row<PHASED>(x, n, lead, t, threads, v);
+    load_row<PHASED>(x, n, lead, inner, t, threads, v);
     float b[GATED ? kHeld : 1];
-    if constexpr (GATED) load_row<PHASED>(x + n, n, lead, t, threads, b);
+    if constexpr (GATED) load_row<PHASED>(x + n, n, lead, inner, t, threads, b);
 #pragma unroll
     for (int i = 0; i < kHeld; i += 2) {
         const float2 y = act2<ACT>(make_float2(v[i], v[i + 1]));

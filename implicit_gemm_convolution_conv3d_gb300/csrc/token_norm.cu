@@ -29,11 +29,12 @@ __global__ void __launch_bounds__(kMaxRowThreads)
     if (row >= p.tokens) return;   // whole warps: a row's threads leave together
     const TX* x = static_cast<const TX*>(p.x) + row * p.x_stride;
     const int lead = PHASED ? row_lead(x) : 0;
+    const bool inner = row > 0 && row + 1 < p.tokens && n >= 8;   // neighbours of a block or more
     float h[kHeld];
-    load_row<PHASED>(x, n, lead, t, threads, h);
+    load_row<PHASED>(x, n, lead, inner, t, threads, h);
     if (p.res) {
         float r[kHeld];
-        load_row<PHASED>(static_cast<const TR*>(p.res) + row * p.res_stride, n, lead, t, threads, r);
+        load_row<PHASED>(static_cast<const TR*>(p.res) + row * p.res_stride, n, lead, inner, t, threads, r);
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) h[i] += r[i];
         if (p.res_out)
@@ -51,9 +52,9 @@ __global__ void __launch_bounds__(kMaxRowThreads)
     if (p.weight) {
         float w[kHeld];
         if (p.weight_dtype == kTokF32)
-            load_row<PHASED>(static_cast<const float*>(p.weight), n, lead, t, threads, w);
+            load_row<PHASED>(static_cast<const float*>(p.weight), n, lead, false, t, threads, w);
         else
-            load_row<PHASED>(static_cast<const TX*>(p.weight), n, lead, t, threads, w);
+            load_row<PHASED>(static_cast<const TX*>(p.weight), n, lead, false, t, threads, w);
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) h[i] *= w[i];
     }

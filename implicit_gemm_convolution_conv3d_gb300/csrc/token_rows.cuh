@@ -63,6 +63,12 @@ __device__ __forceinline__ void store8(__half* p, const float* v) {
     *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
 }
 
+// Eight elements as one (fp32: two) 16-byte accesses.
+template <typename T>
+struct alignas(16) Block8 {
+    uint4 w[sizeof(T) / 2];
+};
+
 // Elements of the row that a 16-byte block of x begins before it.
 template <typename TX>
 __device__ __forceinline__ int row_lead(const TX* x) {
@@ -75,21 +81,57 @@ __device__ __forceinline__ bool in_phase(const T* p, int lead, unsigned bytes) {
     return ((reinterpret_cast<uintptr_t>(p) - static_cast<uintptr_t>(lead) * sizeof(T)) & (bytes - 1u)) == 0;
 }
 
-// The thread's elements of a row; those outside it are zeros.
+// The thread's elements of a row; those outside it are zeros.  inner: rows of the
+// same matrix lie before and behind this one, so that a block which it shares with
+// them may be read whole.
 template <bool PHASED, typename T>
-__device__ __forceinline__ void load_row(const T* p, int n, int lead, int t, int threads,
+__device__ __forceinline__ void load_row(const T* p, int n, int lead, bool inner, int t, int threads,
                                          float (&v)[kHeld]) {
-    const bool wide = !PHASED || in_phase(p, lead, 16u);
+    if (!PHASED) {
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-        const int i0 = (j * threads + t) * 8 - (PHASED ? lead : 0);
-        if (PHASED ? wide && i0 >= 0 && i0 + 8 <= n : i0 < n) {
-            load8(p + i0, v + 8 * j);
-        } else {
+        for (int j = 0; j < kVec; ++j) {
+            const int i0 = (j * threads + t) * 8;
+            if (i0 < n) {
+                load8(p + i0, v + 8 * j);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[8 * j + e] = PHASED && i0 + e >= 0 && i0 + e < n ? to_f32(p[i0 + e]) : 0.0f;
+                for (int e = 0; e < 8; ++e) v[8 * j + e] = 0.0f;
+            }
         }
+        return;
+    }
+    // loads first, without branches between them: a branch's block would wait for
+    // its own load before the next one is issued
+    if (in_phase(p, lead, 16u)) {
+        Block8<T> raw[kVec];
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            const int i0 = (j * threads + t) * 8 - lead;
+            raw[j] = Block8<T>{};
+            if (i0 < n && (inner || (i0 >= 0 && i0 + 8 <= n))) raw[j] = *reinterpret_cast<const Block8<T>*>(p + i0);
+        }
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            load8(reinterpret_cast<const T*>(&raw[j]), v + 8 * j);
+            const int i0 = (j * threads + t) * 8 - lead;
+            if (i0 < n && (i0 < 0 || i0 + 8 > n)) {   // the row's ends
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const bool in = i0 + e >= 0 && i0 + e < n;
+                    if (!in) v[8 * j + e] = 0.0f;
+                    else if (!inner) v[8 * j + e] = to_f32(p[i0 + e]);
+                }
+            }
+        }
+    } else {
+        T raw[kHeld];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int at = ((i >> 3) * threads + t) * 8 - lead + (i & 7);
+            raw[i] = at >= 0 && at < n ? p[at] : from_f32<T>(0.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) v[i] = to_f32(raw[i]);
     }
 }
 
