@@ -542,3 +542,22 @@ def test_refusals(pkg):
         pkg.linear_w8a8(c, c, out=torch.zeros(4, 5, device="cuda"))
     with pytest.raises(ValueError):
         pkg.linear_w8a8(c, c, act="swish")
+
+
+# ------------------------------------------------------------------ the example
+
+@pytest.mark.parametrize("dtype", ["int8", "e4m3"])
+@pytest.mark.parametrize("images", [1, 4])
+def test_patch_mlp_example(pkg, dtype, images):
+    """The patch embedding and two blocks in a graph: each block adds at most the
+    10% of test_block_follows_the_unquantised_one to a stream that keeps its
+    unquantised part."""
+    import importlib.util
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    spec = importlib.util.spec_from_file_location(
+        "patch_mlp_w8a8", os.path.join(root, "examples", "patch_mlp_w8a8.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    error, ms = mod.run(images=images, blocks=2, dtype=dtype, width=640, inner=1280)
+    assert error < 0.10 and ms > 0
