@@ -16,6 +16,8 @@ namespace c3d {
 
 namespace {
 
+constexpr float kMaxFinite = 3.4028235e38f;
+
 template <typename TX, typename TR, bool E4M3, bool PHASED>
 __global__ void __launch_bounds__(kMaxRowThreads)
     norm_row_kernel(const NormParams p) {
@@ -46,7 +48,8 @@ __global__ void __launch_bounds__(kMaxRowThreads)
         const float s = h[i] * p.shrink;
         ss = fmaf(s, s, ss);
     }
-    const float rms = 1.0f / sqrtf(row_sum(ss, warps, shf) * p.mean_of + p.eps);
+    ss = row_sum(ss, warps, shf);
+    const float rms = 1.0f / sqrtf(ss * p.mean_of + p.eps);
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) h[i] *= rms;
     if (p.weight) {
@@ -58,7 +61,8 @@ __global__ void __launch_bounds__(kMaxRowThreads)
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) h[i] *= w[i];
     }
-    const uint32_t top = row_max(held_max(h), warps, shu);
+    uint32_t top = row_max(held_max(h), warps, shu);
+    if (!(ss <= kMaxFinite)) top = 0x7FC00000u;   // the mean square is not finite
     const float scale = row_scale(top, E4M3 ? 448.0f : 127.0f);
     store_codes<PHASED, E4M3>(p.q + row * p.q_stride, n, lead, t, threads, h, scale, row_blank(top));
     if (t == 0) p.scale[row] = scale;
@@ -84,7 +88,8 @@ __global__ void __launch_bounds__(kMaxRowThreads)
         const float h = h_at(i) * p.shrink;
         ss = fmaf(h, h, ss);
     }
-    const float rms = 1.0f / sqrtf(row_sum(ss, warps, shf) * p.mean_of + p.eps);
+    ss = row_sum(ss, warps, shf);
+    const float rms = 1.0f / sqrtf(ss * p.mean_of + p.eps);
     auto v_of = [&](float h, int i) {
         const float w = !p.weight ? 1.0f
                         : p.weight_dtype == kTokF32 ? static_cast<const float*>(p.weight)[i]
@@ -93,7 +98,8 @@ __global__ void __launch_bounds__(kMaxRowThreads)
     };
     uint32_t m = 0;
     for (int i = threadIdx.x; i < n; i += blockDim.x) m = max(m, abs_bits(v_of(h_at(i), i)));
-    const uint32_t top = row_max(m, warps, shu);
+    uint32_t top = row_max(m, warps, shu);
+    if (!(ss <= kMaxFinite)) top = 0x7FC00000u;   // the mean square is not finite
     const float scale = row_scale(top, E4M3 ? 448.0f : 127.0f);
     // each element is read before this thread writes it: residual_out may be an input
     for (int i = threadIdx.x; i < n; i += blockDim.x) {

@@ -21,8 +21,9 @@
  *     rounded only where residual_out stores it (v is computed from the
  *     unrounded h).
  *   - A row of zeros gets scale 1 and codes 0.  A row whose v holds a NaN or
- *     an infinity gets scale NaN and codes 0, so that everything computed
- *     from it is NaN rather than a finite value that means nothing.
+ *     an infinity, or whose mean square is beyond fp32, gets scale NaN and
+ *     codes 0, so that everything computed from it is NaN rather than a finite
+ *     value that means nothing.
  *   - Zero tokens (and zero outputs of the product) are valid and launch
  *     nothing.  A width of zero is CONV_ERR_INVALID.
  */

@@ -147,6 +147,19 @@ def test_norm_not_finite_rows(pkg, width, q, what):
         assert torch.equal(codes[r].view(torch.uint8), clean[0][r].view(torch.uint8))
 
 
+@pytest.mark.parametrize("width", [640, 2048, 40000])
+def test_norm_mean_square_beyond_fp32(pkg, width):
+    """Finite rows whose mean square overflows are marked like rows that are not
+    finite; those whose sum of squares alone would are not."""
+    x = torch.full((3, width), 1e15, device="cuda")
+    x[1] = 3e19
+    x[2] = 1.5e19
+    codes, scale, _ = pkg.rms_norm_quant(x)
+    assert math.isnan(float(scale[1])) and not codes[1].any()
+    for r in (0, 2):
+        assert abs(float(scale[r]) * 127 - 1) < 1e-5 and (codes[r] == 127).all()
+
+
 @pytest.mark.parametrize("mag", [1e-30, 1e-20, 1e18])
 def test_norm_magnitudes(pkg, mag):
     """eps decides below, the squares stay within fp32 above."""
