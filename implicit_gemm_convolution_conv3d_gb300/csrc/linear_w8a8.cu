@@ -1069,40 +1069,35 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
     }
 }
 
-// Rows of any alignment copied to a 16-byte pitch, zeros behind each row: one
-// thread per 16-byte word.
-__global__ void __launch_bounds__(256) pad_rows_kernel(const uint8_t* src, long long stride,
-                                                       long long rows, long long cols, uint8_t* dst,
-                                                       long long pitch) {
-    griddep_launch_dependents();
-    griddep_wait();
-    const long long words = pitch >> 4, total = rows * words;
-    for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total;
-         i += static_cast<long long>(gridDim.x) * 256) {
-        const long long r = i / words, c = (i - r * words) << 4;
-        *reinterpret_cast<uint4*>(dst + r * pitch + c) = load_bytes(src + r * stride + c, cols - c);
+// Operands brought to rows that TMA can address, in one launch: bytes copied to a
+// 16-byte pitch, or int8 widened to f16; zeros behind each row.  One thread per 16
+// bytes read, as one word where the source's rows allow it.
+__device__ __forceinline__ void stage_job(const RowJob& j, unsigned block, unsigned blocks) {
+    const long long words = j.pitch >> 4, total = j.rows * words;
+    for (long long k = static_cast<long long>(block) * 256 + threadIdx.x; k < total;
+         k += static_cast<long long>(blocks) * 256) {
+        const long long r = j.small ? static_cast<long long>(fdiv(static_cast<uint32_t>(k), j.by_words)) : k / words;
+        const long long c = (k - r * words) << 4;
+        const uint8_t* src = j.src + r * j.stride + c;
+        const uint4 v = j.aligned && c + 16 <= j.cols ? __ldg(reinterpret_cast<const uint4*>(src))
+                                                      : load_bytes(src, j.cols - c);
+        if (j.widen) {
+            uint32_t o[8];
+            cvt_chunk(v, o);
+            uint4* d = reinterpret_cast<uint4*>(j.dst + 2 * (r * j.pitch + c));
+            d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        } else {
+            *reinterpret_cast<uint4*>(j.dst + r * j.pitch + c) = v;
+        }
     }
 }
 
-// int8 rows as f16 rows of `pitch` elements (a multiple of 16), zeros behind each
-// row: one thread per 16 codes, read as one word where rows are 16-byte aligned.
-__global__ void __launch_bounds__(256) widen_rows_kernel(const uint8_t* src, long long stride,
-                                                         long long rows, long long cols,
-                                                         uint8_t* dst, long long pitch, int aligned) {
+__global__ void __launch_bounds__(256) stage_rows_kernel(const __grid_constant__ RowJobs jobs) {
     griddep_launch_dependents();
     griddep_wait();
-    const long long words = pitch >> 4, total = rows * words;
-    for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total;
-         i += static_cast<long long>(gridDim.x) * 256) {
-        const long long r = i / words, c = (i - r * words) << 4;
-        const uint4 v = aligned && c + 16 <= cols ? *reinterpret_cast<const uint4*>(src + r * stride + c)
-                                                  : load_bytes(src + r * stride + c, cols - c);
-        uint32_t o[8];
-        cvt_chunk(v, o);
-        uint4* d = reinterpret_cast<uint4*>(dst + 2 * (r * pitch + c));
-        d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        d[1] = make_uint4(o[4], o[5], o[6], o[7]);
-    }
+    if (blockIdx.x < jobs.blocks0) stage_job(jobs.job[0], blockIdx.x, jobs.blocks0);
+    else stage_job(jobs.job[1], blockIdx.x - jobs.blocks0, gridDim.x - jobs.blocks0);
 }
 
 // Clusters of 2, 4 and 8 split-kernel CTAs (one per SM) that the current device
@@ -1301,19 +1296,18 @@ cudaError_t launch_linear(const LinearMaps& maps, const LinearParams& p, const L
                   : launch_split<false>(maps.w, maps.x, s, plan, stream);
 }
 
-cudaError_t launch_pad_rows(const uint8_t* src, long long stride, long long rows, long long cols,
-                            uint8_t* dst, long long pitch, cudaStream_t stream) {
-    const long long blocks = (rows * (pitch >> 4) + 255) / 256;
-    return launch_ex(pad_rows_kernel, static_cast<unsigned>(std::min(blocks, 152ll * 64)), 256, 0, 1,
-                     stream, src, stride, rows, cols, dst, pitch);
-}
-
-cudaError_t launch_widen_rows(const uint8_t* src, long long stride, long long rows, long long cols,
-                              uint8_t* dst, long long pitch, cudaStream_t stream) {
-    const long long blocks = (rows * (pitch >> 4) + 255) / 256;
-    const int aligned = (reinterpret_cast<uintptr_t>(src) & 15u) == 0 && stride % 16 == 0;
-    return launch_ex(widen_rows_kernel, static_cast<unsigned>(std::min(blocks, 152ll * 64)), 256, 0, 1,
-                     stream, src, stride, rows, cols, dst, pitch, aligned);
+cudaError_t launch_stage_rows(RowJobs jobs, cudaStream_t stream) {
+    unsigned blocks[2];
+    for (int i = 0; i < 2; ++i) {
+        RowJob& j = jobs.job[i];
+        const long long words = j.pitch >> 4, total = j.rows * words;
+        j.aligned = (reinterpret_cast<uintptr_t>(j.src) & 15u) == 0 && j.stride % 16 == 0;
+        j.small = total < (1ll << 31) ? 1 : 0;
+        j.by_words = make_fastdiv(static_cast<uint32_t>(words));
+        blocks[i] = static_cast<unsigned>(std::min((total + 255) / 256, 152ll * 32));
+    }
+    jobs.blocks0 = blocks[0];
+    return launch_ex(stage_rows_kernel, blocks[0] + blocks[1], 256, 0, 1, stream, jobs);
 }
 
 }  // namespace c3d

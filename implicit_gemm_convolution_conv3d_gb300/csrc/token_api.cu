@@ -228,11 +228,14 @@ int linear_w8a8_fwd(const void* x, int64_t x_stride, const void* w, int64_t w_st
                           (tokens == 1 ? outputs * elt + 15 & ~15ll : out_stride * elt), 32, 64)))
         return rc;
     cudaError_t e = cudaSuccess;
-    if (copy_x) e = launch_pad_rows(src_x, x_stride, tokens, width, const_cast<uint8_t*>(p.x), pitch, stream);
-    if (e == cudaSuccess && widen)
-        e = launch_widen_rows(src_w, w_stride, outputs, width, const_cast<uint8_t*>(p.w), pitch, stream);
-    if (e == cudaSuccess && copy_w)
-        e = launch_pad_rows(src_w, w_stride, outputs, width, const_cast<uint8_t*>(p.w), pitch, stream);
+    if (copy_x || copy_w || widen) {
+        RowJobs jobs{};
+        if (copy_x)
+            jobs.job[0] = RowJob{src_x, const_cast<uint8_t*>(p.x), x_stride, tokens, width, pitch, 0, 0, 0, {}};
+        if (copy_w || widen)
+            jobs.job[1] = RowJob{src_w, const_cast<uint8_t*>(p.w), w_stride, outputs, width, pitch, widen, 0, 0, {}};
+        e = launch_stage_rows(jobs, stream);
+    }
     if (e == cudaSuccess) e = launch_linear(maps, p, plan, stream);
     return launched(e, "linear_w8a8_fwd launch");
 }

@@ -6,6 +6,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "internal.h"
+
 namespace c3d {
 
 struct NormParams {
@@ -62,7 +64,7 @@ struct LinearPlan {
     size_t smem;
 };
 // whether the pair form runs this product; its int8 weights are then f16 rows in
-// the workspace (launch_widen_rows)
+// the workspace (launch_stage_rows)
 bool linear_pair_form(long long tokens, long long outputs, int e4m3);
 // whether the form for few tokens runs it: any alignment, no tensor maps
 bool linear_thin_form(long long tokens);
@@ -78,13 +80,21 @@ cudaError_t launch_act_quant(const ActParams& p, cudaStream_t stream);
 cudaError_t launch_linear(const LinearMaps& maps, const LinearParams& p, const LinearPlan& plan,
                           cudaStream_t stream);
 
-// dst rows of `pitch` bytes (a multiple of 16, 16-byte aligned) from rows of
-// `cols` bytes `stride` apart, zeros behind each row
-cudaError_t launch_pad_rows(const uint8_t* src, long long stride, long long rows, long long cols,
-                            uint8_t* dst, long long pitch, cudaStream_t stream);
-
-// f16 rows of `pitch` elements (a multiple of 16, 16-byte aligned) from int8 rows
-cudaError_t launch_widen_rows(const uint8_t* src, long long stride, long long rows, long long cols,
-                              uint8_t* dst, long long pitch, cudaStream_t stream);
+// Rows of `cols` bytes, `stride` apart, to rows of `pitch` elements (a multiple of
+// 16; dst 16-byte aligned) with zeros behind them: bytes, or f16 (widen, of int8).
+// rows 0: no job.
+struct RowJob {
+    const uint8_t* src;
+    uint8_t* dst;
+    long long stride, rows, cols, pitch;
+    int widen;
+    int aligned, small;   // the rest is filled at launch
+    FastDiv by_words;
+};
+struct RowJobs {
+    RowJob job[2];
+    unsigned blocks0;
+};
+cudaError_t launch_stage_rows(RowJobs jobs, cudaStream_t stream);
 
 }  // namespace c3d
