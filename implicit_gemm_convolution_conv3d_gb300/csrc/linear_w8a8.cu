@@ -84,6 +84,18 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
     return v;
 }
 
+__device__ __forceinline__ float ld_cluster_f1(uint32_t cluster_addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
 // Four int8 codes as four f16 values: with the sign bit flipped a byte is the
 // code + 128, and below the byte 0x64 it is the f16 number 1024 + 128 + code;
 // 1152 subtracts exactly.  Five instructions for four codes.
@@ -487,23 +499,25 @@ __global__ void __launch_bounds__(kSplitThreads<E4M3>, 1)
         // this rank's share of the tile's tokens, a row of 128 outputs per warp and turn
         const int t_lo = nt * rank / s.splits;
         const int t_hi = static_cast<int>(min(static_cast<long long>(nt * (rank + 1) / s.splits), p.tokens - m0));
-        const int n = n0 + 4 * lane;
+        // a lane's outputs: four neighbours where rows are aligned for one store of
+        // them, else every 32nd, so that a warp's stores lie side by side
+        const int elt = p.out_dtype == kTokF32 ? 4 : 2;
+        const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(p.out_stride * elt)) &
+                           (4 * elt - 1)) == 0;
+        const int first = wide ? 4 * lane : lane, pace = wide ? 1 : 32;
+        const int n = n0 + first;
         float sw[4], b[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const bool in = n + j < p.outputs;
-            sw[j] = in && p.scale_w ? __ldg(p.scale_w + n + j) : 1.0f;
-            b[j] = in && p.bias ? __ldg(p.bias + n + j) : 0.0f;
+            const bool in = n + j * pace < p.outputs;
+            sw[j] = in && p.scale_w ? __ldg(p.scale_w + n + j * pace) : 1.0f;
+            b[j] = in && p.bias ? __ldg(p.bias + n + j * pace) : 0.0f;
         }
-        const int elt = p.out_dtype == kTokF32 ? 4 : 2;
-        const bool wide = n + 3 < p.outputs &&
-                          ((reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(p.out_stride * elt)) &
-                           (4 * elt - 1)) == 0;
         auto finish = [&](float (&v)[4], int t, float sx) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] = epi_act(v[j] * sx * sw[j] + b[j], p.act, p.out_dtype);
             const long long at = (m0 + t) * p.out_stride + n;
-            if (wide) {
+            if (wide && n + 3 < p.outputs) {
                 if (elt == 4)
                     *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) =
                         make_float4(v[0], v[1], v[2], v[3]);
@@ -513,28 +527,47 @@ __global__ void __launch_bounds__(kSplitThreads<E4M3>, 1)
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (n + j < p.outputs) store_one(p.out, p.out_dtype, at + j, v[j]);
+                    if (n + j * pace < p.outputs) store_one(p.out, p.out_dtype, at + j * pace, v[j]);
             }
         };
+        // one token's row in this CTA's or a peer's partial tile
+        auto own = [&](uint32_t a) {
+            if (wide) return lds128(a);
+            return make_uint4(lds32(a), lds32(a + 128u), lds32(a + 256u), lds32(a + 384u));
+        };
+        auto peer = [&](uint32_t a) {
+            if (wide) return ld_cluster_f4(a);
+            return make_float4(ld_cluster_f1(a), ld_cluster_f1(a + 128u), ld_cluster_f1(a + 256u),
+                               ld_cluster_f1(a + 384u));
+        };
         if (s.splits > 1) {
-            // one token a turn: the ranks' partials at once (a peer's shared memory is
+            // the ranks' partials of a token or two at once (a peer's shared memory is
             // far away), then added in rank order
-            for (int t = t_lo + warp - 4; t < t_hi; t += kCvtWarps) {
-                const uint32_t a = ring + static_cast<uint32_t>(t * kRows + 4 * lane) * 4u;
-                const float sx = p.scale_x ? __ldg(p.scale_x + m0 + t) : 1.0f;
-                float4 f[kMaxSplits];
+            constexpr int kTurns = E4M3 ? 2 : 1;
+            for (int t0 = t_lo + warp - 4; t0 < t_hi; t0 += kTurns * kCvtWarps) {
+                float4 f[kTurns][kMaxSplits];
+                float sx[kTurns];
 #pragma unroll
-                for (int r = 0; r < kMaxSplits; ++r)
-                    f[r] = r < s.splits ? ld_cluster_f4(mapa_shared(a, r)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int u = 0; u < kTurns; ++u) {
+                    const int t = min(t0 + u * kCvtWarps, t_hi - 1);
+                    const uint32_t a = ring + static_cast<uint32_t>(t * kRows + first) * 4u;
+                    sx[u] = p.scale_x ? __ldg(p.scale_x + m0 + t) : 1.0f;
 #pragma unroll
-                for (int r = 0; r < kMaxSplits; ++r) {
-                    v[0] += f[r].x;
-                    v[1] += f[r].y;
-                    v[2] += f[r].z;
-                    v[3] += f[r].w;
+                    for (int r = 0; r < kMaxSplits; ++r)
+                        f[u][r] = r < s.splits ? peer(mapa_shared(a, r)) : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
-                finish(v, t, sx);
+#pragma unroll
+                for (int u = 0; u < kTurns; ++u) {
+                    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int r = 0; r < kMaxSplits; ++r) {
+                        v[0] += f[u][r].x;
+                        v[1] += f[u][r].y;
+                        v[2] += f[u][r].z;
+                        v[3] += f[u][r].w;
+                    }
+                    if (t0 + u * kCvtWarps < t_hi) finish(v, t0 + u * kCvtWarps, sx[u]);
+                }
             }
         } else {
             constexpr int kTurns = 4;   // tokens whose loads are in flight together
@@ -543,7 +576,7 @@ __global__ void __launch_bounds__(kSplitThreads<E4M3>, 1)
 #pragma unroll
                 for (int u = 0; u < kTurns; ++u) {
                     const int t = min(t0 + u * kCvtWarps, t_hi - 1);
-                    const uint4 w = lds128(ring + static_cast<uint32_t>(t * kRows + 4 * lane) * 4u);
+                    const uint4 w = own(ring + static_cast<uint32_t>(t * kRows + first) * 4u);
                     v[u][0] = __uint_as_float(w.x);
                     v[u][1] = __uint_as_float(w.y);
                     v[u][2] = __uint_as_float(w.z);

@@ -97,18 +97,27 @@ def _stream(stream: Optional[torch.cuda.Stream], x: torch.Tensor):
         else _raw_stream(x.device.index)
 
 
-def _codes_out(x, rows, width, qdtype, out, scale_out):
+def _new(shape, dtype, x: torch.Tensor, stream) -> torch.Tensor:
+    """A tensor from torch's allocator that the given stream may use: memory of the
+    current stream goes back to its pool only when that stream is done with it."""
+    t = torch.empty(shape, dtype=dtype, device=x.device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _codes_out(x, rows, width, qdtype, out, scale_out, stream):
     """The (given or new) code and scale tensors for rows of x: with the codes'
     row stride and type and the scales' pointer."""
     if out is None:
         code = _CODE.get(qdtype)
         if code is None:
             raise TypeError("qdtype must be torch.int8 or torch.float8_e4m3fn")
-        out, stride = torch.empty(x.shape[:-1] + (width,), dtype=qdtype, device=x.device), width
+        out, stride = _new(x.shape[:-1] + (width,), qdtype, x, stream), width
     else:
         stride, code = _given_rows(out, x.shape, width, rows, _CODE, "out")
     if scale_out is None:
-        scale_out = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        scale_out = _new(x.shape[:-1], torch.float32, x, stream)
         return out, scale_out, stride, code, scale_out.data_ptr()
     return out, scale_out, stride, code, _vector(scale_out, rows, "scale_out")
 
@@ -128,7 +137,7 @@ def rms_norm_quant(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: 
     stands in for ``qdtype``."""
     lib = _fns or _bind()
     rows, width, xs, xc = _rows(x, _FLOAT, "x")
-    out, scale_out, qs, qc, sp = _codes_out(x, rows, width, qdtype, out, scale_out)
+    out, scale_out, qs, qc, sp = _codes_out(x, rows, width, qdtype, out, scale_out, stream)
     wp = _vector(weight, width, "weight", x.dtype)
     wc = xc if weight is None or weight.dtype is x.dtype else CONV_DTYPE_F32
     rp = op = None
@@ -138,7 +147,7 @@ def rms_norm_quant(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: 
             raise ValueError("residual must have x's shape")
         _, _, rs, rc = _rows(residual, _FLOAT, "residual")
         if residual_out is None:
-            residual_out, os_ = torch.empty(x.shape, dtype=residual.dtype, device=x.device), width
+            residual_out, os_ = _new(x.shape, residual.dtype, x, stream), width
         elif residual_out is residual:
             os_ = rs
         else:
@@ -172,7 +181,7 @@ def act_quant(x: torch.Tensor, act: str = "none", gated: bool = False,
         if width % 2:
             raise ValueError("a gated x must have an even number of columns")
         width //= 2
-    out, scale_out, qs, qc, sp = _codes_out(x, rows, width, qdtype, out, scale_out)
+    out, scale_out, qs, qc, sp = _codes_out(x, rows, width, qdtype, out, scale_out, stream)
     st = lib.act_quant_fwd(x.data_ptr(), xc, xs, code, 1 if gated else 0, rows, width, qc,
                            out.data_ptr(), qs, sp, _stream(stream, x))
     if st:
@@ -222,7 +231,7 @@ def linear_w8a8(x: torch.Tensor, w: torch.Tensor, scale_x: Optional[torch.Tensor
         oc = _FLOAT.get(out_dtype)
         if oc is None:
             raise TypeError("out_dtype must be bfloat16, float16 or float32")
-        out, os_ = torch.empty(x.shape[:-1] + (outputs,), dtype=out_dtype, device=x.device), outputs
+        out, os_ = _new(x.shape[:-1] + (outputs,), out_dtype, x, stream), outputs
     else:
         os_, oc = _given_rows(out, x.shape, outputs, rows, _FLOAT, "out")
     xp, wp = x.data_ptr(), w.data_ptr()
@@ -234,7 +243,7 @@ def linear_w8a8(x: torch.Tensor, w: torch.Tensor, scale_x: Optional[torch.Tensor
     else:
         need = _linear_need(lib, xp, xs, wp, ws, qc, rows, outputs, width)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            workspace = _new((need,), torch.uint8, x, stream)
             ws_ptr, ws_bytes = workspace.data_ptr(), need
     st = lib.linear_w8a8_fwd(xp, xs, wp, ws, qc, rows, outputs, width,
                              _vector(scale_x, rows, "scale_x"),

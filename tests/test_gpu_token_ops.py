@@ -467,6 +467,26 @@ def test_block_follows_the_unquantised_one(pkg, tokens, q):
     assert float((y.double() - want).norm() / want.norm()) < 0.10
 
 
+@pytest.mark.parametrize("q", [I8, E4])
+def test_given_stream_owns_what_it_allocates(pkg, q):
+    """Calls on a given stream whose tensors come from the current stream's pool:
+    what is dropped between the calls (workspaces, codes) is not handed to the
+    current stream's work while the given stream still reads it."""
+    g = _gen(21)
+    side = torch.cuda.Stream()
+    x, w = _codes(g, 1030, 2051, q), _codes(g, 1500, 2051, q)   # staged operands
+    want = pkg.linear_w8a8(x, w)
+    torch.cuda.synchronize()
+    got = []
+    for i in range(6):
+        got.append(pkg.linear_w8a8(x, w, stream=side))
+        junk = torch.full((8 << 20,), 255, dtype=torch.uint8, device="cuda")   # the pool's next user
+        del junk
+    side.synchronize()
+    for y in got:
+        assert torch.equal(y, want)
+
+
 @pytest.mark.parametrize("tokens", [1, 37, 700])
 def test_block_on_another_stream_and_in_a_graph(pkg, tokens):
     """Everything runs on the stream it is given, and a captured block replayed
