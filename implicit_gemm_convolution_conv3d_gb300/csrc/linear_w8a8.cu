@@ -300,6 +300,10 @@ __global__ void __launch_bounds__(32 * kThinMaxWarps)
 // The converters of either operand are two groups of four warps on alternate
 // k-steps: a group's step is 600 to 1600 cycles of latency (wait, read, convert,
 // write, fence) that the other's hides.
+// What bounds it: latency (launch, first loads, the partials' way between CTAs, about
+// 4 us in all) and, for int8, the token converters (about 1450 cycles a k-step at
+// 128 tokens): 128 x 8192 x 2048 e4m3 9 us, int8 12 us, where the weights' bytes
+// take 2.5.
 struct SplitParams {
     LinearParams p;
     int tok_tile, out_tiles;
@@ -474,7 +478,8 @@ __global__ void __launch_bounds__(kSplitThreads<E4M3>, 1)
         }
         // the accumulator as [token][output] fp32 over the ring, which every
         // load and MMA has left by now
-        if (warp < 12 && ok && wait_bar(acc_bar, 0, abort_flag, p.status, p.wait_ns)) {
+        if (warp < 12 && ok &&
+            __all_sync(0xffffffffu, wait_bar(acc_bar, 0, abort_flag, p.status, p.wait_ns))) {
             tc_fence_after();
             const int q = warp & 3, half = warp >= 8;
             const int valid = static_cast<int>(min(static_cast<long long>(nt), p.tokens - m0));
@@ -624,11 +629,18 @@ __global__ void __launch_bounds__(kSplitThreads<E4M3>, 1)
 //   warps 12-19  int8: tokens to f16 into TMEM, two groups on alternate k-steps
 // int8: the tokens cross shared memory once as bytes (their f16 form goes to
 // TMEM); the weights come as f16 from the workspace, where one short launch has
-// put them.  What decides this is shared memory, 128 bytes a cycle: per k-step (1024 cycles of
-// MMA) it moves 16 KB of raw tokens in and out, 32 KB of weights in and 32 KB
-// of the MMA's reads, 96 bytes a cycle.  Converting the weights here too
-// takes 128 (raw in and out, f16 in and out), and measured 1475 TFLOP/s at
+// put them.  What decides this is shared memory, 128 bytes a cycle: per k-step
+// (1024 cycles of MMA) it moves 16 KB of raw tokens in and out, 32 KB of weights
+// in and 32 KB of the MMA's reads, 96 bytes a cycle.  Converting the weights here
+// too takes 128 (raw in and out, f16 in and out), and measured 1475 TFLOP/s at
 // 16384 x 8192 x 8192 against 1907; the launch moves 3 bytes per weight.
+// What bounds it now: the tensor pipe under the power cap at long reductions (1057
+// cycles a k-step of 1024; e4m3 3730 TFLOP/s), and between tiles the hand-over
+// of the accumulator (int8, about 2000 cycles a tile).  e4m3's k-steps fill the
+// shared memory's 128 bytes a cycle by themselves, so that at 1024-long reductions
+// the epilogue's staging and scales are what is added (2650 TFLOP/s at 16384 x
+// 8192 x 1024).  Measured and not kept: outputs stored from the registers, a sector
+// per lane (0.88x there), tiles of 128 outputs (a k-step costs the same).
 //
 // Rings: the tokens' raw slots are free once converted, so that their loads run
 // ahead of the MMAs by both rings (4 raw slots, 4 in TMEM); one ring for both
