@@ -180,20 +180,21 @@ __device__ __forceinline__ float relu_nan(float v) {
 // more than memory does, where erfcf alone takes more.  Two of them are
 // special-function operations (2^x and 1/x, a quarter of the rate).
 
-__device__ __forceinline__ float ex2_approx(float x) {   // 2 ulp; subnormal results kept
+// 2^x within 2 ulp; results below 2^-126 are 0 (keeping them takes three more
+// instructions, and the tails are far below their row's scale there).
+__device__ __forceinline__ float ex2_approx(float x) {
     float r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
 // e^m for m <= 0: 2^-t with t = -m log2(e) rounded, times e^(m + t ln 2), what the
-// rounding left over, as 1 + (m + t ln 2); ln 2 in two parts (Cody and Waite,
-// "Software Manual for the Elementary Functions", 1980).  Without it t's rounding
-// costs |m| * 2^-24 of relative error.
+// rounding left over, as 1 + (m + t ln 2) (the argument's correction of Cody and
+// Waite, "Software Manual for the Elementary Functions", 1980, with ln 2 as one
+// fp32 number: 3e-9 |m| off).  Without it t's rounding costs |m| * 2^-24.
 __device__ __forceinline__ float2 exp_neg2(float2 m) {
     const float2 t = __fmul2_rn(m, make_float2(-1.44269504f, -1.44269504f));
-    float2 r = __ffma2_rn(t, make_float2(0.693147182f, 0.693147182f), m);
-    r = __ffma2_rn(t, make_float2(-1.90465421e-9f, -1.90465421e-9f), r);
+    const float2 r = __ffma2_rn(t, make_float2(0.693147182f, 0.693147182f), m);
     const float2 e = make_float2(ex2_approx(-t.x), ex2_approx(-t.y));
     return __ffma2_rn(e, r, e);
 }
