@@ -118,21 +118,29 @@ __device__ __forceinline__ void cvt_chunk(const uint4& v, uint32_t* o) {
 }
 
 // A k-step of `rows` int8 rows (a multiple of 16; 128 bytes each, swizzled) as two
-// boxes of f16 rows (64 elements each, swizzled), by `threads` threads.  Eight
+// boxes of f16 rows (64 elements each, swizzled), by the 128 threads `t`.  Eight
 // threads that share a shared-memory cycle take four neighbouring chunks of row
 // r and of row r^5: bit 2 keeps their reads, bit 0 their writes off each other's
-// banks.
-__device__ __forceinline__ void cvt_rows(uint32_t src, uint32_t dst, int rows, int t,
-                                         int threads) {
-    const int c4 = t & 3, flip = (t & 4) ? 5 : 0;
-#pragma unroll 4
-    for (int u = t >> 3; u < rows; u += threads >> 3) {
-        const int h = 2 * u >= rows, r = (2 * u - (h ? rows : 0)) ^ flip;
-        uint32_t v[8];
-        cvt_chunk(lds128(src + swz(r, 4 * h + c4)), v);
-        const uint32_t box = dst + static_cast<uint32_t>(h * rows) * 128u;
-        sts128(box + swz(r, 2 * c4), v[0], v[1], v[2], v[3]);
-        sts128(box + swz(r, 2 * c4 + 1), v[4], v[5], v[6], v[7]);
+// banks.  A thread's rows are 32 apart, which the swizzle does not see.
+__device__ __forceinline__ void cvt_rows(uint32_t src, uint32_t dst, int rows, int t) {
+    const int c4 = t & 3, r0 = (2 * (t >> 3)) ^ ((t & 4) ? 5 : 0);
+    const int n = (rows - r0 + 31) >> 5;   // this thread's rows
+    const uint32_t d0 = dst + swz(r0, 2 * c4), d1 = dst + swz(r0, 2 * c4 + 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t s0 = src + swz(r0, 4 * h + c4), box = static_cast<uint32_t>(h * rows) * 128u;
+        uint4 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)   // at most 128 rows
+            if (i < n) w[i] = lds128(s0 + 4096u * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i >= n) break;
+            uint32_t v[8];
+            cvt_chunk(w[i], v);
+            sts128(d0 + box + 4096u * i, v[0], v[1], v[2], v[3]);
+            sts128(d1 + box + 4096u * i, v[4], v[5], v[6], v[7]);
+        }
     }
 }
 
@@ -456,7 +464,7 @@ __global__ void __launch_bounds__(kSplitThreads<E4M3>, 1)
                     tmem_st_wait();
                     tc_fence_before();
                 } else {
-                    cvt_rows(src + kRows * kStep, cvt0 + c * s.cvt_bytes, nt, threadIdx.x & 127, 128);
+                    cvt_rows(src + kRows * kStep, cvt0 + c * s.cvt_bytes, nt, threadIdx.x & 127);
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
