@@ -145,11 +145,15 @@ __device__ __forceinline__ void cvt_rows(uint32_t src, uint32_t dst, int rows, i
 }
 
 // Epilogue activation: the convolutions' forms for 16-bit outputs, the
-// fp32-accurate ones for fp32 outputs; both keep a NaN.
-__device__ __forceinline__ float epi_act(float v, int act, int out_dtype) {
-    if (act == kActNone) return v;
+// fp32-accurate ones for fp32 outputs; both keep a NaN.  Out of line: the code
+// behind a mainloop runs once and cold, and the fp32 forms are long.
+__device__ __noinline__ float epi_act_call(float v, int act, int out_dtype) {
     if (act == kActRelu || out_dtype == kTokF32) return activate_f32(v, act);
     return activate(v, act);
+}
+
+__device__ __forceinline__ float epi_act(float v, int act, int out_dtype) {
+    return act == kActNone ? v : epi_act_call(v, act, out_dtype);
 }
 
 __device__ __forceinline__ void store_one(void* out, int dtype, long long at, float v) {
