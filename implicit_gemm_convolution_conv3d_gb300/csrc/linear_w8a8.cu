@@ -313,9 +313,9 @@ __global__ void __launch_bounds__(32 * kThinMaxWarps)
 // k-steps: a group's step is 600 to 1600 cycles of latency (wait, read, convert,
 // write, fence) that the other's hides.
 // What bounds it: latency (launch, first loads, the partials' way between CTAs, about
-// 4 us in all) and, for int8, the token converters (about 1450 cycles a k-step at
-// 128 tokens): 128 x 8192 x 2048 e4m3 9 us, int8 12 us, where the weights' bytes
-// take 2.5.
+// 4 us in all) and, for int8, the token converters (about 1200 cycles a k-step at
+// 128 tokens): 128 x 8192 x 2048 e4m3 8.4 us, int8 11.3 us, where the weights'
+// bytes take 2.5.
 struct SplitParams {
     LinearParams p;
     int tok_tile, out_tiles;
