@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "token_common.cuh"
+#include "token_ops.h"
 #include "token_ops_internal.h"
 
 namespace c3d {
@@ -202,7 +203,8 @@ __device__ __forceinline__ uint4 load_bytes(const uint8_t* src, long long left) 
 // tensor memory, a cluster's reduction) took 8.1 us for one token through
 // 8192 x 2048 int8 against 5.0 here; its 128-row operand would be 1/16 full.
 // Rows of any alignment: the unaligned ones are put together from aligned words.
-constexpr int kThinRows = 16, kThinTok = 16, kThinMaxWarps = 16;
+constexpr int kThinRows = 16, kThinTok = LINEAR_W8A8_NO_WORKSPACE_TOKENS, kThinMaxWarps = 16;
+static_assert(kThinTok == 16, "two blocks of eight tokens");
 
 template <bool E4M3>
 __device__ __forceinline__ void thin_cvt(const uint4& v, uint32_t (&o)[8]) {

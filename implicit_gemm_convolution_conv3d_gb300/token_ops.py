@@ -23,6 +23,8 @@ from . import _raw_current_stream as _raw_stream
 CONV_DTYPE_INT8, CONV_DTYPE_F16, CONV_DTYPE_F32 = 2, 3, 4
 _FLOAT = {torch.bfloat16: 0, torch.float16: CONV_DTYPE_F16, torch.float32: CONV_DTYPE_F32}
 _CODE = {torch.float8_e4m3fn: 1, torch.int8: CONV_DTYPE_INT8}
+_F32 = torch.float32
+NO_WORKSPACE_TOKENS = 16   # LINEAR_W8A8_NO_WORKSPACE_TOKENS of the header
 
 _fns = None
 
@@ -71,12 +73,13 @@ def _rows(t: torch.Tensor, types: dict, what: str) -> Tuple[int, int, int, int]:
         raise ValueError(f"{what} must be viewable as rows") from None
 
 
-def _vector(t: Optional[torch.Tensor], n: int, what: str, other=torch.float32) -> Optional[int]:
+def _vector(t: Optional[torch.Tensor], n: int, what: str, other=_F32) -> Optional[int]:
     """Data pointer of a contiguous CUDA vector of n elements, fp32 (or `other`)."""
     if t is None:
         return None
-    if t.dtype is not torch.float32 and t.dtype is not other:
-        raise TypeError(f"{what} must be float32" + ("" if other is torch.float32 else f" or {other}"))
+    dtype = t.dtype
+    if dtype is not _F32 and dtype is not other:
+        raise TypeError(f"{what} must be float32" + ("" if other is _F32 else f" or {other}"))
     if t.numel() != n or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous CUDA tensor of {n} elements")
     return t.data_ptr()
@@ -86,8 +89,8 @@ def _given_rows(t: torch.Tensor, shape, width: int, rows: int, types: dict,
                 what: str) -> Tuple[int, int]:
     """(row stride, type code) of a given output for tokens of `shape`, `width` wide."""
     out_rows, out_width, stride, code = _rows(t, types, what)
-    if out_width != width or out_rows != rows or len(t.shape) != len(shape) or (
-            len(shape) > 2 and t.shape[:-1] != shape[:-1]):
+    if out_width != width or out_rows != rows or (
+            len(shape) != 2 and t.shape[:-1] != shape[:-1]) or t.dim() != len(shape):
         raise ValueError(f"{what} must have shape {tuple(shape[:-1]) + (width,)}")
     return stride, code
 
@@ -240,7 +243,7 @@ def linear_w8a8(x: torch.Tensor, w: torch.Tensor, scale_x: Optional[torch.Tensor
         if not workspace.is_cuda or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor")
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    else:
+    elif rows > NO_WORKSPACE_TOKENS:
         need = _linear_need(lib, xp, xs, wp, ws, qc, rows, outputs, width)
         if need:
             workspace = _new((need,), torch.uint8, x, stream)

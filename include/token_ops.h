@@ -79,6 +79,9 @@ int linear_w8a8_fwd(const void* x, int64_t x_stride, const void* w, int64_t w_st
                     int64_t out_stride, void* workspace, size_t workspace_bytes,
                     cudaStream_t stream);
 
+/* Up to this many tokens linear_w8a8_fwd needs no workspace. */
+#define LINEAR_W8A8_NO_WORKSPACE_TOKENS 16
+
 /* Bytes of workspace linear_w8a8_fwd needs for these operands: an f16 copy of
  * int8 weights when there are many tokens, and copies at a 16-byte pitch of
  * rows that are not 16-byte aligned (base and stride).  Host-only. */

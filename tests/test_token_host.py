@@ -92,6 +92,18 @@ def test_linear_refuses(lib, kw):
     assert _linear(lib, **kw) == INVALID
 
 
+def test_few_tokens_need_no_workspace(lib):
+    """The binding's constant is the header's, and what the library answers."""
+    from implicit_gemm_convolution_conv3d_gb300 import token_ops
+    n = token_ops.NO_WORKSPACE_TOKENS
+    assert f"#define LINEAR_W8A8_NO_WORKSPACE_TOKENS {n}" in open(HEADER).read()
+    for dtype in (INT8, E4M3):
+        for off in (0, 1):
+            size = lambda t: lib.linear_w8a8_workspace_size(P + off, 65, P + off, 65, dtype, t, 8, 65)   # noqa: E731
+            assert all(size(t) == 0 for t in (1, 2, n))
+            assert size(n + 1) == 80 * (n + 1 + 8)
+
+
 def test_cpu_tensors_are_refused():
     import implicit_gemm_convolution_conv3d_gb300 as p
     x = torch.zeros(2, 32, dtype=torch.bfloat16)
