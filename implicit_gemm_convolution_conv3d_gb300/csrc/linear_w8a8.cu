@@ -709,6 +709,16 @@ __device__ __forceinline__ void scale2(uint32_t& v0, uint32_t& v1, float sx, uin
         : "r"(__float_as_uint(sx)), "r"(f0), "r"(f1), "r"(b0), "r"(b1));
 }
 
+// The same without a bias.
+__device__ __forceinline__ void mul2(uint32_t& v0, uint32_t& v1, float sx, uint32_t f0, uint32_t f1) {
+    asm("{\n\t.reg .b64 v, s, f;\n\t"
+        "mov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 f, {%3, %4};\n\t"
+        "mul.rn.f32x2 v, v, s;\n\tmul.rn.f32x2 v, v, f;\n\t"
+        "mov.b64 {%0, %1}, v;\n\t}"
+        : "+r"(v0), "+r"(v1)
+        : "r"(__float_as_uint(sx)), "r"(f0), "r"(f1));
+}
+
 // The activation of a chunk in registers, in the forms for 16-bit outputs.
 __device__ __forceinline__ void act_chunk(uint32_t (&v)[32], int act) {
     auto each = [&](auto f) {
@@ -1010,13 +1020,22 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
                 uint32_t buf = free_buffer();
                 // the chunk's 32 scales and 32 biases, through the buffer as broadcasts
                 sts32(buf + 4u * lane, __float_as_uint(csw[j]));
-                sts32(buf + 128u + 4u * lane, __float_as_uint(cbi[j]));
+                if (p.bias) sts32(buf + 128u + 4u * lane, __float_as_uint(cbi[j]));
                 __syncwarp();
+                if (p.bias) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint4 f = lds128(buf + 16u * i), b = lds128(buf + 128u + 16u * i);
-                    scale2(y[4 * i], y[4 * i + 1], sx, f.x, f.y, b.x, b.y);
-                    scale2(y[4 * i + 2], y[4 * i + 3], sx, f.z, f.w, b.z, b.w);
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 f = lds128(buf + 16u * i), b = lds128(buf + 128u + 16u * i);
+                        scale2(y[4 * i], y[4 * i + 1], sx, f.x, f.y, b.x, b.y);
+                        scale2(y[4 * i + 2], y[4 * i + 3], sx, f.z, f.w, b.z, b.w);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 f = lds128(buf + 16u * i);
+                        mul2(y[4 * i], y[4 * i + 1], sx, f.x, f.y);
+                        mul2(y[4 * i + 2], y[4 * i + 3], sx, f.z, f.w);
+                    }
                 }
                 __syncwarp();
                 const int c0 = col0 + 32 * j;

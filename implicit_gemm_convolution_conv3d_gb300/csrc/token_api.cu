@@ -212,8 +212,10 @@ int linear_w8a8_fwd(const void* x, int64_t x_stride, const void* w, int64_t w_st
     p.w_stride = copy_w || widen || outputs == 1 ? pitch : w_stride;
     LinearPlan plan;
     if ((rc = launched(plan_linear(p, lim.num_sms, &plan), "linear_w8a8_fwd plan"))) return rc;
-    if (static_cast<long long>(plan.out_tiles) * plan.tok_tiles * plan.splits > kMaxDim) {
-        set_last_error("the output has more than 2^31 tiles");
+    const long long tiles = static_cast<long long>(plan.out_tiles) * plan.tok_tiles * plan.splits;
+    const long long pairs = plan.pair ? plan.grid / 2 : 1;   // each counts its k-steps in 32 bits
+    if (tiles > kMaxDim || (plan.pair && (tiles / pairs + 1) * ((width + 127) / 128) > kMaxDim)) {
+        set_last_error("the output has more tiles than the kernels count");
         return CONV_ERR_UNSUPPORTED;
     }
     const long long elt = size_of(out_dtype);
