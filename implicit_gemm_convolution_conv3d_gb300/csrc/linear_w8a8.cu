@@ -670,7 +670,6 @@ struct PairParams {
     int m_tiles, n_tiles, group_m;
     int k_steps;
     int nacc;                 // accumulators in TMEM
-    int tma_out;              // output rows that TMA can address
     FastDiv f_group, f_gm;
 };
 
@@ -750,7 +749,9 @@ __device__ __forceinline__ int pair_cols(int nt, const PairParams& s) {
     return rest >= s.bn ? s.bn : static_cast<int>((rest + 31) & ~31ll);
 }
 
-template <bool E4M3>
+// TMA_OUT: TMA can address the output's rows; else they are stored element by
+// element, by an instance of its own (that code's registers cost the other 2%).
+template <bool E4M3, bool TMA_OUT>
 __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap x_map,
                        const __grid_constant__ CUtensorMap w_map,
@@ -795,7 +796,7 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
         fence_mbar_init();
         prefetch_tmap(&x_map);
         prefetch_tmap(&w_map);
-        if (s.tma_out) prefetch_tmap(&o_map);
+        if (TMA_OUT) prefetch_tmap(&o_map);
     }
     if (warp == 1) {
         tmem_alloc_pair(smem_u32(misc), 512);
@@ -976,12 +977,12 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
             // columns [c0, c0 + width) to the output.
             auto free_buffer = [&]() {
                 const uint32_t buf = buf0 + (E4M3 ? 0u : static_cast<uint32_t>(nbuf++ & 1) * 2048u);
-                if (s.tma_out && lane == 0) bulk_wait_read<E4M3 ? 0 : 1>();
+                if (TMA_OUT && lane == 0) bulk_wait_read<E4M3 ? 0 : 1>();
                 __syncwarp();
                 return buf;
             };
             auto store_buffer = [&](uint32_t buf, int c0) {
-                if (s.tma_out) {
+                if constexpr (TMA_OUT) {
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -989,29 +990,42 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
                         tma_store_2d(&o_map, buf, static_cast<int>(nbase) + c0, static_cast<int>(m0));
                         bulk_commit();
                     }
-                    return;
-                }
-                // rows that TMA cannot address: element stores, 64 bytes of a row at once
-                __syncwarp();
-                if (f32) {
-                    const int c = lane & 15;
-                    for (int r = lane >> 4; r < 32 && m0 + r < p.tokens; r += 2) {
-                        uint32_t x;
-                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x)
-                                     : "r"(buf + swz64(r, c >> 2) + 4u * (c & 3)) : "memory");
-                        if (nbase + c0 + c < p.outputs)
-                            static_cast<uint32_t*>(p.out)[(m0 + r) * p.out_stride + nbase + c0 + c] = x;
-                    }
                 } else {
-                    for (int r = 0; r < 32 && m0 + r < p.tokens; ++r) {
-                        uint16_t x;
-                        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x)
-                                     : "r"(buf + swz64(r, lane >> 3) + 2u * (lane & 7)) : "memory");
-                        if (nbase + c0 + lane < p.outputs)
-                            static_cast<uint16_t*>(p.out)[(m0 + r) * p.out_stride + nbase + c0 + lane] = x;
+                    // rows that TMA cannot address: element stores, 64 bytes of a row at once,
+                    // eight reads of the buffer ahead of their stores
+                    __syncwarp();
+                    const int rows = static_cast<int>(min(32ll, p.tokens - m0));
+                    if (f32) {
+                        const int c = lane & 15, r0 = lane >> 4;
+                        float* dst = static_cast<float*>(p.out) + (m0 + r0) * p.out_stride + nbase + c0 + c;
+                        const bool in = nbase + c0 + c < p.outputs;
+#pragma unroll
+                        for (int g = 0; g < 32; g += 16) {
+                            uint32_t x[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) x[i] = lds32(buf + swz64(g + 2 * i + r0, c >> 2) + 4u * (c & 3));
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (in && g + 2 * i + r0 < rows)
+                                    dst[(g + 2 * i) * p.out_stride] = __uint_as_float(x[i]);
+                        }
+                    } else {
+                        uint16_t* dst = static_cast<uint16_t*>(p.out) + m0 * p.out_stride + nbase + c0 + lane;
+                        const bool in = nbase + c0 + lane < p.outputs;
+#pragma unroll
+                        for (int g = 0; g < 32; g += 8) {
+                            uint16_t x[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x[i])
+                                             : "r"(buf + swz64(g + i, lane >> 3) + 2u * (lane & 7)) : "memory");
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (in && g + i < rows) dst[(g + i) * p.out_stride] = x[i];
+                        }
                     }
+                    __syncwarp();
                 }
-                __syncwarp();
             };
 #pragma unroll
             for (int j = 0; j < Shape::kChunks; ++j) {
@@ -1075,7 +1089,7 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
             }
         }
         // the staging buffers are read out before the CTA leaves
-        if (s.tma_out && lane == 0) bulk_wait_read<0>();
+        if (TMA_OUT && lane == 0) bulk_wait_read<0>();
     } else if (!E4M3) {
         // ------------------------------------------------------ converters (int8)
         set_max_regs_dec<48>();
@@ -1232,15 +1246,15 @@ cudaError_t launch_split(const CUtensorMap& w_map, const CUtensorMap& x_map, con
                      plan.splits, stream, w_map, x_map, s);
 }
 
-template <bool E4M3>
+template <bool E4M3, bool TMA_OUT>
 cudaError_t launch_pair(const LinearMaps& maps, const PairParams& s, const LinearPlan& plan,
                         cudaStream_t stream) {
     static std::atomic<int> smem_set[kMaxDevices];
-    cudaError_t e = ensure_dynamic_smem(linear_pair_kernel<E4M3>, plan.smem, smem_set);
+    auto kern = linear_pair_kernel<E4M3, TMA_OUT>;
+    cudaError_t e = ensure_dynamic_smem(kern, plan.smem, smem_set);
     if (e != cudaSuccess) return e;
-    return launch_ex(linear_pair_kernel<E4M3>, static_cast<unsigned>(plan.grid),
-                     PairShape<E4M3>::kThreads, plan.smem, 2, stream, maps.x, maps.w,
-                     maps.out, s);
+    return launch_ex(kern, static_cast<unsigned>(plan.grid), PairShape<E4M3>::kThreads, plan.smem, 2, stream,
+                     maps.x, maps.w, maps.out, s);
 }
 
 void plan_pair(const LinearParams& p, int num_sms, LinearPlan* r) {
@@ -1355,10 +1369,13 @@ cudaError_t launch_linear(const LinearMaps& maps, const LinearParams& p, const L
         s.group_m = 8;
         s.k_steps = k_steps;
         s.nacc = p.e4m3 ? 512 / s.bn >= 2 ? 2 : 1 : static_cast<int>(kTmemA) / s.bn >= 2 ? 2 : 1;
-        s.tma_out = plan.tma_out;
         s.f_group = make_fastdiv(static_cast<uint32_t>(s.group_m * s.n_tiles));
         s.f_gm = make_fastdiv(static_cast<uint32_t>(s.group_m));
-        return p.e4m3 ? launch_pair<true>(maps, s, plan, stream) : launch_pair<false>(maps, s, plan, stream);
+        if (p.e4m3)
+            return plan.tma_out ? launch_pair<true, true>(maps, s, plan, stream)
+                                : launch_pair<true, false>(maps, s, plan, stream);
+        return plan.tma_out ? launch_pair<false, true>(maps, s, plan, stream)
+                            : launch_pair<false, false>(maps, s, plan, stream);
     }
     SplitParams s{};
     s.p = p;
