@@ -49,7 +49,8 @@ __global__ void __launch_bounds__(kMaxRowThreads)
         ss = fmaf(s, s, ss);
     }
     ss = row_sum(ss, warps, shf);
-    const float rms = 1.0f / sqrtf(ss * p.mean_of + p.eps);
+    const float mean = ss * p.mean_of + p.eps;
+    const float rms = 1.0f / sqrtf(mean);
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) h[i] *= rms;
     if (p.weight) {
@@ -62,7 +63,7 @@ __global__ void __launch_bounds__(kMaxRowThreads)
         for (int i = 0; i < kHeld; ++i) h[i] *= w[i];
     }
     uint32_t top = row_max(held_max(h), warps, shu);
-    if (!(ss <= kMaxFinite)) top = 0x7FC00000u;   // the mean square is not finite
+    if (!(mean <= kMaxFinite)) top = 0x7FC00000u;   // the mean square is not finite
     const float scale = row_scale(top, E4M3 ? 448.0f : 127.0f);
     store_codes<PHASED, E4M3>(p.q + row * p.q_stride, n, lead, t, threads, h, scale, row_blank(top));
     if (t == 0) p.scale[row] = scale;
@@ -89,7 +90,8 @@ __global__ void __launch_bounds__(kMaxRowThreads)
         ss = fmaf(h, h, ss);
     }
     ss = row_sum(ss, warps, shf);
-    const float rms = 1.0f / sqrtf(ss * p.mean_of + p.eps);
+    const float mean = ss * p.mean_of + p.eps;
+    const float rms = 1.0f / sqrtf(mean);
     auto v_of = [&](float h, int i) {
         const float w = !p.weight ? 1.0f
                         : p.weight_dtype == kTokF32 ? static_cast<const float*>(p.weight)[i]
@@ -99,7 +101,7 @@ __global__ void __launch_bounds__(kMaxRowThreads)
     uint32_t m = 0;
     for (int i = threadIdx.x; i < n; i += blockDim.x) m = max(m, abs_bits(v_of(h_at(i), i)));
     uint32_t top = row_max(m, warps, shu);
-    if (!(ss <= kMaxFinite)) top = 0x7FC00000u;   // the mean square is not finite
+    if (!(mean <= kMaxFinite)) top = 0x7FC00000u;   // the mean square is not finite
     const float scale = row_scale(top, E4M3 ? 448.0f : 127.0f);
     // each element is read before this thread writes it: residual_out may be an input
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
