@@ -20,7 +20,8 @@
  *   - Everything between the inputs and the outputs is held in 32 bits: h is
  *     rounded only where residual_out stores it (v is computed from the
  *     unrounded h).
- *   - A row of zeros gets scale 1 and codes 0.  A row whose v holds a NaN or
+ *   - A row of zeros gets scale 1 and codes 0 (whatever eps is: the norm of
+ *     zeros is zeros).  A row whose v holds a NaN or
  *     an infinity, or whose mean square is beyond fp32, gets scale NaN and
  *     codes 0, so that everything computed from it is NaN rather than a finite
  *     value that means nothing.

@@ -1,5 +1,5 @@
 """rms_norm_quant over the whole fp32 range: mean squares about the largest fp32
-number.
+number, rows of zeros and rows whose squares underflow, with and without eps.
 
 Tolerances as in _token_ref: v is within (width/32 + 64) 2^-24."""
 import math
@@ -51,3 +51,49 @@ def test_mean_square_about_the_largest_number(pkg, width, q, with_residual):
         else:
             assert abs(float(scale[r]) * qmax - 1) < (width / 32 + 64) * 2.0 ** -24
             assert (codes[r].double() == qmax).all(), m
+
+
+@pytest.mark.parametrize("width", WIDTHS)
+@pytest.mark.parametrize("q", [I8, E4])
+@pytest.mark.parametrize("x_type", [BF, FF])
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-6])
+def test_zero_rows_at_any_eps(pkg, width, q, x_type, eps):
+    """A row of zeros has scale 1 and codes 0 whatever eps is; its neighbours are
+    as they would be without it."""
+    g = torch.Generator(device="cuda").manual_seed(width)
+    x = torch.randn(4, width, generator=g, device="cuda").to(x_type)
+    x[x == 0] = 1
+    x[1] = 0
+    x[3] = -0.0
+    w = torch.randn(width, generator=g, device="cuda").to(x_type)
+    w[w == 0] = 1
+    for weight in (None, w):
+        codes, scale, _ = pkg.rms_norm_quant(x, weight, eps, qdtype=q)
+        for r in (1, 3):
+            assert float(scale[r]) == 1.0 and _blank(codes[r])
+        _, v = ref.norm64(x[::2], weight, eps, None)
+        ref.check_quant(v, codes.view(torch.uint8)[::2].view(q), scale[::2],
+                        (width / 32 + 64) * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("width", WIDTHS)
+@pytest.mark.parametrize("q", [I8, E4])
+@pytest.mark.parametrize("eps", [0.0, 1e-38, 1e-30])
+def test_rows_whose_squares_underflow(pkg, width, q, eps):
+    """Rows far below 1 with an eps that does not hide them: the mean square is
+    taken as if fp32 had no lower end."""
+    g = torch.Generator(device="cuda").manual_seed(width + 1)
+    mags = torch.tensor([1.0, 1e-9, 3e-10, 1e-15, 1e-19, 1e-22, 1e-25, 1e-30, 1e-36], device="cuda")
+    x = torch.randn(len(mags), width, generator=g, device="cuda")
+    x = torch.where(x.abs() < 0.1, torch.ones_like(x), x) * mags[:, None]
+    w = 1 + 0.25 * torch.rand(width, generator=g, device="cuda")
+    res = (x * torch.rand(x.shape, generator=g, device="cuda")).contiguous()
+    for weight, residual in ((None, None), (w, res)):
+        codes, scale, _ = pkg.rms_norm_quant(x, weight, eps, residual=residual, qdtype=q)
+        # the sum itself is rounded to fp32: h of the reference is that sum
+        h = x if residual is None else x + residual
+        _, v = ref.norm64(h, weight, eps, None)
+        keep = v.abs().amax(1) > 1e-30     # below: the scale's own lower end
+        ref.check_quant(v[keep], codes.view(torch.uint8)[keep].view(q), scale[keep],
+                        (width / 32 + 64) * 2.0 ** -24)
+        assert torch.isfinite(scale).all()
