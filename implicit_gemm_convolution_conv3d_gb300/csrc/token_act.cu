@@ -30,8 +30,13 @@ __global__ void __launch_bounds__(kMaxRowThreads)
     load_row<PHASED>(x, n, lead, inner, t, threads, v);
     float b[GATED ? kHeld : 1];
     if constexpr (GATED) load_row<PHASED>(x + n, n, lead, inner, t, threads, b);
+    // SiLU and GELU of -inf are NaN: kept as a sum of 0 * x beside them, half an
+    // instruction an element (inside them the gated instances spill)
+    constexpr bool kTails = ACT == kActSilu || ACT == kActGelu;
+    float2 spoilt = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < kHeld; i += 2) {
+        if (kTails) spoilt = __ffma2_rn(make_float2(v[i], v[i + 1]), make_float2(0.0f, 0.0f), spoilt);
         const float2 y = act2<ACT>(make_float2(v[i], v[i + 1]));
         v[i] = y.x;
         v[i + 1] = y.y;
@@ -40,14 +45,15 @@ __global__ void __launch_bounds__(kMaxRowThreads)
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) v[i] *= b[i];
     }
-    const uint32_t top = row_max(held_max(v), threads >> 5, shu);
+    const uint32_t top = row_max(isnan(spoilt.x + spoilt.y) ? kNanBits : held_max(v), threads >> 5, shu);
     const float scale = row_scale(top, E4M3 ? 448.0f : 127.0f);
     store_codes<PHASED, E4M3>(p.q + row * p.q_stride, n, lead, t, threads, v, scale, row_blank(top));
     if (t == 0) p.scale[row] = scale;
 }
 
-// Rows that do not fit: read twice.
-template <typename TX, bool E4M3>
+// Rows that do not fit: read twice; two elements a turn where the activation's
+// arithmetic is two-wide (one else: 2000 x 40000 none 155 us against 212).
+template <typename TX, int ACT, bool E4M3>
 __global__ void __launch_bounds__(kMaxRowThreads)
     act_wide_kernel(const ActParams p) {
     __shared__ uint32_t shu[32];
@@ -56,21 +62,39 @@ __global__ void __launch_bounds__(kMaxRowThreads)
     const long long n = p.width, row = blockIdx.x;
     const TX* x = static_cast<const TX*>(p.x) + row * p.x_stride;
     uint8_t* q = p.q + row * p.q_stride;
-    auto v_at = [&](long long i) {
-        const float a = activate_f32(to_f32(x[i]), p.act);
-        return p.gated ? a * to_f32(x[n + i]) : a;
+    constexpr bool kTails = ACT == kActSilu || ACT == kActGelu;
+    const int pace = blockDim.x, turn = kTails ? 2 * pace : pace;
+    auto v_at = [&](long long i) {   // elements i and (kTails; zero behind the row) i + pace
+        const bool two = kTails && i + pace < n;
+        const float2 x2 = make_float2(to_f32(x[i]), two ? to_f32(x[i + pace]) : 0.0f);
+        float2 v = act2<ACT>(x2);
+        if (kTails) v = __ffma2_rn(x2, make_float2(0.0f, 0.0f), v);   // NaN of +-inf
+        if (p.gated) {
+            v.x *= to_f32(x[n + i]);
+            if (two) v.y *= to_f32(x[n + i + pace]);
+        }
+        return v;
     };
     uint32_t m = 0;
-    for (long long i = threadIdx.x; i < n; i += blockDim.x) m = max(m, abs_bits(v_at(i)));
+    for (long long i = threadIdx.x; i < n; i += turn) {
+        const float2 v = v_at(i);
+        m = max(m, max(abs_bits(v.x), abs_bits(v.y)));
+    }
     const uint32_t top = row_max(m, blockDim.x >> 5, shu);
     const float scale = row_scale(top, E4M3 ? 448.0f : 127.0f);
-    for (long long i = threadIdx.x; i < n; i += blockDim.x)
-        q[i] = row_blank(top) ? 0 : static_cast<uint8_t>(code_of<E4M3>(v_at(i), scale));
+    for (long long i = threadIdx.x; i < n; i += turn) {
+        const float2 v = v_at(i);
+        q[i] = row_blank(top) ? 0 : static_cast<uint8_t>(code_of<E4M3>(v.x, scale));
+        if (kTails && i + pace < n) q[i + pace] = row_blank(top) ? 0 : static_cast<uint8_t>(code_of<E4M3>(v.y, scale));
+    }
     if (threadIdx.x == 0) p.scale[row] = scale;
 }
 
 template <typename TX, int ACT, bool E4M3>
 cudaError_t act_launch(const ActParams& p, cudaStream_t stream) {
+    if (p.width > kMaxRowWidth)
+        return launch_ex(act_wide_kernel<TX, ACT, E4M3>, static_cast<unsigned>(p.tokens),
+                         dim3(kMaxRowThreads), 0, 1, stream, p);
     const int xb = elt_bytes(p.x_dtype);
     const bool inputs = p.width % 8 == 0 && aligned_rows(p.x, p.x_stride, p.tokens, xb, 16);
     const bool wide = inputs && aligned_rows(p.q, p.q_stride, p.tokens, 1, 8);
@@ -84,9 +108,6 @@ cudaError_t act_launch(const ActParams& p, cudaStream_t stream) {
 
 template <typename TX, bool E4M3>
 cudaError_t act_kind(const ActParams& p, cudaStream_t stream) {
-    if (p.width > kMaxRowWidth)
-        return launch_ex(act_wide_kernel<TX, E4M3>, static_cast<unsigned>(p.tokens),
-                         dim3(kMaxRowThreads), 0, 1, stream, p);
     if (p.act == kActRelu) return act_launch<TX, kActRelu, E4M3>(p, stream);
     if (p.act == kActSilu) return act_launch<TX, kActSilu, E4M3>(p, stream);
     if (p.act == kActGelu) return act_launch<TX, kActGelu, E4M3>(p, stream);

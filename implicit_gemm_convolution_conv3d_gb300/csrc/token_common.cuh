@@ -47,6 +47,7 @@ __device__ __forceinline__ float activate_f32(float v, int act) {
 // |v| as an integer that orders like the magnitude, infinities and NaNs on top
 // (so a maximum over these bits keeps a NaN, which fmaxf would drop)
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+constexpr uint32_t kInfBits = 0x7F800000u, kNanBits = 0x7FC00000u;
 
 // The row's scale from its largest |v|: max / qmax by IEEE division, 1 for a
 // row of zeros, NaN for a row that is not finite; never subnormal, so that

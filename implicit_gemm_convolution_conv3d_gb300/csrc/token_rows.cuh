@@ -203,7 +203,9 @@ __device__ __forceinline__ float2 exp_neg2(float2 m) {
 //   v sigmoid(v):  T = e / (1 + e), e = e^-|v|
 //   v Phi(v):      T = Phi(-|v|) = e^(-v^2/2) g(|v|)
 // Below zero that is the tail alone, with its relative accuracy, and nothing
-// overflows on either side.  n = -|v|, cut where the tail is 0 in any case (128; 64).
+// overflows on either side; the tail is 0 where e is below 2^-126 (v < -87.3; -13.2).
+// n = -|v|, cut where the tail is 0 in any case (128; 64).  Infinities come out as
+// the limits 0 and inf; a caller that holds -inf * 0 to be NaN looks at its inputs.
 __device__ __forceinline__ float2 silu2(float2 v) {
     const float2 n = make_float2(fmaxf(-fabsf(v.x), -128.0f), fmaxf(-fabsf(v.y), -128.0f));
     const float2 e = exp_neg2(n);

@@ -21,10 +21,12 @@
  *     rounded only where residual_out stores it (v is computed from the
  *     unrounded h).
  *   - A row of zeros gets scale 1 and codes 0 (whatever eps is: the norm of
- *     zeros is zeros).  A row whose v holds a NaN or
- *     an infinity, or whose mean square is beyond fp32, gets scale NaN and
- *     codes 0, so that everything computed from it is NaN rather than a finite
- *     value that means nothing.
+ *     zeros is zeros).  A row whose v holds a NaN or an infinity, or whose mean
+ *     square is beyond fp32, gets scale NaN and codes 0, so that everything
+ *     computed from it is NaN rather than a finite value that means nothing.
+ *     SiLU and GELU of -inf are NaN (a product with 0), relu's is 0.
+ *   - act_quant_fwd's SiLU and GELU hold their relative accuracy in the negative
+ *     tail down to 2^-119; what is smaller may count as 0.
  *   - Zero tokens (and zero outputs of the product) are valid and launch
  *     nothing.  A width of zero is CONV_ERR_INVALID.
  */
