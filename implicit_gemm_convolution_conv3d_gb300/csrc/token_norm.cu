@@ -29,7 +29,8 @@ constexpr float kLift = 1.98070406285660844e28f;      // 2^94
 __device__ __forceinline__ float inverse_rms(float mean) { return mean == 0.0f ? 0.0f : 1.0f / sqrtf(mean); }
 
 // TINY: a mean square below kTinyMean can occur.  An instance of its own: that
-// branch's registers cost 60000 unaligned rows of 2047 5% (273 us, 287 with it).
+// branch costs 60000 unaligned rows of 2047 5% (273 us, 287 with it), 2000 rows of
+// 40000 (norm_wide_kernel) 6% (367, 387).
 template <typename TX, typename TR, bool E4M3, bool PHASED, bool TINY>
 __global__ void __launch_bounds__(kMaxRowThreads)
     norm_row_kernel(const NormParams p) {
@@ -89,10 +90,10 @@ __global__ void __launch_bounds__(kMaxRowThreads)
 }
 
 // Rows that do not fit: read again for each pass (mean square, maximum, codes).
-template <typename TX, typename TR, bool E4M3>
+template <typename TX, typename TR, bool E4M3, bool TINY>
 __global__ void __launch_bounds__(kMaxRowThreads)
     norm_wide_kernel(const NormParams p) {
-    __shared__ float shf[64];
+    __shared__ float shf[TINY ? 64 : 32];
     __shared__ uint32_t shu[32];
     griddep_launch_dependents();
     griddep_wait();
@@ -103,25 +104,25 @@ __global__ void __launch_bounds__(kMaxRowThreads)
     TR* ro = p.res_out ? static_cast<TR*>(p.res_out) + row * p.res_out_stride : nullptr;
     uint8_t* q = p.q + row * p.q_stride;
     auto h_at = [&](int i) { return to_f32(x[i]) + (r ? to_f32(r[i]) : 0.0f); };
-    auto mean_square = [&](float lift, float* sh) {
+    auto mean_square = [&](float shrink, float* sh) {
         float ss = 0.0f;
         for (int i = threadIdx.x; i < n; i += blockDim.x) {
-            const float h = h_at(i) * lift * p.shrink;
+            const float h = h_at(i) * shrink;
             ss = fmaf(h, h, ss);
         }
         return row_sum(ss, warps, sh) * p.mean_of;
     };
-    float mean = mean_square(1.0f, shf) + p.eps, lift = 1.0f;
-    if (mean < kTinyMean) {
+    float mean = mean_square(p.shrink, shf) + p.eps, lift = 1.0f;
+    if (TINY && mean < kTinyMean) {
         lift = kLift;
-        mean = mean_square(kLift, shf + 32) + p.eps * kLift * kLift;
+        mean = mean_square(p.shrink * kLift, shf + 32) + p.eps * kLift * kLift;
     }
-    const float rms = inverse_rms(mean);
+    const float rms = TINY ? inverse_rms(mean) : 1.0f / sqrtf(mean);
     auto v_of = [&](float h, int i) {
         const float w = !p.weight ? 1.0f
                         : p.weight_dtype == kTokF32 ? static_cast<const float*>(p.weight)[i]
                                                     : to_f32(static_cast<const TX*>(p.weight)[i]);
-        return h * lift * rms * w;
+        return (TINY ? h * lift : h) * rms * w;
     };
     uint32_t m = 0;
     for (int i = threadIdx.x; i < n; i += blockDim.x) m = max(m, abs_bits(v_of(h_at(i), i)));
@@ -139,9 +140,11 @@ __global__ void __launch_bounds__(kMaxRowThreads)
 
 template <typename TX, typename TR, bool E4M3>
 cudaError_t norm_launch(const NormParams& p, cudaStream_t stream) {
-    if (p.width > kMaxRowWidth)
-        return launch_ex(norm_wide_kernel<TX, TR, E4M3>, static_cast<unsigned>(p.tokens),
-                         dim3(kMaxRowThreads), 0, 1, stream, p);
+    const bool tiny = p.eps < kTinyMean;
+    if (p.width > kMaxRowWidth) {
+        auto kern = tiny ? norm_wide_kernel<TX, TR, E4M3, true> : norm_wide_kernel<TX, TR, E4M3, false>;
+        return launch_ex(kern, static_cast<unsigned>(p.tokens), dim3(kMaxRowThreads), 0, 1, stream, p);
+    }
     const int xb = elt_bytes(p.x_dtype), rb = elt_bytes(p.res_dtype);
     const bool inputs = p.width % 8 == 0 && aligned_rows(p.x, p.x_stride, p.tokens, xb, 16) &&
                       aligned_rows(p.res, p.res_stride, p.tokens, rb, 16) &&
@@ -151,7 +154,7 @@ cudaError_t norm_launch(const NormParams& p, cudaStream_t stream) {
     const dim3 block = row_block(p.width, inputs);
     const unsigned grid = row_blocks(p.tokens, block);
 #define C3D_NORM(V, Y) launch_ex(norm_row_kernel<TX, TR, E4M3, V, Y>, grid, block, 0, 1, stream, p)
-    if (p.eps < kTinyMean) return wide ? C3D_NORM(false, true) : C3D_NORM(true, true);
+    if (tiny) return wide ? C3D_NORM(false, true) : C3D_NORM(true, true);
     return wide ? C3D_NORM(false, false) : C3D_NORM(true, false);
 #undef C3D_NORM
 }
