@@ -97,16 +97,18 @@ __global__ void __launch_bounds__(kMaxRowThreads)
     __shared__ uint32_t shu[32];
     griddep_launch_dependents();
     griddep_wait();
-    const int n = static_cast<int>(p.width), warps = blockDim.x >> 5;
+    // unsigned: the last turn's index passes 2^31 where the width is near it
+    const unsigned n = static_cast<unsigned>(p.width);
+    const int warps = blockDim.x >> 5;
     const long long row = blockIdx.x;
     const TX* x = static_cast<const TX*>(p.x) + row * p.x_stride;
     const TR* r = p.res ? static_cast<const TR*>(p.res) + row * p.res_stride : nullptr;
     TR* ro = p.res_out ? static_cast<TR*>(p.res_out) + row * p.res_out_stride : nullptr;
     uint8_t* q = p.q + row * p.q_stride;
-    auto h_at = [&](int i) { return to_f32(x[i]) + (r ? to_f32(r[i]) : 0.0f); };
+    auto h_at = [&](unsigned i) { return to_f32(x[i]) + (r ? to_f32(r[i]) : 0.0f); };
     auto mean_square = [&](float shrink, float* sh) {
         float ss = 0.0f;
-        for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        for (unsigned i = threadIdx.x; i < n; i += blockDim.x) {
             const float h = h_at(i) * shrink;
             ss = fmaf(h, h, ss);
         }
@@ -118,19 +120,19 @@ __global__ void __launch_bounds__(kMaxRowThreads)
         mean = mean_square(p.shrink * kLift, shf + 32) + p.eps * kLift * kLift;
     }
     const float rms = TINY ? inverse_rms(mean) : 1.0f / sqrtf(mean);
-    auto v_of = [&](float h, int i) {
+    auto v_of = [&](float h, unsigned i) {
         const float w = !p.weight ? 1.0f
                         : p.weight_dtype == kTokF32 ? static_cast<const float*>(p.weight)[i]
                                                     : to_f32(static_cast<const TX*>(p.weight)[i]);
         return (TINY ? h * lift : h) * rms * w;
     };
     uint32_t m = 0;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) m = max(m, abs_bits(v_of(h_at(i), i)));
+    for (unsigned i = threadIdx.x; i < n; i += blockDim.x) m = max(m, abs_bits(v_of(h_at(i), i)));
     uint32_t top = row_max(m, warps, shu);
     if (!(mean <= kMaxFinite)) top = 0x7FC00000u;   // the mean square is not finite
     const float scale = row_scale(top, E4M3 ? 448.0f : 127.0f);
     // each element is read before this thread writes it: residual_out may be an input
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    for (unsigned i = threadIdx.x; i < n; i += blockDim.x) {
         const float h = h_at(i);
         q[i] = row_blank(top) ? 0 : static_cast<uint8_t>(code_of<E4M3>(v_of(h, i), scale));
         if (ro) ro[i] = from_f32<TR>(h);

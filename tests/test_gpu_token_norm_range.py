@@ -97,3 +97,19 @@ def test_rows_whose_squares_underflow(pkg, width, q, eps):
         ref.check_quant(v[keep], codes.view(torch.uint8)[keep].view(q), scale[keep],
                         (width / 32 + 64) * 2.0 ** -24)
         assert torch.isfinite(scale).all()
+
+
+def test_row_of_almost_two_to_the_31(pkg):
+    """One row whose width is within a block's stride of 2^31: a few elements that
+    are not zero, at both ends and about 2^30."""
+    width = 2 ** 31 - 7
+    at = torch.tensor([0, 1023, 1024, 2 ** 30 - 1, 2 ** 30, width - 1025, width - 1024, width - 1],
+                      device="cuda")
+    values = torch.tensor([1.0, -2.0, 3.0, -4.0, 5.0, -6.0, 7.0, -8.0], device="cuda")
+    x = torch.zeros(1, width, dtype=BF, device="cuda")
+    x[0, at] = values.to(BF)
+    codes, scale, _ = pkg.rms_norm_quant(x, eps=1e-12)
+    v = values.double() / math.sqrt(float((values.double() ** 2).sum()) / width + 1e-12)
+    assert abs(float(scale) * 127 / float(v.abs().max()) - 1) < 64 * 2.0 ** -24
+    assert torch.equal(codes[0, at].double(), torch.round(v / v.abs().max() * 127))
+    assert int((codes != 0).sum()) == len(at)
