@@ -9,6 +9,10 @@ have to be viewable as rows.  8-bit tensors are ``torch.int8`` or
 ``torch.float8_e4m3fn`` with one fp32 scale per row: value = code * scale.
 Like the convolutions', these calls marshal arguments only, run on the
 current (or the given) stream, and raise on anything the library refuses.
+A given ``stream`` is not made to wait for anything: inputs that another
+stream still writes, and results that another stream reads, are the caller's
+to order (``stream.wait_stream``).  What a call allocates for a given stream
+is that stream's memory.
 """
 from __future__ import annotations
 
@@ -101,11 +105,15 @@ def _stream(stream: Optional[torch.cuda.Stream], x: torch.Tensor):
 
 
 def _new(shape, dtype, x: torch.Tensor, stream) -> torch.Tensor:
-    """A tensor from torch's allocator that the given stream may use: memory of the
-    current stream goes back to its pool only when that stream is done with it."""
-    t = torch.empty(shape, dtype=dtype, device=x.device)
-    if stream is not None:
-        t.record_stream(stream)
+    """A tensor that the call may write at once.  With a given stream it is that
+    stream's memory: a block freed on the current stream could still be in use
+    there.  The caller's stream, which gets the tensor, is recorded on it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=x.device)
+    caller = torch.cuda.current_stream(x.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=x.device)
+    t.record_stream(caller)
     return t
 
 
