@@ -52,6 +52,19 @@ __device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatil
            wait_long_slow(bar, parity, abort_flag, status, limit_ns);
 }
 
+// After an abort: the loads into a ring of `slots` that `issued` k-steps armed.  Each
+// slot's last load is waited for, whoever has seen it: an earlier one has landed
+// (the slot was filled again), and the parity of the last is the barrier's
+// current phase, so that the wait neither passes early nor runs out.
+constexpr __host__ __device__ uint32_t drain_from(uint32_t issued, uint32_t slots) {
+    return issued > slots ? issued - slots : 0u;
+}
+static_assert(drain_from(0, 4) == 0 && drain_from(4, 4) == 0 && drain_from(5, 4) == 1 && drain_from(13, 6) == 7, "");
+
+__device__ __noinline__ void drain_ring(uint32_t full0, uint32_t issued, uint32_t slots) {
+    for (uint32_t i = drain_from(issued, slots); i < issued; ++i) drain_wait(full0 + 8 * (i % slots), (i / slots) & 1u);
+}
+
 // The byte of the 16-byte chunk `c` of row `r` in a 128-byte-swizzled tile.
 __device__ __forceinline__ uint32_t swz(int r, int c) {
     return static_cast<uint32_t>(r) * 128u + (static_cast<uint32_t>(c ^ (r & 7)) << 4);
@@ -342,7 +355,7 @@ __global__ void __launch_bounds__(kSplitThreads<E4M3>, 1)
     const uint32_t cfull0 = empty0 + 8u * kMaxStages, cempty0 = cfull0 + 8u * kMaxCvt;
     const uint32_t acc_bar = cempty0 + 8u * kMaxCvt, drain_bar = acc_bar + 8u;
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem_raw + (drain_bar + 8u - raw));
-    // misc[0] TMEM base, [1] abort flag, [2] k-steps issued, [3] k-steps consumed
+    // misc[0] TMEM base, [1] abort flag, [2] k-steps issued
     volatile uint32_t* abort_flag = misc + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -367,7 +380,6 @@ __global__ void __launch_bounds__(kSplitThreads<E4M3>, 1)
         mbar_init(drain_bar, 1);
         misc[1] = 0u;
         misc[2] = 0u;
-        misc[3] = 0u;
         fence_mbar_init();
         prefetch_tmap(&w_map);
         prefetch_tmap(&x_map);
@@ -418,7 +430,6 @@ __global__ void __launch_bounds__(kSplitThreads<E4M3>, 1)
                     ok = false;
                     break;
                 }
-                if (E4M3) misc[3] = i + 1;
                 tc_fence_after();
                 const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(st) * step);
                 if (E4M3) {
@@ -454,7 +465,6 @@ __global__ void __launch_bounds__(kSplitThreads<E4M3>, 1)
                     ok = false;
                     break;
                 }
-                if ((warp == 4 || warp == 8) && lane == 0) misc[3] = i + 1;
                 const uint32_t src = ring + st * s.stage_bytes;
                 if (warp < 12) {
                     tc_fence_after();
@@ -612,13 +622,8 @@ __global__ void __launch_bounds__(kSplitThreads<E4M3>, 1)
     if (s.splits > 1) cluster_sync();   // the peers have read this CTA's partial tile
     else __syncthreads();
     if (*abort_flag) {
-        // drain: boxes armed but never waited for, then the MMAs in flight
-        if (threadIdx.x == 0) {
-            const uint32_t issued = misc[2], consumed = misc[3];
-            for (uint32_t i = consumed; i < issued; ++i)
-                drain_wait(full0 + 8 * (i % static_cast<uint32_t>(s.stages)),
-                           (i / static_cast<uint32_t>(s.stages)) & 1u);
-        }
+        // drain: the loads, then the MMAs in flight
+        if (threadIdx.x == 0) drain_ring(full0, misc[2], static_cast<uint32_t>(s.stages));
         if (warp == 1 && lane == 0) {
             tc_commit(drain_bar);
             drain_wait(drain_bar, 0);
@@ -770,8 +775,7 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
     const uint32_t tfull0 = empty0 + 8u * kMaxStages, tempty0 = tfull0 + 16u;
     const uint32_t drain_bar = tempty0 + 16u;
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem_pair + (drain_bar + 8u - ring));
-    // misc[0] TMEM base, [1] abort flag, [2] weights' k-steps issued, [3] waited
-    // for, [4] tokens' k-steps issued, [5] waited for
+    // misc[0] TMEM base, [1] abort flag, [2] weights' k-steps issued, [3] tokens'
     volatile uint32_t* abort_flag = misc + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -792,7 +796,7 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
             mbar_init(tempty0 + 8 * i, 2 * Shape::kEpiWarps);
         }
         mbar_init(drain_bar, 1);
-        for (int i = 1; i < 6; ++i) misc[i] = 0u;
+        for (int i = 1; i < 4; ++i) misc[i] = 0u;
         fence_mbar_init();
         prefetch_tmap(&x_map);
         prefetch_tmap(&w_map);
@@ -857,7 +861,7 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
                 const uint64_t adesc = make_smem_desc(ring, 1024u, 2u);
                 const uint64_t bdesc = make_smem_desc(ring + (E4M3 ? kTokBytes : 0u), 1024u, 2u);
                 int st = 0, it = 0;
-                uint32_t ph = 0, consumed = 0;
+                uint32_t ph = 0;
                 bool ok = true, landed = false;   // landed: this stage's operands were seen
                 auto here = [&](int stage, uint32_t phase) {
                     return mbar_test_wait(wfull0 + 8 * stage, phase) &&
@@ -879,7 +883,6 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
                             ok = false;
                             break;
                         }
-                        misc[3] = ++consumed;
                         tc_fence_after();
                         const uint64_t off =
                             static_cast<uint64_t>(static_cast<uint32_t>(st) * (Shape::kStage >> 4));
@@ -921,7 +924,7 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
                         }
                         mbar_arrive_expect_tx(xfull0 + 8 * xs, kTokBytes);
                         tma_load_2d(toks + xs * kTokBytes, &x_map, xfull0 + 8 * xs, i * kStep, m0);
-                        misc[4] = ++issued;
+                        misc[3] = ++issued;
                         if (++xs == Shape::kTokSlots) {
                             xs = 0;
                             ph ^= 1u;
@@ -1102,7 +1105,6 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
             const bool ok = wait_long(xfull0 + 8 * xs, xph, abort_flag, p.status, p.wait_ns) &&
                             wait_long(empty0 + 8 * ts, tph ^ 1u, abort_flag, p.status, p.wait_ns);
             if (!__all_sync(0xffffffffu, ok)) break;
-            if ((warp & 3) == 0 && lane == 0) misc[5] = static_cast<uint32_t>(i + 1);
             tc_fence_after();
             const uint32_t src = toks + xs * kTokBytes;
 #pragma unroll
@@ -1141,11 +1143,8 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
         while (clock64() - t0 < 200000) {
         }
         if (threadIdx.x == 0) {
-            for (uint32_t i = misc[3]; rank == 0 && i < misc[2]; ++i)
-                drain_wait(wfull0 + 8 * (i % Shape::kStages), (i / Shape::kStages) & 1u);
-            for (uint32_t i = misc[5]; !E4M3 && i < misc[4]; ++i)
-                drain_wait(xfull0 + 8 * (i % PairShape<false>::kTokSlots),
-                           (i / PairShape<false>::kTokSlots) & 1u);
+            if (rank == 0) drain_ring(wfull0, misc[2], Shape::kStages);
+            if (!E4M3) drain_ring(xfull0, misc[3], PairShape<false>::kTokSlots);
         }
         if (warp == 1 && lane == 0 && rank == 0) {
             tc_commit_pair(drain_bar, 1);
