@@ -104,6 +104,12 @@ __device__ __forceinline__ float ld_cluster_f1(uint32_t cluster_addr) {
     return v;
 }
 
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
@@ -1143,7 +1149,13 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
         while (clock64() - t0 < 200000) {
         }
         if (threadIdx.x == 0) {
-            if (rank == 0) drain_ring(wfull0, misc[2], Shape::kStages);
+            if (rank == 0) {
+                // the peer's half of a step that it gave up before is not coming
+                const uint32_t theirs = ld_cluster_u32(mapa_shared(smem_u32(misc + 2), 1));
+                for (uint32_t i = max(theirs, drain_from(misc[2], Shape::kStages)); i < misc[2]; ++i)
+                    mbar_complete_tx(wfull0 + 8 * (i % Shape::kStages), Shape::kStage);
+                drain_ring(wfull0, misc[2], Shape::kStages);
+            }
             if (!E4M3) drain_ring(xfull0, misc[3], PairShape<false>::kTokSlots);
         }
         if (warp == 1 && lane == 0 && rank == 0) {

@@ -50,3 +50,25 @@ def test_waits_that_run_out_midway(pkg, m, n, k, q):
         assert torch.equal(pkg.linear_w8a8(x, w), want)
         assert pkg.conv_get_device_status() == 0
     assert gave_up > 0
+
+
+@pytest.mark.parametrize("m,n,k", [(2048, 2048, 2048), (4000, 3000, 640)])
+@pytest.mark.parametrize("q", [torch.int8, torch.float8_e4m3fn])
+def test_pairs_give_up_at_once(pkg, m, n, k, q):
+    """One CTA of a pair may give up earlier than the other: the loads that it never
+    issued are not waited for."""
+    x = torch.ones(m, k, device="cuda").to(q)
+    w = torch.ones(n, k, device="cuda").to(q)
+    pkg.linear_w8a8(x, w)
+    assert pkg.conv_get_device_status() == 0
+    try:
+        for limit in (0, 300, 700, 1000, 1500, 2500, 5000) * 3:
+            pkg.conv_set_wait_limit_ns(limit)
+            start = time.monotonic()
+            pkg.linear_w8a8(x, w)
+            pkg.conv_get_device_status()
+            assert time.monotonic() - start < 0.5, limit
+    finally:
+        pkg.conv_set_wait_limit_ns(2_000_000_000)
+    assert (pkg.linear_w8a8(x, w) == k).all()
+    assert pkg.conv_get_device_status() == 0
