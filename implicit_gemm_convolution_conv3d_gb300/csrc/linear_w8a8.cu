@@ -26,7 +26,13 @@ template <bool E4M3>
 constexpr int kSplitThreads = 128 + 32 * (E4M3 ? 8 : 16);   // converters / epilogue behind four warps
 constexpr int kMaxStages = 8, kMaxCvt = 4, kMaxSplits = 8;
 constexpr uint32_t kBarBytes = 16u * (kMaxStages + kMaxCvt) + 16u;
-constexpr int kSplitSmem = 206 * 1024;   // rings (200 KB at most), barriers, alignment
+// Rings (200 KB at most), barriers, alignment.  Every launch asks for all of it: the
+// kernel holds all of an SM's tensor memory, and where two of its CTAs could share
+// an SM, two clusters could each hold what the other waits for.
+constexpr int kSplitRings = 200 * 1024, kSplitSmem = 206 * 1024;
+static_assert(kSplitRings + kBarBytes + 32 + 1024 <= kSplitSmem, "");
+constexpr int kSmSmem = 228 * 1024;      // of an SM; a CTA takes 1 KB more than it asks for
+static_assert(2 * (kSplitSmem + 1024) > kSmSmem, "one split CTA an SM");
 
 // Bounded wait (see wait_bar) of a role that may wait for thousands of cycles:
 // it sleeps in hardware between looks, so that its polling leaves the issue slots
@@ -1297,18 +1303,16 @@ void plan_split(const LinearParams& p, const ClusterRoom& room, LinearPlan* r) {
     r->splits = 1;
     for (int i = 1; i < 4; ++i)
         if (tiles <= room.of[i] && (1 << i) <= k_steps) r->splits = 1 << i;
-    // rings within 200 KB: raw stages of both operands, converted tokens (f16)
+    // rings within kSplitRings: raw stages of both operands, converted tokens (f16)
     const int stage = (kRows + r->tok_tile) * kStep, cvt = r->tok_tile * 256;
     r->cvt_stages = p.e4m3 ? 0 : (r->tok_tile <= 64 ? kMaxCvt : 2);
-    r->stages = std::min(kMaxStages, (200 * 1024 - r->cvt_stages * cvt) / stage);
+    r->stages = std::min(kMaxStages, (kSplitRings - r->cvt_stages * cvt) / stage);
     const long long per_rank = (k_steps + r->splits - 1) / r->splits;
     r->stages = static_cast<int>(std::min<long long>(r->stages, per_rank));
-    r->stages = std::max(2, r->stages / 2 * 2);   // even (see the converters)
-    // the ring also holds the fp32 partial tile
-    const int ring = std::max(r->stages * stage, r->tok_tile * kRows * 4);
-    r->stages = std::max(r->stages, (ring + 2 * stage - 1) / (2 * stage) * 2);
-    r->smem = static_cast<size_t>(r->stages) * stage + static_cast<size_t>(r->cvt_stages) * cvt + kBarBytes +
-              32 + 1024;
+    // even (see the converters); two stages also hold the fp32 partial tile: (128 + t) 256
+    // bytes against 512 t, t <= 128
+    r->stages = std::max(2, r->stages / 2 * 2);
+    r->smem = kSplitSmem;
 }
 
 }  // namespace

@@ -49,3 +49,29 @@ def test_results_are_not_written_over(pkg, q):
         assert torch.equal(got, want)
         for a, b in zip((*got_norm, *got_act), (*norm, *act)):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_products_and_convolutions_side_by_side(pkg):
+    """Kernels that hold an SM's tensor memory, in clusters of several sizes, on four
+    streams at once: each gives what it gives alone."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    work = []
+    for q, m, n, k in ((I8, 40, 1024, 4096), (E4, 64, 512, 8192), (E4, 128, 2048, 1024),
+                       (I8, 300, 1280, 1280), (E4, 1200, 2560, 640), (I8, 1200, 2560, 640)):
+        x = (torch.randn(m, k, generator=g, device="cuda") * 30).clamp(-127, 127).to(q)
+        w = (torch.randn(n, k, generator=g, device="cuda") * 30).clamp(-127, 127).to(q)
+        work.append(lambda s, x=x, w=w: pkg.linear_w8a8(x, w, stream=s))
+    xc = torch.randn(1, 4, 24, 24, 256, generator=g, device="cuda").bfloat16()
+    wc = torch.randn(256, 3, 3, 3, 256, generator=g, device="cuda").bfloat16()
+    work.append(lambda s: pkg.conv_fwd(xc, wc, 1, 1, 1, stream=s))
+    want = [f(None) for f in work]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(20):
+        for i in range(len(work)):
+            j = (turn + i) % len(work)
+            got.append((j, work[j](streams[(turn * 3 + i) % 4])))
+    torch.cuda.synchronize()
+    for j, y in got:
+        assert torch.equal(y, want[j]), j
