@@ -24,7 +24,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["conv_igemm.cu", "aux_kernels.cu", "conv3d_api.cu", "conv_noalloc.cu", "conv_fused_q.cu",
            "token_norm.cu", "token_act.cu", "linear_w8a8.cu", "token_api.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "tile_table.h", "kernel_common.cuh"]
-TOKEN_HEADERS = ["token_common.cuh", "token_rows.cuh", "token_ops_internal.h"]   # the token operators' own
+# the token operators' own
+TOKEN_HEADERS = ["token_common.cuh", "token_activations.cuh", "token_rows.cuh", "token_ops_internal.h"]
 PUBLIC_HEADERS = ["conv3d.h", "token_ops.h"]
 
 

@@ -11,6 +11,7 @@
 
 #include <algorithm>
 
+#include "token_activations.cuh"
 #include "token_common.cuh"
 #include "token_ops.h"
 #include "token_ops_internal.h"
@@ -170,12 +171,14 @@ __device__ __forceinline__ void cvt_rows(uint32_t src, uint32_t dst, int rows, i
     }
 }
 
-// Epilogue activation: the convolutions' forms for 16-bit outputs, the
-// fp32-accurate ones for fp32 outputs; both keep a NaN.  Out of line: the code
-// behind a mainloop runs once and cold, and the fp32 forms are long.
+// Epilogue activation: for 16-bit outputs the convolutions' SiLU and the row kernels'
+// GELU (the convolutions' is off by 1.5e-7 in erf, more than its value below -5,
+// which both types can hold), for fp32 outputs the fp32-accurate forms; all keep a
+// NaN.  Out of line: the code behind a mainloop runs once and cold, and the fp32
+// forms are long.
 __device__ __noinline__ float epi_act_call(float v, int act, int out_dtype) {
     if (act == kActRelu || out_dtype == kTokF32) return activate_f32(v, act);
-    return activate(v, act);
+    return act == kActSilu ? activate_c<kActSilu>(v) : gelu2<true>(make_float2(v, 0.0f)).x;
 }
 
 __device__ __forceinline__ float epi_act(float v, int act, int out_dtype) {
@@ -739,11 +742,16 @@ __device__ __forceinline__ void mul2(uint32_t& v0, uint32_t& v1, float sx, uint3
 __device__ __forceinline__ void act_chunk(uint32_t (&v)[32], int act) {
     auto each = [&](auto f) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(f(__uint_as_float(v[j])));
+        for (int j = 0; j < 32; j += 2) {
+            const float2 y = f(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
+            v[j] = __float_as_uint(y.x);
+            v[j + 1] = __float_as_uint(y.y);
+        }
     };
-    if (act == kActRelu) each([](float y) { return y < 0.0f ? 0.0f : y; });
-    else if (act == kActSilu) each([](float y) { return activate_c<kActSilu>(y); });
-    else each([](float y) { return activate_c<kActGelu>(y); });
+    if (act == kActRelu) each([](float2 y) { return make_float2(y.x < 0.0f ? 0.0f : y.x, y.y < 0.0f ? 0.0f : y.y); });
+    else if (act == kActSilu)
+        each([](float2 y) { return make_float2(activate_c<kActSilu>(y.x), activate_c<kActSilu>(y.y)); });
+    else each([](float2 y) { return gelu2<true>(y); });
 }
 
 struct PairTile {

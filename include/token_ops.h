@@ -69,7 +69,8 @@ int act_quant_fwd(const void* x, int x_dtype, int64_t x_stride, int act, int gat
 /* The product of tokens x [tokens, width] and weights w [outputs, width],
  * both of `dtype` (INT8 or FP8_E4M3), with fp32 scales [tokens] and
  * [outputs] (NULL: ones), an optional fp32 bias [outputs] and an activation.
- * out: BF16, F16 or F32, [tokens, outputs].
+ * out: BF16, F16 or F32, [tokens, outputs].  The activations keep their relative
+ * accuracy in the negative tail in each of them; SiLU and GELU of -inf are NaN.
  * Sums are fp32: exact for int8 while every partial sum stays within 2^24
  * (any width up to 1024, and wider ones unless nearly all products are at
  * the type's limits with one sign), within a relative 2^-23 per 16 products
