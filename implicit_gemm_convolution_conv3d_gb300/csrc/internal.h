@@ -289,7 +289,9 @@ int launch_limits(LaunchLimits* l);
 
 // Tensor map of a matrix [rows, cols] of 1-, 2- or 4-byte elements, `pitch` bytes
 // between rows (base and pitch multiples of 16): boxes of box_rows rows x
-// box_bytes (64 or 128, the swizzle too), zeros outside the matrix.
+// box_bytes (64 or 128, the swizzle too), zeros outside the matrix.  Stores leave
+// out rows and columns outside it, but write whole 16-byte words: cols * elt has
+// to be a multiple of 16 there.
 int encode_rows(CUtensorMap* m, const void* ptr, int elt, long long cols, long long rows,
                 long long pitch, int box_rows, int box_bytes);
 

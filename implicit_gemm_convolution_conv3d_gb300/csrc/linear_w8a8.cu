@@ -1009,7 +1009,8 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        // columns and rows outside the output are not written
+                        // columns and rows outside the output are not written (its rows end on
+                        // 16 bytes)
                         tma_store_2d(&o_map, buf, static_cast<int>(nbase) + c0, static_cast<int>(m0));
                         bulk_commit();
                     }

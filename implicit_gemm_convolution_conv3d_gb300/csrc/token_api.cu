@@ -219,15 +219,15 @@ int linear_w8a8_fwd(const void* x, int64_t x_stride, const void* w, int64_t w_st
         return CONV_ERR_UNSUPPORTED;
     }
     const long long elt = size_of(out_dtype);
-    plan.tma_out = aligned_to(out, 16) && (tokens == 1 || out_stride * elt % 16 == 0);
+    // TMA stores whole 16-byte words: an output row's last one has to be its own
+    plan.tma_out = aligned_to(out, 16) && out_stride * elt % 16 == 0 && outputs * elt % 16 == 0;
     LinearMaps maps{};
     if ((rc = encode_rows(&maps.x, p.x, 1, width, tokens, p.x_stride, plan.tok_box, 128))) return rc;
     if ((rc = encode_rows(&maps.w, p.w, widen ? 2 : 1, width, outputs, p.w_stride * (widen ? 2 : 1),
                           plan.out_box, 128)))
         return rc;
     if (plan.pair && plan.tma_out &&
-        (rc = encode_rows(&maps.out, out, static_cast<int>(elt), outputs, tokens,
-                          (tokens == 1 ? outputs * elt + 15 & ~15ll : out_stride * elt), 32, 64)))
+        (rc = encode_rows(&maps.out, out, static_cast<int>(elt), outputs, tokens, out_stride * elt, 32, 64)))
         return rc;
     cudaError_t e = cudaSuccess;
     if (copy_x || copy_w || widen) {
