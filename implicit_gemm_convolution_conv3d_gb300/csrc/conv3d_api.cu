@@ -1219,7 +1219,7 @@ int launch_limits(LaunchLimits* l) {
     DeviceInfo* d = nullptr;
     int rc = device_info(&d);
     if (rc) return rc;
-    *l = LaunchLimits{d->num_sms, d->smem_optin, d->status, g_wait_ns};
+    *l = LaunchLimits{d->num_sms, d->status, g_wait_ns};
     return CONV_OK;
 }
 

@@ -281,7 +281,7 @@ cudaError_t launch_pack_tma(const CUtensorMap* in_map, long long N, long long C,
 // What a launch needs to know of the current device, and the bound on the
 // kernels' waits.
 struct LaunchLimits {
-    int num_sms, smem_optin;
+    int num_sms;
     int* status;
     unsigned long long wait_ns;
 };

@@ -686,13 +686,12 @@ __global__ void __launch_bounds__(kSplitThreads<E4M3>, 1)
 // only, not for the 6000 cycles that a tile's epilogue took chunk by chunk.
 struct PairParams {
     LinearParams p;
-    int bn;                   // outputs of a tile: a multiple of 64, at most 256
     int m_tiles, n_tiles, group_m;
     int k_steps;
-    int nacc;                 // accumulators in TMEM
     FastDiv f_group, f_gm;
 };
 
+constexpr int kPairOut = 256;                             // outputs of a tile
 constexpr uint32_t kTokBytes = kRows * kStep;             // tokens of a k-step and CTA
 constexpr uint32_t kTmemA = 256;                          // TMEM columns of the converted tokens
 template <bool E4M3>
@@ -701,6 +700,7 @@ struct PairShape {
     // a ring stage: e4m3 tokens and weights, int8 weights (f16) alone
     static constexpr uint32_t kStage = kWBytes + (E4M3 ? kTokBytes : 0u);
     static constexpr int kStages = E4M3 ? 6 : 4;
+    static constexpr int kAcc = E4M3 ? 2 : 1;        // accumulators in TMEM
     static constexpr int kTokSlots = E4M3 ? 0 : 4;   // int8: raw tokens
     // The two converter groups take alternate k-steps.  A parity wait tells a phase
     // from its neighbours only, so a group has to see every phase of the slots it
@@ -768,10 +768,10 @@ __device__ __forceinline__ PairTile pair_tile(int t, const PairParams& s) {
     return PairTile{first + local - nt * gm, nt};
 }
 
-// Outputs that tile nt's MMAs compute: bn, or the rest rounded up to 32.
+// Outputs that tile nt's MMAs compute: kPairOut, or the rest rounded up to 32.
 __device__ __forceinline__ int pair_cols(int nt, const PairParams& s) {
-    const long long rest = s.p.outputs - static_cast<long long>(nt) * s.bn;
-    return rest >= s.bn ? s.bn : static_cast<int>((rest + 31) & ~31ll);
+    const long long rest = s.p.outputs - static_cast<long long>(nt) * kPairOut;
+    return rest >= kPairOut ? kPairOut : static_cast<int>((rest + 31) & ~31ll);
 }
 
 // TMA_OUT: TMA can address the output's rows; else they are stored element by
@@ -849,7 +849,7 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
                 for (int t = first; t < tiles && ok; t += stride) {
                     const PairTile tl = pair_tile(t, s);
                     const int m0 = tl.mt * 256 + rank * kRows;
-                    const int n0 = tl.nt * s.bn + rank * (pair_cols(tl.nt, s) >> 1);
+                    const int n0 = tl.nt * kPairOut + rank * (pair_cols(tl.nt, s) >> 1);
                     for (int i = 0; i < s.k_steps; ++i) {
                         if (!wait_long(empty0 + 8 * st, ph ^ 1u, abort_flag, p.status, p.wait_ns)) {
                             ok = false;
@@ -892,10 +892,10 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
                     // D fp32, operands f16 (or e4m3: both codes are 0), N, M 256
                     const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(pair_cols(tl.nt, s) >> 3) << 17) |
                                            ((256u >> 4) << 24);
-                    const int acc = it % s.nacc;
-                    const uint32_t aph = static_cast<uint32_t>(it / s.nacc) & 1u;
+                    const int acc = it % Shape::kAcc;
+                    const uint32_t aph = static_cast<uint32_t>(it / Shape::kAcc) & 1u;
                     if (!wait_bar(tempty0 + 8 * acc, aph ^ 1u, abort_flag, p.status, p.wait_ns)) break;
-                    const uint32_t d = tmem + static_cast<uint32_t>(acc * s.bn);
+                    const uint32_t d = tmem + static_cast<uint32_t>(acc * kPairOut);
                     for (int i = 0; i < s.k_steps; ++i) {
                         if (!landed &&
                             (!wait_bar(wfull0 + 8 * st, ph, abort_flag, p.status, p.wait_ns) ||
@@ -964,7 +964,7 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
         for (int t = first; t < tiles; t += stride, ++it) {
             const PairTile tl = pair_tile(t, s);
             const int ncols = pair_cols(tl.nt, s);
-            const long long nbase = static_cast<long long>(tl.nt) * s.bn;
+            const long long nbase = static_cast<long long>(tl.nt) * kPairOut;
             const long long m0 = static_cast<long long>(tl.mt) * 256 + rank * kRows + q * 32;
             // this lane's scale and bias of each 32-column chunk
             float csw[Shape::kChunks], cbi[Shape::kChunks];
@@ -976,14 +976,14 @@ __global__ void __launch_bounds__(PairShape<E4M3>::kThreads, 1)
                 cbi[j] = in && p.bias ? __ldg(p.bias + nbase + c) : 0.0f;
             }
             const float sx = p.scale_x && m0 + lane < p.tokens ? __ldg(p.scale_x + m0 + lane) : 1.0f;
-            const int acc = it % s.nacc;
-            const uint32_t aph = static_cast<uint32_t>(it / s.nacc) & 1u;
+            const int acc = it % Shape::kAcc;
+            const uint32_t aph = static_cast<uint32_t>(it / Shape::kAcc) & 1u;
             if (!__all_sync(0xffffffffu,
                             wait_long(tfull0 + 8 * acc, aph, abort_flag, p.status, p.wait_ns)))
                 break;
             tc_fence_after();
             const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) +
-                                static_cast<uint32_t>(acc * s.bn + col0);
+                                static_cast<uint32_t>(acc * kPairOut + col0);
             // chunks that have outputs; all are loaded (the columns exist), so that the
             // accumulator goes back at once
             const int chunks = max(0, min(Shape::kChunks, (ncols - col0 + 31) >> 5));
@@ -1285,11 +1285,9 @@ cudaError_t launch_pair(const LinearMaps& maps, const PairParams& s, const Linea
 
 void plan_pair(const LinearParams& p, int num_sms, LinearPlan* r) {
     r->pair = 1;
-    r->tok_tile = 256;
-    r->out_tile = 256;
     r->tok_box = r->out_box = kRows;
     r->tok_tiles = static_cast<int>((p.tokens + 255) / 256);
-    r->out_tiles = static_cast<int>((p.outputs + r->out_tile - 1) / r->out_tile);
+    r->out_tiles = static_cast<int>((p.outputs + kPairOut - 1) / kPairOut);
     r->splits = 1;
     r->smem = p.e4m3 ? PairShape<true>::kBytes : PairShape<false>::kBytes;
     const long long tiles = static_cast<long long>(r->tok_tiles) * r->out_tiles;
@@ -1301,7 +1299,7 @@ void plan_split(const LinearParams& p, const ClusterRoom& room, LinearPlan* r) {
     r->tok_tiles = static_cast<int>((p.tokens + kMaxTok - 1) / kMaxTok);
     const long long per = (p.tokens + r->tok_tiles - 1) / r->tok_tiles;
     r->tok_tile = static_cast<int>((per + 15) / 16 * 16);
-    r->out_tile = r->out_box = kRows;
+    r->out_box = kRows;
     r->tok_box = r->tok_tile;
     r->tok_tiles = static_cast<int>((p.tokens + r->tok_tile - 1) / r->tok_tile);
     r->out_tiles = static_cast<int>((p.outputs + kRows - 1) / kRows);
@@ -1387,12 +1385,10 @@ cudaError_t launch_linear(const LinearMaps& maps, const LinearParams& p, const L
     if (plan.pair) {
         PairParams s{};
         s.p = p;
-        s.bn = plan.out_tile;
         s.m_tiles = plan.tok_tiles;
         s.n_tiles = plan.out_tiles;
         s.group_m = 8;
         s.k_steps = k_steps;
-        s.nacc = p.e4m3 ? 512 / s.bn >= 2 ? 2 : 1 : static_cast<int>(kTmemA) / s.bn >= 2 ? 2 : 1;
         s.f_group = make_fastdiv(static_cast<uint32_t>(s.group_m * s.n_tiles));
         s.f_gm = make_fastdiv(static_cast<uint32_t>(s.group_m));
         if (p.e4m3)

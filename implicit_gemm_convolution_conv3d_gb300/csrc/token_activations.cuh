@@ -44,7 +44,7 @@ __device__ __forceinline__ float2 exp_neg2(float2 m) {
 // overflows on either side; the tail is 0 where e is below 2^-126 (v < -87.3; -13.2).
 // n = -|v|, cut where the tail is 0 in any case (128; 64).  Infinities come out as
 // the limits 0 and inf; a caller that holds -inf * 0 to be NaN looks at its inputs,
-// or has gelu2<true> do it (an instruction an element more).
+// or has gelu2<true> do it (half an instruction an element more).
 __device__ __forceinline__ float2 silu2(float2 v) {
     const float2 n = make_float2(fmaxf(-fabsf(v.x), -128.0f), fmaxf(-fabsf(v.y), -128.0f));
     const float2 e = exp_neg2(n);
@@ -68,8 +68,10 @@ __device__ __forceinline__ float2 gelu2(float2 v) {
     for (int i = 7; i >= 0; --i) q = __ffma2_rn(q, t, make_float2(kQ[i], kQ[i]));
     const float2 e = exp_neg2(__fmul2_rn(__fmul2_rn(n, n), make_float2(-0.5f, -0.5f)));
     const float2 tail = __fmul2_rn(__fmul2_rn(q, t), e);
-    const float2 m = INF_TO_NAN ? make_float2(fminf(v.x, n.x), fminf(v.y, n.y)) : n;   // -inf uncut
-    return __ffma2_rn(m, tail, make_float2(relu_nan(v.x), relu_nan(v.y)));
+    // max(v, 0), or v + max(-v, 0): the same but for -inf
+    const float2 r = INF_TO_NAN ? __fadd2_rn(v, make_float2(fmaxf(-v.x, 0.0f), fmaxf(-v.y, 0.0f)))
+                                : make_float2(relu_nan(v.x), relu_nan(v.y));
+    return __ffma2_rn(n, tail, r);
 }
 
 template <int ACT>

@@ -1,6 +1,6 @@
-// token_common.cuh -- what the token kernels (token_quant.cu, linear_w8a8.cu)
-// share: element loads and stores in fp32, activations, and the row scale and
-// codes of the 8-bit outputs.
+// token_common.cuh -- what the token kernels (token_norm.cu, token_act.cu,
+// linear_w8a8.cu) share: element loads and stores in fp32, the fp32 outputs'
+// activations, the row scale and codes of the 8-bit outputs, and launches.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -54,7 +54,7 @@ struct LinearParams {
 // How linear_w8a8_fwd runs a problem (plan_linear)
 struct LinearPlan {
     int pair;               // CTA-pair kernel for many tokens, else the split kernel
-    int tok_tile, out_tile; // tokens and outputs of a tile
+    int tok_tile;           // split: tokens of a tile
     int tok_box, out_box;   // rows of a TMA box of either operand
     int out_tiles, tok_tiles;
     int splits;             // split: CTAs of a cluster that share a tile's reduction
