@@ -1328,16 +1328,19 @@ void plan_split(const LinearParams& p, const ClusterRoom& room, LinearPlan* r) {
 
 // The pair form's tile is 256 tokens high and its k-step costs the same at any
 // width, so it pays where the split form's 128 x 128 tiles would need a second
-// wave (152 SMs): 512 x 8192 x 2048 int8 24.5 us against 33.4, e4m3 11.0 against
-// 21.6; within one wave the split form wins (1024 x 2048 x 2048 int8 16.9 us
-// against 19.3, 512 x 2048 x 8192 e4m3 15.3 against 24.0) except for e4m3 with more
-// than 512 tokens (1024 x 2048 x 2048: 9.9 pair, 11.0 split).  Up to 256 tokens
-// the pair's second CTA would have nothing to do, and int8 weights are not worth
-// widening (256 x 8192 x 2048: 23.5 pair, 16.9 split).
-bool linear_pair_form(long long tokens, long long outputs, int e4m3) {
+// wave: 512 x 8192 x 2048 int8 24.5 us against 33.4, e4m3 11.0 against 21.6.
+// Within one wave the split form wins or is within 3% of it, the more the longer
+// the reduction that it splits and the fewer the tiles (pair, split): int8 1024 x
+// 2048 x 2048 19.3, 16.9; e4m3 600 x 640 x 8192 23.4, 10.2; 1024 x 1024 x 8192 23.6,
+// 14.8; 1024 x 2048 x 8192 23.8, 22.0; 1024 x 2048 x 2048 10.0, 9.9; 4000 x 512 x
+// 512 6.3, 6.5.  Up to 256 tokens the pair's second CTA would have nothing to do, and
+// int8 weights are not worth widening (256 x 8192 x 2048: 23.5 pair, 16.9 split).
+// A wave is counted in sm_103a's 152 SMs, not the current device's: the workspace's
+// size follows from this rule, and its query asks no device.
+bool linear_pair_form(long long tokens, long long outputs) {
+    constexpr int kWave = 152;
     if (tokens <= 256) return false;
-    const long long tiles = (tokens + kMaxTok - 1) / kMaxTok * ((outputs + kRows - 1) / kRows);
-    return tiles > 152 || (e4m3 && tokens > 512);
+    return (tokens + kMaxTok - 1) / kMaxTok * ((outputs + kRows - 1) / kRows) > kWave;
 }
 bool linear_thin_form(long long tokens) { return tokens <= kThinTok; }
 
@@ -1370,7 +1373,7 @@ cudaError_t launch_linear_thin(const LinearParams& p, int num_sms, cudaStream_t 
 
 cudaError_t plan_linear(const LinearParams& p, int num_sms, LinearPlan* r) {
     *r = LinearPlan{};
-    if (linear_pair_form(p.tokens, p.outputs, p.e4m3)) {
+    if (linear_pair_form(p.tokens, p.outputs)) {
         plan_pair(p, num_sms, r);
         return cudaSuccess;
     }

@@ -144,7 +144,7 @@ size_t linear_w8a8_workspace_size(const void* x, int64_t x_stride, const void* w
                                   int64_t width) {
     if (tokens < 1 || outputs < 1 || width < 1 || linear_thin_form(tokens)) return 0;
     const size_t pitch = static_cast<size_t>(round16(width));
-    const bool widen = dtype == CONV_DTYPE_INT8 && linear_pair_form(tokens, outputs, 0);
+    const bool widen = dtype == CONV_DTYPE_INT8 && linear_pair_form(tokens, outputs);
     return (tma_rows(x, x_stride, tokens) ? 0 : pitch * static_cast<size_t>(tokens)) +
            (widen ? 2 : tma_rows(w, w_stride, outputs) ? 0 : 1) * pitch * static_cast<size_t>(outputs);
 }
@@ -197,7 +197,7 @@ int linear_w8a8_fwd(const void* x, int64_t x_stride, const void* w, int64_t w_st
         return launched(launch_linear_thin(p, lim.num_sms, stream), "linear_w8a8_fwd launch");
     // operands that TMA cannot address are copied to an aligned pitch first, and
     // the pair form's int8 weights are widened to f16
-    const bool widen = !p.e4m3 && linear_pair_form(tokens, outputs, 0);
+    const bool widen = !p.e4m3 && linear_pair_form(tokens, outputs);
     const bool copy_x = !tma_rows(x, x_stride, tokens);
     const bool copy_w = !widen && !tma_rows(w, w_stride, outputs);
     const long long pitch = round16(width);

@@ -65,7 +65,7 @@ struct LinearPlan {
 };
 // whether the pair form runs this product; its int8 weights are then f16 rows in
 // the workspace (launch_stage_rows)
-bool linear_pair_form(long long tokens, long long outputs, int e4m3);
+bool linear_pair_form(long long tokens, long long outputs);
 // whether the form for few tokens runs it: any alignment, no tensor maps
 bool linear_thin_form(long long tokens);
 cudaError_t launch_linear_thin(const LinearParams& p, int num_sms, cudaStream_t stream);

@@ -89,3 +89,23 @@ def test_unaligned_operands(pkg, px, ox, pw, ow, q, k, n):
     got = pkg.linear_w8a8(_view(x, px, ox), _view(w, pw, ow), sx, sw)
     assert torch.equal(got, want)
     ref.check_linear(got, x, w, sx, sw)
+
+
+# one wave of 128 x 128 tiles (clusters split the reduction): more tokens than 512 over
+# few outputs, long and short reductions, as many tiles as there are SMs
+@pytest.mark.parametrize("m,n,k", [(600, 640, 8192), (1024, 1024, 8192), (700, 1279, 1283),
+                                   (2000, 640, 2560), (9500, 128, 1280), (19456, 100, 64),
+                                   (513, 1, 4096), (1024, 2432, 144)])
+@pytest.mark.parametrize("q", [I8, E4])
+@pytest.mark.parametrize("out_dtype,act", [(BF, "gelu"), (FF, "none")])
+def test_many_tokens_within_one_wave(pkg, m, n, k, q, out_dtype, act):
+    assert -(-m // 128) * -(-n // 128) <= 152
+    g = torch.Generator(device="cuda").manual_seed(m + n)
+    make = lambda r: (torch.randn(r, k, generator=g, device="cuda") * 40).clamp(-127, 127).to(q)  # noqa: E731
+    x, w = make(m), make(n)
+    sx = torch.rand(m, generator=g, device="cuda") * 0.02 + 0.001
+    sw = (torch.rand(n, generator=g, device="cuda") * 0.02 + 0.001) / math.sqrt(k)
+    b = torch.randn(n, generator=g, device="cuda")
+    got = pkg.linear_w8a8(x, w, sx, sw, bias=b, act=act, out_dtype=out_dtype)
+    ref.check_linear(got, x, w, sx, sw, b, act)
+    assert torch.equal(got, pkg.linear_w8a8(x, w, sx, sw, bias=b, act=act, out_dtype=out_dtype))
