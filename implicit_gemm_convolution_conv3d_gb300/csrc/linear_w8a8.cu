@@ -1327,14 +1327,15 @@ void plan_split(const LinearParams& p, const ClusterRoom& room, LinearPlan* r) {
 }  // namespace
 
 // The pair form's tile is 256 tokens high and its k-step costs the same at any
-// width, so it pays where the split form's 128 x 128 tiles would need a second
-// wave: 512 x 8192 x 2048 int8 24.5 us against 33.4, e4m3 11.0 against 21.6.
-// Within one wave the split form wins or is within 3% of it, the more the longer
-// the reduction that it splits and the fewer the tiles (pair, split): int8 1024 x
-// 2048 x 2048 19.3, 16.9; e4m3 600 x 640 x 8192 23.4, 10.2; 1024 x 1024 x 8192 23.6,
-// 14.8; 1024 x 2048 x 8192 23.8, 22.0; 1024 x 2048 x 2048 10.0, 9.9; 4000 x 512 x
-// 512 6.3, 6.5.  Up to 256 tokens the pair's second CTA would have nothing to do, and
-// int8 weights are not worth widening (256 x 8192 x 2048: 23.5 pair, 16.9 split).
+// width, so it pays where the split form's 128 x 128 tiles need a second wave
+// (us, split and pair: 300 x 8192 x 2048 int8 27.7, 24.8, e4m3 17.7, 10.5; 512 x
+// 8192 x 2048 28.6, 25.1 and 19.3, 10.8; 1280 x 2048 x 2048 27.8, 19.4 and 18.7,
+// 10.3).  Within one wave the split form wins or is within 5%, the more the longer
+// the reduction that it splits and the fewer the tiles (1024 x 2048 x 2048 14.5,
+// 19.2 and 9.8, 9.9; 600 x 640 x 8192 15.3, 44.0 and 10.3, 23.3; 1024 x 2048 x 8192
+// e4m3 22.1, 23.8; 4000 x 512 x 512 7.7, 10.2 and 6.5, 6.2).  Up to 256 tokens the
+// pair's second CTA would have nothing to do, and int8 weights are not worth
+// widening (256 x 8192 x 2048 14.5, 23.9 and 9.8, 9.9).
 // A wave is counted in sm_103a's 152 SMs, not the current device's: the workspace's
 // size follows from this rule, and its query asks no device.
 bool linear_pair_form(long long tokens, long long outputs) {
