@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(32 * kThinMaxWarps)
 // write, fence) that the other's hides.
 // What bounds it: latency (launch, first loads, the partials' way between CTAs, about
 // 4 us in all) and, for int8, the token converters (about 1200 cycles a k-step at
-// 128 tokens): 128 x 8192 x 2048 e4m3 8.4 us, int8 11.3 us, where the weights'
+// 128 tokens): 128 x 8192 x 2048 e4m3 8.4 us, int8 11.2 us, where the weights'
 // bytes take 2.5.
 struct SplitParams {
     LinearParams p;
@@ -669,10 +669,10 @@ __global__ void __launch_bounds__(kSplitThreads<E4M3>, 1)
 // too takes 128 (raw in and out, f16 in and out), and measured 1475 TFLOP/s at
 // 16384 x 8192 x 8192 against 1907; the launch moves 3 bytes per weight.
 // What bounds it now: the tensor pipe under the power cap at long reductions (1057
-// cycles a k-step of 1024; e4m3 3730 TFLOP/s), and between tiles the hand-over
+// cycles a k-step of 1024; e4m3 3600 to 3700 TFLOP/s), and between tiles the hand-over
 // of the accumulator (int8, about 2000 cycles a tile).  e4m3's k-steps fill the
 // shared memory's 128 bytes a cycle by themselves, so that at 1024-long reductions
-// the epilogue's staging and scales are what is added (2650 TFLOP/s at 16384 x
+// the epilogue's staging and scales are what is added (2840 TFLOP/s at 16384 x
 // 8192 x 1024).  Measured and not kept: outputs stored from the registers, a sector
 // per lane (0.88x there), tiles of 128 outputs (a k-step costs the same).
 //

@@ -4,7 +4,9 @@
 //   scale = max|v| / qmax;  q = nearest code of v / scale
 //
 // Read once, held in registers for the row's maximum, written as codes: 3 bytes an
-// element for 16-bit inputs, 5 gated.
+// element for 16-bit inputs, 5 gated.  Bound by memory and, with SiLU or GELU, by
+// issue slots: 16384 x 4096 gated silu 64 us (5.3 TB/s), 9500 x 5120 gelu 46 us, none
+// 26 us (5.6 TB/s).
 #include <cuda_runtime.h>
 
 #include "token_ops_internal.h"
