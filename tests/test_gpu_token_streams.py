@@ -75,3 +75,54 @@ def test_products_and_convolutions_side_by_side(pkg):
     torch.cuda.synchronize()
     for j, y in got:
         assert torch.equal(y, want[j]), j
+
+
+@pytest.mark.parametrize("q", [I8, E4])
+@pytest.mark.parametrize("tokens", [1, 7, 16, 40])
+def test_chains_over_the_same_buffers(pkg, q, tokens):
+    """Blocks back to back, in a graph, over the same buffers: kernels that start
+    while the ones before them run read what those write, not what they read there
+    a few kernels ago."""
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    width, inner = 256, 512
+    layers = []
+    for _ in range(6):
+        up, sup = pkg.act_quant(torch.randn(2 * inner, width, generator=g, device="cuda") / 16, qdtype=q)
+        down, sdown = pkg.act_quant(torch.randn(width, inner, generator=g, device="cuda") / 16, qdtype=q)
+        layers.append((up, sup, down, sdown))
+    new = lambda *s, t=torch.bfloat16: torch.empty(*s, dtype=t, device="cuda")   # noqa: E731
+    a, sa, b, sb = new(tokens, width, t=q), new(tokens, t=torch.float32), \
+        new(tokens, inner, t=q), new(tokens, t=torch.float32)
+    h, y, res = new(tokens, 2 * inner), new(tokens, width), new(tokens, width)
+
+    def chain(sync):
+        for up, sup, down, sdown in layers * 5:
+            pkg.rms_norm_quant(y, residual=res, out=a, scale_out=sa, residual_out=res)
+            sync()
+            pkg.linear_w8a8(a, up, sa, sup, out=h)
+            sync()
+            pkg.act_quant(h, "silu", gated=True, out=b, scale_out=sb)
+            sync()
+            pkg.linear_w8a8(b, down, sb, sdown, out=y)
+            sync()
+
+    start = torch.randn(tokens, width, generator=g, device="cuda").bfloat16()
+
+    def reset():
+        y.copy_(start)
+        res.copy_(start)
+
+    reset()
+    chain(torch.cuda.synchronize)
+    want = y.clone(), res.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(lambda: None)
+    for run in range(10):
+        reset()
+        if run % 2:
+            chain(lambda: None)
+        else:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[0]) and torch.equal(res, want[1]), run
