@@ -22,11 +22,13 @@ LIB = os.path.join(HERE, "libconv3d.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["conv_igemm.cu", "aux_kernels.cu", "conv3d_api.cu", "conv_noalloc.cu", "conv_fused_q.cu",
-           "token_norm.cu", "token_act.cu", "linear_w8a8.cu", "token_api.cu"]
+           "token_norm.cu", "token_act.cu", "linear_w8a8.cu", "token_api.cu",
+           "rotary.cu", "kv_cache.cu", "paged_attention.cu", "attention_api.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "tile_table.h", "kernel_common.cuh"]
 # the token operators' own
-TOKEN_HEADERS = ["token_common.cuh", "token_activations.cuh", "token_rows.cuh", "token_ops_internal.h"]
-PUBLIC_HEADERS = ["conv3d.h", "token_ops.h"]
+TOKEN_HEADERS = ["token_common.cuh", "token_activations.cuh", "token_rows.cuh", "token_ops_internal.h",
+                 "attention_internal.h", "paging.cuh"]
+PUBLIC_HEADERS = ["conv3d.h", "token_ops.h", "token_attention.h"]
 
 
 def nvcc_path() -> str:

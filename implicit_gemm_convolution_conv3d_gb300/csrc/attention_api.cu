@@ -1,0 +1,294 @@
+// attention_api.cu -- the C ABI of rotary positions, the key-value cache and
+// attention (declared in include/token_attention.h): argument checks and launches.
+// No allocation.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstdio>
+
+#include "attention_internal.h"
+#include "token_common.cuh"
+
+namespace c3d {
+
+namespace {
+
+constexpr int64_t kMaxDim = (1ll << 31) - 1;
+constexpr int64_t kMaxTokens = kMaxDim - 256;   // positions that kernels count in 32 bits
+
+int invalid(const char* what) {
+    set_last_error(what);
+    return CONV_ERR_INVALID;
+}
+
+int launched(cudaError_t e, const char* where) {
+    if (e == cudaSuccess) return CONV_OK;
+    char msg[160];
+    std::snprintf(msg, sizeof msg, "%s: %s", where, cudaGetErrorString(e));
+    set_last_error(msg);
+    return CONV_ERR_CUDA;
+}
+
+bool is_float_type(int t) { return t == CONV_DTYPE_BF16 || t == CONV_DTYPE_F16 || t == CONV_DTYPE_F32; }
+bool is_code_type(int t) { return t == CONV_DTYPE_INT8 || t == CONV_DTYPE_FP8_E4M3; }
+bool is_half_type(int t) { return t == CONV_DTYPE_BF16 || t == CONV_DTYPE_F16; }
+int size_of(int t) {
+    return t == CONV_DTYPE_F32 ? 4 : t == CONV_DTYPE_BF16 || t == CONV_DTYPE_F16 ? 2 : 1;
+}
+bool aligned_to(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) % bytes) == 0; }
+bool fits(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
+
+// heads of tokens: [tokens, heads, width] with strides in elements
+const char* bad_heads(const void* p, int64_t tok, int64_t head, int64_t tokens, int64_t heads,
+                      int64_t width, int elt) {
+    if (!p) return "null pointer";
+    if (!aligned_to(p, elt)) return "a pointer is not aligned to its element type";
+    if (tok < 0 || head < 0) return "strides must be 0 or more";
+    if (heads > 1 && head < width) return "a head stride is below the head's width";
+    if (tokens > 1 && tok < width) return "a token stride is below the head's width";
+    return nullptr;
+}
+bool words(const void* p, int64_t tok, int64_t head, int elt) {
+    return aligned_to(p, 16) && tok * elt % 16 == 0 && head * elt % 16 == 0;
+}
+
+const char* bad_cache(const kv_cache* c) {
+    if (!c || !c->k || !c->v) return "null pointer";
+    if (!is_code_type(c->dtype) && !is_half_type(c->dtype))
+        return "a cache must be INT8, FP8_E4M3, BF16 or F16";
+    if (!fits(c->pages, 1, kMaxDim) || !fits(c->heads, 1, 1 << 20) || !fits(c->page_size, 1, 1 << 30))
+        return "a cache must have pages, heads and tokens in a page";
+    if (!fits(c->width, 16, 256) || c->width % 16) return "a cache's width must be a multiple of 16 up to 256";
+    const int elt = size_of(c->dtype);
+    if (!aligned_to(c->k, 16) || !aligned_to(c->v, 16) || c->page_stride * elt % 16 ||
+        c->head_stride * elt % 16 || c->row_stride * elt % 16)
+        return "a cache's rows must be 16-byte aligned";
+    if (c->row_stride < c->width || c->head_stride < 0 || c->page_stride < 0)
+        return "a cache's row stride is below its width";
+    if (is_code_type(c->dtype)) {
+        if (!c->k_scale || !c->v_scale) return "an 8-bit cache needs scales";
+        if (!aligned_to(c->k_scale, 4) || !aligned_to(c->v_scale, 4))
+            return "a pointer is not aligned to its element type";
+        if (c->scale_page_stride < 0 || c->scale_head_stride < 0) return "strides must be 0 or more";
+    }
+    return nullptr;
+}
+
+const char* bad_table(const int32_t* table, int64_t stride, int64_t pages, int64_t sequences) {
+    if (!fits(pages, 0, kMaxDim)) return "a page table's width must be 0 or more, below 2^31";
+    if (pages && sequences && (!table || !aligned_to(table, 4))) return "null or unaligned page table";
+    if (sequences > 1 && stride < pages) return "a page table's stride is below its width";
+    return nullptr;
+}
+
+PageMap page_map(const kv_cache* c, const int32_t* table, int64_t stride, int64_t pages) {
+    PageMap m{};
+    const int elt = size_of(c->dtype);
+    m.table = table;
+    m.table_stride = stride;
+    m.capacity = pages > kMaxTokens / c->page_size ? kMaxTokens : pages * c->page_size;
+    m.pages = c->pages;
+    m.page_stride = c->page_stride * elt;
+    m.head_stride = c->head_stride * elt;
+    m.row_stride = c->row_stride * elt;
+    m.scale_page_stride = c->scale_page_stride;
+    m.scale_head_stride = c->scale_head_stride;
+    m.by_page = make_fastdiv(static_cast<uint32_t>(c->page_size));
+    return m;
+}
+
+int cache_rows(const kv_cache* cache, void* k, void* v, int dtype, int64_t token_stride,
+               int64_t head_stride, int64_t tokens, const int32_t* offsets, const int32_t* starts,
+               const int32_t* page_table, int64_t table_stride, int64_t table_pages, int64_t sequences,
+               bool write, cudaStream_t stream) {
+    const char* name = write ? "kv_cache_write launch" : "kv_cache_read launch";
+    if (!fits(tokens, 0, kMaxDim) || !fits(sequences, 0, kMaxDim))
+        return invalid("tokens and sequences must be 0 or more, below 2^31");
+    if (const char* e = bad_cache(cache)) return invalid(e);
+    if (!is_float_type(dtype)) return invalid("dtype must be BF16, F16 or F32");
+    if (write && is_half_type(cache->dtype) && dtype != cache->dtype)
+        return invalid("rows must have the type of an unquantised cache");
+    if (const char* e = bad_table(page_table, table_stride, table_pages, sequences)) return invalid(e);
+    if (write && !offsets && tokens != sequences)
+        return invalid("without offsets there is one token for each sequence");
+    if (tokens == 0 || sequences == 0) return CONV_OK;
+    if (write ? !starts : !offsets) return invalid("null pointer");
+    if (!aligned_to(offsets, 4) || !aligned_to(starts, 4))
+        return invalid("a pointer is not aligned to its element type");
+    for (const void* p : {static_cast<const void*>(k), static_cast<const void*>(v)})
+        if (const char* e = bad_heads(p, token_stride, head_stride, tokens, cache->heads, cache->width,
+                                      size_of(dtype)))
+            return invalid(e);
+    if (tokens > kMaxDim * 4 / cache->heads) {
+        set_last_error("more rows than the kernels count");
+        return CONV_ERR_UNSUPPORTED;
+    }
+    CacheParams p{};
+    p.k = static_cast<unsigned char*>(cache->k);
+    p.v = static_cast<unsigned char*>(cache->v);
+    p.k_scale = cache->k_scale;
+    p.v_scale = cache->v_scale;
+    p.map = page_map(cache, page_table, table_stride, table_pages);
+    p.rows_k = static_cast<unsigned char*>(k);
+    p.rows_v = static_cast<unsigned char*>(v);
+    p.tok_stride = token_stride;
+    p.head_stride = head_stride;
+    p.offsets = offsets;
+    p.starts = starts;
+    p.tokens = tokens;
+    p.sequences = static_cast<int>(sequences);
+    p.heads = static_cast<int>(cache->heads);
+    p.width = static_cast<int>(cache->width);
+    p.aligned = words(k, token_stride, head_stride, size_of(dtype)) &&
+                words(v, token_stride, head_stride, size_of(dtype));
+    return launched(write ? launch_cache_write(p, dtype, cache->dtype, stream)
+                          : launch_cache_read(p, dtype, cache->dtype, stream), name);
+}
+
+}  // namespace
+
+}  // namespace c3d
+
+using namespace c3d;
+
+extern "C" {
+
+int rotary_fwd(const void* x, int dtype, int64_t x_token_stride, int64_t x_head_stride,
+               const void* positions, int position_bytes, int axes, const int* axis,
+               const double* frequency, int pairs, int interleaved, int inverse, int64_t tokens,
+               int64_t heads, int64_t width, void* out, int64_t out_token_stride,
+               int64_t out_head_stride, cudaStream_t stream) {
+    if (!fits(tokens, 0, kMaxDim) || !fits(heads, 0, 1 << 20) || !fits(width, 1, 1 << 20))
+        return invalid("tokens must be 0 or more, below 2^31, heads and width up to 2^20");
+    if (!is_float_type(dtype)) return invalid("dtype must be BF16, F16 or F32");
+    if (position_bytes != 4 && position_bytes != 8) return invalid("positions must be int32 or int64");
+    if (axes < 1 || axes > ROTARY_MAX_AXES) return invalid("axes must be 1 to 8");
+    if (pairs < 1 || pairs > ROTARY_MAX_PAIRS || 2ll * pairs > width)
+        return invalid("pairs must be 1 to 128, and fit the width");
+    if (!axis || !frequency) return invalid("null pointer");
+    RotaryParams p{};
+    for (int i = 0; i < pairs; ++i) {
+        if (axis[i] < 0 || axis[i] >= axes) return invalid("a pair's axis is not one of the positions'");
+        if (!std::isfinite(frequency[i])) return invalid("a frequency is not finite");
+        double turn = frequency[i] * 0.15915494309189533577;   // 1 / (2 pi)
+        turn -= std::floor(turn);                              // whole turns of whole positions
+        p.turns[i] = turn >= 1.0 ? 0ull : static_cast<unsigned long long>(std::ldexp(turn, 64));
+        p.axis[i] = static_cast<unsigned char>(axis[i]);
+    }
+    if (tokens == 0 || heads == 0) return CONV_OK;
+    const int elt = size_of(dtype);
+    if (const char* e = bad_heads(x, x_token_stride, x_head_stride, tokens, heads, width, elt)) return invalid(e);
+    if (const char* e = bad_heads(out, out_token_stride, out_head_stride, tokens, heads, width, elt))
+        return invalid(e);
+    if (!positions || !aligned_to(positions, position_bytes)) return invalid("null or unaligned positions");
+    p.x = x;
+    p.out = out;
+    p.positions = positions;
+    p.x_tok = x_token_stride;
+    p.x_head = x_head_stride;
+    p.out_tok = out_token_stride;
+    p.out_head = out_head_stride;
+    p.tokens = tokens;
+    p.heads = static_cast<int>(heads);
+    p.width = static_cast<int>(width);
+    p.axes = axes;
+    p.pairs = pairs;
+    p.pos64 = position_bytes == 8;
+    p.interleaved = interleaved != 0;
+    p.inverse = inverse != 0;
+    p.copy_rest = out != x;
+    const bool aligned = words(x, x_token_stride, x_head_stride, elt) &&
+                         words(out, out_token_stride, out_head_stride, elt);
+    return launched(launch_rotary(p, dtype, aligned, stream), "rotary_fwd launch");
+}
+
+int kv_cache_write(const kv_cache* cache, const void* k, const void* v, int dtype,
+                   int64_t token_stride, int64_t head_stride, int64_t tokens,
+                   const int32_t* offsets, const int32_t* starts, const int32_t* page_table,
+                   int64_t table_stride, int64_t table_pages, int64_t sequences,
+                   cudaStream_t stream) {
+    return cache_rows(cache, const_cast<void*>(k), const_cast<void*>(v), dtype, token_stride, head_stride,
+                      tokens, offsets, starts, page_table, table_stride, table_pages, sequences, true, stream);
+}
+
+int kv_cache_read(const kv_cache* cache, void* k, void* v, int dtype, int64_t token_stride,
+                  int64_t head_stride, int64_t tokens, const int32_t* offsets,
+                  const int32_t* starts, const int32_t* page_table, int64_t table_stride,
+                  int64_t table_pages, int64_t sequences, cudaStream_t stream) {
+    return cache_rows(cache, k, v, dtype, token_stride, head_stride, tokens, offsets, starts, page_table,
+                      table_stride, table_pages, sequences, false, stream);
+}
+
+size_t paged_attention_workspace_size(int64_t sequences, int64_t heads, int64_t kv_heads,
+                                      int64_t width, int64_t page_size, int64_t table_pages) {
+    if (sequences < 1 || kv_heads < 1 || heads < kv_heads || heads % kv_heads || !fits(width, 16, 256) ||
+        page_size < 1 || table_pages < 0)
+        return 0;
+    LaunchLimits lim;
+    if (launch_limits(&lim)) return 0;
+    const int64_t capacity = table_pages > kMaxTokens / page_size ? kMaxTokens : table_pages * page_size;
+    const int grid = paged_grid(sequences, kv_heads, heads / kv_heads, static_cast<int>(width), capacity, lim.num_sms);
+    return paged_workspace(grid, static_cast<int>(width));
+}
+
+int paged_attention_fwd(const void* q, int q_dtype, int64_t q_sequence_stride,
+                        int64_t q_head_stride, const kv_cache* cache, const int32_t* page_table,
+                        int64_t table_stride, int64_t table_pages, const int32_t* lengths,
+                        const int32_t* prefix, const float* slopes, float scale, float cap,
+                        int64_t window, int64_t sequences, int64_t heads, void* out,
+                        int64_t out_sequence_stride, int64_t out_head_stride, void* workspace,
+                        size_t workspace_bytes, cudaStream_t stream) {
+    if (!fits(sequences, 0, kMaxDim)) return invalid("sequences must be 0 or more, below 2^31");
+    if (const char* e = bad_cache(cache)) return invalid(e);
+    if (!is_half_type(q_dtype)) return invalid("q_dtype must be BF16 or F16");
+    if (is_half_type(cache->dtype) && q_dtype != cache->dtype)
+        return invalid("q must have the type of an unquantised cache");
+    if (!fits(heads, 1, 1 << 20) || heads % cache->heads) return invalid("heads must be a multiple of the cache's");
+    if (!std::isfinite(scale)) return invalid("scale must be finite");
+    if (!(cap >= 0.0f) || !std::isfinite(cap)) return invalid("cap must be 0 or more");
+    if (window < 0) return invalid("window must be 0 or more");
+    if (const char* e = bad_table(page_table, table_stride, table_pages, sequences)) return invalid(e);
+    if (sequences == 0) return CONV_OK;
+    if (!lengths) return invalid("null pointer");
+    if (!aligned_to(lengths, 4) || !aligned_to(prefix, 4) || !aligned_to(slopes, 4))
+        return invalid("a pointer is not aligned to its element type");
+    if (const char* e = bad_heads(q, q_sequence_stride, q_head_stride, sequences, heads, cache->width, 2))
+        return invalid(e);
+    if (const char* e = bad_heads(out, out_sequence_stride, out_head_stride, sequences, heads, cache->width, 2))
+        return invalid(e);
+    LaunchLimits lim;
+    if (int rc = launch_limits(&lim)) return rc;
+    PagedParams p{};
+    p.q = static_cast<const unsigned char*>(q);
+    p.out = static_cast<unsigned char*>(out);
+    p.k = static_cast<const unsigned char*>(cache->k);
+    p.v = static_cast<const unsigned char*>(cache->v);
+    p.k_scale = cache->k_scale;
+    p.v_scale = cache->v_scale;
+    p.map = page_map(cache, page_table, table_stride, table_pages);
+    p.lengths = lengths;
+    p.prefix = prefix;
+    p.slopes = slopes;
+    p.q_seq = q_sequence_stride;
+    p.q_head = q_head_stride;
+    p.out_seq = out_sequence_stride;
+    p.out_head = out_head_stride;
+    p.scale = scale;
+    p.cap = cap;
+    p.window = static_cast<int>(window > kMaxTokens ? 0 : window);
+    p.sequences = static_cast<int>(sequences);
+    p.kv_heads = static_cast<int>(cache->heads);
+    p.group = static_cast<int>(heads / cache->heads);
+    p.width = static_cast<int>(cache->width);
+    p.grid = paged_grid(sequences, cache->heads, p.group, p.width, p.map.capacity, lim.num_sms);
+    const size_t need = paged_workspace(p.grid, p.width);
+    if (!workspace || workspace_bytes < need || !aligned_to(workspace, 16))
+        return invalid("paged_attention_fwd needs a 16-byte aligned workspace of "
+                       "paged_attention_workspace_size bytes");
+    p.jobs = static_cast<int4*>(workspace);
+    p.partial = reinterpret_cast<float*>(p.jobs + p.grid);
+    return launched(launch_paged(p, q_dtype, cache->dtype, stream), "paged_attention_fwd launch");
+}
+
+}  // extern "C"

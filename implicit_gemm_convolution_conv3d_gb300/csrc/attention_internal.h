@@ -1,0 +1,88 @@
+// attention_internal.h -- parameter blocks and launch entry points shared by
+// attention_api.cu and the kernels of rotary positions, the key-value cache and
+// attention.  Not part of the public ABI.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "token_attention.h"
+
+namespace c3d {
+
+struct RotaryParams {
+    const void* x;
+    void* out;
+    const void* positions;
+    long long x_tok, x_head, out_tok, out_head;
+    long long tokens;
+    int heads, width, axes, pairs;
+    int pos64, interleaved, inverse, copy_rest;
+    // turns of a pair for each unit of its position, as a fraction of 2^64: the
+    // product with a whole position, modulo 2^64, is the angle's fraction of a turn
+    unsigned long long turns[ROTARY_MAX_PAIRS];
+    unsigned char axis[ROTARY_MAX_PAIRS];
+};
+cudaError_t launch_rotary(const RotaryParams& p, int dtype, bool aligned, cudaStream_t stream);
+
+// where a sequence's tokens lie
+struct PageMap {
+    const int32_t* table;
+    long long table_stride;   // entries between sequences
+    long long capacity;       // tokens a row of the table can hold
+    long long pages;
+    long long page_stride, head_stride, row_stride;   // bytes
+    long long scale_page_stride, scale_head_stride;   // elements
+    FastDiv by_page;
+};
+
+struct CacheParams {
+    unsigned char* k;
+    unsigned char* v;
+    float* k_scale;   // NULL: unquantised
+    float* v_scale;
+    PageMap map;
+    unsigned char* rows_k;
+    unsigned char* rows_v;
+    long long tok_stride, head_stride;   // of the rows, elements
+    const int32_t* offsets;   // NULL: row s is sequence s (write only)
+    const int32_t* starts;    // NULL: 0 (read only)
+    long long tokens;
+    int sequences, heads, width;
+    int aligned;   // the rows take 16-byte accesses
+    FastDiv by_units;
+};
+cudaError_t launch_cache_write(const CacheParams& p, int row_dtype, int cache_dtype,
+                               cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheParams& p, int row_dtype, int cache_dtype,
+                              cudaStream_t stream);
+
+struct PagedParams {
+    const unsigned char* q;
+    unsigned char* out;
+    const unsigned char* k;
+    const unsigned char* v;
+    const float* k_scale;
+    const float* v_scale;
+    PageMap map;
+    const int32_t* lengths;
+    const int32_t* prefix;
+    const float* slopes;
+    long long q_seq, q_head, out_seq, out_head;   // elements
+    float scale, cap;
+    int window;            // 0: none
+    int sequences, kv_heads, group, width;
+    int blocks;            // groups of query heads that share a pass over a key head
+    int grid;
+    float* partial;        // workspace: see paged_attention.cu
+    int4* jobs;
+};
+// CTAs of the grid, and query heads of a pass (0: this width is not supported)
+int paged_grid(long long sequences, long long kv_heads, long long group, int width,
+               long long capacity, int num_sms);
+size_t paged_workspace(int grid, int width);
+cudaError_t launch_paged(const PagedParams& p, int q_dtype, int cache_dtype, cudaStream_t stream);
+
+}  // namespace c3d

@@ -1,0 +1,750 @@
+// paged_attention.cu -- attention of one new token of each sequence over a paged
+// cache of keys and values in 8 or 16 bits.
+//
+// For a sequence of n cached tokens and each of its query heads
+//     out = sum_t p_t v_t / sum_t p_t,   p_t = e^(s_t - m),   s_t = f(scale q.k_t)
+// in one pass over the tokens with a running maximum m.  Memory-bound: a key and a
+// value row are read once for the `group` query heads that share them.
+//
+// The work is every sequence's every key head, cut into units of 128 tokens and
+// dealt to the CTAs in equal runs, whatever the lengths are (they are on the device
+// only).  A run's ends may lie inside a key head: those CTAs leave (maximum, sum,
+// output) in the workspace and a second launch joins them in order, so results do
+// not depend on timing.  Within a CTA each warp takes every eighth block of 16 tokens
+// on its own, through its own ring of asynchronous copies: a thread copies exactly
+// the words that it will use itself, so the loop has no barrier.
+//
+// A block is two small matrix products per warp, tokens on the 16-row side:
+//     S^T[16 tokens, 8 heads] = K q^T,    O^T[width, 8 heads] += V^T P^T
+// The reduction index of the first and the rows of the second may be permuted at
+// will, so that a thread's operands are whole 16-byte words of the cache as it lies in
+// memory: no transposition anywhere but P's (one 8 x 8 exchange).  Memory-bound work
+// at 8 heads cannot fill a 128-row tensor-memory tile; the warp-level product reads
+// its operands from registers, where 8-bit codes have to be widened anyway.
+// int8 and e4m3 codes are exact in f16, as are queries times a power of two, so the
+// scores carry fp32 sums of exact products; keys' scales multiply the scores.
+// Values' scales go into the weights: p'_t = 2^(log2 p_t + log2 vscale_t - m'), m' the
+// running maximum of that exponent, so that the f16 weights of the product have all
+// of f16's 11 bits next to their maximum whatever the scales are; the sum of the
+// weights takes 2^(log2 p_t - m') in fp32.
+#include "attention_internal.h"
+#include "paging.cuh"
+#include "token_common.cuh"
+
+namespace c3d {
+
+namespace {
+
+constexpr int kUnit = 128;          // tokens that the work is dealt in
+constexpr int kBlock = 16;          // tokens of a warp's step
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTinyScale = 7.8886091e-31f;   // 2^-100
+
+template <int ES, int DP>
+struct Form {
+    static constexpr int kWarps = ES * DP >= 512 ? 4 : 8;
+    static constexpr int kStages = ES * DP == 64 ? 5 : 3;
+    static constexpr int kCtas = ES * DP <= 128 ? 2 : 1;
+    static constexpr int kKWords = DP * ES / 64;   // 16-byte words of a key row per thread
+    static constexpr int kVBytes = DP * ES / 8;    // bytes of a value row per thread
+    static constexpr int kVWord = kVBytes < 16 ? kVBytes : 16;
+    static constexpr int kVWords = kVBytes / kVWord;
+    static constexpr int kKSlots = 2 * kKWords, kVSlots = 4 * kVWords;
+    static constexpr uint32_t kVOff = kKSlots * 512u;
+    static constexpr uint32_t kScaleOff = kVOff + kVSlots * 32u * kVWord;
+    static constexpr uint32_t kStage = kScaleOff + (ES == 1 ? 128u : 0u);
+    static constexpr uint32_t kRing = kWarps * kStages * kStage;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+template <bool BF>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    if (BF)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// four codes as two f16 pairs
+template <bool E4>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    if (E4) {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
+    } else {
+        // 0x6400 + u is 1024 + u in f16, u = code + 128
+        const uint32_t u = w ^ 0x80808080u;
+        const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 off = __half2half2(__ushort_as_half(0x6480));   // 1152
+        const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+        const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+        lo = *reinterpret_cast<const uint32_t*>(&x);
+        hi = *reinterpret_cast<const uint32_t*>(&y);
+    }
+}
+
+template <int BYTES>
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[BYTES / 4]) {
+    if constexpr (BYTES == 16)
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(addr));
+    else
+        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+}
+
+// What a sequence's query sees: tokens [0, lead) and [from, length), as blocks of 16:
+// first those of the lead, then those from block `skip` on.
+struct Seen {
+    int length, lead, from;
+    int lead_blocks, skip, blocks, units;
+    bool bad;   // more tokens than the table holds
+};
+
+__device__ __forceinline__ Seen seen_by(const PagedParams& p, int s) {
+    Seen v;
+    const int n = p.lengths[s];
+    v.bad = n > p.map.capacity;
+    v.length = v.bad ? 1 : max(n, 0);
+    v.from = p.window > 0 ? max(0, v.length - p.window) : 0;
+    v.lead = p.prefix ? min(max(p.prefix[s], 0), v.length) : 0;
+    if (v.from == 0) v.lead = 0;
+    v.lead_blocks = (v.lead + kBlock - 1) / kBlock;
+    v.skip = max(v.from / kBlock, v.lead_blocks);
+    v.blocks = v.lead_blocks + max((v.length + kBlock - 1) / kBlock - v.skip, 0);
+    v.units = (v.blocks + kUnit / kBlock - 1) / (kUnit / kBlock);
+    return v;
+}
+
+// Units of all sequences (one key head), summed over the block, and where unit
+// `first` of the run falls: its sequence and the units before it.
+template <int THREADS>
+__device__ __forceinline__ long long sum_units(const PagedParams& p, long long* scratch) {
+    long long mine = 0;
+    for (int s = threadIdx.x; s < p.sequences; s += THREADS) mine += seen_by(p, s).units;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x / 32] = mine;
+    __syncthreads();
+    long long all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) all += scratch[w];
+    __syncthreads();
+    return all;
+}
+
+// The sequence s with before(s) <= unit < before(s) + units(s) (units of one key head
+// row: `per` = key heads x blocks times its units), found by the first warp.
+__device__ __forceinline__ void find_unit(const PagedParams& p, long long per, long long unit,
+                                          int* sequence, long long* before) {
+    const int lane = threadIdx.x & 31;
+    long long sum = 0;
+    for (int s0 = 0; s0 < p.sequences; s0 += 32) {
+        const int s = s0 + lane;
+        const long long n = s < p.sequences ? seen_by(p, s).units * per : 0;
+        long long run = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, run, d);
+            if (lane >= d) run += o;
+        }
+        const uint32_t over = __ballot_sync(0xffffffffu, sum + run > unit);
+        if (over) {
+            const int k = __ffs(over) - 1;
+            *sequence = s0 + k;
+            *before = sum + __shfl_sync(0xffffffffu, run - n, k);
+            return;
+        }
+        sum += __shfl_sync(0xffffffffu, run, 31);
+    }
+    *sequence = p.sequences;
+    *before = sum;
+}
+
+// A partial result in the workspace: [query][max, sum, out[DP]]
+template <int DP>
+constexpr int kPartial = 16 * (DP + 2);
+
+// KIND: kTokInt8, kTokE4m3, kTokBf16 or kTokF16; QBF: the queries are bf16; NG: groups
+// of eight query heads.
+template <int KIND, bool QBF, int DP, int NG>
+__global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 ? 2 : 1, DP>::kWarps,
+                                  NG == 1 ? Form<KIND == kTokBf16 || KIND == kTokF16 ? 2 : 1, DP>::kCtas : 1)
+    paged_kernel(const __grid_constant__ PagedParams p) {
+    constexpr bool kCodes = KIND == kTokInt8 || KIND == kTokE4m3;
+    constexpr int ES = kCodes ? 1 : 2;
+    using F = Form<ES, DP>;
+    constexpr int kWarps = F::kWarps;
+    constexpr bool kBf = KIND == kTokBf16;
+    constexpr int kSteps = DP / 16;   // k-steps of the first product
+    constexpr int kTiles = DP / 16;   // 16-row tiles of the second's output
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ long long s_scratch[kWarps];
+    __shared__ int s_seq;
+    __shared__ long long s_before;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
+    griddep_launch_dependents();
+    griddep_wait();
+
+    // this CTA's run of units
+    const long long per = static_cast<long long>(p.kv_heads) * p.blocks;
+    const long long total = sum_units<kWarps * 32>(p, s_scratch) * per;
+    const long long c = blockIdx.x, grid = gridDim.x;
+    // (equal runs; the first total % grid are one longer)
+    const long long share = total / grid, longer = total % grid;
+    long long unit = c * share + min(c, longer);
+    const long long end = unit + share + (c < longer ? 1 : 0);
+    if (threadIdx.x == 0) p.jobs[c] = make_int4(0, 0, 0, 0);
+    // sequences that see nothing get zeros
+    for (long long s = c; s < p.sequences; s += grid) {
+        if (seen_by(p, static_cast<int>(s)).units) continue;
+        for (int i = threadIdx.x; i < p.kv_heads * p.group * p.width; i += kWarps * 32) {
+            unsigned char* o = p.out + (s * p.out_seq + (i / p.width) * p.out_head + i % p.width) * 2;
+            *reinterpret_cast<uint16_t*>(o) = 0;
+        }
+    }
+    if (unit >= end) return;
+    if (warp == 0) {
+        int s;
+        long long b;
+        find_unit(p, per, unit, &s, &b);
+        if (lane == 0) {
+            s_seq = s;
+            s_before = b;
+        }
+    }
+    __syncthreads();
+    int seq = s_seq;
+    long long before = s_before;
+
+    const uint32_t ring = smem_u32(smem) + warp * (F::kStages * F::kStage);
+    const bool whole_blocks = p.map.by_page.d % kBlock == 0;
+    while (unit < end) {
+        const Seen see = seen_by(p, seq);
+        if (see.units == 0) {
+            ++seq;
+            continue;
+        }
+        const long long in = unit - before;
+        const int hb = static_cast<int>(in / see.units);
+        const int u0 = static_cast<int>(in - static_cast<long long>(hb) * see.units);
+        const int u1 = static_cast<int>(min(static_cast<long long>(see.units), u0 + (end - unit)));
+        const int head = hb / p.blocks, qb = hb - head * p.blocks;
+        const int heads_here = min(p.group - qb * 8 * NG, 8 * NG);
+        const int qh0 = head * p.group + qb * 8 * NG;
+
+        // ---- the queries: B operands of the first product
+        uint32_t bq[NG][kSteps][2];
+        float qscale[NG][2];   // of columns 2q, 2q + 1: multiplies the scores
+        float slope[NG][2];
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+            const int h = 8 * n + r;
+            const bool have = h < heads_here;
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) + seq * p.q_seq +
+                                  static_cast<long long>(qh0 + (have ? h : 0)) * p.q_head;
+            float top = 0.0f;
+#pragma unroll
+            for (int st = 0; st < kSteps; ++st) {
+                // the elements of this thread's word of the key rows
+                constexpr int E = 16 / ES;   // elements of a word
+                const int d = (st / (E / 4)) * 4 * E + q * E + (st % (E / 4)) * 4;
+                uint32_t w[2] = {0u, 0u};
+                if (have && d < p.width) {
+                    w[0] = src[d] | static_cast<uint32_t>(src[d + 1]) << 16;
+                    w[1] = src[d + 2] | static_cast<uint32_t>(src[d + 3]) << 16;
+                }
+                bq[n][st][0] = w[0];
+                bq[n][st][1] = w[1];
+                if (kCodes && QBF) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        top = fmaxf(top, fabsf(__uint_as_float(w[i] << 16)));
+                        top = fmaxf(top, fabsf(__uint_as_float(w[i] & 0xFFFF0000u)));
+                    }
+                }
+            }
+            float back = 1.0f;
+            if (kCodes && QBF) {
+                // bf16 queries to f16 by a power of two that brings the largest to [2^7, 2^8):
+                // exact but for elements below 2^-21 of it, off by 2^-33 of it at most
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int ex = static_cast<int>(__float_as_uint(top) >> 23);   // biased
+                const int sh = min(max(261 - ex, 1), 253);                     // 2^(sh - 127): ex -> 134
+                const float up = __uint_as_float(static_cast<uint32_t>(sh) << 23);
+                back = __uint_as_float(static_cast<uint32_t>(254 - sh) << 23);
+#pragma unroll
+                for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t w = bq[n][st][i];
+                        const __half2 x = __floats2half2_rn(__uint_as_float(w << 16) * up,
+                                                            __uint_as_float(w & 0xFFFF0000u) * up);
+                        bq[n][st][i] = *reinterpret_cast<const uint32_t*>(&x);
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                // row 2q + j of this group is held by lanes 4 * (2q + j) ...
+                qscale[n][j] = __shfl_sync(0xffffffffu, back, 4 * (2 * q + j)) * p.scale;
+                const int hh = 8 * n + 2 * q + j;
+                slope[n][j] = p.slopes && hh < heads_here ? p.slopes[qh0 + hh] * kLog2e : 0.0f;
+            }
+        }
+
+        float o[NG][kTiles][4];
+        float m[NG][2], l[NG][2];
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                m[n][j] = -INFINITY;
+                l[n][j] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[n][i][j] = 0.0f;
+        }
+
+        // ---- the warp's blocks
+        const int b0 = u0 * (kUnit / kBlock), b1 = min(u1 * (kUnit / kBlock), see.blocks);
+        auto token_of = [&](int b) {
+            return (b < see.lead_blocks ? b : b - see.lead_blocks + see.skip) * kBlock;
+        };
+        auto visible = [&](int t) { return t < see.length && (t >= see.from || t < see.lead); };
+        const long long head_bytes = head * p.map.head_stride;
+        auto issue = [&](int b, int stage) {
+            const uint32_t dst = ring + stage * F::kStage;
+            const int t0 = token_of(b);
+            long long base = 0;
+            bool ok = !see.bad;
+            if (whole_blocks) {
+                const uint32_t slot = fdiv(static_cast<uint32_t>(t0), p.map.by_page);
+                const long long page = p.map.table[seq * p.map.table_stride + slot];
+                ok = ok && page >= 0 && page < p.map.pages;
+                base = page * p.map.page_stride + head_bytes +
+                       static_cast<long long>(t0 - slot * p.map.by_page.d) * p.map.row_stride;
+            }
+            auto row = [&](int i, long long* at) {
+                const int t = t0 + i;
+                if (!ok || !visible(t)) return false;
+                if (whole_blocks) {
+                    *at = base + i * p.map.row_stride;
+                    return true;
+                }
+                long long sc;
+                return token_row(p.map, seq, t, head, at, &sc);
+            };
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                long long at = 0;
+                const bool have = row(r + 8 * i, &at);
+#pragma unroll
+                for (int w = 0; w < F::kKWords; ++w) {
+                    const int off = (q + 4 * w) * 16;
+                    const bool load = have && off < p.width * ES;
+                    cp_async<16>(dst + (i * F::kKWords + w) * 512u + lane * 16u, p.k + (load ? at + off : 0),
+                                 load ? 16u : 0u);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                long long at = 0;
+                const bool have = row(2 * q + (i & 1) + 8 * (i >> 1), &at);
+#pragma unroll
+                for (int w = 0; w < F::kVWords; ++w) {
+                    const int off = (r + 8 * w) * F::kVWord;
+                    const bool load = have && off < p.width * ES;
+                    cp_async<F::kVWord>(dst + F::kVOff + ((i * F::kVWords + w) * 32u + lane) * F::kVWord,
+                                        p.v + (load ? at + off : 0), load ? F::kVWord : 0u);
+                }
+            }
+            if (kCodes) {
+                // lanes 0-15: the keys' scales, 16-31: the values'; NaN where a page is missing
+                const int t = t0 + (lane & 15);
+                long long at = 0, sc = 0;
+                const bool want = visible(t) || see.bad;
+                const bool have = want && !see.bad && token_row(p.map, seq, t, head, &at, &sc);
+                const uint32_t to = dst + F::kScaleOff + lane * 4u;
+                if (want && !have)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(kNanBits) : "memory");
+                else
+                    cp_async<4>(to, (lane < 16 ? p.k_scale : p.v_scale) + sc, have ? 4u : 0u);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < F::kStages - 1; ++i) {
+            const int b = b0 + warp + i * kWarps;
+            if (b < b1) issue(b, i);
+            cp_async_commit();
+        }
+        int stage = 0;
+        for (int b = b0 + warp; b < b1; b += kWarps) {
+            {
+                const int nb = b + (F::kStages - 1) * kWarps;
+                int ns = stage + F::kStages - 1;
+                if (ns >= F::kStages) ns -= F::kStages;
+                if (nb < b1) issue(nb, ns);
+                cp_async_commit();
+            }
+            cp_async_wait<F::kStages - 1>();
+            __syncwarp();   // the scales come from other lanes' copies
+            const uint32_t src = ring + stage * F::kStage;
+            const int t0 = token_of(b);
+
+            // ---- scores
+            float sc[NG][4];
+#pragma unroll
+            for (int n = 0; n < NG; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sc[n][j] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < F::kKWords; ++w) {
+                uint32_t x[4], y[4];
+                lds<16>(src + w * 512u + lane * 16u, x);
+                lds<16>(src + (F::kKWords + w) * 512u + lane * 16u, y);
+                if constexpr (kCodes) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t x0, x1, y0, y1;
+                        widen4<KIND == kTokE4m3>(x[i], x0, x1);
+                        widen4<KIND == kTokE4m3>(y[i], y0, y1);
+#pragma unroll
+                        for (int n = 0; n < NG; ++n)
+                            mma16816<false>(sc[n], x0, y0, x1, y1, bq[n][4 * w + i][0], bq[n][4 * w + i][1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int n = 0; n < NG; ++n)
+                            mma16816<kBf>(sc[n], x[2 * i], y[2 * i], x[2 * i + 1], y[2 * i + 1],
+                                          bq[n][2 * w + i][0], bq[n][2 * w + i][1]);
+                }
+            }
+            // ---- weights: this thread's tokens are t0 + r and t0 + r + 8
+            float ks[2] = {1.0f, 1.0f}, lv[2] = {0.0f, 0.0f};
+            bool vis[2], none[2] = {false, false};   // none: values too small to count
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = t0 + r + 8 * i;
+                vis[i] = visible(t) || see.bad;
+                if (kCodes) {
+                    float vs;
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks[i]) : "r"(src + F::kScaleOff + (r + 8 * i) * 4u));
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs) : "r"(src + F::kScaleOff + (16 + r + 8 * i) * 4u));
+                    none[i] = vs < kTinyScale;
+                    lv[i] = none[i] ? -100.0f : lg2(vs);
+                } else if (vis[i]) {
+                    long long at, si;   // a missing page spoils the row
+                    if (see.bad || !token_row(p.map, seq, t, head, &at, &si)) ks[i] = __uint_as_float(kNanBits);
+                }
+            }
+            uint32_t bp[NG][2];
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+                float s2[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float s = sc[n][j] * (ks[j >> 1] * qscale[n][j & 1]);
+                    if (p.cap > 0.0f) {
+                        // cap * tanh(s / cap), tanh x = 1 - 2 / (1 + e^2x)
+                        const float e = ex2(s * (2.0f * kLog2e / p.cap));
+                        s = p.cap - 2.0f * p.cap * rcp_approx(1.0f + e);
+                    }
+                    s *= kLog2e;
+                    if (p.slopes)
+                        s -= slope[n][j & 1] * static_cast<float>(see.length - 1 - (t0 + r + 8 * (j >> 1)));
+                    s2[j] = vis[j >> 1] ? s : -INFINITY;
+                }
+                uint32_t w16[2];
+                float pw[4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float top = fmaxf(s2[j] + lv[0], s2[j + 2] + lv[1]);
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    const float now = fmaxf(m[n][j], top);
+                    const float base = now == -INFINITY ? 0.0f : now;
+                    const float fall = ex2(m[n][j] - base);
+                    m[n][j] = now;
+                    pw[j] = none[0] ? 0.0f : ex2(s2[j] + lv[0] - base);
+                    pw[j + 2] = none[1] ? 0.0f : ex2(s2[j + 2] + lv[1] - base);
+                    const float sum = kCodes ? ex2(s2[j] - base) + ex2(s2[j + 2] - base) : pw[j] + pw[j + 2];
+                    l[n][j] = l[n][j] * fall + sum;
+#pragma unroll
+                    for (int i = 0; i < kTiles; ++i) {
+                        o[n][i][j] *= fall;
+                        o[n][i][j + 2] *= fall;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (kBf) {
+                        w16[i] = pack_bf16x2(pw[2 * i], pw[2 * i + 1]);
+                    } else {
+                        const __half2 x = __floats2half2_rn(pw[2 * i], pw[2 * i + 1]);
+                        w16[i] = *reinterpret_cast<const uint32_t*>(&x);
+                    }
+                    bp[n][i] = transpose8x8(w16[i]);
+                }
+            }
+            // ---- output
+#pragma unroll
+            for (int w = 0; w < F::kVWords; ++w) {
+                uint32_t x[4][F::kVWord / 4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    lds<F::kVWord>(src + F::kVOff + ((i * F::kVWords + w) * 32u + lane) * F::kVWord, x[i]);
+#pragma unroll
+                for (int i = 0; i < F::kVWord / 4; ++i) {
+                    // pairs of tokens side by side, an element (and the next) each
+                    if constexpr (kCodes) {
+                        uint32_t a[2][4];   // [tokens of the half][elements 0..3]
+#pragma unroll
+                        for (int hlf = 0; hlf < 2; ++hlf) {
+                            const uint32_t lo = __byte_perm(x[2 * hlf][i], x[2 * hlf + 1][i], 0x5140);
+                            const uint32_t hi = __byte_perm(x[2 * hlf][i], x[2 * hlf + 1][i], 0x7362);
+                            widen4<KIND == kTokE4m3>(lo, a[hlf][0], a[hlf][1]);
+                            widen4<KIND == kTokE4m3>(hi, a[hlf][2], a[hlf][3]);
+                        }
+                        constexpr int kPer = F::kVWord / 2;   // tiles of a word
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int n = 0; n < NG; ++n)
+                                mma16816<false>(o[n][w * kPer + 2 * i + k], a[0][2 * k], a[0][2 * k + 1],
+                                                a[1][2 * k], a[1][2 * k + 1], bp[n][0], bp[n][1]);
+                    } else {
+                        const uint32_t a0 = __byte_perm(x[0][i], x[1][i], 0x5410);
+                        const uint32_t a1 = __byte_perm(x[0][i], x[1][i], 0x7632);
+                        const uint32_t a2 = __byte_perm(x[2][i], x[3][i], 0x5410);
+                        const uint32_t a3 = __byte_perm(x[2][i], x[3][i], 0x7632);
+#pragma unroll
+                        for (int n = 0; n < NG; ++n)
+                            mma16816<kBf>(o[n][w * 4 + i], a0, a1, a2, a3, bp[n][0], bp[n][1]);
+                    }
+                }
+            }
+            __syncwarp();   // all lanes have read this stage's scales
+            if (++stage == F::kStages) stage = 0;
+        }
+        cp_async_wait_all();
+
+        // ---- the warps' results meet in shared memory, over the rings
+        __syncthreads();
+        constexpr int kRow = DP + 4;
+        float* so = reinterpret_cast<float*>(smem);                   // [warp][query][kRow]
+        float* sm = so + kWarps * 8 * NG * kRow;                      // [warp][query][2]
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float sum = l[n][j];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                const int at = warp * 8 * NG + 8 * n + 2 * q + j;
+                if (r == 0) {
+                    sm[2 * at] = m[n][j];
+                    sm[2 * at + 1] = sum;
+                }
+                constexpr int E = F::kVWord / ES;   // elements of a word
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) {
+                    const int d = (2 * i / E) * 8 * E + r * E + (2 * i) % E;
+                    *reinterpret_cast<float2*>(so + at * kRow + d) = make_float2(o[n][i][j], o[n][i][j + 2]);
+                }
+            }
+        }
+        __syncthreads();
+        const bool whole = u0 == 0 && u1 == see.units;
+        const int slot = u0 == 0 ? 1 : 0;
+        float* part = p.partial + (c * 2 + slot) * kPartial<DP>;
+        for (int i = threadIdx.x; i < heads_here * (DP / 2); i += kWarps * 32) {
+            const int h = i / (DP / 2), d = 2 * (i - h * (DP / 2));
+            if (d >= p.width) continue;
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[2 * (w * 8 * NG + h)]);
+            const float base = top == -INFINITY ? 0.0f : top;
+            float x = 0.0f, y = 0.0f, sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const int at = w * 8 * NG + h;
+                const float f = ex2(sm[2 * at] - base);
+                const float2 v = *reinterpret_cast<const float2*>(so + at * kRow + d);
+                x += v.x * f;
+                y += v.y * f;
+                sum += sm[2 * at + 1] * f;
+            }
+            if (whole) {
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                uint32_t w;
+                if (QBF) {
+                    w = pack_bf16x2(x * inv, y * inv);
+                } else {
+                    const __half2 hv = __floats2half2_rn(x * inv, y * inv);
+                    w = *reinterpret_cast<const uint32_t*>(&hv);
+                }
+                uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) + seq * p.out_seq +
+                                static_cast<long long>(qh0 + h) * p.out_head + d;
+                dst[0] = static_cast<uint16_t>(w);
+                dst[1] = static_cast<uint16_t>(w >> 16);
+            } else {
+                if (d == 0) {
+                    part[h * (DP + 2)] = top;
+                    part[h * (DP + 2) + 1] = sum;
+                }
+                *reinterpret_cast<float2*>(part + h * (DP + 2) + 2 + d) = make_float2(x, y);
+            }
+        }
+        if (u0 == 0 && !whole && threadIdx.x == 0) {
+            // this CTA owns the join: how many CTAs share this key head
+            const long long last = before + static_cast<long long>(hb + 1) * see.units - 1;
+            const long long split = longer * (share + 1);
+            const long long c1 = last < split ? last / (share + 1) : longer + (last - split) / share;
+            p.jobs[c] = make_int4(seq, qh0, heads_here, static_cast<int>(c1 - c));
+        }
+        __syncthreads();
+        unit += u1 - u0;
+        if (u1 == see.units && hb + 1 == per) {
+            before += static_cast<long long>(see.units) * per;
+            ++seq;
+        }
+    }
+}
+
+// Joins the partial results of the key heads that several CTAs share, in the order of
+// their tokens: block c joins the one that begins in CTA c's run and goes on beyond it.
+template <bool QBF, int DP>
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int c = blockIdx.x;
+    const int4 job = p.jobs[c];
+    if (job.w == 0) return;
+    const float* first = p.partial + (static_cast<long long>(c) * 2 + 1) * kPartial<DP>;
+    const float* next = p.partial + static_cast<long long>(c + 1) * 2 * kPartial<DP>;
+    for (int i = threadIdx.x; i < job.z * (DP / 2); i += 256) {
+        const int h = i / (DP / 2), d = 2 * (i - h * (DP / 2));
+        if (d >= p.width) continue;
+        const int at = h * (DP + 2);
+        float top = first[at], sum = first[at + 1];
+        float2 v = *reinterpret_cast<const float2*>(first + at + 2 + d);
+        float x = v.x, y = v.y;
+#pragma unroll 4
+        for (int k = 0; k < job.w; ++k) {
+            const float* f = next + static_cast<long long>(k) * 2 * kPartial<DP> + at;
+            const float t = f[0];
+            v = *reinterpret_cast<const float2*>(f + 2 + d);
+            const float now = fmaxf(top, t), base = now == -INFINITY ? 0.0f : now;
+            const float fa = ex2(top - base), fb = ex2(t - base);
+            x = x * fa + v.x * fb;
+            y = y * fa + v.y * fb;
+            sum = sum * fa + f[1] * fb;
+            top = now;
+        }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        uint32_t w;
+        if (QBF) {
+            w = pack_bf16x2(x * inv, y * inv);
+        } else {
+            const __half2 hv = __floats2half2_rn(x * inv, y * inv);
+            w = *reinterpret_cast<const uint32_t*>(&hv);
+        }
+        uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) + job.x * p.out_seq +
+                        static_cast<long long>(job.y + h) * p.out_head + d;
+        dst[0] = static_cast<uint16_t>(w);
+        dst[1] = static_cast<uint16_t>(w >> 16);
+    }
+}
+
+int padded(int width) { return width <= 64 ? 64 : width <= 128 ? 128 : 256; }
+
+template <int KIND, bool QBF, int DP, int NG>
+cudaError_t run(const PagedParams& p, cudaStream_t stream) {
+    constexpr int ES = KIND == kTokBf16 || KIND == kTokF16 ? 2 : 1;
+    using F = Form<ES, DP>;
+    constexpr size_t meet = sizeof(float) * F::kWarps * 8 * NG * (DP + 4 + 2);
+    constexpr size_t smem = F::kRing > meet ? F::kRing : meet;
+    static std::atomic<int> slots[kMaxDevices];
+    cudaError_t e = ensure_dynamic_smem(paged_kernel<KIND, QBF, DP, NG>, smem, slots);
+    if (e != cudaSuccess) return e;
+    e = launch_ex(paged_kernel<KIND, QBF, DP, NG>, static_cast<unsigned>(p.grid), dim3(32 * F::kWarps), smem, 1,
+                  stream, p);
+    if (e != cudaSuccess || p.grid == 1) return e;
+    return launch_ex(paged_join_kernel<QBF, DP>, static_cast<unsigned>(p.grid), dim3(256), 0, 1, stream, p);
+}
+
+template <int KIND, bool QBF>
+cudaError_t by_width(const PagedParams& p, cudaStream_t stream) {
+    const bool two = p.group > 8;
+    if (p.width <= 64) return two ? run<KIND, QBF, 64, 2>(p, stream) : run<KIND, QBF, 64, 1>(p, stream);
+    if (p.width <= 128) return two ? run<KIND, QBF, 128, 2>(p, stream) : run<KIND, QBF, 128, 1>(p, stream);
+    return run<KIND, QBF, 256, 1>(p, stream);
+}
+
+}  // namespace
+
+// Query heads of one pass: 8, or 16 where more share a key head (256-wide heads have no
+// registers for 16).
+static int pass_heads(long long group, int width) { return group > 8 && width <= 128 ? 16 : 8; }
+
+int paged_grid(long long sequences, long long kv_heads, long long group, int width,
+               long long capacity, int num_sms) {
+    // two CTAs an SM, as far as there can be units
+    const long long blocks = (group + pass_heads(group, width) - 1) / pass_heads(group, width);
+    const long long units = (capacity + kUnit - 1) / kUnit;
+    const long long most = 2ll * num_sms;
+    if (units >= most) return static_cast<int>(most);
+    long long n = units * kv_heads * blocks;
+    n = n >= most || sequences >= most ? most : n * sequences;
+    return static_cast<int>(n < 1 ? 1 : n > most ? most : n);
+}
+
+size_t paged_workspace(int grid, int width) {
+    const size_t part = 16 * (static_cast<size_t>(padded(width)) + 2) * sizeof(float);
+    return static_cast<size_t>(grid) * (2 * part + sizeof(int4));
+}
+
+cudaError_t launch_paged(const PagedParams& p0, int q_dtype, int cache_dtype, cudaStream_t stream) {
+    PagedParams p = p0;
+    p.blocks = (p.group + pass_heads(p.group, p.width) - 1) / pass_heads(p.group, p.width);
+    const bool bf = q_dtype == kTokBf16;
+    if (cache_dtype == kTokInt8) return bf ? by_width<kTokInt8, true>(p, stream) : by_width<kTokInt8, false>(p, stream);
+    if (cache_dtype == kTokE4m3) return bf ? by_width<kTokE4m3, true>(p, stream) : by_width<kTokE4m3, false>(p, stream);
+    return bf ? by_width<kTokBf16, true>(p, stream) : by_width<kTokF16, false>(p, stream);
+}
+
+}  // namespace c3d

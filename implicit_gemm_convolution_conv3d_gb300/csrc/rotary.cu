@@ -1,0 +1,145 @@
+// rotary.cu -- rotary positions with several axes (time, height, width).
+//
+// A pair (a, b) of a head becomes (a cos t - b sin t, b cos t + a sin t) with
+// t = position[axis] * frequency.  The turn is taken in whole numbers: with
+// F = 2^64 * frequency / 2 pi, position * F modulo 2^64 is the angle's fraction
+// of a turn, exact for every 64-bit position (no argument reduction, and far
+// positions lose nothing), of which the sine and cosine are taken in fp32.
+// Memory-bound: every element is read and written once.  The sines of a block's
+// tokens are computed once into shared memory and shared by all heads; a thread
+// keeps those of its pairs in registers over the heads it rotates.
+#include "attention_internal.h"
+#include "token_common.cuh"
+
+namespace c3d {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTokens = 32;   // tokens of a block
+constexpr int kSinCos = 2048;    // (cos, sin) of a block
+
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) Vec {
+    T v[VEC];
+};
+
+// VEC elements a load: VEC (half) or VEC / 2 (interleaved) pairs of a unit; VEC == 1
+// is the form for any alignment (interleaved: two elements apart).
+template <typename T, int VEC, bool HALF>
+__global__ void __launch_bounds__(kThreads)
+    rotary_kernel(const __grid_constant__ RotaryParams p, int units, int lanes, int tokens_block) {
+    __shared__ float2 table[kSinCos];
+    griddep_launch_dependents();
+    griddep_wait();
+    constexpr int NP = HALF ? VEC : (VEC > 1 ? VEC / 2 : 1);   // pairs of a unit
+    const long long tok0 = static_cast<long long>(blockIdx.x) * tokens_block;
+    const int here = static_cast<int>(min(static_cast<long long>(tokens_block), p.tokens - tok0));
+    for (int i = threadIdx.x; i < here * p.pairs; i += kThreads) {
+        const int t = i / p.pairs, pair = i - t * p.pairs;
+        const long long at = (tok0 + t) * p.axes + p.axis[pair];
+        const long long pos = p.pos64 ? static_cast<const long long*>(p.positions)[at]
+                                      : static_cast<const int*>(p.positions)[at];
+        const long long turn = static_cast<long long>(static_cast<unsigned long long>(pos) * p.turns[pair]);
+        float s, c;
+        sincospif(__ll2float_rn(turn) * 1.0842021724855044e-19f, &s, &c);   // 2^-63: half turns
+        table[i] = make_float2(c, p.inverse ? -s : s);
+    }
+    __syncthreads();
+    // a thread: unit `u` of token `t`, heads h0, h0 + lanes, ...
+    const int u = threadIdx.x % units, rest = threadIdx.x / units;
+    const int h0 = rest % lanes, t = rest / lanes;
+    if (t >= here) return;
+    const T* x = static_cast<const T*>(p.x) + (tok0 + t) * p.x_tok;
+    T* out = static_cast<T*>(p.out) + (tok0 + t) * p.out_tok;
+    const int rot_units = p.pairs / NP;
+    using V = Vec<T, VEC>;
+    if (u >= rot_units) {   // elements that are not rotated
+        for (int e = 2 * p.pairs + (u - rot_units) * VEC; e < p.width; e += (units - rot_units) * VEC)
+            for (int h = h0; h < p.heads; h += lanes)
+                *reinterpret_cast<V*>(out + h * p.out_head + e) =
+                    *reinterpret_cast<const V*>(x + h * p.x_head + e);
+        return;
+    }
+    float c[NP], s[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const float2 cs = table[t * p.pairs + u * NP + i];
+        c[i] = cs.x;
+        s[i] = cs.y;
+    }
+    constexpr int kUnroll = 4;
+    const int ea = HALF ? u * VEC : u * 2 * NP;
+    const int eb = HALF ? ea + p.pairs : ea + 1;
+    constexpr bool kTwo = HALF || VEC == 1;   // two loads a unit
+    for (int h = h0; h < p.heads; h += kUnroll * lanes) {
+        V a[kUnroll], b[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            const int hh = h + i * lanes;
+            if (hh < p.heads) {
+                a[i] = *reinterpret_cast<const V*>(x + hh * p.x_head + ea);
+                if (kTwo) b[i] = *reinterpret_cast<const V*>(x + hh * p.x_head + eb);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            const int hh = h + i * lanes;
+            if (hh >= p.heads) break;
+            if (kTwo) {
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    const float va = to_f32(a[i].v[j]), vb = to_f32(b[i].v[j]);
+                    a[i].v[j] = from_f32<T>(va * c[j] - vb * s[j]);
+                    b[i].v[j] = from_f32<T>(vb * c[j] + va * s[j]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    const float va = to_f32(a[i].v[2 * j]), vb = to_f32(a[i].v[2 * j + 1]);
+                    a[i].v[2 * j] = from_f32<T>(va * c[j] - vb * s[j]);
+                    a[i].v[2 * j + 1] = from_f32<T>(vb * c[j] + va * s[j]);
+                }
+            }
+            *reinterpret_cast<V*>(out + hh * p.out_head + ea) = a[i];
+            if (kTwo) *reinterpret_cast<V*>(out + hh * p.out_head + eb) = b[i];
+        }
+    }
+}
+
+template <typename T, int VEC, bool HALF>
+cudaError_t run(const RotaryParams& p, cudaStream_t stream) {
+    constexpr int NP = HALF ? VEC : (VEC > 1 ? VEC / 2 : 1);
+    const int rest = p.copy_rest ? (p.width - 2 * p.pairs) / VEC : 0;
+    const int units = p.pairs / NP + (rest < kThreads / 2 ? rest : kThreads / 2);
+    // heads side by side: all, as far as a block reaches; fewer, so that a thread's
+    // sines serve up to four heads, where there are blocks enough without them
+    int lanes = kThreads / units < 1 ? 1 : kThreads / units;
+    if (lanes > p.heads) lanes = p.heads;
+    if (p.tokens * p.heads > 152 * 64 && lanes > (p.heads + 3) / 4) lanes = (p.heads + 3) / 4;
+    int toks = kThreads / (units * lanes);
+    if (toks > kMaxTokens) toks = kMaxTokens;
+    if (toks * p.pairs > kSinCos) toks = kSinCos / p.pairs;
+    const long long blocks = (p.tokens + toks - 1) / toks;
+    return launch_ex(rotary_kernel<T, VEC, HALF>, static_cast<unsigned>(blocks), dim3(kThreads), 0, 1,
+                     stream, p, units, lanes, toks);
+}
+
+template <typename T>
+cudaError_t by_form(const RotaryParams& p, bool aligned, cudaStream_t stream) {
+    constexpr int W = 16 / sizeof(T);
+    const int per = p.interleaved ? 2 * p.pairs : p.pairs;
+    if (aligned && per % W == 0 && (p.width - 2 * p.pairs) % W == 0)
+        return p.interleaved ? run<T, W, false>(p, stream) : run<T, W, true>(p, stream);
+    return p.interleaved ? run<T, 1, false>(p, stream) : run<T, 1, true>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(const RotaryParams& p, int dtype, bool aligned, cudaStream_t stream) {
+    if (dtype == kTokBf16) return by_form<__nv_bfloat16>(p, aligned, stream);
+    if (dtype == kTokF16) return by_form<__half>(p, aligned, stream);
+    return by_form<float>(p, aligned, stream);
+}
+
+}  // namespace c3d
