@@ -291,4 +291,85 @@ int paged_attention_fwd(const void* q, int q_dtype, int64_t q_sequence_stride,
     return launched(launch_paged(p, q_dtype, cache->dtype, stream), "paged_attention_fwd launch");
 }
 
+int packed_attention_fwd(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                         const void* k, const void* v, int64_t k_token_stride,
+                         int64_t k_head_stride, int dtype, const int32_t* q_offsets,
+                         const int32_t* k_offsets, int64_t documents, int64_t q_tokens,
+                         int64_t k_tokens, int64_t heads, int64_t kv_heads, int64_t width,
+                         int causal, int64_t window, const int32_t* prefix, const float* slopes,
+                         float scale, float cap, void* out, int64_t out_token_stride,
+                         int64_t out_head_stride, cudaStream_t stream) {
+    if (!fits(documents, 0, kMaxTokens) || !fits(q_tokens, 0, kMaxTokens) || !fits(k_tokens, 0, kMaxTokens))
+        return invalid("documents and tokens must be 0 or more, below 2^31 - 256");
+    if (!is_half_type(dtype)) return invalid("dtype must be BF16 or F16");
+    if (!fits(width, 8, 128) || width % 8) return invalid("width must be a multiple of 8 up to 128");
+    if (!fits(kv_heads, 1, 1 << 20) || !fits(heads, 1, 1 << 20) || heads % kv_heads)
+        return invalid("heads must be a multiple of kv_heads");
+    if (!std::isfinite(scale)) return invalid("scale must be finite");
+    if (!(cap >= 0.0f) || !std::isfinite(cap)) return invalid("cap must be 0 or more");
+    if (window < 0) return invalid("window must be 0 or more");
+    if (documents == 0 || q_tokens == 0) return CONV_OK;
+    if (!q_offsets || !k_offsets) return invalid("null pointer");
+    if (!aligned_to(q_offsets, 4) || !aligned_to(k_offsets, 4) || !aligned_to(prefix, 4) || !aligned_to(slopes, 4))
+        return invalid("a pointer is not aligned to its element type");
+    if (const char* e = bad_heads(q, q_token_stride, q_head_stride, q_tokens, heads, width, 2)) return invalid(e);
+    if (const char* e = bad_heads(out, out_token_stride, out_head_stride, q_tokens, heads, width, 2))
+        return invalid(e);
+    if (k_tokens)
+        for (const void* t : {k, v})
+            if (const char* e = bad_heads(t, k_token_stride, k_head_stride, k_tokens, kv_heads, width, 2))
+                return invalid(e);
+    // (one row or head has no stride to align)
+    const int64_t qt = q_tokens > 1 ? q_token_stride : heads * 128, qh = heads > 1 ? q_head_stride : 128;
+    const int64_t kt = k_tokens > 1 ? k_token_stride : kv_heads * 128, kh = kv_heads > 1 ? k_head_stride : 128;
+    if (!words(q, qt, qh, 2) || !words(k, kt, kh, 2) || !words(v, kt, kh, 2))
+        return invalid("q, k and v must be 16-byte aligned, and their strides multiples of 16 bytes");
+    if (q_tokens / 128 + documents > kMaxDim / heads) {
+        set_last_error("more tiles than the kernels count");
+        return CONV_ERR_UNSUPPORTED;
+    }
+    LaunchLimits lim;
+    int rc = launch_limits(&lim);
+    if (rc) return rc;
+    PackedParams p{};
+    p.q_offsets = q_offsets;
+    p.k_offsets = k_offsets;
+    p.prefix = prefix;
+    p.slopes = slopes;
+    p.out = static_cast<unsigned char*>(out);
+    p.q = static_cast<const unsigned char*>(q);
+    p.k = static_cast<const unsigned char*>(k);
+    p.v = static_cast<const unsigned char*>(v);
+    p.q_tok = q_token_stride;
+    p.q_head = q_head_stride;
+    p.k_tok = k_token_stride;
+    p.k_head = k_head_stride;
+    p.out_tok = out_token_stride;
+    p.out_head = out_head_stride;
+    p.q_tokens = q_tokens;
+    p.k_tokens = k_tokens;
+    p.documents = static_cast<int>(documents);
+    p.heads = static_cast<int>(heads);
+    p.kv_heads = static_cast<int>(kv_heads);
+    p.width = static_cast<int>(width);
+    p.causal = causal != 0;
+    p.window = static_cast<int>(window > kMaxTokens ? 0 : window);
+    p.scale = scale;
+    p.cap = cap;
+    p.out_aligned = words(out, out_token_stride, out_head_stride, 2);
+    p.status = lim.status;
+    p.wait_ns = lim.wait_ns;
+    PackedMaps maps{};
+    // (without a key nothing is loaded: the queries stand in for the maps' addresses)
+    const bool none = k_tokens == 0;
+    if ((rc = encode_heads(&maps.q, q, width, heads, q_tokens, qh * 2, qt * 2, 128))) return rc;
+    if ((rc = none ? encode_heads(&maps.k, q, width, heads, q_tokens, qh * 2, qt * 2, 128)
+                   : encode_heads(&maps.k, k, width, kv_heads, k_tokens, kh * 2, kt * 2, 128)))
+        return rc;
+    if ((rc = none ? encode_heads(&maps.v, q, width, heads, q_tokens, qh * 2, qt * 2, 128)
+                   : encode_heads(&maps.v, v, width, kv_heads, k_tokens, kh * 2, kt * 2, 128)))
+        return rc;
+    return launched(launch_packed(maps, p, dtype, lim.num_sms, stream), "packed_attention_fwd launch");
+}
+
 }  // extern "C"

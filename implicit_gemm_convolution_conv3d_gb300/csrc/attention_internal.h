@@ -85,4 +85,28 @@ int paged_grid(long long sequences, long long kv_heads, long long group, int wid
 size_t paged_workspace(int grid, int width);
 cudaError_t launch_paged(const PagedParams& p, int q_dtype, int cache_dtype, cudaStream_t stream);
 
+struct PackedParams {
+    const int32_t* q_offsets;
+    const int32_t* k_offsets;
+    const int32_t* prefix;
+    const float* slopes;
+    unsigned char* out;
+    const unsigned char* q;
+    const unsigned char* k;
+    const unsigned char* v;
+    long long q_tok, q_head, k_tok, k_head, out_tok, out_head;   // elements
+    long long q_tokens, k_tokens;
+    int documents, heads, kv_heads, width;
+    int causal, window;
+    float scale, cap;
+    int out_aligned;
+    int* status;
+    unsigned long long wait_ns;
+};
+struct PackedMaps {
+    CUtensorMap q, k, v;
+};
+cudaError_t launch_packed(const PackedMaps& maps, const PackedParams& p, int dtype, int num_sms,
+                          cudaStream_t stream);
+
 }  // namespace c3d

@@ -57,6 +57,9 @@ def _bind():
                                         f32, i64, i64, i64, vp, i64, i64, vp, ctypes.c_size_t, vp]
     lib.paged_attention_workspace_size.argtypes = [i64] * 6
     lib.paged_attention_workspace_size.restype = ctypes.c_size_t
+    lib.packed_attention_fwd.argtypes = [vp, i64, i64, vp, vp, i64, i64, i32, vp, vp, i64, i64,
+                                         i64, i64, i64, i64, i32, i64, vp, vp, f32, f32, vp, i64,
+                                         i64, vp]
     _fns = lib
     return lib
 
@@ -262,7 +265,8 @@ def kv_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torc
                   v_scale: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
                   k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
                   stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
-    """The cache's keys and values as packed rows [tokens, kv_heads, width]: rows ``offsets[s]`` .. ``offsets[s+1]`` are tokens
+    """The cache's keys and values as packed rows [tokens, kv_heads, width], in the form
+    that ``packed_attention`` takes: rows ``offsets[s]`` .. ``offsets[s+1]`` are tokens
     ``starts[s]`` (0 without starts), ... of sequence s.  Either ``tokens`` (the rows of
     new outputs, of type ``dtype``) or both outputs are given.  Rows in no sequence are
     not written; a token whose page is not in the table or the pool reads as NaN."""
@@ -345,4 +349,47 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream, q))
     if st:
         _check(st, "paged_attention_fwd")
+    return out
+
+
+def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor,
+                     k_offsets: Optional[torch.Tensor] = None, causal: bool = False,
+                     scale: Optional[float] = None, cap: float = 0.0, window: int = 0,
+                     prefix: Optional[torch.Tensor] = None, slopes: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Attention within documents packed one after the other: document s has queries
+    ``q[q_offsets[s]:q_offsets[s+1]]`` and keys and values
+    ``k[k_offsets[s]:k_offsets[s+1]]`` (int32 [documents + 1]; without ``k_offsets``
+    they are the same), its queries being its last tokens -> [tokens, heads, width].
+
+    A query at position i sees the keys j of its document with |i - j| < ``window``
+    (if > 0) and j <= i (if ``causal``), and those below ``prefix[s]``; a query that
+    sees nothing gets zeros.  Scores as in ``paged_attention``; the distance is
+    |i - j|.  q, k, v bf16 or fp16, 16-byte aligned, of up to 128 elements a head (a
+    multiple of 8); k and v have the same strides.  Rows in no document are not
+    written."""
+    lib = _fns or _bind()
+    nq, heads, width, qs, qh, code = _heads(q, _HALF, "q")
+    nk, kv_heads, kw, ks, kh, kc = _heads(k, _HALF, "k")
+    if _heads(v, _HALF, "v") != (nk, kv_heads, kw, ks, kh, kc):
+        raise ValueError("k and v must have the same shape, type and strides")
+    if kc != code or kw != width:
+        raise ValueError("q and k must have the same type and width")
+    if q_offsets.dim() != 1 or q_offsets.shape[0] < 1:
+        raise ValueError("q_offsets must be a vector of documents + 1")
+    n = q_offsets.shape[0] - 1
+    if k_offsets is None:
+        if nk != nq:
+            raise ValueError("without k_offsets q and k must have the same tokens")
+        k_offsets = q_offsets
+    out, os_, oh = _given(out, q, _HALF, code, stream)
+    st = lib.packed_attention_fwd(
+        q.data_ptr(), qs, qh, k.data_ptr(), v.data_ptr(), ks, kh, code,
+        _ints(q_offsets, n + 1, "q_offsets"), _ints(k_offsets, n + 1, "k_offsets"), n, nq, nk,
+        heads, kv_heads, width, bool(causal), window, _ints(prefix, n, "prefix"),
+        _slopes(slopes, heads), width ** -0.5 if scale is None else scale, cap, out.data_ptr(),
+        os_, oh, _stream(stream, q))
+    if st:
+        _check(st, "packed_attention_fwd")
     return out

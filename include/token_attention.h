@@ -1,8 +1,8 @@
 /*
  * token_attention.h -- C ABI of libconv3d.so for attention on the tokens of a
  * convolutional patch embedding, image and video: rotary positions with several
- * axes, a paged cache of keys and values in 8 (or 16) bits, and attention of one
- * new token over that cache.
+ * axes, a paged cache of keys and values in 8 (or 16) bits, attention of one new
+ * token over that cache, and attention within documents packed in one buffer.
  *
  *   rotary_fwd            (a, b) -> (a cos t - b sin t, b cos t + a sin t),
  *                         t = position[axis] * frequency, for pairs of a head
@@ -10,6 +10,7 @@
  *                         with a scale per token and head, or as they are
  *   kv_cache_read         the reverse, to packed rows
  *   paged_attention_fwd   softmax over a sequence's cached tokens, for its last one
+ *   packed_attention_fwd  softmax within each document, for all of its tokens
  *
  * Conventions (status codes, conv_last_error, streams and ownership are those of
  * conv3d.h; element types those of token_ops.h):
@@ -115,6 +116,24 @@ int paged_attention_fwd(const void* q, int q_dtype, int64_t q_sequence_stride,
  * arguments are invalid or there is nothing to do). */
 size_t paged_attention_workspace_size(int64_t sequences, int64_t heads, int64_t kv_heads,
                                       int64_t width, int64_t page_size, int64_t table_pages);
+
+/* Attention within documents packed one after the other.
+ *   q, out             [q_tokens, heads, width], k, v [k_tokens, kv_heads, width], all
+ *                      BF16 or all F16; width a multiple of 8 up to 128; k and v
+ *                      share their strides; q, k, v and their strides are multiples
+ *                      of 16 bytes
+ *   q_offsets, k_offsets  int32 [documents + 1]: document s has query rows
+ *                      q_offsets[s] .. q_offsets[s+1] and key rows k_offsets[s] ..;
+ *                      rows of out in no document are left as they are
+ *   causal, window, prefix (int32 [documents]), slopes (fp32 [heads]): as above */
+int packed_attention_fwd(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                         const void* k, const void* v, int64_t k_token_stride,
+                         int64_t k_head_stride, int dtype, const int32_t* q_offsets,
+                         const int32_t* k_offsets, int64_t documents, int64_t q_tokens,
+                         int64_t k_tokens, int64_t heads, int64_t kv_heads, int64_t width,
+                         int causal, int64_t window, const int32_t* prefix, const float* slopes,
+                         float scale, float cap, void* out, int64_t out_token_stride,
+                         int64_t out_head_stride, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
