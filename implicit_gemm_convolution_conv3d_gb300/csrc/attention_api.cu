@@ -246,7 +246,7 @@ int paged_attention_fwd(const void* q, int q_dtype, int64_t q_sequence_stride,
         return invalid("q must have the type of an unquantised cache");
     if (!fits(heads, 1, 1 << 20) || heads % cache->heads) return invalid("heads must be a multiple of the cache's");
     if (!std::isfinite(scale)) return invalid("scale must be finite");
-    if (!(cap >= 0.0f) || !std::isfinite(cap)) return invalid("cap must be 0 or more");
+    if (cap != 0.0f && (!(cap >= 1e-20f) || !std::isfinite(cap))) return invalid("cap must be 0, or 1e-20 or more");
     if (window < 0) return invalid("window must be 0 or more");
     if (const char* e = bad_table(page_table, table_stride, table_pages, sequences)) return invalid(e);
     if (sequences == 0) return CONV_OK;
@@ -306,7 +306,7 @@ int packed_attention_fwd(const void* q, int64_t q_token_stride, int64_t q_head_s
     if (!fits(kv_heads, 1, 1 << 20) || !fits(heads, 1, 1 << 20) || heads % kv_heads)
         return invalid("heads must be a multiple of kv_heads");
     if (!std::isfinite(scale)) return invalid("scale must be finite");
-    if (!(cap >= 0.0f) || !std::isfinite(cap)) return invalid("cap must be 0 or more");
+    if (cap != 0.0f && (!(cap >= 1e-20f) || !std::isfinite(cap))) return invalid("cap must be 0, or 1e-20 or more");
     if (window < 0) return invalid("window must be 0 or more");
     if (documents == 0 || q_tokens == 0) return CONV_OK;
     if (!q_offsets || !k_offsets) return invalid("null pointer");
@@ -350,13 +350,14 @@ int packed_attention_fwd(const void* q, int64_t q_token_stride, int64_t q_head_s
     p.k_tokens = k_tokens;
     p.documents = static_cast<int>(documents);
     p.heads = static_cast<int>(heads);
-    p.kv_heads = static_cast<int>(kv_heads);
+    p.group = static_cast<int>(heads / kv_heads);
     p.width = static_cast<int>(width);
     p.causal = causal != 0;
     p.window = static_cast<int>(window > kMaxTokens ? 0 : window);
     p.scale = scale;
     p.cap = cap;
-    p.out_aligned = words(out, out_token_stride, out_head_stride, 2);
+    p.out_aligned = !words(out, out_token_stride, out_head_stride, 2) ? 0
+                    : aligned_to(out, 32) && out_token_stride % 16 == 0 && out_head_stride % 16 == 0 ? 32 : 16;
     p.status = lim.status;
     p.wait_ns = lim.wait_ns;
     PackedMaps maps{};

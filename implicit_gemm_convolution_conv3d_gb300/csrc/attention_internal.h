@@ -96,10 +96,10 @@ struct PackedParams {
     const unsigned char* v;
     long long q_tok, q_head, k_tok, k_head, out_tok, out_head;   // elements
     long long q_tokens, k_tokens;
-    int documents, heads, kv_heads, width;
+    int documents, heads, group, width;   // group: query heads of a key head
     int causal, window;
     float scale, cap;
-    int out_aligned;
+    int out_aligned;   // bytes that rows of out are aligned to: 32, 16 or fewer (0)
     int* status;
     unsigned long long wait_ns;
 };

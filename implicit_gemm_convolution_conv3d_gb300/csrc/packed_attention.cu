@@ -3,15 +3,17 @@
 // For each document, head and query i:  out = sum_j p_ij v_j / sum_j p_ij,
 // p_ij = e^(s_ij - m_i), in one pass over the keys i sees with a running maximum.
 //
-// A CTA takes one head of NQ tiles of 128 query rows and walks the 128-key tiles that
-// any of them sees.  Both products run on the tensor cores, with everything between
+// A job is one head of NQ tiles of 128 query rows; it walks the 128-key tiles that any
+// of them sees.  CTAs stay on their SM and take every grid-th job.  Both products run on the tensor cores, with everything between
 // them in tensor memory: S = Q K^T (128 x 128 fp32) is read by the four warps of its
 // tile, a row per thread, so that a row's maximum and sum need no exchange; the weights
 // go back as 16-bit words over S, where the second product O += P V takes them as its
 // first operand.  V is read as it lies in memory (its rows are the reduction).
-//   warp 0      TMA producer: Q, then K and V tiles in a ring
+//   warp 0      finds the jobs; TMA producer: Q, then K and V tiles in a ring
 //   warp 1      tensor memory, MMA issuer
 //   warps 4-7   the first tile's rows: softmax, then the output; 8-11 the second's
+// The next job's loads and first scores run under the last softmax and the output of the
+// one before.
 // With two tiles the tensor cores work on one while the other's weights are computed,
 // and K and V are read once for 256 rows; with one tile two CTAs share an SM instead.
 // The maximum that weights are relative to follows the running one only when that has
@@ -51,7 +53,7 @@ __device__ __forceinline__ float elem(const unsigned char* base, long long i) {
     return __half2float(reinterpret_cast<const __half*>(base)[i]);
 }
 
-// A CTA's work: 128 * NQ rows from `row0` of a document, for one head.
+// 128 * NQ rows from `row0` of a document, for one head (negative: no more jobs).
 struct Job {
     int row0, rows;          // of the document; rows: the document's queries
     int keys, shift;         // its keys; position of row r: r + shift
@@ -100,6 +102,51 @@ __device__ bool finite_row(const unsigned char* v, long long at, int width) {
     return true;
 }
 
+// Two values a register pair: one instruction each
+__device__ __forceinline__ uint64_t two(uint32_t a, uint32_t b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t two(float v) { return two(__float_as_uint(v), __float_as_uint(v)); }
+__device__ __forceinline__ void split(uint64_t v, uint32_t& a, uint32_t& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// The largest of 128 values, or of their magnitudes
+template <bool ABS>
+__device__ __forceinline__ float max128(const uint32_t (&s)[4][32]) {
+    float t[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        auto v = [&](int e) { return ABS ? fabsf(__uint_as_float(s[h][e])) : __uint_as_float(s[h][e]); };
+        t[h] = fmaxf(v(0), v(1));
+#pragma unroll
+        for (int e = 2; e < 32; e += 2) t[h] = max3(t[h], v(e), v(e + 1));
+    }
+    return fmaxf(max3(t[0], t[1], t[2]), t[3]);
+}
+
 // A row's score at a key, in powers of two
 __device__ __forceinline__ float shaped(const PackedParams& p, float dot, int i, int j, float slope2) {
     float s = dot * p.scale;
@@ -120,8 +167,8 @@ __device__ __forceinline__ RowMask row_mask(const PackedParams& p, const Job& j,
 // tile that was multiplied (weight 0) has a value that is not finite.  Then the row is
 // computed again, over what it sees alone.
 template <bool BF>
-__device__ __noinline__ void redo_row(const PackedParams& p, const Job& job, const Range& tile_range, int row) {
-    const int kv = static_cast<int>(static_cast<long long>(job.head) * p.kv_heads / p.heads);
+__device__ __forceinline__ void redo_row(const PackedParams& p, const Job& job, const Range& tile_range, int row) {
+    const int kv = job.head / p.group;
     const RowMask m = row_mask(p, job, row);
     const long long vbase = job.k0 * p.k_tok + static_cast<long long>(kv) * p.k_head;
     bool spoiled = false;
@@ -165,91 +212,77 @@ __device__ __noinline__ void redo_row(const PackedParams& p, const Job& job, con
     }
 }
 
+// Bounded waits without a call (see wait_bar and drain_wait): the compiler makes none from
+// warps that have registers of a number of their own.  A role sleeps in hardware between
+// looks, so that its polling leaves the issue slots to the others.
+__device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                          int* status, unsigned long long limit_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    const long long limit = static_cast<long long>(limit_ns > (1ull << 61) ? (1ull << 61) : limit_ns) * 2;
+    while (true) {
+        if (*abort_flag) return false;
+        if (clock64() - t0 > limit) {
+            *abort_flag = 1u;
+            atomicExch(status, kStatusTimeout);
+            return false;
+        }
+        if (mbar_try_wait_for(bar, parity, 20000u)) return true;
+    }
+}
+__device__ __forceinline__ void drain_here(uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 <= kDrainNs) {
+    }
+}
+// the last load of each slot of a ring
+__device__ __forceinline__ void drain_slots(uint32_t full0, uint32_t issued, uint32_t slots) {
+    for (uint32_t n = issued > slots ? issued - slots : 0u; n < issued; ++n)
+        drain_here(full0 + 8 * (n % slots), (n / slots) & 1u);
+}
+
 template <int NQ>
 constexpr int kThreads = 128 + 128 * NQ;
 
-// NQ: query tiles of a CTA.  MOD: scores are capped, biased or scaled by a number that
-// is not positive (else the scale goes into the exponent's one multiply-add).
-template <bool BF, int NQ, bool MOD>
+// What scores go through beside the scale: nothing (the scale then goes into the
+// exponent's one multiply-add), the cap, the distance (or a scale that is not positive).
+constexpr int kCap = 1, kFar = 2;
+
+// NQ: query tiles of a job.
+template <bool BF, int NQ, int MOD>
 __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
     packed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map, const __grid_constant__ PackedParams p,
-                  const int stages) {
+                  const int stages, const int q_bufs) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     const int boxes = (p.width + 63) / 64;
     const uint32_t tile_bytes = boxes * kBoxBytes;
-    const uint32_t q_smem = base, ring = base + NQ * tile_bytes;
+    const uint32_t q_smem = base, ring = base + q_bufs * NQ * tile_bytes;
     const uint32_t bars = ring + stages * tile_bytes;
-    const uint32_t full0 = bars, empty0 = full0 + 8u * kMaxStages, q_full = empty0 + 8u * kMaxStages;
-    const uint32_t s_full0 = q_full + 8u, p_full0 = s_full0 + 16u, o_done0 = p_full0 + 16u;
+    const uint32_t full0 = bars, empty0 = full0 + 8u * kMaxStages;
+    const uint32_t q_full0 = empty0 + 8u * kMaxStages, q_empty0 = q_full0 + 16u;
+    const uint32_t job_full0 = q_empty0 + 16u, job_empty0 = job_full0 + 16u;
+    const uint32_t s_full0 = job_empty0 + 16u, p_full0 = s_full0 + 16u, o_done0 = p_full0 + 16u;
     const uint32_t tail_bar = o_done0 + 16u, drain_bar = tail_bar + 8u;
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem_raw + (drain_bar + 8u - raw));
-    // misc[0] TMEM base, [1] abort flag, [2] loads issued, [3] whether there is work; then the job
+    // misc[0] TMEM base, [1] abort flag, [2] ring loads issued, [3] Q loads issued, [4] whether a
+    // last tile's values are on their way (1 + its phase); then two jobs
     volatile uint32_t* abort_flag = misc + 1;
-    Job* shared_job = reinterpret_cast<Job*>(misc + 4);
+    Job* jobs = reinterpret_cast<Job*>(misc + 6);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    griddep_launch_dependents();
-    griddep_wait();
-    if (warp == 0) {
-        // which document's rows this CTA takes: 128 documents a step, four a lane
-        const int head = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.heads));
-        const long long want = blockIdx.x / static_cast<unsigned>(p.heads);
-        long long before = 0;
-        bool found = false;
-        for (int s0 = 0; s0 < p.documents && !found; s0 += 128) {
-            int off[5];
-#pragma unroll
-            for (int i = 0; i < 5; ++i) {
-                const int s = min(s0 + 4 * lane + i, p.documents);
-                off[i] = static_cast<int>(min(max(static_cast<long long>(p.q_offsets[s]), 0ll), p.q_tokens));
-            }
-            int n[4], mine = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                n[i] = (max(off[i + 1] - off[i], 0) + NQ * kRows - 1) / (NQ * kRows);
-                mine += n[i];
-            }
-            int run = mine;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, run, d);
-                if (lane >= d) run += o;
-            }
-            const uint32_t over = __ballot_sync(0xffffffffu, before + run > want);
-            if (over) {
-                found = true;
-                if (lane == __ffs(over) - 1) {
-                    int at = static_cast<int>(want - before) - (run - mine), i = 0;
-                    while (at >= n[i]) at -= n[i++];
-                    const int s = s0 + 4 * lane + i;
-                    Job j;
-                    j.rows = off[i + 1] - off[i];
-                    j.row0 = (p.causal ? n[i] - 1 - at : at) * NQ * kRows;   // the longest first
-                    const long long kb = min(max(static_cast<long long>(p.k_offsets[s]), 0ll), p.k_tokens);
-                    const long long ke = min(max(static_cast<long long>(p.k_offsets[s + 1]), kb), p.k_tokens);
-                    j.keys = static_cast<int>(ke - kb);
-                    j.shift = j.keys - j.rows;
-                    j.prefix = p.prefix ? min(max(p.prefix[s], 0), j.keys) : 0;
-                    j.q0 = off[i];
-                    j.k0 = kb;
-                    j.head = head;
-                    *shared_job = j;
-                }
-            }
-            before += __shfl_sync(0xffffffffu, run, 31);
-        }
-        if (lane == 0) misc[3] = found;
-    }
-    if (threadIdx.x == 32) {
+    if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) {
             mbar_init(full0 + 8 * i, 1);
             mbar_init(empty0 + 8 * i, 1);
         }
-        mbar_init(q_full, 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full0 + 8 * i, 1);
+            mbar_init(q_empty0 + 8 * i, 1);
+            mbar_init(job_full0 + 8 * i, 1);
+            mbar_init(job_empty0 + 8 * i, 1 + 4 * NQ);
             mbar_init(s_full0 + 8 * i, 1);
             mbar_init(p_full0 + 8 * i, 4);
             mbar_init(o_done0 + 8 * i, 1);
@@ -258,13 +291,13 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
         mbar_init(drain_bar, 1);
         misc[1] = 0u;
         misc[2] = 0u;
+        misc[3] = 0u;
+        misc[4] = 0u;
         fence_mbar_init();
         prefetch_tmap(&q_map);
         prefetch_tmap(&k_map);
         prefetch_tmap(&v_map);
     }
-    __syncthreads();
-    if (!misc[3]) return;   // behind the last document
     if (warp == 1) {
         tmem_alloc(smem_u32(misc), NQ == 2 ? 512 : 256);
         tmem_relinquish();
@@ -273,66 +306,157 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc[0];
-    const Job job = *shared_job;
     const uint32_t o_pitch = boxes * 64u;
-    const int row_end = min(job.row0 + NQ * kRows, job.rows);
-    const Tiles tl = tiles_of(range_of(p, job, job.row0, row_end));
-    Range part[NQ];
-#pragma unroll
-    for (int i = 0; i < NQ; ++i)
-        part[i] = range_of(p, job, job.row0 + i * kRows, min(job.row0 + (i + 1) * kRows, job.rows));
+    griddep_launch_dependents();
+    griddep_wait();
 
-    if (warp == 0) {
-        const int kv = static_cast<int>(static_cast<long long>(job.head) * p.kv_heads / p.heads);
-        int st = 0;
-        uint32_t ph = 0, issued = 0;
-        bool ok = true;
-        if (tl.count > 0 && lane == 0) {
-            mbar_arrive_expect_tx(q_full, NQ * tile_bytes);
-            for (int i = 0; i < NQ; ++i)
-                for (int b = 0; b < boxes; ++b)
-                    tma_load_3d(q_smem + i * tile_bytes + b * kBoxBytes, &q_map, q_full, b * 64, job.head,
-                                static_cast<int>(job.q0 + job.row0 + i * kRows));
-        }
-        for (int n = 0; n < 2 * tl.count && ok; ++n) {
-            const bool value = n & 1;
-            const int t0 = tl.at(n >> 1);
-            // the keys of a tile behind the document's last are other documents': their scores
-            // are replaced, their values (times a weight of 0) have to be finite
-            const bool tail = value && t0 + kRows > job.keys;
-            ok = wait_bar(empty0 + 8 * st, ph ^ 1u, abort_flag, p.status, p.wait_ns);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            const uint32_t dst = ring + st * tile_bytes, bar = tail ? tail_bar : full0 + 8 * st;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar, tile_bytes);
-                for (int b = 0; b < boxes; ++b)
-                    tma_load_3d(dst + b * kBoxBytes, value ? &v_map : &k_map, bar, b * 64, kv,
-                                static_cast<int>(job.k0 + t0));
-            }
-            if (tail) {
-                ok = wait_bar(tail_bar, 0, abort_flag, p.status, p.wait_ns);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    drain_wait(tail_bar, 0);
-                    break;
+    // the tiles of a job, and what each of its query tiles sees
+    auto parts_of = [&](const Job& job, Range (&part)[NQ]) {
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+            part[i] = range_of(p, job, job.row0 + i * kRows, min(job.row0 + (i + 1) * kRows, job.rows));
+        return tiles_of(range_of(p, job, job.row0, min(job.row0 + NQ * kRows, job.rows)));
+    };
+
+    if (warp < 4) {
+        set_max_regs_dec<NQ == 2 ? 72 : 56>();
+        if (warp == 0) {
+            // documents are looked through 128 at a time, four a lane, and never twice
+            int s0 = -128, n[4] = {0, 0, 0, 0}, off[5] = {0, 0, 0, 0, 0}, mine = 0, run = 0;
+            long long before = 0;
+            int all = 0;   // jobs (of one head) of these 128
+            int st = 0;
+            uint32_t ph = 0, issued = 0, q_issued = 0, tails = 0;
+            bool ok = true;
+            for (uint32_t k = 0; ok; ++k) {
+                const uint32_t at = blockIdx.x + k * gridDim.x;
+                const uint32_t want = at / static_cast<uint32_t>(p.heads);
+                while (before + all <= want && s0 < p.documents) {
+                    before += all;
+                    s0 += 128;
+#pragma unroll
+                    for (int i = 0; i < 5; ++i) {
+                        const int s = min(s0 + 4 * lane + i, p.documents);
+                        off[i] = static_cast<int>(min(max(static_cast<long long>(p.q_offsets[s]), 0ll), p.q_tokens));
+                    }
+                    mine = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        n[i] = (max(off[i + 1] - off[i], 0) + NQ * kRows - 1) / (NQ * kRows);
+                        mine += n[i];
+                    }
+                    run = mine;
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int o = __shfl_up_sync(0xffffffffu, run, d);
+                        if (lane >= d) run += o;
+                    }
+                    all = __shfl_sync(0xffffffffu, run, 31);
                 }
-                const int first = job.keys - t0;
-                for (int i = first * 8 + lane; i < kRows * 8; i += 32)
-                    for (int b = 0; b < boxes; ++b)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + b * kBoxBytes + i * 16u), "r"(0u)
-                                     : "memory");
-                fence_proxy_async_smem();
+                const bool more = before + all > want;
+                const uint32_t slot = k & 1u, jph = (k >> 1) & 1u;
+                ok = wait_role(job_empty0 + 8 * slot, jph ^ 1u, abort_flag, p.status, p.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (more) {
+                    const int in = static_cast<int>(want - before);
+                    const int src = __ffs(__ballot_sync(0xffffffffu, run > in)) - 1;
+                    if (lane == src) {
+                        // which of the lane's four documents, and which of its tiles
+                        int t = in - (run - mine), s = s0 + 4 * lane, count = n[0], q0 = off[0], q1 = off[1];
+#pragma unroll
+                        for (int i = 1; i < 4; ++i)
+                            if (t >= count) {
+                                t -= count;
+                                count = n[i];
+                                q0 = off[i];
+                                q1 = off[i + 1];
+                                ++s;
+                            } else {
+                                break;
+                            }
+                        Job job;
+                        job.rows = q1 - q0;
+                        job.row0 = (p.causal ? count - 1 - t : t) * NQ * kRows;   // the longest first
+                        const long long kb = min(max(static_cast<long long>(p.k_offsets[s]), 0ll), p.k_tokens);
+                        const long long ke = min(max(static_cast<long long>(p.k_offsets[s + 1]), kb), p.k_tokens);
+                        job.keys = static_cast<int>(ke - kb);
+                        job.shift = job.keys - job.rows;
+                        job.prefix = p.prefix ? min(max(p.prefix[s], 0), job.keys) : 0;
+                        job.q0 = q0;
+                        job.k0 = kb;
+                        job.head = static_cast<int>(at - want * static_cast<uint32_t>(p.heads));
+                        jobs[slot] = job;
+                    }
+                } else if (lane == 0) {
+                    jobs[slot].head = -1;
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(full0 + 8 * st);
+                if (lane == 0) mbar_arrive(job_full0 + 8 * slot);
+                if (!more) break;
+                const Job job = jobs[slot];
+                Range part[NQ];
+                const Tiles tl = parts_of(job, part);
+                if (tl.count == 0) continue;
+                const int kv = job.head / p.group;
+                const uint32_t qb = q_issued % q_bufs, qph = (q_issued / q_bufs) & 1u;
+                ok = wait_role(q_empty0 + 8 * qb, qph ^ 1u, abort_flag, p.status, p.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ++q_issued;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(q_full0 + 8 * qb, NQ * tile_bytes);
+                    for (int i = 0; i < NQ; ++i)
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_3d(q_smem + (qb * NQ + i) * tile_bytes + b * kBoxBytes, &q_map, q_full0 + 8 * qb,
+                                        b * 64, job.head, static_cast<int>(job.q0 + job.row0 + i * kRows));
+                    misc[3] = q_issued;
+                }
+                for (int n2 = 0; n2 < 2 * tl.count; ++n2) {
+                    const bool value = n2 & 1;
+                    const int t0 = tl.at(n2 >> 1);
+                    // the keys of a tile behind the document's last are other documents': their scores
+                    // are replaced, their values (times a weight of 0) have to be finite
+                    const bool tail = value && t0 + kRows > job.keys;
+                    ok = wait_role(empty0 + 8 * st, ph ^ 1u, abort_flag, p.status, p.wait_ns);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const uint32_t dst = ring + st * tile_bytes, bar = tail ? tail_bar : full0 + 8 * st;
+                    if (lane == 0) {
+                        misc[4] = tail ? 1u + (tails & 1u) : 0u;
+                        mbar_arrive_expect_tx(bar, tile_bytes);
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_3d(dst + b * kBoxBytes, value ? &v_map : &k_map, bar, b * 64, kv,
+                                        static_cast<int>(job.k0 + t0));
+                    }
+                    if (tail) {
+                        ok = wait_role(tail_bar, tails & 1u, abort_flag, p.status, p.wait_ns);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        ++tails;
+                        const int first = job.keys - t0;
+                        for (int i = first * 8 + lane; i < kRows * 8; i += 32)
+                            for (int b = 0; b < boxes; ++b)
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + b * kBoxBytes +
+                                                                                             i * 16u),
+                                             "r"(0u)
+                                             : "memory");
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(full0 + 8 * st);
+                            misc[4] = 0u;
+                        }
+                    }
+                    ++issued;
+                    if (lane == 0) misc[2] = issued;
+                    if (++st == stages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
             }
-            if (lane == 0) misc[2] = ++issued;
-            if (++st == stages) {
-                st = 0;
-                ph ^= 1u;
-            }
-        }
-    } else if (warp == 1) {
-        if (lane == 0 && tl.count > 0) {
+        } else if (warp == 1 && lane == 0) {
             constexpr uint32_t kType = BF ? (1u << 7) | (1u << 10) : 0u;
             const int cols = (p.width + 15) / 16 * 16;
             const uint32_t idesc_s = (1u << 4) | kType | ((kRows >> 3) << 17) | ((kRows >> 4) << 24);
@@ -343,133 +467,206 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
             const uint64_t vdesc = make_smem_desc(ring, 1024u, 2u, kBoxBytes);
             const uint32_t step = tile_bytes >> 4;
             int st = 0;
-            uint32_t ph = 0;
-            uint32_t turn[2] = {0u, 0u};   // steps of either tile so far
+            uint32_t ph = 0, q_used = 0;
+            uint32_t turn[2] = {0u, 0u};   // weights of either tile multiplied so far
             auto next = [&]() {
                 if (++st == stages) {
                     st = 0;
                     ph ^= 1u;
                 }
             };
-            auto scores = [&](int i, int slot) {
-                for (int k = 0; k < cols / 16; ++k) {
-                    const uint64_t off = (k >> 2) * (kBoxBytes >> 4) + 2 * (k & 3);
-                    tc_mma_f16(tmem + i * kRows, qdesc + i * step + off, kdesc + slot * step + off, idesc_s, k != 0);
-                }
-                tc_commit(s_full0 + 8 * i);
-            };
-            bool ok = wait_bar(q_full, 0, abort_flag, p.status, p.wait_ns) &&
-                      wait_bar(full0, 0, abort_flag, p.status, p.wait_ns);
-            if (ok) {
+            bool ok = true;
+            for (uint32_t k = 0; ok; ++k) {
+                if (!wait_role(job_full0 + 8 * (k & 1u), (k >> 1) & 1u, abort_flag, p.status, p.wait_ns)) break;
+                const Job job = jobs[k & 1u];
+                mbar_arrive(job_empty0 + 8 * (k & 1u));
+                if (job.head < 0) break;
+                Range part[NQ];
+                const Tiles tl = parts_of(job, part);
+                if (tl.count == 0) continue;
+                const uint32_t qb = q_used % q_bufs, qph = (q_used / q_bufs) & 1u;
+                ++q_used;
+                const uint64_t qd = qdesc + qb * NQ * step;
+                auto scores = [&](int i, int slot) {
+                    for (int kk = 0; kk < cols / 16; ++kk) {
+                        const uint64_t off = (kk >> 2) * (kBoxBytes >> 4) + 2 * (kk & 3);
+                        tc_mma_f16(tmem + i * kRows, qd + i * step + off, kdesc + slot * step + off, idesc_s, kk != 0);
+                    }
+                    tc_commit(s_full0 + 8 * i);
+                };
+                ok = wait_role(q_full0 + 8 * qb, qph, abort_flag, p.status, p.wait_ns) &&
+                     wait_role(full0 + 8 * st, ph, abort_flag, p.status, p.wait_ns);
+                if (!ok) break;
                 tc_fence_after();
+                bool fresh[2] = {true, true};
 #pragma unroll
                 for (int i = 0; i < NQ; ++i)
-                    if (sees(part[i], tl.at(0))) scores(i, 0);
-                tc_commit(empty0);
-            }
-            next();
-            for (int n = 0; n < tl.count && ok; ++n) {
-                const int t0 = tl.at(n), t1 = tl.at(n + 1);
-                const bool more = n + 1 < tl.count;
-                const int vs = st;
-                const uint32_t vph = ph;
+                    if (sees(part[i], tl.at(0))) scores(i, st);
+                tc_commit(empty0 + 8 * st);
+                if (tl.count == 1) tc_commit(q_empty0 + 8 * qb);
                 next();
-                const int ks = st;
-                const uint32_t kph = ph;
-                if (more) next();
-                bool v_ready = false, k_ready = false;
+                for (int n = 0; n < tl.count && ok; ++n) {
+                    const int t0 = tl.at(n), t1 = tl.at(n + 1);
+                    const bool more = n + 1 < tl.count;
+                    const int vs = st;
+                    const uint32_t vph = ph;
+                    next();
+                    const int ks = st;
+                    const uint32_t kph = ph;
+                    if (more) next();
+                    bool v_ready = false, k_ready = false;
 #pragma unroll
-                for (int i = 0; i < NQ; ++i) {
-                    if (sees(part[i], t0)) {
-                        if (!v_ready) ok = ok && wait_bar(full0 + 8 * vs, vph, abort_flag, p.status, p.wait_ns);
-                        v_ready = true;
-                        ok = ok && wait_bar(p_full0 + 8 * i, turn[i] & 1u, abort_flag, p.status, p.wait_ns);
-                        if (!ok) break;
-                        tc_fence_after();
+                    for (int i = 0; i < NQ; ++i) {
+                        if (sees(part[i], t0)) {
+                            if (!v_ready) ok = ok && wait_role(full0 + 8 * vs, vph, abort_flag, p.status, p.wait_ns);
+                            v_ready = true;
+                            ok = ok && wait_role(p_full0 + 8 * i, turn[i] & 1u, abort_flag, p.status, p.wait_ns);
+                            if (!ok) break;
+                            tc_fence_after();
 #pragma unroll
-                        for (int k = 0; k < kRows / 16; ++k)
-                            tc_mma_f16_ta(tmem + NQ * kRows + i * o_pitch, tmem + i * kRows + 8 * k,
-                                          vdesc + vs * step + k * 128, idesc_o, (turn[i] | k) != 0);
-                        tc_commit(o_done0 + 8 * i);
-                        ++turn[i];
+                            for (int kk = 0; kk < kRows / 16; ++kk)
+                                tc_mma_f16_ta(tmem + NQ * kRows + i * o_pitch, tmem + i * kRows + 8 * kk,
+                                              vdesc + vs * step + kk * 128, idesc_o, !fresh[i] || kk != 0);
+                            tc_commit(o_done0 + 8 * i);
+                            fresh[i] = false;
+                            ++turn[i];
+                        }
+                        if (more && sees(part[i], t1)) {
+                            if (!k_ready) ok = ok && wait_role(full0 + 8 * ks, kph, abort_flag, p.status, p.wait_ns);
+                            k_ready = true;
+                            if (!ok) break;
+                            tc_fence_after();
+                            scores(i, ks);
+                        }
                     }
-                    if (more && sees(part[i], t1)) {
-                        if (!k_ready) ok = ok && wait_bar(full0 + 8 * ks, kph, abort_flag, p.status, p.wait_ns);
-                        k_ready = true;
-                        if (!ok) break;
-                        tc_fence_after();
-                        scores(i, ks);
-                    }
+                    if (!ok) break;
+                    tc_commit(empty0 + 8 * vs);   // (any tile is seen by one of the two)
+                    if (more) tc_commit(empty0 + 8 * ks);
+                    if (n + 2 == tl.count) tc_commit(q_empty0 + 8 * qb);
                 }
-                if (!ok) break;
-                tc_commit(empty0 + 8 * vs);   // (any tile is seen by one of the two)
-                if (more) tc_commit(empty0 + 8 * ks);
             }
         }
-    } else if (warp >= 4) {
+        __syncwarp();
+    } else {
+        set_max_regs_inc<NQ == 2 ? 216 : 200>();
         const int i = (warp - 4) >> 2;
-        const int row = job.row0 + i * kRows + (warp & 3) * 32 + lane;
-        const bool valid = row < job.rows;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + i * kRows, t_o = tmem + lanes + NQ * kRows + i * o_pitch;
-        Range mine = part[0];
-        if (NQ == 2 && i == 1) mine = part[NQ - 1];
-        const RowMask mask = row_mask(p, job, min(row, job.rows - 1));
-        const int a = job.row0 + i * kRows;
-        const int b = min(a + kRows, job.rows);
-        // keys that every row of the tile sees
-        int all_lo = 0, all_hi = job.keys;
-        if (p.window > 0) {
-            all_lo = static_cast<int>(max(0ll, static_cast<long long>(b) + job.shift - p.window));
-            all_hi = static_cast<int>(min(static_cast<long long>(all_hi), static_cast<long long>(a) + job.shift + p.window));
-        }
-        if (p.causal) all_hi = min(all_hi, a + job.shift + 1);
-        const float slope2 = MOD && p.slopes ? p.slopes[job.head] * kLog2e : 0.0f;
+        // the cap's constants: scores times its polynomial are powers of two already
+        const float cap2 = p.cap * kLog2e, per_cap = MOD & kCap ? p.scale / p.cap : 0.0f;
         const float c = MOD ? 1.0f : p.scale * kLog2e;
-        const int pos = row + job.shift;
-        float ref = -INFINITY, sum = 0.0f;   // ref: what the weights are relative to
         uint32_t turn = 0;
         bool ok = true;
-        for (int n = 0; n < tl.count; ++n) {
-            const int t0 = tl.at(n);
-            if (!sees(mine, t0)) continue;
-            ok = wait_bar(s_full0 + 8 * i, turn & 1u, abort_flag, p.status, p.wait_ns);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
+        for (uint32_t k = 0; ok; ++k) {
+            ok = wait_role(job_full0 + 8 * (k & 1u), (k >> 1) & 1u, abort_flag, p.status, p.wait_ns);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            const Job job = jobs[k & 1u];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(job_empty0 + 8 * (k & 1u));
+            if (job.head < 0) break;
+            Range part[NQ];
+            const Tiles tl = parts_of(job, part);
+            const Range mine = NQ == 2 && i == 1 ? part[NQ - 1] : part[0];
+            const int row = job.row0 + i * kRows + (warp & 3) * 32 + lane;
+            const bool valid = row < job.rows;
+            const RowMask mask = row_mask(p, job, min(row, job.rows - 1));
+            const int a = job.row0 + i * kRows, b = min(a + kRows, job.rows);
+            // keys that every row of the tile sees
+            int all_lo = 0, all_hi = job.keys;
+            if (p.window > 0) {
+                all_lo = static_cast<int>(max(0ll, static_cast<long long>(b) + job.shift - p.window));
+                all_hi = static_cast<int>(min(static_cast<long long>(all_hi), static_cast<long long>(a) + job.shift + p.window));
             }
-            tc_fence_after();
-            uint32_t s[4][32];
+            if (p.causal) all_hi = min(all_hi, a + job.shift + 1);
+            const float slope2 = (MOD & kFar) && p.slopes ? p.slopes[job.head] * kLog2e : 0.0f;
+            const int pos = row + job.shift;
+            float ref = -INFINITY, sum = 0.0f;   // ref: what the weights are relative to
+            bool fresh = true;
+            for (int n = 0; n < tl.count; ++n) {
+                const int t0 = tl.at(n);
+                if (!sees(mine, t0)) continue;
+                ok = wait_role(s_full0 + 8 * i, turn & 1u, abort_flag, p.status, p.wait_ns);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t s[4][32];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) tmem_ld_32x32b_x32(t_s + 32 * h, s[h]);
-            tmem_ld_wait();
-            if (MOD) {
+                for (int h = 0; h < 4; ++h) tmem_ld_32x32b_x32(t_s + 32 * h, s[h]);
+                tmem_ld_wait();
+                if (MOD & kCap) {
+                    if (__any_sync(0xffffffffu, !(max128<true>(s) * fabsf(per_cap) <= 1.0f))) {
 #pragma unroll
-                for (int h = 0; h < 4; ++h)
+                        for (int h = 0; h < 4; ++h)
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        s[h][e] = __float_as_uint(shaped(p, __uint_as_float(s[h][e]), pos, t0 + 32 * h + e, slope2));
-            }
-            const bool open = t0 + kRows <= job.keys &&
-                              (t0 + kRows <= job.prefix || (t0 >= all_lo && t0 + kRows <= all_hi));
-            if (!open) {
+                            for (int e = 0; e < 32; ++e)
+                                s[h][e] = __float_as_uint(
+                                    cap2 - 2.0f * cap2 * rcp_approx(1.0f + ex2(__uint_as_float(s[h][e]) * (2.0f * kLog2e * per_cap))));
+                    } else {
+                        // tanh(x) for |x| <= 1 as x times a polynomial in x^2, within 2.5e-7 (a
+                        // least-squares fit reweighted towards equal errors): packed multiply-adds
+                        // where the exponential's form takes two turns of the special-function
+                        // unit a value
+                        constexpr float kTanh[6] = {0.99999684f,   -0.33324003f, 0.13253523f,
+                                                    -0.050972834f, 0.016114153f, -0.0028394549f};
+                        uint64_t co[6];
+                        float f = cap2 * per_cap;
 #pragma unroll
-                for (int h = 0; h < 4; ++h)
+                        for (int d = 0; d < 6; ++d) {
+                            co[d] = two(kTanh[d] * f);
+                            f *= per_cap * per_cap;
+                        }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!mask(t0 + 32 * h + e)) s[h][e] = __float_as_uint(-INFINITY);
-            }
-            float top = -INFINITY;
+                        for (int h = 0; h < 4; ++h)
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
+                            for (int e = 0; e < 32; e += 2) {
+                                const uint64_t x = two(s[h][e], s[h][e + 1]), u = mul2(x, x);
+                                uint64_t y = fma2(u, co[5], co[4]);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(s[h][e]));
-            if (turn == 0) {
-                ref = top;
-            } else {
-                const bool rise = top * c > ref * c + kLag;
-                if (__any_sync(0xffffffffu, rise)) {
-                    ok = wait_bar(o_done0 + 8 * i, (turn - 1) & 1u, abort_flag, p.status, p.wait_ns);
+                                for (int d = 3; d >= 0; --d) y = fma2(u, y, co[d]);
+                                split(mul2(x, y), s[h][e], s[h][e + 1]);
+                            }
+                    }
+                }
+                if (MOD & kFar) {
+                    const uint64_t f = two(MOD & kCap ? 1.0f : p.scale * kLog2e);
+                    if (t0 + kRows <= a + job.shift + 1 || t0 >= b - 1 + job.shift) {
+                        // all keys on one side of all rows: the distance is linear
+                        const float g = t0 >= b - 1 + job.shift ? -slope2 : slope2;
+                        const float g0 = g * static_cast<float>(t0 - pos);
+#pragma unroll
+                        for (int h = 0; h < 4; ++h)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                const float d = static_cast<float>(32 * h + e);
+                                const uint64_t far = fma2(two(g), two(__float_as_uint(d), __float_as_uint(d + 1.0f)), two(g0));
+                                split(fma2(two(s[h][e], s[h][e + 1]), f, far), s[h][e], s[h][e + 1]);
+                            }
+                    } else {
+                        const float rel = static_cast<float>(t0 - pos), ff = MOD & kCap ? 1.0f : p.scale * kLog2e;
+#pragma unroll
+                        for (int h = 0; h < 4; ++h)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                s[h][e] = __float_as_uint(fmaf(__uint_as_float(s[h][e]), ff,
+                                                               -slope2 * fabsf(rel + static_cast<float>(32 * h + e))));
+                    }
+                }
+                const bool open = t0 + kRows <= job.keys &&
+                                  (t0 + kRows <= job.prefix || (t0 >= all_lo && t0 + kRows <= all_hi));
+                if (!open) {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!mask(t0 + 32 * h + e)) s[h][e] = __float_as_uint(-INFINITY);
+                }
+                const float top = max128<false>(s);
+                if (fresh) {
+                    ref = top;
+                } else if (__any_sync(0xffffffffu, top * c > ref * c + kLag)) {
+                    ok = wait_role(o_done0 + 8 * i, (turn - 1) & 1u, abort_flag, p.status, p.wait_ns);
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
                         break;
@@ -488,70 +685,93 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                         tmem_st_32x32b_x8(t_o + d, o);
                     }
                 }
-            }
-            const float off = ref == -INFINITY ? 0.0f : ref * c;
+                fresh = false;
+                const uint64_t off = two(ref == -INFINITY ? 0.0f : -ref * c), cc = two(c);
+                uint64_t sums[2] = {0ull, 0ull};
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
+                for (int h = 0; h < 4; ++h) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float x = ex2(fmaf(__uint_as_float(s[h][e]), c, -off));
-                    const float y = ex2(fmaf(__uint_as_float(s[h][e + 1]), c, -off));
-                    sum += x + y;
-                    s[h >> 1][(h & 1) * 16 + e / 2] = pack2<BF>(x, y);
+                    for (int e = 0; e < 32; e += 2) {
+                        const uint64_t v = two(s[h][e], s[h][e + 1]);
+                        uint32_t x, y;
+                        split(MOD ? add2(v, off) : fma2(v, cc, off), x, y);
+                        const float px = ex2(__uint_as_float(x)), py = ex2(__uint_as_float(y));
+                        sums[e / 2 & 1] = add2(sums[e / 2 & 1], two(__float_as_uint(px), __float_as_uint(py)));
+                        s[h >> 1][(h & 1) * 16 + e / 2] = pack2<BF>(px, py);
+                    }
+                    if (h == 1) tmem_st_32x32b_x32(t_s, s[0]);
                 }
-            tmem_st_32x32b_x32(t_s, s[0]);
-            tmem_st_32x32b_x32(t_s + 32, s[1]);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_full0 + 8 * i);
-            ++turn;
-        }
-        if (ok && turn > 0) ok = wait_bar(o_done0 + 8 * i, (turn - 1) & 1u, abort_flag, p.status, p.wait_ns);
-        if (__all_sync(0xffffffffu, ok)) {
-            tc_fence_after();
-            const float inv = turn == 0 || sum == 0.0f ? 0.0f : 1.0f / sum;
+                tmem_st_32x32b_x32(t_s + 32, s[1]);
+                {
+                    uint32_t x, y;
+                    split(add2(sums[0], sums[1]), x, y);
+                    sum += __uint_as_float(x) + __uint_as_float(y);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full0 + 8 * i);
+                ++turn;
+            }
+            if (!ok) break;
+            if (!fresh) {
+                ok = wait_role(o_done0 + 8 * i, (turn - 1) & 1u, abort_flag, p.status, p.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+            }
+            // ---- the output rows
+            const float inv = fresh || sum == 0.0f ? 0.0f : 1.0f / sum;
             uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) + (job.q0 + row) * p.out_tok +
                             static_cast<long long>(job.head) * p.out_head;
             bool odd = false;
-            for (int d = 0; d < p.width; d += 8) {
-                uint32_t o[8];
-                if (turn > 0) {
-                    tmem_ld_32x32b_x8(t_o + d, o);
+            for (int d = 0; d < p.width; d += 16) {
+                uint32_t o[2][8];
+                if (!fresh) {
+                    tmem_ld_32x32b_x8(t_o + d, o[0]);
+                    tmem_ld_32x32b_x8(t_o + d + 8, o[1]);
                     tmem_ld_wait();
                 }
-                uint32_t w[4];
+                uint32_t w[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = turn > 0 && inv != 0.0f ? __uint_as_float(o[2 * e]) * inv : 0.0f;
-                    const float y = turn > 0 && inv != 0.0f ? __uint_as_float(o[2 * e + 1]) * inv : 0.0f;
-                    odd = odd || !(fabsf(x) + fabsf(y) < INFINITY);
+                for (int e = 0; e < 8; ++e) {
+                    const float x = inv != 0.0f ? __uint_as_float(o[e >> 2][2 * (e & 3)]) * inv : 0.0f;
+                    const float y = inv != 0.0f ? __uint_as_float(o[e >> 2][2 * (e & 3) + 1]) * inv : 0.0f;
+                    odd = odd || (d + 2 * e < p.width && !(fabsf(x) + fabsf(y) < INFINITY));
                     w[e] = pack2<BF>(x, y);
                 }
-                if (valid && p.out_aligned) {
+                const int left = p.width - d;
+                if (valid && left >= 16 && p.out_aligned == 32) {
+                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + d), "r"(w[0]),
+                                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                                 : "memory");
+                } else if (valid && p.out_aligned) {
                     *reinterpret_cast<uint4*>(dst + d) = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (left >= 16) *reinterpret_cast<uint4*>(dst + d + 8) = make_uint4(w[4], w[5], w[6], w[7]);
                 } else if (valid) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) dst[d + e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
+                    for (int e = 0; e < 16; ++e)
+                        if (e < left) dst[d + e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
                 }
                 __syncwarp();
             }
             if (valid && odd) redo_row<BF>(p, job, mine, row);
+            __syncwarp();
+            tc_fence_before();
         }
-        tc_fence_before();
     }
     __syncwarp();
     __syncthreads();
     if (*abort_flag) {
         // drain: the loads, then the MMAs in flight
         if (threadIdx.x == 0) {
-            if (tl.count > 0) drain_wait(q_full, 0);
-            for (uint32_t n = misc[2] > static_cast<uint32_t>(stages) ? misc[2] - stages : 0u; n < misc[2]; ++n)
-                drain_wait(full0 + 8 * (n % stages), (n / stages) & 1u);
+            if (misc[4]) drain_here(tail_bar, misc[4] - 1u);
+            drain_slots(q_full0, misc[3], q_bufs);
+            drain_slots(full0, misc[2], stages);
         }
         if (threadIdx.x == 32) {
             tc_commit(drain_bar);
-            drain_wait(drain_bar, 0);
+            drain_here(drain_bar, 0);
         }
         __syncthreads();
     }
@@ -561,36 +781,41 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
     }
 }
 
-template <bool BF, int NQ, bool MOD>
-cudaError_t run(const PackedMaps& maps, const PackedParams& p, cudaStream_t stream) {
+template <bool BF, int NQ, int MOD>
+cudaError_t run(const PackedMaps& maps, const PackedParams& p, int num_sms, cudaStream_t stream) {
     const uint32_t tile = static_cast<uint32_t>((p.width + 63) / 64) * kBoxBytes;
-    // shared memory of the SM, or half of it for two CTAs
+    // shared memory of the SM, or half of it for two CTAs; Q twice where tiles are small
     const uint32_t room = (NQ == 2 ? 232448u : 115200u) - 1024u - 512u;
-    int stages = static_cast<int>((room - NQ * tile) / tile);
+    const int q_bufs = tile == kBoxBytes ? 2 : 1;
+    int stages = static_cast<int>((room - q_bufs * NQ * tile) / tile);
     if (stages > kMaxStages) stages = kMaxStages;
-    const size_t smem = 1024u + (NQ + stages) * tile + 512u;
+    const size_t smem = 1024u + (q_bufs * NQ + stages) * tile + 512u;
     static std::atomic<int> slots[kMaxDevices];
     cudaError_t e = ensure_dynamic_smem(packed_kernel<BF, NQ, MOD>, smem, slots);
     if (e != cudaSuccess) return e;
-    const long long blocks = (p.q_tokens / (NQ * kRows) + p.documents) * p.heads;
-    return launch_ex(packed_kernel<BF, NQ, MOD>, static_cast<unsigned>(blocks), dim3(kThreads<NQ>), smem, 1, stream,
-                     maps.q, maps.k, maps.v, p, stages);
+    const long long most = (p.q_tokens / (NQ * kRows) + p.documents) * p.heads;
+    const long long resident = static_cast<long long>(num_sms) * (NQ == 1 ? 2 : 1);
+    return launch_ex(packed_kernel<BF, NQ, MOD>, static_cast<unsigned>(most < resident ? most : resident),
+                     dim3(kThreads<NQ>), smem, 1, stream, maps.q, maps.k, maps.v, p, stages, q_bufs);
+}
+
+template <bool BF, int NQ>
+cudaError_t by_mod(const PackedMaps& maps, const PackedParams& p, int num_sms, cudaStream_t stream) {
+    const bool far = p.slopes || !(p.scale > 0.0f);
+    if (p.cap > 0.0f)
+        return far ? run<BF, NQ, kCap | kFar>(maps, p, num_sms, stream) : run<BF, NQ, kCap>(maps, p, num_sms, stream);
+    return far ? run<BF, NQ, kFar>(maps, p, num_sms, stream) : run<BF, NQ, 0>(maps, p, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_packed(const PackedMaps& maps, const PackedParams& p, int dtype, int num_sms,
                           cudaStream_t stream) {
-    const bool mod = p.cap > 0.0f || p.slopes || !(p.scale > 0.0f);
     const bool bf = dtype == kTokBf16;
-    // two tiles where documents are long and there are CTAs enough for all SMs
-    const bool two = p.q_tokens / p.documents >= 1024 && p.q_tokens / 256 * p.heads >= num_sms;
-    if (two) {
-        if (bf) return mod ? run<true, 2, true>(maps, p, stream) : run<true, 2, false>(maps, p, stream);
-        return mod ? run<false, 2, true>(maps, p, stream) : run<false, 2, false>(maps, p, stream);
-    }
-    if (bf) return mod ? run<true, 1, true>(maps, p, stream) : run<true, 1, false>(maps, p, stream);
-    return mod ? run<false, 1, true>(maps, p, stream) : run<false, 1, false>(maps, p, stream);
+    // two tiles where documents are long and there are jobs enough for all SMs
+    const bool two_tiles = p.q_tokens / p.documents >= 1024 && p.q_tokens / 256 * p.heads >= num_sms;
+    if (two_tiles) return bf ? by_mod<true, 2>(maps, p, num_sms, stream) : by_mod<false, 2>(maps, p, num_sms, stream);
+    return bf ? by_mod<true, 1>(maps, p, num_sms, stream) : by_mod<false, 1>(maps, p, num_sms, stream);
 }
 
 }  // namespace c3d
