@@ -10,7 +10,7 @@
 // go back as 16-bit words over S, where the second product O += P V takes them as its
 // first operand.  V is read as it lies in memory (its rows are the reduction).
 //   warp 0      finds the jobs; TMA producer: Q, then K and V tiles in a ring
-//   warp 1      tensor memory, MMA issuer
+//   warp 1      tensor memory; issues the first tile's products, warp 2 the second's
 //   warps 4-7   the first tile's rows: softmax, then the output; 8-11 the second's
 // The next job's loads and first scores run under the last softmax and the output of the
 // one before.
@@ -54,12 +54,21 @@ __device__ __forceinline__ float elem(const unsigned char* base, long long i) {
 }
 
 // 128 * NQ rows from `row0` of a document, for one head (negative: no more jobs).
+// Its key tiles, in order, are those of the document's lead (lead_tiles), then those from
+// tile `skip` on; a query tile sees the first `lead` of them and those from lo to hi.
+struct Seen {
+    int lead, lo, hi;
+    __device__ bool operator()(int n) const { return n < lead || (n >= lo && n < hi); }
+};
 struct Job {
-    int row0, rows;          // of the document; rows: the document's queries
+    int head, row0, rows;    // rows: the document's queries
     int keys, shift;         // its keys; position of row r: r + shift
     int prefix;
+    int count, lead_tiles, skip;
+    Seen seen[2];
+    int unused;
     long long q0, k0;        // packed rows of the document's first query and key
-    int head;
+    __device__ int key(int n) const { return (n < lead_tiles ? n : n - lead_tiles + skip) * kRows; }
 };
 
 // The keys that rows [a, b) of the job see: [lo, hi) of any of them, and [0, lead).
@@ -79,20 +88,19 @@ __device__ __forceinline__ Range range_of(const PackedParams& p, const Job& j, i
     return r;
 }
 
-// The key tiles of the whole job, in order: those of the lead, then those from `skip` on.
-struct Tiles {
-    int lead, skip, count;
-    __device__ int at(int n) const { return (n < lead ? n : n - lead + skip) * kRows; }
-};
-__device__ __forceinline__ Tiles tiles_of(const Range& r) {
-    Tiles t;
-    t.lead = (r.lead + kRows - 1) / kRows;
-    t.skip = max(r.lo / kRows, t.lead);
-    t.count = t.lead + max((r.hi + kRows - 1) / kRows - t.skip, 0);
-    return t;
-}
-__device__ __forceinline__ bool sees(const Range& r, int t0) {
-    return t0 < r.lead || (t0 < r.hi && t0 + kRows > r.lo);
+// The key tiles of a job of nq query tiles
+__device__ __forceinline__ void plan_tiles(const PackedParams& p, Job& j, int nq) {
+    const Range all = range_of(p, j, j.row0, min(j.row0 + nq * kRows, j.rows));
+    j.lead_tiles = (all.lead + kRows - 1) / kRows;
+    j.skip = max(all.lo / kRows, j.lead_tiles);
+    j.count = j.lead_tiles + max((all.hi + kRows - 1) / kRows - j.skip, 0);
+    for (int i = 0; i < 2; ++i) {
+        const int a = j.row0 + i * kRows;
+        const Range r = range_of(p, j, a, i < nq ? min(a + kRows, j.rows) : a);
+        j.seen[i].lead = r.lead ? j.lead_tiles : 0;
+        j.seen[i].lo = r.hi > r.lo ? max(r.lo / kRows, j.skip) - j.skip + j.lead_tiles : 0;
+        j.seen[i].hi = r.hi > r.lo ? max((r.hi + kRows - 1) / kRows, j.skip) - j.skip + j.lead_tiles : 0;
+    }
 }
 
 template <bool BF>
@@ -167,14 +175,14 @@ __device__ __forceinline__ RowMask row_mask(const PackedParams& p, const Job& j,
 // tile that was multiplied (weight 0) has a value that is not finite.  Then the row is
 // computed again, over what it sees alone.
 template <bool BF>
-__device__ __forceinline__ void redo_row(const PackedParams& p, const Job& job, const Range& tile_range, int row) {
+__device__ __forceinline__ void redo_row(const PackedParams& p, const Job& job, const Seen& seen, int row) {
     const int kv = job.head / p.group;
     const RowMask m = row_mask(p, job, row);
     const long long vbase = job.k0 * p.k_tok + static_cast<long long>(kv) * p.k_head;
     bool spoiled = false;
-    const Tiles tl = tiles_of(tile_range);
-    for (int n = 0; n < tl.count && !spoiled; ++n) {
-        const int t0 = tl.at(n);
+    for (int n = 0; n < job.count && !spoiled; ++n) {
+        const int t0 = job.key(n);
+        if (!seen(n)) continue;
         for (int j = t0; j < min(t0 + kRows, job.keys) && !spoiled; ++j)
             if (!m(j)) spoiled = !finite_row<BF>(p.v, vbase + j * p.k_tok, p.width);
     }
@@ -214,20 +222,22 @@ __device__ __forceinline__ void redo_row(const PackedParams& p, const Job& job, 
 
 // Bounded waits without a call (see wait_bar and drain_wait): the compiler makes none from
 // warps that have registers of a number of their own.  A role sleeps in hardware between
-// looks, so that its polling leaves the issue slots to the others.
+// looks, so that its polling leaves the issue slots to the others.  Whole warps wait, with
+// one answer for all lanes.
 __device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
                                           int* status, unsigned long long limit_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
+    constexpr uint32_t kAll = 0xffffffffu;
+    if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
     const long long t0 = clock64();
     const long long limit = static_cast<long long>(limit_ns > (1ull << 61) ? (1ull << 61) : limit_ns) * 2;
     while (true) {
-        if (*abort_flag) return false;
-        if (clock64() - t0 > limit) {
+        if (__any_sync(kAll, *abort_flag != 0u)) return false;
+        if (__any_sync(kAll, clock64() - t0 > limit)) {
             *abort_flag = 1u;
             atomicExch(status, kStatusTimeout);
             return false;
         }
-        if (mbar_try_wait_for(bar, parity, 20000u)) return true;
+        if (__all_sync(kAll, mbar_try_wait_for(bar, parity, 20000u))) return true;
     }
 }
 __device__ __forceinline__ void drain_here(uint32_t bar, uint32_t parity) {
@@ -239,6 +249,50 @@ __device__ __forceinline__ void drain_here(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ void drain_slots(uint32_t full0, uint32_t issued, uint32_t slots) {
     for (uint32_t n = issued > slots ? issued - slots : 0u; n < issued; ++n)
         drain_here(full0 + 8 * (n % slots), (n / slots) & 1u);
+}
+
+// One lane's predicate, and instructions under it
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r;
+}
+// (a value that every lane holds alike, said so to the compiler)
+__device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
+
+__device__ __forceinline__ void mma_if(uint32_t lane, uint32_t d, uint32_t a_low, uint32_t a_high, uint32_t b_low,
+                                       uint32_t b_high, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "setp.ne.b32 p, %7, 0;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], a, b, %6, p;\n\t}" ::"r"(lane),
+        "r"(d), "r"(a_low), "r"(a_high), "r"(b_low), "r"(b_high), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ta_if(uint32_t lane, uint32_t d, uint32_t a, uint32_t b_low, uint32_t b_high,
+                                          uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 b, {%3, %4};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], b, %5, p;\n\t}" ::"r"(lane),
+        "r"(d), "r"(a), "r"(b_low), "r"(b_high), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t lane, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(lane),
+        "r"(bar)
+        : "memory");
 }
 
 template <int NQ>
@@ -276,19 +330,19 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) {
             mbar_init(full0 + 8 * i, 1);
-            mbar_init(empty0 + 8 * i, 1);
+            mbar_init(empty0 + 8 * i, NQ);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full0 + 8 * i, 1);
-            mbar_init(q_empty0 + 8 * i, 1);
+            mbar_init(q_empty0 + 8 * i, NQ);
             mbar_init(job_full0 + 8 * i, 1);
-            mbar_init(job_empty0 + 8 * i, 1 + 4 * NQ);
+            mbar_init(job_empty0 + 8 * i, 5 * NQ);
             mbar_init(s_full0 + 8 * i, 1);
             mbar_init(p_full0 + 8 * i, 4);
             mbar_init(o_done0 + 8 * i, 1);
         }
         mbar_init(tail_bar, 1);
-        mbar_init(drain_bar, 1);
+        mbar_init(drain_bar, NQ);
         misc[1] = 0u;
         misc[2] = 0u;
         misc[3] = 0u;
@@ -309,14 +363,6 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
     const uint32_t o_pitch = boxes * 64u;
     griddep_launch_dependents();
     griddep_wait();
-
-    // the tiles of a job, and what each of its query tiles sees
-    auto parts_of = [&](const Job& job, Range (&part)[NQ]) {
-#pragma unroll
-        for (int i = 0; i < NQ; ++i)
-            part[i] = range_of(p, job, job.row0 + i * kRows, min(job.row0 + (i + 1) * kRows, job.rows));
-        return tiles_of(range_of(p, job, job.row0, min(job.row0 + NQ * kRows, job.rows)));
-    };
 
     if (warp < 4) {
         set_max_regs_dec<NQ == 2 ? 72 : 56>();
@@ -356,7 +402,6 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                 const bool more = before + all > want;
                 const uint32_t slot = k & 1u, jph = (k >> 1) & 1u;
                 ok = wait_role(job_empty0 + 8 * slot, jph ^ 1u, abort_flag, p.status, p.wait_ns);
-                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 if (more) {
                     const int in = static_cast<int>(want - before);
@@ -386,6 +431,8 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                         job.q0 = q0;
                         job.k0 = kb;
                         job.head = static_cast<int>(at - want * static_cast<uint32_t>(p.heads));
+                        job.unused = 0;
+                        plan_tiles(p, job, NQ);
                         jobs[slot] = job;
                     }
                 } else if (lane == 0) {
@@ -395,13 +442,10 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                 if (lane == 0) mbar_arrive(job_full0 + 8 * slot);
                 if (!more) break;
                 const Job job = jobs[slot];
-                Range part[NQ];
-                const Tiles tl = parts_of(job, part);
-                if (tl.count == 0) continue;
+                if (job.count == 0) continue;
                 const int kv = job.head / p.group;
                 const uint32_t qb = q_issued % q_bufs, qph = (q_issued / q_bufs) & 1u;
                 ok = wait_role(q_empty0 + 8 * qb, qph ^ 1u, abort_flag, p.status, p.wait_ns);
-                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 ++q_issued;
                 if (lane == 0) {
@@ -412,14 +456,13 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                                         b * 64, job.head, static_cast<int>(job.q0 + job.row0 + i * kRows));
                     misc[3] = q_issued;
                 }
-                for (int n2 = 0; n2 < 2 * tl.count; ++n2) {
+                for (int n2 = 0; n2 < 2 * job.count; ++n2) {
                     const bool value = n2 & 1;
-                    const int t0 = tl.at(n2 >> 1);
+                    const int t0 = job.key(n2 >> 1);
                     // the keys of a tile behind the document's last are other documents': their scores
                     // are replaced, their values (times a weight of 0) have to be finite
                     const bool tail = value && t0 + kRows > job.keys;
                     ok = wait_role(empty0 + 8 * st, ph ^ 1u, abort_flag, p.status, p.wait_ns);
-                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     const uint32_t dst = ring + st * tile_bytes, bar = tail ? tail_bar : full0 + 8 * st;
                     if (lane == 0) {
@@ -431,7 +474,6 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                     }
                     if (tail) {
                         ok = wait_role(tail_bar, tails & 1u, abort_flag, p.status, p.wait_ns);
-                        ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         ++tails;
                         const int first = job.keys - t0;
@@ -456,93 +498,86 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                     }
                 }
             }
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp <= NQ) {
+            // One warp a query tile, all lanes together and one of them issuing: addresses and
+            // decisions then stay in uniform registers, which the instructions take them from.
+            // Small code counts: it shares its instruction cache with the softmax loops.
             constexpr uint32_t kType = BF ? (1u << 7) | (1u << 10) : 0u;
-            const int cols = (p.width + 15) / 16 * 16;
+            const uint32_t ksteps = (p.width + 15) / 16;
             const uint32_t idesc_s = (1u << 4) | kType | ((kRows >> 3) << 17) | ((kRows >> 4) << 24);
-            const uint32_t idesc_o = (1u << 4) | kType | (1u << 16) | (static_cast<uint32_t>(cols >> 3) << 17) |
-                                     ((kRows >> 4) << 24);
-            const uint64_t qdesc = make_smem_desc(q_smem, 1024u, 2u);
-            const uint64_t kdesc = make_smem_desc(ring, 1024u, 2u);
-            const uint64_t vdesc = make_smem_desc(ring, 1024u, 2u, kBoxBytes);
-            const uint32_t step = tile_bytes >> 4;
-            int st = 0;
-            uint32_t ph = 0, q_used = 0;
-            uint32_t turn[2] = {0u, 0u};   // weights of either tile multiplied so far
+            const uint32_t idesc_o = (1u << 4) | kType | (1u << 16) | (ksteps * 2u << 17) | ((kRows >> 4) << 24);
+            // descriptors by their words: the address (and the V blocks' distance) below, the
+            // 8-row groups' distance, the version and the swizzle above
+            constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+            const uint32_t i = NQ == 1 ? 0u : static_cast<uint32_t>(uniform(warp - 1));
+            const uint32_t step = tile_bytes >> 4, el = elect_lane();
+            const uint32_t q_low = ((q_smem >> 4) | (1u << 16)) + i * step, k_low = (ring >> 4) | (1u << 16);
+            const uint32_t v_low = (ring >> 4) | ((kBoxBytes >> 4) << 16);
+            const uint32_t t_s = tmem + i * kRows, t_o = tmem + NQ * kRows + i * o_pitch;
+            const uint32_t s_full = s_full0 + 8 * i, p_full = p_full0 + 8 * i, o_done = o_done0 + 8 * i;
+            uint32_t slot = 0, ph = 0, q_buf = 0, q_ph = 0, pph = 0;
+            bool ok = true;
             auto next = [&]() {
-                if (++st == stages) {
-                    st = 0;
+                if (++slot == static_cast<uint32_t>(stages)) {
+                    slot = 0;
                     ph ^= 1u;
                 }
             };
-            bool ok = true;
             for (uint32_t k = 0; ok; ++k) {
-                if (!wait_role(job_full0 + 8 * (k & 1u), (k >> 1) & 1u, abort_flag, p.status, p.wait_ns)) break;
-                const Job job = jobs[k & 1u];
-                mbar_arrive(job_empty0 + 8 * (k & 1u));
-                if (job.head < 0) break;
-                Range part[NQ];
-                const Tiles tl = parts_of(job, part);
-                if (tl.count == 0) continue;
-                const uint32_t qb = q_used % q_bufs, qph = (q_used / q_bufs) & 1u;
-                ++q_used;
-                const uint64_t qd = qdesc + qb * NQ * step;
-                auto scores = [&](int i, int slot) {
-                    for (int kk = 0; kk < cols / 16; ++kk) {
-                        const uint64_t off = (kk >> 2) * (kBoxBytes >> 4) + 2 * (kk & 3);
-                        tc_mma_f16(tmem + i * kRows, qd + i * step + off, kdesc + slot * step + off, idesc_s, kk != 0);
-                    }
-                    tc_commit(s_full0 + 8 * i);
-                };
-                ok = wait_role(q_full0 + 8 * qb, qph, abort_flag, p.status, p.wait_ns) &&
-                     wait_role(full0 + 8 * st, ph, abort_flag, p.status, p.wait_ns);
+                ok = wait_role(job_full0 + 8 * (k & 1u), (k >> 1) & 1u, abort_flag, p.status, p.wait_ns);
                 if (!ok) break;
-                tc_fence_after();
-                bool fresh[2] = {true, true};
-#pragma unroll
-                for (int i = 0; i < NQ; ++i)
-                    if (sees(part[i], tl.at(0))) scores(i, st);
-                tc_commit(empty0 + 8 * st);
-                if (tl.count == 1) tc_commit(q_empty0 + 8 * qb);
-                next();
-                for (int n = 0; n < tl.count && ok; ++n) {
-                    const int t0 = tl.at(n), t1 = tl.at(n + 1);
-                    const bool more = n + 1 < tl.count;
-                    const int vs = st;
-                    const uint32_t vph = ph;
-                    next();
-                    const int ks = st;
-                    const uint32_t kph = ph;
-                    if (more) next();
-                    bool v_ready = false, k_ready = false;
-#pragma unroll
-                    for (int i = 0; i < NQ; ++i) {
-                        if (sees(part[i], t0)) {
-                            if (!v_ready) ok = ok && wait_role(full0 + 8 * vs, vph, abort_flag, p.status, p.wait_ns);
-                            v_ready = true;
-                            ok = ok && wait_role(p_full0 + 8 * i, turn[i] & 1u, abort_flag, p.status, p.wait_ns);
-                            if (!ok) break;
-                            tc_fence_after();
-#pragma unroll
-                            for (int kk = 0; kk < kRows / 16; ++kk)
-                                tc_mma_f16_ta(tmem + NQ * kRows + i * o_pitch, tmem + i * kRows + 8 * kk,
-                                              vdesc + vs * step + kk * 128, idesc_o, !fresh[i] || kk != 0);
-                            tc_commit(o_done0 + 8 * i);
-                            fresh[i] = false;
-                            ++turn[i];
-                        }
-                        if (more && sees(part[i], t1)) {
-                            if (!k_ready) ok = ok && wait_role(full0 + 8 * ks, kph, abort_flag, p.status, p.wait_ns);
-                            k_ready = true;
-                            if (!ok) break;
-                            tc_fence_after();
-                            scores(i, ks);
-                        }
-                    }
+                const Job& job = jobs[k & 1u];
+                const int count = uniform(job.count);
+                const Seen seen{uniform(job.seen[i].lead), uniform(job.seen[i].lo), uniform(job.seen[i].hi)};
+                const bool last = uniform(job.head + 1) == 0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(job_empty0 + 8 * (k & 1u));
+                if (last) break;
+                if (count == 0) continue;
+                ok = wait_role(q_full0 + 8 * q_buf, q_ph, abort_flag, p.status, p.wait_ns);
+                if (!ok) break;
+                const uint32_t q_at = q_low + q_buf * NQ * step;
+                uint32_t add = 0u;
+#pragma unroll 1
+                for (int n = 0; n < count; ++n) {
+                    const bool active = seen(n);
+                    ok = wait_role(full0 + 8 * slot, ph, abort_flag, p.status, p.wait_ns);
                     if (!ok) break;
-                    tc_commit(empty0 + 8 * vs);   // (any tile is seen by one of the two)
-                    if (more) tc_commit(empty0 + 8 * ks);
-                    if (n + 2 == tl.count) tc_commit(q_empty0 + 8 * qb);
+                    if (active) {
+                        // (the scores before were read, and their weights multiplied, by then)
+                        tc_fence_after();
+                        const uint32_t b = k_low + slot * step;
+                        mma_if(el, t_s, q_at, kHigh, b, kHigh, idesc_s, 0u);
+#pragma unroll
+                        for (uint32_t kk = 1; kk < 8; ++kk) {
+                            const uint32_t off = (kk >> 2) * (kBoxBytes >> 4) + 2 * (kk & 3);
+                            if (kk < ksteps) mma_if(el, t_s, q_at + off, kHigh, b + off, kHigh, idesc_s, 1u);
+                        }
+                        commit_if(el, s_full);
+                    }
+                    commit_if(el, empty0 + 8 * slot);
+                    if (n + 1 == count) commit_if(el, q_empty0 + 8 * q_buf);
+                    next();
+                    ok = wait_role(full0 + 8 * slot, ph, abort_flag, p.status, p.wait_ns);
+                    if (!ok) break;
+                    if (active) {
+                        ok = wait_role(p_full, pph, abort_flag, p.status, p.wait_ns);
+                        if (!ok) break;
+                        pph ^= 1u;
+                        tc_fence_after();
+                        const uint32_t b = v_low + slot * step;
+#pragma unroll
+                        for (uint32_t kk = 0; kk < kRows / 16; ++kk)
+                            mma_ta_if(el, t_o, t_s + 8 * kk, b + kk * 128, kHigh, idesc_o, kk ? 1u : add);
+                        commit_if(el, o_done);
+                        add = 1u;
+                    }
+                    commit_if(el, empty0 + 8 * slot);
+                    next();
+                }
+                if (++q_buf == static_cast<uint32_t>(q_bufs)) {
+                    q_buf = 0;
+                    q_ph ^= 1u;
                 }
             }
         }
@@ -555,18 +590,16 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
         // the cap's constants: scores times its polynomial are powers of two already
         const float cap2 = p.cap * kLog2e, per_cap = MOD & kCap ? p.scale / p.cap : 0.0f;
         const float c = MOD ? 1.0f : p.scale * kLog2e;
-        uint32_t turn = 0;
+        uint32_t turn = 0;   // this tile's units so far
         bool ok = true;
         for (uint32_t k = 0; ok; ++k) {
             ok = wait_role(job_full0 + 8 * (k & 1u), (k >> 1) & 1u, abort_flag, p.status, p.wait_ns);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            if (!ok) break;
             const Job job = jobs[k & 1u];
             __syncwarp();
             if (lane == 0) mbar_arrive(job_empty0 + 8 * (k & 1u));
             if (job.head < 0) break;
-            Range part[NQ];
-            const Tiles tl = parts_of(job, part);
-            const Range mine = NQ == 2 && i == 1 ? part[NQ - 1] : part[0];
+            const Seen mine = NQ == 2 && i == 1 ? job.seen[1] : job.seen[0];
             const int row = job.row0 + i * kRows + (warp & 3) * 32 + lane;
             const bool valid = row < job.rows;
             const RowMask mask = row_mask(p, job, min(row, job.rows - 1));
@@ -582,14 +615,11 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
             const int pos = row + job.shift;
             float ref = -INFINITY, sum = 0.0f;   // ref: what the weights are relative to
             bool fresh = true;
-            for (int n = 0; n < tl.count; ++n) {
-                const int t0 = tl.at(n);
-                if (!sees(mine, t0)) continue;
+            for (int n = 0; n < job.count; ++n) {
+                const int t0 = job.key(n);
+                if (!mine(n)) continue;
                 ok = wait_role(s_full0 + 8 * i, turn & 1u, abort_flag, p.status, p.wait_ns);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
+                if (!ok) break;
                 tc_fence_after();
                 uint32_t s[4][32];
 #pragma unroll
@@ -667,10 +697,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                     ref = top;
                 } else if (__any_sync(0xffffffffu, top * c > ref * c + kLag)) {
                     ok = wait_role(o_done0 + 8 * i, (turn - 1) & 1u, abort_flag, p.status, p.wait_ns);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!ok) break;
                     tc_fence_after();
                     const float now = fmaxf(ref, top);
                     const float f = now == -INFINITY ? 1.0f : ex2((ref - now) * c);
@@ -716,7 +743,6 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
             if (!ok) break;
             if (!fresh) {
                 ok = wait_role(o_done0 + 8 * i, (turn - 1) & 1u, abort_flag, p.status, p.wait_ns);
-                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -769,8 +795,8 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
             drain_slots(q_full0, misc[3], q_bufs);
             drain_slots(full0, misc[2], stages);
         }
-        if (threadIdx.x == 32) {
-            tc_commit(drain_bar);
+        if (warp >= 1 && warp <= NQ) {
+            commit_if(elect_lane(), drain_bar);
             drain_here(drain_bar, 0);
         }
         __syncthreads();
@@ -785,11 +811,11 @@ template <bool BF, int NQ, int MOD>
 cudaError_t run(const PackedMaps& maps, const PackedParams& p, int num_sms, cudaStream_t stream) {
     const uint32_t tile = static_cast<uint32_t>((p.width + 63) / 64) * kBoxBytes;
     // shared memory of the SM, or half of it for two CTAs; Q twice where tiles are small
-    const uint32_t room = (NQ == 2 ? 232448u : 115200u) - 1024u - 512u;
+    const uint32_t room = (NQ == 2 ? 232448u : 115200u) - 1024u - 640u;
     const int q_bufs = tile == kBoxBytes ? 2 : 1;
     int stages = static_cast<int>((room - q_bufs * NQ * tile) / tile);
     if (stages > kMaxStages) stages = kMaxStages;
-    const size_t smem = 1024u + (q_bufs * NQ + stages) * tile + 512u;
+    const size_t smem = 1024u + (q_bufs * NQ + stages) * tile + 640u;
     static std::atomic<int> slots[kMaxDevices];
     cudaError_t e = ensure_dynamic_smem(packed_kernel<BF, NQ, MOD>, smem, slots);
     if (e != cudaSuccess) return e;
