@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
     const uint32_t q_full0 = empty0 + 8u * kMaxStages, q_empty0 = q_full0 + 16u;
     const uint32_t job_full0 = q_empty0 + 16u, job_empty0 = job_full0 + 16u;
     const uint32_t s_full0 = job_empty0 + 16u, p_full0 = s_full0 + 16u, o_done0 = p_full0 + 16u;
-    const uint32_t tail_bar = o_done0 + 16u, drain_bar = tail_bar + 8u;
+    const uint32_t turn_bar0 = o_done0 + 16u, tail_bar = turn_bar0 + 16u, drain_bar = tail_bar + 8u;
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem_raw + (drain_bar + 8u - raw));
     // misc[0] TMEM base, [1] abort flag, [2] ring loads issued, [3] Q loads issued, [4] whether a
     // last tile's values are on their way (1 + its phase); then two jobs
@@ -340,6 +340,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
             mbar_init(s_full0 + 8 * i, 1);
             mbar_init(p_full0 + 8 * i, 4);
             mbar_init(o_done0 + 8 * i, 1);
+            mbar_init(turn_bar0 + 8 * i, 1);
         }
         mbar_init(tail_bar, 1);
         mbar_init(drain_bar, NQ);
@@ -515,8 +516,22 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
             const uint32_t v_low = (ring >> 4) | ((kBoxBytes >> 4) << 16);
             const uint32_t t_s = tmem + i * kRows, t_o = tmem + NQ * kRows + i * o_pitch;
             const uint32_t s_full = s_full0 + 8 * i, p_full = p_full0 + 8 * i, o_done = o_done0 + 8 * i;
-            uint32_t slot = 0, ph = 0, q_buf = 0, q_ph = 0, pph = 0;
+            uint32_t slot = 0, ph = 0, q_buf = 0, q_ph = 0, pph = 0, my_turn = 0;
             bool ok = true;
+            // The two warps take turns, so that the tensor cores finish one tile's products, then
+            // the other's, and not both at once: each softmax then has the SM's other units
+            // while the other tile's products run.  A turn is the weights' product with a key
+            // tile and the scores with the next.
+            auto take_turn = [&]() {
+                if (NQ == 1) return true;
+                const bool mine = wait_role(turn_bar0 + 8 * i, my_turn ^ (i == 0 ? 1u : 0u), abort_flag, p.status, p.wait_ns);
+                my_turn ^= 1u;
+                return mine;
+            };
+            auto pass_turn = [&]() {
+                __syncwarp();
+                if (NQ == 2 && lane == 0) mbar_arrive(turn_bar0 + 8 * (i ^ 1u));
+            };
             auto next = [&]() {
                 if (++slot == static_cast<uint32_t>(stages)) {
                     slot = 0;
@@ -534,7 +549,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                 if (lane == 0) mbar_arrive(job_empty0 + 8 * (k & 1u));
                 if (last) break;
                 if (count == 0) continue;
-                ok = wait_role(q_full0 + 8 * q_buf, q_ph, abort_flag, p.status, p.wait_ns);
+                ok = wait_role(q_full0 + 8 * q_buf, q_ph, abort_flag, p.status, p.wait_ns) && take_turn();
                 if (!ok) break;
                 const uint32_t q_at = q_low + q_buf * NQ * step;
                 uint32_t add = 0u;
@@ -557,8 +572,11 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                     }
                     commit_if(el, empty0 + 8 * slot);
                     if (n + 1 == count) commit_if(el, q_empty0 + 8 * q_buf);
+                    pass_turn();
                     next();
                     ok = wait_role(full0 + 8 * slot, ph, abort_flag, p.status, p.wait_ns);
+                    if (!ok) break;
+                    ok = take_turn();
                     if (!ok) break;
                     if (active) {
                         ok = wait_role(p_full, pph, abort_flag, p.status, p.wait_ns);
@@ -575,6 +593,8 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                     commit_if(el, empty0 + 8 * slot);
                     next();
                 }
+                if (!ok) break;
+                pass_turn();
                 if (++q_buf == static_cast<uint32_t>(q_bufs)) {
                     q_buf = 0;
                     q_ph ^= 1u;
