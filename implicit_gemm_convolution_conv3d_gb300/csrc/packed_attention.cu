@@ -9,8 +9,9 @@
 // tile, a row per thread, so that a row's maximum and sum need no exchange; the weights
 // go back as 16-bit words over S, where the second product O += P V takes them as its
 // first operand.  V is read as it lies in memory (its rows are the reduction).
-//   warp 0      finds the jobs; TMA producer: Q, then K and V tiles in a ring
+//   warp 0      TMA producer: Q, then K and V tiles in a ring
 //   warp 1      tensor memory; issues the first tile's products, warp 2 the second's
+//   warp 3      finds the jobs and plans them, up to four ahead
 //   warps 4-7   the first tile's rows: softmax, then the output; 8-11 the second's
 // The next job's loads and first scores run under the last softmax and the output of the
 // one before.
@@ -31,6 +32,8 @@ namespace {
 constexpr int kRows = 128;             // query rows and keys of a tile
 constexpr uint32_t kBoxBytes = 16384;  // 128 rows of 64 elements
 constexpr int kMaxStages = 8;
+constexpr uint32_t kJobs = 4;          // jobs planned ahead
+constexpr uint32_t kSmallBytes = 768;  // shared memory of the barriers and jobs
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLag = 8.0f;           // powers of two that weights may exceed 1 by
 
@@ -162,9 +165,16 @@ __device__ __forceinline__ float shaped(const PackedParams& p, float dot, int i,
     return s * kLog2e - slope2 * fabsf(static_cast<float>(i - j));
 }
 
+__device__ __forceinline__ uint32_t bits_below(int n) {
+    return static_cast<uint32_t>((1ull << min(max(n, 0), 32)) - 1ull);
+}
 struct RowMask {
     int lo, hi, lead, keys;
     __device__ bool operator()(int j) const { return j < keys && ((j >= lo && j < hi) || j < lead); }
+    // keys j .. j + 31 as bits
+    __device__ uint32_t bits(int j) const {
+        return ((bits_below(hi - j) & ~bits_below(lo - j)) | bits_below(lead - j)) & bits_below(keys - j);
+    }
 };
 __device__ __forceinline__ RowMask row_mask(const PackedParams& p, const Job& j, int row) {
     const Range r = range_of(p, j, row, row + 1);
@@ -227,12 +237,13 @@ __device__ __forceinline__ void redo_row(const PackedParams& p, const Job& job, 
 __device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
                                           int* status, unsigned long long limit_ns) {
     constexpr uint32_t kAll = 0xffffffffu;
-    if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
+    // (without a limit to wait for, nothing is waited for)
+    if (__all_sync(kAll, limit_ns ? mbar_try_wait(bar, parity) : mbar_test_wait(bar, parity))) return true;
     const long long t0 = clock64();
     const long long limit = static_cast<long long>(limit_ns > (1ull << 61) ? (1ull << 61) : limit_ns) * 2;
     while (true) {
         if (__any_sync(kAll, *abort_flag != 0u)) return false;
-        if (__any_sync(kAll, clock64() - t0 > limit)) {
+        if (__any_sync(kAll, clock64() - t0 >= limit)) {
             *abort_flag = 1u;
             atomicExch(status, kStatusTimeout);
             return false;
@@ -317,12 +328,12 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
     const uint32_t bars = ring + stages * tile_bytes;
     const uint32_t full0 = bars, empty0 = full0 + 8u * kMaxStages;
     const uint32_t q_full0 = empty0 + 8u * kMaxStages, q_empty0 = q_full0 + 16u;
-    const uint32_t job_full0 = q_empty0 + 16u, job_empty0 = job_full0 + 16u;
-    const uint32_t s_full0 = job_empty0 + 16u, p_full0 = s_full0 + 16u, o_done0 = p_full0 + 16u;
+    const uint32_t job_full0 = q_empty0 + 16u, job_empty0 = job_full0 + 8u * kJobs;
+    const uint32_t s_full0 = job_empty0 + 8u * kJobs, p_full0 = s_full0 + 16u, o_done0 = p_full0 + 16u;
     const uint32_t turn_bar0 = o_done0 + 16u, tail_bar = turn_bar0 + 16u, drain_bar = tail_bar + 8u;
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem_raw + (drain_bar + 8u - raw));
     // misc[0] TMEM base, [1] abort flag, [2] ring loads issued, [3] Q loads issued, [4] whether a
-    // last tile's values are on their way (1 + its phase); then two jobs
+    // last tile's values are on their way (1 + its phase), [5] to which slot; then the jobs
     volatile uint32_t* abort_flag = misc + 1;
     Job* jobs = reinterpret_cast<Job*>(misc + 6);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -335,12 +346,14 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full0 + 8 * i, 1);
             mbar_init(q_empty0 + 8 * i, NQ);
-            mbar_init(job_full0 + 8 * i, 1);
-            mbar_init(job_empty0 + 8 * i, 5 * NQ);
             mbar_init(s_full0 + 8 * i, 1);
             mbar_init(p_full0 + 8 * i, 4);
             mbar_init(o_done0 + 8 * i, 1);
             mbar_init(turn_bar0 + 8 * i, 1);
+        }
+        for (uint32_t i = 0; i < kJobs; ++i) {
+            mbar_init(job_full0 + 8 * i, 1);
+            mbar_init(job_empty0 + 8 * i, 1 + 5 * NQ);
         }
         mbar_init(tail_bar, 1);
         mbar_init(drain_bar, NQ);
@@ -367,18 +380,18 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
 
     if (warp < 4) {
         set_max_regs_dec<NQ == 2 ? 72 : 56>();
-        if (warp == 0) {
-            // documents are looked through 128 at a time, four a lane, and never twice
+        if (warp == 3) {
+            // Documents are looked through 128 at a time, four a lane, and never twice; a lane
+            // plans one of the CTA's next jobs, 32 in all.
             int s0 = -128, n[4] = {0, 0, 0, 0}, off[5] = {0, 0, 0, 0, 0}, mine = 0, run = 0;
             long long before = 0;
             int all = 0;   // jobs (of one head) of these 128
-            int st = 0;
-            uint32_t ph = 0, issued = 0, q_issued = 0, tails = 0;
             bool ok = true;
-            for (uint32_t k = 0; ok; ++k) {
-                const uint32_t at = blockIdx.x + k * gridDim.x;
+            for (uint32_t k = 0; ok;) {
+                const uint32_t at = blockIdx.x + (k + lane) * gridDim.x;
                 const uint32_t want = at / static_cast<uint32_t>(p.heads);
-                while (before + all <= want && s0 < p.documents) {
+                const uint32_t first = __shfl_sync(0xffffffffu, want, 0);
+                while (before + all <= first && s0 < p.documents) {
                     before += all;
                     s0 += 128;
 #pragma unroll
@@ -400,105 +413,147 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                     }
                     all = __shfl_sync(0xffffffffu, run, 31);
                 }
-                const bool more = before + all > want;
-                const uint32_t slot = k & 1u, jph = (k >> 1) & 1u;
-                ok = wait_role(job_empty0 + 8 * slot, jph ^ 1u, abort_flag, p.status, p.wait_ns);
-                if (!ok) break;
-                if (more) {
-                    const int in = static_cast<int>(want - before);
-                    const int src = __ffs(__ballot_sync(0xffffffffu, run > in)) - 1;
-                    if (lane == src) {
-                        // which of the lane's four documents, and which of its tiles
-                        int t = in - (run - mine), s = s0 + 4 * lane, count = n[0], q0 = off[0], q1 = off[1];
+                // the jobs among these documents: the first lanes'
+                const bool here = want - before < all;
+                const int count = __popc(__ballot_sync(0xffffffffu, here));
+                const int in = here ? static_cast<int>(want - before) : 0;
+                int src = 0;   // the lane whose four documents hold it
 #pragma unroll
-                        for (int i = 1; i < 4; ++i)
-                            if (t >= count) {
-                                t -= count;
-                                count = n[i];
-                                q0 = off[i];
-                                q1 = off[i + 1];
-                                ++s;
-                            } else {
-                                break;
-                            }
-                        Job job;
-                        job.rows = q1 - q0;
-                        job.row0 = (p.causal ? count - 1 - t : t) * NQ * kRows;   // the longest first
-                        const long long kb = min(max(static_cast<long long>(p.k_offsets[s]), 0ll), p.k_tokens);
-                        const long long ke = min(max(static_cast<long long>(p.k_offsets[s + 1]), kb), p.k_tokens);
-                        job.keys = static_cast<int>(ke - kb);
-                        job.shift = job.keys - job.rows;
-                        job.prefix = p.prefix ? min(max(p.prefix[s], 0), job.keys) : 0;
-                        job.q0 = q0;
-                        job.k0 = kb;
-                        job.head = static_cast<int>(at - want * static_cast<uint32_t>(p.heads));
-                        job.unused = 0;
-                        plan_tiles(p, job, NQ);
-                        jobs[slot] = job;
+                for (int d = 16; d > 0; d >>= 1)
+                    if (__shfl_sync(0xffffffffu, run, src + d - 1) <= in) src += d;
+                src = min(src, 31);
+                int t = in - (__shfl_sync(0xffffffffu, run, src) - __shfl_sync(0xffffffffu, mine, src));
+                int s = s0 + 4 * src, tiles = 0, q0 = 0, q1 = 0;
+                bool found = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = __shfl_sync(0xffffffffu, n[i], src);
+                    const int a = __shfl_sync(0xffffffffu, off[i], src), b = __shfl_sync(0xffffffffu, off[i + 1], src);
+                    if (found) continue;
+                    if (t < c) {
+                        found = true;
+                        tiles = c;
+                        q0 = a;
+                        q1 = b;
+                        s += i;
+                    } else {
+                        t -= c;
                     }
-                } else if (lane == 0) {
-                    jobs[slot].head = -1;
                 }
+                Job job;
+                job.head = -1;
+                if (here) {
+                    job.rows = q1 - q0;
+                    job.row0 = (p.causal ? tiles - 1 - t : t) * NQ * kRows;   // the longest first
+                    const long long kb = min(max(static_cast<long long>(p.k_offsets[s]), 0ll), p.k_tokens);
+                    const long long ke = min(max(static_cast<long long>(p.k_offsets[s + 1]), kb), p.k_tokens);
+                    job.keys = static_cast<int>(ke - kb);
+                    job.shift = job.keys - job.rows;
+                    job.prefix = p.prefix ? min(max(p.prefix[s], 0), job.keys) : 0;
+                    job.q0 = q0;
+                    job.k0 = kb;
+                    job.head = static_cast<int>(at - want * static_cast<uint32_t>(p.heads));
+                    job.unused = 0;
+                    plan_tiles(p, job, NQ);
+                }
+                const int post = max(count, 1);   // behind the last one, the word that it was
+                for (int l = 0; l < post; ++l, ++k) {
+                    const uint32_t slot = k % kJobs, jph = (k / kJobs) & 1u;
+                    ok = wait_role(job_empty0 + 8 * slot, jph ^ 1u, abort_flag, p.status, p.wait_ns);
+                    if (!ok) break;
+                    if (lane == l) jobs[slot] = job;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(job_full0 + 8 * slot);
+                }
+                if (count == 0) break;
+            }
+        } else if (warp == 0) {
+            int st = 0;
+            uint32_t ph = 0, issued = 0, q_buf = 0, q_ph = 0, q_issued = 0, tail_ph = 0;
+            bool ok = true;
+            // The keys of a tile behind the document's last are other documents': their scores are
+            // replaced, their values (times a weight of 0) have to be finite.  The last tile's
+            // values land on a barrier of their own and are cleared behind the last key before
+            // they are handed on; meanwhile the next job's loads go out.
+            int tail_first = -1;
+            uint32_t tail_slot = 0;
+            auto finish_tail = [&]() {
+                if (tail_first < 0) return true;
+                if (!wait_role(tail_bar, tail_ph, abort_flag, p.status, p.wait_ns)) return false;
+                const uint32_t dst = ring + tail_slot * tile_bytes;
+                for (int i = tail_first * 8 + lane; i < kRows * 8; i += 32)
+                    for (int b = 0; b < boxes; ++b)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + b * kBoxBytes + i * 16u), "r"(0u)
+                                     : "memory");
+                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(job_full0 + 8 * slot);
-                if (!more) break;
-                const Job job = jobs[slot];
+                if (lane == 0) {
+                    mbar_arrive(full0 + 8 * tail_slot);
+                    misc[4] = 0u;
+                }
+                tail_ph ^= 1u;
+                tail_first = -1;
+                return true;
+            };
+            // a wait that lets no tail wait longer than it has to
+            auto wait_free = [&](uint32_t bar, uint32_t parity) {
+                if (tail_first >= 0 && !__all_sync(0xffffffffu, mbar_test_wait(bar, parity)) && !finish_tail()) return false;
+                return wait_role(bar, parity, abort_flag, p.status, p.wait_ns);
+            };
+            for (uint32_t k = 0; ok; ++k) {
+                ok = wait_free(job_full0 + 8 * (k % kJobs), (k / kJobs) & 1u);
+                if (!ok) break;
+                const Job job = jobs[k % kJobs];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(job_empty0 + 8 * (k % kJobs));
+                if (job.head < 0) break;
                 if (job.count == 0) continue;
                 const int kv = job.head / p.group;
-                const uint32_t qb = q_issued % q_bufs, qph = (q_issued / q_bufs) & 1u;
-                ok = wait_role(q_empty0 + 8 * qb, qph ^ 1u, abort_flag, p.status, p.wait_ns);
+                ok = wait_free(q_empty0 + 8 * q_buf, q_ph ^ 1u);
                 if (!ok) break;
                 ++q_issued;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(q_full0 + 8 * qb, NQ * tile_bytes);
+                    mbar_arrive_expect_tx(q_full0 + 8 * q_buf, NQ * tile_bytes);
                     for (int i = 0; i < NQ; ++i)
                         for (int b = 0; b < boxes; ++b)
-                            tma_load_3d(q_smem + (qb * NQ + i) * tile_bytes + b * kBoxBytes, &q_map, q_full0 + 8 * qb,
+                            tma_load_3d(q_smem + (q_buf * NQ + i) * tile_bytes + b * kBoxBytes, &q_map, q_full0 + 8 * q_buf,
                                         b * 64, job.head, static_cast<int>(job.q0 + job.row0 + i * kRows));
                     misc[3] = q_issued;
+                }
+                if (++q_buf == static_cast<uint32_t>(q_bufs)) {
+                    q_buf = 0;
+                    q_ph ^= 1u;
                 }
                 for (int n2 = 0; n2 < 2 * job.count; ++n2) {
                     const bool value = n2 & 1;
                     const int t0 = job.key(n2 >> 1);
-                    // the keys of a tile behind the document's last are other documents': their scores
-                    // are replaced, their values (times a weight of 0) have to be finite
                     const bool tail = value && t0 + kRows > job.keys;
-                    ok = wait_role(empty0 + 8 * st, ph ^ 1u, abort_flag, p.status, p.wait_ns);
+                    ok = (!tail || finish_tail()) && wait_free(empty0 + 8 * st, ph ^ 1u);
                     if (!ok) break;
                     const uint32_t dst = ring + st * tile_bytes, bar = tail ? tail_bar : full0 + 8 * st;
+                    ++issued;
+                    if (tail) {
+                        tail_first = job.keys - t0;
+                        tail_slot = st;
+                    }
                     if (lane == 0) {
-                        misc[4] = tail ? 1u + (tails & 1u) : 0u;
+                        if (tail) {
+                            misc[4] = 1u + tail_ph;
+                            misc[5] = st;
+                        }
+                        misc[2] = issued;
                         mbar_arrive_expect_tx(bar, tile_bytes);
                         for (int b = 0; b < boxes; ++b)
                             tma_load_3d(dst + b * kBoxBytes, value ? &v_map : &k_map, bar, b * 64, kv,
                                         static_cast<int>(job.k0 + t0));
                     }
-                    if (tail) {
-                        ok = wait_role(tail_bar, tails & 1u, abort_flag, p.status, p.wait_ns);
-                        if (!ok) break;
-                        ++tails;
-                        const int first = job.keys - t0;
-                        for (int i = first * 8 + lane; i < kRows * 8; i += 32)
-                            for (int b = 0; b < boxes; ++b)
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + b * kBoxBytes +
-                                                                                             i * 16u),
-                                             "r"(0u)
-                                             : "memory");
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(full0 + 8 * st);
-                            misc[4] = 0u;
-                        }
-                    }
-                    ++issued;
-                    if (lane == 0) misc[2] = issued;
                     if (++st == stages) {
                         st = 0;
                         ph ^= 1u;
                     }
                 }
             }
+            if (ok) finish_tail();
         } else if (warp <= NQ) {
             // One warp a query tile, all lanes together and one of them issuing: addresses and
             // decisions then stay in uniform registers, which the instructions take them from.
@@ -539,14 +594,14 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                 }
             };
             for (uint32_t k = 0; ok; ++k) {
-                ok = wait_role(job_full0 + 8 * (k & 1u), (k >> 1) & 1u, abort_flag, p.status, p.wait_ns);
+                ok = wait_role(job_full0 + 8 * (k % kJobs), (k / kJobs) & 1u, abort_flag, p.status, p.wait_ns);
                 if (!ok) break;
-                const Job& job = jobs[k & 1u];
+                const Job& job = jobs[k % kJobs];
                 const int count = uniform(job.count);
                 const Seen seen{uniform(job.seen[i].lead), uniform(job.seen[i].lo), uniform(job.seen[i].hi)};
                 const bool last = uniform(job.head + 1) == 0;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(job_empty0 + 8 * (k & 1u));
+                if (lane == 0) mbar_arrive(job_empty0 + 8 * (k % kJobs));
                 if (last) break;
                 if (count == 0) continue;
                 ok = wait_role(q_full0 + 8 * q_buf, q_ph, abort_flag, p.status, p.wait_ns) && take_turn();
@@ -613,11 +668,11 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
         uint32_t turn = 0;   // this tile's units so far
         bool ok = true;
         for (uint32_t k = 0; ok; ++k) {
-            ok = wait_role(job_full0 + 8 * (k & 1u), (k >> 1) & 1u, abort_flag, p.status, p.wait_ns);
+            ok = wait_role(job_full0 + 8 * (k % kJobs), (k / kJobs) & 1u, abort_flag, p.status, p.wait_ns);
             if (!ok) break;
-            const Job job = jobs[k & 1u];
+            const Job job = jobs[k % kJobs];
             __syncwarp();
-            if (lane == 0) mbar_arrive(job_empty0 + 8 * (k & 1u));
+            if (lane == 0) mbar_arrive(job_empty0 + 8 * (k % kJobs));
             if (job.head < 0) break;
             const Seen mine = NQ == 2 && i == 1 ? job.seen[1] : job.seen[0];
             const int row = job.row0 + i * kRows + (warp & 3) * 32 + lane;
@@ -645,39 +700,50 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
 #pragma unroll
                 for (int h = 0; h < 4; ++h) tmem_ld_32x32b_x32(t_s + 32 * h, s[h]);
                 tmem_ld_wait();
+                // tanh(x) for |x| <= 3/4 as x times a polynomial in x^2, within 2.1e-7 (a
+                // least-squares fit reweighted towards equal errors): packed multiply-adds where
+                // the exponential's form takes two turns of the special-function unit a value.
+                // A score is then x times `co` in its square, in powers of two.
+                constexpr float kTanh[5] = {0.999997199f, -0.333230764f, 0.132260904f, -0.0492804274f, 0.0123188179f};
+                uint64_t co[5];
+                bool small = false;   // all scores of the warp's tile are within the polynomial's reach
                 if (MOD & kCap) {
-                    if (__any_sync(0xffffffffu, !(max128<true>(s) * fabsf(per_cap) <= 1.0f))) {
+                    small = __all_sync(0xffffffffu, max128<true>(s) * fabsf(per_cap) <= 0.75f);
+                    float f = cap2 * per_cap;
 #pragma unroll
-                        for (int h = 0; h < 4; ++h)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                s[h][e] = __float_as_uint(
-                                    cap2 - 2.0f * cap2 * rcp_approx(1.0f + ex2(__uint_as_float(s[h][e]) * (2.0f * kLog2e * per_cap))));
-                    } else {
-                        // tanh(x) for |x| <= 1 as x times a polynomial in x^2, within 2.5e-7 (a
-                        // least-squares fit reweighted towards equal errors): packed multiply-adds
-                        // where the exponential's form takes two turns of the special-function
-                        // unit a value
-                        constexpr float kTanh[6] = {0.99999684f,   -0.33324003f, 0.13253523f,
-                                                    -0.050972834f, 0.016114153f, -0.0028394549f};
-                        uint64_t co[6];
-                        float f = cap2 * per_cap;
-#pragma unroll
-                        for (int d = 0; d < 6; ++d) {
-                            co[d] = two(kTanh[d] * f);
-                            f *= per_cap * per_cap;
-                        }
-#pragma unroll
-                        for (int h = 0; h < 4; ++h)
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                const uint64_t x = two(s[h][e], s[h][e + 1]), u = mul2(x, x);
-                                uint64_t y = fma2(u, co[5], co[4]);
-#pragma unroll
-                                for (int d = 3; d >= 0; --d) y = fma2(u, y, co[d]);
-                                split(mul2(x, y), s[h][e], s[h][e + 1]);
-                            }
+                    for (int d = 0; d < 5; ++d) {
+                        co[d] = two(kTanh[d] * f);
+                        f *= per_cap * per_cap;
                     }
+                }
+                auto factor = [&](uint64_t x) {
+                    const uint64_t u = mul2(x, x);
+                    uint64_t y = fma2(u, co[4], co[3]);
+#pragma unroll
+                    for (int d = 2; d >= 0; --d) y = fma2(u, y, co[d]);
+                    return y;
+                };
+                auto capped = [&](float v) {
+                    return cap2 - 2.0f * cap2 * rcp_approx(1.0f + ex2(v * (2.0f * kLog2e * per_cap)));
+                };
+                // the cap alone keeps the order of scores: where all are seen their maximum is taken
+                // before it, and small ones go through it on their way into the exponent
+                const bool open = t0 + kRows <= job.keys &&
+                                  (t0 + kRows <= job.prefix || (t0 >= all_lo && t0 + kRows <= all_hi));
+                const bool late = MOD == kCap && small && open;
+                if ((MOD & kCap) && !small) {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) s[h][e] = __float_as_uint(capped(__uint_as_float(s[h][e])));
+                } else if ((MOD & kCap) && !late) {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const uint64_t x = two(s[h][e], s[h][e + 1]);
+                            split(mul2(x, factor(x)), s[h][e], s[h][e + 1]);
+                        }
                 }
                 if (MOD & kFar) {
                     const uint64_t f = two(MOD & kCap ? 1.0f : p.scale * kLog2e);
@@ -703,16 +769,22 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                                                                -slope2 * fabsf(rel + static_cast<float>(32 * h + e))));
                     }
                 }
-                const bool open = t0 + kRows <= job.keys &&
-                                  (t0 + kRows <= job.prefix || (t0 >= all_lo && t0 + kRows <= all_hi));
                 if (!open) {
 #pragma unroll
-                    for (int h = 0; h < 4; ++h)
+                    for (int h = 0; h < 4; ++h) {
+                        const uint32_t m = mask.bits(t0 + 32 * h);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (!mask(t0 + 32 * h + e)) s[h][e] = __float_as_uint(-INFINITY);
+                            if (!(m >> e & 1u)) s[h][e] = __float_as_uint(-INFINITY);
+                    }
                 }
-                const float top = max128<false>(s);
+                float top = max128<false>(s);
+                if (late) {
+                    uint32_t x, y;
+                    const uint64_t v = two(top);
+                    split(mul2(v, factor(v)), x, y);
+                    top = top == -INFINITY ? top : __uint_as_float(x);
+                }
                 if (fresh) {
                     ref = top;
                 } else if (__any_sync(0xffffffffu, top * c > ref * c + kLag)) {
@@ -735,19 +807,23 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                 fresh = false;
                 const uint64_t off = two(ref == -INFINITY ? 0.0f : -ref * c), cc = two(c);
                 uint64_t sums[2] = {0ull, 0ull};
+                auto weights = [&](auto exponent) {
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
+                    for (int h = 0; h < 4; ++h) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const uint64_t v = two(s[h][e], s[h][e + 1]);
-                        uint32_t x, y;
-                        split(MOD ? add2(v, off) : fma2(v, cc, off), x, y);
-                        const float px = ex2(__uint_as_float(x)), py = ex2(__uint_as_float(y));
-                        sums[e / 2 & 1] = add2(sums[e / 2 & 1], two(__float_as_uint(px), __float_as_uint(py)));
-                        s[h >> 1][(h & 1) * 16 + e / 2] = pack2<BF>(px, py);
+                        for (int e = 0; e < 32; e += 2) {
+                            uint32_t x, y;
+                            split(exponent(two(s[h][e], s[h][e + 1])), x, y);
+                            const float px = ex2(__uint_as_float(x)), py = ex2(__uint_as_float(y));
+                            sums[e / 2 & 1] = add2(sums[e / 2 & 1], two(__float_as_uint(px), __float_as_uint(py)));
+                            s[h >> 1][(h & 1) * 16 + e / 2] = pack2<BF>(px, py);
+                        }
+                        if (h == 1) tmem_st_32x32b_x32(t_s, s[0]);
                     }
-                    if (h == 1) tmem_st_32x32b_x32(t_s, s[0]);
-                }
+                };
+                if (MOD == 0) weights([&](uint64_t v) { return fma2(v, cc, off); });
+                else if (late) weights([&](uint64_t v) { return fma2(v, factor(v), off); });
+                else weights([&](uint64_t v) { return add2(v, off); });
                 tmem_st_32x32b_x32(t_s + 32, s[1]);
                 {
                     uint32_t x, y;
@@ -771,32 +847,43 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
             uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) + (job.q0 + row) * p.out_tok +
                             static_cast<long long>(job.head) * p.out_head;
             bool odd = false;
-            for (int d = 0; d < p.width; d += 16) {
-                uint32_t o[2][8];
-                if (!fresh) {
-                    tmem_ld_32x32b_x8(t_o + d, o[0]);
-                    tmem_ld_32x32b_x8(t_o + d + 8, o[1]);
+#pragma unroll 1
+            for (int d = 0; d < p.width; d += 32) {
+                uint32_t o[32];
+                if (fresh) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0u;
+                } else {
+                    tmem_ld_32x32b_x32(t_o + d, o);
                     tmem_ld_wait();
                 }
-                uint32_t w[8];
+                // (a row that saw nothing has a sum of 0, whatever its products are)
+                const int left = p.width - d;
+                uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float x = inv != 0.0f ? __uint_as_float(o[e >> 2][2 * (e & 3)]) * inv : 0.0f;
-                    const float y = inv != 0.0f ? __uint_as_float(o[e >> 2][2 * (e & 3) + 1]) * inv : 0.0f;
-                    odd = odd || (d + 2 * e < p.width && !(fabsf(x) + fabsf(y) < INFINITY));
+                for (int e = 0; e < 16; ++e) {
+                    const float x = inv == 0.0f ? 0.0f : __uint_as_float(o[2 * e]) * inv;
+                    const float y = inv == 0.0f ? 0.0f : __uint_as_float(o[2 * e + 1]) * inv;
+                    odd = odd || (2 * e < left && !(fabsf(x) + fabsf(y) < INFINITY));
                     w[e] = pack2<BF>(x, y);
                 }
-                const int left = p.width - d;
-                if (valid && left >= 16 && p.out_aligned == 32) {
-                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + d), "r"(w[0]),
-                                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                                 : "memory");
-                } else if (valid && p.out_aligned) {
-                    *reinterpret_cast<uint4*>(dst + d) = make_uint4(w[0], w[1], w[2], w[3]);
-                    if (left >= 16) *reinterpret_cast<uint4*>(dst + d + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-                } else if (valid) {
+                __syncwarp();
+                if (!valid) {
+                } else if (p.out_aligned == 32 && left >= 32) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
+                    for (int e = 0; e < 16; e += 8)
+                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + d + 2 * e),
+                                     "r"(w[e]), "r"(w[e + 1]), "r"(w[e + 2]), "r"(w[e + 3]), "r"(w[e + 4]),
+                                     "r"(w[e + 5]), "r"(w[e + 6]), "r"(w[e + 7])
+                                     : "memory");
+                } else if (p.out_aligned) {
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        if (2 * e < left)
+                            *reinterpret_cast<uint4*>(dst + d + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
                         if (e < left) dst[d + e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
                 }
                 __syncwarp();
@@ -811,7 +898,10 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
     if (*abort_flag) {
         // drain: the loads, then the MMAs in flight
         if (threadIdx.x == 0) {
-            if (misc[4]) drain_here(tail_bar, misc[4] - 1u);
+            if (misc[4]) {
+                drain_here(tail_bar, misc[4] - 1u);
+                mbar_arrive(full0 + 8 * misc[5]);
+            }
             drain_slots(q_full0, misc[3], q_bufs);
             drain_slots(full0, misc[2], stages);
         }
@@ -831,11 +921,11 @@ template <bool BF, int NQ, int MOD>
 cudaError_t run(const PackedMaps& maps, const PackedParams& p, int num_sms, cudaStream_t stream) {
     const uint32_t tile = static_cast<uint32_t>((p.width + 63) / 64) * kBoxBytes;
     // shared memory of the SM, or half of it for two CTAs; Q twice where tiles are small
-    const uint32_t room = (NQ == 2 ? 232448u : 115200u) - 1024u - 640u;
+    const uint32_t room = (NQ == 2 ? 232448u : 115200u) - 1024u - kSmallBytes;
     const int q_bufs = tile == kBoxBytes ? 2 : 1;
     int stages = static_cast<int>((room - q_bufs * NQ * tile) / tile);
     if (stages > kMaxStages) stages = kMaxStages;
-    const size_t smem = 1024u + (q_bufs * NQ + stages) * tile + 640u;
+    const size_t smem = 1024u + (q_bufs * NQ + stages) * tile + kSmallBytes;
     static std::atomic<int> slots[kMaxDevices];
     cudaError_t e = ensure_dynamic_smem(packed_kernel<BF, NQ, MOD>, smem, slots);
     if (e != cudaSuccess) return e;
@@ -858,8 +948,8 @@ cudaError_t by_mod(const PackedMaps& maps, const PackedParams& p, int num_sms, c
 cudaError_t launch_packed(const PackedMaps& maps, const PackedParams& p, int dtype, int num_sms,
                           cudaStream_t stream) {
     const bool bf = dtype == kTokBf16;
-    // two tiles where documents are long and there are jobs enough for all SMs
-    const bool two_tiles = p.q_tokens / p.documents >= 1024 && p.q_tokens / 256 * p.heads >= num_sms;
+    // two tiles where documents have them and there are jobs enough for all SMs
+    const bool two_tiles = p.q_tokens / p.documents > kRows && p.q_tokens / 256 * p.heads >= num_sms;
     if (two_tiles) return bf ? by_mod<true, 2>(maps, p, num_sms, stream) : by_mod<false, 2>(maps, p, num_sms, stream);
     return bf ? by_mod<true, 1>(maps, p, num_sms, stream) : by_mod<false, 1>(maps, p, num_sms, stream);
 }
