@@ -106,13 +106,6 @@ __device__ __forceinline__ void plan_tiles(const PackedParams& p, Job& j, int nq
     }
 }
 
-template <bool BF>
-__device__ bool finite_row(const unsigned char* v, long long at, int width) {
-    for (int d = 0; d < width; ++d)
-        if (!(fabsf(elem<BF>(v, at + d)) <= 3.4e38f)) return false;
-    return true;
-}
-
 // Two values a register pair: one instruction each
 __device__ __forceinline__ uint64_t two(uint32_t a, uint32_t b) {
     uint64_t r;
@@ -183,47 +176,55 @@ __device__ __forceinline__ RowMask row_mask(const PackedParams& p, const Job& j,
 
 // A row whose result is not finite although what it sees may be: an unseen key of a
 // tile that was multiplied (weight 0) has a value that is not finite.  Then the row is
-// computed again, over what it sees alone.
+// computed again, over what it sees alone.  Rolled loops: it should not take the
+// instruction cache from the others.
 template <bool BF>
 __device__ __forceinline__ void redo_row(const PackedParams& p, const Job& job, const Seen& seen, int row) {
     const int kv = job.head / p.group;
     const RowMask m = row_mask(p, job, row);
     const long long vbase = job.k0 * p.k_tok + static_cast<long long>(kv) * p.k_head;
-    bool spoiled = false;
-    for (int n = 0; n < job.count && !spoiled; ++n) {
-        const int t0 = job.key(n);
-        if (!seen(n)) continue;
-        for (int j = t0; j < min(t0 + kRows, job.keys) && !spoiled; ++j)
-            if (!m(j)) spoiled = !finite_row<BF>(p.v, vbase + j * p.k_tok, p.width);
-    }
-    if (!spoiled) return;
     const long long qb = (job.q0 + row) * p.q_tok + static_cast<long long>(job.head) * p.q_head;
     const float slope2 = p.slopes ? p.slopes[job.head] * kLog2e : 0.0f;
-    auto score = [&](int j) {
-        float s = 0.0f;
-        for (int d = 0; d < p.width; ++d) s += elem<BF>(p.q, qb + d) * elem<BF>(p.k, vbase + j * p.k_tok + d);
-        return shaped(p, s, row + job.shift, j, slope2);
-    };
     float top = -INFINITY, sum = 0.0f, o[128];
-    bool nan = false;
-    for (int pass = 0; pass < 2 && !nan; ++pass) {
-        if (pass)
-            for (int d = 0; d < p.width; ++d) o[d] = 0.0f;
-        for (int part = 0; part < 2; ++part)
-            for (int j = part ? max(m.lo, m.lead) : 0; j < (part ? m.hi : min(m.lead, m.keys)); ++j) {
-                const float s = score(j);
-                if (!pass) {
+    bool spoiled = false, nan = false;
+#pragma unroll 1
+    for (int d = 0; d < p.width; ++d) o[d] = 0.0f;
+    // pass 0: is an unseen key's value the cause?  1: the maximum, 2: the sums
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        if ((pass && !spoiled) || nan) break;
+#pragma unroll 1
+        for (int n = 0; n < job.count; ++n) {
+            if (!seen(n)) continue;
+            const int t0 = job.key(n);
+#pragma unroll 1
+            for (int j = t0; j < min(t0 + kRows, job.keys); ++j) {
+                if (m(j) != (pass != 0)) continue;
+                const long long at = vbase + j * p.k_tok;
+                float s = 0.0f;
+                if (pass) {
+#pragma unroll 1
+                    for (int d = 0; d < p.width; ++d) s += elem<BF>(p.q, qb + d) * elem<BF>(p.k, at + d);
+                    s = shaped(p, s, row + job.shift, j, slope2);
                     nan = nan || !(s < INFINITY);
-                    top = fmaxf(top, s);
-                } else if (top > -INFINITY) {
-                    const float w = ex2(s - top);
-                    sum += w;
-                    for (int d = 0; d < p.width; ++d) o[d] += w * elem<BF>(p.v, vbase + j * p.k_tok + d);
+                    if (pass == 1) top = fmaxf(top, s);
+                    s = top == -INFINITY ? 0.0f : ex2(s - top);
+                    if (pass == 2) sum += s;
+                }
+                if (pass == 1) continue;
+#pragma unroll 1
+                for (int d = 0; d < p.width; ++d) {
+                    const float v = elem<BF>(p.v, at + d);
+                    if (pass == 0) spoiled = spoiled || !(fabsf(v) < INFINITY);
+                    else o[d] += s * v;
                 }
             }
+        }
     }
+    if (!spoiled) return;
     uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) + (job.q0 + row) * p.out_tok +
                     static_cast<long long>(job.head) * p.out_head;
+#pragma unroll 1
     for (int d = 0; d < p.width; ++d) {
         const float v = nan ? __uint_as_float(kNanBits) : sum == 0.0f ? 0.0f : o[d] / sum;
         dst[d] = static_cast<uint16_t>(pack2<BF>(v, 0.0f));
@@ -235,21 +236,15 @@ __device__ __forceinline__ void redo_row(const PackedParams& p, const Job& job, 
 // looks, so that its polling leaves the issue slots to the others.  Whole warps wait, with
 // one answer for all lanes.
 __device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
-                                          int* status, unsigned long long limit_ns) {
+                                          int* status, long long limit_cycles) {
     constexpr uint32_t kAll = 0xffffffffu;
     // (without a limit to wait for, nothing is waited for)
-    if (__all_sync(kAll, limit_ns ? mbar_try_wait(bar, parity) : mbar_test_wait(bar, parity))) return true;
+    if (__all_sync(kAll, limit_cycles ? mbar_try_wait(bar, parity) : mbar_test_wait(bar, parity))) return true;
     const long long t0 = clock64();
-    const long long limit = static_cast<long long>(limit_ns > (1ull << 61) ? (1ull << 61) : limit_ns) * 2;
-    while (true) {
-        if (__any_sync(kAll, *abort_flag != 0u)) return false;
-        if (__any_sync(kAll, clock64() - t0 >= limit)) {
-            *abort_flag = 1u;
-            atomicExch(status, kStatusTimeout);
-            return false;
-        }
+    while (!__any_sync(kAll, *abort_flag != 0u || clock64() - t0 >= limit_cycles))
         if (__all_sync(kAll, mbar_try_wait_for(bar, parity, 20000u))) return true;
-    }
+    if (atomicExch(const_cast<uint32_t*>(abort_flag), 1u) == 0u) atomicExch(status, kStatusTimeout);
+    return false;
 }
 __device__ __forceinline__ void drain_here(uint32_t bar, uint32_t parity) {
     const uint64_t t0 = globaltimer_ns();
@@ -337,6 +332,8 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
     volatile uint32_t* abort_flag = misc + 1;
     Job* jobs = reinterpret_cast<Job*>(misc + 6);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (two cycles a nanosecond, as in wait_bar)
+    const long long limit = static_cast<long long>(p.wait_ns > (1ull << 61) ? (1ull << 61) : p.wait_ns) * 2;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) {
@@ -459,7 +456,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                 const int post = max(count, 1);   // behind the last one, the word that it was
                 for (int l = 0; l < post; ++l, ++k) {
                     const uint32_t slot = k % kJobs, jph = (k / kJobs) & 1u;
-                    ok = wait_role(job_empty0 + 8 * slot, jph ^ 1u, abort_flag, p.status, p.wait_ns);
+                    ok = wait_role(job_empty0 + 8 * slot, jph ^ 1u, abort_flag, p.status, limit);
                     if (!ok) break;
                     if (lane == l) jobs[slot] = job;
                     __syncwarp();
@@ -479,9 +476,11 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
             uint32_t tail_slot = 0;
             auto finish_tail = [&]() {
                 if (tail_first < 0) return true;
-                if (!wait_role(tail_bar, tail_ph, abort_flag, p.status, p.wait_ns)) return false;
+                if (!wait_role(tail_bar, tail_ph, abort_flag, p.status, limit)) return false;
                 const uint32_t dst = ring + tail_slot * tile_bytes;
+#pragma unroll 1
                 for (int i = tail_first * 8 + lane; i < kRows * 8; i += 32)
+#pragma unroll 1
                     for (int b = 0; b < boxes; ++b)
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + b * kBoxBytes + i * 16u), "r"(0u)
                                      : "memory");
@@ -495,45 +494,52 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                 tail_first = -1;
                 return true;
             };
-            // a wait that lets no tail wait longer than it has to
-            auto wait_free = [&](uint32_t bar, uint32_t parity) {
-                if (tail_first >= 0 && !__all_sync(0xffffffffu, mbar_test_wait(bar, parity)) && !finish_tail()) return false;
-                return wait_role(bar, parity, abort_flag, p.status, p.wait_ns);
-            };
+            // (a job's queries and first keys do not depend on the tail before)
             for (uint32_t k = 0; ok; ++k) {
-                ok = wait_free(job_full0 + 8 * (k % kJobs), (k / kJobs) & 1u);
+                ok = wait_role(job_full0 + 8 * (k % kJobs), (k / kJobs) & 1u, abort_flag, p.status, limit);
                 if (!ok) break;
-                const Job job = jobs[k % kJobs];
+                const Job& shared = jobs[k % kJobs];
+                const int head = shared.head, keys = shared.keys, lead_tiles = shared.lead_tiles, skip = shared.skip;
+                const int q_row = static_cast<int>(shared.q0) + shared.row0, k_row = static_cast<int>(shared.k0);
+                const int count = head < 0 ? 0 : shared.count, kv = head / p.group;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(job_empty0 + 8 * (k % kJobs));
-                if (job.head < 0) break;
-                if (job.count == 0) continue;
-                const int kv = job.head / p.group;
-                ok = wait_free(q_empty0 + 8 * q_buf, q_ph ^ 1u);
-                if (!ok) break;
-                ++q_issued;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(q_full0 + 8 * q_buf, NQ * tile_bytes);
-                    for (int i = 0; i < NQ; ++i)
-                        for (int b = 0; b < boxes; ++b)
+                if (count) {
+                    ok = wait_role(q_empty0 + 8 * q_buf, q_ph ^ 1u, abort_flag, p.status, limit);
+                    if (!ok) break;
+                    ++q_issued;
+                    if (lane == 0) {
+                        misc[3] = q_issued;
+                        mbar_arrive_expect_tx(q_full0 + 8 * q_buf, NQ * tile_bytes);
+#pragma unroll 1
+                        for (int t = 0; t < NQ * boxes; ++t) {
+                            const int i = boxes == 1 ? t : t >> 1, b = boxes == 1 ? 0 : t & 1;
                             tma_load_3d(q_smem + (q_buf * NQ + i) * tile_bytes + b * kBoxBytes, &q_map, q_full0 + 8 * q_buf,
-                                        b * 64, job.head, static_cast<int>(job.q0 + job.row0 + i * kRows));
-                    misc[3] = q_issued;
+                                        b * 64, head, q_row + i * kRows);
+                        }
+                    }
+                    if (++q_buf == static_cast<uint32_t>(q_bufs)) {
+                        q_buf = 0;
+                        q_ph ^= 1u;
+                    }
                 }
-                if (++q_buf == static_cast<uint32_t>(q_bufs)) {
-                    q_buf = 0;
-                    q_ph ^= 1u;
-                }
-                for (int n2 = 0; n2 < 2 * job.count; ++n2) {
+#pragma unroll 1
+                for (int n2 = 0; n2 < 2 * max(count, 1); ++n2) {
                     const bool value = n2 & 1;
-                    const int t0 = job.key(n2 >> 1);
-                    const bool tail = value && t0 + kRows > job.keys;
-                    ok = (!tail || finish_tail()) && wait_free(empty0 + 8 * st, ph ^ 1u);
+                    if (value && !finish_tail()) {
+                        ok = false;
+                        break;
+                    }
+                    if (!count) continue;
+                    const int n = n2 >> 1, t0 = (n < lead_tiles ? n : n - lead_tiles + skip) * kRows;
+                    const bool tail = value && t0 + kRows > keys;
+                    ok = wait_role(empty0 + 8 * st, ph ^ 1u, abort_flag, p.status, limit);
                     if (!ok) break;
                     const uint32_t dst = ring + st * tile_bytes, bar = tail ? tail_bar : full0 + 8 * st;
+                    const void* map = value ? &v_map : &k_map;
                     ++issued;
                     if (tail) {
-                        tail_first = job.keys - t0;
+                        tail_first = keys - t0;
                         tail_slot = st;
                     }
                     if (lane == 0) {
@@ -543,17 +549,16 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                         }
                         misc[2] = issued;
                         mbar_arrive_expect_tx(bar, tile_bytes);
-                        for (int b = 0; b < boxes; ++b)
-                            tma_load_3d(dst + b * kBoxBytes, value ? &v_map : &k_map, bar, b * 64, kv,
-                                        static_cast<int>(job.k0 + t0));
+                        tma_load_3d(dst, map, bar, 0, kv, k_row + t0);
+                        if (boxes == 2) tma_load_3d(dst + kBoxBytes, map, bar, 64, kv, k_row + t0);
                     }
                     if (++st == stages) {
                         st = 0;
                         ph ^= 1u;
                     }
                 }
+                if (head < 0) break;
             }
-            if (ok) finish_tail();
         } else if (warp <= NQ) {
             // One warp a query tile, all lanes together and one of them issuing: addresses and
             // decisions then stay in uniform registers, which the instructions take them from.
@@ -579,7 +584,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
             // tile and the scores with the next.
             auto take_turn = [&]() {
                 if (NQ == 1) return true;
-                const bool mine = wait_role(turn_bar0 + 8 * i, my_turn ^ (i == 0 ? 1u : 0u), abort_flag, p.status, p.wait_ns);
+                const bool mine = wait_role(turn_bar0 + 8 * i, my_turn ^ (i == 0 ? 1u : 0u), abort_flag, p.status, limit);
                 my_turn ^= 1u;
                 return mine;
             };
@@ -594,7 +599,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                 }
             };
             for (uint32_t k = 0; ok; ++k) {
-                ok = wait_role(job_full0 + 8 * (k % kJobs), (k / kJobs) & 1u, abort_flag, p.status, p.wait_ns);
+                ok = wait_role(job_full0 + 8 * (k % kJobs), (k / kJobs) & 1u, abort_flag, p.status, limit);
                 if (!ok) break;
                 const Job& job = jobs[k % kJobs];
                 const int count = uniform(job.count);
@@ -604,14 +609,14 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                 if (lane == 0) mbar_arrive(job_empty0 + 8 * (k % kJobs));
                 if (last) break;
                 if (count == 0) continue;
-                ok = wait_role(q_full0 + 8 * q_buf, q_ph, abort_flag, p.status, p.wait_ns) && take_turn();
+                ok = wait_role(q_full0 + 8 * q_buf, q_ph, abort_flag, p.status, limit) && take_turn();
                 if (!ok) break;
                 const uint32_t q_at = q_low + q_buf * NQ * step;
                 uint32_t add = 0u;
 #pragma unroll 1
                 for (int n = 0; n < count; ++n) {
                     const bool active = seen(n);
-                    ok = wait_role(full0 + 8 * slot, ph, abort_flag, p.status, p.wait_ns);
+                    ok = wait_role(full0 + 8 * slot, ph, abort_flag, p.status, limit);
                     if (!ok) break;
                     if (active) {
                         // (the scores before were read, and their weights multiplied, by then)
@@ -629,12 +634,12 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                     if (n + 1 == count) commit_if(el, q_empty0 + 8 * q_buf);
                     pass_turn();
                     next();
-                    ok = wait_role(full0 + 8 * slot, ph, abort_flag, p.status, p.wait_ns);
+                    ok = wait_role(full0 + 8 * slot, ph, abort_flag, p.status, limit);
                     if (!ok) break;
                     ok = take_turn();
                     if (!ok) break;
                     if (active) {
-                        ok = wait_role(p_full, pph, abort_flag, p.status, p.wait_ns);
+                        ok = wait_role(p_full, pph, abort_flag, p.status, limit);
                         if (!ok) break;
                         pph ^= 1u;
                         tc_fence_after();
@@ -668,7 +673,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
         uint32_t turn = 0;   // this tile's units so far
         bool ok = true;
         for (uint32_t k = 0; ok; ++k) {
-            ok = wait_role(job_full0 + 8 * (k % kJobs), (k / kJobs) & 1u, abort_flag, p.status, p.wait_ns);
+            ok = wait_role(job_full0 + 8 * (k % kJobs), (k / kJobs) & 1u, abort_flag, p.status, limit);
             if (!ok) break;
             const Job job = jobs[k % kJobs];
             __syncwarp();
@@ -693,7 +698,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
             for (int n = 0; n < job.count; ++n) {
                 const int t0 = job.key(n);
                 if (!mine(n)) continue;
-                ok = wait_role(s_full0 + 8 * i, turn & 1u, abort_flag, p.status, p.wait_ns);
+                ok = wait_role(s_full0 + 8 * i, turn & 1u, abort_flag, p.status, limit);
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t s[4][32];
@@ -788,13 +793,14 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                 if (fresh) {
                     ref = top;
                 } else if (__any_sync(0xffffffffu, top * c > ref * c + kLag)) {
-                    ok = wait_role(o_done0 + 8 * i, (turn - 1) & 1u, abort_flag, p.status, p.wait_ns);
+                    ok = wait_role(o_done0 + 8 * i, (turn - 1) & 1u, abort_flag, p.status, limit);
                     if (!ok) break;
                     tc_fence_after();
                     const float now = fmaxf(ref, top);
                     const float f = now == -INFINITY ? 1.0f : ex2((ref - now) * c);
                     ref = now;
                     sum *= f;
+#pragma unroll 1
                     for (uint32_t d = 0; d < o_pitch; d += 8) {
                         uint32_t o[8];
                         tmem_ld_32x32b_x8(t_o + d, o);
@@ -838,7 +844,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
             }
             if (!ok) break;
             if (!fresh) {
-                ok = wait_role(o_done0 + 8 * i, (turn - 1) & 1u, abort_flag, p.status, p.wait_ns);
+                ok = wait_role(o_done0 + 8 * i, (turn - 1) & 1u, abort_flag, p.status, limit);
                 if (!ok) break;
                 tc_fence_after();
             }
