@@ -852,7 +852,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
             const float inv = fresh || sum == 0.0f ? 0.0f : 1.0f / sum;
             uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) + (job.q0 + row) * p.out_tok +
                             static_cast<long long>(job.head) * p.out_head;
-            bool odd = false;
+            float odd = 0.0f;   // becomes NaN with the first result that is not finite
 #pragma unroll 1
             for (int d = 0; d < p.width; d += 32) {
                 uint32_t o[32];
@@ -868,9 +868,10 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                 uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float x = inv == 0.0f ? 0.0f : __uint_as_float(o[2 * e]) * inv;
-                    const float y = inv == 0.0f ? 0.0f : __uint_as_float(o[2 * e + 1]) * inv;
-                    odd = odd || (2 * e < left && !(fabsf(x) + fabsf(y) < INFINITY));
+                    const bool none = inv == 0.0f || 2 * e >= left;
+                    const float x = none ? 0.0f : __uint_as_float(o[2 * e]) * inv;
+                    const float y = none ? 0.0f : __uint_as_float(o[2 * e + 1]) * inv;
+                    odd = fmaf(x, 0.0f, fmaf(y, 0.0f, odd));
                     w[e] = pack2<BF>(x, y);
                 }
                 __syncwarp();
@@ -894,7 +895,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                 }
                 __syncwarp();
             }
-            if (valid && odd) redo_row<BF>(p, job, mine, row);
+            if (valid && odd != 0.0f) redo_row<BF>(p, job, mine, row);
             __syncwarp();
             tc_fence_before();
         }
