@@ -52,7 +52,8 @@ struct CacheParams {
     long long tokens;
     int sequences, heads, width;
     int aligned;   // the rows take 16-byte accesses
-    FastDiv by_units;
+    int parts;     // groups of lanes that share a token's rows (filled at launch)
+    FastDiv by_parts, by_runs;
 };
 cudaError_t launch_cache_write(const CacheParams& p, int row_dtype, int cache_dtype,
                                cudaStream_t stream);

@@ -3,12 +3,15 @@
 // Writing takes each row's largest magnitude, scale = max / qmax, and stores the
 // nearest codes (the rules of token_common.cuh: the same codes and scales as
 // act_quant_fwd); reading multiplies codes by their scale and rounds once.
-// Memory-bound: every row is read and written once.  A row is a group of 8, 16 or
-// 32 lanes with 8 elements each, so a row's maximum takes three to five shuffles
-// and nothing leaves the warp; keys and values are rows of one launch.
+// Memory-bound: every row is read and written once.  To write, a row is a group of 8, 10,
+// 16 or 32 lanes with 8 elements each, so a row's maximum takes three to five shuffles
+// and nothing leaves the warp; keys and values are rows of one launch, and a group
+// takes several of a token's rows at once.
 #include "attention_internal.h"
 #include "paging.cuh"
 #include "token_common.cuh"
+
+#include <type_traits>
 
 namespace c3d {
 
@@ -16,171 +19,349 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Eight elements of a row as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const T* src, int count, bool aligned, float (&v)[8]) {
-    if (aligned && count >= 8) {
-        constexpr int W = 16 / sizeof(T);
-        alignas(16) T e[8];
+struct Raw {
+    uint32_t w[2 * sizeof(T)];
+};
+
+template <typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* src, int count, bool aligned) {
+    Raw<T> r;
+    if (aligned) {
 #pragma unroll
-        for (int i = 0; i < 8 / W; ++i)
-            reinterpret_cast<uint4*>(e)[i] = reinterpret_cast<const uint4*>(src)[i];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_f32(e[i]);
+        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
+            const uint4 v = reinterpret_cast<const uint4*>(src)[i];
+            r.w[4 * i] = v.x;
+            r.w[4 * i + 1] = v.y;
+            r.w[4 * i + 2] = v.z;
+            r.w[4 * i + 3] = v.w;
+        }
     } else {
+        T* e = reinterpret_cast<T*>(r.w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < count ? to_f32(src[i]) : 0.0f;
+        for (int i = 0; i < 8; ++i) e[i] = i < count ? src[i] : from_f32<T>(0.0f);
     }
+    return r;
 }
 
 template <typename T>
-__device__ __forceinline__ void store8(T* dst, int count, bool aligned, const float (&v)[8]) {
+__device__ __forceinline__ void widen8(const Raw<T>& r, float (&v)[8]) {
+    const T* e = reinterpret_cast<const T*>(r.w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f32(e[i]);
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* dst, bool aligned, const float (&v)[8]) {
     alignas(16) T e[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) e[i] = from_f32<T>(v[i]);
-    if (aligned && count >= 8) {
-        constexpr int W = 16 / sizeof(T);
+    if (aligned) {
 #pragma unroll
-        for (int i = 0; i < 8 / W; ++i)
+        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
             reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(e)[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < count) dst[i] = e[i];
+        for (int i = 0; i < 8; ++i) dst[i] = e[i];
     }
 }
 
-// The unit of a group of lanes: a token's key or value row of one head.  A warp's
-// groups are neighbours; `first` is the warp's first unit.
+// The unit of a group of G lanes: one of `parts` shares of a token's 2 * heads rows (the
+// keys' heads, then the values').  One look at the offsets and the table serves it.
 struct Unit {
-    long long token, pos;
-    int head, value, sequence;
-    bool in;   // belongs to a sequence
+    long long token, row, scale;   // row, scale: of head 0 in the pool
+    int part;
+    bool in, there;                // belongs to a sequence; has a page
 };
 
 template <int G>
-__device__ __forceinline__ Unit unit_of(const CacheParams& p, long long first) {
+__device__ __forceinline__ Unit unit_of(const CacheParams& p) {
+    const long long first =
+        (static_cast<long long>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32) * (32 / G);
     Unit u;
-    const int per = 2 * p.heads;
-    const long long token0 = first / per;
-    const uint32_t at = static_cast<uint32_t>(first - token0 * per) + (threadIdx.x & 31) / G;
-    const uint32_t more = fdiv(at, p.by_units);
-    const int k = static_cast<int>(at - more * per);
+    const long long token0 = first / p.parts;
+    const uint32_t group = (threadIdx.x & 31) / G;
+    const uint32_t at = static_cast<uint32_t>(first - token0 * p.parts) + group;
+    const uint32_t more = fdiv(at, p.by_parts);
     u.token = token0 + more;
-    u.value = k >= p.heads;
-    u.head = u.value ? k - p.heads : k;
-    u.in = u.token < p.tokens;
+    u.part = static_cast<int>(at - more * p.parts);
+    u.in = u.token < p.tokens && group < 32 / G;   // (ten lanes a row leave two over)
+    u.row = u.scale = 0;
+    long long sequence = u.token, pos = 0;
     if (!p.offsets) {
-        u.sequence = static_cast<int>(u.token);
-        u.pos = u.in ? p.starts[u.token] : 0;
-        return u;
+        if (u.in) pos = p.starts[u.token];
+    } else {
+        int s = find_sequence(p.offsets, p.sequences, token0);
+        while (s + 1 < p.sequences && p.offsets[s + 1] <= u.token) ++s;
+        const long long begin = p.offsets[s], end = p.offsets[s + 1];
+        u.in = u.in && u.token >= begin && u.token < end;
+        sequence = s;
+        pos = u.token - begin + (p.starts ? p.starts[s] : 0);
     }
-    int s = find_sequence(p.offsets, p.sequences, token0);
-    while (s + 1 < p.sequences && p.offsets[s + 1] <= u.token) ++s;
-    u.sequence = s;
-    const long long begin = p.offsets[s];
-    u.in = u.in && u.token >= begin && u.token < p.offsets[s + 1];
-    u.pos = u.token - begin + (p.starts && u.in ? p.starts[s] : 0);
+    u.there = u.in && token_row(p.map, sequence, pos, 0, &u.row, &u.scale);
     return u;
 }
 
-template <typename T, int CACHE, int G>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ CacheParams p) {
-    griddep_launch_dependents();
-    griddep_wait();
-    const long long first =
-        (static_cast<long long>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32) * (32 / G);
-    const Unit u = unit_of<G>(p, first);
-    const int e = (threadIdx.x % G) * 8;
-    const int count = p.width - e;   // elements of this lane (0 or less: none)
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    if (u.in && count > 0)
-        load8(reinterpret_cast<const T*>(u.value ? p.rows_v : p.rows_k) + u.token * p.tok_stride +
-                  u.head * p.head_stride + e,
-              count, p.aligned, v);
-    long long row = 0, at = 0;
-    const bool there = u.in && token_row(p.map, u.sequence, u.pos, u.head, &row, &at);
-    unsigned char* dst = (u.value ? p.v : p.k) + row;
-    if (CACHE == kTokBf16 || CACHE == kTokF16) {
-        if (there && count > 0) store8(reinterpret_cast<T*>(dst) + e, 8, true, v);
-    } else {
-        constexpr bool E4 = CACHE == kTokE4m3;
+// The largest magnitude of eight elements, as fp32 bits that order like it (abs_bits).
+template <typename T>
+__device__ __forceinline__ uint32_t top_of(const Raw<T>& r) {
+    if constexpr (sizeof(T) == 4) {
         uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, abs_bits(v[i]));
+        for (int i = 0; i < 8; ++i) top = max(top, r.w[i] & 0x7FFFFFFFu);
+        return top;
+    } else {
+        // magnitudes of 16-bit floats order like their bits, two at a time
+        uint32_t m = r.w[0] & 0x7FFF7FFFu;
 #pragma unroll
-        for (int d = G / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-        if (!there) return;
-        const float scale = row_scale(top, E4 ? 448.0f : 127.0f);
-        if (threadIdx.x % G == 0) (u.value ? p.v_scale : p.k_scale)[at] = scale;
-        if (count <= 0) return;
+        for (int i = 1; i < 4; ++i) m = __vmaxu2(m, r.w[i] & 0x7FFF7FFFu);
+        const uint32_t top = max(m & 0xFFFFu, m >> 16);
+        if constexpr (std::is_same<T, __half>::value)
+            return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(top))));
+        return top << 16;
+    }
+}
+
+// Two quotients by one scale, rounded once (quot_corrected's steps, two values an
+// instruction); the sign of a zero quotient is put back for e4m3, which has one.
+template <bool E4>
+__device__ __forceinline__ float2 quotients(float x, float y, float scale, float inv, bool quick) {
+    if (!quick) return make_float2(x / scale, y / scale);
+    float2 q;
+    asm("{\n\t.reg .b64 v, s, r, q;\n\t"
+        "mov.b64 v, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\tmov.b64 r, {%5, %5};\n\t"
+        "mul.rn.f32x2 q, v, r;\n\t"
+        "fma.rn.f32x2 s, s, q, v;\n\t"
+        "fma.rn.f32x2 q, s, r, q;\n\t"
+        "mov.b64 {%0, %1}, q;\n\t}"
+        : "=f"(q.x), "=f"(q.y)
+        : "f"(x), "f"(y), "f"(-scale), "f"(inv));
+    if (E4) {
+        q.x = __uint_as_float(__float_as_uint(q.x) | (__float_as_uint(x) & 0x80000000u));
+        q.y = __uint_as_float(__float_as_uint(q.y) | (__float_as_uint(y) & 0x80000000u));
+    }
+    return q;
+}
+
+// G lanes a row: 8, 10, 16 or 32.  A lane's rows are reduced side by side; lane r of the
+// group then takes row r's two divisions for all.
+template <typename T, int CACHE, int G, int R>
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ CacheParams p) {
+    static_assert(R <= G, "a lane for each row's scale");
+    griddep_launch_dependents();
+    griddep_wait();
+    const Unit u = unit_of<G>(p);
+    const int lane = threadIdx.x & 31, in_row = lane % G, e = in_row * 8;
+    const bool mine = u.there && e < p.width;
+    Raw<T> raw[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int row = u.part + r * p.parts;
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(2 * sizeof(T)); ++i) raw[r].w[i] = 0u;
+        if (!mine || row >= 2 * p.heads) continue;
+        const bool value = row >= p.heads;
+        const T* src = reinterpret_cast<const T*>(value ? p.rows_v : p.rows_k) + u.token * p.tok_stride +
+                       (value ? row - p.heads : row) * p.head_stride + e;
+        raw[r] = load_raw(src, p.width - e, p.aligned);
+    }
+    if (CACHE == kTokBf16 || CACHE == kTokF16) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int row = u.part + r * p.parts;
+            if (!mine || row >= 2 * p.heads) continue;
+            const bool value = row >= p.heads;
+            unsigned char* dst = (value ? p.v : p.k) + u.row + (value ? row - p.heads : row) * p.map.head_stride;
+            reinterpret_cast<uint4*>(dst)[in_row] = make_uint4(raw[r].w[0], raw[r].w[1], raw[r].w[2], raw[r].w[3]);
+        }
+        return;
+    }
+    constexpr bool E4 = CACHE == kTokE4m3;
+    uint32_t top[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) top[r] = top_of(raw[r]);
+    constexpr int kReach = G == 32 ? 16 : G > 8 ? 8 : 4;
+#pragma unroll
+    for (int d = kReach; d > 0; d >>= 1)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint32_t o = __shfl_down_sync(0xffffffffu, top[r], d);
+            if (in_row + d < G) top[r] = max(top[r], o);
+        }
+    // lane r of the group: row r
+    uint32_t own = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const uint32_t t = __shfl_sync(0xffffffffu, top[r], lane - in_row);
+        if (in_row == r) own = t;
+    }
+    const float own_scale = row_scale(own, E4 ? 448.0f : 127.0f);
+    // 0 for a row that is blank
+    const float own_inv = row_blank(own) ? 0.0f : 1.0f / own_scale;
+    {
+        const int row = u.part + in_row * p.parts;
+        if (u.there && in_row < R && row < 2 * p.heads) {
+            const bool value = row >= p.heads;
+            (value ? p.v_scale : p.k_scale)[u.scale + (value ? row - p.heads : row) * p.map.scale_head_stride] =
+                own_scale;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float scale = __shfl_sync(0xffffffffu, own_scale, lane - in_row + r);
+        const float inv = __shfl_sync(0xffffffffu, own_inv, lane - in_row + r);
+        const int row = u.part + r * p.parts;
+        if (!mine || row >= 2 * p.heads) continue;
+        const bool value = row >= p.heads;
+        unsigned char* dst = (value ? p.v : p.k) + u.row + (value ? row - p.heads : row) * p.map.head_stride;
         uint32_t w[2] = {0u, 0u};
-        if (!row_blank(top)) {
-            const float r = 1.0f / scale;
+        if (inv != 0.0f) {
+            float v[8];
+            widen8(raw[r], v);
             const bool quick = quot_corrected_ok(scale);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float c = quick ? quot_corrected(v[i], scale, r) : v[i] / scale;
-                const uint32_t b = E4 ? __nv_cvt_float_to_fp8(c, __NV_SATFINITE, __NV_E4M3)
-                                      : static_cast<uint32_t>(__float2int_rn(c)) & 0xFFu;
-                w[i / 4] |= b << (8 * (i % 4));
+            for (int i = 0; i < 8; i += 2) {
+                const float2 q = quotients<E4>(v[i], v[i + 1], scale, inv, quick);
+                // int8: nearest (ties to even) by the addition of 1.5 * 2^23, |q| <= 127.5
+                const uint32_t b = E4 ? __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3)
+                                      : __byte_perm(__float_as_uint(q.x + 12582912.0f),
+                                                    __float_as_uint(q.y + 12582912.0f), 0x0040);
+                w[i / 4] = i % 4 == 0 ? b : __byte_perm(w[i / 4], b, 0x5410);
             }
         }
         *reinterpret_cast<uint2*>(dst + e) = make_uint2(w[0], w[1]);
     }
 }
 
-template <typename T, int CACHE, int G>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheParams p) {
-    griddep_launch_dependents();
-    griddep_wait();
-    const long long first =
-        (static_cast<long long>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32) * (32 / G);
-    const Unit u = unit_of<G>(p, first);
-    const int e = (threadIdx.x % G) * 8;
-    if (!u.in || e >= p.width) return;
-    long long row = 0, at = 0;
-    const bool there = token_row(p.map, u.sequence, u.pos, u.head, &row, &at);
-    const unsigned char* src = (u.value ? p.v : p.k) + row;
-    float v[8];
-    if (!there) {
+// Eight codes (or 16-bit elements) as fp32, times their scale
+template <int CACHE>
+__device__ __forceinline__ void values8(const uint32_t (&w)[4], float scale, float (&v)[8]) {
+    if (CACHE == kTokBf16 || CACHE == kTokF16) {
+        Raw<__half> r{{w[0], w[1], w[2], w[3]}};
+        if (CACHE == kTokF16) widen8(r, v);
+        else widen8(*reinterpret_cast<Raw<__nv_bfloat16>*>(&r), v);
+        return;
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(kNanBits);
-    } else if (CACHE == kTokBf16) {
-        load8(reinterpret_cast<const __nv_bfloat16*>(src) + e, 8, true, v);
-    } else if (CACHE == kTokF16) {
-        load8(reinterpret_cast<const __half*>(src) + e, 8, true, v);
-    } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(src + e);
-        const float scale = (u.value ? p.v_scale : p.k_scale)[at];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t b = ((i < 4 ? w.x : w.y) >> (8 * (i % 4))) & 0xFFu;
-            if (CACHE == kTokE4m3)
-                v[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(b), __NV_E4M3))) * scale;
-            else
-                v[i] = static_cast<float>(static_cast<signed char>(b)) * scale;
+    for (int i = 0; i < 8; i += 2) {
+        const uint32_t b = w[i / 4] >> (8 * (i % 4));
+        if (CACHE == kTokE4m3) {
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(b), __NV_E4M3);
+            const float2 f = __half22float2(__half2(h));
+            v[i] = f.x * scale;
+            v[i + 1] = f.y * scale;
+        } else {
+            // 2^23 + 128 + code as fp32 bits, less 2^23 + 128
+            const uint32_t o = b ^ 0x8080u;
+            v[i] = (__uint_as_float(__byte_perm(o, 0x4B000000u, 0x7440)) - 8388736.0f) * scale;
+            v[i + 1] = (__uint_as_float(__byte_perm(o, 0x4B000000u, 0x7441)) - 8388736.0f) * scale;
         }
     }
-    store8(reinterpret_cast<T*>(u.value ? p.rows_v : p.rows_k) + u.token * p.tok_stride +
-               u.head * p.head_stride + e,
-           8, p.aligned, v);
+}
+
+// A share is every parts * G-th run of eight elements of the token's rows, so that lanes
+// take neighbours whatever the width is; up to R of them a lane.
+template <typename T, int CACHE, int G, int R>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 5) cache_read_kernel(const __grid_constant__ CacheParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const Unit u = unit_of<G>(p);
+    if (!u.in) return;
+    constexpr bool kCodes = CACHE == kTokInt8 || CACHE == kTokE4m3;
+    const int runs = p.width / 8, all = 2 * p.heads * runs;
+    const int first = u.part * G + threadIdx.x % G, step = p.parts * G;
+    // the first one's row and element; the next is `rows` rows and `on` elements further
+    const int row0 = fdiv(first, p.by_runs), e0 = (first - row0 * runs) * 8;
+    const int rows = fdiv(step, p.by_runs), on = (step - rows * runs) * 8;
+    uint32_t w[R][4];
+    float scale[R];
+    int row = row0, e = e0;
+    auto next = [&]() {
+        row += rows;
+        e += on;
+        if (e >= p.width) {
+            e -= p.width;
+            ++row;
+        }
+    };
+#pragma unroll
+    for (int r = 0; r < R; ++r, next()) {
+        if (!u.there || first + r * step >= all) continue;
+        const bool value = row >= p.heads;
+        const int head = value ? row - p.heads : row;
+        const unsigned char* src = (value ? p.v : p.k) + u.row + head * p.map.head_stride;
+        if (kCodes) {
+            const uint2 c = *reinterpret_cast<const uint2*>(src + e);
+            w[r][0] = c.x;
+            w[r][1] = c.y;
+            scale[r] = (value ? p.v_scale : p.k_scale)[u.scale + head * p.map.scale_head_stride];
+        } else {
+            const uint4 c = *reinterpret_cast<const uint4*>(src + 2 * e);
+            w[r][0] = c.x;
+            w[r][1] = c.y;
+            w[r][2] = c.z;
+            w[r][3] = c.w;
+        }
+    }
+    row = row0;
+    e = e0;
+#pragma unroll
+    for (int r = 0; r < R; ++r, next()) {
+        if (first + r * step >= all) break;
+        const bool value = row >= p.heads;
+        float v[8];
+        if (u.there) {
+            values8<CACHE>(w[r], kCodes ? scale[r] : 1.0f, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(kNanBits);
+        }
+        store8(reinterpret_cast<T*>(value ? p.rows_v : p.rows_k) + u.token * p.tok_stride +
+                   (value ? row - p.heads : row) * p.head_stride + e,
+               p.aligned, v);
+    }
+}
+
+template <typename Kernel>
+cudaError_t run(Kernel kern, CacheParams p, int parts, int lanes, cudaStream_t stream) {
+    p.parts = parts;
+    p.by_parts = make_fastdiv(static_cast<uint32_t>(parts));
+    p.by_runs = make_fastdiv(static_cast<uint32_t>(p.width / 8));
+    const long long units = p.tokens * parts, per = kThreads / 32 * (32 / lanes);
+    return launch_ex(kern, static_cast<unsigned>((units + per - 1) / per), dim3(kThreads), 0, 1, stream, p);
+}
+
+// Several rows (or runs of elements) a lane where that leaves the SMs two blocks each:
+// their loads are in flight together behind one look at the table.  Fewer of fp32, for
+// the registers.
+template <typename T, int CACHE, int G>
+cudaError_t write_by_rows(const CacheParams& p, cudaStream_t stream) {
+    constexpr int kMany = sizeof(T) == 4 ? 4 : 8;
+    const bool many = p.tokens * 2 * p.heads / kMany * G >= 2 * 152 * kThreads;
+    return many ? run(cache_write_kernel<T, CACHE, G, kMany>, p, (2 * p.heads + kMany - 1) / kMany, G, stream)
+                : run(cache_write_kernel<T, CACHE, G, 1>, p, 2 * p.heads, G, stream);
+}
+
+template <typename T, int CACHE, int G>
+cudaError_t read_by_rows(const CacheParams& p, cudaStream_t stream) {
+    constexpr int kMany = CACHE == kTokInt8 || CACHE == kTokE4m3 ? 8 : 4;
+    const int runs = 2 * p.heads * (p.width / 8);
+    const bool many = p.tokens * runs / kMany >= 2 * 152 * kThreads;
+    return many ? run(cache_read_kernel<T, CACHE, G, kMany>, p, (runs + kMany * G - 1) / (kMany * G), G, stream)
+                : run(cache_read_kernel<T, CACHE, G, 1>, p, (runs + G - 1) / G, G, stream);
 }
 
 template <typename T, int CACHE, bool WRITE>
-cudaError_t by_width(CacheParams p, cudaStream_t stream) {
-    const int g = p.width <= 64 ? 8 : p.width <= 128 ? 16 : 32;
-    const long long units = p.tokens * 2 * p.heads;
-    const long long per = (kThreads / 32) * (32 / g);
-    const unsigned blocks = static_cast<unsigned>((units + per - 1) / per);
-    p.by_units = make_fastdiv(static_cast<uint32_t>(2 * p.heads));
-    auto go = [&](auto kern) { return launch_ex(kern, blocks, dim3(kThreads), 0, 1, stream, p); };
-    if (WRITE)
-        return g == 8 ? go(cache_write_kernel<T, CACHE, 8>)
-                      : g == 16 ? go(cache_write_kernel<T, CACHE, 16>) : go(cache_write_kernel<T, CACHE, 32>);
-    return g == 8 ? go(cache_read_kernel<T, CACHE, 8>)
-                  : g == 16 ? go(cache_read_kernel<T, CACHE, 16>) : go(cache_read_kernel<T, CACHE, 32>);
+cudaError_t by_width(const CacheParams& p, cudaStream_t stream) {
+    if constexpr (WRITE)
+        return p.width <= 64    ? write_by_rows<T, CACHE, 8>(p, stream)
+               : p.width <= 80  ? write_by_rows<T, CACHE, 10>(p, stream)
+               : p.width <= 128 ? write_by_rows<T, CACHE, 16>(p, stream)
+                                : write_by_rows<T, CACHE, 32>(p, stream);
+    else
+        return 2 * p.heads * (p.width / 8) >= 32 * 8 ? read_by_rows<T, CACHE, 32>(p, stream)
+                                                     : read_by_rows<T, CACHE, 8>(p, stream);
 }
 
 template <typename T, bool WRITE>
