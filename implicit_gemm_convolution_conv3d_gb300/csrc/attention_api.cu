@@ -64,6 +64,7 @@ const char* bad_cache(const kv_cache* c) {
     if (!aligned_to(c->k, 16) || !aligned_to(c->v, 16) || c->page_stride * elt % 16 ||
         c->head_stride * elt % 16 || c->row_stride * elt % 16)
         return "a cache's rows must be 16-byte aligned";
+    if (c->row_stride > 1 << 26) return "a cache's row stride must be below 2^26";
     if (c->row_stride < c->width || c->head_stride < 0 || c->page_stride < 0)
         return "a cache's row stride is below its width";
     if (is_code_type(c->dtype)) {
@@ -288,7 +289,23 @@ int paged_attention_fwd(const void* q, int q_dtype, int64_t q_sequence_stride,
                        "paged_attention_workspace_size bytes");
     p.jobs = static_cast<int4*>(workspace);
     p.partial = reinterpret_cast<float*>(p.jobs + p.grid);
-    return launched(launch_paged(p, q_dtype, cache->dtype, stream), "paged_attention_fwd launch");
+    p.status = lim.status;
+    p.wait_ns = lim.wait_ns;
+    // blocks of tokens that lie in one page (or in two halves) are loaded by TMA, with their
+    // scales where those are 16-byte aligned
+    const int elt = size_of(cache->dtype);
+    const bool scales = !is_code_type(cache->dtype) ||
+                        (aligned_to(cache->k_scale, 16) && aligned_to(cache->v_scale, 16) &&
+                         cache->scale_page_stride % 4 == 0 && cache->scale_head_stride % 4 == 0);
+    p.rows_box = !scales || cache->page_size % 8 ? 0 : cache->page_size % 16 ? 8 : 16;
+    PagedMaps maps{};
+    if (p.rows_box)
+        for (int i = 0; i < 2; ++i)
+            if (int rc = encode_pages(i ? &maps.v : &maps.k, i ? cache->v : cache->k, elt, cache->width,
+                                      cache->page_size, cache->heads, cache->pages, p.map.row_stride,
+                                      p.map.head_stride, p.map.page_stride, p.rows_box))
+                return rc;
+    return launched(launch_paged(maps, p, q_dtype, cache->dtype, stream), "paged_attention_fwd launch");
 }
 
 int packed_attention_fwd(const void* q, int64_t q_token_stride, int64_t q_head_stride,

@@ -79,12 +79,19 @@ struct PagedParams {
     int grid;
     float* partial;        // workspace: see paged_attention.cu
     int4* jobs;
+    int rows_box;          // tokens of a TMA load: 16, 8, or 0 (pages of other sizes: word by word)
+    int* status;           // device status word and the bound on every wait
+    unsigned long long wait_ns;
+};
+struct PagedMaps {
+    CUtensorMap k, v;
 };
 // CTAs of the grid, and query heads of a pass (0: this width is not supported)
 int paged_grid(long long sequences, long long kv_heads, long long group, int width,
                long long capacity, int num_sms);
 size_t paged_workspace(int grid, int width);
-cudaError_t launch_paged(const PagedParams& p, int q_dtype, int cache_dtype, cudaStream_t stream);
+cudaError_t launch_paged(const PagedMaps& maps, const PagedParams& p, int q_dtype, int cache_dtype,
+                         cudaStream_t stream);
 
 struct PackedParams {
     const int32_t* q_offsets;

@@ -11,14 +11,18 @@
 // only).  A run's ends may lie inside a key head: those CTAs leave (maximum, sum,
 // output) in the workspace and a second launch joins them in order, so results do
 // not depend on timing.  Within a CTA each warp takes every eighth block of 16 tokens
-// on its own, through its own ring of asynchronous copies: a thread copies exactly
-// the words that it will use itself, so the loop has no barrier.
+// on its own, through its own ring of TMA loads: two instructions a block where its
+// tokens lie in one page (four where pages hold a multiple of eight), which leaves the
+// load units to the shared-memory side.  Blocks at an edge of what is seen, in pages
+// of other sizes, or in pages that are not there come word by word.
 //
 // A block is two small matrix products per warp, tokens on the 16-row side:
 //     S^T[16 tokens, 8 heads] = K q^T,    O^T[width, 8 heads] += V^T P^T
-// The reduction index of the first and the rows of the second may be permuted at
-// will, so that a thread's operands are whole 16-byte words of the cache as it lies in
-// memory: no transposition anywhere but P's (one 8 x 8 exchange).  Memory-bound work
+// The reduction index of the first, the rows of the second and the tokens' order may be
+// permuted at will, so that a thread's operands are whole 16-byte words of the cache as
+// it lies in memory, read without bank conflicts from 128-byte swizzled rows: row r of
+// the product is token r ^ ((r & 1) << 2) of the block's eight.  Nothing is transposed
+// but P (one 8 x 8 exchange).  Memory-bound work
 // at 8 heads cannot fill a 128-row tensor-memory tile; the warp-level product reads
 // its operands from registers, where 8-bit codes have to be widened anyway.
 // int8 and e4m3 codes are exact in f16, as are queries times a power of two, so the
@@ -39,22 +43,35 @@ constexpr int kUnit = 128;          // tokens that the work is dealt in
 constexpr int kBlock = 16;          // tokens of a warp's step
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTinyScale = 7.8886091e-31f;   // 2^-100
+// Weights may exceed 1 by 2^4 before what they are relative to follows: the outputs are
+// rarely rescaled, and a block of tokens without a new maximum needs no exchange of it.
+constexpr float kLag = 4.0f;
 
 template <int ES, int DP>
 struct Form {
     static constexpr int kWarps = ES * DP >= 512 ? 4 : 8;
-    static constexpr int kStages = ES * DP == 64 ? 5 : 3;
     static constexpr int kCtas = ES * DP <= 128 ? 2 : 1;
-    static constexpr int kKWords = DP * ES / 64;   // 16-byte words of a key row per thread
-    static constexpr int kVBytes = DP * ES / 8;    // bytes of a value row per thread
+    static constexpr int kStages = 3;
+    static constexpr int kBoxes = (DP * ES + 127) / 128;   // 128-byte columns of a row
+    static constexpr int kKWords = DP * ES / 64;           // 16-byte words of a key row per thread
+    static constexpr int kVBytes = DP * ES / 8;            // bytes of a value row per thread
     static constexpr int kVWord = kVBytes < 16 ? kVBytes : 16;
     static constexpr int kVWords = kVBytes / kVWord;
-    static constexpr int kKSlots = 2 * kKWords, kVSlots = 4 * kVWords;
-    static constexpr uint32_t kVOff = kKSlots * 512u;
-    static constexpr uint32_t kScaleOff = kVOff + kVSlots * 32u * kVWord;
-    static constexpr uint32_t kStage = kScaleOff + (ES == 1 ? 128u : 0u);
+    static constexpr uint32_t kBox = kBlock * 128u;        // 16 rows of 128 bytes, swizzled
+    static constexpr uint32_t kVOff = kBoxes * kBox;
+    static constexpr uint32_t kStage = 2 * kVOff;
     static constexpr uint32_t kRing = kWarps * kStages * kStage;
+    // behind the rings: 16 tokens' scales of keys and of values for each stage (128 bytes),
+    // then the stages' barriers; 1024 for the rings' alignment
+    static constexpr uint32_t kScales = 128u;
+    static constexpr uint32_t kBars = kRing + kWarps * kStages * kScales;
+    static constexpr uint32_t kBytes = kBars + kWarps * kStages * 8u + 1024u;
 };
+
+// Byte of 16-byte word `c` of row `r` in a box.
+__device__ __forceinline__ uint32_t word_at(int r, int c) {
+    return static_cast<uint32_t>((c >> 3) * (kBlock * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -118,6 +135,18 @@ __device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[BYTES / 4]) {
                      : "r"(addr));
     else
         asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+}
+
+// Bounded wait for a stage by the whole warp (see wait_bar).
+__device__ __forceinline__ bool wait_block(uint32_t bar, uint32_t parity, int* status, unsigned long long limit_ns) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    if (__all_sync(kAll, limit_ns ? mbar_try_wait(bar, parity) : mbar_test_wait(bar, parity))) return true;
+    const long long t0 = clock64();
+    const long long limit = static_cast<long long>(limit_ns > (1ull << 61) ? (1ull << 61) : limit_ns) * 2;
+    while (!__any_sync(kAll, clock64() - t0 >= limit))
+        if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
+    atomicExch(status, kStatusTimeout);
+    return false;
 }
 
 // What a sequence's query sees: tokens [0, lead) and [from, length), as blocks of 16:
@@ -197,7 +226,8 @@ constexpr int kPartial = 16 * (DP + 2);
 template <int KIND, bool QBF, int DP, int NG>
 __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 ? 2 : 1, DP>::kWarps,
                                   NG == 1 ? Form<KIND == kTokBf16 || KIND == kTokF16 ? 2 : 1, DP>::kCtas : 1)
-    paged_kernel(const __grid_constant__ PagedParams p) {
+    paged_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                 const __grid_constant__ PagedParams p) {
     constexpr bool kCodes = KIND == kTokInt8 || KIND == kTokE4m3;
     constexpr int ES = kCodes ? 1 : 2;
     using F = Form<ES, DP>;
@@ -205,11 +235,25 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
     constexpr bool kBf = KIND == kTokBf16;
     constexpr int kSteps = DP / 16;   // k-steps of the first product
     constexpr int kTiles = DP / 16;   // 16-row tiles of the second's output
-    extern __shared__ __align__(16) unsigned char smem[];
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    unsigned char* smem = smem_raw + (base - raw);
     __shared__ long long s_scratch[kWarps];
     __shared__ int s_seq;
     __shared__ long long s_before;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
+    const uint32_t ring = base + warp * (F::kStages * F::kStage);
+    const uint32_t scales = base + F::kRing + warp * (F::kStages * F::kScales);
+    const uint32_t full0 = base + F::kBars + warp * (F::kStages * 8u);
+    if (lane == 0) {
+        for (int i = 0; i < F::kStages; ++i) mbar_init(full0 + 8 * i, 1);
+        fence_mbar_init();
+        if (p.rows_box) {
+            prefetch_tmap(&k_map);
+            prefetch_tmap(&v_map);
+        }
+    }
+    __syncwarp();
     griddep_launch_dependents();
     griddep_wait();
 
@@ -244,8 +288,10 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
     int seq = s_seq;
     long long before = s_before;
 
-    const uint32_t ring = smem_u32(smem) + warp * (F::kStages * F::kStage);
-    const bool whole_blocks = p.map.by_page.d % kBlock == 0;
+    int stage = 0;        // the ring's next stage, and its phase
+    uint32_t phase = 0;
+    bool dead = false;    // a wait ran out: no more work, but the CTA's barriers are kept
+    const uint32_t block_bytes = 2u * F::kBoxes * F::kBox + (kCodes ? 128u : 0u);
     while (unit < end) {
         const Seen see = seen_by(p, seq);
         if (see.units == 0) {
@@ -314,7 +360,8 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 // row 2q + j of this group is held by lanes 4 * (2q + j) ...
-                qscale[n][j] = __shfl_sync(0xffffffffu, back, 4 * (2 * q + j)) * p.scale;
+                // (without a cap the change to powers of two goes along)
+                qscale[n][j] = __shfl_sync(0xffffffffu, back, 4 * (2 * q + j)) * p.scale * (p.cap > 0.0f ? 1.0f : kLog2e);
                 const int hh = 8 * n + 2 * q + j;
                 slope[n][j] = p.slopes && hh < heads_here ? p.slopes[qh0 + hh] * kLog2e : 0.0f;
             }
@@ -341,85 +388,113 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
             return (b < see.lead_blocks ? b : b - see.lead_blocks + see.skip) * kBlock;
         };
         auto visible = [&](int t) { return t < see.length && (t >= see.from || t < see.lead); };
-        const long long head_bytes = head * p.map.head_stride;
-        auto issue = [&](int b, int stage) {
-            const uint32_t dst = ring + stage * F::kStage;
-            const int t0 = token_of(b);
-            long long base = 0;
-            bool ok = !see.bad;
-            if (whole_blocks) {
-                const uint32_t slot = fdiv(static_cast<uint32_t>(t0), p.map.by_page);
-                const long long page = p.map.table[seq * p.map.table_stride + slot];
-                ok = ok && page >= 0 && page < p.map.pages;
-                base = page * p.map.page_stride + head_bytes +
-                       static_cast<long long>(t0 - slot * p.map.by_page.d) * p.map.row_stride;
-            }
-            auto row = [&](int i, long long* at) {
-                const int t = t0 + i;
-                if (!ok || !visible(t)) return false;
-                if (whole_blocks) {
-                    *at = base + i * p.map.row_stride;
-                    return true;
-                }
-                long long sc;
-                return token_row(p.map, seq, t, head, at, &sc);
-            };
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                long long at = 0;
-                const bool have = row(r + 8 * i, &at);
-#pragma unroll
-                for (int w = 0; w < F::kKWords; ++w) {
-                    const int off = (q + 4 * w) * 16;
-                    const bool load = have && off < p.width * ES;
-                    cp_async<16>(dst + (i * F::kKWords + w) * 512u + lane * 16u, p.k + (load ? at + off : 0),
-                                 load ? 16u : 0u);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                long long at = 0;
-                const bool have = row(2 * q + (i & 1) + 8 * (i >> 1), &at);
-#pragma unroll
-                for (int w = 0; w < F::kVWords; ++w) {
-                    const int off = (r + 8 * w) * F::kVWord;
-                    const bool load = have && off < p.width * ES;
-                    cp_async<F::kVWord>(dst + F::kVOff + ((i * F::kVWords + w) * 32u + lane) * F::kVWord,
-                                        p.v + (load ? at + off : 0), load ? F::kVWord : 0u);
-                }
-            }
-            if (kCodes) {
-                // lanes 0-15: the keys' scales, 16-31: the values'; NaN where a page is missing
-                const int t = t0 + (lane & 15);
-                long long at = 0, sc = 0;
-                const bool want = visible(t) || see.bad;
-                const bool have = want && !see.bad && token_row(p.map, seq, t, head, &at, &sc);
-                const uint32_t to = dst + F::kScaleOff + lane * 4u;
-                if (want && !have)
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(kNanBits) : "memory");
-                else
-                    cp_async<4>(to, (lane < 16 ? p.k_scale : p.v_scale) + sc, have ? 4u : 0u);
-            }
+        // whether all 16 tokens are seen (and there)
+        auto all_seen = [&](int t0) {
+            return t0 + kBlock <= see.length && (t0 >= see.from || t0 + kBlock <= see.lead) && !see.bad;
         };
+        const int32_t* table = p.map.table + seq * p.map.table_stride;
+        // the pages of the next block to ask for: of its first eight tokens and the others
+        auto page_of = [&](int b, int half) {
+            const int t = min(token_of(b) + 8 * half, see.length - 1);
+            return b < b1 ? table[fdiv(static_cast<uint32_t>(t), p.map.by_page)] : 0;
+        };
+        const bool look = p.rows_box != 0 && !see.bad;
+        int page0 = 0, page1 = 0;
+        auto look_ahead = [&](int b) {
+            if (!look) return;
+            page0 = page_of(b, 0);
+            page1 = p.rows_box == 8 ? page_of(b, 1) : page0;
+        };
+        look_ahead(b0 + warp);
+        uint32_t slow = 0;   // stages that were filled word by word (bits)
+        auto issue = [&](int b, int st) {
+            const uint32_t dst = ring + st * F::kStage, sdst = scales + st * F::kScales, bar = full0 + 8 * st;
+            const int t0 = token_of(b), pa = page0, pb = page1;
+            look_ahead(b + kWarps);
+            if (look && all_seen(t0) && pa >= 0 && pa < p.map.pages && pb >= 0 && pb < p.map.pages) {
+                slow &= ~(1u << st);
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, block_bytes);
+                    for (int h = 0; h < 16; h += p.rows_box) {
+                        const int page = h ? pb : pa;
+                        const int off = t0 + h - static_cast<int>(fdiv(static_cast<uint32_t>(t0 + h), p.map.by_page) * p.map.by_page.d);
 #pragma unroll
-        for (int i = 0; i < F::kStages - 1; ++i) {
-            const int b = b0 + warp + i * kWarps;
-            if (b < b1) issue(b, i);
-            cp_async_commit();
+                        for (int x = 0; x < F::kBoxes; ++x) {
+                            tma_load_4d(dst + x * F::kBox + h * 128u, &k_map, bar, x * (128 / ES), off, head, page);
+                            tma_load_4d(dst + F::kVOff + x * F::kBox + h * 128u, &v_map, bar, x * (128 / ES), off, head, page);
+                        }
+                        if (kCodes) {
+                            const long long at = page * p.map.scale_page_stride + head * p.map.scale_head_stride + off;
+                            bulk_load_1d(sdst + h * 4u, p.k_scale + at, p.rows_box * 4u, bar);
+                            bulk_load_1d(sdst + 64u + h * 4u, p.v_scale + at, p.rows_box * 4u, bar);
+                        }
+                    }
+                }
+                return;
+            }
+            // word by word: a block's edge, pages that end in it, pages that are not there
+            slow |= 1u << st;
+#pragma unroll 1
+            for (int i = 0; i < kBlock; ++i) {
+                long long at = 0, sc;
+                const bool have = !see.bad && visible(t0 + i) && token_row(p.map, seq, t0 + i, head, &at, &sc);
+#pragma unroll
+                for (int c = lane; c < F::kBoxes * 16; c += 32) {
+                    const int w = c % (F::kBoxes * 8);   // a key's words, then a value's
+                    const bool value = c >= F::kBoxes * 8, load = have && w * 16 < p.width * ES;
+                    cp_async<16>(dst + (value ? F::kVOff : 0u) + word_at(i, w),
+                                 (value ? p.v : p.k) + (load ? at + w * 16 : 0), load ? 16u : 0u);
+                }
+            }
+            // NaN for the scale of a token whose page is missing, which spoils the row
+            const int t = t0 + (lane & 15);
+            long long at = 0, sc = 0;
+            const bool want = visible(t) || see.bad;
+            const bool have = want && !see.bad && token_row(p.map, seq, t, head, &at, &sc);
+            if (kCodes && (have || !want))
+                cp_async<4>(sdst + lane * 4u, (lane < 16 ? p.k_scale : p.v_scale) + sc, have ? 4u : 0u);
+            else
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(sdst + lane * 4u),
+                             "f"(want && !have ? __uint_as_float(kNanBits) : 1.0f)
+                             : "memory");
+        };
+        {
+            int st = stage;
+#pragma unroll
+            for (int i = 0; i < F::kStages - 1; ++i) {
+                const int b = b0 + warp + i * kWarps;
+                if (b < b1 && !dead) issue(b, st);
+                if (++st == F::kStages) st = 0;
+            }
         }
-        int stage = 0;
-        for (int b = b0 + warp; b < b1; b += kWarps) {
+        for (int b = b0 + warp; b < b1 && !dead; b += kWarps) {
             {
                 const int nb = b + (F::kStages - 1) * kWarps;
                 int ns = stage + F::kStages - 1;
                 if (ns >= F::kStages) ns -= F::kStages;
                 if (nb < b1) issue(nb, ns);
-                cp_async_commit();
             }
-            cp_async_wait<F::kStages - 1>();
-            __syncwarp();   // the scales come from other lanes' copies
-            const uint32_t src = ring + stage * F::kStage;
+            const bool by_words = slow >> stage & 1u;
+            if (by_words) {
+                // (the barrier's phase passes without a load)
+                cp_async_wait_all();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full0 + 8 * stage);
+            }
+            if (!wait_block(full0 + 8 * stage, phase, p.status, p.wait_ns)) {
+                // what is on its way lands before the shared memory is given up
+                cp_async_wait_all();
+                dead = true;
+                for (int i = 0; i < F::kStages && b + i * kWarps < b1; ++i) {
+                    const int st = (stage + i) % F::kStages;
+                    if (!(slow >> st & 1u)) drain_wait(full0 + 8 * st, stage + i < F::kStages ? phase : phase ^ 1u);
+                }
+                break;
+            }
+            const uint32_t src = ring + stage * F::kStage, ssrc = scales + stage * F::kScales;
             const int t0 = token_of(b);
+            const int r0 = r ^ ((r & 1) << 2);   // the token of the product's row r; r + 8: r0 + 8
 
             // ---- scores
             float sc[NG][4];
@@ -430,8 +505,8 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
 #pragma unroll
             for (int w = 0; w < F::kKWords; ++w) {
                 uint32_t x[4], y[4];
-                lds<16>(src + w * 512u + lane * 16u, x);
-                lds<16>(src + (F::kKWords + w) * 512u + lane * 16u, y);
+                lds<16>(src + word_at(r0, q + 4 * w), x);
+                lds<16>(src + word_at(r0 + 8, q + 4 * w), y);
                 if constexpr (kCodes) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -451,72 +526,93 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
                                           bq[n][2 * w + i][0], bq[n][2 * w + i][1]);
                 }
             }
-            // ---- weights: this thread's tokens are t0 + r and t0 + r + 8
+            // ---- weights: this thread's tokens are t0 + r0 and t0 + r0 + 8
             float ks[2] = {1.0f, 1.0f}, lv[2] = {0.0f, 0.0f};
-            bool vis[2], none[2] = {false, false};   // none: values too small to count
+            bool none[2] = {false, false};   // values too small to count
+            if (kCodes || by_words) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = t0 + r + 8 * i;
-                vis[i] = visible(t) || see.bad;
-                if (kCodes) {
-                    float vs;
-                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks[i]) : "r"(src + F::kScaleOff + (r + 8 * i) * 4u));
-                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs) : "r"(src + F::kScaleOff + (16 + r + 8 * i) * 4u));
-                    none[i] = vs < kTinyScale;
-                    lv[i] = none[i] ? -100.0f : lg2(vs);
-                } else if (vis[i]) {
-                    long long at, si;   // a missing page spoils the row
-                    if (see.bad || !token_row(p.map, seq, t, head, &at, &si)) ks[i] = __uint_as_float(kNanBits);
+                for (int i = 0; i < 2; ++i) {
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks[i]) : "r"(ssrc + (r0 + 8 * i) * 4u));
+                    if (kCodes) {
+                        float vs;
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs) : "r"(ssrc + (16 + r0 + 8 * i) * 4u));
+                        none[i] = vs < kTinyScale;
+                        lv[i] = none[i] ? -100.0f : lg2(vs);
+                    }
                 }
             }
-            uint32_t bp[NG][2];
+            float s2[NG][4];   // scores in powers of two
 #pragma unroll
-            for (int n = 0; n < NG; ++n) {
-                float s2[4];
+            for (int n = 0; n < NG; ++n)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float s = sc[n][j] * (ks[j >> 1] * qscale[n][j & 1]);
                     if (p.cap > 0.0f) {
                         // cap * tanh(s / cap), tanh x = 1 - 2 / (1 + e^2x)
                         const float e = ex2(s * (2.0f * kLog2e / p.cap));
-                        s = p.cap - 2.0f * p.cap * rcp_approx(1.0f + e);
+                        s = (p.cap - 2.0f * p.cap * rcp_approx(1.0f + e)) * kLog2e;
                     }
-                    s *= kLog2e;
                     if (p.slopes)
-                        s -= slope[n][j & 1] * static_cast<float>(see.length - 1 - (t0 + r + 8 * (j >> 1)));
-                    s2[j] = vis[j >> 1] ? s : -INFINITY;
+                        s -= slope[n][j & 1] * static_cast<float>(see.length - 1 - (t0 + r0 + 8 * (j >> 1)));
+                    s2[n][j] = s;
                 }
-                uint32_t w16[2];
+            if (!all_seen(t0)) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (!visible(t0 + r0 + 8 * i) && !see.bad) {
+#pragma unroll
+                        for (int n = 0; n < NG; ++n) s2[n][2 * i] = s2[n][2 * i + 1] = -INFINITY;
+                    }
+            }
+            bool rise = false;
+#pragma unroll
+            for (int n = 0; n < NG; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    rise |= fmaxf(s2[n][j] + lv[0], s2[n][j + 2] + lv[1]) > m[n][j] + kLag;
+            if (__any_sync(0xffffffffu, rise)) {
+                // all tokens' maximum, and everything relative to it
+#pragma unroll
+                for (int n = 0; n < NG; ++n)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float top = fmaxf(s2[n][j] + lv[0], s2[n][j + 2] + lv[1]);
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        const float now = fmaxf(m[n][j], top);
+                        const float fall = now == -INFINITY ? 1.0f : ex2(m[n][j] - now);
+                        m[n][j] = now;
+                        l[n][j] *= fall;
+#pragma unroll
+                        for (int i = 0; i < kTiles; ++i) {
+                            o[n][i][j] *= fall;
+                            o[n][i][j + 2] *= fall;
+                        }
+                    }
+            }
+            uint32_t bp[NG][2];
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
                 float pw[4];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float top = fmaxf(s2[j] + lv[0], s2[j + 2] + lv[1]);
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                    const float now = fmaxf(m[n][j], top);
-                    const float base = now == -INFINITY ? 0.0f : now;
-                    const float fall = ex2(m[n][j] - base);
-                    m[n][j] = now;
-                    pw[j] = none[0] ? 0.0f : ex2(s2[j] + lv[0] - base);
-                    pw[j + 2] = none[1] ? 0.0f : ex2(s2[j + 2] + lv[1] - base);
-                    const float sum = kCodes ? ex2(s2[j] - base) + ex2(s2[j + 2] - base) : pw[j] + pw[j + 2];
-                    l[n][j] = l[n][j] * fall + sum;
-#pragma unroll
-                    for (int i = 0; i < kTiles; ++i) {
-                        o[n][i][j] *= fall;
-                        o[n][i][j + 2] *= fall;
-                    }
+                    const float base = m[n][j] == -INFINITY ? 0.0f : m[n][j];
+                    const float x = s2[n][j] - base, y = s2[n][j + 2] - base;
+                    pw[j] = none[0] ? 0.0f : ex2(x + lv[0]);
+                    pw[j + 2] = none[1] ? 0.0f : ex2(y + lv[1]);
+                    l[n][j] += kCodes ? ex2(x) + ex2(y) : pw[j] + pw[j + 2];
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
+                    uint32_t w16;
                     if (kBf) {
-                        w16[i] = pack_bf16x2(pw[2 * i], pw[2 * i + 1]);
+                        w16 = pack_bf16x2(pw[2 * i], pw[2 * i + 1]);
                     } else {
                         const __half2 x = __floats2half2_rn(pw[2 * i], pw[2 * i + 1]);
-                        w16[i] = *reinterpret_cast<const uint32_t*>(&x);
+                        w16 = *reinterpret_cast<const uint32_t*>(&x);
                     }
-                    bp[n][i] = transpose8x8(w16[i]);
+                    bp[n][i] = transpose8x8(w16);
                 }
             }
             // ---- output
@@ -525,7 +621,12 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
                 uint32_t x[4][F::kVWord / 4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    lds<F::kVWord>(src + F::kVOff + ((i * F::kVWords + w) * 32u + lane) * F::kVWord, x[i]);
+                    {
+                        // the tokens of the product's rows 2q, 2q + 1, 2q + 8 and 2q + 9
+                        const int t = ((2 * q + (i & 1)) ^ ((i & 1) << 2)) + 8 * (i >> 1);
+                        const int c = F::kVWord == 16 ? r + 8 * w : r >> 1;
+                        lds<F::kVWord>(src + F::kVOff + word_at(t, c) + (F::kVWord == 16 ? 0u : (r & 1) * 8u), x[i]);
+                    }
 #pragma unroll
                 for (int i = 0; i < F::kVWord / 4; ++i) {
                     // pairs of tokens side by side, an element (and the next) each
@@ -556,10 +657,12 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
                     }
                 }
             }
-            __syncwarp();   // all lanes have read this stage's scales
-            if (++stage == F::kStages) stage = 0;
+            __syncwarp();   // all lanes have read this stage
+            if (++stage == F::kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
         }
-        cp_async_wait_all();
 
         // ---- the warps' results meet in shared memory, over the rings
         __syncthreads();
@@ -636,6 +739,7 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
             const long long c1 = last < split ? last / (share + 1) : longer + (last - split) / share;
             p.jobs[c] = make_int4(seq, qh0, heads_here, static_cast<int>(c1 - c));
         }
+        fence_proxy_async_smem();   // the next loads come over what was written here
         __syncthreads();
         unit += u1 - u0;
         if (u1 == see.units && hb + 1 == per) {
@@ -693,26 +797,27 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 int padded(int width) { return width <= 64 ? 64 : width <= 128 ? 128 : 256; }
 
 template <int KIND, bool QBF, int DP, int NG>
-cudaError_t run(const PagedParams& p, cudaStream_t stream) {
+cudaError_t run(const PagedMaps& maps, const PagedParams& p, cudaStream_t stream) {
     constexpr int ES = KIND == kTokBf16 || KIND == kTokF16 ? 2 : 1;
     using F = Form<ES, DP>;
     constexpr size_t meet = sizeof(float) * F::kWarps * 8 * NG * (DP + 4 + 2);
-    constexpr size_t smem = F::kRing > meet ? F::kRing : meet;
+    static_assert(meet <= F::kRing, "the warps' results meet over the rings");
+    constexpr size_t smem = F::kBytes;
     static std::atomic<int> slots[kMaxDevices];
     cudaError_t e = ensure_dynamic_smem(paged_kernel<KIND, QBF, DP, NG>, smem, slots);
     if (e != cudaSuccess) return e;
     e = launch_ex(paged_kernel<KIND, QBF, DP, NG>, static_cast<unsigned>(p.grid), dim3(32 * F::kWarps), smem, 1,
-                  stream, p);
+                  stream, maps.k, maps.v, p);
     if (e != cudaSuccess || p.grid == 1) return e;
     return launch_ex(paged_join_kernel<QBF, DP>, static_cast<unsigned>(p.grid), dim3(256), 0, 1, stream, p);
 }
 
 template <int KIND, bool QBF>
-cudaError_t by_width(const PagedParams& p, cudaStream_t stream) {
+cudaError_t by_width(const PagedMaps& m, const PagedParams& p, cudaStream_t stream) {
     const bool two = p.group > 8;
-    if (p.width <= 64) return two ? run<KIND, QBF, 64, 2>(p, stream) : run<KIND, QBF, 64, 1>(p, stream);
-    if (p.width <= 128) return two ? run<KIND, QBF, 128, 2>(p, stream) : run<KIND, QBF, 128, 1>(p, stream);
-    return run<KIND, QBF, 256, 1>(p, stream);
+    if (p.width <= 64) return two ? run<KIND, QBF, 64, 2>(m, p, stream) : run<KIND, QBF, 64, 1>(m, p, stream);
+    if (p.width <= 128) return two ? run<KIND, QBF, 128, 2>(m, p, stream) : run<KIND, QBF, 128, 1>(m, p, stream);
+    return run<KIND, QBF, 256, 1>(m, p, stream);
 }
 
 }  // namespace
@@ -738,13 +843,16 @@ size_t paged_workspace(int grid, int width) {
     return static_cast<size_t>(grid) * (2 * part + sizeof(int4));
 }
 
-cudaError_t launch_paged(const PagedParams& p0, int q_dtype, int cache_dtype, cudaStream_t stream) {
+cudaError_t launch_paged(const PagedMaps& maps, const PagedParams& p0, int q_dtype, int cache_dtype,
+                         cudaStream_t stream) {
     PagedParams p = p0;
     p.blocks = (p.group + pass_heads(p.group, p.width) - 1) / pass_heads(p.group, p.width);
     const bool bf = q_dtype == kTokBf16;
-    if (cache_dtype == kTokInt8) return bf ? by_width<kTokInt8, true>(p, stream) : by_width<kTokInt8, false>(p, stream);
-    if (cache_dtype == kTokE4m3) return bf ? by_width<kTokE4m3, true>(p, stream) : by_width<kTokE4m3, false>(p, stream);
-    return bf ? by_width<kTokBf16, true>(p, stream) : by_width<kTokF16, false>(p, stream);
+    if (cache_dtype == kTokInt8)
+        return bf ? by_width<kTokInt8, true>(maps, p, stream) : by_width<kTokInt8, false>(maps, p, stream);
+    if (cache_dtype == kTokE4m3)
+        return bf ? by_width<kTokE4m3, true>(maps, p, stream) : by_width<kTokE4m3, false>(maps, p, stream);
+    return bf ? by_width<kTokBf16, true>(maps, p, stream) : by_width<kTokF16, false>(maps, p, stream);
 }
 
 }  // namespace c3d
