@@ -291,6 +291,12 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
     int stage = 0;        // the ring's next stage, and its phase
     uint32_t phase = 0;
     bool dead = false;    // a wait ran out: no more work, but the CTA's barriers are kept
+    // where this thread's words lie: the key rows r0 and r0 + 8 (8 rows: 1024 bytes on) and the
+    // values' rows of the product's 2q, 2q + 1, 2q + 8 and 2q + 9
+    const int r0 = r ^ ((r & 1) << 2);
+    const uint32_t k_at = word_at(r0, q), v_at0 = word_at(2 * q, F::kVWord == 16 ? r : r >> 1),
+                   v_at1 = word_at((2 * q + 1) ^ 4, F::kVWord == 16 ? r : r >> 1);
+    const uint32_t v_half = F::kVOff + (F::kVWord == 16 ? 0u : (r & 1) * 8u);
     const uint32_t block_bytes = 2u * F::kBoxes * F::kBox + (kCodes ? 128u : 0u);
     while (unit < end) {
         const Seen see = seen_by(p, seq);
@@ -388,10 +394,6 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
             return (b < see.lead_blocks ? b : b - see.lead_blocks + see.skip) * kBlock;
         };
         auto visible = [&](int t) { return t < see.length && (t >= see.from || t < see.lead); };
-        // whether all 16 tokens are seen (and there)
-        auto all_seen = [&](int t0) {
-            return t0 + kBlock <= see.length && (t0 >= see.from || t0 + kBlock <= see.lead) && !see.bad;
-        };
         const int32_t* table = p.map.table + seq * p.map.table_stride;
         // the pages of the next block to ask for: of its first eight tokens and the others
         auto page_of = [&](int b, int half) {
@@ -411,7 +413,9 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
             const uint32_t dst = ring + st * F::kStage, sdst = scales + st * F::kScales, bar = full0 + 8 * st;
             const int t0 = token_of(b), pa = page0, pb = page1;
             look_ahead(b + kWarps);
-            if (look && all_seen(t0) && pa >= 0 && pa < p.map.pages && pb >= 0 && pb < p.map.pages) {
+            // (all 16 tokens are seen, in pages that are there)
+            if (look && t0 + kBlock <= see.length && (t0 >= see.from || t0 + kBlock <= see.lead) && pa >= 0 &&
+                pa < p.map.pages && pb >= 0 && pb < p.map.pages) {
                 slow &= ~(1u << st);
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar, block_bytes);
@@ -494,19 +498,21 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
             }
             const uint32_t src = ring + stage * F::kStage, ssrc = scales + stage * F::kScales;
             const int t0 = token_of(b);
-            const int r0 = r ^ ((r & 1) << 2);   // the token of the product's row r; r + 8: r0 + 8
 
             // ---- scores
-            float sc[NG][4];
+            // (two sums: a product waits for the one before in its own)
+            float sc[NG][4], sd[NG][4];
 #pragma unroll
             for (int n = 0; n < NG; ++n)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sc[n][j] = 0.0f;
+                for (int j = 0; j < 4; ++j) sc[n][j] = sd[n][j] = 0.0f;
 #pragma unroll
             for (int w = 0; w < F::kKWords; ++w) {
                 uint32_t x[4], y[4];
-                lds<16>(src + word_at(r0, q + 4 * w), x);
-                lds<16>(src + word_at(r0 + 8, q + 4 * w), y);
+                // (the next word is in the other half of the row, its eighth in the next box)
+                const uint32_t at = src + (w >> 1) * F::kBox + (k_at ^ ((w & 1) * 64u));
+                lds<16>(at, x);
+                lds<16>(at + 1024u, y);
                 if constexpr (kCodes) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -515,17 +521,22 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
                         widen4<KIND == kTokE4m3>(y[i], y0, y1);
 #pragma unroll
                         for (int n = 0; n < NG; ++n)
-                            mma16816<false>(sc[n], x0, y0, x1, y1, bq[n][4 * w + i][0], bq[n][4 * w + i][1]);
+                            mma16816<false>(i & 1 ? sd[n] : sc[n], x0, y0, x1, y1, bq[n][4 * w + i][0],
+                                            bq[n][4 * w + i][1]);
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int n = 0; n < NG; ++n)
-                            mma16816<kBf>(sc[n], x[2 * i], y[2 * i], x[2 * i + 1], y[2 * i + 1],
+                            mma16816<kBf>(i & 1 ? sd[n] : sc[n], x[2 * i], y[2 * i], x[2 * i + 1], y[2 * i + 1],
                                           bq[n][2 * w + i][0], bq[n][2 * w + i][1]);
                 }
             }
+#pragma unroll
+            for (int n = 0; n < NG; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sc[n][j] += sd[n][j];
             // ---- weights: this thread's tokens are t0 + r0 and t0 + r0 + 8
             float ks[2] = {1.0f, 1.0f}, lv[2] = {0.0f, 0.0f};
             bool none[2] = {false, false};   // values too small to count
@@ -556,7 +567,7 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
                         s -= slope[n][j & 1] * static_cast<float>(see.length - 1 - (t0 + r0 + 8 * (j >> 1)));
                     s2[n][j] = s;
                 }
-            if (!all_seen(t0)) {
+            if (by_words) {   // (others are seen whole)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     if (!visible(t0 + r0 + 8 * i) && !see.bad) {
@@ -621,12 +632,7 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
                 uint32_t x[4][F::kVWord / 4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    {
-                        // the tokens of the product's rows 2q, 2q + 1, 2q + 8 and 2q + 9
-                        const int t = ((2 * q + (i & 1)) ^ ((i & 1) << 2)) + 8 * (i >> 1);
-                        const int c = F::kVWord == 16 ? r + 8 * w : r >> 1;
-                        lds<F::kVWord>(src + F::kVOff + word_at(t, c) + (F::kVWord == 16 ? 0u : (r & 1) * 8u), x[i]);
-                    }
+                    lds<F::kVWord>(src + v_half + (i & 1 ? v_at1 : v_at0) + (i >> 1) * 1024u + w * F::kBox, x[i]);
 #pragma unroll
                 for (int i = 0; i < F::kVWord / 4; ++i) {
                     // pairs of tokens side by side, an element (and the next) each
@@ -808,7 +814,8 @@ cudaError_t run(const PagedMaps& maps, const PagedParams& p, cudaStream_t stream
     if (e != cudaSuccess) return e;
     e = launch_ex(paged_kernel<KIND, QBF, DP, NG>, static_cast<unsigned>(p.grid), dim3(32 * F::kWarps), smem, 1,
                   stream, maps.k, maps.v, p);
-    if (e != cudaSuccess || p.grid == 1) return e;
+    // (a table of no more than a unit's tokens leaves nothing to join)
+    if (e != cudaSuccess || p.grid == 1 || p.map.capacity <= kUnit) return e;
     return launch_ex(paged_join_kernel<QBF, DP>, static_cast<unsigned>(p.grid), dim3(256), 0, 1, stream, p);
 }
 
