@@ -283,6 +283,7 @@ int paged_attention_fwd(const void* q, int q_dtype, int64_t q_sequence_stride,
     p.group = static_cast<int>(heads / cache->heads);
     p.width = static_cast<int>(cache->width);
     p.grid = paged_grid(sequences, cache->heads, p.group, p.width, p.map.capacity, lim.num_sms);
+    p.num_sms = lim.num_sms;
     const size_t need = paged_workspace(p.grid, p.width);
     if (!workspace || workspace_bytes < need || !aligned_to(workspace, 16))
         return invalid("paged_attention_fwd needs a 16-byte aligned workspace of "
@@ -297,7 +298,10 @@ int paged_attention_fwd(const void* q, int q_dtype, int64_t q_sequence_stride,
     const bool scales = !is_code_type(cache->dtype) ||
                         (aligned_to(cache->k_scale, 16) && aligned_to(cache->v_scale, 16) &&
                          cache->scale_page_stride % 4 == 0 && cache->scale_head_stride % 4 == 0);
-    p.rows_box = !scales || cache->page_size % 8 ? 0 : cache->page_size % 16 ? 8 : 16;
+    p.rows_box = !scales || cache->page_size % 8           ? 0
+                 : cache->page_size % 16                    ? 8
+                 : cache->page_size % 32 || p.width * elt > 128 ? 16
+                                                            : 32;
     PagedMaps maps{};
     if (p.rows_box)
         for (int i = 0; i < 2; ++i)

@@ -76,10 +76,10 @@ struct PagedParams {
     int window;            // 0: none
     int sequences, kv_heads, group, width;
     int blocks;            // groups of query heads that share a pass over a key head
-    int grid;
+    int grid, num_sms;     // grid: CTAs at most
     float* partial;        // workspace: see paged_attention.cu
     int4* jobs;
-    int rows_box;          // tokens of a TMA load: 16, 8, or 0 (pages of other sizes: word by word)
+    int rows_box;          // tokens of a TMA load: 32 (rows up to 128 bytes), 16, 8, or 0 (none: word by word)
     int* status;           // device status word and the bound on every wait
     unsigned long long wait_ns;
 };

@@ -6,14 +6,14 @@
 // in one pass over the tokens with a running maximum m.  Memory-bound: a key and a
 // value row are read once for the `group` query heads that share them.
 //
-// The work is every sequence's every key head, cut into units of 128 tokens and
-// dealt to the CTAs in equal runs, whatever the lengths are (they are on the device
+// The work is every sequence's every key head, cut into units of a block of tokens for
+// each warp and dealt to the CTAs in equal runs, whatever the lengths are (they are on the device
 // only).  A run's ends may lie inside a key head: those CTAs leave (maximum, sum,
 // output) in the workspace and a second launch joins them in order, so results do
-// not depend on timing.  Within a CTA each warp takes every eighth block of 16 tokens
-// on its own, through its own ring of TMA loads: two instructions a block where its
-// tokens lie in one page (four where pages hold a multiple of eight), which leaves the
-// load units to the shared-memory side.  Blocks at an edge of what is seen, in pages
+// not depend on timing.  Within a CTA each warp takes blocks of 16 or 32 tokens (4 KB of
+// keys and values at least: what a block costs beside its data is the same) on its own,
+// through its own ring of TMA loads: two a run of 32, 16 or 8 tokens, as many as pages
+// hold a multiple of, which leaves the load units to the shared-memory side.  Blocks at an edge of what is seen, in pages
 // of other sizes, or in pages that are not there come word by word.
 //
 // A block is two small matrix products per warp, tokens on the 16-row side:
@@ -39,8 +39,6 @@ namespace c3d {
 
 namespace {
 
-constexpr int kUnit = 128;          // tokens that the work is dealt in
-constexpr int kBlock = 16;          // tokens of a warp's step
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTinyScale = 7.8886091e-31f;   // 2^-100
 // Weights may exceed 1 by 2^4 before what they are relative to follows: the outputs are
@@ -49,28 +47,35 @@ constexpr float kLag = 4.0f;
 
 template <int ES, int DP>
 struct Form {
-    static constexpr int kWarps = ES * DP >= 512 ? 4 : 8;
-    static constexpr int kCtas = ES * DP <= 128 ? 2 : 1;
-    static constexpr int kStages = 3;
+    static constexpr int kWarps = 4;
+    static constexpr int kStages = ES * DP >= 512 ? 3 : 2;
     static constexpr int kBoxes = (DP * ES + 127) / 128;   // 128-byte columns of a row
+    static constexpr int kSubs = kBoxes == 1 ? 2 : 1;      // products of 16 tokens in a block
+    static constexpr int kBlock = 16 * kSubs;
+    static constexpr int kUnit = kWarps * kBlock;
     static constexpr int kKWords = DP * ES / 64;           // 16-byte words of a key row per thread
     static constexpr int kVBytes = DP * ES / 8;            // bytes of a value row per thread
     static constexpr int kVWord = kVBytes < 16 ? kVBytes : 16;
     static constexpr int kVWords = kVBytes / kVWord;
-    static constexpr uint32_t kBox = kBlock * 128u;        // 16 rows of 128 bytes, swizzled
-    static constexpr uint32_t kVOff = kBoxes * kBox;
+    static constexpr uint32_t kBox = 16u * 128u;           // 16 rows of 128 bytes, swizzled
+    static constexpr uint32_t kVOff = kSubs * kBoxes * kBox;
     static constexpr uint32_t kStage = 2 * kVOff;
     static constexpr uint32_t kRing = kWarps * kStages * kStage;
-    // behind the rings: 16 tokens' scales of keys and of values for each stage (128 bytes),
-    // then the stages' barriers; 1024 for the rings' alignment
-    static constexpr uint32_t kScales = 128u;
+    // behind the rings: a block's scales of keys and of values for each stage, then the
+    // stages' barriers; 1024 for the rings' alignment
+    static constexpr uint32_t kScales = 2u * kBlock * 4u;
     static constexpr uint32_t kBars = kRing + kWarps * kStages * kScales;
     static constexpr uint32_t kBytes = kBars + kWarps * kStages * 8u + 1024u;
 };
 
-// Byte of 16-byte word `c` of row `r` in a box.
+// CTAs of an SM: three of one group of query heads, two of two (their registers), as far
+// as shared memory goes: some compute while another joins its warps' results at a key
+// head's end.
+constexpr int ctas_of(int es, int dp, int ng) { return es * dp >= 512 ? 1 : ng == 1 ? 3 : 2; }
+
+// Byte of 16-byte word `c` of row `r` in boxes of 16 rows (of 32, if there is one column).
 __device__ __forceinline__ uint32_t word_at(int r, int c) {
-    return static_cast<uint32_t>((c >> 3) * (kBlock * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    return static_cast<uint32_t>((c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -149,7 +154,7 @@ __device__ __forceinline__ bool wait_block(uint32_t bar, uint32_t parity, int* s
     return false;
 }
 
-// What a sequence's query sees: tokens [0, lead) and [from, length), as blocks of 16:
+// What a sequence's query sees: tokens [0, lead) and [from, length), as blocks:
 // first those of the lead, then those from block `skip` on.
 struct Seen {
     int length, lead, from;
@@ -157,7 +162,9 @@ struct Seen {
     bool bad;   // more tokens than the table holds
 };
 
+template <typename F>
 __device__ __forceinline__ Seen seen_by(const PagedParams& p, int s) {
+    constexpr int kBlock = F::kBlock;
     Seen v;
     const int n = p.lengths[s];
     v.bad = n > p.map.capacity;
@@ -168,16 +175,17 @@ __device__ __forceinline__ Seen seen_by(const PagedParams& p, int s) {
     v.lead_blocks = (v.lead + kBlock - 1) / kBlock;
     v.skip = max(v.from / kBlock, v.lead_blocks);
     v.blocks = v.lead_blocks + max((v.length + kBlock - 1) / kBlock - v.skip, 0);
-    v.units = (v.blocks + kUnit / kBlock - 1) / (kUnit / kBlock);
+    v.units = (v.blocks + F::kWarps - 1) / F::kWarps;
     return v;
 }
 
 // Units of all sequences (one key head), summed over the block, and where unit
 // `first` of the run falls: its sequence and the units before it.
-template <int THREADS>
+template <typename F>
 __device__ __forceinline__ long long sum_units(const PagedParams& p, long long* scratch) {
+    constexpr int THREADS = 32 * F::kWarps;
     long long mine = 0;
-    for (int s = threadIdx.x; s < p.sequences; s += THREADS) mine += seen_by(p, s).units;
+    for (int s = threadIdx.x; s < p.sequences; s += THREADS) mine += seen_by<F>(p, s).units;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
     if ((threadIdx.x & 31) == 0) scratch[threadIdx.x / 32] = mine;
@@ -191,13 +199,14 @@ __device__ __forceinline__ long long sum_units(const PagedParams& p, long long* 
 
 // The sequence s with before(s) <= unit < before(s) + units(s) (units of one key head
 // row: `per` = key heads x blocks times its units), found by the first warp.
+template <typename F>
 __device__ __forceinline__ void find_unit(const PagedParams& p, long long per, long long unit,
                                           int* sequence, long long* before) {
     const int lane = threadIdx.x & 31;
     long long sum = 0;
     for (int s0 = 0; s0 < p.sequences; s0 += 32) {
         const int s = s0 + lane;
-        const long long n = s < p.sequences ? seen_by(p, s).units * per : 0;
+        const long long n = s < p.sequences ? seen_by<F>(p, s).units * per : 0;
         long long run = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -225,13 +234,13 @@ constexpr int kPartial = 16 * (DP + 2);
 // of eight query heads.
 template <int KIND, bool QBF, int DP, int NG>
 __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 ? 2 : 1, DP>::kWarps,
-                                  NG == 1 ? Form<KIND == kTokBf16 || KIND == kTokF16 ? 2 : 1, DP>::kCtas : 1)
+                                  ctas_of(KIND == kTokBf16 || KIND == kTokF16 ? 2 : 1, DP, NG))
     paged_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                  const __grid_constant__ PagedParams p) {
     constexpr bool kCodes = KIND == kTokInt8 || KIND == kTokE4m3;
     constexpr int ES = kCodes ? 1 : 2;
     using F = Form<ES, DP>;
-    constexpr int kWarps = F::kWarps;
+    constexpr int kWarps = F::kWarps, kBlock = F::kBlock;
     constexpr bool kBf = KIND == kTokBf16;
     constexpr int kSteps = DP / 16;   // k-steps of the first product
     constexpr int kTiles = DP / 16;   // 16-row tiles of the second's output
@@ -259,7 +268,7 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
 
     // this CTA's run of units
     const long long per = static_cast<long long>(p.kv_heads) * p.blocks;
-    const long long total = sum_units<kWarps * 32>(p, s_scratch) * per;
+    const long long total = sum_units<F>(p, s_scratch) * per;
     const long long c = blockIdx.x, grid = gridDim.x;
     // (equal runs; the first total % grid are one longer)
     const long long share = total / grid, longer = total % grid;
@@ -268,7 +277,7 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
     if (threadIdx.x == 0) p.jobs[c] = make_int4(0, 0, 0, 0);
     // sequences that see nothing get zeros
     for (long long s = c; s < p.sequences; s += grid) {
-        if (seen_by(p, static_cast<int>(s)).units) continue;
+        if (seen_by<F>(p, static_cast<int>(s)).units) continue;
         for (int i = threadIdx.x; i < p.kv_heads * p.group * p.width; i += kWarps * 32) {
             unsigned char* o = p.out + (s * p.out_seq + (i / p.width) * p.out_head + i % p.width) * 2;
             *reinterpret_cast<uint16_t*>(o) = 0;
@@ -278,7 +287,7 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
     if (warp == 0) {
         int s;
         long long b;
-        find_unit(p, per, unit, &s, &b);
+        find_unit<F>(p, per, unit, &s, &b);
         if (lane == 0) {
             s_seq = s;
             s_before = b;
@@ -297,9 +306,11 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
     const uint32_t k_at = word_at(r0, q), v_at0 = word_at(2 * q, F::kVWord == 16 ? r : r >> 1),
                    v_at1 = word_at((2 * q + 1) ^ 4, F::kVWord == 16 ? r : r >> 1);
     const uint32_t v_half = F::kVOff + (F::kVWord == 16 ? 0u : (r & 1) * 8u);
-    const uint32_t block_bytes = 2u * F::kBoxes * F::kBox + (kCodes ? 128u : 0u);
+    const uint32_t block_bytes = F::kStage + (kCodes ? F::kScales : 0u);
+    // lanes that load a block's runs of rows_box tokens
+    const int runs = p.rows_box ? kBlock / p.rows_box : 1, run_at = min(lane, runs - 1) * p.rows_box;
     while (unit < end) {
-        const Seen see = seen_by(p, seq);
+        const Seen see = seen_by<F>(p, seq);
         if (see.units == 0) {
             ++seq;
             continue;
@@ -389,49 +400,45 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
         }
 
         // ---- the warp's blocks
-        const int b0 = u0 * (kUnit / kBlock), b1 = min(u1 * (kUnit / kBlock), see.blocks);
+        const int b0 = u0 * kWarps, b1 = min(u1 * kWarps, see.blocks);
         auto token_of = [&](int b) {
             return (b < see.lead_blocks ? b : b - see.lead_blocks + see.skip) * kBlock;
         };
         auto visible = [&](int t) { return t < see.length && (t >= see.from || t < see.lead); };
         const int32_t* table = p.map.table + seq * p.map.table_stride;
-        // the pages of the next block to ask for: of its first eight tokens and the others
-        auto page_of = [&](int b, int half) {
-            const int t = min(token_of(b) + 8 * half, see.length - 1);
-            return b < b1 ? table[fdiv(static_cast<uint32_t>(t), p.map.by_page)] : 0;
-        };
+        // the page of this lane's run of the next block to ask for
         const bool look = p.rows_box != 0 && !see.bad;
-        int page0 = 0, page1 = 0;
+        int page_ahead = 0;
         auto look_ahead = [&](int b) {
-            if (!look) return;
-            page0 = page_of(b, 0);
-            page1 = p.rows_box == 8 ? page_of(b, 1) : page0;
+            if (!look || b >= b1) return;
+            const int t = min(token_of(b) + run_at, see.length - 1);
+            page_ahead = table[fdiv(static_cast<uint32_t>(t), p.map.by_page)];
         };
         look_ahead(b0 + warp);
         uint32_t slow = 0;   // stages that were filled word by word (bits)
         auto issue = [&](int b, int st) {
             const uint32_t dst = ring + st * F::kStage, sdst = scales + st * F::kScales, bar = full0 + 8 * st;
-            const int t0 = token_of(b), pa = page0, pb = page1;
+            const int t0 = token_of(b), page = page_ahead;
             look_ahead(b + kWarps);
-            // (all 16 tokens are seen, in pages that are there)
-            if (look && t0 + kBlock <= see.length && (t0 >= see.from || t0 + kBlock <= see.lead) && pa >= 0 &&
-                pa < p.map.pages && pb >= 0 && pb < p.map.pages) {
+            // (all tokens are seen, in pages that are there)
+            if (look && t0 + kBlock <= see.length && (t0 >= see.from || t0 + kBlock <= see.lead) &&
+                __all_sync(0xffffffffu, page >= 0 && page < p.map.pages)) {
                 slow &= ~(1u << st);
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar, block_bytes);
-                    for (int h = 0; h < 16; h += p.rows_box) {
-                        const int page = h ? pb : pa;
-                        const int off = t0 + h - static_cast<int>(fdiv(static_cast<uint32_t>(t0 + h), p.map.by_page) * p.map.by_page.d);
+                if (lane == 0) mbar_arrive_expect_tx(bar, block_bytes);
+                __syncwarp();
+                if (lane < runs) {
+                    const int t = t0 + run_at;
+                    const int off = t - static_cast<int>(fdiv(static_cast<uint32_t>(t), p.map.by_page) * p.map.by_page.d);
 #pragma unroll
-                        for (int x = 0; x < F::kBoxes; ++x) {
-                            tma_load_4d(dst + x * F::kBox + h * 128u, &k_map, bar, x * (128 / ES), off, head, page);
-                            tma_load_4d(dst + F::kVOff + x * F::kBox + h * 128u, &v_map, bar, x * (128 / ES), off, head, page);
-                        }
-                        if (kCodes) {
-                            const long long at = page * p.map.scale_page_stride + head * p.map.scale_head_stride + off;
-                            bulk_load_1d(sdst + h * 4u, p.k_scale + at, p.rows_box * 4u, bar);
-                            bulk_load_1d(sdst + 64u + h * 4u, p.v_scale + at, p.rows_box * 4u, bar);
-                        }
+                    for (int x = 0; x < F::kBoxes; ++x) {
+                        tma_load_4d(dst + x * F::kBox + run_at * 128u, &k_map, bar, x * (128 / ES), off, head, page);
+                        tma_load_4d(dst + F::kVOff + x * F::kBox + run_at * 128u, &v_map, bar, x * (128 / ES), off, head,
+                                    page);
+                    }
+                    if (kCodes) {
+                        const long long at = page * p.map.scale_page_stride + head * p.map.scale_head_stride + off;
+                        bulk_load_1d(sdst + run_at * 4u, p.k_scale + at, p.rows_box * 4u, bar);
+                        bulk_load_1d(sdst + (kBlock + run_at) * 4u, p.v_scale + at, p.rows_box * 4u, bar);
                     }
                 }
                 return;
@@ -451,16 +458,19 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
                 }
             }
             // NaN for the scale of a token whose page is missing, which spoils the row
-            const int t = t0 + (lane & 15);
-            long long at = 0, sc = 0;
-            const bool want = visible(t) || see.bad;
-            const bool have = want && !see.bad && token_row(p.map, seq, t, head, &at, &sc);
-            if (kCodes && (have || !want))
-                cp_async<4>(sdst + lane * 4u, (lane < 16 ? p.k_scale : p.v_scale) + sc, have ? 4u : 0u);
-            else
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(sdst + lane * 4u),
-                             "f"(want && !have ? __uint_as_float(kNanBits) : 1.0f)
-                             : "memory");
+#pragma unroll 1
+            for (int e = lane; e < 2 * kBlock; e += 32) {
+                const int t = t0 + e % kBlock;
+                long long at = 0, sc = 0;
+                const bool want = visible(t) || see.bad;
+                const bool have = want && !see.bad && token_row(p.map, seq, t, head, &at, &sc);
+                if (kCodes && (have || !want))
+                    cp_async<4>(sdst + e * 4u, (e < kBlock ? p.k_scale : p.v_scale) + sc, have ? 4u : 0u);
+                else
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(sdst + e * 4u),
+                                 "f"(want && !have ? __uint_as_float(kNanBits) : 1.0f)
+                                 : "memory");
+            }
         };
         {
             int st = stage;
@@ -499,95 +509,105 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
             const uint32_t src = ring + stage * F::kStage, ssrc = scales + stage * F::kScales;
             const int t0 = token_of(b);
 
-            // ---- scores
-            // (two sums: a product waits for the one before in its own)
-            float sc[NG][4], sd[NG][4];
+            // ---- scores (two sums: a product waits for the one before in its own)
+            float s2[F::kSubs][NG][4];   // in powers of two
+            float lv[F::kSubs][2];
+            bool none[F::kSubs][2];      // values too small to count
 #pragma unroll
-            for (int n = 0; n < NG; ++n)
+            for (int u = 0; u < F::kSubs; ++u) {
+                float sc[NG][4], sd[NG][4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sc[n][j] = sd[n][j] = 0.0f;
+                for (int n = 0; n < NG; ++n)
 #pragma unroll
-            for (int w = 0; w < F::kKWords; ++w) {
-                uint32_t x[4], y[4];
-                // (the next word is in the other half of the row, its eighth in the next box)
-                const uint32_t at = src + (w >> 1) * F::kBox + (k_at ^ ((w & 1) * 64u));
-                lds<16>(at, x);
-                lds<16>(at + 1024u, y);
-                if constexpr (kCodes) {
+                    for (int j = 0; j < 4; ++j) sc[n][j] = sd[n][j] = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t x0, x1, y0, y1;
-                        widen4<KIND == kTokE4m3>(x[i], x0, x1);
-                        widen4<KIND == kTokE4m3>(y[i], y0, y1);
+                for (int w = 0; w < F::kKWords; ++w) {
+                    uint32_t x[4], y[4];
+                    // (the next word is in the other half of the row, its eighth in the next box)
+                    const uint32_t at = src + (u + (w >> 1)) * F::kBox + (k_at ^ ((w & 1) * 64u));
+                    lds<16>(at, x);
+                    lds<16>(at + 1024u, y);
+                    if constexpr (kCodes) {
 #pragma unroll
-                        for (int n = 0; n < NG; ++n)
-                            mma16816<false>(i & 1 ? sd[n] : sc[n], x0, y0, x1, y1, bq[n][4 * w + i][0],
-                                            bq[n][4 * w + i][1]);
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t x0, x1, y0, y1;
+                            widen4<KIND == kTokE4m3>(x[i], x0, x1);
+                            widen4<KIND == kTokE4m3>(y[i], y0, y1);
+#pragma unroll
+                            for (int n = 0; n < NG; ++n)
+                                mma16816<false>(i & 1 ? sd[n] : sc[n], x0, y0, x1, y1, bq[n][4 * w + i][0],
+                                                bq[n][4 * w + i][1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int n = 0; n < NG; ++n)
+                                mma16816<kBf>(i & 1 ? sd[n] : sc[n], x[2 * i], y[2 * i], x[2 * i + 1], y[2 * i + 1],
+                                              bq[n][2 * w + i][0], bq[n][2 * w + i][1]);
                     }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int n = 0; n < NG; ++n)
-                            mma16816<kBf>(i & 1 ? sd[n] : sc[n], x[2 * i], y[2 * i], x[2 * i + 1], y[2 * i + 1],
-                                          bq[n][2 * w + i][0], bq[n][2 * w + i][1]);
                 }
-            }
-#pragma unroll
-            for (int n = 0; n < NG; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sc[n][j] += sd[n][j];
-            // ---- weights: this thread's tokens are t0 + r0 and t0 + r0 + 8
-            float ks[2] = {1.0f, 1.0f}, lv[2] = {0.0f, 0.0f};
-            bool none[2] = {false, false};   // values too small to count
-            if (kCodes || by_words) {
+                // this thread's tokens are t0 + 16 u + r0 and the eighth after it
+                float ks[2] = {1.0f, 1.0f};
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks[i]) : "r"(ssrc + (r0 + 8 * i) * 4u));
+                    lv[u][i] = 0.0f;
+                    none[u][i] = false;
+                    if (!kCodes && !by_words) continue;
+                    const uint32_t at = ssrc + (16 * u + r0 + 8 * i) * 4u;
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks[i]) : "r"(at));
                     if (kCodes) {
                         float vs;
-                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs) : "r"(ssrc + (16 + r0 + 8 * i) * 4u));
-                        none[i] = vs < kTinyScale;
-                        lv[i] = none[i] ? -100.0f : lg2(vs);
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs) : "r"(at + kBlock * 4u));
+                        none[u][i] = vs < kTinyScale;
+                        lv[u][i] = none[u][i] ? -100.0f : lg2(vs);
                     }
                 }
+#pragma unroll
+                for (int n = 0; n < NG; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float s = (sc[n][j] + sd[n][j]) * (ks[j >> 1] * qscale[n][j & 1]);
+                        if (p.cap > 0.0f) {
+                            // cap * tanh(s / cap), tanh x = 1 - 2 / (1 + e^2x)
+                            const float e = ex2(s * (2.0f * kLog2e / p.cap));
+                            s = (p.cap - 2.0f * p.cap * rcp_approx(1.0f + e)) * kLog2e;
+                        }
+                        if (p.slopes)
+                            s -= slope[n][j & 1] * static_cast<float>(see.length - 1 - (t0 + 16 * u + r0 + 8 * (j >> 1)));
+                        s2[u][n][j] = s;
+                    }
             }
-            float s2[NG][4];   // scores in powers of two
-#pragma unroll
-            for (int n = 0; n < NG; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float s = sc[n][j] * (ks[j >> 1] * qscale[n][j & 1]);
-                    if (p.cap > 0.0f) {
-                        // cap * tanh(s / cap), tanh x = 1 - 2 / (1 + e^2x)
-                        const float e = ex2(s * (2.0f * kLog2e / p.cap));
-                        s = (p.cap - 2.0f * p.cap * rcp_approx(1.0f + e)) * kLog2e;
-                    }
-                    if (p.slopes)
-                        s -= slope[n][j & 1] * static_cast<float>(see.length - 1 - (t0 + r0 + 8 * (j >> 1)));
-                    s2[n][j] = s;
-                }
+            // ---- weights
             if (by_words) {   // (others are seen whole)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (!visible(t0 + r0 + 8 * i) && !see.bad) {
+                for (int u = 0; u < F::kSubs; ++u)
 #pragma unroll
-                        for (int n = 0; n < NG; ++n) s2[n][2 * i] = s2[n][2 * i + 1] = -INFINITY;
-                    }
+                    for (int i = 0; i < 2; ++i)
+                        if (!visible(t0 + 16 * u + r0 + 8 * i) && !see.bad) {
+#pragma unroll
+                            for (int n = 0; n < NG; ++n) s2[u][n][2 * i] = s2[u][n][2 * i + 1] = -INFINITY;
+                        }
             }
+            float best[NG][2];   // of this thread's tokens
             bool rise = false;
 #pragma unroll
             for (int n = 0; n < NG; ++n)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    rise |= fmaxf(s2[n][j] + lv[0], s2[n][j + 2] + lv[1]) > m[n][j] + kLag;
+                for (int j = 0; j < 2; ++j) {
+                    best[n][j] = fmaxf(s2[0][n][j] + lv[0][0], s2[0][n][j + 2] + lv[0][1]);
+                    if (F::kSubs == 2)
+                        best[n][j] = fmaxf(best[n][j], fmaxf(s2[F::kSubs - 1][n][j] + lv[F::kSubs - 1][0],
+                                                             s2[F::kSubs - 1][n][j + 2] + lv[F::kSubs - 1][1]));
+                    rise |= best[n][j] > m[n][j] + kLag;
+                }
             if (__any_sync(0xffffffffu, rise)) {
                 // all tokens' maximum, and everything relative to it
 #pragma unroll
                 for (int n = 0; n < NG; ++n)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float top = fmaxf(s2[n][j] + lv[0], s2[n][j + 2] + lv[1]);
+                        float top = best[n][j];
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -602,64 +622,67 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
                         }
                     }
             }
-            uint32_t bp[NG][2];
-#pragma unroll
-            for (int n = 0; n < NG; ++n) {
-                float pw[4];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float base = m[n][j] == -INFINITY ? 0.0f : m[n][j];
-                    const float x = s2[n][j] - base, y = s2[n][j + 2] - base;
-                    pw[j] = none[0] ? 0.0f : ex2(x + lv[0]);
-                    pw[j + 2] = none[1] ? 0.0f : ex2(y + lv[1]);
-                    l[n][j] += kCodes ? ex2(x) + ex2(y) : pw[j] + pw[j + 2];
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t w16;
-                    if (kBf) {
-                        w16 = pack_bf16x2(pw[2 * i], pw[2 * i + 1]);
-                    } else {
-                        const __half2 x = __floats2half2_rn(pw[2 * i], pw[2 * i + 1]);
-                        w16 = *reinterpret_cast<const uint32_t*>(&x);
-                    }
-                    bp[n][i] = transpose8x8(w16);
-                }
-            }
             // ---- output
 #pragma unroll
-            for (int w = 0; w < F::kVWords; ++w) {
-                uint32_t x[4][F::kVWord / 4];
+            for (int u = 0; u < F::kSubs; ++u) {
+                uint32_t bp[NG][2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    lds<F::kVWord>(src + v_half + (i & 1 ? v_at1 : v_at0) + (i >> 1) * 1024u + w * F::kBox, x[i]);
+                for (int n = 0; n < NG; ++n) {
+                    float pw[4];
 #pragma unroll
-                for (int i = 0; i < F::kVWord / 4; ++i) {
-                    // pairs of tokens side by side, an element (and the next) each
-                    if constexpr (kCodes) {
-                        uint32_t a[2][4];   // [tokens of the half][elements 0..3]
+                    for (int j = 0; j < 2; ++j) {
+                        const float base = m[n][j] == -INFINITY ? 0.0f : m[n][j];
+                        const float x = s2[u][n][j] - base, y = s2[u][n][j + 2] - base;
+                        pw[j] = none[u][0] ? 0.0f : ex2(x + lv[u][0]);
+                        pw[j + 2] = none[u][1] ? 0.0f : ex2(y + lv[u][1]);
+                        l[n][j] += kCodes ? ex2(x) + ex2(y) : pw[j] + pw[j + 2];
+                    }
 #pragma unroll
-                        for (int hlf = 0; hlf < 2; ++hlf) {
-                            const uint32_t lo = __byte_perm(x[2 * hlf][i], x[2 * hlf + 1][i], 0x5140);
-                            const uint32_t hi = __byte_perm(x[2 * hlf][i], x[2 * hlf + 1][i], 0x7362);
-                            widen4<KIND == kTokE4m3>(lo, a[hlf][0], a[hlf][1]);
-                            widen4<KIND == kTokE4m3>(hi, a[hlf][2], a[hlf][3]);
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t w16;
+                        if (kBf) {
+                            w16 = pack_bf16x2(pw[2 * i], pw[2 * i + 1]);
+                        } else {
+                            const __half2 x = __floats2half2_rn(pw[2 * i], pw[2 * i + 1]);
+                            w16 = *reinterpret_cast<const uint32_t*>(&x);
                         }
-                        constexpr int kPer = F::kVWord / 2;   // tiles of a word
+                        bp[n][i] = transpose8x8(w16);
+                    }
+                }
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
+                for (int w = 0; w < F::kVWords; ++w) {
+                    uint32_t x[4][F::kVWord / 4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        lds<F::kVWord>(src + v_half + (i & 1 ? v_at1 : v_at0) + (i >> 1) * 1024u + (u + w) * F::kBox, x[i]);
+#pragma unroll
+                    for (int i = 0; i < F::kVWord / 4; ++i) {
+                        // pairs of tokens side by side, an element (and the next) each
+                        if constexpr (kCodes) {
+                            uint32_t a[2][4];   // [tokens of the half][elements 0..3]
+#pragma unroll
+                            for (int hlf = 0; hlf < 2; ++hlf) {
+                                const uint32_t lo = __byte_perm(x[2 * hlf][i], x[2 * hlf + 1][i], 0x5140);
+                                const uint32_t hi = __byte_perm(x[2 * hlf][i], x[2 * hlf + 1][i], 0x7362);
+                                widen4<KIND == kTokE4m3>(lo, a[hlf][0], a[hlf][1]);
+                                widen4<KIND == kTokE4m3>(hi, a[hlf][2], a[hlf][3]);
+                            }
+                            constexpr int kPer = F::kVWord / 2;   // tiles of a word
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                for (int n = 0; n < NG; ++n)
+                                    mma16816<false>(o[n][w * kPer + 2 * i + k], a[0][2 * k], a[0][2 * k + 1],
+                                                    a[1][2 * k], a[1][2 * k + 1], bp[n][0], bp[n][1]);
+                        } else {
+                            const uint32_t a0 = __byte_perm(x[0][i], x[1][i], 0x5410);
+                            const uint32_t a1 = __byte_perm(x[0][i], x[1][i], 0x7632);
+                            const uint32_t a2 = __byte_perm(x[2][i], x[3][i], 0x5410);
+                            const uint32_t a3 = __byte_perm(x[2][i], x[3][i], 0x7632);
 #pragma unroll
                             for (int n = 0; n < NG; ++n)
-                                mma16816<false>(o[n][w * kPer + 2 * i + k], a[0][2 * k], a[0][2 * k + 1],
-                                                a[1][2 * k], a[1][2 * k + 1], bp[n][0], bp[n][1]);
-                    } else {
-                        const uint32_t a0 = __byte_perm(x[0][i], x[1][i], 0x5410);
-                        const uint32_t a1 = __byte_perm(x[0][i], x[1][i], 0x7632);
-                        const uint32_t a2 = __byte_perm(x[2][i], x[3][i], 0x5410);
-                        const uint32_t a3 = __byte_perm(x[2][i], x[3][i], 0x7632);
-#pragma unroll
-                        for (int n = 0; n < NG; ++n)
-                            mma16816<kBf>(o[n][w * 4 + i], a0, a1, a2, a3, bp[n][0], bp[n][1]);
+                                mma16816<kBf>(o[n][w * 4 + i], a0, a1, a2, a3, bp[n][0], bp[n][1]);
+                        }
                     }
                 }
             }
@@ -757,35 +780,77 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
 
 // Joins the partial results of the key heads that several CTAs share, in the order of
 // their tokens: block c joins the one that begins in CTA c's run and goes on beyond it.
+// Every part's weight is taken first, so that the sums' loads do not wait for one another.
+constexpr int kMaxParts = 480;   // and CTAs of the first launch
+
 template <bool QBF, int DP>
 __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedParams p) {
+    __shared__ float weight[16][kMaxParts];
+    __shared__ float total[16];
     griddep_launch_dependents();
     griddep_wait();
-    const int c = blockIdx.x;
-    const int4 job = p.jobs[c];
+    const int c = blockIdx.x, lane = threadIdx.x & 31;
+    const int4 job = p.jobs[c];   // sequence, first query head, heads, further parts
     if (job.w == 0) return;
-    const float* first = p.partial + (static_cast<long long>(c) * 2 + 1) * kPartial<DP>;
-    const float* next = p.partial + static_cast<long long>(c + 1) * 2 * kPartial<DP>;
+    // part k of head h: the owner's second slot, then the others' first ones
+    auto part = [&](int k, int h) {
+        return p.partial + ((static_cast<long long>(c) + k) * 2 + (k == 0)) * kPartial<DP> + h * (DP + 2);
+    };
+    // a few parts: every thread takes their weights itself, all loads at once
+    constexpr int kFew = 8;
+    const bool few = job.w < kFew;
+    for (int h = threadIdx.x >> 5; h < job.z && !few; h += 8) {
+        float top = -INFINITY;
+        for (int k = lane; k <= job.w; k += 32) top = fmaxf(top, part(k, h)[0]);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float base = top == -INFINITY ? 0.0f : top;
+        float sum = 0.0f;
+        for (int k = lane; k <= job.w; k += 32) {
+            const float f = ex2(part(k, h)[0] - base);
+            weight[h][k] = f;
+            sum += part(k, h)[1] * f;
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane == 0) total[h] = sum;
+    }
+    __syncthreads();
     for (int i = threadIdx.x; i < job.z * (DP / 2); i += 256) {
         const int h = i / (DP / 2), d = 2 * (i - h * (DP / 2));
         if (d >= p.width) continue;
-        const int at = h * (DP + 2);
-        float top = first[at], sum = first[at + 1];
-        float2 v = *reinterpret_cast<const float2*>(first + at + 2 + d);
-        float x = v.x, y = v.y;
-#pragma unroll 4
-        for (int k = 0; k < job.w; ++k) {
-            const float* f = next + static_cast<long long>(k) * 2 * kPartial<DP> + at;
-            const float t = f[0];
-            v = *reinterpret_cast<const float2*>(f + 2 + d);
-            const float now = fmaxf(top, t), base = now == -INFINITY ? 0.0f : now;
-            const float fa = ex2(top - base), fb = ex2(t - base);
-            x = x * fa + v.x * fb;
-            y = y * fa + v.y * fb;
-            sum = sum * fa + f[1] * fb;
-            top = now;
+        float x = 0.0f, y = 0.0f, all = 0.0f;
+        if (few) {
+            float2 ms[kFew], v[kFew];
+#pragma unroll
+            for (int k = 0; k < kFew; ++k) {
+                const float* f = part(min(k, job.w), h);
+                ms[k] = *reinterpret_cast<const float2*>(f);
+                v[k] = *reinterpret_cast<const float2*>(f + 2 + d);
+            }
+            float top = ms[0].x;
+#pragma unroll
+            for (int k = 1; k < kFew; ++k) top = fmaxf(top, ms[k].x);
+            const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+            for (int k = 0; k < kFew; ++k) {
+                if (k > job.w) break;
+                const float f = ex2(ms[k].x - base);
+                x = fmaf(v[k].x, f, x);
+                y = fmaf(v[k].y, f, y);
+                all = fmaf(ms[k].y, f, all);
+            }
+        } else {
+#pragma unroll 8
+            for (int k = 0; k <= job.w; ++k) {
+                const float f = weight[h][k];
+                const float2 v = *reinterpret_cast<const float2*>(part(k, h) + 2 + d);
+                x = fmaf(v.x, f, x);
+                y = fmaf(v.y, f, y);
+            }
+            all = total[h];
         }
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float inv = all == 0.0f ? 0.0f : 1.0f / all;
         uint32_t w;
         if (QBF) {
             w = pack_bf16x2(x * inv, y * inv);
@@ -803,9 +868,12 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 int padded(int width) { return width <= 64 ? 64 : width <= 128 ? 128 : 256; }
 
 template <int KIND, bool QBF, int DP, int NG>
-cudaError_t run(const PagedMaps& maps, const PagedParams& p, cudaStream_t stream) {
+cudaError_t run(const PagedMaps& maps, const PagedParams& p0, cudaStream_t stream) {
     constexpr int ES = KIND == kTokBf16 || KIND == kTokF16 ? 2 : 1;
     using F = Form<ES, DP>;
+    constexpr int kCtas = ctas_of(ES, DP, NG);
+    PagedParams p = p0;
+    p.grid = p0.grid < kCtas * p0.num_sms ? p0.grid : kCtas * p0.num_sms;
     constexpr size_t meet = sizeof(float) * F::kWarps * 8 * NG * (DP + 4 + 2);
     static_assert(meet <= F::kRing, "the warps' results meet over the rings");
     constexpr size_t smem = F::kBytes;
@@ -815,7 +883,7 @@ cudaError_t run(const PagedMaps& maps, const PagedParams& p, cudaStream_t stream
     e = launch_ex(paged_kernel<KIND, QBF, DP, NG>, static_cast<unsigned>(p.grid), dim3(32 * F::kWarps), smem, 1,
                   stream, maps.k, maps.v, p);
     // (a table of no more than a unit's tokens leaves nothing to join)
-    if (e != cudaSuccess || p.grid == 1 || p.map.capacity <= kUnit) return e;
+    if (e != cudaSuccess || p.grid == 1 || p.map.capacity <= F::kUnit) return e;
     return launch_ex(paged_join_kernel<QBF, DP>, static_cast<unsigned>(p.grid), dim3(256), 0, 1, stream, p);
 }
 
@@ -835,10 +903,10 @@ static int pass_heads(long long group, int width) { return group > 8 && width <=
 
 int paged_grid(long long sequences, long long kv_heads, long long group, int width,
                long long capacity, int num_sms) {
-    // two CTAs an SM, as far as there can be units
+    // three CTAs an SM at most, as far as there can be units
     const long long blocks = (group + pass_heads(group, width) - 1) / pass_heads(group, width);
-    const long long units = (capacity + kUnit - 1) / kUnit;
-    const long long most = 2ll * num_sms;
+    const long long units = (capacity + 63) / 64;   // (the smallest form's)
+    const long long most = 3ll * num_sms < kMaxParts ? 3ll * num_sms : kMaxParts;
     if (units >= most) return static_cast<int>(most);
     long long n = units * kv_heads * blocks;
     n = n >= most || sequences >= most ? most : n * sequences;
