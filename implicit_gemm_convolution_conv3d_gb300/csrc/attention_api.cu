@@ -199,9 +199,13 @@ int rotary_fwd(const void* x, int dtype, int64_t x_token_stride, int64_t x_head_
     p.interleaved = interleaved != 0;
     p.inverse = inverse != 0;
     p.copy_rest = out != x;
-    const bool aligned = words(x, x_token_stride, x_head_stride, elt) &&
-                         words(out, out_token_stride, out_head_stride, elt);
-    return launched(launch_rotary(p, dtype, aligned, stream), "rotary_fwd launch");
+    int align = 16;
+    const int64_t at[6] = {static_cast<int64_t>(reinterpret_cast<uintptr_t>(x)),
+                           static_cast<int64_t>(reinterpret_cast<uintptr_t>(out)), x_token_stride * elt,
+                           x_head_stride * elt, out_token_stride * elt, out_head_stride * elt};
+    for (int64_t v : at)
+        while (v % align) align /= 2;
+    return launched(launch_rotary(p, dtype, align, stream), "rotary_fwd launch");
 }
 
 int kv_cache_write(const kv_cache* cache, const void* k, const void* v, int dtype,

@@ -25,7 +25,8 @@ struct RotaryParams {
     unsigned long long turns[ROTARY_MAX_PAIRS];
     unsigned char axis[ROTARY_MAX_PAIRS];
 };
-cudaError_t launch_rotary(const RotaryParams& p, int dtype, bool aligned, cudaStream_t stream);
+// align: bytes (up to 16) that all rows are aligned to
+cudaError_t launch_rotary(const RotaryParams& p, int dtype, int align, cudaStream_t stream);
 
 // where a sequence's tokens lie
 struct PageMap {

@@ -35,26 +35,49 @@ __global__ void __launch_bounds__(kThreads)
     constexpr int NP = HALF ? VEC : (VEC > 1 ? VEC / 2 : 1);   // pairs of a unit
     const long long tok0 = static_cast<long long>(blockIdx.x) * tokens_block;
     const int here = static_cast<int>(min(static_cast<long long>(tokens_block), p.tokens - tok0));
+    // a thread: unit `u` of token `t`, heads h0, h0 + lanes, ...
+    const int u = threadIdx.x % units, rest = threadIdx.x / units;
+    const int h0 = rest % lanes, t = rest / lanes;
+    const T* x = static_cast<const T*>(p.x) + (tok0 + t) * p.x_tok;
+    T* out = static_cast<T*>(p.out) + (tok0 + t) * p.out_tok;
+    const int rot_units = p.pairs / NP;
+    using V = Vec<T, VEC>;
+    constexpr int kUnroll = 4;
+    const int ea = HALF ? u * VEC : u * 2 * NP;
+    const int eb = HALF ? ea + p.pairs : ea + 1;
+    constexpr bool kTwo = HALF || VEC == 1;   // two loads a unit
+    V a[kUnroll], b[kUnroll];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            const int hh = h + i * lanes;
+            if (hh < p.heads) {
+                a[i] = *reinterpret_cast<const V*>(x + hh * p.x_head + ea);
+                if (kTwo) b[i] = *reinterpret_cast<const V*>(x + hh * p.x_head + eb);
+            }
+        }
+    };
+    // (on their way while the sines are taken)
+    const bool turns = t < here && u < rot_units;
+    if (turns) load(h0);
     for (int i = threadIdx.x; i < here * p.pairs; i += kThreads) {
-        const int t = i / p.pairs, pair = i - t * p.pairs;
-        const long long at = (tok0 + t) * p.axes + p.axis[pair];
+        const int tt = i / p.pairs, pair = i - tt * p.pairs;
+        // (a lane's own entry: by its generic address, as the constant path takes one lane's at a time)
+        unsigned long long per;
+        uint32_t axis;
+        asm("ld.u64 %0, [%1];" : "=l"(per) : "l"(p.turns + pair));
+        asm("ld.u8 %0, [%1];" : "=r"(axis) : "l"(p.axis + pair));
+        const long long at = (tok0 + tt) * p.axes + axis;
         const long long pos = p.pos64 ? static_cast<const long long*>(p.positions)[at]
                                       : static_cast<const int*>(p.positions)[at];
-        const long long turn = static_cast<long long>(static_cast<unsigned long long>(pos) * p.turns[pair]);
+        const long long turn = static_cast<long long>(static_cast<unsigned long long>(pos) * per);
         float s, c;
         sincospif(__ll2float_rn(turn) * 1.0842021724855044e-19f, &s, &c);   // 2^-63: half turns
         table[i] = make_float2(c, p.inverse ? -s : s);
     }
     __syncthreads();
-    // a thread: unit `u` of token `t`, heads h0, h0 + lanes, ...
-    const int u = threadIdx.x % units, rest = threadIdx.x / units;
-    const int h0 = rest % lanes, t = rest / lanes;
     if (t >= here) return;
-    const T* x = static_cast<const T*>(p.x) + (tok0 + t) * p.x_tok;
-    T* out = static_cast<T*>(p.out) + (tok0 + t) * p.out_tok;
-    const int rot_units = p.pairs / NP;
-    using V = Vec<T, VEC>;
-    if (u >= rot_units) {   // elements that are not rotated
+    if (!turns) {   // elements that are not rotated
         for (int e = 2 * p.pairs + (u - rot_units) * VEC; e < p.width; e += (units - rot_units) * VEC)
             for (int h = h0; h < p.heads; h += lanes)
                 *reinterpret_cast<V*>(out + h * p.out_head + e) =
@@ -68,20 +91,8 @@ __global__ void __launch_bounds__(kThreads)
         c[i] = cs.x;
         s[i] = cs.y;
     }
-    constexpr int kUnroll = 4;
-    const int ea = HALF ? u * VEC : u * 2 * NP;
-    const int eb = HALF ? ea + p.pairs : ea + 1;
-    constexpr bool kTwo = HALF || VEC == 1;   // two loads a unit
     for (int h = h0; h < p.heads; h += kUnroll * lanes) {
-        V a[kUnroll], b[kUnroll];
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            const int hh = h + i * lanes;
-            if (hh < p.heads) {
-                a[i] = *reinterpret_cast<const V*>(x + hh * p.x_head + ea);
-                if (kTwo) b[i] = *reinterpret_cast<const V*>(x + hh * p.x_head + eb);
-            }
-        }
+        if (h != h0) load(h);
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
             const int hh = h + i * lanes;
@@ -125,21 +136,28 @@ cudaError_t run(const RotaryParams& p, cudaStream_t stream) {
                      stream, p, units, lanes, toks);
 }
 
+// The widest loads that the rows' alignment, the pairs' distance and the elements left
+// over allow: 16 bytes, 8, 4 (of 16-bit elements), or one element at a time.
 template <typename T>
-cudaError_t by_form(const RotaryParams& p, bool aligned, cudaStream_t stream) {
+cudaError_t by_form(const RotaryParams& p, int align, cudaStream_t stream) {
+    const int per = p.interleaved ? 2 * p.pairs : p.pairs, rest = p.width - 2 * p.pairs;
+    auto fits = [&](int vec) {
+        return align >= vec * static_cast<int>(sizeof(T)) && per % vec == 0 && rest % vec == 0;
+    };
     constexpr int W = 16 / sizeof(T);
-    const int per = p.interleaved ? 2 * p.pairs : p.pairs;
-    if (aligned && per % W == 0 && (p.width - 2 * p.pairs) % W == 0)
-        return p.interleaved ? run<T, W, false>(p, stream) : run<T, W, true>(p, stream);
+    if (fits(W)) return p.interleaved ? run<T, W, false>(p, stream) : run<T, W, true>(p, stream);
+    if (fits(W / 2)) return p.interleaved ? run<T, W / 2, false>(p, stream) : run<T, W / 2, true>(p, stream);
+    if constexpr (W == 8)
+        if (fits(2)) return p.interleaved ? run<T, 2, false>(p, stream) : run<T, 2, true>(p, stream);
     return p.interleaved ? run<T, 1, false>(p, stream) : run<T, 1, true>(p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_rotary(const RotaryParams& p, int dtype, bool aligned, cudaStream_t stream) {
-    if (dtype == kTokBf16) return by_form<__nv_bfloat16>(p, aligned, stream);
-    if (dtype == kTokF16) return by_form<__half>(p, aligned, stream);
-    return by_form<float>(p, aligned, stream);
+cudaError_t launch_rotary(const RotaryParams& p, int dtype, int align, cudaStream_t stream) {
+    if (dtype == kTokBf16) return by_form<__nv_bfloat16>(p, align, stream);
+    if (dtype == kTokF16) return by_form<__half>(p, align, stream);
+    return by_form<float>(p, align, stream);
 }
 
 }  // namespace c3d
