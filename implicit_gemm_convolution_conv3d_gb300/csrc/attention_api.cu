@@ -3,9 +3,12 @@
 // No allocation.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
+#include <initializer_list>
+#include <utility>
 
 #include "attention_internal.h"
 #include "token_common.cuh"
@@ -39,6 +42,22 @@ int size_of(int t) {
 bool aligned_to(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) % bytes) == 0; }
 bool fits(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
 
+// whether rows of `width` elements share some, for dimensions {size, stride} that lie in
+// one another in some order
+bool overlap(int64_t width, std::initializer_list<std::pair<int64_t, int64_t>> dims) {
+    std::pair<int64_t, int64_t> d[3];
+    int n = 0;
+    for (const auto& e : dims)
+        if (e.first > 1) d[n++] = {e.second, e.first};
+    std::sort(d, d + n);
+    __int128 extent = width;
+    for (int i = 0; i < n; ++i) {
+        if (d[i].first < extent) return true;
+        extent += static_cast<__int128>(d[i].second - 1) * d[i].first;
+    }
+    return false;
+}
+
 // heads of tokens: [tokens, heads, width] with strides in elements
 const char* bad_heads(const void* p, int64_t tok, int64_t head, int64_t tokens, int64_t heads,
                       int64_t width, int elt) {
@@ -48,6 +67,12 @@ const char* bad_heads(const void* p, int64_t tok, int64_t head, int64_t tokens, 
     if (heads > 1 && head < width) return "a head stride is below the head's width";
     if (tokens > 1 && tok < width) return "a token stride is below the head's width";
     return nullptr;
+}
+// the same of an output, whose rows nothing else may share
+const char* bad_out(const void* p, int64_t tok, int64_t head, int64_t tokens, int64_t heads,
+                    int64_t width, int elt) {
+    if (const char* e = bad_heads(p, tok, head, tokens, heads, width, elt)) return e;
+    return overlap(width, {{tokens, tok}, {heads, head}}) ? "an output's rows overlap" : nullptr;
 }
 bool words(const void* p, int64_t tok, int64_t head, int elt) {
     return aligned_to(p, 16) && tok * elt % 16 == 0 && head * elt % 16 == 0;
@@ -67,11 +92,15 @@ const char* bad_cache(const kv_cache* c) {
     if (c->row_stride > 1 << 26) return "a cache's row stride must be below 2^26";
     if (c->row_stride < c->width || c->head_stride < 0 || c->page_stride < 0)
         return "a cache's row stride is below its width";
+    if (overlap(c->width, {{c->pages, c->page_stride}, {c->heads, c->head_stride}, {c->page_size, c->row_stride}}))
+        return "a cache's rows overlap";
     if (is_code_type(c->dtype)) {
         if (!c->k_scale || !c->v_scale) return "an 8-bit cache needs scales";
         if (!aligned_to(c->k_scale, 4) || !aligned_to(c->v_scale, 4))
             return "a pointer is not aligned to its element type";
         if (c->scale_page_stride < 0 || c->scale_head_stride < 0) return "strides must be 0 or more";
+        if (overlap(1, {{c->pages, c->scale_page_stride}, {c->heads, c->scale_head_stride}, {c->page_size, 1}}))
+            return "a cache's scales overlap";
     }
     return nullptr;
 }
@@ -118,8 +147,8 @@ int cache_rows(const kv_cache* cache, void* k, void* v, int dtype, int64_t token
     if (!aligned_to(offsets, 4) || !aligned_to(starts, 4))
         return invalid("a pointer is not aligned to its element type");
     for (const void* p : {static_cast<const void*>(k), static_cast<const void*>(v)})
-        if (const char* e = bad_heads(p, token_stride, head_stride, tokens, cache->heads, cache->width,
-                                      size_of(dtype)))
+        if (const char* e = (write ? bad_heads : bad_out)(p, token_stride, head_stride, tokens, cache->heads,
+                                                          cache->width, size_of(dtype)))
             return invalid(e);
     if (tokens > kMaxDim * 4 / cache->heads) {
         set_last_error("more rows than the kernels count");
@@ -180,7 +209,7 @@ int rotary_fwd(const void* x, int dtype, int64_t x_token_stride, int64_t x_head_
     if (tokens == 0 || heads == 0) return CONV_OK;
     const int elt = size_of(dtype);
     if (const char* e = bad_heads(x, x_token_stride, x_head_stride, tokens, heads, width, elt)) return invalid(e);
-    if (const char* e = bad_heads(out, out_token_stride, out_head_stride, tokens, heads, width, elt))
+    if (const char* e = bad_out(out, out_token_stride, out_head_stride, tokens, heads, width, elt))
         return invalid(e);
     if (!positions || !aligned_to(positions, position_bytes)) return invalid("null or unaligned positions");
     p.x = x;
@@ -260,7 +289,7 @@ int paged_attention_fwd(const void* q, int q_dtype, int64_t q_sequence_stride,
         return invalid("a pointer is not aligned to its element type");
     if (const char* e = bad_heads(q, q_sequence_stride, q_head_stride, sequences, heads, cache->width, 2))
         return invalid(e);
-    if (const char* e = bad_heads(out, out_sequence_stride, out_head_stride, sequences, heads, cache->width, 2))
+    if (const char* e = bad_out(out, out_sequence_stride, out_head_stride, sequences, heads, cache->width, 2))
         return invalid(e);
     LaunchLimits lim;
     if (int rc = launch_limits(&lim)) return rc;
@@ -338,7 +367,7 @@ int packed_attention_fwd(const void* q, int64_t q_token_stride, int64_t q_head_s
     if (!aligned_to(q_offsets, 4) || !aligned_to(k_offsets, 4) || !aligned_to(prefix, 4) || !aligned_to(slopes, 4))
         return invalid("a pointer is not aligned to its element type");
     if (const char* e = bad_heads(q, q_token_stride, q_head_stride, q_tokens, heads, width, 2)) return invalid(e);
-    if (const char* e = bad_heads(out, out_token_stride, out_head_stride, q_tokens, heads, width, 2))
+    if (const char* e = bad_out(out, out_token_stride, out_head_stride, q_tokens, heads, width, 2))
         return invalid(e);
     if (k_tokens)
         for (const void* t : {k, v})

@@ -4,8 +4,8 @@ paged cache of keys and values in 8 (or 16) bits, attention of one new token ove
 that cache, and attention within documents packed in one buffer.
 
 Heads of tokens are ``[tokens, heads, width]`` tensors whose last dimension is
-contiguous; tokens and heads may have any stride, as parts of one projection's
-rows have.  A cache is a pair of ``[pages, kv_heads, page_size, width]`` tensors,
+contiguous; tokens and heads may have any stride from the width on, as parts of one
+projection's rows have, and an output's or a cache's rows may not overlap.  A cache is a pair of ``[pages, kv_heads, page_size, width]`` tensors,
 with fp32 scales ``[pages, kv_heads, page_size]`` where it is ``torch.int8`` or
 ``torch.float8_e4m3fn`` (value = code * scale); ``page_table`` [sequences, pages of
 the longest] int32 says where token t of a sequence lies: row ``t % page_size`` of
@@ -62,6 +62,16 @@ def _bind():
                                          i64, vp]
     _fns = lib
     return lib
+
+
+def _here(x: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
+    """One device for all of a call's tensors: the current one, which launches."""
+    d = x.device
+    if d.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {d}, which is not the current device")
+    for t in others:
+        if t is not None and t.device != d:
+            raise ValueError(f"all tensors of a call must be on {d}")
 
 
 def _heads(t: torch.Tensor, types: dict, what: str) -> Tuple[int, int, int, int, int, int]:
@@ -220,6 +230,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, sections: Sequence[int],
         os_, oh = ts, hs
     else:
         out, os_, oh = _given(out, x, _FLOAT, code, stream)
+    _here(x, positions, out)
     st = lib.rotary_fwd(x.data_ptr(), code, ts, hs, positions.data_ptr(), positions.element_size(),
                         axes, axis, freq, n, pairs == "interleaved", bool(inverse), tokens, heads,
                         width, out.data_ptr(), os_, oh, _stream(stream, x))
@@ -252,6 +263,7 @@ def kv_cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
     tp, tstride, pages, n = _table(page_table)
     if offsets is None and tokens != n:
         raise ValueError("without offsets there is one token for each sequence of page_table")
+    _here(k, v, k_cache, v_cache, page_table, starts, k_scale, v_scale, offsets)
     st = lib.kv_cache_write(c, k.data_ptr(), v.data_ptr(), code, ts, hs, tokens,
                             _ints(offsets, n + 1, "offsets"), _ints(starts, n, "starts"), tp,
                             tstride, pages, n, _stream(stream, k))
@@ -285,6 +297,7 @@ def kv_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torc
     if heads != c.heads or width != c.width:
         raise ValueError(f"k_out and v_out must be [tokens, {c.heads}, {c.width}] for this cache")
     tp, tstride, pages, n = _table(page_table)
+    _here(k_cache, v_cache, page_table, offsets, starts, k_scale, v_scale, k_out, v_out)
     st = lib.kv_cache_read(c, k_out.data_ptr(), v_out.data_ptr(), code, ts, hs, rows,
                            _ints(offsets, n + 1, "offsets"), _ints(starts, n, "starts"), tp,
                            tstride, pages, n, _stream(stream, k_cache))
@@ -342,6 +355,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                                       pages),), torch.uint8, q, stream)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
+    _here(q, k_cache, v_cache, page_table, lengths, k_scale, v_scale, prefix, slopes, out, workspace)
     st = lib.paged_attention_fwd(
         q.data_ptr(), code, qs, qh, c, tp, tstride, pages, _ints(lengths, n, "lengths"),
         _ints(prefix, n, "prefix"), _slopes(slopes, heads),
@@ -384,6 +398,7 @@ def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offset
             raise ValueError("without k_offsets q and k must have the same tokens")
         k_offsets = q_offsets
     out, os_, oh = _given(out, q, _HALF, code, stream)
+    _here(q, k, v, q_offsets, k_offsets, prefix, slopes, out)
     st = lib.packed_attention_fwd(
         q.data_ptr(), qs, qh, k.data_ptr(), v.data_ptr(), ks, kh, code,
         _ints(q_offsets, n + 1, "q_offsets"), _ints(k_offsets, n + 1, "k_offsets"), n, nq, nk,

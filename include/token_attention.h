@@ -24,6 +24,7 @@
  *     What it does not see takes no part, whatever it holds.  A query that sees
  *     nothing (or whose scores are all -inf) gets zeros.
  *   - Query head h reads key head h / (heads / kv_heads).
+ *   - Rows of an output or of a cache that overlap are refused.
  */
 #ifndef TOKEN_ATTENTION_GB300_H
 #define TOKEN_ATTENTION_GB300_H
