@@ -50,12 +50,6 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <bool BF>
-__device__ __forceinline__ float elem(const unsigned char* base, long long i) {
-    if (BF) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(base)[i]);
-    return __half2float(reinterpret_cast<const __half*>(base)[i]);
-}
-
 // 128 * NQ rows from `row0` of a document, for one head (negative: no more jobs).
 // Its key tiles, in order, are those of the document's lead (lead_tiles), then those from
 // tile `skip` on; a query tile sees the first `lead` of them and those from lo to hi.
@@ -163,7 +157,6 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
 }
 struct RowMask {
     int lo, hi, lead, keys;
-    __device__ bool operator()(int j) const { return j < keys && ((j >= lo && j < hi) || j < lead); }
     // keys j .. j + 31 as bits
     __device__ uint32_t bits(int j) const {
         return ((bits_below(hi - j) & ~bits_below(lo - j)) | bits_below(lead - j)) & bits_below(keys - j);
@@ -174,60 +167,73 @@ __device__ __forceinline__ RowMask row_mask(const PackedParams& p, const Job& j,
     return RowMask{r.lo, r.hi, r.lead, j.keys};
 }
 
+// Four elements of a row
+template <bool BF>
+__device__ __forceinline__ void four(const unsigned char* base, long long i, float (&v)[4]) {
+    const uint2 w = *reinterpret_cast<const uint2*>(base + 2 * i);
+    const uint32_t x[2] = {w.x, w.y};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint16_t h = static_cast<uint16_t>(x[e >> 1] >> (16 * (e & 1)));
+        v[e] = BF ? __uint_as_float(static_cast<uint32_t>(h) << 16) : __half2float(__ushort_as_half(h));
+    }
+}
+
 // A row whose result is not finite although what it sees may be: an unseen key of a
 // tile that was multiplied (weight 0) has a value that is not finite.  Then the row is
-// computed again, over what it sees alone.  Rolled loops: it should not take the
-// instruction cache from the others.
+// computed again, over what it sees alone, by the whole warp, four elements a lane (about
+// 100 cycles a key: the other warps wait meanwhile, and their waits are bounded).  Rolled
+// loops: it should not take the instruction cache from the others.
 template <bool BF>
-__device__ __forceinline__ void redo_row(const PackedParams& p, const Job& job, const Seen& seen, int row) {
-    const int kv = job.head / p.group;
+__device__ __forceinline__ void redo_row(const PackedParams& p, const Job& job, const Seen& seen, int row, int lane) {
     const RowMask m = row_mask(p, job, row);
-    const long long vbase = job.k0 * p.k_tok + static_cast<long long>(kv) * p.k_head;
-    const long long qb = (job.q0 + row) * p.q_tok + static_cast<long long>(job.head) * p.q_head;
+    const bool in = 4 * lane < p.width;
+    const long long base = job.k0 * p.k_tok + static_cast<long long>(job.head / p.group) * p.k_head + 4 * lane;
     const float slope2 = p.slopes ? p.slopes[job.head] * kLog2e : 0.0f;
-    float top = -INFINITY, sum = 0.0f, o[128];
+    float top = -INFINITY, sum = 0.0f, q[4] = {}, o[4] = {};
+    if (in) four<BF>(p.q, (job.q0 + row) * p.q_tok + static_cast<long long>(job.head) * p.q_head + 4 * lane, q);
     bool spoiled = false, nan = false;
+    // pass 0: is an unseen key's value the cause?  1: the row
 #pragma unroll 1
-    for (int d = 0; d < p.width; ++d) o[d] = 0.0f;
-    // pass 0: is an unseen key's value the cause?  1: the maximum, 2: the sums
+    for (int pass = 0; pass < 2; ++pass) {
+        if (pass && !__any_sync(0xffffffffu, spoiled)) return;
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        if ((pass && !spoiled) || nan) break;
+        for (int n = 0; n < 4 * job.count; ++n) {
+            const int j0 = job.key(n >> 2) + 32 * (n & 3);
+            uint32_t bits = m.bits(j0);
+            if (pass == 0) bits = ~bits & bits_below(job.keys - j0);
+            if (!seen(n >> 2)) bits = 0u;
 #pragma unroll 1
-        for (int n = 0; n < job.count; ++n) {
-            if (!seen(n)) continue;
-            const int t0 = job.key(n);
-#pragma unroll 1
-            for (int j = t0; j < min(t0 + kRows, job.keys); ++j) {
-                if (m(j) != (pass != 0)) continue;
-                const long long at = vbase + j * p.k_tok;
-                float s = 0.0f;
-                if (pass) {
-#pragma unroll 1
-                    for (int d = 0; d < p.width; ++d) s += elem<BF>(p.q, qb + d) * elem<BF>(p.k, at + d);
-                    s = shaped(p, s, row + job.shift, j, slope2);
-                    nan = nan || !(s < INFINITY);
-                    if (pass == 1) top = fmaxf(top, s);
-                    s = top == -INFINITY ? 0.0f : ex2(s - top);
-                    if (pass == 2) sum += s;
+            for (; bits; bits &= bits - 1u) {
+                const int j = j0 + __ffs(bits) - 1;
+                float k[4] = {}, v[4] = {};
+                if (in) four<BF>(p.v, base + j * p.k_tok, v);
+                if (pass == 0) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) spoiled = spoiled || !(fabsf(v[e]) < INFINITY);
+                    continue;
                 }
-                if (pass == 1) continue;
-#pragma unroll 1
-                for (int d = 0; d < p.width; ++d) {
-                    const float v = elem<BF>(p.v, at + d);
-                    if (pass == 0) spoiled = spoiled || !(fabsf(v) < INFINITY);
-                    else o[d] += s * v;
-                }
+                if (in) four<BF>(p.k, base + j * p.k_tok, k);
+                float s = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+                s = shaped(p, s, row + job.shift, j, slope2);
+                nan = nan || !(s < INFINITY);
+                const float now = fmaxf(top, s);
+                const float fall = now == -INFINITY ? 1.0f : ex2(top - now), w = now == -INFINITY ? 0.0f : ex2(s - now);
+                top = now;
+                sum = fmaf(sum, fall, w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = fmaf(w, v[e], o[e] * fall);
             }
         }
     }
-    if (!spoiled) return;
     uint16_t* dst = reinterpret_cast<uint16_t*>(p.out) + (job.q0 + row) * p.out_tok +
-                    static_cast<long long>(job.head) * p.out_head;
-#pragma unroll 1
-    for (int d = 0; d < p.width; ++d) {
-        const float v = nan ? __uint_as_float(kNanBits) : sum == 0.0f ? 0.0f : o[d] / sum;
-        dst[d] = static_cast<uint16_t>(pack2<BF>(v, 0.0f));
+                    static_cast<long long>(job.head) * p.out_head + 4 * lane;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float r = nan ? __uint_as_float(kNanBits) : sum == 0.0f ? 0.0f : o[e] / sum;
+        if (in) dst[e] = static_cast<uint16_t>(pack2<BF>(r, 0.0f));
     }
 }
 
@@ -895,7 +901,8 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                 }
                 __syncwarp();
             }
-            if (valid && odd != 0.0f) redo_row<BF>(p, job, mine, row);
+            for (uint32_t again = __ballot_sync(0xffffffffu, valid && odd != 0.0f); again; again &= again - 1u)
+                redo_row<BF>(p, job, mine, row - lane + __ffs(again) - 1, lane);
             __syncwarp();
             tc_fence_before();
         }
