@@ -4,8 +4,8 @@
 // p_ij = e^(s_ij - m_i), in one pass over the keys i sees with a running maximum.
 //
 // A job is one head of NQ tiles of 128 query rows; it walks the 128-key tiles that any
-// of them sees.  CTAs stay on their SM and take every grid-th job.  Both products run on the tensor cores, with everything between
-// them in tensor memory: S = Q K^T (128 x 128 fp32) is read by the four warps of its
+// of them sees.  CTAs stay on their SM and take every grid-th job.  Both products run on
+// the tensor cores, with everything between them in tensor memory: S = Q K^T (128 x 128 fp32) is read by the four warps of its
 // tile, a row per thread, so that a row's maximum and sum need no exchange; the weights
 // go back as 16-bit words over S, where the second product O += P V takes them as its
 // first operand.  V is read as it lies in memory (its rows are the reduction).
@@ -15,8 +15,20 @@
 //   warps 4-7   the first tile's rows: softmax, then the output; 8-11 the second's
 // The next job's loads and first scores run under the last softmax and the output of the
 // one before.
-// With two tiles the tensor cores work on one while the other's weights are computed,
-// and K and V are read once for 256 rows; with one tile two CTAs share an SM instead.
+//
+// With two tiles a job the tensor cores work on one while the other's weights are
+// computed, and K and V are read once for 256 rows; with one tile two CTAs share an SM.
+// Two are taken where documents are longer than a tile and their jobs reach every SM:
+// 14400 x 16 x 128 967 against 1147 us, 1024-long documents of 64-wide heads 80 against 88,
+// 256-long ones 34 each; between 256 and 768 either is ahead by up to 10%, as the number of
+// tiles is even or odd.
+// What bounds it: at 128-wide heads the tensor cores (14400 x 16 x 128: 1750 TFLOP/s of
+// 1915); at 64 the chain of one tile's steps, as its scores and weights share their place:
+// of 2400 cycles for a key tile of both query tiles 1700 are a softmax from scores to
+// weights, the rest its two products and the hand-overs.  So the weights are handed over in
+// two halves, and a turn's scores are issued right behind its product, their keys having
+// been waited for before it (822 to 799 us at 64; leaving out the exponentials and the
+// maximum gains 10%).  Without the turns 128-wide heads take 1304 us.
 // The maximum that weights are relative to follows the running one only when that has
 // grown by more than 2^8 (weights up to 256 keep their 11 or 8 bits, sums are fp32), so
 // that O is rarely rescaled: only then does a softmax warp wait for the product before.
@@ -331,7 +343,8 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
     const uint32_t q_full0 = empty0 + 8u * kMaxStages, q_empty0 = q_full0 + 16u;
     const uint32_t job_full0 = q_empty0 + 16u, job_empty0 = job_full0 + 8u * kJobs;
     const uint32_t s_full0 = job_empty0 + 8u * kJobs, p_full0 = s_full0 + 16u, o_done0 = p_full0 + 16u;
-    const uint32_t turn_bar0 = o_done0 + 16u, tail_bar = turn_bar0 + 16u, drain_bar = tail_bar + 8u;
+    const uint32_t turn_bar0 = o_done0 + 16u, half_full0 = turn_bar0 + 16u, tail_bar = half_full0 + 16u;
+    const uint32_t drain_bar = tail_bar + 8u;
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem_raw + (drain_bar + 8u - raw));
     // misc[0] TMEM base, [1] abort flag, [2] ring loads issued, [3] Q loads issued, [4] whether a
     // last tile's values are on their way (1 + its phase), [5] to which slot; then the jobs
@@ -350,6 +363,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
             mbar_init(q_full0 + 8 * i, 1);
             mbar_init(q_empty0 + 8 * i, NQ);
             mbar_init(s_full0 + 8 * i, 1);
+            mbar_init(half_full0 + 8 * i, 4);
             mbar_init(p_full0 + 8 * i, 4);
             mbar_init(o_done0 + 8 * i, 1);
             mbar_init(turn_bar0 + 8 * i, 1);
@@ -581,7 +595,8 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
             const uint32_t q_low = ((q_smem >> 4) | (1u << 16)) + i * step, k_low = (ring >> 4) | (1u << 16);
             const uint32_t v_low = (ring >> 4) | ((kBoxBytes >> 4) << 16);
             const uint32_t t_s = tmem + i * kRows, t_o = tmem + NQ * kRows + i * o_pitch;
-            const uint32_t s_full = s_full0 + 8 * i, p_full = p_full0 + 8 * i, o_done = o_done0 + 8 * i;
+            const uint32_t s_full = s_full0 + 8 * i, o_done = o_done0 + 8 * i;
+            const uint32_t half_full = half_full0 + 8 * i, p_full = p_full0 + 8 * i;
             uint32_t slot = 0, ph = 0, q_buf = 0, q_ph = 0, pph = 0, my_turn = 0;
             bool ok = true;
             // The two warps take turns, so that the tensor cores finish one tile's products, then
@@ -619,11 +634,10 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                 if (!ok) break;
                 const uint32_t q_at = q_low + q_buf * NQ * step;
                 uint32_t add = 0u;
+                ok = wait_role(full0 + 8 * slot, ph, abort_flag, p.status, limit);
 #pragma unroll 1
-                for (int n = 0; n < count; ++n) {
+                for (int n = 0; ok && n < count; ++n) {
                     const bool active = seen(n);
-                    ok = wait_role(full0 + 8 * slot, ph, abort_flag, p.status, limit);
-                    if (!ok) break;
                     if (active) {
                         // (the scores before were read, and their weights multiplied, by then)
                         tc_fence_after();
@@ -640,24 +654,32 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                     if (n + 1 == count) commit_if(el, q_empty0 + 8 * q_buf);
                     pass_turn();
                     next();
+                    const uint32_t at = slot;
                     ok = wait_role(full0 + 8 * slot, ph, abort_flag, p.status, limit);
                     if (!ok) break;
-                    ok = take_turn();
+                    // the next keys too, so that their scores follow this product at once
+                    next();
+                    if (n + 1 < count) ok = wait_role(full0 + 8 * slot, ph, abort_flag, p.status, limit);
+                    ok = ok && take_turn();
                     if (!ok) break;
                     if (active) {
-                        ok = wait_role(p_full, pph, abort_flag, p.status, limit);
+                        const uint32_t b = v_low + at * step;
+#pragma unroll 1
+                        for (uint32_t half = 0; half < 2; ++half) {
+                            ok = wait_role(half ? p_full : half_full, pph, abort_flag, p.status, limit);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (uint32_t kk = 0; kk < kRows / 32; ++kk)
+                                mma_ta_if(el, t_o, t_s + 32 * half + 8 * kk, b + (4 * half + kk) * 128, kHigh, idesc_o,
+                                          kk || half ? 1u : add);
+                        }
                         if (!ok) break;
                         pph ^= 1u;
-                        tc_fence_after();
-                        const uint32_t b = v_low + slot * step;
-#pragma unroll
-                        for (uint32_t kk = 0; kk < kRows / 16; ++kk)
-                            mma_ta_if(el, t_o, t_s + 8 * kk, b + kk * 128, kHigh, idesc_o, kk ? 1u : add);
                         commit_if(el, o_done);
                         add = 1u;
                     }
-                    commit_if(el, empty0 + 8 * slot);
-                    next();
+                    commit_if(el, empty0 + 8 * at);
                 }
                 if (!ok) break;
                 pass_turn();
@@ -830,7 +852,13 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                             sums[e / 2 & 1] = add2(sums[e / 2 & 1], two(__float_as_uint(px), __float_as_uint(py)));
                             s[h >> 1][(h & 1) * 16 + e / 2] = pack2<BF>(px, py);
                         }
-                        if (h == 1) tmem_st_32x32b_x32(t_s, s[0]);
+                        if (h == 1) {   // the first half's product can begin
+                            tmem_st_32x32b_x32(t_s, s[0]);
+                            tmem_st_wait();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(half_full0 + 8 * i);
+                        }
                     }
                 };
                 if (MOD == 0) weights([&](uint64_t v) { return fma2(v, cc, off); });
