@@ -23,12 +23,12 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["conv_igemm.cu", "aux_kernels.cu", "conv3d_api.cu", "conv_noalloc.cu", "conv_fused_q.cu",
            "token_norm.cu", "token_act.cu", "linear_w8a8.cu", "token_api.cu",
-           "rotary.cu", "kv_cache.cu", "paged_attention.cu", "packed_attention.cu",
-           "attention_api.cu"]
+           "token_rotary.cu", "token_kv_cache.cu", "token_paged_attention.cu",
+           "token_packed_attention.cu", "token_attention_api.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "tile_table.h", "kernel_common.cuh"]
 # the token operators' own
 TOKEN_HEADERS = ["token_common.cuh", "token_activations.cuh", "token_rows.cuh", "token_ops_internal.h",
-                 "attention_internal.h", "paging.cuh"]
+                 "token_attention_internal.h", "token_paging.cuh"]
 PUBLIC_HEADERS = ["conv3d.h", "token_ops.h", "token_attention.h"]
 
 

@@ -1246,52 +1246,6 @@ int encode_rows(CUtensorMap* m, const void* ptr, int elt, long long cols, long l
     return CONV_OK;
 }
 
-int encode_heads(CUtensorMap* m, const void* ptr, long long width, long long heads, long long rows,
-                 long long head_pitch, long long row_pitch, int box_rows) {
-    if (!load_entry_points()) {
-        set_error("the driver's tensor-map encoders are not available");
-        return CONV_ERR_CUDA;
-    }
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(heads),
-                                static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_pitch), static_cast<cuuint64_t>(row_pitch)};
-    const cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)};
-    const cuuint32_t es[3] = {1u, 1u, 1u};
-    CUresult r = g_encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(ptr), dims, strides, box,
-                                es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) {
-        set_error("cuTensorMapEncodeTiled failed (code %s%lld)", "", static_cast<long long>(r));
-        return CONV_ERR_CUDA;
-    }
-    return CONV_OK;
-}
-
-int encode_pages(CUtensorMap* m, const void* ptr, int elt, long long width, long long rows, long long heads,
-                 long long pages, long long row_pitch, long long head_pitch, long long page_pitch, int box_rows) {
-    if (!load_entry_points()) {
-        set_error("the driver's tensor-map encoders are not available");
-        return CONV_ERR_CUDA;
-    }
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows),
-                                static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(pages)};
-    // (one head or page has no pitch of its own)
-    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(row_pitch),
-                                   static_cast<cuuint64_t>(heads > 1 ? head_pitch : row_pitch),
-                                   static_cast<cuuint64_t>(pages > 1 ? page_pitch : row_pitch)};
-    const cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / elt), static_cast<cuuint32_t>(box_rows), 1, 1};
-    const cuuint32_t es[4] = {1u, 1u, 1u, 1u};
-    CUresult r = g_encode_tiled(m, elt == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
-                                const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) {
-        set_error("cuTensorMapEncodeTiled failed (code %s%lld)", "", static_cast<long long>(r));
-        return CONV_ERR_CUDA;
-    }
-    return CONV_OK;
-}
-
 Overrides overrides() {
     std::lock_guard<std::mutex> lk(g_ovr_mutex);
     return g_ovr;

@@ -295,18 +295,6 @@ int launch_limits(LaunchLimits* l);
 int encode_rows(CUtensorMap* m, const void* ptr, int elt, long long cols, long long rows,
                 long long pitch, int box_rows, int box_bytes);
 
-// Tensor map of heads [rows, heads, width] of 16-bit elements (pitches in bytes, multiples
-// of 16, as the base): boxes of box_rows rows x 64 elements of one head, 128-byte
-// swizzle, zeros outside.
-int encode_heads(CUtensorMap* m, const void* ptr, long long width, long long heads, long long rows,
-                 long long head_pitch, long long row_pitch, int box_rows);
-
-// Tensor map of a paged cache [pages, heads, rows, width] (pitches in bytes, multiples of
-// 16, as the base): boxes of box_rows rows x 128 bytes of one head of one page, 128-byte
-// swizzle, zeros behind the width.
-int encode_pages(CUtensorMap* m, const void* ptr, int elt, long long width, long long rows, long long heads,
-                 long long pages, long long row_pitch, long long head_pitch, long long page_pitch, int box_rows);
-
 int* device_status_ptr();   // device address of the status word (current device)
 
 // The process's plan / path overrides (conv_set_overrides), copied under a

@@ -1,4 +1,4 @@
-// attention_api.cu -- the C ABI of rotary positions, the key-value cache and
+// token_attention_api.cu -- the C ABI of rotary positions, the key-value cache and
 // attention (declared in include/token_attention.h): argument checks and launches.
 // No allocation.
 #include <cuda_runtime.h>
@@ -10,7 +10,7 @@
 #include <initializer_list>
 #include <utility>
 
-#include "attention_internal.h"
+#include "token_attention_internal.h"
 #include "token_common.cuh"
 
 namespace c3d {
@@ -110,6 +110,61 @@ const char* bad_table(const int32_t* table, int64_t stride, int64_t pages, int64
     if (pages && sequences && (!table || !aligned_to(table, 4))) return "null or unaligned page table";
     if (sequences > 1 && stride < pages) return "a page table's stride is below its width";
     return nullptr;
+}
+
+// cuTensorMapEncodeTiled, found in the driver as the convolutions find it
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Tensor map of RANK dimensions, innermost first (strides in bytes, multiples of 16, of all
+// but that one): boxes of `box` elements, 128-byte swizzle,
+// zeros outside.
+template <int RANK>
+int encode(CUtensorMap* m, const void* ptr, int elt, const cuuint64_t (&dims)[RANK],
+           const cuuint64_t (&strides)[RANK - 1], const cuuint32_t (&box)[RANK]) {
+    static const EncodeTiled fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        return cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                           cudaSuccess &&
+                       q == cudaDriverEntryPointSuccess
+                   ? reinterpret_cast<EncodeTiled>(f)
+                   : nullptr;
+    }();
+    if (!fn) {
+        set_last_error("the driver's tensor-map encoder is not available");
+        return CONV_ERR_CUDA;
+    }
+    cuuint32_t steps[RANK];
+    for (cuuint32_t& s : steps) s = 1;
+    const CUresult r = fn(m, elt == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, RANK,
+                          const_cast<void*>(ptr), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return CONV_OK;
+    char msg[96];
+    std::snprintf(msg, sizeof msg, "cuTensorMapEncodeTiled failed (code %d)", static_cast<int>(r));
+    set_last_error(msg);
+    return CONV_ERR_CUDA;
+}
+
+cuuint64_t u64(int64_t v) { return static_cast<cuuint64_t>(v); }
+
+// Heads [rows, heads, width] of 16-bit elements: box_rows rows x 64 elements of one head
+int encode_heads(CUtensorMap* m, const void* ptr, int64_t width, int64_t heads, int64_t rows,
+                 int64_t head_pitch, int64_t row_pitch, int box_rows) {
+    return encode<3>(m, ptr, 2, {u64(width), u64(heads), u64(rows)}, {u64(head_pitch), u64(row_pitch)},
+                     {64u, 1u, static_cast<cuuint32_t>(box_rows)});
+}
+
+// A cache [pages, heads, rows, width]: box_rows rows x 128 bytes of one head of one page
+// (one head or page has no pitch of its own)
+int encode_pages(CUtensorMap* m, const void* ptr, int elt, int64_t width, int64_t rows, int64_t heads,
+                 int64_t pages, int64_t row_pitch, int64_t head_pitch, int64_t page_pitch, int box_rows) {
+    return encode<4>(m, ptr, elt, {u64(width), u64(rows), u64(heads), u64(pages)},
+                     {u64(row_pitch), u64(heads > 1 ? head_pitch : row_pitch), u64(pages > 1 ? page_pitch : row_pitch)},
+                     {static_cast<cuuint32_t>(128 / elt), static_cast<cuuint32_t>(box_rows), 1u, 1u});
 }
 
 PageMap page_map(const kv_cache* c, const int32_t* table, int64_t stride, int64_t pages) {

@@ -1,4 +1,4 @@
-// attention_internal.h -- parameter blocks and launch entry points shared by
+// token_attention_internal.h -- parameter blocks and launch entry points shared by
 // attention_api.cu and the kernels of rotary positions, the key-value cache and
 // attention.  Not part of the public ABI.
 #pragma once

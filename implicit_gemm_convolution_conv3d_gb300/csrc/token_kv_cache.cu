@@ -1,4 +1,4 @@
-// kv_cache.cu -- rows of keys and values into a paged cache and back.
+// token_kv_cache.cu -- rows of keys and values into a paged cache and back.
 //
 // Writing takes each row's largest magnitude, scale = max / qmax, and stores the
 // nearest codes (the rules of token_common.cuh: the same codes and scales as
@@ -7,8 +7,13 @@
 // 16 or 32 lanes with 8 elements each, so a row's maximum takes three to five shuffles
 // and nothing leaves the warp; keys and values are rows of one launch, and a group
 // takes several of a token's rows at once.
-#include "attention_internal.h"
-#include "paging.cuh"
+// Measured: bf16 caches 6.5 TB/s both ways (108000 x 16 x 64; a copy runs at 6.8);
+// 8 bits, 216000 x 8 x 128: reading 225 us (5.9 TB/s), writing 309 (4.3 TB/s: the maximum,
+// two divisions a row and the codes' rounding are about 30 instructions for eight
+// elements, and the issue slots what it waits for).  One new token of each of 64
+// sequences: 8 us, the host's time for a call.
+#include "token_attention_internal.h"
+#include "token_paging.cuh"
 #include "token_common.cuh"
 
 #include <type_traits>
@@ -332,26 +337,37 @@ cudaError_t run(Kernel kern, CacheParams p, int parts, int lanes, cudaStream_t s
     return launch_ex(kern, static_cast<unsigned>((units + per - 1) / per), dim3(kThreads), 0, 1, stream, p);
 }
 
-// Several rows (or runs of elements) a lane where that leaves the SMs two blocks each:
-// their loads are in flight together behind one look at the table.  Fewer of fp32, for
-// the registers.
+// Several rows a lane where that leaves the SMs two blocks each: their loads are in flight
+// together behind one look at the table.  Eight, or four where that wastes fewer lanes'
+// rows (2, 4, 10 or 12 rows a token) and of fp32, for the registers.  216000 tokens x 8
+// heads x 128, e4m3: 309 us with eight, 332 with four, 611 with one; 108000 x 1 x 128: 60, 43
+// and 50; 64 x 8 x 128 (too few): 10.2 with eight, 8.2 with one.
 template <typename T, int CACHE, int G>
 cudaError_t write_by_rows(const CacheParams& p, cudaStream_t stream) {
-    constexpr int kMany = sizeof(T) == 4 ? 4 : 8;
-    const bool many = p.tokens * 2 * p.heads / kMany * G >= 2 * 152 * kThreads;
-    return many ? run(cache_write_kernel<T, CACHE, G, kMany>, p, (2 * p.heads + kMany - 1) / kMany, G, stream)
-                : run(cache_write_kernel<T, CACHE, G, 1>, p, 2 * p.heads, G, stream);
+    const int rows = 2 * p.heads;
+    const bool eight = sizeof(T) < 4 && (rows + 7) / 8 * 8 == (rows + 3) / 4 * 4;
+    const bool many = p.tokens * rows / (eight ? 8 : 4) * G >= 2 * 152 * kThreads;
+    if (!many) return run(cache_write_kernel<T, CACHE, G, 1>, p, rows, G, stream);
+    if constexpr (sizeof(T) < 4)
+        if (eight) return run(cache_write_kernel<T, CACHE, G, 8>, p, (rows + 7) / 8, G, stream);
+    return run(cache_write_kernel<T, CACHE, G, 4>, p, (rows + 3) / 4, G, stream);
 }
 
-template <typename T, int CACHE, int G>
-cudaError_t read_by_rows(const CacheParams& p, cudaStream_t stream) {
-    constexpr int kMany = CACHE == kTokInt8 || CACHE == kTokE4m3 ? 8 : 4;
+// Reads: up to eight runs of elements a lane (four of 16-bit ones, for the registers), as
+// above: 216000 x 8 x 128, e4m3: 225 us, 254 with four, 453 with one.  Eight lanes share a
+// token's runs: 32 took 182 us for 108000 x 16 x 80 int8 where eight take 158, and twice as
+// long for one or two heads.
+template <typename T, int CACHE>
+cudaError_t read_by_runs(const CacheParams& p, cudaStream_t stream) {
+    constexpr int G = 8, kMany = CACHE == kTokInt8 || CACHE == kTokE4m3 ? 8 : 4;
     const int runs = 2 * p.heads * (p.width / 8);
     const bool many = p.tokens * runs / kMany >= 2 * 152 * kThreads;
     return many ? run(cache_read_kernel<T, CACHE, G, kMany>, p, (runs + kMany * G - 1) / (kMany * G), G, stream)
                 : run(cache_read_kernel<T, CACHE, G, 1>, p, (runs + G - 1) / G, G, stream);
 }
 
+// Lanes of a written row: the fewest that hold it, eight elements each.  (80-wide rows in 16
+// lanes: 310 us where ten lanes take 215, 108000 x 16 x 80 int8.)
 template <typename T, int CACHE, bool WRITE>
 cudaError_t by_width(const CacheParams& p, cudaStream_t stream) {
     if constexpr (WRITE)
@@ -360,8 +376,7 @@ cudaError_t by_width(const CacheParams& p, cudaStream_t stream) {
                : p.width <= 128 ? write_by_rows<T, CACHE, 16>(p, stream)
                                 : write_by_rows<T, CACHE, 32>(p, stream);
     else
-        return 2 * p.heads * (p.width / 8) >= 32 * 8 ? read_by_rows<T, CACHE, 32>(p, stream)
-                                                     : read_by_rows<T, CACHE, 8>(p, stream);
+        return read_by_runs<T, CACHE>(p, stream);
 }
 
 template <typename T, bool WRITE>

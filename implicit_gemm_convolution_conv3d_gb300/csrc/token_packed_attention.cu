@@ -1,4 +1,4 @@
-// packed_attention.cu -- attention within documents packed one after the other.
+// token_packed_attention.cu -- attention within documents packed one after the other.
 //
 // For each document, head and query i:  out = sum_j p_ij v_j / sum_j p_ij,
 // p_ij = e^(s_ij - m_i), in one pass over the keys i sees with a running maximum.
@@ -34,7 +34,7 @@
 // that O is rarely rescaled: only then does a softmax warp wait for the product before.
 // Weights are rounded to the inputs' 16-bit type for the second product, whose
 // operands have one type; the sum of weights takes them unrounded.
-#include "attention_internal.h"
+#include "token_attention_internal.h"
 #include "token_common.cuh"
 
 namespace c3d {
@@ -316,6 +316,14 @@ __device__ __forceinline__ void commit_if(uint32_t lane, uint32_t bar) {
         "setp.ne.b32 q, %0, 0;\n\t"
         "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(lane),
         "r"(bar)
+        : "memory");
+}
+
+// 32 lanes x 8 consecutive 32-bit columns, the reverse of tmem_ld_32x32b_x8
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
         : "memory");
 }
 

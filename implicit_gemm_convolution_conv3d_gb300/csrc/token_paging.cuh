@@ -1,7 +1,7 @@
-// paging.cuh -- device helpers of the paged key-value cache: which sequence a
+// token_paging.cuh -- device helpers of the paged key-value cache: which sequence a
 // packed row belongs to, and where a token's row lies.
 #pragma once
-#include "attention_internal.h"
+#include "token_attention_internal.h"
 
 namespace c3d {
 

@@ -66,12 +66,12 @@ def _bind():
 
 def _here(x: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
     """One device for all of a call's tensors: the current one, which launches."""
-    d = x.device
-    if d.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {d}, which is not the current device")
+    d = x.get_device()
+    if d != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {x.device}, which is not the current device")
     for t in others:
-        if t is not None and t.device != d:
-            raise ValueError(f"all tensors of a call must be on {d}")
+        if t is not None and t.get_device() != d:
+            raise ValueError(f"all tensors of a call must be on {x.device}")
 
 
 def _heads(t: torch.Tensor, types: dict, what: str) -> Tuple[int, int, int, int, int, int]:

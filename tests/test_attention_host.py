@@ -196,6 +196,9 @@ def test_one_device(monkeypatch):
         def __init__(self, i):
             self.device = torch.device("cuda", i)
 
+        def get_device(self):
+            return self.device.index
+
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     t._here(At(1), At(1), None)
     with pytest.raises(ValueError, match="current"):
