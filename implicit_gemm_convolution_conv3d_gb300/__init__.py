@@ -12,7 +12,9 @@ Names follow the C ABI (``conv_fwd``, ``pack_ncdhw_bf16_to_ndhwc``,
 degenerate 3-D forms D=T=1 (and H=R=1 for 1-D), as the FlyDSL PR #860
 conv2d/conv1d wrapper commit does.  ``rms_norm_quant``, ``act_quant`` and
 ``linear_w8a8`` (module ``token_ops``) are the 8-bit operators on the tokens
-that a patch embedding makes.
+that a patch embedding makes; ``rotary``, ``kv_cache_write``, ``kv_cache_read``,
+``paged_attention`` and ``packed_attention`` (module ``token_attention``) are
+attention on them.
 """
 from __future__ import annotations
 

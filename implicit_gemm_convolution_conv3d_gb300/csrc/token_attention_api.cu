@@ -199,6 +199,7 @@ int cache_rows(const kv_cache* cache, void* k, void* v, int dtype, int64_t token
         return invalid("without offsets there is one token for each sequence");
     if (tokens == 0 || sequences == 0) return CONV_OK;
     if (write ? !starts : !offsets) return invalid("null pointer");
+    if (write ? cache->k == cache->v : k == v) return invalid("keys and values must be written to places of their own");
     if (!aligned_to(offsets, 4) || !aligned_to(starts, 4))
         return invalid("a pointer is not aligned to its element type");
     for (const void* p : {static_cast<const void*>(k), static_cast<const void*>(v)})
@@ -424,6 +425,7 @@ int packed_attention_fwd(const void* q, int64_t q_token_stride, int64_t q_head_s
     if (const char* e = bad_heads(q, q_token_stride, q_head_stride, q_tokens, heads, width, 2)) return invalid(e);
     if (const char* e = bad_out(out, out_token_stride, out_head_stride, q_tokens, heads, width, 2))
         return invalid(e);
+    if (out == q) return invalid("out may not be q");
     if (k_tokens)
         for (const void* t : {k, v})
             if (const char* e = bad_heads(t, k_token_stride, k_head_stride, k_tokens, kv_heads, width, 2))

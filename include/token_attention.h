@@ -24,7 +24,8 @@
  *     What it does not see takes no part, whatever it holds.  A query that sees
  *     nothing (or whose scores are all -inf) gets zeros.
  *   - Query head h reads key head h / (heads / kv_heads).
- *   - Rows of an output or of a cache that overlap are refused.
+ *   - Rows of an output or of a cache that overlap are refused; outputs overlap no input
+ *     (but rotary_fwd's, which may be x itself).
  */
 #ifndef TOKEN_ATTENTION_GB300_H
 #define TOKEN_ATTENTION_GB300_H

@@ -53,7 +53,7 @@ def test_rotary_refuses(lib, kw):
 
 def _cache(**kw):
     from implicit_gemm_convolution_conv3d_gb300.token_attention import _Cache
-    a = dict(k=P, v=P, k_scale=P, v_scale=P, dtype=INT8, pages=4, heads=2, page_size=16, width=64,
+    a = dict(k=P, v=2 * P, k_scale=P, v_scale=2 * P, dtype=INT8, pages=4, heads=2, page_size=16, width=64,
              page_stride=2048, head_stride=1024, row_stride=64, scale_page_stride=32, scale_head_stride=16)
     a.update(kw)
     return _Cache(**a)
@@ -66,7 +66,7 @@ BAD_CACHES = [dict(k=None), dict(k_scale=None), dict(k=P + 8), dict(dtype=F32), 
 
 
 def _rows(lib, write, cache, **kw):
-    a = dict(k=P, v=P, dtype=BF16, ts=128, hs=64, tokens=5, offsets=P, starts=P, table=P, tstride=8, tpages=8,
+    a = dict(k=P, v=2 * P, dtype=BF16, ts=128, hs=64, tokens=5, offsets=P, starts=P, table=P, tstride=8, tpages=8,
              sequences=3)
     a.update(kw)
     f = lib.kv_cache_write if write else lib.kv_cache_read
@@ -122,7 +122,7 @@ def test_paged_refuses_caches(lib):
 def _packed(lib, **kw):
     a = dict(q=P, qt=256, qh=64, k=P, v=P, kt=128, kh=64, dtype=BF16, qo=P, ko=P, documents=2, nq=8, nk=8,
              heads=4, kv_heads=2, width=64, causal=0, window=0, prefix=None, slopes=None, scale=0.125, cap=0.0,
-             out=P, ot=256, oh=64)
+             out=2 * P, ot=256, oh=64)
     a.update(kw)
     return lib.packed_attention_fwd(*a.values(), None)
 
@@ -185,6 +185,9 @@ def test_overlapping_outputs_and_caches(lib):
     for kw in (dict(head_stride=960), dict(head_stride=0), dict(page_stride=0), dict(page_stride=1024),
                dict(scale_head_stride=8), dict(scale_page_stride=16), dict(row_stride=96)):
         assert _rows(lib, True, _cache(**kw)) == INVALID, kw
+    assert _rows(lib, True, _cache(v=P, k=P), k=P, v=2 * P) == INVALID    # one pool for both
+    assert _rows(lib, False, _cache(), k=P, v=P) == INVALID
+    assert _packed(lib, out=2 * P, q=2 * P, ot=256) == INVALID
     inside = _cache(row_stride=128, head_stride=64, scale_page_stride=64, scale_head_stride=32)
     assert _rows(lib, True, inside, tokens=0, sequences=0) == OK
 
