@@ -8,8 +8,8 @@
 // Memory-bound: every element is read and written once.  The sines of a block's
 // tokens are computed once into shared memory and shared by all heads; a thread
 // keeps those of its pairs in registers over the heads it rotates.
-// Measured: 216000 x 32 x 128 bf16 637 us interleaved (5.6 TB/s of 6.8), 665 in halves;
-// 100000 x 16 x 64 fp32 122 us (6.7 TB/s); 200000 x 2 x 128 109 us: with two heads to share
+// Measured: 216000 x 32 x 128 bf16 598 us interleaved (5.9 TB/s of 6.8), 610 in halves;
+// 100000 x 16 x 64 fp32 122 us (6.7 TB/s); 200000 x 2 x 128 82 us: with two heads to share
 // them the sines are what it computes.  One token: 6 us, the host's time for a call.
 #include "token_attention_internal.h"
 #include "token_common.cuh"
@@ -27,10 +27,19 @@ struct alignas(sizeof(T) * VEC) Vec {
     T v[VEC];
 };
 
+// Heads whose loads a thread has in flight, and blocks of an SM that its registers have to
+// allow: for 16-bit elements by four or eight many threads with a few loads each, else
+// few with many.  216000 x 32 x 128 bf16 interleaved: two heads and five blocks 596 us, four heads
+// and two blocks 640, two and six (spills) 715; in halves (two loads a head) one head and
+// five blocks 608, two and four 649, four and two 665; 100000 x 16 x 64 fp32 in halves 127
+// with one and five, 122 with four and two.
+template <typename T, int VEC>
+constexpr bool kManyThreads = sizeof(T) == 2 && VEC >= 4;
+
 // VEC elements a load: VEC (half) or VEC / 2 (interleaved) pairs of a unit; VEC == 1
 // is the form for any alignment (interleaved: two elements apart).
 template <typename T, int VEC, bool HALF>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kManyThreads<T, VEC> ? 5 : 0)
     rotary_kernel(const __grid_constant__ RotaryParams p, int units, int lanes, int tokens_block) {
     __shared__ float2 table[kSinCos];
     griddep_launch_dependents();
@@ -45,7 +54,7 @@ __global__ void __launch_bounds__(kThreads)
     T* out = static_cast<T*>(p.out) + (tok0 + t) * p.out_tok;
     const int rot_units = p.pairs / NP;
     using V = Vec<T, VEC>;
-    constexpr int kUnroll = 4;
+    constexpr int kUnroll = !kManyThreads<T, VEC> ? 4 : HALF ? 1 : 2;
     const int ea = HALF ? u * VEC : u * 2 * NP;
     const int eb = HALF ? ea + p.pairs : ea + 1;
     constexpr bool kTwo = HALF || VEC == 1;   // two loads a unit
@@ -128,7 +137,7 @@ cudaError_t run(const RotaryParams& p, cudaStream_t stream) {
     const int units = p.pairs / NP + (rest < kThreads / 2 ? rest : kThreads / 2);
     // heads side by side: all, as far as a block reaches; fewer, so that a thread's
     // sines serve up to four heads, where there are blocks enough without them (216000 x
-    // 32 x 128: 637 us so, 888 with all side by side; 1000 x 24 x 128: 9.5 and 13.3)
+    // 32 x 128: 640 us so, 888 with all side by side; 1000 x 24 x 128: 9.5 and 13.3)
     int lanes = kThreads / units < 1 ? 1 : kThreads / units;
     if (lanes > p.heads) lanes = p.heads;
     if (p.tokens * p.heads > 152 * 64 && lanes > (p.heads + 3) / 4) lanes = (p.heads + 3) / 4;
