@@ -4,14 +4,15 @@
 // p_ij = e^(s_ij - m_i), in one pass over the keys i sees with a running maximum.
 //
 // A job is one head of NQ tiles of 128 query rows; it walks the 128-key tiles that any
-// of them sees.  CTAs stay on their SM and take every grid-th job.  Both products run on
-// the tensor cores, with everything between them in tensor memory: S = Q K^T (128 x 128 fp32) is read by the four warps of its
-// tile, a row per thread, so that a row's maximum and sum need no exchange; the weights
-// go back as 16-bit words over S, where the second product O += P V takes them as its
-// first operand.  V is read as it lies in memory (its rows are the reduction).
+// of them sees.  CTAs stay on their SM and take one job after the other (kDealtFrom).  Both
+// products run on the tensor cores, with everything between them in tensor memory:
+// S = Q K^T (128 x 128 fp32) is read by the four warps of its tile, a row per thread, so
+// that a row's maximum and sum need no exchange; the weights go back as 16-bit words over
+// S, where the second product O += P V takes them as its first operand.  V is read as it
+// lies in memory (its rows are the reduction).
 //   warp 0      TMA producer: Q, then K and V tiles in a ring
 //   warp 1      tensor memory; issues the first tile's products, warp 2 the second's
-//   warp 3      finds the jobs and plans them, up to four ahead
+//   warp 3      finds the jobs and plans them, up to four ahead (one, where they are dealt)
 //   warps 4-7   the first tile's rows: softmax, then the output; 8-11 the second's
 // The next job's loads and first scores run under the last softmax and the output of the
 // one before.
@@ -45,7 +46,16 @@ constexpr int kRows = 128;             // query rows and keys of a tile
 constexpr uint32_t kBoxBytes = 16384;  // 128 rows of 64 elements
 constexpr int kMaxStages = 8;
 constexpr uint32_t kJobs = 4;          // jobs planned ahead
-constexpr uint32_t kSmallBytes = 768;  // shared memory of the barriers and jobs
+constexpr uint32_t kSmallBytes = 896;  // shared memory of the barriers, jobs and the dealer's answers
+constexpr uint32_t kAsk = 8;           // asked for at once behind the last job
+// Mean tokens of a document above which jobs are dealt to CTAs that ask (cluster launch
+// control: a CTA takes the index of one that has not started), so that none waits for
+// another's longer documents: 2 x 8192 causal 336 us, 372 with every grid-th job a CTA;
+// 24 documents of 100 to 1403 139 and 145; 40 of 30 to 1600 causal 146 and 166.  The grid then
+// has a CTA for every job that there could be, and those behind the last job are taken
+// too, kAsk at a time: a buffer of 65536 rows with 1000 in use takes 22 us either way.  Of
+// short documents the planner finds 32 jobs at a time instead (100 x 100: 22 us, 28 dealt).
+constexpr long long kDealtFrom = 384;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLag = 8.0f;           // powers of two that weights may exceed 1 by
 
@@ -79,6 +89,7 @@ struct Job {
     long long q0, k0;        // packed rows of the document's first query and key
     __device__ int key(int n) const { return (n < lead_tiles ? n : n - lead_tiles + skip) * kRows; }
 };
+static_assert(344 + kJobs * sizeof(Job) <= kSmallBytes - 16 * kAsk - 8, "barriers, words, jobs, the dealer's answers");
 
 // The keys that rows [a, b) of the job see: [lo, hi) of any of them, and [0, lead).
 struct Range {
@@ -327,6 +338,30 @@ __device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t
         : "memory");
 }
 
+// Takes one of the grid's CTAs that has not started yet: the answer (16 bytes) arrives on
+// a barrier.  Nobody asks again who has seen that there was none left.
+__device__ __forceinline__ void ask_for_cta(uint32_t answer, uint32_t bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+        "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ bool taken_cta(uint32_t answer, uint32_t* index) {
+    uint32_t taken, x;
+    asm volatile(
+        "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 a, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t}"
+        : "=r"(taken), "=r"(x)
+        : "r"(answer)
+        : "memory");
+    *index = x;
+    return taken != 0u;
+}
+
 template <int NQ>
 constexpr int kThreads = 128 + 128 * NQ;
 
@@ -339,7 +374,7 @@ template <bool BF, int NQ, int MOD>
 __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
     packed_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map, const __grid_constant__ PackedParams p,
-                  const int stages, const int q_bufs) {
+                  const int stages, const int q_bufs, const int dealt) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -353,6 +388,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
     const uint32_t s_full0 = job_empty0 + 8u * kJobs, p_full0 = s_full0 + 16u, o_done0 = p_full0 + 16u;
     const uint32_t turn_bar0 = o_done0 + 16u, half_full0 = turn_bar0 + 16u, tail_bar = half_full0 + 16u;
     const uint32_t drain_bar = tail_bar + 8u;
+    const uint32_t deal_answer = bars + kSmallBytes - 16u * kAsk, deal_bar = deal_answer - 8u;
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem_raw + (drain_bar + 8u - raw));
     // misc[0] TMEM base, [1] abort flag, [2] ring loads issued, [3] Q loads issued, [4] whether a
     // last tile's values are on their way (1 + its phase), [5] to which slot; then the jobs
@@ -382,6 +418,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
         }
         mbar_init(tail_bar, 1);
         mbar_init(drain_bar, NQ);
+        mbar_init(deal_bar, 1);
         misc[1] = 0u;
         misc[2] = 0u;
         misc[3] = 0u;
@@ -406,17 +443,54 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
     if (warp < 4) {
         set_max_regs_dec<NQ == 2 ? 72 : 56>();
         if (warp == 3) {
-            // Documents are looked through 128 at a time, four a lane, and never twice; a lane
-            // plans one of the CTA's next jobs, 32 in all.
+            // Documents are looked through 128 at a time, four a lane; a lane plans one of the
+            // CTA's next jobs, 32 in all.  Where jobs are dealt, it is one at a time, the next
+            // taken when all roles have begun the last; the grid has a CTA for every job that
+            // there could be, and behind the last job they are taken kAsk at a time.
+            uint32_t ticket = blockIdx.x, have = 1u, deal_ph = 0;   // have: lanes with a ticket
+            bool more = true;        // there may be CTAs left to take
+            long long total = -1;    // jobs of one head, once known
+            auto deal = [&]() {
+                const uint32_t ask = total < 0 ? 1u : kAsk;
+                if (lane == 0) mbar_arrive_expect_tx(deal_bar, 16u * ask);
+                __syncwarp();
+                if (lane < ask) ask_for_cta(deal_answer + 16u * lane, deal_bar);
+                __syncwarp();
+                if (!wait_role(deal_bar, deal_ph, abort_flag, p.status, limit)) {
+                    drain_here(deal_bar, deal_ph);   // they land before the shared memory is given up
+                    return false;
+                }
+                deal_ph ^= 1u;
+                const bool taken = lane < ask && taken_cta(deal_answer + 16u * lane, &ticket);
+                more = __all_sync(0xffffffffu, taken || lane >= ask);
+                have = __ballot_sync(0xffffffffu,
+                                     taken && (total < 0 || ticket / static_cast<uint32_t>(p.heads) < total));
+                fence_proxy_async_smem();
+                return true;
+            };
             int s0 = -128, n[4] = {0, 0, 0, 0}, off[5] = {0, 0, 0, 0, 0}, mine = 0, run = 0;
             long long before = 0;
             int all = 0;   // jobs (of one head) of these 128
             bool ok = true;
             for (uint32_t k = 0; ok;) {
-                const uint32_t at = blockIdx.x + (k + lane) * gridDim.x;
-                const uint32_t want = at / static_cast<uint32_t>(p.heads);
+                if (dealt && !have && more) {
+                    const uint32_t last = k - 1;
+                    ok = (k == 0 || wait_role(job_empty0 + 8 * (last % kJobs), (last / kJobs) & 1u, abort_flag, p.status,
+                                              limit)) &&
+                         deal();
+                    continue;
+                }
+                const bool some = !dealt || have;
+                const uint32_t at = dealt ? __shfl_sync(0xffffffffu, ticket, have ? __ffs(have) - 1 : 0)
+                                          : blockIdx.x + (k + lane) * gridDim.x;
+                have &= have - 1u;
+                const uint32_t want = dealt && (lane || !some) ? 0xffffffffu : at / static_cast<uint32_t>(p.heads);
                 const uint32_t first = __shfl_sync(0xffffffffu, want, 0);
-                while (before + all <= first && s0 < p.documents) {
+                if (first < before) {   // (dealt out of order)
+                    s0 = -128;
+                    before = all = 0;
+                }
+                while (some && before + all <= first && s0 < p.documents) {
                     before += all;
                     s0 += 128;
 #pragma unroll
@@ -441,6 +515,10 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                 // the jobs among these documents: the first lanes'
                 const bool here = want - before < all;
                 const int count = __popc(__ballot_sync(0xffffffffu, here));
+                if (dealt && some && count == 0) {
+                    total = before + all;
+                    continue;
+                }
                 const int in = here ? static_cast<int>(want - before) : 0;
                 int src = 0;   // the lane whose four documents hold it
 #pragma unroll
@@ -981,8 +1059,9 @@ cudaError_t run(const PackedMaps& maps, const PackedParams& p, int num_sms, cuda
     if (e != cudaSuccess) return e;
     const long long most = (p.q_tokens / (NQ * kRows) + p.documents) * p.heads;
     const long long resident = static_cast<long long>(num_sms) * (NQ == 1 ? 2 : 1);
-    return launch_ex(packed_kernel<BF, NQ, MOD>, static_cast<unsigned>(most < resident ? most : resident),
-                     dim3(kThreads<NQ>), smem, 1, stream, maps.q, maps.k, maps.v, p, stages, q_bufs);
+    const int dealt = most > resident && p.q_tokens / p.documents > kDealtFrom;
+    return launch_ex(packed_kernel<BF, NQ, MOD>, static_cast<unsigned>(most < resident || dealt ? most : resident),
+                     dim3(kThreads<NQ>), smem, 1, stream, maps.q, maps.k, maps.v, p, stages, q_bufs, dealt);
 }
 
 template <bool BF, int NQ>
