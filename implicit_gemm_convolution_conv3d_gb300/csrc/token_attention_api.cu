@@ -318,7 +318,9 @@ size_t paged_attention_workspace_size(int64_t sequences, int64_t heads, int64_t 
     LaunchLimits lim;
     if (launch_limits(&lim)) return 0;
     const int64_t capacity = table_pages > kMaxTokens / page_size ? kMaxTokens : table_pages * page_size;
-    const int grid = paged_grid(sequences, kv_heads, heads / kv_heads, static_cast<int>(width), capacity, lim.num_sms);
+    const int64_t group = heads / kv_heads;
+    if (paged_whole(sequences, kv_heads, group, static_cast<int>(width), capacity, lim.num_sms)) return 0;
+    const int grid = paged_grid(sequences, kv_heads, group, static_cast<int>(width), capacity, lim.num_sms);
     return paged_workspace(grid, static_cast<int>(width));
 }
 
@@ -373,12 +375,16 @@ int paged_attention_fwd(const void* q, int q_dtype, int64_t q_sequence_stride,
     p.width = static_cast<int>(cache->width);
     p.grid = paged_grid(sequences, cache->heads, p.group, p.width, p.map.capacity, lim.num_sms);
     p.num_sms = lim.num_sms;
+    p.whole = paged_whole(sequences, cache->heads, p.group, p.width, p.map.capacity, lim.num_sms);
+    // (a workspace that is given has to do for heads that are split, too)
     const size_t need = paged_workspace(p.grid, p.width);
-    if (!workspace || workspace_bytes < need || !aligned_to(workspace, 16))
+    if (workspace ? workspace_bytes < need || !aligned_to(workspace, 16) : !p.whole)
         return invalid("paged_attention_fwd needs a 16-byte aligned workspace of "
                        "paged_attention_workspace_size bytes");
-    p.jobs = static_cast<int4*>(workspace);
-    p.partial = reinterpret_cast<float*>(p.jobs + p.grid);
+    if (!p.whole) {
+        p.jobs = static_cast<int4*>(workspace);
+        p.partial = reinterpret_cast<float*>(p.jobs + p.grid);
+    }
     p.status = lim.status;
     p.wait_ns = lim.wait_ns;
     // blocks of tokens that lie in one page (or in two halves) are loaded by TMA, with their

@@ -78,7 +78,8 @@ struct PagedParams {
     int sequences, kv_heads, group, width;
     int blocks;            // groups of query heads that share a pass over a key head
     int grid, num_sms;     // grid: CTAs at most
-    float* partial;        // workspace: see paged_attention.cu
+    bool whole;            // key heads are not split
+    float* partial;        // workspace: see token_paged_attention.cu
     int4* jobs;
     int rows_box;          // tokens of a TMA load: 32 (rows up to 128 bytes), 16, 8, or 0 (none: word by word)
     int* status;           // device status word and the bound on every wait
@@ -87,7 +88,10 @@ struct PagedParams {
 struct PagedMaps {
     CUtensorMap k, v;
 };
-// CTAs of the grid, and query heads of a pass (0: this width is not supported)
+// Whether every key head has a CTA of its own, which needs no workspace
+bool paged_whole(long long sequences, long long kv_heads, long long group, int width,
+                 long long capacity, int num_sms);
+// CTAs of the grid otherwise
 int paged_grid(long long sequences, long long kv_heads, long long group, int width,
                long long capacity, int num_sms);
 size_t paged_workspace(int grid, int width);

@@ -184,7 +184,7 @@ __device__ __forceinline__ Seen seen_by(const PagedParams& p, int s) {
     v.lead_blocks = (v.lead + kBlock - 1) / kBlock;
     v.skip = max(v.from / kBlock, v.lead_blocks);
     v.blocks = v.lead_blocks + max((v.length + kBlock - 1) / kBlock - v.skip, 0);
-    v.units = (v.blocks + F::kWarps - 1) / F::kWarps;
+    v.units = p.whole ? v.blocks != 0 : (v.blocks + F::kWarps - 1) / F::kWarps;
     return v;
 }
 
@@ -277,13 +277,14 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
 
     // this CTA's run of units
     const long long per = static_cast<long long>(p.kv_heads) * p.blocks;
-    const long long total = sum_units<F>(p, s_scratch) * per;
     const long long c = blockIdx.x, grid = gridDim.x;
-    // (equal runs; the first total % grid are one longer)
+    // (equal runs; the first total % grid are one longer.  Key heads that are not split have a
+    // unit and a CTA each, those of sequences that see nothing too)
+    const long long total = p.whole ? grid : sum_units<F>(p, s_scratch) * per;
     const long long share = total / grid, longer = total % grid;
     long long unit = c * share + min(c, longer);
     const long long end = unit + share + (c < longer ? 1 : 0);
-    if (threadIdx.x == 0) p.jobs[c] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 0 && !p.whole) p.jobs[c] = make_int4(0, 0, 0, 0);
     // sequences that see nothing get zeros
     for (long long s = c; s < p.sequences; s += grid) {
         if (seen_by<F>(p, static_cast<int>(s)).units) continue;
@@ -293,18 +294,24 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
         }
     }
     if (unit >= end) return;
-    if (warp == 0) {
-        int s;
-        long long b;
-        find_unit<F>(p, per, unit, &s, &b);
-        if (lane == 0) {
-            s_seq = s;
-            s_before = b;
+    int seq = static_cast<int>(c / per);
+    long long before = seq * per;
+    if (p.whole) {
+        if (seen_by<F>(p, seq).units == 0) return;
+    } else {
+        if (warp == 0) {
+            int s;
+            long long b;
+            find_unit<F>(p, per, unit, &s, &b);
+            if (lane == 0) {
+                s_seq = s;
+                s_before = b;
+            }
         }
+        __syncthreads();
+        seq = s_seq;
+        before = s_before;
     }
-    __syncthreads();
-    int seq = s_seq;
-    long long before = s_before;
 
     int stage = 0;        // the ring's next stage, and its phase
     uint32_t phase = 0;
@@ -409,7 +416,7 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
         }
 
         // ---- the warp's blocks
-        const int b0 = u0 * kWarps, b1 = min(u1 * kWarps, see.blocks);
+        const int b0 = u0 * kWarps, b1 = p.whole ? see.blocks : min(u1 * kWarps, see.blocks);
         auto token_of = [&](int b) {
             return (b < see.lead_blocks ? b : b - see.lead_blocks + see.skip) * kBlock;
         };
@@ -790,6 +797,7 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
 // Joins the partial results of the key heads that several CTAs share, in the order of
 // their tokens: block c joins the one that begins in CTA c's run and goes on beyond it.
 // Every part's weight is taken first, so that the sums' loads do not wait for one another.
+constexpr int kWholeTokens = 384;
 constexpr int kMaxParts = 480;   // and CTAs of the first launch
 
 template <bool QBF, int DP>
@@ -883,7 +891,7 @@ cudaError_t run(const PagedMaps& maps, const PagedParams& p0, cudaStream_t strea
     using F = Form<ES, DP>;
     constexpr int kCtas = ctas_of(ES, DP, NG);
     PagedParams p = p0;
-    p.grid = p0.grid < kCtas * p0.num_sms ? p0.grid : kCtas * p0.num_sms;
+    p.grid = p.whole ? p.sequences * p.kv_heads * p.blocks : p0.grid < kCtas * p0.num_sms ? p0.grid : kCtas * p0.num_sms;
     constexpr size_t meet = sizeof(float) * F::kWarps * 8 * NG * (DP + 4 + 2);
     static_assert(meet <= F::kRing, "the warps' results meet over the rings");
     constexpr size_t smem = F::kBytes;
@@ -893,7 +901,7 @@ cudaError_t run(const PagedMaps& maps, const PagedParams& p0, cudaStream_t strea
     e = launch_ex(paged_kernel<KIND, QBF, DP, NG>, static_cast<unsigned>(p.grid), dim3(32 * F::kWarps), smem, 1,
                   stream, maps.k, maps.v, p);
     // (a table of no more than a unit's tokens leaves nothing to join)
-    if (e != cudaSuccess || p.grid == 1 || p.map.capacity <= F::kUnit) return e;
+    if (e != cudaSuccess || p.whole || p.grid == 1 || p.map.capacity <= F::kUnit) return e;
     return launch_ex(paged_join_kernel<QBF, DP>, static_cast<unsigned>(p.grid), dim3(256), 0, 1, stream, p);
 }
 
@@ -910,6 +918,17 @@ cudaError_t by_width(const PagedMaps& m, const PagedParams& p, cudaStream_t stre
 // Query heads of one pass: 8, or 16 where more share a key head (256-wide heads have no
 // registers for 16).
 static int pass_heads(long long group, int width) { return group > 8 && width <= 128 ? 16 : 8; }
+
+// Key heads are not split where tables hold few tokens and each head has a CTA of its own
+// among those that run at once: there is nothing to join then, no workspace to allocate
+// (6 us of a call's 20 on the host), and no unit to look for.  A CTA alone takes longer than
+// several and the join from about 500 tokens on: 8 key heads of 128, e4m3, 333 tokens
+// 16.4 us both, 750 20.5 and 16.4, 2000 30.7 and 18.4.
+bool paged_whole(long long sequences, long long kv_heads, long long group, int width,
+                 long long capacity, int num_sms) {
+    const long long blocks = (group + pass_heads(group, width) - 1) / pass_heads(group, width);
+    return capacity <= kWholeTokens && sequences <= num_sms && kv_heads * blocks * sequences <= 2ll * num_sms;
+}
 
 int paged_grid(long long sequences, long long kv_heads, long long group, int width,
                long long capacity, int num_sms) {

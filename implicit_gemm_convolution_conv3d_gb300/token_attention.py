@@ -351,8 +351,9 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         raise ValueError("page_table must have a row for each sequence")
     out, os_, oh = _given(out, q, _HALF, code, stream)
     if workspace is None:
-        workspace = _new((_paged_need(lib, q.device.index, n, heads, c.heads, width, c.page_size,
-                                      pages),), torch.uint8, q, stream)
+        need = _paged_need(lib, q.get_device(), n, heads, c.heads, width, c.page_size, pages)
+        if need:
+            workspace = _new((need,), torch.uint8, q, stream)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     _here(q, k_cache, v_cache, page_table, lengths, k_scale, v_scale, prefix, slopes, out, workspace)
@@ -360,7 +361,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         q.data_ptr(), code, qs, qh, c, tp, tstride, pages, _ints(lengths, n, "lengths"),
         _ints(prefix, n, "prefix"), _slopes(slopes, heads),
         width ** -0.5 if scale is None else scale, cap, window, n, heads, out.data_ptr(), os_, oh,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream, q))
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream, q))
     if st:
         _check(st, "paged_attention_fwd")
     return out

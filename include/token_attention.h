@@ -114,8 +114,8 @@ int paged_attention_fwd(const void* q, int q_dtype, int64_t q_sequence_stride,
                         int64_t out_sequence_stride, int64_t out_head_stride, void* workspace,
                         size_t workspace_bytes, cudaStream_t stream);
 
-/* Bytes of workspace paged_attention_fwd needs on the current device (0: the
- * arguments are invalid or there is nothing to do). */
+/* Bytes of workspace paged_attention_fwd needs on the current device (0: none, and
+ * NULL will do; or the arguments are invalid). */
 size_t paged_attention_workspace_size(int64_t sequences, int64_t heads, int64_t kv_heads,
                                       int64_t width, int64_t page_size, int64_t table_pages);
 

@@ -124,3 +124,36 @@ def test_one_token_steps_in_a_graph(pkg):
         assert torch.equal(out, want), i
     for a, b in zip(cache.values(), twin.values()):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", [torch.float8_e4m3fn, BF])
+@pytest.mark.parametrize("pages", [23, 24, 25])
+@pytest.mark.parametrize("seqs", [1, 7, 300])
+def test_tables_that_are_split_or_not(pkg, seqs, pages, dtype):
+    """Tables of up to and beyond the tokens that one CTA takes alone, batches of up to and
+    beyond those that run at once, sequences that see nothing or more than there is."""
+    heads, kv, width, page = 8, 2, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(seqs + pages)
+    most = pages * page
+    lengths = [(0, most, 1, most - 1, 17, -3, 130)[i % 7] if i else most for i in range(seqs)]
+    cache = _cache(seqs * pages, kv, page, width, dtype)
+    table = torch.randperm(seqs * pages, generator=g, device="cuda").view(seqs, pages).int()
+    kept = [max(n, 0) for n in lengths]
+    off = _ints([0] + torch.tensor(kept).cumsum(0).tolist())
+    rows = [torch.randn(sum(kept), kv, width, generator=g, device="cuda").bfloat16() for _ in range(2)]
+    pkg.kv_cache_write(*rows, page_table=table, starts=_ints([0] * seqs), offsets=off, **cache)
+    q = torch.randn(seqs, heads, width, generator=g, device="cuda").bfloat16()
+    got = pkg.paged_attention(q, page_table=table, lengths=_ints(lengths), **cache)
+    codes = dtype is not BF
+    coarse = float(cache["v_scale"].nan_to_num().max()) * 448 if codes else None
+    for s in sorted(set(range(min(seqs, 8))) | {seqs - 1}):
+        if lengths[s] <= 0:
+            assert not got[s].any()
+            continue
+        hk, hv = _held(cache, table[s], lengths[s])
+        want, tol = ref.attention64(q[s:s + 1], hk, hv, weights=torch.float16 if codes else BF, coarse=coarse)
+        ref.check(got[s:s + 1], want, tol)
+    if seqs == 7:
+        lengths[3] = most + 1     # past the table
+        got = pkg.paged_attention(q, page_table=table, lengths=_ints(lengths), **cache)
+        assert bool(got[3].isnan().all()) and not got[:3].isnan().any() and not got[4:].isnan().any()
