@@ -15,13 +15,13 @@
 // through its own ring of TMA loads: two a run of 32, 16 or 8 tokens, as many as pages
 // hold a multiple of, which leaves the load units to the shared-memory side.  Blocks at an
 // edge of what is seen, in pages of other sizes, or in pages that are not there come word
-// by word (all blocks so: three times the time for 8-bit caches, twice for 16-bit ones).
+// by word (all blocks so, before lanes looked up their tokens: 1325 us for 414, int8).
 //
 // Measured, 200 sequences of 1 to 8192 tokens, 8 key heads of 128 for 32 query heads: bf16
-// 545 us (6.5 TB/s of 6.8); int8 408 us (4.5 TB/s), e4m3 380 (4.8): there the widening of
-// codes and the weights are what it spends its time on, one instruction for two elements at
-// best, and not memory.  So are 64- and 80-wide heads (3.4 and 3.1 TB/s): a block's
-// scores, exponentials and join cost the same for fewer bytes.  256-wide: 6.2 TB/s.
+// 550 us (6.4 TB/s of 6.8); int8, capped, 336 us (5.4 TB/s), e4m3 317 (5.8): there the
+// widening of codes and the weights are what it spends its time on, one instruction for two
+// elements at best, and not memory.  So are 64- and 80-wide heads (4.1 and 3.3 TB/s): a
+// block's scores, exponentials and join cost the same for fewer bytes.  256-wide: 6.2 TB/s.
 // One sequence of 216000 tokens, e4m3: 110 us (4.2 TB/s).
 //
 // A block is two small matrix products per warp, tokens on the 16-row side:
@@ -459,27 +459,32 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
                 }
                 return;
             }
-            // word by word: a block's edge, pages that end in it, pages that are not there
+            // word by word: a block's edge, pages that end in it, pages that are not there.  Each
+            // lane looks its token up, so that the table is waited for once: every sequence has
+            // such a block at its end (200 ragged sequences, int8: 336 us, 408 token by token)
             slow |= 1u << st;
+            const int mine = t0 + lane % kBlock;
+            long long row = 0, sc = 0;
+            const bool seen = visible(mine), have = !see.bad && seen && token_row(p.map, seq, mine, head, &row, &sc);
+            const uint32_t all = __ballot_sync(0xffffffffu, have);
+            // (rows of one column: two tokens at a time)
+            constexpr int kWords = F::kBoxes * 16, kAtOnce = kWords == 16 ? 2 : 1;   // a key's words, then a value's
 #pragma unroll 1
-            for (int i = 0; i < kBlock; ++i) {
-                long long at = 0, sc;
-                const bool have = !see.bad && visible(t0 + i) && token_row(p.map, seq, t0 + i, head, &at, &sc);
+            for (int i0 = 0; i0 < kBlock; i0 += kAtOnce) {
+                const int i = i0 + (kAtOnce == 2 ? lane >> 4 : 0);
+                const long long at = __shfl_sync(0xffffffffu, row, i);
 #pragma unroll
-                for (int c = lane; c < F::kBoxes * 16; c += 32) {
-                    const int w = c % (F::kBoxes * 8);   // a key's words, then a value's
-                    const bool value = c >= F::kBoxes * 8, load = have && w * 16 < p.width * ES;
+                for (int c = lane % kWords; c < kWords; c += 32) {
+                    const int w = c % (F::kBoxes * 8);
+                    const bool value = c >= F::kBoxes * 8, load = (all >> i & 1u) && w * 16 < p.width * ES;
                     cp_async<16>(dst + (value ? F::kVOff : 0u) + word_at(i, w),
                                  (value ? p.v : p.k) + (load ? at + w * 16 : 0), load ? 16u : 0u);
                 }
             }
             // NaN for the scale of a token whose page is missing, which spoils the row
-#pragma unroll 1
+            const bool want = seen || see.bad;
+#pragma unroll
             for (int e = lane; e < 2 * kBlock; e += 32) {
-                const int t = t0 + e % kBlock;
-                long long at = 0, sc = 0;
-                const bool want = visible(t) || see.bad;
-                const bool have = want && !see.bad && token_row(p.map, seq, t, head, &at, &sc);
                 if (kCodes && (have || !want))
                     cp_async<4>(sdst + e * 4u, (e < kBlock ? p.k_scale : p.v_scale) + sc, have ? 4u : 0u);
                 else
