@@ -757,7 +757,8 @@ def conv1d(x, w, stride=1, padding=0, dilation=1, scale_x=None, scale_w=None, **
 
 from .token_ops import act_quant, linear_w8a8, rms_norm_quant   # noqa: E402
 from .token_attention import (   # noqa: E402
-    kv_cache_read, kv_cache_write, packed_attention, paged_attention, rotary)
+    kv_cache_read, kv_cache_write, packed_attention, paged_attention,
+    paged_attention_workspace_size, rotary)
 
 __all__ = [
     "conv_fwd", "conv_fwd_noalloc", "conv_fwd_plan", "conv_out_dims", "conv_get_device_status",
@@ -769,5 +770,5 @@ __all__ = [
     "conv_bwd_weight_point", "conv_fwd_workspace_size", "conv_get_device_status_stream",
     "set_overrides", "overrides", "conv_fwd_ncdhw_fp8", "conv_fwd_ncdhw_fp8_workspace_size",
     "rms_norm_quant", "act_quant", "linear_w8a8", "rotary", "kv_cache_write", "kv_cache_read",
-    "paged_attention", "packed_attention",
+    "paged_attention", "paged_attention_workspace_size", "packed_attention",
 ]

@@ -323,6 +323,14 @@ def _paged_need(lib, device, *sizes) -> int:
     return need
 
 
+def paged_attention_workspace_size(sequences: int, heads: int, kv_heads: int, width: int,
+                                   page_size: int, table_pages: int) -> int:
+    """Bytes of workspace that ``paged_attention`` of these sizes takes on the current
+    device; 0 where it takes none."""
+    return _paged_need(_fns or _bind(), torch.cuda.current_device(), sequences, heads, kv_heads,
+                       width, page_size, table_pages)
+
+
 def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                     page_table: torch.Tensor, lengths: torch.Tensor,
                     k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
@@ -339,8 +347,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     ``cap`` > 0 cap * tanh(score / cap), and with ``slopes`` [heads] less slope *
     distance.  With ``window`` > 0 only the last ``window`` tokens and the first
     ``prefix[s]`` are seen; pages of unseen tokens are not looked at.  The workspace
-    is taken from torch's allocator unless one is given (calls that may overlap
-    need one each)."""
+    (``paged_attention_workspace_size`` bytes) is taken from torch's allocator unless
+    one is given (calls that may overlap need one each)."""
     lib = _fns or _bind()
     c = _cache(k_cache, v_cache, k_scale, v_scale)
     n, heads, width, qs, qh, code = _heads(q, _HALF, "q")

@@ -144,6 +144,10 @@ def test_tables_that_are_split_or_not(pkg, seqs, pages, dtype):
     pkg.kv_cache_write(*rows, page_table=table, starts=_ints([0] * seqs), offsets=off, **cache)
     q = torch.randn(seqs, heads, width, generator=g, device="cuda").bfloat16()
     got = pkg.paged_attention(q, page_table=table, lengths=_ints(lengths), **cache)
+    need = pkg.paged_attention_workspace_size(seqs, heads, kv, width, page, pages)
+    assert (need == 0) == (pages < 25 and seqs < 300)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    assert torch.equal(got, pkg.paged_attention(q, page_table=table, lengths=_ints(lengths), workspace=ws, **cache))
     codes = dtype is not BF
     coarse = float(cache["v_scale"].nan_to_num().max()) * 448 if codes else None
     for s in sorted(set(range(min(seqs, 8))) | {seqs - 1}):
