@@ -107,3 +107,37 @@ def test_two_calls_at_once(pkg):
     for pair in got:
         for a, b in zip(pair, want):
             assert torch.equal(a, b)
+
+
+def test_calls_that_take_one_anothers_output(pkg):
+    """Launches may begin before the one ahead of them has ended, but see all of it."""
+    lens = [2300, 600, 1500]
+    q, k, v = (_rows(sum(lens), h, 128, 11 + i) for i, h in enumerate((16, 16, 16)))
+    off = _offsets(lens)
+    args = dict(q_offsets=off, causal=True)
+    outs = [torch.empty_like(q) for _ in range(6)]
+
+    def chain(wait):
+        x = q
+        for o in outs:
+            x = pkg.packed_attention(x, k, x, out=o, **args)   # values from the call before
+            if wait:
+                torch.cuda.synchronize()
+        return [o.clone() for o in outs]
+
+    want = chain(True)
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    got = chain(False)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for o in outs:
+        o.zero_()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = chain(False)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
