@@ -17,12 +17,12 @@
 // edge of what is seen, in pages of other sizes, or in pages that are not there come word
 // by word (all blocks so, before lanes looked up their tokens: 1325 us for 414, int8).
 //
-// Measured, 200 sequences of 1 to 8192 tokens, 8 key heads of 128 for 32 query heads: bf16
-// 550 us (6.4 TB/s of 6.8); int8, capped, 336 us (5.4 TB/s), e4m3 317 (5.8): there the
-// widening of codes and the weights are what it spends its time on, one instruction for two
-// elements at best, and not memory.  So are 64- and 80-wide heads (4.1 and 3.3 TB/s): a
-// block's scores, exponentials and join cost the same for fewer bytes.  256-wide: 6.2 TB/s.
-// One sequence of 216000 tokens, e4m3: 110 us (4.2 TB/s).
+// Measured, 200 sequences of 1 to 8192 tokens, 8 key heads of 128 for 32 query heads, back
+// to back: fp16 492 us; int8, capped, 297 us (84% of the floor's bytes at 6.8 TB/s): there the
+// widening of codes and the weights are what it spends its time on beside memory, one
+// instruction for two elements at best.  So are 64- and 80-wide heads (4.1 and 3.3 TB/s
+// alone): a block's scores, exponentials and join cost the same for fewer bytes.  256-wide:
+// 6.2 TB/s.  One sequence of 216000 tokens, e4m3: 86 us (5.3 TB/s).
 //
 // A block is two small matrix products per warp, tokens on the 16-row side:
 //     S^T[16 tokens, 8 heads] = K q^T,    O^T[width, 8 heads] += V^T P^T
@@ -272,7 +272,8 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
         }
     }
     __syncwarp();
-    griddep_launch_dependents();
+    // (the next launch is not let in early: its CTAs, waiting, kept this one's and the join's
+    // from their places: 200 ragged sequences back to back 423 us so, 297 without)
     griddep_wait();
 
     // this CTA's run of units
@@ -809,7 +810,6 @@ template <bool QBF, int DP>
 __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedParams p) {
     __shared__ float weight[16][kMaxParts];
     __shared__ float total[16];
-    griddep_launch_dependents();
     griddep_wait();
     const int c = blockIdx.x, lane = threadIdx.x & 31;
     const int4 job = p.jobs[c];   // sequence, first query head, heads, further parts
