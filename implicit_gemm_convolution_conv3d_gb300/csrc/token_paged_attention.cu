@@ -78,7 +78,7 @@ struct Form {
 
 // CTAs of an SM: three of one group of query heads, two of two (their registers), as far
 // as shared memory goes: some compute while another joins its warps' results at a key
-// head's end.  (Two instead of three: 200 ragged sequences of up to 8192, 8 key heads of
+// head's end.  (Two instead of three, before edges were looked up by lanes: 200 ragged sequences of up to 8192, 8 key heads of
 // 128, int8 433 us for 414; 16 key heads of 64 650 for 561; one of 216000 107 for 110.)
 constexpr int ctas_of(int es, int dp, int ng) { return es * dp >= 512 ? 1 : ng == 1 ? 3 : 2; }
 
