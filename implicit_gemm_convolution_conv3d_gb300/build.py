@@ -28,7 +28,7 @@ SOURCES = ["conv_igemm.cu", "aux_kernels.cu", "conv3d_api.cu", "conv_noalloc.cu"
 HEADERS = ["ptx.cuh", "internal.h", "tile_table.h", "kernel_common.cuh"]
 # the token operators' own
 TOKEN_HEADERS = ["token_common.cuh", "token_activations.cuh", "token_rows.cuh", "token_ops_internal.h",
-                 "token_attention_internal.h", "token_paging.cuh"]
+                 "token_attention_internal.h", "token_paging.cuh", "token_scores.cuh"]
 PUBLIC_HEADERS = ["conv3d.h", "token_ops.h", "token_attention.h"]
 
 

@@ -368,6 +368,7 @@ int paged_attention_fwd(const void* q, int q_dtype, int64_t q_sequence_stride,
     p.out_head = out_head_stride;
     p.scale = scale;
     p.cap = cap;
+    p.inv_cap = cap > 0.0f ? 1.0f / cap : 0.0f;
     p.window = static_cast<int>(window > kMaxTokens ? 0 : window);
     p.sequences = static_cast<int>(sequences);
     p.kv_heads = static_cast<int>(cache->heads);

@@ -73,7 +73,7 @@ struct PagedParams {
     const int32_t* prefix;
     const float* slopes;
     long long q_seq, q_head, out_seq, out_head;   // elements
-    float scale, cap;
+    float scale, cap, inv_cap;   // inv_cap: 1 / cap
     int window;            // 0: none
     int sequences, kv_heads, group, width;
     int blocks;            // groups of query heads that share a pass over a key head

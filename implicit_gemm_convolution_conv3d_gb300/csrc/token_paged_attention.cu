@@ -41,13 +41,12 @@
 // weights takes 2^(log2 p_t - m') in fp32.
 #include "token_attention_internal.h"
 #include "token_paging.cuh"
-#include "token_common.cuh"
+#include "token_scores.cuh"
 
 namespace c3d {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTinyScale = 7.8886091e-31f;   // 2^-100
 // Weights may exceed 1 by 2^4 before what they are relative to follows: the outputs are
 // rarely rescaled, and a block of tokens without a new maximum needs no exchange of it.
@@ -87,11 +86,6 @@ __device__ __forceinline__ uint32_t word_at(int r, int c) {
     return static_cast<uint32_t>((c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ float lg2(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -532,7 +526,7 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
             const int t0 = token_of(b);
 
             // ---- scores (two sums: a product waits for the one before in its own)
-            float s2[F::kSubs][NG][4];   // in powers of two
+            float s2[F::kSubs][NG][4];   // in powers of two, but before a cap
             float lv[F::kSubs][2];
             bool none[F::kSubs][2];      // values too small to count
 #pragma unroll
@@ -588,17 +582,46 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
 #pragma unroll
                 for (int n = 0; n < NG; ++n)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float s = (sc[n][j] + sd[n][j]) * (ks[j >> 1] * qscale[n][j & 1]);
-                        if (p.cap > 0.0f) {
-                            // cap * tanh(s / cap), tanh x = 1 - 2 / (1 + e^2x)
-                            const float e = ex2(s * (2.0f * kLog2e / p.cap));
-                            s = (p.cap - 2.0f * p.cap * rcp_approx(1.0f + e)) * kLog2e;
+                    for (int j = 0; j < 4; ++j)
+                        s2[u][n][j] = (sc[n][j] + sd[n][j]) * (ks[j >> 1] * qscale[n][j & 1]);
+            }
+            if (p.cap > 0.0f) {
+                // all of the warp's scores within the polynomial's reach (most blocks), or each as it lies
+                float top = 0.0f;
+#pragma unroll
+                for (int u = 0; u < F::kSubs; ++u)
+#pragma unroll
+                    for (int n = 0; n < NG; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) top = fmaxf(top, fabsf(s2[u][n][j]));
+                const bool small = __all_sync(0xffffffffu, top * p.inv_cap <= kTanhReach);
+#pragma unroll
+                for (int u = 0; u < F::kSubs; ++u)
+#pragma unroll
+                    for (int n = 0; n < NG; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; j += 2) {
+                            float (&s)[4] = s2[u][n];
+                            if (small) {
+                                uint32_t a, b;
+                                split(cap_pair(two(__float_as_uint(s[j]), __float_as_uint(s[j + 1])), two(p.inv_cap)), a, b);
+                                s[j] = __uint_as_float(a);
+                                s[j + 1] = __uint_as_float(b);
+                            } else {
+                                s[j] = cap_score(s[j], p.cap, p.inv_cap) * kLog2e;
+                                s[j + 1] = cap_score(s[j + 1], p.cap, p.inv_cap) * kLog2e;
+                            }
                         }
-                        if (p.slopes)
-                            s -= slope[n][j & 1] * static_cast<float>(see.length - 1 - (t0 + 16 * u + r0 + 8 * (j >> 1)));
-                        s2[u][n][j] = s;
-                    }
+            }
+            if (p.slopes) {
+#pragma unroll
+                for (int u = 0; u < F::kSubs; ++u)
+#pragma unroll
+                    for (int n = 0; n < NG; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            s2[u][n][j] -= slope[n][j & 1] *
+                                           static_cast<float>(see.length - 1 - (t0 + 16 * u + r0 + 8 * (j >> 1)));
             }
             // ---- weights
             if (by_words) {   // (others are seen whole)
