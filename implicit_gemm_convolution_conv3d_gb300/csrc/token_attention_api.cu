@@ -474,6 +474,11 @@ int packed_attention_fwd(const void* q, int64_t q_token_stride, int64_t q_head_s
     p.window = static_cast<int>(window > kMaxTokens ? 0 : window);
     p.scale = scale;
     p.cap = cap;
+    p.inv_cap = cap > 0.0f ? 1.0f / cap : 0.0f;
+    // the coefficients of the cap's polynomial go with scale (scale / cap)^2d, d = 0 to 4
+    const double first = std::fabs(static_cast<double>(scale)), ratio = cap > 0.0f ? first / cap : 0.0;
+    const double last = first * std::pow(ratio, 8);
+    p.per_cap = std::min(first, last) > 1e-30 && std::max(first, last) < 1e30 ? static_cast<float>(ratio) : INFINITY;
     p.out_aligned = !words(out, out_token_stride, out_head_stride, 2) ? 0
                     : aligned_to(out, 32) && out_token_stride % 16 == 0 && out_head_stride % 16 == 0 ? 32 : 16;
     p.status = lim.status;

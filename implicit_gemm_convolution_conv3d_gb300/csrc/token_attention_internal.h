@@ -111,7 +111,8 @@ struct PackedParams {
     long long q_tokens, k_tokens;
     int documents, heads, group, width;   // group: query heads of a key head
     int causal, window;
-    float scale, cap;
+    float scale, cap, inv_cap;   // inv_cap: 1 / cap
+    float per_cap;               // |scale| / cap, or infinite where the cap's polynomial cannot hold its powers
     int out_aligned;   // bytes that rows of out are aligned to: 32, 16 or fewer (0)
     int* status;
     unsigned long long wait_ns;

@@ -36,7 +36,7 @@
 // Weights are rounded to the inputs' 16-bit type for the second product, whose
 // operands have one type; the sum of weights takes them unrounded.
 #include "token_attention_internal.h"
-#include "token_common.cuh"
+#include "token_scores.cuh"
 
 namespace c3d {
 
@@ -56,14 +56,7 @@ constexpr uint32_t kAsk = 8;           // asked for at once behind the last job
 // too, kAsk at a time: a buffer of 65536 rows with 1000 in use takes 22 us either way.  Of
 // short documents the planner finds 32 jobs at a time instead (100 x 100: 22 us, 28 dealt).
 constexpr long long kDealtFrom = 384;
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLag = 8.0f;           // powers of two that weights may exceed 1 by
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 template <bool BF>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -123,31 +116,6 @@ __device__ __forceinline__ void plan_tiles(const PackedParams& p, Job& j, int nq
     }
 }
 
-// Two values a register pair: one instruction each
-__device__ __forceinline__ uint64_t two(uint32_t a, uint32_t b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t two(float v) { return two(__float_as_uint(v), __float_as_uint(v)); }
-__device__ __forceinline__ void split(uint64_t v, uint32_t& a, uint32_t& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -171,7 +139,7 @@ __device__ __forceinline__ float max128(const uint32_t (&s)[4][32]) {
 // A row's score at a key, in powers of two
 __device__ __forceinline__ float shaped(const PackedParams& p, float dot, int i, int j, float slope2) {
     float s = dot * p.scale;
-    if (p.cap > 0.0f) s = p.cap - 2.0f * p.cap * rcp_approx(1.0f + ex2(s * (2.0f * kLog2e / p.cap)));
+    if (p.cap > 0.0f) s = cap_score(s, p.cap, p.inv_cap);
     return s * kLog2e - slope2 * fabsf(static_cast<float>(i - j));
 }
 
@@ -780,8 +748,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
         const int i = (warp - 4) >> 2;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + i * kRows, t_o = tmem + lanes + NQ * kRows + i * o_pitch;
-        // the cap's constants: scores times its polynomial are powers of two already
-        const float cap2 = p.cap * kLog2e, per_cap = MOD & kCap ? p.scale / p.cap : 0.0f;
+        const float per_cap = p.per_cap;
         const float c = MOD ? 1.0f : p.scale * kLog2e;
         uint32_t turn = 0;   // this tile's units so far
         bool ok = true;
@@ -818,16 +785,16 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
 #pragma unroll
                 for (int h = 0; h < 4; ++h) tmem_ld_32x32b_x32(t_s + 32 * h, s[h]);
                 tmem_ld_wait();
-                // tanh(x) for |x| <= 3/4 as x times a polynomial in x^2, within 2.1e-7 (a
-                // least-squares fit reweighted towards equal errors): packed multiply-adds where
-                // the exponential's form takes two turns of the special-function unit a value.
-                // A score is then x times `co` in its square, in powers of two.
-                constexpr float kTanh[5] = {0.999997199f, -0.333230764f, 0.132260904f, -0.0492804274f, 0.0123188179f};
+                // Scores that are all within the cap's polynomial go through it with the scale and the
+                // cap in its coefficients: a score is then its product times `co` in that product's
+                // square, in powers of two, where the exponential's form takes two turns of the
+                // special-function unit a value.  (Where these coefficients were no normal numbers,
+                // per_cap is infinite and no score is within.)
                 uint64_t co[5];
                 bool small = false;   // all scores of the warp's tile are within the polynomial's reach
                 if (MOD & kCap) {
-                    small = __all_sync(0xffffffffu, max128<true>(s) * fabsf(per_cap) <= 0.75f);
-                    float f = cap2 * per_cap;
+                    small = __all_sync(0xffffffffu, max128<true>(s) * per_cap <= kTanhReach);
+                    float f = p.scale * kLog2e;
 #pragma unroll
                     for (int d = 0; d < 5; ++d) {
                         co[d] = two(kTanh[d] * f);
@@ -841,19 +808,28 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                     for (int d = 2; d >= 0; --d) y = fma2(u, y, co[d]);
                     return y;
                 };
-                auto capped = [&](float v) {
-                    return cap2 - 2.0f * cap2 * rcp_approx(1.0f + ex2(v * (2.0f * kLog2e * per_cap)));
-                };
                 // the cap alone keeps the order of scores: where all are seen their maximum is taken
                 // before it, and small ones go through it on their way into the exponent
                 const bool open = t0 + kRows <= job.keys &&
                                   (t0 + kRows <= job.prefix || (t0 >= all_lo && t0 + kRows <= all_hi));
                 const bool late = MOD == kCap && small && open;
                 if ((MOD & kCap) && !small) {
+                    // (through tensor memory, 32 at a time: unrolled over the row, this rare form's code
+                    // and registers cost the usual one 6%)
+#pragma unroll 1
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t t[32];
+                        tmem_ld_32x32b_x32(t_s + 32 * h, t);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int h = 0; h < 4; ++h)
+                        for (int e = 0; e < 32; e += 2)
+                            split(cap_pair_any(mul2(two(t[e], t[e + 1]), two(p.scale)), p.cap, p.inv_cap), t[e], t[e + 1]);
+                        tmem_st_32x32b_x32(t_s + 32 * h, t);
+                    }
+                    tmem_st_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) s[h][e] = __float_as_uint(capped(__uint_as_float(s[h][e])));
+                    for (int h = 0; h < 4; ++h) tmem_ld_32x32b_x32(t_s + 32 * h, s[h]);
+                    tmem_ld_wait();
                 } else if ((MOD & kCap) && !late) {
 #pragma unroll
                     for (int h = 0; h < 4; ++h)

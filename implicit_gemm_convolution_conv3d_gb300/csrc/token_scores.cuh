@@ -56,6 +56,20 @@ __device__ __forceinline__ uint64_t cap_pair(uint64_t s, uint64_t inv_cap) {
     return mul2(s, y);
 }
 
+// Any two
+__device__ __forceinline__ uint64_t cap_pair_any(uint64_t s, float cap, float inv_cap) {
+    uint32_t x[2], near[2], r[2];
+    split(mul2(s, two(inv_cap)), x[0], x[1]);
+    split(cap_pair(s, two(inv_cap)), near[0], near[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float v = __uint_as_float(x[i]);
+        const float far = cap * (kLog2e - 2.0f * kLog2e * rcp_approx(1.0f + ex2(v * (2.0f * kLog2e))));
+        r[i] = fabsf(v) <= kTanhReach ? near[i] : __float_as_uint(far);
+    }
+    return two(r[0], r[1]);
+}
+
 // Any score, capped
 __device__ __forceinline__ float cap_score(float s, float cap, float inv_cap) {
     const float x = s * inv_cap, u = x * x;
