@@ -57,6 +57,9 @@ constexpr uint32_t kAsk = 8;           // asked for at once behind the last job
 // short documents the planner finds 32 jobs at a time instead (100 x 100: 22 us, 28 dealt).
 constexpr long long kDealtFrom = 384;
 constexpr float kLag = 8.0f;           // powers of two that weights may exceed 1 by
+// f16 weights (and their sum) are taken 2^7 times as large, up to 2^15 of f16's 2^16: those
+// of 2^-31 of the largest one still count, where 2^-24 would be the least otherwise.
+constexpr float kUp = 7.0f;
 
 template <bool BF>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -900,7 +903,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                     }
                 }
                 fresh = false;
-                const uint64_t off = two(ref == -INFINITY ? 0.0f : -ref * c), cc = two(c);
+                const uint64_t off = two(ref == -INFINITY ? 0.0f : fmaf(-ref, c, BF ? 0.0f : kUp)), cc = two(c);
                 uint64_t sums[2] = {0ull, 0ull};
                 auto weights = [&](auto exponent) {
 #pragma unroll

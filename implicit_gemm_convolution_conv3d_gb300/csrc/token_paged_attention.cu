@@ -51,6 +51,9 @@ constexpr float kTinyScale = 7.8886091e-31f;   // 2^-100
 // Weights may exceed 1 by 2^4 before what they are relative to follows: the outputs are
 // rarely rescaled, and a block of tokens without a new maximum needs no exchange of it.
 constexpr float kLag = 4.0f;
+// f16 weights are taken 2^11 times as large, next to f16's largest (2^15 of 2^16): those of
+// 2^-35 of the largest one still count, where 2^-24 would be the least otherwise.
+constexpr float kUp = 11.0f, kDown = 1.0f / 2048.0f;
 
 template <int ES, int DP>
 struct Form {
@@ -676,10 +679,12 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
                     float pw[4];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float base = m[n][j] == -INFINITY ? 0.0f : m[n][j];
+                        // (the sum of weights without values' scales: the factor stays out of it, as it
+                        // is large enough where these are small)
+                        const float base = m[n][j] == -INFINITY ? 0.0f : m[n][j] - (kCodes || kBf ? 0.0f : kUp);
                         const float x = s2[u][n][j] - base, y = s2[u][n][j + 2] - base;
-                        pw[j] = none[u][0] ? 0.0f : ex2(x + lv[u][0]);
-                        pw[j + 2] = none[u][1] ? 0.0f : ex2(y + lv[u][1]);
+                        pw[j] = none[u][0] ? 0.0f : ex2(x + (kCodes ? lv[u][0] + kUp : 0.0f));
+                        pw[j + 2] = none[u][1] ? 0.0f : ex2(y + (kCodes ? lv[u][1] + kUp : 0.0f));
                         l[n][j] += kCodes ? ex2(x) + ex2(y) : pw[j] + pw[j + 2];
                     }
 #pragma unroll
@@ -784,6 +789,10 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
                 x += v.x * f;
                 y += v.y * f;
                 sum += sm[2 * at + 1] * f;
+            }
+            if (kCodes) {
+                x *= kDown;
+                y *= kDown;
             }
             if (whole) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
