@@ -58,8 +58,12 @@ constexpr uint32_t kAsk = 8;           // asked for at once behind the last job
 constexpr long long kDealtFrom = 384;
 constexpr float kLag = 8.0f;           // powers of two that weights may exceed 1 by
 // f16 weights (and their sum) are taken 2^7 times as large, up to 2^15 of f16's 2^16: those
-// of 2^-31 of the largest one still count, where 2^-24 would be the least otherwise.
-constexpr float kUp = 7.0f;
+// of 2^-31 of the largest one still count, where 2^-24 would be the least otherwise.  bf16
+// weights have fp32's range and are taken 2^-24 times as large, so that sums over 2^16 keys
+// (2^24, with weights of 1) hold for values up to the type's largest; results below 2^-112
+// lose bits instead.
+template <bool BF>
+constexpr float kUp = BF ? -24.0f : 7.0f;
 
 template <bool BF>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -903,7 +907,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                     }
                 }
                 fresh = false;
-                const uint64_t off = two(ref == -INFINITY ? 0.0f : fmaf(-ref, c, BF ? 0.0f : kUp)), cc = two(c);
+                const uint64_t off = two(ref == -INFINITY ? 0.0f : fmaf(-ref, c, kUp<BF>)), cc = two(c);
                 uint64_t sums[2] = {0ull, 0ull};
                 auto weights = [&](auto exponent) {
 #pragma unroll

@@ -52,8 +52,10 @@ constexpr float kTinyScale = 7.8886091e-31f;   // 2^-100
 // rarely rescaled, and a block of tokens without a new maximum needs no exchange of it.
 constexpr float kLag = 4.0f;
 // f16 weights are taken 2^11 times as large, next to f16's largest (2^15 of 2^16): those of
-// 2^-35 of the largest one still count, where 2^-24 would be the least otherwise.
-constexpr float kUp = 11.0f, kDown = 1.0f / 2048.0f;
+// 2^-35 of the largest one still count, where 2^-24 would be the least otherwise.  bf16
+// weights have fp32's range and are taken 2^-24 times as large, so that sums over 2^20
+// tokens hold for values up to the type's largest (results below 2^-112 lose bits instead).
+constexpr float kUp = 11.0f, kDown = 1.0f / 2048.0f, kUpBf16 = -24.0f;
 
 template <int ES, int DP>
 struct Form {
@@ -681,7 +683,7 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
                     for (int j = 0; j < 2; ++j) {
                         // (the sum of weights without values' scales: the factor stays out of it, as it
                         // is large enough where these are small)
-                        const float base = m[n][j] == -INFINITY ? 0.0f : m[n][j] - (kCodes || kBf ? 0.0f : kUp);
+                        const float base = m[n][j] == -INFINITY ? 0.0f : m[n][j] - (kCodes ? 0.0f : kBf ? kUpBf16 : kUp);
                         const float x = s2[u][n][j] - base, y = s2[u][n][j + 2] - base;
                         pw[j] = none[u][0] ? 0.0f : ex2(x + (kCodes ? lv[u][0] + kUp : 0.0f));
                         pw[j + 2] = none[u][1] ? 0.0f : ex2(y + (kCodes ? lv[u][1] + kUp : 0.0f));

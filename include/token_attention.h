@@ -23,6 +23,9 @@
  *     (|i - j| < window, if window > 0, and j <= i, if causal) or j < prefix[sequence].
  *     What it does not see takes no part, whatever it holds.  A query that sees
  *     nothing (or whose scores are all -inf) gets zeros.
+ *   - BF16 values may be of any size: their weighted sums are held in fp32 below 2^128
+ *     for 2^16 keys (2^20 tokens of a paged cache) whatever the scores are.  Results
+ *     below 2^-112 lose bits.
  *   - Query head h reads key head h / (heads / kv_heads).
  *   - Rows of an output or of a cache that overlap are refused; outputs overlap no input
  *     (but rotary_fwd's, which may be x itself).
