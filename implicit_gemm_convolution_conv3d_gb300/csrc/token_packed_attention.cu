@@ -89,7 +89,7 @@ struct Job {
     long long q0, k0;        // packed rows of the document's first query and key
     __device__ int key(int n) const { return (n < lead_tiles ? n : n - lead_tiles + skip) * kRows; }
 };
-static_assert(344 + kJobs * sizeof(Job) <= kSmallBytes - 16 * kAsk - 8, "barriers, words, jobs, the dealer's answers");
+static_assert(352 + kJobs * sizeof(Job) <= kSmallBytes - 16 * kAsk - 8, "barriers, words, jobs, the dealer's answers");
 
 // The keys that rows [a, b) of the job see: [lo, hi) of any of them, and [0, lead).
 struct Range {
@@ -165,10 +165,12 @@ __device__ __forceinline__ RowMask row_mask(const PackedParams& p, const Job& j,
     return RowMask{r.lo, r.hi, r.lead, j.keys};
 }
 
-// Four elements of a row
+// Four elements of a row, as they lie in memory and as fp32
+__device__ __forceinline__ uint2 four_raw(const unsigned char* base, long long i) {
+    return *reinterpret_cast<const uint2*>(base + 2 * i);
+}
 template <bool BF>
-__device__ __forceinline__ void four(const unsigned char* base, long long i, float (&v)[4]) {
-    const uint2 w = *reinterpret_cast<const uint2*>(base + 2 * i);
+__device__ __forceinline__ void four(uint2 w, float (&v)[4]) {
     const uint32_t x[2] = {w.x, w.y};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -179,50 +181,81 @@ __device__ __forceinline__ void four(const unsigned char* base, long long i, flo
 
 // A row whose result is not finite although what it sees may be: an unseen key of a
 // tile that was multiplied (weight 0) has a value that is not finite.  Then the row is
-// computed again, over what it sees alone, by the whole warp, four elements a lane (about
-// 100 cycles a key: the other warps wait meanwhile, and their waits are bounded).  Rolled
-// loops: it should not take the instruction cache from the others.
+// computed again, over what it sees alone, by the whole warp, four elements a lane and eight
+// keys at a time, so that their loads are in flight together: 260 cycles a key, 620 one at a
+// time (127 rows over 60000 keys: 265 ms and 625).  The other warps wait meanwhile, and count
+// their bounds from its last word that it goes on.
 template <bool BF>
-__device__ __forceinline__ void redo_row(const PackedParams& p, const Job& job, const Seen& seen, int row, int lane) {
+__device__ __forceinline__ void redo_row(const PackedParams& p, const Job& job, const Seen& seen, int row, int lane,
+                                         uint32_t* goes_on) {
+    constexpr int kAtOnce = 8;
     const RowMask m = row_mask(p, job, row);
     const bool in = 4 * lane < p.width;
     const long long base = job.k0 * p.k_tok + static_cast<long long>(job.head / p.group) * p.k_head + 4 * lane;
     const float slope2 = p.slopes ? p.slopes[job.head] * kLog2e : 0.0f;
     float top = -INFINITY, sum = 0.0f, q[4] = {}, o[4] = {};
-    if (in) four<BF>(p.q, (job.q0 + row) * p.q_tok + static_cast<long long>(job.head) * p.q_head + 4 * lane, q);
+    if (in) four<BF>(four_raw(p.q, (job.q0 + row) * p.q_tok + static_cast<long long>(job.head) * p.q_head + 4 * lane), q);
     bool spoiled = false, nan = false;
     // pass 0: is an unseen key's value the cause?  1: the row
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         if (pass && !__any_sync(0xffffffffu, spoiled)) return;
 #pragma unroll 1
-        for (int n = 0; n < 4 * job.count; ++n) {
-            const int j0 = job.key(n >> 2) + 32 * (n & 3);
+        for (int n = 0; n < 128 / kAtOnce * job.count; ++n) {
+            constexpr int kPer = 128 / kAtOnce;   // of a tile
+            const int j0 = job.key(n / kPer) + n % kPer * kAtOnce;
+            if (lane == 0) atomicAdd(goes_on, 1u);
             uint32_t bits = m.bits(j0);
             if (pass == 0) bits = ~bits & bits_below(job.keys - j0);
-            if (!seen(n >> 2)) bits = 0u;
-#pragma unroll 1
-            for (; bits; bits &= bits - 1u) {
-                const int j = j0 + __ffs(bits) - 1;
-                float k[4] = {}, v[4] = {};
-                if (in) four<BF>(p.v, base + j * p.k_tok, v);
-                if (pass == 0) {
+            if (!seen(n / kPer)) bits = 0u;
+            bits &= (1u << kAtOnce) - 1u;
+            if (!bits) continue;
+            uint2 kw[kAtOnce], vw[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const bool load = in && (bits >> i & 1u);
+                kw[i] = vw[i] = make_uint2(0u, 0u);
+                if (load) vw[i] = four_raw(p.v, base + (j0 + i) * p.k_tok);
+                if (load && pass) kw[i] = four_raw(p.k, base + (j0 + i) * p.k_tok);
+            }
+            float s[kAtOnce], v[4], now = top;
+            if (pass == 0) {
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) {
+                    four<BF>(vw[i], v);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) spoiled = spoiled || !(fabsf(v[e]) < INFINITY);
-                    continue;
                 }
-                if (in) four<BF>(p.k, base + j * p.k_tok, k);
-                float s = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
+                continue;
+            }
 #pragma unroll
-                for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-                s = shaped(p, s, row + job.shift, j, slope2);
-                nan = nan || !(s < INFINITY);
-                const float now = fmaxf(top, s);
-                const float fall = now == -INFINITY ? 1.0f : ex2(top - now), w = now == -INFINITY ? 0.0f : ex2(s - now);
-                top = now;
-                sum = fmaf(sum, fall, w);
+            for (int i = 0; i < kAtOnce; ++i) {
+                four<BF>(kw[i], v);
+                s[i] = q[0] * v[0] + q[1] * v[1] + q[2] * v[2] + q[3] * v[3];
+            }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] = fmaf(w, v[e], o[e] * fall);
+            for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                s[i] = bits >> i & 1u ? shaped(p, s[i], row + job.shift, j0 + i, slope2) : -INFINITY;
+                nan = nan || !(s[i] < INFINITY);
+                now = fmaxf(now, s[i]);
+            }
+            if (now == -INFINITY) continue;
+            const float fall = ex2(top - now);
+            top = now;
+            sum *= fall;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] *= fall;
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const float w = ex2(s[i] - now + kUp<BF>);
+                sum += w;
+                four<BF>(vw[i], v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = fmaf(w, v[e], o[e]);
             }
         }
     }
@@ -238,15 +271,22 @@ __device__ __forceinline__ void redo_row(const PackedParams& p, const Job& job, 
 // Bounded waits without a call (see wait_bar and drain_wait): the compiler makes none from
 // warps that have registers of a number of their own.  A role sleeps in hardware between
 // looks, so that its polling leaves the issue slots to the others.  Whole warps wait, with
-// one answer for all lanes.
+// one answer for all lanes.  The bound counts anew while rows are computed again: their
+// warps say so in a word behind the abort flag (kGoesOn).
+constexpr int kGoesOn = 5;
 __device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
                                           int* status, long long limit_cycles) {
     constexpr uint32_t kAll = 0xffffffffu;
     // (without a limit to wait for, nothing is waited for)
     if (__all_sync(kAll, limit_cycles ? mbar_try_wait(bar, parity) : mbar_test_wait(bar, parity))) return true;
-    const long long t0 = clock64();
-    while (!__any_sync(kAll, *abort_flag != 0u || clock64() - t0 >= limit_cycles))
+    long long t0 = clock64();
+    uint32_t last = abort_flag[kGoesOn];
+    while (!__any_sync(kAll, *abort_flag != 0u || clock64() - t0 >= limit_cycles)) {
         if (__all_sync(kAll, mbar_try_wait_for(bar, parity, 20000u))) return true;
+        const uint32_t now = abort_flag[kGoesOn];
+        if (now != last) t0 = clock64();
+        last = now;
+    }
     if (atomicExch(const_cast<uint32_t*>(abort_flag), 1u) == 0u) atomicExch(status, kStatusTimeout);
     return false;
 }
@@ -366,9 +406,10 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
     const uint32_t deal_answer = bars + kSmallBytes - 16u * kAsk, deal_bar = deal_answer - 8u;
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem_raw + (drain_bar + 8u - raw));
     // misc[0] TMEM base, [1] abort flag, [2] ring loads issued, [3] Q loads issued, [4] whether a
-    // last tile's values are on their way (1 + its phase), [5] to which slot; then the jobs
+    // last tile's values are on their way (1 + its phase), [5] to which slot, [6] counts while rows
+    // are computed again; then the jobs
     volatile uint32_t* abort_flag = misc + 1;
-    Job* jobs = reinterpret_cast<Job*>(misc + 6);
+    Job* jobs = reinterpret_cast<Job*>(misc + 8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // (two cycles a nanosecond, as in wait_bar)
     const long long limit = static_cast<long long>(p.wait_ns > (1ull << 61) ? (1ull << 61) : p.wait_ns) * 2;
@@ -398,6 +439,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
         misc[2] = 0u;
         misc[3] = 0u;
         misc[4] = 0u;
+        misc[1 + kGoesOn] = 0u;
         fence_mbar_init();
         prefetch_tmap(&q_map);
         prefetch_tmap(&k_map);
@@ -998,7 +1040,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                 __syncwarp();
             }
             for (uint32_t again = __ballot_sync(0xffffffffu, valid && odd != 0.0f); again; again &= again - 1u)
-                redo_row<BF>(p, job, mine, row - lane + __ffs(again) - 1, lane);
+                redo_row<BF>(p, job, mine, row - lane + __ffs(again) - 1, lane, misc + 1 + kGoesOn);
             __syncwarp();
             tc_fence_before();
         }
