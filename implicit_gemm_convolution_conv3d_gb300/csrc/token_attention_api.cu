@@ -377,11 +377,15 @@ int paged_attention_fwd(const void* q, int q_dtype, int64_t q_sequence_stride,
     p.grid = paged_grid(sequences, cache->heads, p.group, p.width, p.map.capacity, lim.num_sms);
     p.num_sms = lim.num_sms;
     p.whole = paged_whole(sequences, cache->heads, p.group, p.width, p.map.capacity, lim.num_sms);
-    // (a workspace that is given has to do for heads that are split, too)
+    // (one of 0 bytes, where that is the size, is none; any other that is given has to do for
+    // heads that are split, too)
     const size_t need = paged_workspace(p.grid, p.width);
-    if (workspace ? workspace_bytes < need || !aligned_to(workspace, 16) : !p.whole)
-        return invalid("paged_attention_fwd needs a 16-byte aligned workspace of "
-                       "paged_attention_workspace_size bytes");
+    const bool given = workspace && (workspace_bytes || !p.whole);
+    if (given ? workspace_bytes < need || !aligned_to(workspace, 16) : !p.whole)
+        return invalid(p.whole ? "paged_attention_fwd needs no workspace here, and one that is given must be 16-byte "
+                                 "aligned and large enough for key heads that are split"
+                               : "paged_attention_fwd needs a 16-byte aligned workspace of "
+                                 "paged_attention_workspace_size bytes");
     if (!p.whole) {
         p.jobs = static_cast<int4*>(workspace);
         p.partial = reinterpret_cast<float*>(p.jobs + p.grid);

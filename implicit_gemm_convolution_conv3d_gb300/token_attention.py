@@ -348,7 +348,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     distance.  With ``window`` > 0 only the last ``window`` tokens and the first
     ``prefix[s]`` are seen; pages of unseen tokens are not looked at.  The workspace
     (``paged_attention_workspace_size`` bytes) is taken from torch's allocator unless
-    one is given (calls that may overlap need one each)."""
+    one is given (calls that may overlap need one each; where the size is 0, one of
+    0 bytes, or of the size of longer tables)."""
     lib = _fns or _bind()
     c = _cache(k_cache, v_cache, k_scale, v_scale)
     n, heads, width, qs, qh, code = _heads(q, _HALF, "q")

@@ -107,7 +107,9 @@ int kv_cache_read(const kv_cache* cache, void* k, void* v, int dtype, int64_t to
  *   prefix, slopes     int32 [sequences] or NULL; fp32 [heads] or NULL
  *   workspace          paged_attention_workspace_size bytes, 16-byte aligned; its
  *                      contents before the call do not matter.  Calls that may
- *                      run at the same time need one each
+ *                      run at the same time need one each.  Where that size is 0,
+ *                      NULL or any pointer with 0 bytes; a workspace of more bytes
+ *                      is checked for the size of split heads all the same
  * Scales of values have to be positive; those below 2^-100 count as 0. */
 int paged_attention_fwd(const void* q, int q_dtype, int64_t q_sequence_stride,
                         int64_t q_head_stride, const kv_cache* cache, const int32_t* page_table,
