@@ -133,34 +133,54 @@ def _table(t: torch.Tensor) -> Tuple[int, int, int, int]:
     return t.data_ptr(), (t.stride(0) if n > 1 else pages), pages, n
 
 
+def _own(shape, stride) -> Tuple[int, ...]:
+    """Strides in which a dimension of one element, whose stride is nobody's, has the extent
+    of those behind it."""
+    out, extent = [], 1
+    for n, s in zip(reversed(shape), reversed(stride)):
+        s = s if n > 1 else extent
+        extent = max(extent, n * s)
+        out.append(s)
+    return tuple(reversed(out))
+
+
+def _strides(a: torch.Tensor, b: torch.Tensor, what: str) -> Tuple[int, ...]:
+    """The strides that two tensors of one shape share, but the last, which is contiguous."""
+    shape, stride, other = a.shape, a.stride(), b.stride()
+    if 1 in shape:
+        stride, other = _own(shape, stride), _own(shape, other)
+    if stride != other:
+        raise ValueError(f"{what} must have the same strides")
+    if stride[-1] != 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return stride[:-1]
+
+
 def _cache(k: torch.Tensor, v: torch.Tensor, k_scale, v_scale) -> _Cache:
     code = _CACHE.get(k.dtype)
     if code is None:
         raise TypeError(f"a cache has dtype {k.dtype}: one of {[str(d) for d in _CACHE]}")
     if k.dim() != 4 or not k.is_cuda or not v.is_cuda:
         raise ValueError("a cache must be CUDA tensors [pages, kv_heads, page_size, width]")
-    if v.dtype is not k.dtype or v.shape != k.shape or v.stride() != k.stride():
-        raise ValueError("k_cache and v_cache must have the same shape, type and strides")
-    shape, stride = k.shape, k.stride()
-    if stride[3] != 1 and shape[3] > 1:
-        raise ValueError("a cache must have contiguous rows")
+    shape = k.shape
+    if v.dtype is not k.dtype or v.shape != shape:
+        raise ValueError("k_cache and v_cache must have the same shape and type")
+    stride = _strides(k, v, "k_cache and v_cache")
     kp = vp = None
-    ps = hs = 0
+    scale = (0, 0)
     if k.dtype in _CODE:
         if k_scale is None or v_scale is None:
             raise ValueError("an 8-bit cache needs k_scale and v_scale")
         for s in (k_scale, v_scale):
             if s.dtype is not torch.float32:
                 raise TypeError("scales must be float32")
-            if s.shape != shape[:3] or not s.is_cuda or s.stride(2) != 1:
-                raise ValueError(f"scales must be CUDA tensors {tuple(shape[:3])} with contiguous rows")
-        ps, hs, _ = k_scale.stride()
-        if v_scale.stride() != k_scale.stride():
-            raise ValueError("k_scale and v_scale must have the same strides")
+            if s.shape != shape[:3] or not s.is_cuda:
+                raise ValueError(f"scales must be CUDA tensors {tuple(shape[:3])}")
+        scale = _strides(k_scale, v_scale, "k_scale and v_scale")
         kp, vp = k_scale.data_ptr(), v_scale.data_ptr()
     elif k_scale is not None or v_scale is not None:
         raise ValueError("only an 8-bit cache has scales")
-    return _Cache(k.data_ptr(), v.data_ptr(), kp, vp, code, *shape, *stride[:3], ps, hs)
+    return _Cache(k.data_ptr(), v.data_ptr(), kp, vp, code, *shape, *stride, *scale)
 
 
 # ------------------------------------------------------------------ rotary positions
