@@ -58,6 +58,22 @@ bool overlap(int64_t width, std::initializer_list<std::pair<int64_t, int64_t>> d
     return false;
 }
 
+// frequency / 2 pi, modulo 1, in units of 2^-64 (nearest), modulo 2^64.  1 / 2 pi is the sum
+// of two doubles, exact to 2^-110, so that the product with the frequency's 53 bits is exact
+// beyond 2^-64 for frequencies up to 2^40, and to 2^-105 of the turns themselves beyond.
+unsigned long long turns_of(double frequency) {
+    constexpr double kHigh = 0x1.45f306dc9c883p-3, kLow = -0x1.6b01ec5417056p-57;
+    const double f = std::fabs(frequency);
+    const volatile double product = f * kHigh;   // (rounded here, whatever a compiler fuses)
+    const double high = product, low = std::fma(f, kHigh, -high) + f * kLow;
+    // whole turns of whole positions do not count; what is left is exact in each part
+    const double a = (high - std::floor(high)) * 0x1p64, b = (low - std::rint(low)) * 0x1p64;
+    const double whole = std::floor(a), rest = b + (a - whole);   // a < 2^64, |rest| <= 2^63 + 1
+    unsigned long long t = static_cast<unsigned long long>(whole);
+    t += rest < 0.0 ? 0ull - static_cast<unsigned long long>(0.5 - rest) : static_cast<unsigned long long>(rest + 0.5);
+    return frequency < 0.0 ? 0ull - t : t;
+}
+
 // heads of tokens: [tokens, heads, width] with strides in elements
 const char* bad_heads(const void* p, int64_t tok, int64_t head, int64_t tokens, int64_t heads,
                       int64_t width, int elt) {
@@ -257,9 +273,7 @@ int rotary_fwd(const void* x, int dtype, int64_t x_token_stride, int64_t x_head_
     for (int i = 0; i < pairs; ++i) {
         if (axis[i] < 0 || axis[i] >= axes) return invalid("a pair's axis is not one of the positions'");
         if (!std::isfinite(frequency[i])) return invalid("a frequency is not finite");
-        double turn = frequency[i] * 0.15915494309189533577;   // 1 / (2 pi)
-        turn -= std::floor(turn);                              // whole turns of whole positions
-        p.turns[i] = turn >= 1.0 ? 0ull : static_cast<unsigned long long>(std::ldexp(turn, 64));
+        p.turns[i] = turns_of(frequency[i]);
         p.axis[i] = static_cast<unsigned char>(axis[i]);
     }
     if (tokens == 0 || heads == 0) return CONV_OK;

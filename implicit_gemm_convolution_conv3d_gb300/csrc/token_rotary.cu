@@ -2,9 +2,9 @@
 //
 // A pair (a, b) of a head becomes (a cos t - b sin t, b cos t + a sin t) with
 // t = position[axis] * frequency.  The turn is taken in whole numbers: with
-// F = 2^64 * frequency / 2 pi, position * F modulo 2^64 is the angle's fraction
-// of a turn, exact for every 64-bit position (no argument reduction, and far
-// positions lose nothing), of which the sine and cosine are taken in fp32.
+// F = 2^64 * frequency / 2 pi, to the nearest whole number, position * F modulo 2^64
+// is the angle's fraction of a turn, within |position| 2^-65 of a turn for every 64-bit
+// position (no argument reduction), of which the sine and cosine are taken in fp32.
 // Memory-bound: every element is read and written once.  The sines of a block's
 // tokens are computed once into shared memory and shared by all heads; a thread
 // keeps those of its pairs in registers over the heads it rotates.

@@ -230,7 +230,8 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, sections: Sequence[int],
     with "shared" base^(-p/N) over all N pairs; ``frequencies`` [N] gives them
     outright, and ``scales`` [axes] multiplies them (positions in other units).
     ``pairs``: "half" pairs elements (p, p + N), "interleaved" (2p, 2p + 1); elements
-    from 2N on stay as they are.  Angles are exact for far positions.  ``inverse``
+    from 2N on stay as they are.  Angles are exact to 2 pi |position| 2^-65, then in
+    fp32, for far positions too.  ``inverse``
     turns back: the gradient with respect to x of a loss whose gradient with respect
     to the result is x.  x bf16, fp16 or fp32; ``out`` may be ``x``."""
     lib = _fns or _bind()

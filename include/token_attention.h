@@ -52,7 +52,9 @@ extern "C" {
  *   interleaved        pair p is elements (2p, 2p + 1), else (p, p + pairs); the
  *                      elements from 2 * pairs on are copied
  *   inverse            turns back: also the gradient of x from that of out
- * Angles are exact to the frequency's 53 bits for any position. */
+ * A frequency's turn for each unit of position is held to 2^-65 of a turn (frequencies up to
+ * 2^40), so an angle is exact to 2 pi |position| 2^-65 radians, before its sine and cosine
+ * are taken in fp32. */
 int rotary_fwd(const void* x, int dtype, int64_t x_token_stride, int64_t x_head_stride,
                const void* positions, int position_bytes, int axes, const int* axis,
                const double* frequency, int pairs, int interleaved, int inverse, int64_t tokens,
