@@ -12,7 +12,8 @@ the longest] int32 says where token t of a sequence lies: row ``t % page_size`` 
 page ``page_table[s, t // page_size]``.  Lengths, offsets and tables are device
 tensors: no call waits for the GPU.  Like the other token operators these marshal
 arguments only, run on the current (or the given) stream, and raise on anything
-the library refuses.
+the library refuses.  They are for serving and record no gradient, but for ``rotary``,
+whose gradient is the inverse rotation.
 """
 from __future__ import annotations
 
@@ -85,7 +86,7 @@ def _heads(t: torch.Tensor, types: dict, what: str) -> Tuple[int, int, int, int,
         raise ValueError(f"{what} must be [tokens, heads, width]")
     tokens, heads, width = t.shape
     ts, hs, last = t.stride()
-    if last != 1 and width > 1:
+    if last != 1 and width > 1 and tokens and heads:
         raise ValueError(f"{what} must have contiguous rows")
     return tokens, heads, width, (ts if tokens > 1 else heads * width), (hs if heads > 1 else width), code
 
@@ -215,6 +216,23 @@ def _ladder(sections: Tuple[int, ...], base: float, ladder: str, scales, frequen
     return n, (ctypes.c_int * n)(*axis), (ctypes.c_double * n)(*freq)
 
 
+class _Rotary(torch.autograd.Function):
+    """rotary of an x that wants a gradient: the inverse rotation of the result's."""
+
+    @staticmethod
+    def forward(ctx, x, positions, stream, inverse, kw):
+        ctx.save_for_backward(positions)
+        ctx.inverse, ctx.kw = inverse, kw
+        return rotary(x, positions, inverse=inverse, stream=stream, **kw)
+
+    @staticmethod
+    def backward(ctx, grad):
+        # (contiguous: a gradient that was broadcast has strides of 0; on the stream that
+        # autograd runs this on)
+        return (rotary(grad.contiguous(), *ctx.saved_tensors, inverse=not ctx.inverse, **ctx.kw),
+                None, None, None, None)
+
+
 def rotary(x: torch.Tensor, positions: torch.Tensor, sections: Sequence[int],
            base: float = 10000.0, ladder: str = "axis", pairs: str = "half",
            scales: Optional[Sequence[float]] = None,
@@ -233,7 +251,12 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, sections: Sequence[int],
     from 2N on stay as they are.  Angles are exact to 2 pi |position| 2^-65, then in
     fp32, for far positions too.  ``inverse``
     turns back: the gradient with respect to x of a loss whose gradient with respect
-    to the result is x.  x bf16, fp16 or fp32; ``out`` may be ``x``."""
+    to the result is x; where x requires a gradient, it is recorded so (not with
+    ``out``, which records nothing).  x bf16, fp16 or fp32; ``out`` may be ``x``."""
+    if out is None and x.requires_grad and torch.is_grad_enabled():
+        return _Rotary.apply(x, positions, stream, bool(inverse), dict(
+            sections=tuple(sections), base=base, ladder=ladder, pairs=pairs, scales=scales,
+            frequencies=frequencies))
     lib = _fns or _bind()
     n, axis, freq = _ladder(tuple(sections), float(base), ladder,
                             None if scales is None else tuple(scales),
