@@ -1,4 +1,4 @@
-"""The cache's dimensions of size one may have any stride."""
+"""Caches in other orders and with padding; dimensions of size one may have any stride."""
 import pytest
 import torch
 
@@ -64,3 +64,37 @@ def test_strides_of_dimensions_of_one(pkg, dtype, pages, heads, page):
         turned = torch.ones(4, 16, 2, device="cuda").transpose(1, 2)
         with pytest.raises(ValueError):
             pkg.kv_cache_read(a, a.clone(), four, _ints([0, 4]), tokens=4, k_scale=turned, v_scale=turned)
+
+
+@pytest.mark.parametrize("dtype", [I8, BF])
+@pytest.mark.parametrize("order", ["phtw", "pthw", "hptw", "tphw", "thpw", "htpw"])
+@pytest.mark.parametrize("pads", [(0, 0, 0), (16, 0, 0), (0, 48, 0), (0, 0, 112), (16, 32, 80)])
+def test_orders_and_padding(pkg, dtype, order, pads):
+    """Pages, heads and tokens of a cache in any order in memory, with rows, and what
+    follows them, padded: strides that are no multiples of one another."""
+    pages, heads, page, width, n = 13, 3, 32, 48, 400
+    g = torch.Generator(device="cuda").manual_seed(7)
+    q = torch.randn(2, 2 * heads, width, generator=g, device="cuda").bfloat16()
+    k, v = (torch.randn(n, heads, width, generator=g, device="cuda").bfloat16() for _ in range(2))
+    table = torch.randperm(pages, generator=g, device="cuda").int()[None].repeat(2, 1)
+    sizes, stride, extent = dict(p=pages, h=heads, t=page, w=width), {}, 1
+    for d, pad in zip(reversed(order), (0,) + pads):
+        stride[d] = extent + (pad if d != "w" else 0)
+        extent = stride[d] * sizes[d]
+    results = []
+    for strides in (None, [stride[d] for d in "phtw"]):
+        made = []
+        for _ in range(2):
+            if strides is None:
+                made.append(torch.zeros(pages, heads, page, width, device="cuda").to(dtype))
+            else:
+                flat = torch.full((extent,), 9, device="cuda").to(dtype)
+                made.append(flat.as_strided((pages, heads, page, width), strides))
+        s = [torch.zeros(pages, heads, page, device="cuda") if dtype is I8 else None for _ in range(2)]
+        pkg.kv_cache_write(k, v, *made, table[:1], _ints([0]), *s, offsets=_ints([0, n]))
+        ko, vo = pkg.kv_cache_read(*made, table[:1], _ints([0, n]), tokens=n, k_scale=s[0], v_scale=s[1])
+        y = pkg.paged_attention(q, *made, table, _ints([n, 77]), k_scale=s[0], v_scale=s[1])
+        assert not y.isnan().any()
+        results.append([ko, vo, y])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
