@@ -1,5 +1,5 @@
 // token_attention_internal.h -- parameter blocks and launch entry points shared by
-// attention_api.cu and the kernels of rotary positions, the key-value cache and
+// token_attention_api.cu and the kernels of rotary positions, the key-value cache and
 // attention.  Not part of the public ABI.
 #pragma once
 #include <cstddef>

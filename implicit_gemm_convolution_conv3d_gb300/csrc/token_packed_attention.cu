@@ -20,15 +20,16 @@
 // With two tiles a job the tensor cores work on one while the other's weights are
 // computed, and K and V are read once for 256 rows; with one tile two CTAs share an SM.
 // Two are taken where documents are longer than a tile and their jobs reach every SM:
-// 14400 x 16 x 128 967 against 1147 us, 1024-long documents of 64-wide heads 80 against 88,
-// 256-long ones 34 each; between 256 and 768 either is ahead by up to 10%, as the number of
-// tiles is even or odd.
-// What bounds it: at 128-wide heads the tensor cores (14400 x 16 x 128: 1750 TFLOP/s of
-// 1915); at 64 the chain of one tile's steps, as its scores and weights share their place:
+// 14400 x 16 x 128 948 against 1104 us, 1024-long documents of 64-wide heads 81 against 89,
+// 256-long ones 34 each; between 256 and 768 either is ahead by up to 14%, as the number of
+// tiles is even or odd (54 of 300 63 against 57, 32 of 500 50 against 58).
+// What bounds it: at 128-wide heads the tensor cores (14400 x 16 x 128: 1790 TFLOP/s of
+// 1915 back to back on the same inputs, 1600 on changing ones, under the power cap); at 64
+// the chain of one tile's steps, as its scores and weights share their place:
 // of 2400 cycles for a key tile of both query tiles 1700 are a softmax from scores to
 // weights, the rest its two products and the hand-overs.  So the weights are handed over in
 // two halves, and a turn's scores are issued right behind its product, their keys having
-// been waited for before it (822 to 799 us at 64; leaving out the exponentials and the
+// been waited for before it (822 to 799 us at 64, 788 by now; leaving out the exponentials and the
 // maximum gains 10%).  Without the turns 128-wide heads take 1304 us.
 // The maximum that weights are relative to follows the running one only when that has
 // grown by more than 2^8 (weights up to 256 keep their 11 or 8 bits, sums are fp32), so
@@ -50,11 +51,12 @@ constexpr uint32_t kSmallBytes = 896;  // shared memory of the barriers, jobs an
 constexpr uint32_t kAsk = 8;           // asked for at once behind the last job
 // Mean tokens of a document above which jobs are dealt to CTAs that ask (cluster launch
 // control: a CTA takes the index of one that has not started), so that none waits for
-// another's longer documents: 2 x 8192 causal 336 us, 372 with every grid-th job a CTA;
-// 24 documents of 100 to 1403 139 and 145; 40 of 30 to 1600 causal 146 and 166.  The grid then
-// has a CTA for every job that there could be, and those behind the last job are taken
-// too, kAsk at a time: a buffer of 65536 rows with 1000 in use takes 22 us either way.  Of
-// short documents the planner finds 32 jobs at a time instead (100 x 100: 22 us, 28 dealt).
+// another's longer documents: 2 x 8192 causal 332 us, 360 with every grid-th job a CTA;
+// 24 documents of 100 to 1403 with slopes 210 and 223; 40 of 30 to 1600 causal 169 and 196
+// (lengths drawn at random).  The grid then has a CTA for every job that there could be, and
+// those behind the last job are taken too, kAsk at a time: a buffer of 65536 rows with 1000
+// in use takes 17 us either way.  Of short documents the planner finds 32 jobs at a time
+// instead (100 x 100: 21 us, 33 dealt).
 constexpr long long kDealtFrom = 384;
 constexpr float kLag = 8.0f;           // powers of two that weights may exceed 1 by
 // f16 weights (and their sum) are taken 2^7 times as large, up to 2^15 of f16's 2^16: those

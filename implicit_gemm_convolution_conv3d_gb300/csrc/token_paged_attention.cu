@@ -15,7 +15,7 @@
 // through its own ring of TMA loads: two a run of 32, 16 or 8 tokens, as many as pages
 // hold a multiple of, which leaves the load units to the shared-memory side.  Blocks at an
 // edge of what is seen, in pages of other sizes, or in pages that are not there come word
-// by word (all blocks so, before lanes looked up their tokens: 1325 us for 414, int8).
+// by word.
 //
 // Measured, 200 sequences of 1 to 8192 tokens, 8 key heads of 128 for 32 query heads, back
 // to back: fp16 492 us; int8, capped, 297 us (84% of the floor's bytes at 6.8 TB/s): there the
@@ -82,8 +82,9 @@ struct Form {
 
 // CTAs of an SM: three of one group of query heads, two of two (their registers), as far
 // as shared memory goes: some compute while another joins its warps' results at a key
-// head's end.  (Two instead of three, before edges were looked up by lanes: 200 ragged sequences of up to 8192, 8 key heads of
-// 128, int8 433 us for 414; 16 key heads of 64 650 for 561; one of 216000 107 for 110.)
+// head's end.  (Two instead of three: 200 ragged sequences of up to 8192, 8 key heads of 128,
+// int8 340 us for 292, fp16 533 for 504; 16 key heads of 64, int8, 490 for 389; one of 216000
+// e4m3 83 for 85.)
 constexpr int ctas_of(int es, int dp, int ng) { return es * dp >= 512 ? 1 : ng == 1 ? 3 : 2; }
 
 // Byte of 16-byte word `c` of row `r` in boxes of 16 rows (of 32, if there is one column).
@@ -852,9 +853,10 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     auto part = [&](int k, int h) {
         return p.partial + ((static_cast<long long>(c) + k) * 2 + (k == 0)) * kPartial<DP> + h * (DP + 2);
     };
-    // a few parts: every thread takes their weights itself, all loads at once (a call of
-    // 333 tokens, 16 heads of 64: 14.3 us, 15.4 through the warps' weights)
-    constexpr int kFew = 8;
+    // a few parts: every thread takes their weights itself, all loads at once (16 heads of 64,
+    // bf16, in a graph: 400 tokens, 4 parts, 7.5 us, 8.3 through the warps' weights; 800, 7
+    // parts, 8.0 and 8.5; but 900, 8 parts, 8.4 and 7.6)
+    constexpr int kFew = 7;
     const bool few = job.w < kFew;
     for (int h = threadIdx.x >> 5; h < job.z && !few; h += 8) {
         float top = -INFINITY;
@@ -959,10 +961,12 @@ cudaError_t by_width(const PagedMaps& m, const PagedParams& p, cudaStream_t stre
 static int pass_heads(long long group, int width) { return group > 8 && width <= 128 ? 16 : 8; }
 
 // Key heads are not split where tables hold few tokens and each head has a CTA of its own
-// among those that run at once: there is nothing to join then, no workspace to allocate
-// (6 us of a call's 20 on the host), and no unit to look for.  A CTA alone takes longer than
-// several and the join from about 500 tokens on: 8 key heads of 128, e4m3, 333 tokens
-// 16.4 us both, 750 20.5 and 16.4, 2000 30.7 and 18.4.
+// among those that run at once: there is nothing to join then, no workspace to allocate,
+// and no unit to look for.  A CTA alone takes longer than several and the join from about 450
+// tokens on (one sequence in a graph, 8 key heads of 128, e4m3: 333 tokens 7.4 us for 8.0, 384
+// 6.6 for 7.8, 450 8.5 for 8.0, 650 10.6 for 8.5; 16 of 64, bf16: 384 5.4 for 7.0, 450 6.9 for
+// 7.7, 650 8.4 for 7.9); outside a graph the host's time of a second launch and the workspace
+// is 2 us of 17.
 bool paged_whole(long long sequences, long long kv_heads, long long group, int width,
                  long long capacity, int num_sms) {
     const long long blocks = (group + pass_heads(group, width) - 1) / pass_heads(group, width);
