@@ -66,6 +66,9 @@ constexpr float kLag = 8.0f;           // powers of two that weights may exceed 
 // lose bits instead.
 template <bool BF>
 constexpr float kUp = BF ? -24.0f : 7.0f;
+// Scores from here on (powers of two) are in steps of a quarter and more: f16 weights follow
+// the maximum at once, as the steps could take lagging ones out of f16's range.
+constexpr float kCoarse = 2097152.0f;
 
 template <bool BF>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -932,7 +935,7 @@ __global__ void __launch_bounds__(kThreads<NQ>, NQ == 1 ? 2 : 1)
                 }
                 if (fresh) {
                     ref = top;
-                } else if (__any_sync(0xffffffffu, top * c > ref * c + kLag)) {
+                } else if (__any_sync(0xffffffffu, top * c > ref * c + (BF || fabsf(top * c) < kCoarse ? kLag : 0.0f))) {
                     ok = wait_role(o_done0 + 8 * i, (turn - 1) & 1u, abort_flag, p.status, limit);
                     if (!ok) break;
                     tc_fence_after();

@@ -56,6 +56,9 @@ constexpr float kLag = 4.0f;
 // weights have fp32's range and are taken 2^-24 times as large, so that sums over 2^20
 // tokens hold for values up to the type's largest (results below 2^-112 lose bits instead).
 constexpr float kUp = 11.0f, kDown = 1.0f / 2048.0f, kUpBf16 = -24.0f;
+// Scores from here on (powers of two) are in steps of a quarter and more: f16 weights follow
+// the maximum at once, as the steps could take lagging ones out of f16's range.
+constexpr float kCoarse = 2097152.0f;
 
 template <int ES, int DP>
 struct Form {
@@ -650,7 +653,7 @@ __global__ void __launch_bounds__(32 * Form<KIND == kTokBf16 || KIND == kTokF16 
                     if (F::kSubs == 2)
                         best[n][j] = fmaxf(best[n][j], fmaxf(s2[F::kSubs - 1][n][j] + lv[F::kSubs - 1][0],
                                                              s2[F::kSubs - 1][n][j + 2] + lv[F::kSubs - 1][1]));
-                    rise |= best[n][j] > m[n][j] + kLag;
+                    rise |= best[n][j] > m[n][j] + kLag || (!kBf && fabsf(best[n][j]) >= kCoarse);
                 }
             if (__any_sync(0xffffffffu, rise)) {
                 // all tokens' maximum, and everything relative to it
