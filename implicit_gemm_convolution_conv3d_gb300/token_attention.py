@@ -255,8 +255,9 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, sections: Sequence[int],
     ``out``, which records nothing).  x bf16, fp16 or fp32; ``out`` may be ``x``."""
     if out is None and x.requires_grad and torch.is_grad_enabled():
         return _Rotary.apply(x, positions, stream, bool(inverse), dict(
-            sections=tuple(sections), base=base, ladder=ladder, pairs=pairs, scales=scales,
-            frequencies=frequencies))
+            sections=tuple(sections), base=base, ladder=ladder, pairs=pairs,
+            scales=None if scales is None else tuple(scales),
+            frequencies=None if frequencies is None else tuple(frequencies)))
     lib = _fns or _bind()
     n, axis, freq = _ladder(tuple(sections), float(base), ladder,
                             None if scales is None else tuple(scales),

@@ -141,3 +141,15 @@ def test_streams_and_empty(pkg):
     none = torch.zeros(0, 3, 80, device="cuda", requires_grad=True)
     pkg.rotary(none, p[:0], (9, 20)).sum().backward()
     assert none.grad.shape == (0, 3, 80)
+
+
+def test_arguments_that_change(pkg):
+    """The backward pass takes the frequencies and scales of the call, whatever became of the lists."""
+    x, w, p = _inputs(FF, axes=2)
+    freq, scales = [0.1 * (i + 1) for i in range(29)], [1.0, 2.0]
+    leaf = x.clone().requires_grad_()
+    y = pkg.rotary(leaf, p, (9, 20), frequencies=freq, scales=scales)
+    want = pkg.rotary(w, p, (9, 20), frequencies=freq, scales=scales, inverse=True)
+    freq[:], scales[:] = [0.0] * 29, [0.0, 0.0]
+    y.backward(w)
+    assert torch.equal(leaf.grad, want)
